@@ -13,8 +13,10 @@ from concurrent.futures import ThreadPoolExecutor
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _CSRC = os.path.join(_HERE, "csrc")
 _BUILD = os.path.join(_HERE, "_build")
-SOURCES = ["abi.cu", "vote_simt.cu", "vote_tc.cu", "vote_cluster.cu", "pool_topk.cu", "gather.cu", "decode.cu", "hit_rate.cu"]
-HEADERS = ["snapkv_common.cuh", "snapkv_internal.h", "sm100_ptx.cuh", "tc_common.cuh"]
+SOURCES = ["abi.cu", "vote_simt.cu", "vote_tc.cu", "vote_cluster.cu", "pool_topk.cu", "gather.cu", "decode.cu", "hit_rate.cu",
+           "cache_abi.cu", "attend.cu", "q4.cu", "evict.cu"]
+HEADERS = ["snapkv_common.cuh", "snapkv_internal.h", "sm100_ptx.cuh", "tc_common.cuh", "abi_common.h",
+           "cache_internal.h", "q4.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]
@@ -52,7 +54,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, checked: bool = Fals
     extra = ["-DSNAPKV_CHECKED"] if checked else []
     os.makedirs(build_dir, exist_ok=True)
     header_deps = [os.path.join(_CSRC, h) for h in HEADERS] + [
-        os.path.join(os.path.dirname(_HERE), "include", "snapkv.h")]
+        os.path.join(os.path.dirname(_HERE), "include", h) for h in ("snapkv.h", "snapkv_cache.h")]
     objs, jobs = [], []
     for src in SOURCES:
         s = os.path.join(_CSRC, src)

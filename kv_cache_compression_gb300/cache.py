@@ -1,0 +1,290 @@
+"""Python binding of include/snapkv_cache.h: operators on a cache that is being decoded over.
+
+Decode attention with grouped queries that keeps a running score of every cached row, eviction by
+that score, and a cache held in 4 bits. As in ``snapkv``, every computation runs in the library's
+CUDA kernels and arguments mirror the header; calls run on ``stream`` (default: the current stream
+of the tensors' device), allocate what the caller does not pass, and raise on a refused call.
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+
+from . import snapkv as _sk
+from .snapkv import ERR_INVALID_ARG, OK, SnapKVError, new_workspace
+
+GROUP = 64   # channels of a 4-bit row that share one (h, z)
+
+
+class _Q4Struct(ctypes.Structure):
+    """Mirror of snapkv_q4_cache."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_meta", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_meta", ctypes.c_void_p), ("cap", ctypes.c_int64), ("batch", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+_lib = None
+
+
+def lib():
+    """The loaded library with the prototypes of include/snapkv_cache.h."""
+    global _lib
+    if _lib is None:
+        L = _sk.lib()
+        P, I32, I64, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+        C = ctypes.POINTER(_Q4Struct)
+        for name, res, args in [
+                ("snapkv_scored_workspace_size", SZ, [I32, I32, I32, I32, I64]),
+                ("snapkv_decode_attend_scored", I32,
+                 [P, P, P, I64, P, P, F, P, I32, I32, I32, I32, I32, P, SZ, P, P]),
+                ("snapkv_q4_append", I32, [C, P, P, I64, P, P, P, I32, P, P]),
+                ("snapkv_q4_read", I32, [C, P, I64, P, P, I32, P]),
+                ("snapkv_q4_decode_attend", I32, [P, C, P, P, F, P, I32, I32, P, SZ, P, P]),
+                ("snapkv_evict_workspace_size", SZ, [I32, I32, I64]),
+                ("snapkv_evict", I32, [P, P, I64, P, P, P, I64, I64, P, I32, I32, I32, I32, P, SZ, P, P]),
+                ("snapkv_q4_evict", I32, [C, P, P, P, I64, I64, P, P, SZ, P, P])]:
+            f = getattr(L, name)
+            f.restype, f.argtypes = res, args
+        _lib = L
+    return _lib
+
+
+def _check(name, t, shape, dtype, device):
+    """One tensor argument: shape, type, device and density (the kernels take dense tensors)."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _lengths(name, t, batch, device):
+    import torch
+    _check(name, t, (batch,), torch.int32, device)
+
+
+def _status(t, device):
+    import torch
+    if t is not None and (t.dtype != torch.int32 or t.device != device or t.numel() < 1):
+        raise ValueError(f"dev_status must be an int32 tensor on {device}")
+    return _sk._ptr(t)
+
+
+def _room(workspace, need, device):
+    """The caller's workspace or a new one."""
+    if workspace is None:
+        return new_workspace(need, device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
+
+
+def _call(name, device, stream, *args):
+    """Calls a library function with `device` current (kernels launch there) and the stream last."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"{name} needs CUDA tensors, not {device}")
+    with torch.cuda.device(device):
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        st = getattr(lib(), name)(*args, ctypes.c_void_p(stream.cuda_stream))
+    if st != OK:
+        raise SnapKVError(st, name)
+
+
+@dataclass
+class Q4Cache:
+    """A K/V cache held in 4 bits (the layout of snapkv_q4_cache): k_codes, v_codes uint8 [B,H,cap,d/2] and
+    k_meta, v_meta bfloat16 [B,H,cap,d/64,2] (step h, centre z). 144 bytes per row of K and V at d = 128,
+    against 512 in bf16."""
+    k_codes: object
+    k_meta: object
+    v_codes: object
+    v_meta: object
+
+    def __post_init__(self):
+        import torch
+        if self.k_codes.dim() != 4 or self.k_codes.shape[-1] not in (32, 64):
+            raise ValueError("k_codes must be [B, H, cap, d / 2] with d 64 or 128")
+        B, H, cap, half = self.k_codes.shape
+        dev = self.k_codes.device
+        _check("k_codes", self.k_codes, (B, H, cap, half), torch.uint8, dev)
+        _check("v_codes", self.v_codes, (B, H, cap, half), torch.uint8, dev)
+        for name, t in (("k_meta", self.k_meta), ("v_meta", self.v_meta)):
+            _check(name, t, (B, H, cap, half * 2 // GROUP, 2), torch.bfloat16, dev)
+
+    @classmethod
+    def empty(cls, batch, heads, cap, head_dim, device):
+        """An uninitialised cache (rows are written by q4_append)."""
+        import torch
+        codes = [torch.empty((batch, heads, cap, head_dim // 2), dtype=torch.uint8, device=device) for _ in "kv"]
+        meta = [torch.empty((batch, heads, cap, head_dim // GROUP, 2), dtype=torch.bfloat16, device=device)
+                for _ in "kv"]
+        return cls(codes[0], meta[0], codes[1], meta[1])
+
+    @property
+    def shape(self):
+        """(B, H, cap, d)"""
+        B, H, cap, half = self.k_codes.shape
+        return B, H, cap, 2 * half
+
+    @property
+    def device(self):
+        return self.k_codes.device
+
+    def _struct(self):
+        B, H, cap, d = self.shape
+        return ctypes.byref(_Q4Struct(self.k_codes.data_ptr(), self.k_meta.data_ptr(), self.v_codes.data_ptr(),
+                                      self.v_meta.data_ptr(), cap, B, H, d))
+
+
+def scored_workspace_size(batch, q_heads, heads, head_dim, cap) -> int:
+    return int(lib().snapkv_scored_workspace_size(batch, q_heads, heads, head_dim, cap))
+
+
+def evict_workspace_size(batch, heads, cap) -> int:
+    return int(lib().snapkv_evict_workspace_size(batch, heads, cap))
+
+
+def _attend_args(where, q, shape, dev, len_, score, out, workspace):
+    """Checks and completes what the two attention calls share."""
+    import torch
+    B, H, cap, d = shape
+    if q.dim() != 3:
+        raise ValueError("q must be [B, q_heads, d]")
+    q_heads = q.shape[1]
+    if q_heads < 1 or q_heads % H:
+        raise SnapKVError(ERR_INVALID_ARG, where)
+    _check("q", q, (B, q_heads, d), q.dtype, dev)
+    _lengths("len_", len_, B, dev)
+    if out is None:
+        out = torch.empty_like(q)
+    _check("out", out, q.shape, q.dtype, dev)
+    if score is not None:
+        _check("score", score, (B, H, cap), torch.float32, dev)
+        workspace = _room(workspace, scored_workspace_size(B, q_heads, H, d, cap), dev)
+    else:
+        workspace = None
+    return q_heads, out, workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def decode_attend_scored(q, k_cache, v_cache, len_, score=None, *, decay=1.0, out=None, workspace=None,
+                         dev_status=None, stream=None):
+    """snapkv_decode_attend_scored: q [B,Hq,d] over rows < len_[b] of k_cache, v_cache [B,H,cap,d] (Hq a
+    multiple of H) -> out [B,Hq,d]. ``score`` fp32 [B,H,cap], if given, becomes decay * score + the
+    attention each row received, in place (rows < len_[b] only; clear it before the first step)."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [B, H, cap, d]")
+    B, H, cap, d = k_cache.shape
+    dev = k_cache.device
+    _check("k_cache", k_cache, k_cache.shape, q.dtype, dev)
+    _check("v_cache", v_cache, k_cache.shape, q.dtype, dev)
+    q_heads, out, workspace, ws_bytes = _attend_args("snapkv_decode_attend_scored", q, k_cache.shape, dev, len_,
+                                                     score, out, workspace)
+    _call("snapkv_decode_attend_scored", dev, stream, _sk._ptr(q), _sk._ptr(k_cache), _sk._ptr(v_cache), cap,
+          _sk._ptr(len_), _sk._ptr(score), float(decay), _sk._ptr(out), B, q_heads, H, d, _sk._dtype_code(q),
+          _sk._ptr(workspace), ws_bytes, _status(dev_status, dev))
+    return out
+
+
+def q4_decode_attend(q, cache, len_, score=None, *, decay=1.0, out=None, workspace=None, dev_status=None,
+                     stream=None):
+    """snapkv_q4_decode_attend: decode_attend_scored over a Q4Cache; q and out are bf16 or fp32."""
+    dev = cache.device
+    q_heads, out, workspace, ws_bytes = _attend_args("snapkv_q4_decode_attend", q, cache.shape, dev, len_, score,
+                                                     out, workspace)
+    _call("snapkv_q4_decode_attend", dev, stream, _sk._ptr(q), cache._struct(), _sk._ptr(len_), _sk._ptr(score),
+          float(decay), _sk._ptr(out), q_heads, _sk._dtype_code(q), _sk._ptr(workspace), ws_bytes,
+          _status(dev_status, dev))
+    return out
+
+
+def q4_append(cache, k_new, v_new, len_in, len_out=None, *, n_new=None, dev_status=None, stream=None):
+    """snapkv_q4_append: quantises k_new, v_new [B,H,rows,d] (or [B,H,d], one row) into rows len_in[b] on of a
+    Q4Cache, n_new[b] of them if given. Returns len_out [B] (len_in is only read)."""
+    import torch
+    B, H, cap, d = cache.shape
+    dev = cache.device
+    rows = k_new.shape[2] if k_new.dim() == 4 else 1
+    shape = (B, H, rows, d) if k_new.dim() == 4 else (B, H, d)
+    _check("k_new", k_new, shape, k_new.dtype, dev)
+    _check("v_new", v_new, shape, k_new.dtype, dev)
+    _lengths("len_in", len_in, B, dev)
+    if n_new is not None:
+        _lengths("n_new", n_new, B, dev)
+    if len_out is None:
+        len_out = torch.empty_like(len_in)
+    _lengths("len_out", len_out, B, dev)
+    _call("snapkv_q4_append", dev, stream, cache._struct(), _sk._ptr(k_new), _sk._ptr(v_new), rows,
+          _sk._ptr(n_new), _sk._ptr(len_in), _sk._ptr(len_out), _sk._dtype_code(k_new), _status(dev_status, dev))
+    return len_out
+
+
+def q4_read(cache, rows, *, start=None, dtype=None, k_out=None, v_out=None, stream=None):
+    """snapkv_q4_read: the values (dtype: bf16 or fp32, default bf16) that rows start[b] .. start[b] + rows - 1
+    of a Q4Cache stand for, as k, v [B,H,rows,d]; rows outside the cache are zeros."""
+    import torch
+    B, H, cap, d = cache.shape
+    dev = cache.device
+    if dtype is None:
+        dtype = torch.bfloat16 if k_out is None else k_out.dtype
+    if start is not None:
+        _lengths("start", start, B, dev)
+    k_out = torch.empty((B, H, rows, d), dtype=dtype, device=dev) if k_out is None else k_out
+    v_out = torch.empty((B, H, rows, d), dtype=dtype, device=dev) if v_out is None else v_out
+    _check("k_out", k_out, (B, H, rows, d), dtype, dev)
+    _check("v_out", v_out, (B, H, rows, d), dtype, dev)
+    _call("snapkv_q4_read", dev, stream, cache._struct(), _sk._ptr(start), int(rows), _sk._ptr(k_out),
+          _sk._ptr(v_out), _sk._dtype_code(k_out))
+    return k_out, v_out
+
+
+def _evict_args(shape, dev, score, len_in, len_out, keep, recent, idx_out, want_idx, workspace):
+    """Checks and completes what the two evictions share."""
+    import torch
+    B, H, cap, d = shape
+    _check("score", score, (B, H, cap), torch.float32, dev)
+    _lengths("len_in", len_in, B, dev)
+    if len_out is None:
+        len_out = torch.empty_like(len_in)
+    _lengths("len_out", len_out, B, dev)
+    left = int(keep) + int(recent)
+    if idx_out is None and want_idx and left > 0:
+        idx_out = torch.empty((B, H, left), dtype=torch.int32, device=dev)
+    if idx_out is not None:
+        _check("idx_out", idx_out, (B, H, left), torch.int32, dev)
+    workspace = _room(workspace, evict_workspace_size(B, H, cap), dev)
+    return len_out, idx_out, workspace, workspace.numel() * workspace.element_size()
+
+
+def evict(k_cache, v_cache, score, len_in, len_out=None, *, keep, recent, idx_out=None, want_idx=True,
+          workspace=None, dev_status=None, stream=None):
+    """snapkv_evict: brings sequences of more than keep + recent rows down to the ``keep`` rows of largest score
+    and the newest ``recent``, per head and in place (k_cache, v_cache [B,H,cap,d], score [B,H,cap]). Returns
+    (len_out [B], idx [B,H,keep+recent] or None): the new lengths and the slot each row came from."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [B, H, cap, d]")
+    B, H, cap, d = k_cache.shape
+    dev = k_cache.device
+    _check("k_cache", k_cache, k_cache.shape, k_cache.dtype, dev)
+    _check("v_cache", v_cache, k_cache.shape, k_cache.dtype, dev)
+    len_out, idx_out, workspace, ws_bytes = _evict_args(k_cache.shape, dev, score, len_in, len_out, keep, recent,
+                                                        idx_out, want_idx, workspace)
+    _call("snapkv_evict", dev, stream, _sk._ptr(k_cache), _sk._ptr(v_cache), cap, _sk._ptr(score),
+          _sk._ptr(len_in), _sk._ptr(len_out), int(keep), int(recent), _sk._ptr(idx_out), B, H, d,
+          _sk._dtype_code(k_cache), _sk._ptr(workspace), ws_bytes, _status(dev_status, dev))
+    return len_out, idx_out
+
+
+def q4_evict(cache, score, len_in, len_out=None, *, keep, recent, idx_out=None, want_idx=True, workspace=None,
+             dev_status=None, stream=None):
+    """snapkv_q4_evict: evict for a Q4Cache."""
+    dev = cache.device
+    len_out, idx_out, workspace, ws_bytes = _evict_args(cache.shape, dev, score, len_in, len_out, keep, recent,
+                                                        idx_out, want_idx, workspace)
+    _call("snapkv_q4_evict", dev, stream, cache._struct(), _sk._ptr(score), _sk._ptr(len_in), _sk._ptr(len_out),
+          int(keep), int(recent), _sk._ptr(idx_out), _sk._ptr(workspace), ws_bytes, _status(dev_status, dev))
+    return len_out, idx_out

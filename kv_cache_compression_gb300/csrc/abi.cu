@@ -6,8 +6,7 @@
 
 #include <vector>
 
-#include <nvtx3/nvToolsExt.h>
-
+#include "abi_common.h"
 #include "snapkv_common.cuh"
 #include "snapkv_internal.h"
 
@@ -16,27 +15,7 @@ namespace snapkv {
 namespace {
 
 constexpr int kVoteChunk = 1024;   // prompt columns per CTA of the score/vote kernels
-constexpr int64_t kMaxPrompt = (int64_t)1 << 30;
 constexpr int kMaxObs = 128;
-
-size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-// An NVTX range around an entry point's host work (validation and enqueueing), so that a profiler's
-// timeline shows which library call enqueued which kernels; without a tool attached it costs a few
-// nanoseconds.
-struct HostRange {
-  explicit HostRange(const char* name) { nvtxRangePushA(name); }
-  ~HostRange() { nvtxRangePop(); }
-  HostRange(const HostRange&) = delete;
-  HostRange& operator=(const HostRange&) = delete;
-};
-
-bool overlaps(const void* a, size_t an, const void* b, size_t bn) {
-  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-  return a0 < b0 + bn && b0 < a0 + an;
-}
 
 // V may be device memory or page-locked host memory mapped into the device's address space: the
 // compression reads only the kept rows and the window rows of V, so a caller whose values live on

@@ -9,6 +9,9 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
+from functools import lru_cache
+
+import torch
 
 from . import snapkv as _sk
 from .snapkv import ERR_INVALID_ARG, OK, SnapKVError, new_workspace
@@ -51,7 +54,7 @@ def lib():
 
 def _check(name, t, shape, dtype, device):
     """One tensor argument: shape, type, device and density (the kernels take dense tensors)."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
@@ -62,15 +65,19 @@ def _check(name, t, shape, dtype, device):
 
 
 def _lengths(name, t, batch, device):
-    import torch
     _check(name, t, (batch,), torch.int32, device)
 
 
 def _status(t, device):
-    import torch
-    if t is not None and (t.dtype != torch.int32 or t.device != device or t.numel() < 1):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.device != device or t.numel() < 1:
         raise ValueError(f"dev_status must be an int32 tensor on {device}")
-    return _sk._ptr(t)
+    return t.data_ptr()
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _room(workspace, need, device):
@@ -83,19 +90,25 @@ def _room(workspace, need, device):
 
 
 def _call(name, device, stream, *args):
-    """Calls a library function with `device` current (kernels launch there) and the stream last."""
-    import torch
+    """Calls a library function with `device` current (kernels launch there) and the stream last.
+
+    A decode step makes several of these calls and each kernel takes microseconds, so the usual case
+    (the tensors' device is the current one) takes the raw stream handle and no context manager."""
     if device.type != "cuda":
         raise ValueError(f"{name} needs CUDA tensors, not {device}")
-    with torch.cuda.device(device):
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-        st = getattr(lib(), name)(*args, ctypes.c_void_p(stream.cuda_stream))
+    f = getattr(_lib or lib(), name)
+    index = device.index
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        st = f(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            st = f(*args, handle)
     if st != OK:
         raise SnapKVError(st, name)
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class Q4Cache:
     """A K/V cache held in 4 bits (the layout of snapkv_q4_cache): k_codes, v_codes uint8 [B,H,cap,d/2] and
     k_meta, v_meta bfloat16 [B,H,cap,d/64,2] (step h, centre z). 144 bytes per row of K and V at d = 128,
@@ -106,7 +119,6 @@ class Q4Cache:
     v_meta: object
 
     def __post_init__(self):
-        import torch
         if self.k_codes.dim() != 4 or self.k_codes.shape[-1] not in (32, 64):
             raise ValueError("k_codes must be [B, H, cap, d / 2] with d 64 or 128")
         B, H, cap, half = self.k_codes.shape
@@ -115,43 +127,35 @@ class Q4Cache:
         _check("v_codes", self.v_codes, (B, H, cap, half), torch.uint8, dev)
         for name, t in (("k_meta", self.k_meta), ("v_meta", self.v_meta)):
             _check(name, t, (B, H, cap, half * 2 // GROUP, 2), torch.bfloat16, dev)
+        object.__setattr__(self, "shape", (B, H, cap, 2 * half))   # B, H, cap, d
+        object.__setattr__(self, "device", dev)
+
+    def _struct(self):
+        B, H, cap, d = self.shape
+        return _Q4Struct(self.k_codes.data_ptr(), self.k_meta.data_ptr(), self.v_codes.data_ptr(),
+                         self.v_meta.data_ptr(), cap, B, H, d)
 
     @classmethod
     def empty(cls, batch, heads, cap, head_dim, device):
         """An uninitialised cache (rows are written by q4_append)."""
-        import torch
         codes = [torch.empty((batch, heads, cap, head_dim // 2), dtype=torch.uint8, device=device) for _ in "kv"]
         meta = [torch.empty((batch, heads, cap, head_dim // GROUP, 2), dtype=torch.bfloat16, device=device)
                 for _ in "kv"]
         return cls(codes[0], meta[0], codes[1], meta[1])
 
-    @property
-    def shape(self):
-        """(B, H, cap, d)"""
-        B, H, cap, half = self.k_codes.shape
-        return B, H, cap, 2 * half
 
-    @property
-    def device(self):
-        return self.k_codes.device
-
-    def _struct(self):
-        B, H, cap, d = self.shape
-        return ctypes.byref(_Q4Struct(self.k_codes.data_ptr(), self.k_meta.data_ptr(), self.v_codes.data_ptr(),
-                                      self.v_meta.data_ptr(), cap, B, H, d))
-
-
+@lru_cache(maxsize=256)
 def scored_workspace_size(batch, q_heads, heads, head_dim, cap) -> int:
     return int(lib().snapkv_scored_workspace_size(batch, q_heads, heads, head_dim, cap))
 
 
+@lru_cache(maxsize=256)
 def evict_workspace_size(batch, heads, cap) -> int:
     return int(lib().snapkv_evict_workspace_size(batch, heads, cap))
 
 
 def _attend_args(where, q, shape, dev, len_, score, out, workspace):
     """Checks and completes what the two attention calls share."""
-    import torch
     B, H, cap, d = shape
     if q.dim() != 3:
         raise ValueError("q must be [B, q_heads, d]")
@@ -184,9 +188,9 @@ def decode_attend_scored(q, k_cache, v_cache, len_, score=None, *, decay=1.0, ou
     _check("v_cache", v_cache, k_cache.shape, q.dtype, dev)
     q_heads, out, workspace, ws_bytes = _attend_args("snapkv_decode_attend_scored", q, k_cache.shape, dev, len_,
                                                      score, out, workspace)
-    _call("snapkv_decode_attend_scored", dev, stream, _sk._ptr(q), _sk._ptr(k_cache), _sk._ptr(v_cache), cap,
-          _sk._ptr(len_), _sk._ptr(score), float(decay), _sk._ptr(out), B, q_heads, H, d, _sk._dtype_code(q),
-          _sk._ptr(workspace), ws_bytes, _status(dev_status, dev))
+    _call("snapkv_decode_attend_scored", dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), cap,
+          _ptr(len_), _ptr(score), float(decay), _ptr(out), B, q_heads, H, d, _sk._dtype_code(q),
+          _ptr(workspace), ws_bytes, _status(dev_status, dev))
     return out
 
 
@@ -196,8 +200,8 @@ def q4_decode_attend(q, cache, len_, score=None, *, decay=1.0, out=None, workspa
     dev = cache.device
     q_heads, out, workspace, ws_bytes = _attend_args("snapkv_q4_decode_attend", q, cache.shape, dev, len_, score,
                                                      out, workspace)
-    _call("snapkv_q4_decode_attend", dev, stream, _sk._ptr(q), cache._struct(), _sk._ptr(len_), _sk._ptr(score),
-          float(decay), _sk._ptr(out), q_heads, _sk._dtype_code(q), _sk._ptr(workspace), ws_bytes,
+    _call("snapkv_q4_decode_attend", dev, stream, _ptr(q), cache._struct(), _ptr(len_), _ptr(score),
+          float(decay), _ptr(out), q_heads, _sk._dtype_code(q), _ptr(workspace), ws_bytes,
           _status(dev_status, dev))
     return out
 
@@ -205,7 +209,6 @@ def q4_decode_attend(q, cache, len_, score=None, *, decay=1.0, out=None, workspa
 def q4_append(cache, k_new, v_new, len_in, len_out=None, *, n_new=None, dev_status=None, stream=None):
     """snapkv_q4_append: quantises k_new, v_new [B,H,rows,d] (or [B,H,d], one row) into rows len_in[b] on of a
     Q4Cache, n_new[b] of them if given. Returns len_out [B] (len_in is only read)."""
-    import torch
     B, H, cap, d = cache.shape
     dev = cache.device
     rows = k_new.shape[2] if k_new.dim() == 4 else 1
@@ -218,15 +221,14 @@ def q4_append(cache, k_new, v_new, len_in, len_out=None, *, n_new=None, dev_stat
     if len_out is None:
         len_out = torch.empty_like(len_in)
     _lengths("len_out", len_out, B, dev)
-    _call("snapkv_q4_append", dev, stream, cache._struct(), _sk._ptr(k_new), _sk._ptr(v_new), rows,
-          _sk._ptr(n_new), _sk._ptr(len_in), _sk._ptr(len_out), _sk._dtype_code(k_new), _status(dev_status, dev))
+    _call("snapkv_q4_append", dev, stream, cache._struct(), _ptr(k_new), _ptr(v_new), rows,
+          _ptr(n_new), _ptr(len_in), _ptr(len_out), _sk._dtype_code(k_new), _status(dev_status, dev))
     return len_out
 
 
 def q4_read(cache, rows, *, start=None, dtype=None, k_out=None, v_out=None, stream=None):
     """snapkv_q4_read: the values (dtype: bf16 or fp32, default bf16) that rows start[b] .. start[b] + rows - 1
     of a Q4Cache stand for, as k, v [B,H,rows,d]; rows outside the cache are zeros."""
-    import torch
     B, H, cap, d = cache.shape
     dev = cache.device
     if dtype is None:
@@ -237,14 +239,13 @@ def q4_read(cache, rows, *, start=None, dtype=None, k_out=None, v_out=None, stre
     v_out = torch.empty((B, H, rows, d), dtype=dtype, device=dev) if v_out is None else v_out
     _check("k_out", k_out, (B, H, rows, d), dtype, dev)
     _check("v_out", v_out, (B, H, rows, d), dtype, dev)
-    _call("snapkv_q4_read", dev, stream, cache._struct(), _sk._ptr(start), int(rows), _sk._ptr(k_out),
-          _sk._ptr(v_out), _sk._dtype_code(k_out))
+    _call("snapkv_q4_read", dev, stream, cache._struct(), _ptr(start), int(rows), _ptr(k_out),
+          _ptr(v_out), _sk._dtype_code(k_out))
     return k_out, v_out
 
 
 def _evict_args(shape, dev, score, len_in, len_out, keep, recent, idx_out, want_idx, workspace):
     """Checks and completes what the two evictions share."""
-    import torch
     B, H, cap, d = shape
     _check("score", score, (B, H, cap), torch.float32, dev)
     _lengths("len_in", len_in, B, dev)
@@ -273,9 +274,9 @@ def evict(k_cache, v_cache, score, len_in, len_out=None, *, keep, recent, idx_ou
     _check("v_cache", v_cache, k_cache.shape, k_cache.dtype, dev)
     len_out, idx_out, workspace, ws_bytes = _evict_args(k_cache.shape, dev, score, len_in, len_out, keep, recent,
                                                         idx_out, want_idx, workspace)
-    _call("snapkv_evict", dev, stream, _sk._ptr(k_cache), _sk._ptr(v_cache), cap, _sk._ptr(score),
-          _sk._ptr(len_in), _sk._ptr(len_out), int(keep), int(recent), _sk._ptr(idx_out), B, H, d,
-          _sk._dtype_code(k_cache), _sk._ptr(workspace), ws_bytes, _status(dev_status, dev))
+    _call("snapkv_evict", dev, stream, _ptr(k_cache), _ptr(v_cache), cap, _ptr(score),
+          _ptr(len_in), _ptr(len_out), int(keep), int(recent), _ptr(idx_out), B, H, d,
+          _sk._dtype_code(k_cache), _ptr(workspace), ws_bytes, _status(dev_status, dev))
     return len_out, idx_out
 
 
@@ -285,6 +286,6 @@ def q4_evict(cache, score, len_in, len_out=None, *, keep, recent, idx_out=None, 
     dev = cache.device
     len_out, idx_out, workspace, ws_bytes = _evict_args(cache.shape, dev, score, len_in, len_out, keep, recent,
                                                         idx_out, want_idx, workspace)
-    _call("snapkv_q4_evict", dev, stream, cache._struct(), _sk._ptr(score), _sk._ptr(len_in), _sk._ptr(len_out),
-          int(keep), int(recent), _sk._ptr(idx_out), _sk._ptr(workspace), ws_bytes, _status(dev_status, dev))
+    _call("snapkv_q4_evict", dev, stream, cache._struct(), _ptr(score), _ptr(len_in), _ptr(len_out),
+          int(keep), int(recent), _ptr(idx_out), _ptr(workspace), ws_bytes, _status(dev_status, dev))
     return len_out, idx_out

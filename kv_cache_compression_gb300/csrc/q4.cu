@@ -47,30 +47,69 @@ __device__ __forceinline__ void store8(float* p, const float* x) {
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// The level numbers of eight values as nibbles. (x - z) / (2h) + 7.5 is rounded to the nearest whole
-// number, ties to even, as if computed exactly: a product with the reciprocal decides wherever the
-// result is not within 2^-14 of a tie (its error is below 16 * 3 * 2^-24 there), a 64-bit division
-// the rest. Ties are not rare: bf16 rows hold small multiples of their group's step.
-__device__ __forceinline__ uint32_t levels(const float* x, float h, float z) {
-  const float r = 1.0f / (2.0f * h);
-  uint32_t u = 0;
-  float near = 0.f;   // how far from a whole number, at most
+// Two fp32 operations in one instruction (each rounded as usual).
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return r;
+}
+
+// The level numbers of eight values as nibbles, in q4_pack's order. (x - z) / (2h) + 7.5 has to be
+// rounded as if computed exactly: ties are common (0.7 % of normal bf16 values lie half-way between
+// two levels). So no quotient is trusted: a product with r = 1 / (2h) only finds the nearest border
+// between levels, z + 2h k, and the sign of x - z - 2h k, exact in fp32 up to the difference's own
+// rounding error (which kExact puts back; bf16 values leave none that a border is near to), says on
+// which side x lies. The border's error of one does not matter where it can occur, half-way between two
+// borders. On the border itself the even level wins: level numbers there are k + 7 and k + 8.
+// kClamp is for groups whose rounded h and z leave a value more than a step outside the levels.
+template <bool kExact, bool kClamp> __device__ __forceinline__ uint32_t levels(const float* x, float h, float z, float r) {
+  constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: adding it rounds to a whole number, in the low bits
+  const float nz = 0.0f - z;              // (not -z: x + nz is never -0)
+  const float2 nz2 = make_float2(nz, nz), r2 = make_float2(r, r), magic = make_float2(kMagic, kMagic),
+               unmagic = make_float2(-kMagic, -kMagic), step = make_float2(-2.0f * h, -2.0f * h);
+  float whole[8], side[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float y = fminf(fmaxf(fmaf(x[e] - z, r, 7.5f), 0.0f), 15.0f);
-    const float whole = y + 12582912.0f;   // 1.5 * 2^23: the low bits become rint(y)
-    near = fmaxf(near, fabsf(y - (whole - 12582912.0f)));
-    u |= (__float_as_uint(whole) & 15u) << (4 * e);
-  }
-  if (near > 0.5f - 0x1p-14f) {
-    u = 0;
-#pragma unroll 1
-    for (int e = 0; e < 8; ++e) {
-      const double y = ((double)x[e] - (double)z) / (2.0 * (double)h) + 7.5;
-      u |= (uint32_t)(int)rint(fmin(fmax(y, 0.0), 15.0)) << (4 * e);
+  for (int e = 0; e < 8; e += 2) {
+    const float2 v = make_float2(x[e], x[e + 1]);
+    const float2 d = add2(v, nz2);
+    float2 w = fma2(d, r2, magic);
+    if (kClamp) {
+      w.x = fminf(fmaxf(w.x, kMagic - 7.0f), kMagic + 7.0f);
+      w.y = fminf(fmaxf(w.y, kMagic - 7.0f), kMagic + 7.0f);
     }
+    float2 s = fma2(add2(w, unmagic), step, d);
+    if (kExact) {
+      const float bx = d.x - v.x, by = d.y - v.y;
+      s.x += (v.x - (d.x - bx)) + (nz - bx);
+      s.y += (v.y - (d.y - by)) + (nz - by);
+    }
+    whole[e] = w.x;
+    whole[e + 1] = w.y;
+    side[e] = s.x;
+    side[e + 1] = s.y;
   }
-  return u;
+  // k + 8, less one below the border, or on it if that is odd: (bits of s) - (k & 1) is negative just then.
+  constexpr int kOrder[8] = {5, 7, 1, 3, 4, 6, 0, 2};   // from the top nibble down
+  uint32_t u = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t k = __float_as_uint(whole[kOrder[i]]);
+    const int below = (__float_as_int(side[kOrder[i]]) - (int)(k & 1u)) >> 31;
+    u = u * 16u + k + (uint32_t)below;
+  }
+  // each k came with the bits of 1.5 * 2^23, and 8 is still missing: whole nibbles again, mod 2^32
+  constexpr uint32_t kBits = 0x4B400000u;
+  constexpr uint32_t kAll = kBits * 0x11111111u;
+  return u - kAll + 0x88888888u;
 }
 
 template <typename T, int D>
@@ -129,8 +168,8 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(Q4Job a) {
     const float diff = hi - lo;
     const float back = hi - diff;
     const float err = (hi - (diff + back)) + (back - lo);
-    float q = __fdiv_rn(diff, 30.0f);
-    q += (fmaf(-q, 30.0f, diff) + err) * (1.0f / 30.0f);
+    float q = diff * (1.0f / 30.0f);
+    q = fmaf(fmaf(-q, 30.0f, diff) + err, 1.0f / 30.0f, q);
     __nv_bfloat16 hb = __float2bfloat16_rn(q), zb = __float2bfloat16_rn(0.5f * (hi + lo));
     float h = __bfloat162float(hb), z = __bfloat162float(zb);
     if (h < 0x1p-126f) h = 0.f;
@@ -138,7 +177,9 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(Q4Job a) {
     if (!(h < INFINITY) || !(fabsf(z) < INFINITY)) {
       h = z = __uint_as_float(0x7FC00000u);
     } else if (h > 0.f) {
-      u = levels(x, h, z);
+      const float r = __fdividef(1.0f, 2.0f * h);
+      constexpr bool kExact = sizeof(T) == 4;
+      u = fmaxf(hi - z, z - lo) < 15.9f * h ? levels<kExact, false>(x, h, z, r) : levels<kExact, true>(x, h, z, r);
     }
     if (mine) {
       codes[row * (D / 8) + q4_word<kNg>(g, o)] = q4_pack(u);

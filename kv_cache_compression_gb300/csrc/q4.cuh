@@ -31,19 +31,14 @@ __device__ __forceinline__ void q4_operands(uint32_t w, uint32_t s, uint32_t* ou
 // Word index, within a row of NG groups, of channels 8 * o .. 8 * o + 7 of group g.
 template <int NG> __device__ __forceinline__ constexpr int q4_word(int g, int o) { return NG * o + g; }
 
-// Packs eight level numbers, given as nibbles u of x (channel e in bits 4e .. 4e + 3), into a word.
+// Packs eight level numbers u of channels 0 .. 7, given as nibbles in the order (from bit 0 up)
+// 2 0 6 4 3 1 7 5, into a word. In that order each half has its pairs' nibbles as [2 3 | 0 1], so that two
+// of the four m fields are in place and two are one bit off, and the signs are a byte swap away.
 __device__ __forceinline__ uint32_t q4_pack(uint32_t x) {
-  const uint32_t neg = ~x & 0x88888888u;              // u < 8: t negative
-  const uint32_t mag = (x ^ ((neg >> 3) * 7u)) & 0x77777777u;   // u - 8, or 7 - u
-  uint32_t w = 0;
-  constexpr int kSign[4] = {15, 14, 7, 6}, kMag[4] = {3, 0, 11, 8};
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int at = 16 * (e & 1), j = e >> 1;
-    w |= ((neg >> (4 * e + 3)) & 1u) << (at + kSign[j]);
-    w |= ((mag >> (4 * e)) & 7u) << (at + kMag[j]);
-  }
-  return w;
+  const uint32_t neg = ~x & 0x88888888u;                               // u < 8: t negative
+  const uint32_t mag = (x ^ (neg - (neg >> 3))) & 0x77777777u;         // u - 8, or 7 - u
+  const uint32_t s = prmt(neg, neg, 0x2301);
+  return (mag & 0x07070707u) | ((mag >> 1) & 0x38383838u) | (s & 0x80808080u) | ((s << 3) & 0x40404040u);
 }
 
 // The level of channel e (0 .. 7) of a word.

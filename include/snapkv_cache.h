@@ -42,11 +42,11 @@ extern "C" {
  * dtype    snapkv_dtype of q, k_cache, v_cache and out. Products and sums are of fp32 accuracy: bf16
  *          weights enter the second product as two bf16 parts, fp32 values as three.
  * workspace device, >= snapkv_scored_workspace_size(...) bytes, 256-byte aligned (contents on entry
- *          do not matter); not used, and may be NULL, without a score
+ *          do not matter); `scored` says whether a score is given (its logits then need most of the room)
  * Sums run in a fixed order: the same call on the same device gives the same bits.
  */
 SNAPKV_API size_t snapkv_scored_workspace_size(int32_t batch, int32_t q_heads, int32_t heads, int32_t head_dim,
-                                               int64_t cap);
+                                               int64_t cap, int32_t scored);
 SNAPKV_API snapkv_status snapkv_decode_attend_scored(const void* q, const void* k_cache, const void* v_cache,
                                                      int64_t cap, const int32_t* len, float* score, float decay,
                                                      void* out, int32_t batch, int32_t q_heads, int32_t heads,

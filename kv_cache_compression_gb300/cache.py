@@ -37,7 +37,7 @@ def lib():
         P, I32, I64, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
         C = ctypes.POINTER(_Q4Struct)
         for name, res, args in [
-                ("snapkv_scored_workspace_size", SZ, [I32, I32, I32, I32, I64]),
+                ("snapkv_scored_workspace_size", SZ, [I32, I32, I32, I32, I64, I32]),
                 ("snapkv_decode_attend_scored", I32,
                  [P, P, P, I64, P, P, F, P, I32, I32, I32, I32, I32, P, SZ, P, P]),
                 ("snapkv_q4_append", I32, [C, P, P, I64, P, P, P, I32, P, P]),
@@ -145,8 +145,8 @@ class Q4Cache:
 
 
 @lru_cache(maxsize=256)
-def scored_workspace_size(batch, q_heads, heads, head_dim, cap) -> int:
-    return int(lib().snapkv_scored_workspace_size(batch, q_heads, heads, head_dim, cap))
+def scored_workspace_size(batch, q_heads, heads, head_dim, cap, scored=True) -> int:
+    return int(lib().snapkv_scored_workspace_size(batch, q_heads, heads, head_dim, cap, bool(scored)))
 
 
 @lru_cache(maxsize=256)
@@ -169,10 +169,8 @@ def _attend_args(where, q, shape, dev, len_, score, out, workspace):
     _check("out", out, q.shape, q.dtype, dev)
     if score is not None:
         _check("score", score, (B, H, cap), torch.float32, dev)
-        workspace = _room(workspace, scored_workspace_size(B, q_heads, H, d, cap), dev)
-    else:
-        workspace = None
-    return q_heads, out, workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace = _room(workspace, scored_workspace_size(B, q_heads, H, d, cap, score is not None), dev)
+    return q_heads, out, workspace, workspace.numel() * workspace.element_size()
 
 
 def decode_attend_scored(q, k_cache, v_cache, len_, score=None, *, decay=1.0, out=None, workspace=None,

@@ -3,28 +3,36 @@
 //   s_gr = q_g . k_r / sqrt(d),  p_gr = softmax over r < len,  o_g = sum_r p_gr v_r
 //   score_r = decay * score_r + sum_g p_gr
 //
-// One thread-block cluster per (sequence, KV head); its CTAs take equal spans of the head's rows,
-// the warps of a CTA every kWarps-th tile of the span. A warp runs an online softmax (running
-// maximum m and sum l per query, output o not yet normalised, logits in the log2 domain) over its
-// tiles; warps meet in shared memory, CTAs through distributed shared memory, and the last step
-// normalises. A score needs the final maximum and sum, so the logits of a span wait in shared memory
-// (or, where they do not fit, in the workspace) and are turned into weights after that meeting:
-// rows are read once, in one launch.
+// Two launches. The first walks all tiles (a few dozen rows of one head) of all heads as one flat list,
+// of which every CTA of one wave takes an equal, contiguous share, whatever the sequences' lengths: a
+// CTA's share covers the end of one head, whole heads, and the start of another. A warp takes every
+// kWarps-th tile of the share with an online softmax (running maximum m and sum l per query, output o
+// not yet normalised, logits in the log2 domain); at the end of a head the CTA's warps meet in shared
+// memory. A head that lies in one share is finished there; the parts of others, and the logits that a
+// score will need, go to the workspace. The second launch joins the parts and turns logits into
+// weights. It is released early (programmatic dependent launch) and waits on the device for the first.
+// Rows are read once. (One cluster per head with the logits in shared memory, and everything in one
+// launch, was measured first: 222 us where this takes 105 on 2048 4-bit heads of 2208 rows, as whole
+// clusters wait for their longest part, and shared memory left four to eight warps per SM.)
 //
-// Both products run on the tensor cores as m16n8k16 with eight queries: q K^T has the queries as
-// rows 0 .. 7 of A and eight cached rows as the columns of B; P V has the weights as A, which the
-// first product's accumulators already are, lane for lane. Rows 8 .. 15 of A are not wasted: they hold
-// the same queries' second bf16 part, so that a weight enters the second product with 16 bits of
-// mantissa. fp32 calls split q, p and the cached values into three bf16 parts (24 bits); a product
-// drops nothing above 2^-24 of its factors.
+// Both products run on the tensor cores as m16n8k16 with eight queries as the columns: K Q^T has sixteen
+// cached rows by sixteen channels as A, V^T P^T sixteen channels by sixteen cached rows. Weights cross
+// from one's accumulators to the other's B operand by an 8 x 8 transpose in registers (movmatrix). They
+// enter the second product in two bf16 parts (16 bits of mantissa); fp32 calls split q, p and the cached
+// values into three (24 bits) and drop nothing above 2^-24 of a product's factors. (With the queries as
+// rows of A in the first product no transpose is needed, but half of A is zeros, which cost twice the
+// instructions and, as A takes four neighbouring registers, moves around each: 475 instructions per
+// 16 rows of 4-bit K and V against 300.)
 //
 // With a decode step's few queries the kernel is bound by the cache's bytes. Legacy mma.sync is fast
 // enough for that (128 cached values per instruction, against about 50 per clock and SM that HBM
 // delivers at 4 bits), and unlike tcgen05.mma it takes levels and weights from registers, where
 // unpacking and the softmax leave them.
 //
-// Each warp moves its own tiles with cp.async through a ring of its own, so warps never wait for
-// one another inside the row loop.
+// Each warp moves its own tiles with cp.async through a ring of its own, which runs ahead across the
+// ends of heads, so warps wait for one another only where a head ends.
+#include <type_traits>
+
 #include "cache_internal.h"
 #include "q4.cuh"
 #include "sm100_ptx.cuh"
@@ -32,9 +40,6 @@
 
 namespace snapkv {
 namespace {
-
-constexpr int kMaxCluster = 8;
-constexpr int kLogitsSmem = 64 * 1024;   // a span's logits stay in shared memory up to this size
 
 struct AttendArgs {
   const void* q;
@@ -44,16 +49,79 @@ struct AttendArgs {
   const uint8_t* vm;
   const int32_t* len;
   float* score;
-  float* logits;      // null: in shared memory
   void* out;
   float decay, scale_log2;
   int64_t cap;
-  int heads, group;
+  int batch, heads, group;
+  int passes, tile_q;   // queries are served tile_q at a time (the last of `passes` passes may have fewer)
+  int ctas;             // of the first launch
+  // workspace: a head is (sequence, KV head, pass) here
+  float* logits;        // [heads][cap][tile_q] (scores only)
+  float* stats;         // [heads][2][tile_q]: maximum and sum of a head that one CTA finished
+  float* parts;         // [ctas][2] of (o [tile_q][D], m [tile_q], l [tile_q])
   int32_t* dev_status;
 };
 
+// The CTAs of the first launch that get a share: no more than give every warp a tile.
+constexpr int kWarps = 4;
+__device__ __forceinline__ int working_ctas(int64_t total, int ctas) {
+  const int64_t most = (total + kWarps - 1) / kWarps;
+  return most < ctas ? (int)most : ctas;
+}
+
+// The first launch's schedule. Flat tile index = (tiles of the sequences before, times heads per
+// sequence) + (head within the sequence) * tiles + tile.
+struct Plan {
+  int64_t total;         // tiles
+  int64_t before;        // tiles per head of the sequences before the sought one
+  int seq;               // the sought sequence
+  int ctas;
+};
+
+__device__ __forceinline__ int64_t share_start(int64_t total, int ctas, int c) {
+  // total * c / ctas without overflow: total < 2^43, c <= ctas <= 1024
+  return total * c / ctas;
+}
+
+// The CTA whose share holds flat tile t.
+__device__ __forceinline__ int share_of(int64_t total, int ctas, int64_t t) {
+  int c = (int)(t * ctas / total);
+  while (c > 0 && share_start(total, ctas, c) > t) --c;
+  while (share_start(total, ctas, c + 1) <= t) ++c;
+  return c;
+}
+
+__device__ __forceinline__ int visible_rows(const AttendArgs& a, int b) {
+  const int n = a.len[b];
+  return n < 0 ? 0 : (int64_t)n > a.cap ? (int)a.cap : n;
+}
+
+// Exclusive sum over the block of v (thread order) and the block's total.
+template <int THREADS> __device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t* sums, int64_t* total) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int64_t x = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += sums[w];
+    all += sums[w];
+  }
+  *total = all;
+  return before + x - v;
+}
+
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
 }
 template <int N> __device__ __forceinline__ void cp_async_small(void* dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(ptx::smem_u32(dst)), "l"(src), "n"(N), "r"(bytes) : "memory");
@@ -63,18 +131,41 @@ template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.as
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two fp32 values as a bf16 pair (x in the low half), and what that leaves of them.
-__device__ __forceinline__ uint32_t split2(float& x, float& y) {
-  const __nv_bfloat162 two = __floats2bfloat162_rn(x, y);
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(&two);
-  x -= __uint_as_float(w << 16);
-  y -= __uint_as_float(w & 0xFFFF0000u);
+// Transposes an 8 x 8 matrix of 16-bit elements that the warp holds a row per four lanes.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// Four 8 x 8 matrices of 16-bit elements, their 16-byte rows at the addresses of lanes 0 .. 7, 8 .. 15, ...
+template <bool TRANS> __device__ __forceinline__ void load_matrices(const void* row, uint32_t (&x)[4]) {
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(ptx::smem_u32(row)) : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(ptx::smem_u32(row)) : "memory");
+}
+
+// Two fp32 values as a bf16 pair (x in the low half).
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+  const __nv_bfloat162 two = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&two);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+// The pair, and in v what `share` times it leaves of the values.
+__device__ __forceinline__ uint32_t split2(float2& v, float share = 1.0f) {
+  const uint32_t w = pack2(v);
+  v = fma2(unpack2(w), make_float2(-share, -share), v);
   return w;
 }
 
@@ -91,19 +182,18 @@ constexpr float kQ4P = 0x1p80f, kQ4OutEven = 0x1p51f, kQ4OutOdd = 0x1p53f;
 // Format Q4 (codes and pairs) or dense rows of IO; IO is the type of q and out.
 template <bool Q4, typename IO, int D> struct Shape {
   static constexpr bool kWide = sizeof(IO) == 4;                    // fp32: three bf16 parts
+  static constexpr int kParts = kWide ? 3 : 2;                      // of a weight
   static constexpr int kNg = D / kQ4Group;
   static constexpr int kRow = Q4 ? D / 2 : D * (int)sizeof(IO);     // bytes of a row of K (and of V)
   static constexpr int kMeta = Q4 ? 4 * kNg : 0;
-  // Rows of a tile: 4 to 9 KB of K and V together.
-  static constexpr int kTile = Q4 ? 32 : (kRow >= 256 ? 16 : 32);
-  static constexpr int kStage = 2 * kTile * (kRow + kMeta);
-  static constexpr int kStages = Q4 ? 4 : (kRow >= 512 ? 2 : 3);
-  static constexpr int kWarps = 4;
+  static constexpr int kTile = Q4 ? 32 : (kRow >= 256 ? 16 : 32);   // rows
+  static constexpr int kStage = 2 * kTile * (kRow + kMeta);         // 4 to 16 KB of K and V together
+  static constexpr int kStages = 3;
+  static constexpr int kWarps = snapkv::kWarps;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRing = kWarps * kStages * kStage;
-  // After the row loop the ring holds the warps' partial outputs, then the CTA's.
-  static constexpr int kMerge = (kWarps + 1) * kQueryTile * D * 4;
-  static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kCtasPerSm = Q4 ? (kWide ? 2 : 3) : kRow >= 512 ? 1 : 2;   // what the ring leaves room for
+  static constexpr int smem(int tile_q) { return kRing + kWarps * tile_q * D * 4; }
 };
 
 // 16-byte pieces of a row are stored XORed with the row's low three bits where rows are a multiple of
@@ -114,405 +204,537 @@ template <int ROW> __device__ __forceinline__ uint32_t piece_at(int row, int pie
   return row * ROW + (piece << 4);
 }
 
-template <bool Q4, typename IO, int D>
-__global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads) attend_kernel(AttendArgs a) {
+// NG 32-bit words of shared memory (the second is 0 where there is one).
+template <int NG> __device__ __forceinline__ uint2 load_words(const uint8_t* at) {
+  if constexpr (NG == 2) return *reinterpret_cast<const uint2*>(at);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(at), 0u);
+}
+
+// Row j of an 8-row tile. Where the second product gathers its rows by hand, they are mixed so that the
+// rows 2 i and 2 i + 1 of the four lanes that read together lie in different banks.
+template <bool MIXED> __device__ __forceinline__ int row_of(int j) { return MIXED ? (j >> 1) + 4 * (j & 1) : j; }
+
+// FOUR (bf16, at most four queries a pass): the second product's columns 4 .. 7 are the second parts of
+// the weights in columns 0 .. 3, and one instruction does for both. The first product then has every
+// query twice.
+template <bool Q4, typename IO, int D, bool FOUR>
+__global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::kCtasPerSm) attend_kernel(AttendArgs a) {
   using S = Shape<Q4, IO, D>;
+  static_assert(!FOUR || !S::kWide, "two parts");
+  constexpr int kParts = FOUR ? 1 : S::kParts;
   constexpr int kSteps = D / 16;          // 16-channel steps of the first product
-  constexpr int kCols = D / 8;            // 8-channel column tiles of the second
+  constexpr int kPairs = D / 16;          // 16-channel tiles of the second: two of a lane's D / 8 channels
   constexpr int kSub = S::kTile / 16;     // 16-row parts of a tile
   constexpr int kNg = S::kNg;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float warp_m[S::kWarps][kQueryTile], warp_l[S::kWarps][kQueryTile];
-  __shared__ float cta_m[kQueryTile], cta_l[kQueryTile];   // read by the whole cluster
-  __shared__ float head_m[kQueryTile], head_r[kQueryTile]; // the head's maximum, and 1 / its sum
+  __shared__ int64_t sums[S::kWarps];
+  __shared__ Plan plan;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int qi = lane / 4, li = lane % 4;   // this lane's query (or column), and its place among four
-  const uint32_t rank = ptx::cluster_rank(), csize = ptx::cluster_size();
-  const int64_t bh = blockIdx.x / csize;
-  const int b = (int)(bh / a.heads);
-  int n = a.len[b];
-  if ((int64_t)n > a.cap) {
-    if (rank == 0 && tid == 0 && bh % a.heads == 0) report(a.dev_status, SNAPKV_ERR_CAPACITY);
-    n = (int)a.cap;
-  }
-  if (n < 0) n = 0;
-  // Spans are whole tiles; r1 - r0 is 0 for CTAs past the end.
-  const int per = ((n + (int)csize - 1) / (int)csize + S::kTile - 1) / S::kTile * S::kTile;
-  const int r0 = min((int64_t)n, (int64_t)rank * per), r1 = min((int64_t)n, (int64_t)r0 + per);
-  const int tiles = (r1 - r0 + S::kTile - 1) / S::kTile;
-  const uint8_t* kc = a.k + bh * a.cap * S::kRow;
-  const uint8_t* vc = a.v + bh * a.cap * S::kRow;
-  const uint8_t* kmc = Q4 ? a.km + bh * a.cap * S::kMeta : nullptr;
-  const uint8_t* vmc = Q4 ? a.vm + bh * a.cap * S::kMeta : nullptr;
-  uint8_t* ring = smem + warp * (S::kStages * S::kStage);
+  // In accumulators a lane holds row (K Q^T) or channel (V^T P^T) j and j + 8 of 16 for queries qa and qa + 1; in
+  // operands it holds column j, or rows j and j + 8, at places 2 i, 2 i + 1, 2 i + 8 and 2 i + 9 along k.
+  const int j = lane / 4, i = lane % 4;
+  const int qa = FOUR ? 2 * i % 4 : 2 * i;
+  const float part2 = FOUR && i >= 2 ? 1.0f : 0.0f;   // this lane's columns are second parts
+  const int jrow = row_of<Q4 || S::kWide>(j);         // row j of an 8-row tile, as it lies in the cache
+  const int per_seq = a.heads * a.passes;   // heads of a sequence
+  const Q4Ones ones;
 
-  // Copies tile t of the span into ring slot `slot`; rows at or past r1 become zeros, whatever the
-  // cache holds there.
-  auto fetch = [&](int t, int slot) {
-    uint8_t* dst = ring + slot * S::kStage;
-    const int base = r0 + t * S::kTile;
-    constexpr int kPieces = S::kRow / 16, kAll = S::kTile * kPieces;
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const uint8_t* src = kv ? vc : kc;
-      uint8_t* to = dst + kv * (S::kTile * S::kRow);
-#pragma unroll
-      for (int j = 0; j < kAll / 32; ++j) {
-        const int u = lane + 32 * j, row = u / kPieces, piece = u % kPieces;
-        const bool in = base + row < r1;
-        cp_async16(to + piece_at<S::kRow>(row, piece), src + (int64_t)(in ? base + row : r0) * S::kRow + piece * 16, in ? 16 : 0);
-      }
-      if constexpr (Q4) {
-        const uint8_t* msrc = kv ? vmc : kmc;
-        uint8_t* mto = dst + 2 * (S::kTile * S::kRow) + kv * (S::kTile * S::kMeta);
-#pragma unroll
-        for (int j = 0; j < (S::kTile + 31) / 32; ++j) {
-          const int row = lane + 32 * j;
-          const bool in = base + row < r1;
-          cp_async_small<S::kMeta>(mto + row * S::kMeta, msrc + (int64_t)(in ? base + row : r0) * S::kMeta, in ? S::kMeta : 0);
+  // ---- this CTA's share of the tiles, and the sequence it starts in
+  {
+    const int chunk = (a.batch + S::kThreads - 1) / S::kThreads;
+    const int b0 = min(a.batch, tid * chunk), b1 = min(a.batch, b0 + chunk);
+    int64_t mine = 0, total;
+    for (int b = b0; b < b1; ++b) {
+      mine += (visible_rows(a, b) + S::kTile - 1) / S::kTile;
+      if (blockIdx.x == 0 && (int64_t)a.len[b] > a.cap) report(a.dev_status, SNAPKV_ERR_CAPACITY);
+    }
+    int64_t before = block_scan64<S::kThreads>(mine, sums, &total);
+    const int ctas = working_ctas(total * per_seq, a.ctas);
+    if ((int)blockIdx.x >= ctas) return;   // (the whole block)
+    const int64_t start = share_start(total * per_seq, ctas, (int)blockIdx.x);
+    if (tid == 0) {
+      plan.total = total * per_seq;
+      plan.ctas = ctas;
+    }
+    if (start >= before * per_seq && start < (before + mine) * per_seq)
+      for (int b = b0; b < b1; ++b) {
+        const int tiles = (visible_rows(a, b) + S::kTile - 1) / S::kTile;
+        if (start < (before + tiles) * per_seq) {
+          plan.before = before;
+          plan.seq = b;
+          break;
         }
+        before += tiles;
+      }
+    __syncthreads();
+  }
+  int64_t at = share_start(plan.total, plan.ctas, (int)blockIdx.x);
+  const int64_t end = share_start(plan.total, plan.ctas, (int)blockIdx.x + 1);   // > at
+
+  // A place in the list: a tile of a head, and what its addresses need.
+  struct Place {
+    int seq, head, rows, tiles, tile;   // head: within the sequence, over passes
+  };
+  Place here;
+  here.seq = plan.seq;
+  here.rows = visible_rows(a, here.seq);
+  here.tiles = (here.rows + S::kTile - 1) / S::kTile;
+  {
+    const int64_t in_seq = at - plan.before * per_seq;
+    here.head = (int)(in_seq / here.tiles);
+    here.tile = (int)(in_seq - (int64_t)here.head * here.tiles);
+  }
+  // Moves p, whose tile may have run past its head, to the head that holds it (which exists).
+  auto settle = [&](Place& p) {
+    while (p.tile >= p.tiles) {
+      p.tile -= p.tiles;
+      if (++p.head == per_seq) {
+        p.head = 0;
+        do {
+          p.rows = visible_rows(a, ++p.seq);
+          p.tiles = (p.rows + S::kTile - 1) / S::kTile;
+        } while (p.tiles == 0);
       }
     }
   };
 
-  const int passes = (a.group + kQueryTile - 1) / kQueryTile;
-  for (int pass = 0; pass < passes; ++pass) {
-    const int tile_q = min(kQueryTile, a.group - pass * kQueryTile);   // queries of this pass
-    const int64_t q0 = bh * a.group + pass * kQueryTile;
-    const bool live = qi < tile_q;
-    float* logits = a.logits ? a.logits + (bh * a.cap + r0) * min(kQueryTile, a.group)
-                             : reinterpret_cast<float*>(smem + S::kSmem);
+  uint8_t* ring = smem + warp * (S::kStages * S::kStage);
+  float* meet = reinterpret_cast<float*>(smem + S::kRing);   // [kWarps][tile_q][D]
 
-    // The ring starts filling before the queries are looked at.
+  // Copies a tile into ring slot `slot`; rows past the head's end become zeros, whatever the cache holds.
+  auto fetch = [&](const Place& p, int slot) {
+    constexpr int kPieces = S::kRow / 16, kAll = S::kTile * kPieces;
+    uint8_t* dst = ring + slot * S::kStage;
+    const int64_t row0 = ((int64_t)p.seq * a.heads + p.head / a.passes) * a.cap + (int64_t)p.tile * S::kTile;
+    const int left = p.rows - p.tile * S::kTile;   // > 0
+    auto copy = [&](auto whole) {   // whole tiles, all but a head's last, need no look at each row
 #pragma unroll
-    for (int s = 0; s < S::kStages - 1; ++s) {
-      if (warp + s * S::kWarps < tiles) fetch(warp + s * S::kWarps, s);
-      cp_commit();
-    }
-
-    // A operands of the first product: channels c .. c + 3 of query qi for each step, as the lane's
-    // share of the row is laid out (see `first product` below).
-    uint32_t qa[kSteps][S::kWide ? 6 : 2];
-    float qsum[Q4 ? kNg : 1];
-    if constexpr (Q4) {
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint8_t* src = (kv ? a.v : a.k) + row0 * S::kRow + lane * 16;
+        uint8_t* to = dst + kv * (S::kTile * S::kRow);
 #pragma unroll
-      for (int g = 0; g < kNg; ++g) qsum[g] = 0.f;
-    }
-    const IO* qp = static_cast<const IO*>(a.q) + (q0 + (live ? qi : 0)) * D;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      int c;
-      if constexpr (Q4)
-        c = 64 * (s / 4) + 16 * li + 8 * ((s % 4) / 2) + 4 * (s % 2);
-      else
-        c = S::kWide ? 16 * s + 4 * li : 32 * (s / 2) + 8 * li + 4 * (s % 2);
-      float x[4];
-      if constexpr (S::kWide) {
-        const float4 f = *reinterpret_cast<const float4*>(qp + c);
-        x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
-      } else {
-        const uint2 f = *reinterpret_cast<const uint2*>(qp + c);
-        x[0] = __uint_as_float(f.x << 16); x[1] = __uint_as_float(f.x & 0xFFFF0000u);
-        x[2] = __uint_as_float(f.y << 16); x[3] = __uint_as_float(f.y & 0xFFFF0000u);
+        for (int j = 0; j < kAll / 32; ++j) {
+          const int u = lane + 32 * j, row = u / kPieces, piece = u % kPieces;
+          if constexpr (decltype(whole)::value) {
+            cp_async16(to + piece_at<S::kRow>(row, piece), src + j * 512);
+          } else {
+            const bool in = row < left;
+            cp_async16(to + piece_at<S::kRow>(row, piece), in ? src + j * 512 : src - lane * 16, in ? 16 : 0);
+          }
+        }
+        if constexpr (Q4) {
+          static_assert(S::kTile == 32, "a row's pair per lane");
+          const uint8_t* msrc = (kv ? a.vm : a.km) + row0 * S::kMeta;
+          uint8_t* mto = dst + 2 * (S::kTile * S::kRow) + kv * (S::kTile * S::kMeta) + lane * S::kMeta;
+          if constexpr (decltype(whole)::value) {
+            cp_async_small<S::kMeta>(mto, msrc + lane * S::kMeta, S::kMeta);
+          } else {
+            const bool in = lane < left;
+            cp_async_small<S::kMeta>(mto, msrc + (in ? lane * S::kMeta : 0), in ? S::kMeta : 0);
+          }
+        }
       }
-      if (!live) x[0] = x[1] = x[2] = x[3] = 0.f;
+    };
+    if (left >= S::kTile)
+      copy(std::true_type{});
+    else
+      copy(std::false_type{});
+  };
+
+  // The ring starts filling: tiles at + warp, + kWarps, ...
+  Place ahead = here;
+  int64_t ahead_at = at + warp;
+  ahead.tile += warp;
+  auto fetch_next = [&](int slot) {
+    if (ahead_at < end) {
+      settle(ahead);
+      fetch(ahead, slot);
+      ahead.tile += S::kWarps;
+      ahead_at += S::kWarps;
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < S::kStages - 1; ++s) fetch_next(s);
+  int slot = 0;
+  int64_t mine_at = at + warp;            // this warp's next tile
+  const int64_t share0 = at;
+
+  while (at < end) {   // one head, or the part of it that lies in the share
+    const int pass = here.head % a.passes;
+    const int tile_q = min(a.tile_q, a.group - pass * a.tile_q);
+    const int64_t bh = (int64_t)here.seq * a.heads + here.head / a.passes;
+    const int64_t vh = (int64_t)here.seq * per_seq + here.head;
+    const int64_t q0 = bh * a.group + (int64_t)pass * a.tile_q;
+    const int64_t seg_end = min(end, at + (here.tiles - here.tile));
+    const int n = here.rows;
+    float* logits = a.score ? a.logits + vh * a.cap * a.tile_q : nullptr;
+
+    // B operands of the first product: channels c .. c + 3 of the query of column j for each step, as the
+    // lane's share of the rows is laid out (see `first product` below).
+    const int qcol = FOUR ? j % 4 : j;
+    uint32_t qb[kSteps][S::kWide ? 6 : 2];
+    float qsum[Q4 ? kNg : 1][2];   // per group, of queries qa and qa + 1
+    {
+      const IO* qp = static_cast<const IO*>(a.q) + (q0 + (qcol < tile_q ? qcol : 0)) * D;
+      float sum[Q4 ? kNg : 1] = {};
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        int c;
+        if constexpr (Q4)
+          c = 64 * (s / 4) + 16 * i + 8 * ((s % 4) / 2) + 4 * (s % 2);
+        else
+          c = 16 * s + (S::kWide ? 4 * i : 2 * i);
+        float2 x, y;
+        if constexpr (S::kWide) {
+          const float4 f = *reinterpret_cast<const float4*>(qp + c);
+          x = make_float2(f.x, f.y);
+          y = make_float2(f.z, f.w);
+        } else {
+          const uint32_t* f = reinterpret_cast<const uint32_t*>(qp + c);
+          x = unpack2(f[0]);
+          y = unpack2(f[Q4 ? 1 : 4]);
+        }
+        if (qcol >= tile_q) x = y = make_float2(0.f, 0.f);
+        if constexpr (Q4) {
+          sum[s / 4] += (x.x + x.y) + (y.x + y.y);
+          x = mul2(x, make_float2(kQ4QEven, kQ4QEven));
+          y = mul2(y, make_float2(kQ4QOdd, kQ4QOdd));
+        }
+#pragma unroll
+        for (int part = 0; part < (S::kWide ? 3 : 1); ++part) {
+          qb[s][2 * part] = split2(x);
+          qb[s][2 * part + 1] = split2(y);
+        }
+      }
       if constexpr (Q4) {
-        qsum[s / 4] += (x[0] + x[1]) + (x[2] + x[3]);
-        x[0] *= kQ4QEven; x[1] *= kQ4QEven; x[2] *= kQ4QOdd; x[3] *= kQ4QOdd;
-      }
 #pragma unroll
-      for (int part = 0; part < (S::kWide ? 3 : 1); ++part) {
-        qa[s][2 * part] = split2(x[0], x[1]);
-        qa[s][2 * part + 1] = split2(x[2], x[3]);
-      }
-    }
-    if constexpr (Q4) {
-#pragma unroll
-      for (int g = 0; g < kNg; ++g) {
-        qsum[g] += __shfl_xor_sync(0xffffffffu, qsum[g], 1);
-        qsum[g] += __shfl_xor_sync(0xffffffffu, qsum[g], 2);
-        qsum[g] *= a.scale_log2;
+        for (int g = 0; g < kNg; ++g) {
+          sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+          sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+          sum[g] *= a.scale_log2;
+          qsum[g][0] = __shfl_sync(0xffffffffu, sum[g], 4 * qa);
+          qsum[g][1] = __shfl_sync(0xffffffffu, sum[g], 4 * qa + 4);
+        }
       }
     }
     const float dot_scale = Q4 ? a.scale_log2 * kQ4Dot : a.scale_log2;
 
-    float m = -INFINITY, l = 0.f;
-    float o[kCols][4];
+    // Per query qa, qa + 1:
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // Channel pair t of the lane: [0], [1] its first channel for queries qa, qa + 1; [2], [3] its second.
+    float o[kPairs][4];
 #pragma unroll
-    for (int t = 0; t < kCols; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-    float oz[Q4 ? kNg : 1];
+    for (int t = 0; t < kPairs; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+    float oz[Q4 ? kNg : 1][2];   // sum of p z over this lane's rows
     if constexpr (Q4) {
 #pragma unroll
-      for (int g = 0; g < kNg; ++g) oz[g] = 0.f;
+      for (int g = 0; g < kNg; ++g) oz[g][0] = oz[g][1] = 0.f;
     }
 
-    // A product of A (two or three parts) with one B pair of words whose values need no split.
-    auto mma_parts = [&](float* c, const uint32_t* w, uint32_t b0, uint32_t b1) {
-      if constexpr (S::kWide) {
-        mma16816(c, w[0], w[2], w[1], w[3], b0, b1);
-        mma16816(c, w[4], 0u, w[5], 0u, b0, b1);
-      } else {
-        mma16816(c, w[0], 0u, w[1], 0u, b0, b1);
-      }
+    // First product: B in one part (bf16), or three (fp32).
+    auto mma_q = [&](float* c, const uint32_t* w, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+      for (int part = 0; part < (S::kWide ? 3 : 1); ++part) mma16816(c, a0, a1, a2, a3, w[2 * part], w[2 * part + 1]);
     };
 
-    int slot = 0;
-    for (int t = warp; t < tiles; t += S::kWarps) {
+    // Weights of rows j (x[0]) and j + 8 (x[1]), for queries qa and qa + 1, as B operands in parts.
+    auto weight_parts = [&](float2 (&x)[2], uint32_t (&w)[S::kParts][2]) {
+#pragma unroll
+      for (int part = 0; part < kParts; ++part)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if constexpr (FOUR) {
+            split2(x[half], part2);
+            w[0][half] = transpose8(pack2(x[half]));
+          } else {
+            w[part][half] = transpose8(split2(x[half]));
+          }
+        }
+    };
+
+    for (; mine_at < seg_end; mine_at += S::kWarps) {
       cp_wait<S::kStages - 2>();
       __syncwarp();   // every lane's copies of this tile have landed; the slot before it is free
-      {
-        const int ahead = t + (S::kStages - 1) * S::kWarps;
-        const int into = slot == 0 ? S::kStages - 1 : slot - 1;
-        if (ahead < tiles) fetch(ahead, into);
-        cp_commit();
-      }
+      fetch_next(slot == 0 ? S::kStages - 1 : slot - 1);
       const uint8_t* kt = ring + slot * S::kStage;
       const uint8_t* vt = kt + S::kTile * S::kRow;
       const uint8_t* kmt = kt + 2 * (S::kTile * S::kRow);
       const uint8_t* vmt = kmt + S::kTile * S::kMeta;
       slot = slot + 1 == S::kStages ? 0 : slot + 1;
-      const int base = r0 + t * S::kTile;
+      const int base = (here.tile + (int)(mine_at - at)) * S::kTile;
 
-      // ---- first product: logits of kSub x 16 rows. Column 2i of an 8-row tile is row i, column 2i + 1
-      // row i + 4, so that the rows a lane reads in the second product are neighbours of other lanes' rows.
-      float sv[kSub][4];   // rows li, 4 + li, 8 + li, 12 + li of a part, for query qi
-      const int krow = (qi >> 1) + 4 * (qi & 1);
+      // ---- first product: logits of kSub x 16 rows
+      float sv[kSub][4];   // row j of a part for queries qa, qa + 1, then row j + 8
 #pragma unroll
       for (int sub = 0; sub < kSub; ++sub) {
+        if constexpr (Q4) {
+          uint32_t w[2][2 * kNg];   // words (o = 0, 1; g) of this lane's 16 channels a group, of rows j, j + 8
+          float2 hz[2][kNg];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int row = 16 * sub + 8 * half + krow;
-          if constexpr (Q4) {
-            uint32_t w[2 * kNg];   // words (o = 0, 1; g) of this lane's 16 channels a group
+          for (int half = 0; half < 2; ++half) {
+            const int row = 16 * sub + 8 * half + jrow;
+            const uint2 kz = load_words<kNg>(kmt + row * S::kMeta);
+            hz[half][0] = unpack2(kz.x);
             if constexpr (kNg == 2) {
-              const uint4 x = *reinterpret_cast<const uint4*>(kt + row * S::kRow + 16 * li);
-              w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+              hz[half][1] = unpack2(kz.y);
+              const uint4 x = *reinterpret_cast<const uint4*>(kt + row * S::kRow + 16 * i);
+              w[half][0] = x.x; w[half][1] = x.y; w[half][2] = x.z; w[half][3] = x.w;
             } else {
-              const uint2 x = *reinterpret_cast<const uint2*>(kt + row * S::kRow + 8 * li);
-              w[0] = x.x; w[1] = x.y;
+              const uint2 x = *reinterpret_cast<const uint2*>(kt + row * S::kRow + 8 * i);
+              w[half][0] = x.x; w[half][1] = x.y;
             }
-            float dot[kNg][4];
-#pragma unroll
-            for (int g = 0; g < kNg; ++g) {
-              dot[g][0] = dot[g][1] = dot[g][2] = dot[g][3] = 0.f;
-#pragma unroll
-              for (int o2 = 0; o2 < 2; ++o2) {
-                const uint32_t word = w[q4_word<kNg>(g, o2)];
-                uint32_t e[4];
-                q4_operands(word, prmt(word, word, 0x2301), e);
-                mma_parts(dot[g], qa[4 * g + 2 * o2], e[0], e[1]);
-                mma_parts(dot[g], qa[4 * g + 2 * o2 + 1], e[2], e[3]);
-              }
-            }
-#pragma unroll
-            for (int col = 0; col < 2; ++col) {
-              const int r = 16 * sub + 8 * half + 4 * col + li;
-              float d = 0.f, zq = 0.f;
-#pragma unroll
-              for (int g = 0; g < kNg; ++g) {
-                const uint32_t hz = *reinterpret_cast<const uint32_t*>(kmt + r * S::kMeta + 4 * g);
-                const float x = S::kWide ? dot[g][col] + dot[g][col + 2] : dot[g][col];
-                d = fmaf(__uint_as_float(hz << 16), x, d);
-                zq = fmaf(__uint_as_float(hz & 0xFFFF0000u), qsum[g], zq);
-              }
-              sv[sub][2 * half + col] = fmaf(d, dot_scale, zq);
-            }
-          } else {
-            float dot[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int s4 = 0; s4 < S::kRow / 64; ++s4) {
-              const uint4 x = *reinterpret_cast<const uint4*>(kt + piece_at<S::kRow>(row, 4 * s4 + li));
-              if constexpr (S::kWide) {
-                float f[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};
-                const uint32_t* w = qa[s4];
-#pragma unroll
-                for (int part = 0; part < 3; ++part) {
-                  const uint32_t b0 = split2(f[0], f[1]), b1 = split2(f[2], f[3]);
-                  mma16816(dot, w[0], w[2], w[1], w[3], b0, b1);
-                  if (part == 0) mma16816(dot, w[4], 0u, w[5], 0u, b0, b1);
-                }
-              } else {
-                mma16816(dot, qa[2 * s4][0], 0u, qa[2 * s4][1], 0u, x.x, x.y);
-                mma16816(dot, qa[2 * s4 + 1][0], 0u, qa[2 * s4 + 1][1], 0u, x.z, x.w);
-              }
-            }
-#pragma unroll
-            for (int col = 0; col < 2; ++col)
-              sv[sub][2 * half + col] = (S::kWide ? dot[col] + dot[col + 2] : dot[col]) * dot_scale;
           }
+          float d[4] = {}, zq[4] = {};
+#pragma unroll
+          for (int g = 0; g < kNg; ++g) {
+            float dot[4] = {};
+#pragma unroll
+            for (int o2 = 0; o2 < 2; ++o2) {
+              uint32_t e[2][4];
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const uint32_t word = w[half][q4_word<kNg>(g, o2)];
+                q4_operands(ones, word, prmt(word, word, 0x2301), e[half]);
+              }
+              mma_q(dot, qb[4 * g + 2 * o2], e[0][0], e[1][0], e[0][1], e[1][1]);
+              mma_q(dot, qb[4 * g + 2 * o2 + 1], e[0][2], e[1][2], e[0][3], e[1][3]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              d[e] = fmaf(hz[e / 2][g].x, dot[e], d[e]);
+              zq[e] = fmaf(hz[e / 2][g].y, qsum[g][e % 2], zq[e]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sv[sub][e] = fmaf(d[e], dot_scale, zq[e]);
+        } else if constexpr (S::kWide) {
+          float dot[4] = {};
+#pragma unroll
+          for (int s4 = 0; s4 < kSteps; ++s4) {
+            float2 f[2][2];   // [rows j, j + 8][channels 4 i, + 1 and 4 i + 2, + 3 of the step's 16]
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const float4 x = *reinterpret_cast<const float4*>(kt + piece_at<S::kRow>(16 * sub + 8 * half + jrow, 4 * s4 + i));
+              f[half][0] = make_float2(x.x, x.y);
+              f[half][1] = make_float2(x.z, x.w);
+            }
+#pragma unroll
+            for (int kp = 0; kp < 3; ++kp) {   // parts of the keys; those of the queries with them
+              const uint32_t a0 = split2(f[0][0]), a1 = split2(f[1][0]), a2 = split2(f[0][1]), a3 = split2(f[1][1]);
+#pragma unroll
+              for (int part = 0; part < 3 - kp; ++part)
+                mma16816(dot, a0, a1, a2, a3, qb[s4][2 * part], qb[s4][2 * part + 1]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sv[sub][e] = dot[e] * dot_scale;
+        } else {
+          float dot[4] = {};
+#pragma unroll
+          for (int s4 = 0; s4 < kSteps; ++s4) {
+            // matrices: rows 0 .. 7 and 8 .. 15 of the step's first eight channels, then of the others
+            uint32_t x[4];
+            load_matrices<false>(kt + piece_at<S::kRow>(16 * sub + lane % 16, 2 * s4 + lane / 16), x);
+            mma_q(dot, qb[s4], x[0], x[1], x[2], x[3]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sv[sub][e] = dot[e] * dot_scale;
         }
       }
 
       // ---- masks, the running maximum, and the logits that the scores will need
-      const bool whole = base + S::kTile <= r1;
-      float top = -INFINITY;
+      const int left = n - base - jrow;   // rows 16 sub + 8 half of the tile below this are visible
+      if (base + S::kTile > n) {
 #pragma unroll
-      for (int sub = 0; sub < kSub; ++sub)
+        for (int sub = 0; sub < kSub; ++sub)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = base + 16 * sub + 4 * e + li;
-          if (!whole && r >= r1) sv[sub][e] = -INFINITY;
-          if (a.score && live && (whole || r < r1)) logits[(int64_t)(r - r0) * tile_q + qi] = sv[sub][e];
-          top = fmaxf(top, sv[sub][e]);
-        }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float m_new = fmaxf(m, top);
-      if (__any_sync(0xffffffffu, m_new > m)) {
-        const float corr = m == -INFINITY ? 0.f : ex2(m - m_new);
-        l *= corr;
+          for (int e = 0; e < 4; ++e)
+            if (16 * sub + 8 * (e / 2) >= left) sv[sub][e] = -INFINITY;
+      }
+      if (logits && !(FOUR && i >= 2)) {
+        float* to = logits + ((int64_t)base + jrow) * a.tile_q + qa;
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-          o[c][0] *= corr; o[c][1] *= corr; o[c][2] *= corr; o[c][3] *= corr;
+        for (int sub = 0; sub < kSub; ++sub)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (16 * sub + 8 * (e / 2) < left && qa + e % 2 < tile_q)
+              to[(16 * sub + 8 * (e / 2)) * a.tile_q + e % 2] = sv[sub][e];
+      }
+      float top[2] = {m[0], m[1]};
+#pragma unroll
+      for (int sub = 0; sub < kSub; ++sub) {
+        top[0] = fmaxf(top[0], fmaxf(sv[sub][0], sv[sub][2]));
+        top[1] = fmaxf(top[1], fmaxf(sv[sub][1], sv[sub][3]));
+      }
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], off));
+        top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], off));
+      }
+      if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+        const float c0 = m[0] == -INFINITY ? 0.f : ex2(m[0] - top[0]), c1 = m[1] == -INFINITY ? 0.f : ex2(m[1] - top[1]);
+        l[0] *= c0;
+        l[1] *= c1;
+#pragma unroll
+        for (int t = 0; t < kPairs; ++t) {
+          o[t][0] *= c0; o[t][1] *= c1; o[t][2] *= c0; o[t][3] *= c1;
         }
         if constexpr (Q4) {
 #pragma unroll
-          for (int g = 0; g < kNg; ++g) oz[g] *= corr;
+          for (int g = 0; g < kNg; ++g) {
+            oz[g][0] *= c0;
+            oz[g][1] *= c1;
+          }
         }
-        m = m_new;
+        m[0] = top[0];
+        m[1] = top[1];
       }
-      const float shift = m == -INFINITY ? 0.f : m;
+      const float2 shift = make_float2(m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]);
 
       // ---- second product
 #pragma unroll
       for (int sub = 0; sub < kSub; ++sub) {
-        float p[4];
+        float2 p[2];   // rows j, j + 8
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[e] = ex2(sv[sub][e] - shift);
-          l += p[e];
+        for (int half = 0; half < 2; ++half) {
+          const float2 x = add2(make_float2(sv[sub][2 * half], sv[sub][2 * half + 1]), shift);
+          p[half] = make_float2(ex2(x.x), ex2(x.y));
+          l[0] += p[half].x;
+          l[1] += p[half].y;
         }
-        const int c0 = krow;   // this lane's column tile channels: 8 c0 .. + 7 (and 64 on)
         if constexpr (Q4) {
-          uint32_t hz[4][kNg];
+          float2 hz[2][kNg];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int g = 0; g < kNg; ++g)
-              hz[e][g] = *reinterpret_cast<const uint32_t*>(vmt + (16 * sub + 4 * e + li) * S::kMeta + 4 * g);
-          uint32_t w[4][kNg];
+          for (int half = 0; half < 2; ++half) {
+            const uint2 vz = load_words<kNg>(vmt + (16 * sub + 8 * half + jrow) * S::kMeta);
+            hz[half][0] = unpack2(vz.x);
+            if constexpr (kNg == 2) hz[half][1] = unpack2(vz.y);
+          }
+          uint32_t w[4][kNg];   // rows 2 i, 2 i + 1, 2 i + 8, 2 i + 9: i, 4 + i, 8 + i, 12 + i of the cache
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint8_t* at = vt + (16 * sub + 4 * e + li) * S::kRow + 4 * kNg * c0;
-            if constexpr (kNg == 2) {
-              const uint2 x = *reinterpret_cast<const uint2*>(at);
-              w[e][0] = x.x; w[e][1] = x.y;
-            } else {
-              w[e][0] = *reinterpret_cast<const uint32_t*>(at);
-            }
+            const uint2 x = load_words<kNg>(vt + (16 * sub + 4 * e + i) * S::kRow + 4 * kNg * j);
+            w[e][0] = x.x;
+            if constexpr (kNg == 2) w[e][1] = x.y;
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int half = 0; half < 2; ++half) {
 #pragma unroll
-            for (int g = 0; g < kNg; ++g) oz[g] = fmaf(p[e], __uint_as_float(hz[e][g] & 0xFFFF0000u), oz[g]);
-            p[e] *= kQ4P;
+            for (int g = 0; g < kNg; ++g) {
+              oz[g][0] = fmaf(p[half].x, hz[half][g].y, oz[g][0]);
+              oz[g][1] = fmaf(p[half].y, hz[half][g].y, oz[g][1]);
+            }
+            p[half] = mul2(p[half], make_float2(kQ4P, kQ4P));
           }
 #pragma unroll
           for (int g = 0; g < kNg; ++g) {
-            float ph[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) ph[e] = p[e] * __uint_as_float(hz[e][g] << 16);
-            uint32_t pa[S::kWide ? 6 : 4];
-#pragma unroll
-            for (int part = 0; part < (S::kWide ? 3 : 2); ++part) {
-              pa[2 * part] = split2(ph[0], ph[1]);
-              pa[2 * part + 1] = split2(ph[2], ph[3]);
-            }
-            uint32_t lo[2][4], hi[2][4];   // [even, odd channels][pair]: rows (li, 4 + li), rows (8 + li, 12 + li)
+            float2 ph[2] = {mul2(p[0], make_float2(hz[0][g].x, hz[0][g].x)), mul2(p[1], make_float2(hz[1][g].x, hz[1][g].x))};
+            uint32_t pb[S::kParts][2];
+            weight_parts(ph, pb);
+            // channels 2 c (odd = 0) and 2 c + 1 of rows 2 i, 2 i + 1 and of rows 2 i + 8, 2 i + 9
+            uint32_t lo[2][4], hi[2][4];
 #pragma unroll
             for (int odd = 0; odd < 2; ++odd) {
               const uint32_t sel = odd ? 0x7632 : 0x5410, swap = odd ? 0x6723 : 0x4501;
-              q4_operands(prmt(w[0][g], w[1][g], sel), prmt(w[0][g], w[1][g], swap), lo[odd]);
-              q4_operands(prmt(w[2][g], w[3][g], sel), prmt(w[2][g], w[3][g], swap), hi[odd]);
+              q4_operands(ones, prmt(w[0][g], w[1][g], sel), prmt(w[0][g], w[1][g], swap), lo[odd]);
+              q4_operands(ones, prmt(w[2][g], w[3][g], sel), prmt(w[2][g], w[3][g], swap), hi[odd]);
             }
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              mma16816(o[8 * g + c], pa[0], pa[2], pa[1], pa[3], lo[c & 1][c >> 1], hi[c & 1][c >> 1]);
-              if constexpr (S::kWide) mma16816(o[8 * g + c], pa[4], 0u, pa[5], 0u, lo[c & 1][c >> 1], hi[c & 1][c >> 1]);
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int part = 0; part < kParts; ++part)
+                mma16816(o[4 * g + c], lo[0][c], lo[1][c], hi[0][c], hi[1][c], pb[part][0], pb[part][1]);
+          }
+        } else if constexpr (S::kWide) {
+          uint32_t pb[S::kParts][2];
+          weight_parts(p, pb);
+#pragma unroll
+          for (int c4 = 0; c4 < kPairs / 2; ++c4) {   // channels 4 of 32 c4 + 4 j on
+            float f[4][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 x = *reinterpret_cast<const float4*>(vt + piece_at<S::kRow>(16 * sub + 4 * e + i, 8 * c4 + j));
+              f[e][0] = x.x; f[e][1] = x.y; f[e][2] = x.z; f[e][3] = x.w;
+            }
+#pragma unroll
+            for (int c = 0; c < 4; c += 2) {
+              float2 v0 = make_float2(f[0][c], f[1][c]), v2 = make_float2(f[2][c], f[3][c]);
+              float2 v1 = make_float2(f[0][c + 1], f[1][c + 1]), v3 = make_float2(f[2][c + 1], f[3][c + 1]);
+#pragma unroll
+              for (int vp = 0; vp < 3; ++vp) {   // parts of the values; those of the weights with them
+                const uint32_t a0 = split2(v0), a1 = split2(v1), a2 = split2(v2), a3 = split2(v3);
+#pragma unroll
+                for (int part = 0; part < 3 - vp; ++part)
+                  mma16816(o[2 * c4 + c / 2], a0, a1, a2, a3, pb[part][0], pb[part][1]);
+              }
             }
           }
         } else {
-          uint32_t pa[S::kWide ? 6 : 4];
+          uint32_t pb[S::kParts][2];
+          weight_parts(p, pb);
 #pragma unroll
-          for (int part = 0; part < (S::kWide ? 3 : 2); ++part) {
-            pa[2 * part] = split2(p[0], p[1]);
-            pa[2 * part + 1] = split2(p[2], p[3]);
-          }
+          for (int t = 0; t < kPairs; ++t) {
+            // transposed matrices: the first and the second eight channels by rows 0 .. 7, then by rows 8 .. 15
+            uint32_t x[4];
+            load_matrices<true>(vt + piece_at<S::kRow>(16 * sub + lane % 8 + 8 * (lane / 16), 2 * t + (lane / 8) % 2), x);
 #pragma unroll
-          for (int g = 0; g < kNg; ++g) {
-            if constexpr (S::kWide) {
-#pragma unroll
-              for (int h2 = 0; h2 < 2; ++h2) {
-                float f[4][4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float4 x = *reinterpret_cast<const float4*>(
-                      vt + piece_at<S::kRow>(16 * sub + 4 * e + li, 16 * g + 2 * c0 + h2));
-                  f[e][0] = x.x; f[e][1] = x.y; f[e][2] = x.z; f[e][3] = x.w;
-                }
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  float* acc = o[8 * g + 4 * h2 + c];
-#pragma unroll
-                  for (int part = 0; part < 3; ++part) {
-                    const uint32_t b0 = split2(f[0][c], f[1][c]), b1 = split2(f[2][c], f[3][c]);
-                    mma16816(acc, pa[0], pa[2], pa[1], pa[3], b0, b1);
-                    if (part == 0) mma16816(acc, pa[4], 0u, pa[5], 0u, b0, b1);
-                  }
-                }
-              }
-            } else {
-              uint32_t w[4][4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint4 x = *reinterpret_cast<const uint4*>(vt + piece_at<S::kRow>(16 * sub + 4 * e + li, 8 * g + c0));
-                w[e][0] = x.x; w[e][1] = x.y; w[e][2] = x.z; w[e][3] = x.w;
-              }
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const uint32_t sel = c & 1 ? 0x7632 : 0x5410;
-                mma16816(o[8 * g + c], pa[0], pa[2], pa[1], pa[3], prmt(w[0][c >> 1], w[1][c >> 1], sel),
-                         prmt(w[2][c >> 1], w[3][c >> 1], sel));
-              }
-            }
+            for (int part = 0; part < kParts; ++part) mma16816(o[t], x[0], x[1], x[2], x[3], pb[part][0], pb[part][1]);
           }
         }
       }
     }
-    cp_wait<0>();
 
-    // ---- the warps of the CTA meet. Lane (qi, li) holds, of query qi, channels 8 li + c (column 0) and
-    // 32 + 8 li + c (column 1) of each 64-channel group; rows 8 .. 15 of the accumulators add to them.
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    if constexpr (Q4) {
+    // ---- the warps meet
 #pragma unroll
-      for (int g = 0; g < kNg; ++g) {
-        oz[g] += __shfl_xor_sync(0xffffffffu, oz[g], 1);
-        oz[g] += __shfl_xor_sync(0xffffffffu, oz[g], 2);
-      }
-    }
-    __syncthreads();   // every warp is done with its ring
-    float* part = reinterpret_cast<float*>(smem);
-    if (li == 0) {
-      warp_m[warp][qi] = m;
-      warp_l[warp][qi] = l;
-    }
+    for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
-    for (int g = 0; g < kNg; ++g)
+      for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], off);
+        if constexpr (Q4) {
 #pragma unroll
-      for (int col = 0; col < 2; ++col) {
-        float* to = part + (warp * kQueryTile + qi) * D + 64 * g + 32 * col + 8 * li;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          float x = o[8 * g + c][col] + o[8 * g + c][col + 2];
-          if constexpr (Q4) x = fmaf(x, (c >> 1) & 1 ? kQ4OutOdd : kQ4OutEven, oz[g]);
-          to[c] = x;
+          for (int g = 0; g < kNg; ++g) oz[g][e] += __shfl_xor_sync(0xffffffffu, oz[g][e], off);
         }
       }
+    if constexpr (FOUR) {   // columns 4 .. 7 onto columns 0 .. 3
+#pragma unroll
+      for (int t = 0; t < kPairs; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][e] += __shfl_xor_sync(0xffffffffu, o[t][e], 2);
+    }
+    __syncthreads();   // every warp has left the last meeting
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int qq = qa + e;
+      if (qq < tile_q && !(FOUR && i >= 2)) {
+        if (j == 0) {
+          warp_m[warp][qq] = m[e];
+          warp_l[warp][qq] = l[e];
+        }
+        float* to = meet + (warp * a.tile_q + qq) * D;
+#pragma unroll
+        for (int t = 0; t < kPairs; ++t) {
+          float x = o[t][e], y = o[t][e + 2];
+          int c;   // the pair's first channel
+          if constexpr (Q4) {
+            const int g = t / 4, pair = t % 4;
+            c = 64 * g + 8 * j + 2 * pair;
+            x = fmaf(x, pair & 1 ? kQ4OutOdd : kQ4OutEven, oz[g][e]);
+            y = fmaf(y, pair & 1 ? kQ4OutOdd : kQ4OutEven, oz[g][e]);
+          } else {
+            c = S::kWide ? 32 * (t / 2) + 4 * j + 2 * (t % 2) : 16 * t + j;
+          }
+          to[c] = x;
+          to[c + (Q4 || S::kWide ? 1 : 8)] = y;
+        }
+      }
+    }
     __syncthreads();
-    float* cta_o = part + S::kWarps * kQueryTile * D;
+    const bool whole = here.tile == 0 && seg_end == at + here.tiles;   // the head lies in this share
+    float* part = a.parts + ((int64_t)blockIdx.x * 2 + (at > share0 ? 1 : 0)) * a.tile_q * (D + 2);
     for (int u = tid; u < tile_q * D; u += S::kThreads) {
       const int qq = u / D, c = u % D;
       float top = -INFINITY;
@@ -522,67 +744,154 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads) attend_kernel(Atte
 #pragma unroll
       for (int w = 0; w < S::kWarps; ++w) {
         const float f = warp_m[w][qq] == -INFINITY ? 0.f : ex2(warp_m[w][qq] - top);
-        x = fmaf(part[(w * kQueryTile + qq) * D + c], f, x);
+        x = fmaf(meet[(w * a.tile_q + qq) * D + c], f, x);
         sum = fmaf(warp_l[w][qq], f, sum);
       }
-      cta_o[u] = x;
-      if (c == 0) {
-        cta_m[qq] = top;
-        cta_l[qq] = sum;
+      if (whole) {
+        store1<IO>(static_cast<IO*>(a.out) + q0 * D + u, sum == 0.f ? 0.f : x / sum);
+        if (c == 0 && a.score) {
+          a.stats[vh * 2 * a.tile_q + qq] = top;
+          a.stats[(vh * 2 + 1) * a.tile_q + qq] = sum;
+        }
+      } else {
+        part[u] = x;
+        if (c == 0) {
+          part[a.tile_q * D + qq] = top;
+          part[a.tile_q * (D + 1) + qq] = sum;
+        }
       }
     }
+    // the next head
+    here.tile += (int)(seg_end - at);
+    at = seg_end;
+    if (at < end) settle(here);
+  }
+  cp_wait<0>();
+}
 
-    // ---- the CTAs of the head meet
-    ptx::cluster_sync();
-    if (tid < tile_q) {
-      float top = -INFINITY;
-      for (uint32_t r = 0; r < csize; ++r)
-        top = fmaxf(top, __uint_as_float(ptx::dsmem_ld_u32(ptx::map_rank(&cta_m[tid], r))));
-      float sum = 0.f;
-      for (uint32_t r = 0; r < csize; ++r) {
-        const float mr = __uint_as_float(ptx::dsmem_ld_u32(ptx::map_rank(&cta_m[tid], r)));
-        if (mr != -INFINITY) sum = fmaf(__uint_as_float(ptx::dsmem_ld_u32(ptx::map_rank(&cta_l[tid], r))), ex2(mr - top), sum);
-      }
-      head_m[tid] = top == -INFINITY ? 0.f : top;
-      head_r[tid] = sum == 0.f ? 0.f : 1.0f / sum;   // no row: zeros; a NaN stays one
+// The second launch: block (0, head) joins the parts of a head's passes, blocks (1 .., head) add the
+// weights of kJoinRows rows each to its scores.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 1024;
+
+template <typename IO, int D, int TILE>
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(AttendArgs a) {
+  __shared__ int64_t sums[kJoinThreads / 32];
+  __shared__ int64_t seq_before, all;   // tiles
+  __shared__ float head_m[kQueryTile], head_r[kQueryTile];
+  const int tid = threadIdx.x;
+  const int64_t bh = blockIdx.y;
+  const int b = (int)(bh / a.heads), h = (int)(bh % a.heads);
+  const int per_seq = a.heads * a.passes;
+  {
+    int64_t mine = 0, upto = 0, total, upto_total;
+    for (int s = tid; s < a.batch; s += kJoinThreads) {
+      const int t = (visible_rows(a, s) + TILE - 1) / TILE;
+      mine += t;
+      if (s < b) upto += t;
+    }
+    block_scan64<kJoinThreads>(mine, sums, &total);
+    __syncthreads();
+    block_scan64<kJoinThreads>(upto, sums, &upto_total);
+    if (tid == 0) {
+      all = total * per_seq;
+      seq_before = upto_total * per_seq;
     }
     __syncthreads();
+  }
+  const int ctas = working_ctas(all, a.ctas);
+  const int n = visible_rows(a, b);
+  const int tiles = (n + TILE - 1) / TILE;
+  const int r0 = ((int)blockIdx.x - 1) * kJoinRows, r1 = min(n, r0 + kJoinRows);
+  if (blockIdx.x > 0 && r0 >= n) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  constexpr int kPer = kJoinRows / kJoinThreads;
+  float w[kPer];   // the summed weights of this thread's rows
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) w[i] = 0.f;
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int tile_q = min(a.tile_q, a.group - pass * a.tile_q);
+    const int64_t vh = bh * a.passes + pass;
+    const int64_t q0 = bh * a.group + (int64_t)pass * a.tile_q;
+    const int64_t f0 = seq_before + (int64_t)(h * a.passes + pass) * tiles;
     IO* out = static_cast<IO*>(a.out) + q0 * D;
-    for (int u = (int)rank * S::kThreads + tid; u < tile_q * D; u += (int)csize * S::kThreads) {
-      const int qq = u / D;
-      float x = 0.f;
-      for (uint32_t r = 0; r < csize; ++r) {
-        const float mr = __uint_as_float(ptx::dsmem_ld_u32(ptx::map_rank(&cta_m[qq], r)));
-        if (mr != -INFINITY) x = fmaf(__uint_as_float(ptx::dsmem_ld_u32(ptx::map_rank(&cta_o[u], r))), ex2(mr - head_m[qq]), x);
-      }
-      store1<IO>(out + u, x * head_r[qq]);
+    if (tiles == 0) {   // (block 0 only)
+      for (int u = tid; u < tile_q * D; u += kJoinThreads) store1<IO>(out + u, 0.f);
+      continue;
     }
-    if (a.score) {
-      float* sc = a.score + bh * a.cap + r0;
-      const float decay = pass == 0 ? a.decay : 1.0f;
-      for (int r = tid; r < r1 - r0; r += S::kThreads) {
-        float w = 0.f;
-        for (int qq = 0; qq < tile_q; ++qq) w = fmaf(ex2(logits[(int64_t)r * tile_q + qq] - head_m[qq]), head_r[qq], w);
-        sc[r] = decay != 0.f ? fmaf(decay, sc[r], w) : w;
+    const int c0 = share_of(all, ctas, f0), c1 = share_of(all, ctas, f0 + tiles - 1);
+    if (c0 == c1 && blockIdx.x == 0) continue;   // finished in the first launch
+    const int64_t size = (int64_t)a.tile_q * (D + 2);
+    // The head is the last segment of CTA c0 (slot 1, unless the share starts with it) and the first of the others.
+    const float* first = a.parts + ((int64_t)c0 * 2 + (share_start(all, ctas, c0) < f0 ? 1 : 0)) * size;
+    const float* rest = a.parts + ((int64_t)c0 + 1) * 2 * size;
+    const int more = c1 - c0;
+    __syncthreads();   // the last pass's maxima have been used
+    for (int qq = tid / 32; qq < tile_q; qq += kJoinThreads / 32) {   // a warp per query
+      const int lane = tid % 32;
+      float top, sum;
+      if (c0 == c1) {
+        top = __ldcg(a.stats + vh * 2 * a.tile_q + qq);
+        sum = __ldcg(a.stats + (vh * 2 + 1) * a.tile_q + qq);
+      } else {
+        const int64_t at_m = (int64_t)a.tile_q * D + qq, at_l = (int64_t)a.tile_q * (D + 1) + qq;
+        top = -INFINITY;
+        for (int i = lane; i <= more; i += 32) top = fmaxf(top, __ldcg((i ? rest + (i - 1) * 2 * size : first) + at_m));
+        top = warp_max(top);
+        sum = 0.f;
+        for (int i = lane; i <= more; i += 32) {
+          const float* p = i ? rest + (i - 1) * 2 * size : first;
+          const float m = __ldcg(p + at_m);
+          if (m != -INFINITY) sum = fmaf(__ldcg(p + at_l), ex2(m - top), sum);
+        }
+        sum = warp_sum(sum);
+      }
+      if (lane == 0) {
+        head_m[qq] = top == -INFINITY ? 0.f : top;
+        head_r[qq] = sum == 0.f ? 0.f : 1.0f / sum;   // a NaN stays one
       }
     }
-    ptx::cluster_sync();   // no CTA leaves, or reuses its memory, while its partial may still be read
+    __syncthreads();
+    if (blockIdx.x == 0) {
+      for (int u = tid; u < tile_q * D; u += kJoinThreads) {
+        const int qq = u / D;
+        const int64_t at_m = (int64_t)a.tile_q * D + qq;
+        float x = 0.f;
+#pragma unroll 4
+        for (int i = 0; i <= more; ++i) {
+          const float* p = i ? rest + (i - 1) * 2 * size : first;
+          const float m = __ldcg(p + at_m), v = __ldcg(p + u);
+          x = fmaf(v, m == -INFINITY ? 0.f : ex2(m - head_m[qq]), x);
+        }
+        store1<IO>(out + u, x * head_r[qq]);
+      }
+    } else {
+      const float* logits = a.logits + vh * a.cap * a.tile_q;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int r = r0 + i * kJoinThreads + tid;
+        if (r < r1)
+          for (int qq = 0; qq < tile_q; ++qq)
+            w[i] = fmaf(ex2(__ldcg(logits + (int64_t)r * a.tile_q + qq) - head_m[qq]), head_r[qq], w[i]);
+      }
+    }
+  }
+  if (blockIdx.x > 0) {
+    float* sc = a.score + bh * a.cap;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = r0 + i * kJoinThreads + tid;
+      if (r < r1) sc[r] = a.decay != 0.f ? fmaf(a.decay, sc[r], w[i]) : w[i];
+    }
   }
 }
 
-template <bool Q4, typename IO, int D>
+template <bool Q4, typename IO, int D, bool FOUR>
 cudaError_t launch_typed(const AttendJob& job) {
   using S = Shape<Q4, IO, D>;
-  const int64_t bh = (int64_t)job.batch * job.heads;
-  const int group = job.q_heads / job.heads, tile_q = group < kQueryTile ? group : kQueryTile;
-  // CTAs per head: enough for two per SM, with at least a tile per warp each.
-  int64_t csize = 2 * (int64_t)device_sm_count() / bh;
-  const int64_t most = (job.cap + S::kTile * S::kWarps - 1) / (S::kTile * S::kWarps);
-  if (csize > most) csize = most;
-  if (csize > kMaxCluster) csize = kMaxCluster;
-  if (csize < 1) csize = 1;
-  const int64_t per = ((job.cap + csize - 1) / csize + S::kTile - 1) / S::kTile * S::kTile;
-  const int64_t logits = job.score ? per * tile_q * 4 : 0;
+  const AttendLayout L = attend_layout(job.batch, job.q_heads, job.heads, D, job.cap, job.score != nullptr);
+  char* ws = static_cast<char*>(job.workspace);
   AttendArgs a;
   a.q = job.q;
   a.k = static_cast<const uint8_t*>(job.k);
@@ -591,43 +900,78 @@ cudaError_t launch_typed(const AttendJob& job) {
   a.vm = static_cast<const uint8_t*>(job.v_meta);
   a.len = job.len;
   a.score = job.score;
-  a.logits = logits <= kLogitsSmem ? nullptr : job.logits;
   a.out = job.out;
   a.decay = job.decay;
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
   a.cap = job.cap;
+  a.batch = job.batch;
   a.heads = job.heads;
-  a.group = group;
+  a.group = job.q_heads / job.heads;
+  a.passes = L.passes;
+  a.tile_q = L.tile_q;
+  a.parts = reinterpret_cast<float*>(ws + L.parts);
+  a.stats = reinterpret_cast<float*>(ws + L.stats);
+  a.logits = reinterpret_cast<float*>(ws + L.logits);
   a.dev_status = job.dev_status;
-  const cudaError_t err = allow_dynamic_smem<attend_kernel<Q4, IO, D>>(S::kSmem + kLogitsSmem);
+  // One wave of CTAs, or fewer where their warps would have no tile each.
+  const int smem = S::smem(L.tile_q);
+  cudaError_t err = allow_dynamic_smem<attend_kernel<Q4, IO, D, FOUR>>(S::smem(kQueryTile));
+  if (err != cudaSuccess) return err;
+  static std::atomic<int> occupancy[kQueryTile + 1];   // CTAs per SM by tile_q (0: not asked yet)
+  int resident = occupancy[L.tile_q].load(std::memory_order_relaxed);
+  if (resident < 1) {
+    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, attend_kernel<Q4, IO, D, FOUR>, S::kThreads, smem);
+    if (err != cudaSuccess) return err;
+    if (resident < 1) return cudaErrorInvalidConfiguration;
+    occupancy[L.tile_q].store(resident, std::memory_order_relaxed);
+  }
+  const int64_t tiles = (int64_t)job.batch * job.heads * L.passes * ((job.cap + S::kTile - 1) / S::kTile);
+  int64_t ctas = (int64_t)device_sm_count() * resident;
+  if (ctas > (tiles + kWarps - 1) / kWarps) ctas = (tiles + kWarps - 1) / kWarps;
+  if (ctas > L.max_ctas) ctas = L.max_ctas;
+  a.ctas = (int)ctas;
+  attend_kernel<Q4, IO, D, FOUR><<<(unsigned)ctas, S::kThreads, smem, job.stream>>>(a);
+  err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(bh * csize));
-  cfg.blockDim = dim3(S::kThreads);
-  cfg.dynamicSmemBytes = S::kSmem + (a.logits ? 0 : (size_t)logits);
+  cfg.gridDim = dim3(1 + (unsigned)(job.score ? (job.cap + kJoinRows - 1) / kJoinRows : 0), (unsigned)(job.batch * job.heads));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = job.stream;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)csize;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_kernel<Q4, IO, D>, a);
+  return cudaLaunchKernelEx(&cfg, attend_join_kernel<IO, D, S::kTile>, a);
+}
+
+template <bool Q4, int D> cudaError_t launch_dim(const AttendJob& job) {
+  if (job.dtype == SNAPKV_F32) return launch_typed<Q4, float, D, false>(job);
+  return job.q_heads / job.heads <= 4 ? launch_typed<Q4, __nv_bfloat16, D, true>(job)
+                                      : launch_typed<Q4, __nv_bfloat16, D, false>(job);
 }
 
 template <bool Q4> cudaError_t launch_format(const AttendJob& job) {
-  if (job.dtype == SNAPKV_BF16)
-    return job.head_dim == 64 ? launch_typed<Q4, __nv_bfloat16, 64>(job) : launch_typed<Q4, __nv_bfloat16, 128>(job);
-  return job.head_dim == 64 ? launch_typed<Q4, float, 64>(job) : launch_typed<Q4, float, 128>(job);
+  return job.head_dim == 64 ? launch_dim<Q4, 64>(job) : launch_dim<Q4, 128>(job);
 }
 
 }  // namespace
 
-size_t attend_logits_bytes(int batch, int q_heads, int heads, int head_dim, int64_t cap) {
-  (void)head_dim;
+AttendLayout attend_layout(int batch, int q_heads, int heads, int head_dim, int64_t cap, bool scored) {
+  AttendLayout L;
   const int group = q_heads / heads;
-  return (size_t)batch * heads * (size_t)cap * (group < kQueryTile ? group : kQueryTile) * sizeof(float);
+  L.tile_q = group < kQueryTile ? group : kQueryTile;
+  L.passes = (group + kQueryTile - 1) / kQueryTile;
+  const size_t vh = (size_t)batch * heads * L.passes;
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  // No more CTAs than there can be tiles for their warps (the smallest tile has 16 rows).
+  const int64_t tiles = (int64_t)vh * ((cap + 15) / 16);
+  L.max_ctas = (int)(tiles < kMaxAttendCtas ? tiles : kMaxAttendCtas);
+  L.parts = 0;
+  L.stats = L.parts + up((size_t)L.max_ctas * 2 * L.tile_q * (head_dim + 2) * sizeof(float));
+  L.logits = L.stats + up(vh * 2 * L.tile_q * sizeof(float));
+  L.total = L.logits + (scored ? up(vh * (size_t)cap * L.tile_q * sizeof(float)) : 0);
+  return L;
 }
 
 cudaError_t launch_attend(const AttendJob& job) {

@@ -58,8 +58,9 @@ snapkv_status run_attend(AttendJob& job, size_t kv_bytes, size_t kv_meta_bytes, 
   if (!aligned16(job.q) || !aligned16(job.k) || !aligned16(job.v) || !aligned16(job.out) || !aligned16(job.score) ||
       !aligned4(job.len) || !aligned4(job.dev_status))
     return SNAPKV_ERR_INVALID_ARG;
-  const size_t need = attend_logits_bytes(job.batch, job.q_heads, job.heads, job.head_dim, job.cap);
-  if (job.score && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u))) return SNAPKV_ERR_WORKSPACE;
+  const size_t need =
+      attend_layout(job.batch, job.q_heads, job.heads, job.head_dim, job.cap, job.score != nullptr).total;
+  if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)) return SNAPKV_ERR_WORKSPACE;
   const size_t q_bytes = (size_t)job.batch * job.q_heads * job.head_dim * elem_bytes(job.dtype);
   const Span spans[] = {{job.q, q_bytes, false},
                         {job.k, kv_bytes, false},
@@ -69,10 +70,10 @@ snapkv_status run_attend(AttendJob& job, size_t kv_bytes, size_t kv_meta_bytes, 
                         {job.len, (size_t)job.batch * 4, false},
                         {job.score, (size_t)job.batch * job.heads * (size_t)job.cap * 4, true},
                         {job.out, q_bytes, true},
-                        {job.score ? workspace : nullptr, need, true},
+                        {workspace, need, true},
                         {job.dev_status, 4, true}};
   if (!disjoint(spans)) return SNAPKV_ERR_INVALID_ARG;
-  job.logits = static_cast<float*>(workspace);
+  job.workspace = workspace;
   return launch_attend(job) == cudaSuccess ? SNAPKV_OK : SNAPKV_ERR_CUDA;
 }
 
@@ -110,10 +111,11 @@ using namespace snapkv;
 
 extern "C" {
 
-size_t snapkv_scored_workspace_size(int32_t batch, int32_t q_heads, int32_t heads, int32_t head_dim, int64_t cap) {
+size_t snapkv_scored_workspace_size(int32_t batch, int32_t q_heads, int32_t heads, int32_t head_dim, int64_t cap,
+                                    int32_t scored) {
   if (check_sizes(batch, heads, head_dim, cap) != SNAPKV_OK) return 0;
   if (q_heads < heads || q_heads % heads != 0) return 0;
-  return up256(attend_logits_bytes(batch, q_heads, heads, head_dim, cap));
+  return attend_layout(batch, q_heads, heads, head_dim, cap, scored != 0).total;
 }
 
 snapkv_status snapkv_decode_attend_scored(const void* q, const void* k_cache, const void* v_cache, int64_t cap,

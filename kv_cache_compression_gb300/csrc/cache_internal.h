@@ -38,12 +38,20 @@ struct AttendJob {
   float* score;         // may be null
   float decay;
   void* out;
-  float* logits;        // workspace: [B*H][cap][min(G, kQueryTile)], used where shared memory is too small
+  void* workspace;      // attend_layout(...).total bytes
   int32_t* dev_status;
   cudaStream_t stream;
 };
 
-size_t attend_logits_bytes(int batch, int q_heads, int heads, int head_dim, int64_t cap);
+// Workspace layout of an attention call (byte offsets, each 256-aligned), and how its queries are cut.
+struct AttendLayout {
+  size_t parts, stats, logits, total;
+  int tile_q, passes, max_ctas;
+};
+
+constexpr int kMaxAttendCtas = 1024;   // bounds the workspace, not tied to a device's SM count
+
+AttendLayout attend_layout(int batch, int q_heads, int heads, int head_dim, int64_t cap, bool scored);
 cudaError_t launch_attend(const AttendJob& job);
 
 struct Q4Job {

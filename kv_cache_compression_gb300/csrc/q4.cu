@@ -47,22 +47,6 @@ __device__ __forceinline__ void store8(float* p, const float* x) {
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// Two fp32 operations in one instruction (each rounded as usual).
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 r;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t&>(r))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
-  return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t&>(r))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
-  return r;
-}
-
 // The level numbers of eight values as nibbles, in q4_pack's order. (x - z) / (2h) + 7.5 has to be
 // rounded as if computed exactly: ties are common (0.7 % of normal bf16 values lie half-way between
 // two levels). So no quotient is trusted: a product with r = 1 / (2h) only finds the nearest border

@@ -19,13 +19,47 @@ constexpr uint32_t kQ4MaskOdd = 0x800E800Eu, kQ4OneOdd = 0x00010001u;     // pai
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
 
+// The constant bits in registers that the compiler cannot see through: an AND-OR takes one immediate at
+// most, and with both as immediates it becomes two instructions.
+struct Q4Ones {
+  uint32_t even, odd;
+  __device__ __forceinline__ Q4Ones() {
+    asm volatile("mov.b32 %0, %1;" : "=r"(even) : "n"(kQ4OneEven));
+    asm volatile("mov.b32 %0, %1;" : "=r"(odd) : "n"(kQ4OneOdd));
+  }
+};
+
 // The operands of pairs 0 .. 3 from a register with the two halves as stored (w) and with each
 // half's bytes swapped (s).
-__device__ __forceinline__ void q4_operands(uint32_t w, uint32_t s, uint32_t* out) {
-  out[0] = (w & kQ4MaskEven) | kQ4OneEven;
-  out[1] = ((w << 1) & kQ4MaskOdd) | kQ4OneOdd;
-  out[2] = (s & kQ4MaskEven) | kQ4OneEven;
-  out[3] = ((s << 1) & kQ4MaskOdd) | kQ4OneOdd;
+__device__ __forceinline__ void q4_operands(const Q4Ones& one, uint32_t w, uint32_t s, uint32_t* out) {
+  out[0] = (w & kQ4MaskEven) | one.even;
+  out[1] = ((w << 1) & kQ4MaskOdd) | one.odd;
+  out[2] = (s & kQ4MaskEven) | one.even;
+  out[3] = ((s << 1) & kQ4MaskOdd) | one.odd;
+}
+
+// Two fp32 operations in one instruction (each rounded as usual).
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return r;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
 }
 
 // Word index, within a row of NG groups, of channels 8 * o .. 8 * o + 7 of group g.

@@ -36,8 +36,10 @@ def test_every_declared_function_is_exported(lib):
 
 
 def test_workspace_sizes(lib):
-    assert kc.scored_workspace_size(2, 8, 4, 128, 1000) == 2 * 4 * 1000 * 2 * 4
-    assert kc.scored_workspace_size(2, 64, 4, 128, 1000) == 2 * 4 * 1000 * 8 * 4     # eight queries at a time
+    plain, scored = (kc.scored_workspace_size(2, 8, 4, 128, 1000, s) for s in (False, True))
+    assert plain > 0 and scored - plain == 2 * 4 * 1000 * 2 * 4                        # a logit per query and row
+    wide = [kc.scored_workspace_size(2, 64, 4, 128, 1000, s) for s in (False, True)]   # eight queries at a time
+    assert wide[1] - wide[0] == 2 * 64 * 1000 * 4
     assert kc.scored_workspace_size(1, 3, 2, 128, 1000) == 0                          # not a multiple
     assert kc.scored_workspace_size(1, 2, 2, 96, 1000) == 0
     assert kc.evict_workspace_size(2, 3, 100) == 2560                                  # 2400, in 256s
@@ -68,6 +70,7 @@ def _attend(lib, **kw):
     (dict(out=MB), sk.ERR_INVALID_ARG),              # over the queries
     (dict(score=4 * MB), sk.ERR_INVALID_ARG),        # the score over the values
     (dict(ws=7 * MB), sk.ERR_INVALID_ARG),           # the workspace over the score
+    (dict(ws=2 * MB, score=0), sk.ERR_INVALID_ARG),  # over the keys
     (dict(dev=6 * MB), sk.ERR_INVALID_ARG),          # the status word over the lengths
 ])
 def test_attend_refusals(lib, kw, status):
@@ -88,7 +91,7 @@ def test_bad_caches_are_refused_by_every_call(lib, kw, status):
     c = ctypes.byref(_cache(**kw))
     assert lib.snapkv_q4_append(c, P(MB), P(2 * MB), 1, None, P(3 * MB), P(4 * MB), 1, None, None) == status
     assert lib.snapkv_q4_read(c, None, 1, P(MB), P(2 * MB), 1, None) == status
-    assert lib.snapkv_q4_decode_attend(P(MB), c, P(3 * MB), None, 1.0, P(4 * MB), 4, 1, None, 0, None, None) == status
+    assert lib.snapkv_q4_decode_attend(P(MB), c, P(3 * MB), None, 1.0, P(4 * MB), 4, 1, P(5 * MB), MB, None, None) == status
     assert lib.snapkv_q4_evict(c, P(MB), P(3 * MB), P(4 * MB), 10, 5, None, P(5 * MB), MB, None, None) == status
     assert lib.snapkv_q4_append(None, P(MB), P(2 * MB), 1, None, P(3 * MB), P(4 * MB), 1, None, None) \
         == sk.ERR_INVALID_ARG
@@ -110,10 +113,10 @@ def test_q4_refusals(lib):
     assert read(k=0) == read(rows=0) == read(dt=2) == read(k=2 * MB) == read(start=3 * MB + 1) == sk.ERR_INVALID_ARG
     assert read(v=19 * MB) == sk.ERR_INVALID_ARG                                       # over the cache
 
-    def attend(q=MB, out=2 * MB, hq=4, score=None, ws=None, wsb=0, decay=1.0):
+    def attend(q=MB, out=2 * MB, hq=4, score=None, ws=6 * MB, wsb=MB, decay=1.0):
         return lib.snapkv_q4_decode_attend(P(q), c, P(3 * MB), P(score), decay, P(out), hq, 1, P(ws), wsb, None, None)
     assert attend(q=0) == attend(out=0) == attend(hq=3) == attend(out=16 * MB) == attend(decay=2.0) == sk.ERR_INVALID_ARG
-    assert attend(score=5 * MB) == sk.ERR_WORKSPACE
+    assert attend(ws=0) == attend(score=5 * MB, ws=6 * MB + 8) == attend(wsb=1000) == sk.ERR_WORKSPACE
 
 
 @pytest.mark.parametrize("kw,status", [

@@ -60,6 +60,7 @@ struct AttendArgs {
   float* stats;         // [heads][2][tile_q]: maximum and sum of a head that one CTA finished
   float* parts;         // [ctas][2] of (o [tile_q][D], m [tile_q], l [tile_q])
   int32_t* dev_status;
+  Q4Ones ones;
 };
 
 // The CTAs of the first launch that get a share: no more than give every warp a tile.
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
   const float part2 = FOUR && i >= 2 ? 1.0f : 0.0f;   // this lane's columns are second parts
   const int jrow = row_of<Q4 || S::kWide>(j);         // row j of an 8-row tile, as it lies in the cache
   const int per_seq = a.heads * a.passes;   // heads of a sequence
-  const Q4Ones ones;
+  const Q4Ones ones = a.ones;
 
   // ---- this CTA's share of the tiles, and the sequence it starts in
   {

@@ -19,14 +19,10 @@ constexpr uint32_t kQ4MaskOdd = 0x800E800Eu, kQ4OneOdd = 0x00010001u;     // pai
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
 
-// The constant bits in registers that the compiler cannot see through: an AND-OR takes one immediate at
-// most, and with both as immediates it becomes two instructions.
+// The constant bits, as a kernel argument: an AND-OR takes one immediate at most, and with both constants
+// known to the compiler it becomes two instructions.
 struct Q4Ones {
-  uint32_t even, odd;
-  __device__ __forceinline__ Q4Ones() {
-    asm volatile("mov.b32 %0, %1;" : "=r"(even) : "n"(kQ4OneEven));
-    asm volatile("mov.b32 %0, %1;" : "=r"(odd) : "n"(kQ4OneOdd));
-  }
+  uint32_t even = kQ4OneEven, odd = kQ4OneOdd;
 };
 
 // The operands of pairs 0 .. 3 from a register with the two halves as stored (w) and with each

@@ -41,6 +41,8 @@
 namespace snapkv {
 namespace {
 
+constexpr int kDirectTiles = 4;   // a warp's tiles up to which a head is left to one CTA
+
 struct AttendArgs {
   const void* q;
   const uint8_t* k;
@@ -55,8 +57,10 @@ struct AttendArgs {
   int batch, heads, group;
   int passes, tile_q;   // queries are served tile_q at a time (the last of `passes` passes may have fewer)
   int ctas;             // of the first launch
+  bool direct;          // a CTA per head, which finishes it (no second launch)
   // workspace: a head is (sequence, KV head, pass) here
-  float* logits;        // [heads][cap][tile_q] (scores only)
+  float* logits;        // [heads][tile_q][logit_stride] (scores only)
+  int64_t logit_stride; // cap, rounded up to whole 32-byte sectors
   float* stats;         // [heads][2][tile_q]: maximum and sum of a head that one CTA finished
   float* parts;         // [ctas][2] of (o [tile_q][D], m [tile_q], l [tile_q])
   int32_t* dev_status;
@@ -70,25 +74,17 @@ __device__ __forceinline__ int working_ctas(int64_t total, int ctas) {
   return most < ctas ? (int)most : ctas;
 }
 
-// The first launch's schedule. Flat tile index = (tiles of the sequences before, times heads per
-// sequence) + (head within the sequence) * tiles + tile.
-struct Plan {
-  int64_t total;         // tiles
-  int64_t before;        // tiles per head of the sequences before the sought one
-  int seq;               // the sought sequence
-  int ctas;
-};
-
+// CTA c's share of `total` tiles starts here. (c <= ctas <= 1024 and total < 2^43: no product overflows;
+// short lists, where the latency counts, get by with a 32-bit division.)
 __device__ __forceinline__ int64_t share_start(int64_t total, int ctas, int c) {
-  // total * c / ctas without overflow: total < 2^43, c <= ctas <= 1024
+  if (total < (1 << 22)) return (uint32_t)total * (uint32_t)c / (uint32_t)ctas;
   return total * c / ctas;
 }
 
-// The CTA whose share holds flat tile t.
+// The CTA whose share holds flat tile t: the last one that starts at or before it.
 __device__ __forceinline__ int share_of(int64_t total, int ctas, int64_t t) {
-  int c = (int)(t * ctas / total);
-  while (c > 0 && share_start(total, ctas, c) > t) --c;
-  while (share_start(total, ctas, c + 1) <= t) ++c;
+  int c = total < (1 << 22) ? (int)((uint32_t)t * (uint32_t)ctas / (uint32_t)total) : (int)(t * ctas / total);
+  while (c + 1 < ctas && share_start(total, ctas, c + 1) <= t) ++c;   // (never behind: floor(t * ctas / total) starts at or before t)
   return c;
 }
 
@@ -97,25 +93,35 @@ __device__ __forceinline__ int visible_rows(const AttendArgs& a, int b) {
   return n < 0 ? 0 : (int64_t)n > a.cap ? (int)a.cap : n;
 }
 
-// Exclusive sum over the block of v (thread order) and the block's total.
-template <int THREADS> __device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t* sums, int64_t* total) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  int64_t x = v;
+// Flat tile index = (tiles of the sequences before, times heads per sequence) + (head within the sequence) *
+// tiles + tile.
+template <int TILE> __device__ __forceinline__ int tiles_of(const AttendArgs& a, int b) {
+  return (visible_rows(a, b) + TILE - 1) / TILE;
+}
+
+// Sums over the sequences: lane i takes a run of them, `mine` tiles after `upto`.
+struct SeqScan {
+  int b0, b1;
+  int64_t upto, mine, total;
+};
+template <int TILE> __device__ __forceinline__ SeqScan scan_sequences(const AttendArgs& a) {
+  const int lane = threadIdx.x % 32;
+  const int chunk = (a.batch + 31) / 32;
+  SeqScan s;
+  s.b0 = min(a.batch, lane * chunk);
+  s.b1 = min(a.batch, s.b0 + chunk);
+  s.mine = 0;
+#pragma unroll 4
+  for (int b = s.b0; b < s.b1; ++b) s.mine += tiles_of<TILE>(a, b);
+  int64_t x = s.mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
     if (lane >= off) x += y;
   }
-  if (lane == 31) sums[warp] = x;
-  __syncthreads();
-  int64_t before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) before += sums[w];
-    all += sums[w];
-  }
-  *total = all;
-  return before + x - v;
+  s.total = __shfl_sync(0xffffffffu, x, 31);
+  s.upto = x - s.mine;
+  return s;
 }
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
@@ -229,8 +235,7 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
   constexpr int kNg = S::kNg;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float warp_m[S::kWarps][kQueryTile], warp_l[S::kWarps][kQueryTile];
-  __shared__ int64_t sums[S::kWarps];
-  __shared__ Plan plan;
+  __shared__ float head_m[kQueryTile], head_r[kQueryTile];
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -243,49 +248,55 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
   const int per_seq = a.heads * a.passes;   // heads of a sequence
   const Q4Ones ones = a.ones;
 
-  // ---- this CTA's share of the tiles, and the sequence it starts in
-  {
-    const int chunk = (a.batch + S::kThreads - 1) / S::kThreads;
-    const int b0 = min(a.batch, tid * chunk), b1 = min(a.batch, b0 + chunk);
-    int64_t mine = 0, total;
-    for (int b = b0; b < b1; ++b) {
-      mine += (visible_rows(a, b) + S::kTile - 1) / S::kTile;
-      if (blockIdx.x == 0 && (int64_t)a.len[b] > a.cap) report(a.dev_status, SNAPKV_ERR_CAPACITY);
+  // ---- this CTA's share of the tiles, and the sequence it starts in (every warp finds them for itself)
+  int64_t at, end, before;
+  int first_seq;
+  if (a.direct) {
+    const int vh = (int)blockIdx.x;
+    first_seq = vh / per_seq;
+    const int tiles = tiles_of<S::kTile>(a, first_seq);
+    before = 0;   // (a list of this sequence alone)
+    at = (int64_t)(vh - first_seq * per_seq) * tiles;
+    end = at + tiles;
+    if (vh % per_seq == 0 && tid == 0 && (int64_t)a.len[first_seq] > a.cap) report(a.dev_status, SNAPKV_ERR_CAPACITY);
+    if (tiles == 0) {
+      const int pass = vh % a.passes, bh = vh / a.passes;
+      IO* out = static_cast<IO*>(a.out) + ((int64_t)bh * a.group + pass * a.tile_q) * D;
+      for (int u = tid; u < min(a.tile_q, a.group - pass * a.tile_q) * D; u += S::kThreads) store1<IO>(out + u, 0.f);
+      return;
     }
-    int64_t before = block_scan64<S::kThreads>(mine, sums, &total);
-    const int ctas = working_ctas(total * per_seq, a.ctas);
-    if ((int)blockIdx.x >= ctas) return;   // (the whole block)
-    const int64_t start = share_start(total * per_seq, ctas, (int)blockIdx.x);
-    if (tid == 0) {
-      plan.total = total * per_seq;
-      plan.ctas = ctas;
+  } else {
+    const SeqScan scan = scan_sequences<S::kTile>(a);
+    if (blockIdx.x == 0 && warp == 0)
+      for (int b = scan.b0; b < scan.b1; ++b)
+        if ((int64_t)a.len[b] > a.cap) report(a.dev_status, SNAPKV_ERR_CAPACITY);
+    const int64_t total = scan.total * per_seq;
+    const int ctas = working_ctas(total, a.ctas);
+    if ((int)blockIdx.x >= ctas) return;
+    at = share_start(total, ctas, (int)blockIdx.x);
+    end = share_start(total, ctas, (int)blockIdx.x + 1);   // > at
+    int seq = -1;
+    int64_t upto = scan.upto;
+    if (at >= upto * per_seq && at < (upto + scan.mine) * per_seq) {
+      seq = scan.b0;
+      for (int t; at >= (upto + (t = tiles_of<S::kTile>(a, seq))) * per_seq; ++seq) upto += t;
     }
-    if (start >= before * per_seq && start < (before + mine) * per_seq)
-      for (int b = b0; b < b1; ++b) {
-        const int tiles = (visible_rows(a, b) + S::kTile - 1) / S::kTile;
-        if (start < (before + tiles) * per_seq) {
-          plan.before = before;
-          plan.seq = b;
-          break;
-        }
-        before += tiles;
-      }
-    __syncthreads();
+    const int owner = __ffs(__ballot_sync(0xffffffffu, seq >= 0)) - 1;
+    first_seq = __shfl_sync(0xffffffffu, seq, owner);
+    before = __shfl_sync(0xffffffffu, upto, owner);
   }
-  int64_t at = share_start(plan.total, plan.ctas, (int)blockIdx.x);
-  const int64_t end = share_start(plan.total, plan.ctas, (int)blockIdx.x + 1);   // > at
 
   // A place in the list: a tile of a head, and what its addresses need.
   struct Place {
     int seq, head, rows, tiles, tile;   // head: within the sequence, over passes
   };
   Place here;
-  here.seq = plan.seq;
+  here.seq = first_seq;
   here.rows = visible_rows(a, here.seq);
   here.tiles = (here.rows + S::kTile - 1) / S::kTile;
   {
-    const int64_t in_seq = at - plan.before * per_seq;
-    here.head = (int)(in_seq / here.tiles);
+    const int64_t in_seq = at - before * per_seq;
+    here.head = in_seq < ((int64_t)1 << 32) ? (int)((uint32_t)in_seq / (uint32_t)here.tiles) : (int)(in_seq / here.tiles);
     here.tile = (int)(in_seq - (int64_t)here.head * here.tiles);
   }
   // Moves p, whose tile may have run past its head, to the head that holds it (which exists).
@@ -372,7 +383,7 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
     const int64_t q0 = bh * a.group + (int64_t)pass * a.tile_q;
     const int64_t seg_end = min(end, at + (here.tiles - here.tile));
     const int n = here.rows;
-    float* logits = a.score ? a.logits + vh * a.cap * a.tile_q : nullptr;
+    float* logits = a.score ? a.logits + vh * a.tile_q * a.logit_stride : nullptr;
 
     // B operands of the first product: channels c .. c + 3 of the query of column j for each step, as the
     // lane's share of the rows is laid out (see `first product` below).
@@ -557,13 +568,17 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
             if (16 * sub + 8 * (e / 2) >= left) sv[sub][e] = -INFINITY;
       }
       if (logits && !(FOUR && i >= 2)) {
-        float* to = logits + ((int64_t)base + jrow) * a.tile_q + qa;
 #pragma unroll
-        for (int sub = 0; sub < kSub; ++sub)
+        for (int e2 = 0; e2 < 2; ++e2) {
+          float* to = logits + (qa + e2) * a.logit_stride + base + jrow;
+          if (qa + e2 < tile_q) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (16 * sub + 8 * (e / 2) < left && qa + e % 2 < tile_q)
-              to[(16 * sub + 8 * (e / 2)) * a.tile_q + e % 2] = sv[sub][e];
+            for (int sub = 0; sub < kSub; ++sub)
+#pragma unroll
+              for (int half = 0; half < 2; ++half)
+                if (16 * sub + 8 * half < left) to[16 * sub + 8 * half] = sv[sub][2 * half + e2];
+          }
+        }
       }
       float top[2] = {m[0], m[1]};
 #pragma unroll
@@ -750,7 +765,10 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
       }
       if (whole) {
         store1<IO>(static_cast<IO*>(a.out) + q0 * D + u, sum == 0.f ? 0.f : x / sum);
-        if (c == 0 && a.score) {
+        if (c == 0 && a.direct) {
+          head_m[qq] = top == -INFINITY ? 0.f : top;
+          head_r[qq] = sum == 0.f ? 0.f : 1.0f / sum;
+        } else if (c == 0 && a.score) {
           a.stats[vh * 2 * a.tile_q + qq] = top;
           a.stats[(vh * 2 + 1) * a.tile_q + qq] = sum;
         }
@@ -762,6 +780,15 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
         }
       }
     }
+    if (a.direct && a.score) {   // (one pass: the launcher saw to it)
+      __syncthreads();
+      float* sc = a.score + bh * a.cap;
+      for (int r = tid; r < n; r += S::kThreads) {
+        float w = 0.f;
+        for (int qq = 0; qq < tile_q; ++qq) w = fmaf(ex2(logits[qq * a.logit_stride + r] - head_m[qq]), head_r[qq], w);
+        sc[r] = a.decay != 0.f ? fmaf(a.decay, sc[r], w) : w;
+      }
+    }
     // the next head
     here.tile += (int)(seg_end - at);
     at = seg_end;
@@ -770,121 +797,144 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
   cp_wait<0>();
 }
 
-// The second launch: block (0, head) joins the parts of a head's passes, blocks (1 .., head) add the
-// weights of kJoinRows rows each to its scores.
+// The second launch. Its work comes in items of one warp each: an output row whose head was cut (or is
+// empty), or kJoinRows rows of a head's scores. Where a head's parts lie follows from the schedule.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 1024;
+constexpr int kJoinRows = 256;
+
+// A head's parts: the last segment of one CTA (its slot 1, unless the share starts with the head) and the
+// first of `more` others after it.
+struct Parts {
+  const float* first;
+  const float* rest;
+  int64_t stride;   // from one of the rest to the next
+  int more;
+  __device__ __forceinline__ const float* operator[](int i) const { return i ? rest + (i - 1) * stride : first; }
+};
+
+template <int D> __device__ __forceinline__ Parts find_parts(const AttendArgs& a, int64_t total, int64_t f0, int tiles) {
+  const int ctas = working_ctas(total, a.ctas);
+  const int64_t size = (int64_t)a.tile_q * (D + 2);
+  const int c0 = share_of(total, ctas, f0);
+  Parts p;
+  p.more = share_of(total, ctas, f0 + tiles - 1) - c0;
+  p.first = a.parts + ((int64_t)c0 * 2 + (share_start(total, ctas, c0) < f0 ? 1 : 0)) * size;
+  p.rest = a.parts + ((int64_t)c0 + 1) * 2 * size;
+  p.stride = 2 * size;
+  return p;
+}
+
+// Adds a part's maximum and sum to a running pair.
+__device__ __forceinline__ void join(float& top, float& sum, float m, float l) {
+  if (m == -INFINITY) return;
+  const float next = fmaxf(top, m);
+  sum = fmaf(l, ex2(m - next), top == -INFINITY ? 0.f : sum * ex2(top - next));
+  top = next;
+}
 
 template <typename IO, int D, int TILE>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(AttendArgs a) {
-  __shared__ int64_t sums[kJoinThreads / 32];
-  __shared__ int64_t seq_before, all;   // tiles
-  __shared__ float head_m[kQueryTile], head_r[kQueryTile];
-  const int tid = threadIdx.x;
-  const int64_t bh = blockIdx.y;
-  const int b = (int)(bh / a.heads), h = (int)(bh % a.heads);
+  const int lane = threadIdx.x % 32;
   const int per_seq = a.heads * a.passes;
-  {
-    int64_t mine = 0, upto = 0, total, upto_total;
-    for (int s = tid; s < a.batch; s += kJoinThreads) {
-      const int t = (visible_rows(a, s) + TILE - 1) / TILE;
-      mine += t;
-      if (s < b) upto += t;
+  const SeqScan scan = scan_sequences<TILE>(a);
+  const int64_t total = scan.total * per_seq;   // tiles
+  // tiles of the sequences before b (all lanes ask together)
+  auto tiles_before = [&](int b) {
+    int64_t upto = -1;
+    if (b >= scan.b0 && b < scan.b1) {
+      upto = scan.upto;
+      for (int s = scan.b0; s < b; ++s) upto += tiles_of<TILE>(a, s);
     }
-    block_scan64<kJoinThreads>(mine, sums, &total);
-    __syncthreads();
-    block_scan64<kJoinThreads>(upto, sums, &upto_total);
-    if (tid == 0) {
-      all = total * per_seq;
-      seq_before = upto_total * per_seq;
-    }
-    __syncthreads();
-  }
-  const int ctas = working_ctas(all, a.ctas);
-  const int n = visible_rows(a, b);
-  const int tiles = (n + TILE - 1) / TILE;
-  const int r0 = ((int)blockIdx.x - 1) * kJoinRows, r1 = min(n, r0 + kJoinRows);
-  if (blockIdx.x > 0 && r0 >= n) return;
+    return __shfl_sync(0xffffffffu, upto, __ffs(__ballot_sync(0xffffffffu, upto >= 0)) - 1);
+  };
+  const int64_t out_rows = (int64_t)a.batch * a.heads * a.group;
+  const int chunks = a.score ? (int)((a.cap + kJoinRows - 1) / kJoinRows) : 0;
+  const int64_t items = out_rows + (int64_t)a.batch * a.heads * chunks;
+  const int64_t warps = (int64_t)gridDim.x * (kJoinThreads / 32);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-
-  constexpr int kPer = kJoinRows / kJoinThreads;
-  float w[kPer];   // the summed weights of this thread's rows
+  for (int64_t item = (int64_t)blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32; item < items; item += warps) {
+    if (item < out_rows) {
+      const int64_t bh = item / a.group;
+      const int b = (int)(bh / a.heads), h = (int)(bh - (int64_t)b * a.heads), g = (int)(item - bh * a.group);
+      const int pass = g / a.tile_q, q = g - pass * a.tile_q;
+      const int tiles = tiles_of<TILE>(a, b);
+      constexpr int kPer = D / 32;
+      float x[kPer] = {};
+      float scale = 0.f;
+      if (tiles > 0) {
+        const Parts parts = find_parts<D>(a, total, tiles_before(b) * per_seq + (int64_t)(h * a.passes + pass) * tiles, tiles);
+        if (parts.more == 0) continue;   // finished in the first launch
+        const int at_m = a.tile_q * D + q, at_l = a.tile_q * (D + 1) + q;
+        float top = -INFINITY, sum = 0.f;
+        for (int i = lane; i <= parts.more; i += 32) join(top, sum, __ldcg(parts[i] + at_m), __ldcg(parts[i] + at_l));
+        const float all = warp_max(top);
+        sum = warp_sum(top == -INFINITY ? 0.f : sum * ex2(top - all));
+        scale = sum == 0.f ? 0.f : 1.0f / sum;   // a NaN stays one
+#pragma unroll 4
+        for (int i = 0; i <= parts.more; ++i) {
+          const float m = __ldcg(parts[i] + at_m);
+          const float f = m == -INFINITY ? 0.f : ex2(m - all);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) w[i] = 0.f;
-  for (int pass = 0; pass < a.passes; ++pass) {
-    const int tile_q = min(a.tile_q, a.group - pass * a.tile_q);
-    const int64_t vh = bh * a.passes + pass;
-    const int64_t q0 = bh * a.group + (int64_t)pass * a.tile_q;
-    const int64_t f0 = seq_before + (int64_t)(h * a.passes + pass) * tiles;
-    IO* out = static_cast<IO*>(a.out) + q0 * D;
-    if (tiles == 0) {   // (block 0 only)
-      for (int u = tid; u < tile_q * D; u += kJoinThreads) store1<IO>(out + u, 0.f);
+          for (int e = 0; e < kPer; ++e) x[e] = fmaf(__ldcg(parts[i] + q * D + 32 * e + lane), f, x[e]);
+        }
+      }
+      IO* out = static_cast<IO*>(a.out) + item * D;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) store1<IO>(out + 32 * e + lane, x[e] * scale);
       continue;
     }
-    const int c0 = share_of(all, ctas, f0), c1 = share_of(all, ctas, f0 + tiles - 1);
-    if (c0 == c1 && blockIdx.x == 0) continue;   // finished in the first launch
-    const int64_t size = (int64_t)a.tile_q * (D + 2);
-    // The head is the last segment of CTA c0 (slot 1, unless the share starts with it) and the first of the others.
-    const float* first = a.parts + ((int64_t)c0 * 2 + (share_start(all, ctas, c0) < f0 ? 1 : 0)) * size;
-    const float* rest = a.parts + ((int64_t)c0 + 1) * 2 * size;
-    const int more = c1 - c0;
-    __syncthreads();   // the last pass's maxima have been used
-    for (int qq = tid / 32; qq < tile_q; qq += kJoinThreads / 32) {   // a warp per query
-      const int lane = tid % 32;
-      float top, sum;
-      if (c0 == c1) {
-        top = __ldcg(a.stats + vh * 2 * a.tile_q + qq);
-        sum = __ldcg(a.stats + (vh * 2 + 1) * a.tile_q + qq);
-      } else {
-        const int64_t at_m = (int64_t)a.tile_q * D + qq, at_l = (int64_t)a.tile_q * (D + 1) + qq;
-        top = -INFINITY;
-        for (int i = lane; i <= more; i += 32) top = fmaxf(top, __ldcg((i ? rest + (i - 1) * 2 * size : first) + at_m));
-        top = warp_max(top);
-        sum = 0.f;
-        for (int i = lane; i <= more; i += 32) {
-          const float* p = i ? rest + (i - 1) * 2 * size : first;
-          const float m = __ldcg(p + at_m);
-          if (m != -INFINITY) sum = fmaf(__ldcg(p + at_l), ex2(m - top), sum);
+    const int64_t bh = (item - out_rows) / chunks;
+    const int b = (int)(bh / a.heads), h = (int)(bh - (int64_t)b * a.heads);
+    const int n = visible_rows(a, b);
+    const int row = (int)(item - out_rows - bh * chunks) * kJoinRows + lane;   // + 32, 64, ...
+    if (row - lane >= n) continue;
+    const int tiles = tiles_of<TILE>(a, b);
+    const int64_t f0 = tiles_before(b) * per_seq + (int64_t)h * a.passes * tiles;
+    constexpr int kPer = kJoinRows / 32;
+    float w[kPer] = {};   // the summed weights
+    for (int pass = 0; pass < a.passes; ++pass) {
+      const int tile_q = min(a.tile_q, a.group - pass * a.tile_q);
+      const int64_t vh = bh * a.passes + pass;
+      const Parts parts = find_parts<D>(a, total, f0 + (int64_t)pass * tiles, tiles);
+      // four lanes a query
+      const int q = lane / 4;
+      float top = -INFINITY, sum = 0.f;
+      if (q < tile_q) {
+        if (parts.more == 0) {
+          top = __ldcg(a.stats + vh * 2 * a.tile_q + q);
+          sum = lane % 4 == 0 ? __ldcg(a.stats + (vh * 2 + 1) * a.tile_q + q) : 0.f;
+        } else {
+          for (int i = lane % 4; i <= parts.more; i += 4)
+            join(top, sum, __ldcg(parts[i] + a.tile_q * D + q), __ldcg(parts[i] + a.tile_q * (D + 1) + q));
         }
-        sum = warp_sum(sum);
       }
-      if (lane == 0) {
-        head_m[qq] = top == -INFINITY ? 0.f : top;
-        head_r[qq] = sum == 0.f ? 0.f : 1.0f / sum;   // a NaN stays one
-      }
-    }
-    __syncthreads();
-    if (blockIdx.x == 0) {
-      for (int u = tid; u < tile_q * D; u += kJoinThreads) {
-        const int qq = u / D;
-        const int64_t at_m = (int64_t)a.tile_q * D + qq;
-        float x = 0.f;
-#pragma unroll 4
-        for (int i = 0; i <= more; ++i) {
-          const float* p = i ? rest + (i - 1) * 2 * size : first;
-          const float m = __ldcg(p + at_m), v = __ldcg(p + u);
-          x = fmaf(v, m == -INFINITY ? 0.f : ex2(m - head_m[qq]), x);
-        }
-        store1<IO>(out + u, x * head_r[qq]);
-      }
-    } else {
-      const float* logits = a.logits + vh * a.cap * a.tile_q;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int r = r0 + i * kJoinThreads + tid;
-        if (r < r1)
-          for (int qq = 0; qq < tile_q; ++qq)
-            w[i] = fmaf(ex2(__ldcg(logits + (int64_t)r * a.tile_q + qq) - head_m[qq]), head_r[qq], w[i]);
+      for (int off = 1; off < 4; off <<= 1) {
+        const float m = __shfl_xor_sync(0xffffffffu, top, off), l = __shfl_xor_sync(0xffffffffu, sum, off);
+        join(top, sum, m, l);
+      }
+      const float scale = sum == 0.f ? 0.f : 1.0f / sum;
+      const float shift = top == -INFINITY ? 0.f : top;
+      const float* logits = a.logits + vh * a.tile_q * a.logit_stride + row;
+      for (int qq = 0; qq < tile_q; ++qq, logits += a.logit_stride) {
+        const float m = __shfl_sync(0xffffffffu, shift, 4 * qq), r = __shfl_sync(0xffffffffu, scale, 4 * qq);
+        float x[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) x[i] = row + 32 * i < n ? __ldcg(logits + 32 * i) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) w[i] = fmaf(ex2(x[i] - m), r, w[i]);
       }
     }
-  }
-  if (blockIdx.x > 0) {
-    float* sc = a.score + bh * a.cap;
+    float* sc = a.score + bh * a.cap + row;
+    float old[kPer] = {};
+    if (a.decay != 0.f) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int r = r0 + i * kJoinThreads + tid;
-      if (r < r1) sc[r] = a.decay != 0.f ? fmaf(a.decay, sc[r], w[i]) : w[i];
+      for (int i = 0; i < kPer; ++i)
+        if (row + 32 * i < n) old[i] = sc[32 * i];
     }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (row + 32 * i < n) sc[32 * i] = fmaf(a.decay, old[i], w[i]);
   }
 }
 
@@ -913,6 +963,7 @@ cudaError_t launch_typed(const AttendJob& job) {
   a.parts = reinterpret_cast<float*>(ws + L.parts);
   a.stats = reinterpret_cast<float*>(ws + L.stats);
   a.logits = reinterpret_cast<float*>(ws + L.logits);
+  a.logit_stride = L.logit_stride;
   a.dev_status = job.dev_status;
   // One wave of CTAs, or fewer where their warps would have no tile each.
   const int smem = S::smem(L.tile_q);
@@ -926,16 +977,24 @@ cudaError_t launch_typed(const AttendJob& job) {
     if (resident < 1) return cudaErrorInvalidConfiguration;
     occupancy[L.tile_q].store(resident, std::memory_order_relaxed);
   }
-  const int64_t tiles = (int64_t)job.batch * job.heads * L.passes * ((job.cap + S::kTile - 1) / S::kTile);
+  const int64_t heads = (int64_t)job.batch * job.heads * L.passes;
+  // Short caches: a CTA per head, in one launch.
+  a.direct = job.cap <= kDirectTiles * kWarps * S::kTile && L.passes == 1;
+  const int64_t tiles = heads * ((job.cap + S::kTile - 1) / S::kTile);
   int64_t ctas = (int64_t)device_sm_count() * resident;
   if (ctas > (tiles + kWarps - 1) / kWarps) ctas = (tiles + kWarps - 1) / kWarps;
   if (ctas > L.max_ctas) ctas = L.max_ctas;
+  if (a.direct) ctas = heads;
   a.ctas = (int)ctas;
   attend_kernel<Q4, IO, D, FOUR><<<(unsigned)ctas, S::kThreads, smem, job.stream>>>(a);
   err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
+  if (err != cudaSuccess || a.direct) return err;
+  const int64_t items = (int64_t)job.batch * job.q_heads +
+                        (job.score ? (int64_t)job.batch * job.heads * ((job.cap + kJoinRows - 1) / kJoinRows) : 0);
+  int64_t blocks = (items + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+  if (blocks > (int64_t)device_sm_count() * 8) blocks = (int64_t)device_sm_count() * 8;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1 + (unsigned)(job.score ? (job.cap + kJoinRows - 1) / kJoinRows : 0), (unsigned)(job.batch * job.heads));
+  cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = job.stream;
   cudaLaunchAttribute attr[1];
@@ -971,7 +1030,8 @@ AttendLayout attend_layout(int batch, int q_heads, int heads, int head_dim, int6
   L.parts = 0;
   L.stats = L.parts + up((size_t)L.max_ctas * 2 * L.tile_q * (head_dim + 2) * sizeof(float));
   L.logits = L.stats + up(vh * 2 * L.tile_q * sizeof(float));
-  L.total = L.logits + (scored ? up(vh * (size_t)cap * L.tile_q * sizeof(float)) : 0);
+  L.logit_stride = (cap + 7) / 8 * 8;
+  L.total = L.logits + (scored ? up(vh * (size_t)L.logit_stride * L.tile_q * sizeof(float)) : 0);
   return L;
 }
 

@@ -46,6 +46,7 @@ struct AttendJob {
 // Workspace layout of an attention call (byte offsets, each 256-aligned), and how its queries are cut.
 struct AttendLayout {
   size_t parts, stats, logits, total;
+  int64_t logit_stride;
   int tile_q, passes, max_ctas;
 };
 

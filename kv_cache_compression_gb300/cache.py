@@ -14,7 +14,7 @@ from functools import lru_cache
 import torch
 
 from . import snapkv as _sk
-from .snapkv import ERR_INVALID_ARG, OK, SnapKVError, new_workspace
+from .snapkv import ERR_INVALID_ARG, OK, SnapKVError
 
 GROUP = 64   # channels of a 4-bit row that share one (h, z)
 
@@ -26,14 +26,13 @@ class _Q4Struct(ctypes.Structure):
                 ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
-_lib = None
+_functions = {}   # name -> library function with its prototype
 
 
 def lib():
     """The loaded library with the prototypes of include/snapkv_cache.h."""
-    global _lib
-    if _lib is None:
-        L = _sk.lib()
+    L = _sk.lib()
+    if not _functions:
         P, I32, I64, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
         C = ctypes.POINTER(_Q4Struct)
         for name, res, args in [
@@ -48,20 +47,21 @@ def lib():
                 ("snapkv_q4_evict", I32, [C, P, P, P, I64, I64, P, P, SZ, P, P])]:
             f = getattr(L, name)
             f.restype, f.argtypes = res, args
-        _lib = L
-    return _lib
+            _functions[name] = f
+    return L
 
 
 def _check(name, t, shape, dtype, device):
     """One tensor argument: shape, type, device and density (the kernels take dense tensors)."""
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _lengths(name, t, batch, device):
@@ -76,17 +76,25 @@ def _status(t, device):
     return t.data_ptr()
 
 
+_DTYPES = {torch.float32: _sk.F32, torch.bfloat16: _sk.BF16}
+
+
+def _dtype_code(t):
+    code = _DTYPES.get(t.dtype)
+    return _sk._dtype_code(t) if code is None else code   # (which raises)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
 def _room(workspace, need, device):
-    """The caller's workspace or a new one."""
+    """The caller's workspace or a new one, and its bytes."""
     if workspace is None:
-        return new_workspace(need, device)
+        return torch.empty(need, dtype=torch.uint8, device=device), need
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _call(name, device, stream, *args):
@@ -96,7 +104,10 @@ def _call(name, device, stream, *args):
     (the tensors' device is the current one) takes the raw stream handle and no context manager."""
     if device.type != "cuda":
         raise ValueError(f"{name} needs CUDA tensors, not {device}")
-    f = getattr(_lib or lib(), name)
+    f = _functions.get(name)
+    if f is None:
+        lib()
+        f = _functions[name]
     index = device.index
     handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == index:
@@ -166,11 +177,12 @@ def _attend_args(where, q, shape, dev, len_, score, out, workspace):
     _lengths("len_", len_, B, dev)
     if out is None:
         out = torch.empty_like(q)
-    _check("out", out, q.shape, q.dtype, dev)
+    else:
+        _check("out", out, q.shape, q.dtype, dev)
     if score is not None:
         _check("score", score, (B, H, cap), torch.float32, dev)
-    workspace = _room(workspace, scored_workspace_size(B, q_heads, H, d, cap, score is not None), dev)
-    return q_heads, out, workspace, workspace.numel() * workspace.element_size()
+    workspace, ws_bytes = _room(workspace, scored_workspace_size(B, q_heads, H, d, cap, score is not None), dev)
+    return q_heads, out, workspace, ws_bytes
 
 
 def decode_attend_scored(q, k_cache, v_cache, len_, score=None, *, decay=1.0, out=None, workspace=None,
@@ -187,7 +199,7 @@ def decode_attend_scored(q, k_cache, v_cache, len_, score=None, *, decay=1.0, ou
     q_heads, out, workspace, ws_bytes = _attend_args("snapkv_decode_attend_scored", q, k_cache.shape, dev, len_,
                                                      score, out, workspace)
     _call("snapkv_decode_attend_scored", dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), cap,
-          _ptr(len_), _ptr(score), float(decay), _ptr(out), B, q_heads, H, d, _sk._dtype_code(q),
+          _ptr(len_), _ptr(score), float(decay), _ptr(out), B, q_heads, H, d, _dtype_code(q),
           _ptr(workspace), ws_bytes, _status(dev_status, dev))
     return out
 
@@ -199,7 +211,7 @@ def q4_decode_attend(q, cache, len_, score=None, *, decay=1.0, out=None, workspa
     q_heads, out, workspace, ws_bytes = _attend_args("snapkv_q4_decode_attend", q, cache.shape, dev, len_, score,
                                                      out, workspace)
     _call("snapkv_q4_decode_attend", dev, stream, _ptr(q), cache._struct(), _ptr(len_), _ptr(score),
-          float(decay), _ptr(out), q_heads, _sk._dtype_code(q), _ptr(workspace), ws_bytes,
+          float(decay), _ptr(out), q_heads, _dtype_code(q), _ptr(workspace), ws_bytes,
           _status(dev_status, dev))
     return out
 
@@ -218,9 +230,10 @@ def q4_append(cache, k_new, v_new, len_in, len_out=None, *, n_new=None, dev_stat
         _lengths("n_new", n_new, B, dev)
     if len_out is None:
         len_out = torch.empty_like(len_in)
-    _lengths("len_out", len_out, B, dev)
+    else:
+        _lengths("len_out", len_out, B, dev)
     _call("snapkv_q4_append", dev, stream, cache._struct(), _ptr(k_new), _ptr(v_new), rows,
-          _ptr(n_new), _ptr(len_in), _ptr(len_out), _sk._dtype_code(k_new), _status(dev_status, dev))
+          _ptr(n_new), _ptr(len_in), _ptr(len_out), _dtype_code(k_new), _status(dev_status, dev))
     return len_out
 
 
@@ -233,12 +246,17 @@ def q4_read(cache, rows, *, start=None, dtype=None, k_out=None, v_out=None, stre
         dtype = torch.bfloat16 if k_out is None else k_out.dtype
     if start is not None:
         _lengths("start", start, B, dev)
-    k_out = torch.empty((B, H, rows, d), dtype=dtype, device=dev) if k_out is None else k_out
-    v_out = torch.empty((B, H, rows, d), dtype=dtype, device=dev) if v_out is None else v_out
-    _check("k_out", k_out, (B, H, rows, d), dtype, dev)
-    _check("v_out", v_out, (B, H, rows, d), dtype, dev)
+    shape = (B, H, rows, d)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _check("k_out", k_out, shape, dtype, dev)
+    if v_out is None:
+        v_out = torch.empty_like(k_out)
+    else:
+        _check("v_out", v_out, shape, dtype, dev)
     _call("snapkv_q4_read", dev, stream, cache._struct(), _ptr(start), int(rows), _ptr(k_out),
-          _ptr(v_out), _sk._dtype_code(k_out))
+          _ptr(v_out), _dtype_code(k_out))
     return k_out, v_out
 
 
@@ -249,14 +267,15 @@ def _evict_args(shape, dev, score, len_in, len_out, keep, recent, idx_out, want_
     _lengths("len_in", len_in, B, dev)
     if len_out is None:
         len_out = torch.empty_like(len_in)
-    _lengths("len_out", len_out, B, dev)
+    else:
+        _lengths("len_out", len_out, B, dev)
     left = int(keep) + int(recent)
-    if idx_out is None and want_idx and left > 0:
-        idx_out = torch.empty((B, H, left), dtype=torch.int32, device=dev)
     if idx_out is not None:
         _check("idx_out", idx_out, (B, H, left), torch.int32, dev)
-    workspace = _room(workspace, evict_workspace_size(B, H, cap), dev)
-    return len_out, idx_out, workspace, workspace.numel() * workspace.element_size()
+    elif want_idx and left > 0:
+        idx_out = torch.empty((B, H, left), dtype=torch.int32, device=dev)
+    workspace, ws_bytes = _room(workspace, evict_workspace_size(B, H, cap), dev)
+    return len_out, idx_out, workspace, ws_bytes
 
 
 def evict(k_cache, v_cache, score, len_in, len_out=None, *, keep, recent, idx_out=None, want_idx=True,
@@ -274,7 +293,7 @@ def evict(k_cache, v_cache, score, len_in, len_out=None, *, keep, recent, idx_ou
                                                         idx_out, want_idx, workspace)
     _call("snapkv_evict", dev, stream, _ptr(k_cache), _ptr(v_cache), cap, _ptr(score),
           _ptr(len_in), _ptr(len_out), int(keep), int(recent), _ptr(idx_out), B, H, d,
-          _sk._dtype_code(k_cache), _ptr(workspace), ws_bytes, _status(dev_status, dev))
+          _dtype_code(k_cache), _ptr(workspace), ws_bytes, _status(dev_status, dev))
     return len_out, idx_out
 
 

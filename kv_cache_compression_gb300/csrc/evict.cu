@@ -1,11 +1,12 @@
 // In-place eviction by accumulated attention: the heaviest rows and the newest ones stay.
 //
-// One thread-block cluster per (sequence, head). The candidates' scores (slots below n = len - recent)
-// become 32-bit keys whose unsigned order is the scores' order; each CTA keeps its span's keys in
-// shared memory where they fit. A radix select (four 8-bit digits, histograms added up through
-// distributed shared memory) finds the key of rank `keep`; ties at it go to the lower slots. A scan in
-// slot order then lists the freed slots below `keep` and the staying rows above it, and the i-th of
-// the one takes the i-th of the other.
+// A CTA per (sequence, head), or a thread-block cluster for long caches of few heads. The candidates'
+// scores (slots below n = len - recent) become 32-bit keys whose unsigned order is the scores' order;
+// each CTA keeps its span's keys in shared memory where they fit. A radix select (four 8-bit digits,
+// histograms in four copies against atomics meeting at one bin, added up through distributed shared
+// memory in a cluster) finds the key of rank `keep`; ties at it go to the lower slots. A scan in slot
+// order then lists the freed slots below `keep` and the staying rows above it, and the i-th of the one
+// takes the i-th of the other.
 //
 // In-place order of moves. Freed slots are nobody's source and the rows they take lie at or above
 // `keep`, so those moves need no order among themselves. The newest rows then come down by
@@ -23,11 +24,11 @@
 namespace snapkv {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kKeysSmem = 64 * 1024;   // a span's keys stay in shared memory up to this size
-constexpr int kMaxIndex = kThreads;    // pairs resolved at a time
+constexpr int kMaxIndex = 256;         // pairs resolved at a time
+constexpr int kCopies = 4;             // of a histogram
+constexpr int kRun = 16;               // keys a thread looks at between two scans, at most
 
 struct EvictArgs {
   EvictJob j;
@@ -41,9 +42,9 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Exclusive sum over the block's threads of v, in thread order; *total is the block's sum. `sums` holds
-// kWarps + 1 values; the caller syncs between two uses of the same one.
-__device__ __forceinline__ int block_scan(int v, int* sums, int* total) {
+// Exclusive sum over the block's threads of v, in thread order; *total is the block's sum. The caller
+// syncs between two uses of `sums`.
+template <int WARPS> __device__ __forceinline__ int block_scan(int v, int* sums, int* total) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   int x = v;
 #pragma unroll
@@ -53,35 +54,39 @@ __device__ __forceinline__ int block_scan(int v, int* sums, int* total) {
   }
   if (lane == 31) sums[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int s = lane < kWarps ? sums[lane] : 0;
+  int before = 0, all = 0;
 #pragma unroll
-    for (int off = 1; off < kWarps; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, off);
-      if (lane >= off) s += y;
-    }
-    if (lane < kWarps) sums[lane] = s;
+  for (int w = 0; w < WARPS; ++w) {
+    const int y = sums[w];
+    if (w < warp) before += y;
+    all += y;
   }
-  __syncthreads();
-  *total = sums[kWarps - 1];
-  return x - v + (warp ? sums[warp - 1] : 0);
+  *total = all;
+  return before + x - v;
 }
 
-template <int ROW, int META>
-__global__ void __launch_bounds__(kThreads) evict_kernel(EvictArgs args) {
+template <int ROW, int META, int THREADS>
+__global__ void __launch_bounds__(THREADS) evict_kernel(EvictArgs args) {
   const EvictJob& j = args.j;
   constexpr int kPieces = ROW / 16;       // 16-byte pieces of a row of K (and of V)
+  constexpr int kWarps = THREADS / 32;
   extern __shared__ uint32_t key_smem[];
-  __shared__ uint32_t hist[4][256];       // one per digit, read by the whole cluster
-  __shared__ uint32_t all[256];
-  __shared__ uint32_t pick_digit, pick_left;
+  __shared__ uint32_t hist[4][kCopies][256];   // a digit's histogram; copy 0 is read by the whole cluster
+  __shared__ __align__(16) uint32_t all[256];
   __shared__ int counts[3];               // ties, freed slots, staying rows of this CTA's span
-  __shared__ int sums_a[kWarps + 1], sums_b[kWarps + 1];
+  __shared__ int sums_a[kWarps], sums_b[kWarps];
   __shared__ int first_free[kMaxCluster + 1], first_stay[kMaxCluster + 1];
   __shared__ int pair_to[kMaxIndex], pair_from[kMaxIndex];
 
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid % 32;
   const uint32_t rank = ptx::cluster_rank(), csize = ptx::cluster_size();
+  const bool alone = csize == 1;
+  auto sync_head = [&] {   // all CTAs of the head
+    if (alone)
+      __syncthreads();
+    else
+      ptx::cluster_sync();
+  };
   const int64_t bh = blockIdx.x / csize;
   const int b = (int)(bh / j.heads);
   const bool first = bh % j.heads == 0 && rank == 0 && tid == 0;
@@ -96,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(EvictArgs args) {
   int32_t* idx = j.idx ? j.idx + bh * left : nullptr;
   if (len <= left) {   // the whole cluster agrees
     if (idx)
-      for (int s = (int)rank * kThreads + tid; s < left; s += (int)csize * kThreads) idx[s] = s;
+      for (int s = (int)rank * THREADS + tid; s < left; s += (int)csize * THREADS) idx[s] = s;
     return;
   }
   const int n = len - recent;
@@ -105,104 +110,164 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(EvictArgs args) {
   const int per = (n + (int)csize - 1) / (int)csize;
   const int s0 = min((int64_t)n, (int64_t)rank * per), s1 = min((int64_t)n, (int64_t)s0 + per);
 
-  for (int i = tid; i < 4 * 256; i += kThreads) (&hist[0][0])[i] = 0;
+  // The keys arrive while the histograms are cleared; the first digit is counted from them on the way.
   if (tid < 3) counts[tid] = 0;
-  if (args.keys_in_smem)
-    for (int s = s0 + tid; s < s1; s += kThreads) key_smem[s - s0] = order_key(score[s]);
+  for (int i = tid; i < 4 * kCopies * 256; i += THREADS) (&hist[0][0][0])[i] = 0;
   __syncthreads();
   auto key_of = [&](int s) { return args.keys_in_smem ? key_smem[s - s0] : order_key(score[s]); };
+  const int copy = tid / 32 % kCopies;
+#pragma unroll 4
+  for (int s = s0 + tid; s < s1; s += THREADS) {
+    const uint32_t key = order_key(score[s]);
+    if (args.keys_in_smem) key_smem[s - s0] = key;
+    atomicAdd(&hist[3][copy][key >> 24], 1u);
+  }
 
   // ---- the key of rank `keep` from the top, digit by digit; `want` of the keys that share the digits
-  // found so far are kept. (keep = 0: nothing is, whatever the digits.)
-  uint32_t prefix = 0, want = (uint32_t)keep;
+  // found so far are kept, of `among`. (keep = 0: none, and the search runs to the largest key.)
+  uint32_t prefix = 0, want = (uint32_t)keep, among = 0;
   for (int d = 3; d >= 0; --d) {
     const int shift = 8 * d;
-    for (int s = s0 + tid; s < s1; s += kThreads) {
-      const uint32_t key = key_of(s);
-      if (d == 3 || key >> (shift + 8) == prefix) atomicAdd(&hist[d][(key >> shift) & 255u], 1u);
-    }
-    ptx::cluster_sync();
-    if (tid < 256) {
-      uint32_t x = 0;
-      for (uint32_t r = 0; r < csize; ++r) x += ptx::dsmem_ld_u32(ptx::map_rank(&hist[d][tid], r));
-      all[tid] = x;
-    }
+    if (d < 3)
+      for (int s = s0 + tid; s < s1; s += THREADS) {
+        const uint32_t key = key_of(s);
+        if (key >> (shift + 8) == prefix) atomicAdd(&hist[d][copy][(key >> shift) & 255u], 1u);
+      }
     __syncthreads();
-    if (tid < 32) {   // eight bins a lane, from the top
-      uint32_t mine = 0;
-      for (int i = 0; i < 8; ++i) mine += all[255 - (8 * tid + i)];
-      uint32_t upto = mine;
+    for (int i = tid; i < 256; i += THREADS) {
+      uint32_t x = hist[d][0][i];
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, upto, off);
-        if (tid >= off) upto += y;
-      }
-      uint32_t above = upto - mine;
-      if (want > above && want <= upto)
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t bin = 255 - (8 * tid + i);
-          if (want <= above + all[bin]) {
-            pick_digit = bin;
-            pick_left = want - above;
-            break;
-          }
-          above += all[bin];
-        }
-      if (keep == 0 && tid == 0) {
-        pick_digit = 255;
-        pick_left = 0;
+      for (int c = 1; c < kCopies; ++c) x += hist[d][c][i];
+      (alone ? all : hist[d][0])[i] = x;
+    }
+    if (!alone) {
+      ptx::cluster_sync();
+      for (int i = tid; i < 256; i += THREADS) {
+        uint32_t x = 0;
+        for (uint32_t r = 0; r < csize; ++r) x += ptx::dsmem_ld_u32(ptx::map_rank(&hist[d][0][i], r));
+        all[i] = x;
       }
     }
     __syncthreads();
-    prefix = (prefix << 8) | pick_digit;
-    want = pick_left;
+    // Every warp finds the digit for itself, eight bins a lane from the top.
+    uint32_t bins[8], mine = 0;
+    {
+      const uint4 hi = *reinterpret_cast<const uint4*>(&all[252 - 8 * lane]), lo = *reinterpret_cast<const uint4*>(&all[248 - 8 * lane]);
+      bins[0] = hi.w; bins[1] = hi.z; bins[2] = hi.y; bins[3] = hi.x;
+      bins[4] = lo.w; bins[5] = lo.z; bins[6] = lo.y; bins[7] = lo.x;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mine += bins[i];
+    uint32_t upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += y;
+    }
+    const uint32_t owner = __ballot_sync(0xffffffffu, want > upto - mine && want <= upto);
+    uint32_t digit = 255, next = 0, count = 0, above = upto - mine;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (want > above && want <= above + bins[i]) {
+        digit = 255 - (8 * lane + i);
+        next = want - above;
+        count = bins[i];
+      }
+      above += bins[i];
+    }
+    const int from = owner ? __ffs(owner) - 1 : 0;   // none with keep = 0 (lane 0 then has the defaults)
+    prefix = (prefix << 8) | __shfl_sync(0xffffffffu, digit, from);
+    want = __shfl_sync(0xffffffffu, next, from);
+    among = __shfl_sync(0xffffffffu, count, from);
+    // (`all` is written again behind the next digit's first barrier)
   }
 
-  // ---- ties before this span
-  {
-    int mine = 0;
-    for (int s = s0 + tid; s < s1; s += kThreads) mine += key_of(s) == prefix;
-    if (mine) atomicAdd(&counts[0], mine);
-  }
-  ptx::cluster_sync();
+  // ---- ties before this span, where not all of them stay
+  const bool rank_ties = want < among;
   int ties = 0;
-  for (uint32_t r = 0; r < rank; ++r) ties += (int)ptx::dsmem_ld_u32(ptx::map_rank(&counts[0], r));
+  if (!alone && rank_ties) {
+    int mine = 0;
+    for (int s = s0 + tid; s < s1; s += THREADS) mine += key_of(s) == prefix;
+    if (mine) atomicAdd(&counts[0], mine);
+    ptx::cluster_sync();
+    for (uint32_t r = 0; r < rank; ++r) ties += (int)ptx::dsmem_ld_u32(ptx::map_rank(&counts[0], r));
+  }
 
-  // ---- in slot order: freed slots below `keep` are listed from the front of the span's part of
-  // `slots`, staying rows at or above it from its back.
+  // ---- in slot order: freed slots below `keep` are listed from the front, staying rows at or above it
+  // from the back of the span's part of `slots` (or, few pairs of one CTA, in shared memory).
+  const bool in_smem = alone && min(keep, n - keep) <= kMaxIndex;
+  const int run = min(kRun, (s1 - s0 + THREADS - 1) / THREADS);   // neighbouring slots of a thread
   int n_free = 0, n_stay = 0;
-  for (int base = s0; base < s1; base += kThreads) {
-    const int s = base + tid;
-    const uint32_t key = s < s1 ? key_of(s) : 0u;
-    const bool tie = s < s1 && key == prefix;
-    int tie_total, total;
-    const int tie_rank = ties + block_scan(tie, sums_a, &tie_total);
-    const bool stays = s < s1 && (key > prefix ? keep > 0 : tie && tie_rank < (int)want);
-    const bool frees = s < s1 && !stays && s < keep, above = stays && s >= keep;
-    // two counts in one scan: both are at most kThreads
-    const int at = block_scan((int)frees | ((int)above << 16), sums_b, &total);
-    if (frees) slots[s0 + n_free + (at & 0xFFFF)] = s;
-    if (above) slots[s1 - 1 - (n_stay + (at >> 16))] = s;
-    if (idx && stays && s < keep) idx[s] = s;
-    ties += tie_total;
+  for (int base = s0; base < s1; base += run * THREADS) {
+    const int t0 = min((int64_t)s1, (int64_t)base + tid * run), t1 = min((int64_t)s1, (int64_t)t0 + run);
+    int tie_rank = 0;
+    if (rank_ties) {
+      int mine = 0, tie_total;
+      for (int s = t0; s < t1; ++s) mine += key_of(s) == prefix;
+      tie_rank = ties + block_scan<kWarps>(mine, sums_a, &tie_total);
+      ties += tie_total;
+    }
+    uint32_t stays = 0;   // bit per slot of the run
+    int mine = 0, total;
+    for (int s = t0; s < t1; ++s) {
+      const uint32_t key = key_of(s);
+      bool stay = key > prefix;
+      if (key == prefix) {
+        stay = want > 0 && (!rank_ties || tie_rank < (int)want);
+        ++tie_rank;
+      }
+      if (stay) stays |= 1u << (s - t0);
+      mine += stay ? (s >= keep ? 1 << 16 : 0) : (s < keep ? 1 : 0);   // two counts of at most run * THREADS < 2^15
+    }
+    int at = block_scan<kWarps>(mine, sums_b, &total);
+    for (int s = t0; s < t1; ++s) {
+      const bool stay = stays >> (s - t0) & 1u;
+      if (!stay && s < keep) {
+        const int p = n_free + (at & 0xFFFF);
+        if (in_smem)
+          pair_to[p] = s;
+        else
+          slots[s0 + p] = s;
+        at += 1;
+      } else if (stay && s >= keep) {
+        const int p = n_stay + (at >> 16);
+        if (in_smem)
+          pair_from[p] = s;
+        else
+          slots[s1 - 1 - p] = s;
+        at += 1 << 16;
+      } else if (idx && stay) {
+        idx[s] = s;
+      }
+    }
     n_free += total & 0xFFFF;
     n_stay += total >> 16;
+    __syncthreads();   // the scans' sums are free again
   }
-  if (tid == 0) {
-    counts[1] = n_free;
-    counts[2] = n_stay;
-  }
-  ptx::cluster_sync();   // also makes the lists of the other CTAs visible
-  if (tid <= (int)csize) {
-    int f = 0, t = 0;
-    for (int r = 0; r < tid; ++r) {
-      f += (int)ptx::dsmem_ld_u32(ptx::map_rank(&counts[1], (uint32_t)r));
-      t += (int)ptx::dsmem_ld_u32(ptx::map_rank(&counts[2], (uint32_t)r));
+  if (alone) {
+    if (tid == 0) {
+      first_free[0] = first_stay[0] = 0;
+      first_free[1] = n_free;
+      first_stay[1] = n_stay;
     }
-    first_free[tid] = f;
-    first_stay[tid] = t;
+    __syncthreads();
+  } else {
+    if (tid == 0) {
+      counts[1] = n_free;
+      counts[2] = n_stay;
+    }
+    ptx::cluster_sync();   // also makes the lists of the other CTAs visible
+    if (tid <= (int)csize) {
+      int f = 0, t = 0;
+      for (int r = 0; r < tid; ++r) {
+        f += (int)ptx::dsmem_ld_u32(ptx::map_rank(&counts[1], (uint32_t)r));
+        t += (int)ptx::dsmem_ld_u32(ptx::map_rank(&counts[2], (uint32_t)r));
+      }
+      first_free[tid] = f;
+      first_stay[tid] = t;
+    }
+    __syncthreads();
   }
-  __syncthreads();
 
   // ---- the i-th freed slot takes the i-th staying row; pairs are shared out evenly over the CTAs
   const int pairs = min(first_free[csize], first_stay[csize]);   // (equal)
@@ -210,38 +275,44 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(EvictArgs args) {
   const int p0 = min(pairs, (int)rank * p_per), p1 = min(pairs, p0 + p_per);
   for (int base = p0; base < p1; base += kMaxIndex) {
     const int count = min(kMaxIndex, p1 - base);
-    if (tid < count) {
-      const int p = base + tid;
-      int rf = 0, rs = 0;
-      while (p >= first_free[rf + 1]) ++rf;
-      while (p >= first_stay[rs + 1]) ++rs;
-      const int e1 = min((int64_t)n, (int64_t)(rs + 1) * per);   // end of that CTA's span
-      const int to = __ldcg(slots + (int64_t)rf * per + (p - first_free[rf]));
-      const int from = __ldcg(slots + e1 - 1 - (p - first_stay[rs]));
+    for (int t = tid; t < count; t += THREADS) {
+      int to, from;
+      if (in_smem) {
+        to = pair_to[t];
+        from = pair_from[t];
+      } else {
+        const int p = base + t;
+        int rf = 0, rs = 0;
+        while (p >= first_free[rf + 1]) ++rf;
+        while (p >= first_stay[rs + 1]) ++rs;
+        const int e1 = min((int64_t)n, (int64_t)(rs + 1) * per);   // end of that CTA's span
+        to = __ldcg(slots + (int64_t)rf * per + (p - first_free[rf]));
+        from = __ldcg(slots + e1 - 1 - (p - first_stay[rs]));
+      }
       const bool ok = in_bounds(to >= 0 && to < keep && from >= keep && from < n, j.dev_status);
-      pair_to[tid] = ok ? to : 0;
-      pair_from[tid] = ok ? from : 0;
-      score[pair_to[tid]] = score[pair_from[tid]];
-      if (idx) idx[pair_to[tid]] = pair_from[tid];
+      pair_to[t] = ok ? to : 0;
+      pair_from[t] = ok ? from : 0;
+      score[pair_to[t]] = score[pair_from[t]];
+      if (idx) idx[pair_to[t]] = pair_from[t];
       if constexpr (META > 0) {
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           uint8_t* meta = static_cast<uint8_t*>(j.meta[kv]) + bh * j.cap * META;
           if constexpr (META == 8)
-            reinterpret_cast<uint2*>(meta)[pair_to[tid]] = reinterpret_cast<const uint2*>(meta)[pair_from[tid]];
+            reinterpret_cast<uint2*>(meta)[pair_to[t]] = reinterpret_cast<const uint2*>(meta)[pair_from[t]];
           else
-            reinterpret_cast<uint32_t*>(meta)[pair_to[tid]] = reinterpret_cast<const uint32_t*>(meta)[pair_from[tid]];
+            reinterpret_cast<uint32_t*>(meta)[pair_to[t]] = reinterpret_cast<const uint32_t*>(meta)[pair_from[t]];
         }
       }
     }
     __syncthreads();
-    constexpr int kUnroll = 4;
+    constexpr int kUnroll = 8;
     const int items = count * 2 * kPieces;
-    for (int u0 = tid; u0 < items; u0 += kUnroll * kThreads) {
+    for (int u0 = tid; u0 < items; u0 += kUnroll * THREADS) {
       uint4 x[kUnroll];
 #pragma unroll
       for (int i = 0; i < kUnroll; ++i) {
-        const int u = u0 + i * kThreads;
+        const int u = u0 + i * THREADS;
         if (u < items) {
           const int p = u / (2 * kPieces), kv = (u / kPieces) & 1, c = u % kPieces;
           x[i] = static_cast<const uint4*>(j.rows[kv])[(bh * j.cap + pair_from[p]) * kPieces + c];
@@ -249,7 +320,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(EvictArgs args) {
       }
 #pragma unroll
       for (int i = 0; i < kUnroll; ++i) {
-        const int u = u0 + i * kThreads;
+        const int u = u0 + i * THREADS;
         if (u < items) {
           const int p = u / (2 * kPieces), kv = (u / kPieces) & 1, c = u % kPieces;
           static_cast<uint4*>(j.rows[kv])[(bh * j.cap + pair_to[p]) * kPieces + c] = x[i];
@@ -258,7 +329,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(EvictArgs args) {
     }
     __syncthreads();
   }
-  ptx::cluster_sync();   // every staying row has left its old place
+  sync_head();   // every staying row has left its old place
 
   // ---- the newest rows: slots n .. len - 1 come down to keep .. left - 1
   {
@@ -266,29 +337,29 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(EvictArgs args) {
     const int mine = (2 * kPieces - (int)rank + (int)csize - 1) / (int)csize;
     if (mine > 0) {
       constexpr int kUnroll = 4;
-      const int batch = kThreads / mine * kUnroll;   // rows at a time (2 * kPieces <= 64 < kThreads)
+      const int batch = THREADS / mine * kUnroll;   // rows at a time (2 * kPieces <= 64 < THREADS)
       const int lane_row = tid / mine, lane_col = (int)rank + (int)csize * (tid % mine);
       const int kv = lane_col / kPieces, c = lane_col % kPieces;
-      const bool active = lane_row < kThreads / mine;
+      const bool active = lane_row < THREADS / mine;
       uint4* rows = static_cast<uint4*>(j.rows[active ? kv : 0]) + bh * j.cap * kPieces + c;
       for (int base = 0; base < recent; base += batch) {
         uint4 x[kUnroll];
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-          const int r = base + lane_row + i * (kThreads / mine);
+          const int r = base + lane_row + i * (THREADS / mine);
           if (active && r < recent) x[i] = rows[(int64_t)(n + r) * kPieces];
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-          const int r = base + lane_row + i * (kThreads / mine);
+          const int r = base + lane_row + i * (THREADS / mine);
           if (active && r < recent) rows[(int64_t)(keep + r) * kPieces] = x[i];
         }
       }
     }
   }
   if (rank == csize - 1) {   // scores, (h, z) pairs and indices are small: one CTA
-    for (int base = 0; base < recent; base += kThreads) {
+    for (int base = 0; base < recent; base += THREADS) {
       const int r = base + tid;
       float x = 0.f;
       uint2 m[2] = {};
@@ -322,9 +393,32 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(EvictArgs args) {
       }
     }
     __syncthreads();
-    for (int s = left + tid; s < len; s += kThreads) score[s] = 0.f;
+    for (int s = left + tid; s < len; s += THREADS) score[s] = 0.f;
   }
-  ptx::cluster_sync();   // no CTA leaves while its counts may still be read
+  if (!alone) ptx::cluster_sync();   // no CTA leaves while its counts may still be read
+}
+
+template <int ROW, int META, int THREADS> cudaError_t launch_sized(const EvictJob& job, int64_t csize) {
+  const int64_t bh = (int64_t)job.batch * job.heads;
+  const int64_t key_bytes = (job.cap + csize - 1) / csize * 4;
+  EvictArgs a;
+  a.j = job;
+  a.keys_in_smem = key_bytes <= kKeysSmem;
+  const cudaError_t err = allow_dynamic_smem<evict_kernel<ROW, META, THREADS>>(kKeysSmem);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(bh * csize));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = a.keys_in_smem ? (size_t)key_bytes : 0;
+  cfg.stream = job.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)csize;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_kernel<ROW, META, THREADS>, a);
 }
 
 template <int ROW, int META> cudaError_t launch_typed(const EvictJob& job) {
@@ -335,25 +429,8 @@ template <int ROW, int META> cudaError_t launch_typed(const EvictJob& job) {
   if (csize > most) csize = most;
   if (csize > kMaxCluster) csize = kMaxCluster;
   if (csize < 1) csize = 1;
-  const int64_t key_bytes = (job.cap + csize - 1) / csize * 4;
-  EvictArgs a;
-  a.j = job;
-  a.keys_in_smem = key_bytes <= kKeysSmem;
-  const cudaError_t err = allow_dynamic_smem<evict_kernel<ROW, META>>(kKeysSmem);
-  if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(bh * csize));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = a.keys_in_smem ? (size_t)key_bytes : 0;
-  cfg.stream = job.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)csize;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_kernel<ROW, META>, a);
+  return (job.cap + csize - 1) / csize <= 4096 ? launch_sized<ROW, META, 256>(job, csize)
+                                               : launch_sized<ROW, META, 512>(job, csize);
 }
 
 }  // namespace

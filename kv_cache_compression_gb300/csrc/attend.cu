@@ -193,13 +193,13 @@ template <bool Q4, typename IO, int D> struct Shape {
   static constexpr int kNg = D / kQ4Group;
   static constexpr int kRow = Q4 ? D / 2 : D * (int)sizeof(IO);     // bytes of a row of K (and of V)
   static constexpr int kMeta = Q4 ? 4 * kNg : 0;
-  static constexpr int kTile = Q4 ? 32 : (kRow >= 256 ? 16 : 32);   // rows
+  static constexpr int kTile = Q4 ? 64 : (kRow >= 256 ? 16 : 32);   // rows
   static constexpr int kStage = 2 * kTile * (kRow + kMeta);         // 4 to 16 KB of K and V together
-  static constexpr int kStages = 3;
+  static constexpr int kStages = Q4 ? 2 : 3;
   static constexpr int kWarps = snapkv::kWarps;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kCtasPerSm = Q4 ? (kWide ? 2 : 3) : kRow >= 512 ? 1 : 2;   // what the ring leaves room for
+  static constexpr int kCtasPerSm = kRow >= 512 ? 1 : 2;   // what the ring leaves room for
   static constexpr int smem(int tile_q) { return kRing + kWarps * tile_q * D * 4; }
 };
 
@@ -338,14 +338,16 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
           }
         }
         if constexpr (Q4) {
-          static_assert(S::kTile == 32, "a row's pair per lane");
-          const uint8_t* msrc = (kv ? a.vm : a.km) + row0 * S::kMeta;
+          const uint8_t* msrc = (kv ? a.vm : a.km) + row0 * S::kMeta + lane * S::kMeta;
           uint8_t* mto = dst + 2 * (S::kTile * S::kRow) + kv * (S::kTile * S::kMeta) + lane * S::kMeta;
-          if constexpr (decltype(whole)::value) {
-            cp_async_small<S::kMeta>(mto, msrc + lane * S::kMeta, S::kMeta);
-          } else {
-            const bool in = lane < left;
-            cp_async_small<S::kMeta>(mto, msrc + (in ? lane * S::kMeta : 0), in ? S::kMeta : 0);
+#pragma unroll
+          for (int row = 0; row < S::kTile; row += 32) {
+            if constexpr (decltype(whole)::value) {
+              cp_async_small<S::kMeta>(mto + row * S::kMeta, msrc + row * S::kMeta, S::kMeta);
+            } else {
+              const bool in = lane + row < left;
+              cp_async_small<S::kMeta>(mto + row * S::kMeta, in ? msrc + row * S::kMeta : msrc - lane * S::kMeta, in ? S::kMeta : 0);
+            }
           }
         }
       }
@@ -797,10 +799,12 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
   cp_wait<0>();
 }
 
-// The second launch. Its work comes in items of one warp each: an output row whose head was cut (or is
-// empty), or kJoinRows rows of a head's scores. Where a head's parts lie follows from the schedule.
+// The second launch. The warps of its first blocks each join 32 channels of an output row whose head was
+// cut (or is empty); the other blocks each add the weights of kJoinRows rows to a head's scores. Where a head's
+// parts lie follows from the schedule. The kernel is all latency: loads are issued together and early,
+// and registers are kept to what lets four blocks share an SM.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 256;
+constexpr int kJoinRows = 2048;
 
 // A head's parts: the last segment of one CTA (its slot 1, unless the share starts with the head) and the
 // first of `more` others after it.
@@ -833,109 +837,130 @@ __device__ __forceinline__ void join(float& top, float& sum, float m, float l) {
 }
 
 template <typename IO, int D, int TILE>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(AttendArgs a) {
-  const int lane = threadIdx.x % 32;
+__global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs a, int out_blocks, int chunks) {
+  __shared__ float head_m[kQueryTile], head_r[kQueryTile];
+  const int tid = threadIdx.x, lane = tid % 32;
   const int per_seq = a.heads * a.passes;
-  const SeqScan scan = scan_sequences<TILE>(a);
-  const int64_t total = scan.total * per_seq;   // tiles
-  // tiles of the sequences before b (all lanes ask together)
-  auto tiles_before = [&](int b) {
+  const bool scores = (int)blockIdx.x >= out_blocks;
+  // This block's head, or this warp's output row and 32 of its channels.
+  constexpr int kSlices = D / 32;
+  const int64_t slice = (int64_t)blockIdx.x * (kJoinThreads / 32) + tid / 32;
+  const int block = (int)blockIdx.x - out_blocks;
+  const int64_t out_row = slice / kSlices;
+  if (!scores && out_row >= (int64_t)a.batch * a.heads * a.group) return;
+  const int bh = scores ? block / chunks : (int)(out_row / a.group);
+  const int b = bh / a.heads, h = bh - b * a.heads;
+  const int n = visible_rows(a, b), tiles = tiles_of<TILE>(a, b);
+  const int r0 = scores ? (block - bh * chunks) * kJoinRows : 0;
+  if (scores && r0 >= n) return;
+  int64_t total, f0;   // tiles in all, and before this head's first pass
+  {
+    const SeqScan scan = scan_sequences<TILE>(a);
+    total = scan.total * per_seq;
     int64_t upto = -1;
     if (b >= scan.b0 && b < scan.b1) {
       upto = scan.upto;
       for (int s = scan.b0; s < b; ++s) upto += tiles_of<TILE>(a, s);
     }
-    return __shfl_sync(0xffffffffu, upto, __ffs(__ballot_sync(0xffffffffu, upto >= 0)) - 1);
-  };
-  const int64_t out_rows = (int64_t)a.batch * a.heads * a.group;
-  const int chunks = a.score ? (int)((a.cap + kJoinRows - 1) / kJoinRows) : 0;
-  const int64_t items = out_rows + (int64_t)a.batch * a.heads * chunks;
-  const int64_t warps = (int64_t)gridDim.x * (kJoinThreads / 32);
+    const int owner = __ffs(__ballot_sync(0xffffffffu, upto >= 0)) - 1;
+    f0 = __shfl_sync(0xffffffffu, upto, owner) * per_seq + (int64_t)h * a.passes * tiles;
+  }
+  Parts parts = {};   // of the first pass, or of the output row's
+  {
+    const int pass = scores ? 0 : (int)(out_row - (int64_t)bh * a.group) / a.tile_q;
+    if (tiles > 0) parts = find_parts<D>(a, total, f0 + (int64_t)pass * tiles, tiles);
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int64_t item = (int64_t)blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32; item < items; item += warps) {
-    if (item < out_rows) {
-      const int64_t bh = item / a.group;
-      const int b = (int)(bh / a.heads), h = (int)(bh - (int64_t)b * a.heads), g = (int)(item - bh * a.group);
-      const int pass = g / a.tile_q, q = g - pass * a.tile_q;
-      const int tiles = tiles_of<TILE>(a, b);
-      constexpr int kPer = D / 32;
-      float x[kPer] = {};
-      float scale = 0.f;
-      if (tiles > 0) {
-        const Parts parts = find_parts<D>(a, total, tiles_before(b) * per_seq + (int64_t)(h * a.passes + pass) * tiles, tiles);
-        if (parts.more == 0) continue;   // finished in the first launch
-        const int at_m = a.tile_q * D + q, at_l = a.tile_q * (D + 1) + q;
-        float top = -INFINITY, sum = 0.f;
-        for (int i = lane; i <= parts.more; i += 32) join(top, sum, __ldcg(parts[i] + at_m), __ldcg(parts[i] + at_l));
-        const float all = warp_max(top);
-        sum = warp_sum(top == -INFINITY ? 0.f : sum * ex2(top - all));
-        scale = sum == 0.f ? 0.f : 1.0f / sum;   // a NaN stays one
-#pragma unroll 4
-        for (int i = 0; i <= parts.more; ++i) {
-          const float m = __ldcg(parts[i] + at_m);
-          const float f = m == -INFINITY ? 0.f : ex2(m - all);
+
+  if (!scores) {
+    const int g = (int)(out_row - (int64_t)bh * a.group), pass = g / a.tile_q, q = g - pass * a.tile_q;
+    const int c = (int)(slice % kSlices) * 32 + lane;
+    float x = 0.f, sum = 0.f;
+    if (tiles > 0) {
+      if (parts.more == 0) return;   // finished in the first launch
+      const int at_m = a.tile_q * D + q, at_l = a.tile_q * (D + 1) + q;
+      float top = -INFINITY;
+      for (int i0 = 0; i0 <= parts.more; i0 += 32) {   // a part per lane, and eight parts' channels at a time
+        const bool in = i0 + lane <= parts.more;
+        const float m = in ? __ldcg(parts[i0 + lane] + at_m) : -INFINITY, l = in ? __ldcg(parts[i0 + lane] + at_l) : 0.f;
+        const float next = fmaxf(top, warp_max(m));
+        if (next == -INFINITY) continue;
+        const float f = m == -INFINITY ? 0.f : ex2(m - next), old = top == -INFINITY ? 0.f : ex2(top - next);
+        top = next;
+        x *= old;
+        sum = fmaf(sum, old, warp_sum(l * f));
+        const int here = min(32, parts.more + 1 - i0);
+#pragma unroll 1
+        for (int i = 0; i < here; i += 8) {
+          float v[8];
 #pragma unroll
-          for (int e = 0; e < kPer; ++e) x[e] = fmaf(__ldcg(parts[i] + q * D + 32 * e + lane), f, x[e]);
+          for (int e = 0; e < 8; ++e) v[e] = i + e < here ? __ldcg(parts[i0 + i + e] + q * D + c) : 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x = fmaf(v[e], __shfl_sync(0xffffffffu, f, (i + e) & 31), x);
         }
       }
-      IO* out = static_cast<IO*>(a.out) + item * D;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) store1<IO>(out + 32 * e + lane, x[e] * scale);
-      continue;
     }
-    const int64_t bh = (item - out_rows) / chunks;
-    const int b = (int)(bh / a.heads), h = (int)(bh - (int64_t)b * a.heads);
-    const int n = visible_rows(a, b);
-    const int row = (int)(item - out_rows - bh * chunks) * kJoinRows + lane;   // + 32, 64, ...
-    if (row - lane >= n) continue;
-    const int tiles = tiles_of<TILE>(a, b);
-    const int64_t f0 = tiles_before(b) * per_seq + (int64_t)h * a.passes * tiles;
-    constexpr int kPer = kJoinRows / 32;
-    float w[kPer] = {};   // the summed weights
-    for (int pass = 0; pass < a.passes; ++pass) {
-      const int tile_q = min(a.tile_q, a.group - pass * a.tile_q);
-      const int64_t vh = bh * a.passes + pass;
-      const Parts parts = find_parts<D>(a, total, f0 + (int64_t)pass * tiles, tiles);
-      // four lanes a query
-      const int q = lane / 4;
-      float top = -INFINITY, sum = 0.f;
-      if (q < tile_q) {
-        if (parts.more == 0) {
-          top = __ldcg(a.stats + vh * 2 * a.tile_q + q);
-          sum = lane % 4 == 0 ? __ldcg(a.stats + (vh * 2 + 1) * a.tile_q + q) : 0.f;
-        } else {
-          for (int i = lane % 4; i <= parts.more; i += 4)
-            join(top, sum, __ldcg(parts[i] + a.tile_q * D + q), __ldcg(parts[i] + a.tile_q * (D + 1) + q));
-        }
-      }
+    store1<IO>(static_cast<IO*>(a.out) + out_row * D + c, sum == 0.f ? 0.f : x / sum);   // (a NaN stays one)
+    return;
+  }
+
+  constexpr int kPer = kJoinRows / kJoinThreads;
+  const int row = r0 + tid;   // + kJoinThreads, ...
+  float* sc = a.score + (int64_t)bh * a.cap + row;
+  float w[kPer];
 #pragma unroll
-      for (int off = 1; off < 4; off <<= 1) {
-        const float m = __shfl_xor_sync(0xffffffffu, top, off), l = __shfl_xor_sync(0xffffffffu, sum, off);
-        join(top, sum, m, l);
-      }
-      const float scale = sum == 0.f ? 0.f : 1.0f / sum;
-      const float shift = top == -INFINITY ? 0.f : top;
-      const float* logits = a.logits + vh * a.tile_q * a.logit_stride + row;
-      for (int qq = 0; qq < tile_q; ++qq, logits += a.logit_stride) {
-        const float m = __shfl_sync(0xffffffffu, shift, 4 * qq), r = __shfl_sync(0xffffffffu, scale, 4 * qq);
-        float x[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) x[i] = row + 32 * i < n ? __ldcg(logits + 32 * i) : 0.f;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) w[i] = fmaf(ex2(x[i] - m), r, w[i]);
-      }
-    }
-    float* sc = a.score + bh * a.cap + row;
-    float old[kPer] = {};
-    if (a.decay != 0.f) {
+  for (int i = 0; i < kPer; ++i) w[i] = a.decay != 0.f && row + i * kJoinThreads < n ? a.decay * sc[i * kJoinThreads] : 0.f;
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int tile_q = min(a.tile_q, a.group - pass * a.tile_q);
+    const int64_t vh = (int64_t)bh * a.passes + pass;
+    const float* logits = a.logits + vh * a.tile_q * a.logit_stride + row;
+    auto load = [&](int q, float (&x)[kPer]) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (row + 32 * i < n) old[i] = sc[32 * i];
-    }
+        x[i] = row + i * kJoinThreads < n ? __ldcg(logits + q * a.logit_stride + i * kJoinThreads) : -INFINITY;
+    };
+    constexpr int kAtOnce = 2;
+    float x[kAtOnce][kPer];   // some queries' logits are under way while the maxima are found
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (row + 32 * i < n) sc[32 * i] = fmaf(a.decay, old[i], w[i]);
+    for (int q = 0; q < kAtOnce; ++q)
+      if (q < tile_q) load(q, x[q]);
+    const int q = tid / 32;   // a warp per query
+    if (q < tile_q) {
+      float top = -INFINITY, sum = 0.f;
+      if (pass > 0) parts = find_parts<D>(a, total, f0 + (int64_t)pass * tiles, tiles);
+      if (parts.more == 0) {
+        top = __ldcg(a.stats + vh * 2 * a.tile_q + q);
+        sum = __ldcg(a.stats + (vh * 2 + 1) * a.tile_q + q);
+      } else {
+        for (int i = lane; i <= parts.more; i += 32) {
+          const float* p = parts[i] + a.tile_q * D + q;
+          join(top, sum, __ldcg(p), __ldcg(p + a.tile_q));
+        }
+        const float all = warp_max(top);
+        sum = warp_sum(top == -INFINITY ? 0.f : sum * ex2(top - all));
+        top = all;
+      }
+      if (lane == 0) {
+        head_m[q] = top == -INFINITY ? 0.f : top;
+        head_r[q] = sum == 0.f ? 0.f : 1.0f / sum;
+      }
+    }
+    __syncthreads();
+    for (int q0 = 0; q0 < tile_q; q0 += kAtOnce) {
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e)
+        if (q0 + e < tile_q) {
+          const float m = head_m[q0 + e], r = head_r[q0 + e];
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) w[i] = fmaf(ex2(x[e][i] - m), r, w[i]);
+          if (q0 + e + kAtOnce < tile_q) load(q0 + e + kAtOnce, x[e]);
+        }
+    }
+    if (pass + 1 < a.passes) __syncthreads();   // the maxima have been used
   }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (row + i * kJoinThreads < n) sc[i * kJoinThreads] = w[i];
 }
 
 template <bool Q4, typename IO, int D, bool FOUR>
@@ -989,10 +1014,12 @@ cudaError_t launch_typed(const AttendJob& job) {
   attend_kernel<Q4, IO, D, FOUR><<<(unsigned)ctas, S::kThreads, smem, job.stream>>>(a);
   err = cudaGetLastError();
   if (err != cudaSuccess || a.direct) return err;
-  const int64_t items = (int64_t)job.batch * job.q_heads +
-                        (job.score ? (int64_t)job.batch * job.heads * ((job.cap + kJoinRows - 1) / kJoinRows) : 0);
-  int64_t blocks = (items + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
-  if (blocks > (int64_t)device_sm_count() * 8) blocks = (int64_t)device_sm_count() * 8;
+  const int64_t chunks = job.score ? (job.cap + kJoinRows - 1) / kJoinRows : 0;
+  const int64_t score_blocks = (int64_t)job.batch * job.heads * chunks;
+  const int64_t slices = (int64_t)job.batch * job.q_heads * (D / 32);
+  const int64_t out_blocks = (slices + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+  const int64_t blocks = out_blocks + score_blocks;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kJoinThreads);
@@ -1002,7 +1029,7 @@ cudaError_t launch_typed(const AttendJob& job) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_join_kernel<IO, D, S::kTile>, a);
+  return cudaLaunchKernelEx(&cfg, attend_join_kernel<IO, D, S::kTile>, a, (int)out_blocks, (int)chunks);
 }
 
 template <bool Q4, int D> cudaError_t launch_dim(const AttendJob& job) {

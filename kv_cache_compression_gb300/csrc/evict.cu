@@ -3,8 +3,7 @@
 // A CTA per (sequence, head), or a thread-block cluster for long caches of few heads. The candidates'
 // scores (slots below n = len - recent) become 32-bit keys whose unsigned order is the scores' order;
 // each CTA keeps its span's keys in shared memory where they fit. A radix select (four 8-bit digits,
-// histograms in four copies against atomics meeting at one bin, added up through distributed shared
-// memory in a cluster) finds the key of rank `keep`; ties at it go to the lower slots. A scan in slot
+// histograms added up through distributed shared memory in a cluster) finds the key of rank `keep`; ties at it go to the lower slots. A scan in slot
 // order then lists the freed slots below `keep` and the staying rows above it, and the i-th of the one
 // takes the i-th of the other.
 //
@@ -26,9 +25,8 @@ namespace {
 
 constexpr int kMaxCluster = 8;
 constexpr int kKeysSmem = 64 * 1024;   // a span's keys stay in shared memory up to this size
-constexpr int kMaxIndex = 256;         // pairs resolved at a time
-constexpr int kCopies = 4;             // of a histogram
-constexpr int kRun = 16;               // keys a thread looks at between two scans, at most
+constexpr int kMaxIndex = 1024;        // pairs resolved at a time
+constexpr int kRun = 15;               // keys a thread looks at between two scans, at most (odd: no bank conflicts)
 
 struct EvictArgs {
   EvictJob j;
@@ -71,7 +69,7 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(EvictArgs args) {
   constexpr int kPieces = ROW / 16;       // 16-byte pieces of a row of K (and of V)
   constexpr int kWarps = THREADS / 32;
   extern __shared__ uint32_t key_smem[];
-  __shared__ uint32_t hist[4][kCopies][256];   // a digit's histogram; copy 0 is read by the whole cluster
+  __shared__ __align__(16) uint32_t hist[4][256];       // one per digit, read by the whole cluster
   __shared__ __align__(16) uint32_t all[256];
   __shared__ int counts[3];               // ties, freed slots, staying rows of this CTA's span
   __shared__ int sums_a[kWarps], sums_b[kWarps];
@@ -112,15 +110,14 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(EvictArgs args) {
 
   // The keys arrive while the histograms are cleared; the first digit is counted from them on the way.
   if (tid < 3) counts[tid] = 0;
-  for (int i = tid; i < 4 * kCopies * 256; i += THREADS) (&hist[0][0][0])[i] = 0;
+  for (int i = tid; i < 4 * 256; i += THREADS) (&hist[0][0])[i] = 0;
   __syncthreads();
   auto key_of = [&](int s) { return args.keys_in_smem ? key_smem[s - s0] : order_key(score[s]); };
-  const int copy = tid / 32 % kCopies;
-#pragma unroll 4
+#pragma unroll 8
   for (int s = s0 + tid; s < s1; s += THREADS) {
     const uint32_t key = order_key(score[s]);
     if (args.keys_in_smem) key_smem[s - s0] = key;
-    atomicAdd(&hist[3][copy][key >> 24], 1u);
+    atomicAdd(&hist[3][key >> 24], 1u);
   }
 
   // ---- the key of rank `keep` from the top, digit by digit; `want` of the keys that share the digits
@@ -131,28 +128,23 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(EvictArgs args) {
     if (d < 3)
       for (int s = s0 + tid; s < s1; s += THREADS) {
         const uint32_t key = key_of(s);
-        if (key >> (shift + 8) == prefix) atomicAdd(&hist[d][copy][(key >> shift) & 255u], 1u);
+        if (key >> (shift + 8) == prefix) atomicAdd(&hist[d][(key >> shift) & 255u], 1u);
       }
-    __syncthreads();
-    for (int i = tid; i < 256; i += THREADS) {
-      uint32_t x = hist[d][0][i];
-#pragma unroll
-      for (int c = 1; c < kCopies; ++c) x += hist[d][c][i];
-      (alone ? all : hist[d][0])[i] = x;
-    }
+    sync_head();
+    const uint32_t* sum = hist[d];
     if (!alone) {
-      ptx::cluster_sync();
       for (int i = tid; i < 256; i += THREADS) {
         uint32_t x = 0;
-        for (uint32_t r = 0; r < csize; ++r) x += ptx::dsmem_ld_u32(ptx::map_rank(&hist[d][0][i], r));
+        for (uint32_t r = 0; r < csize; ++r) x += ptx::dsmem_ld_u32(ptx::map_rank(&hist[d][i], r));
         all[i] = x;
       }
+      __syncthreads();
+      sum = all;
     }
-    __syncthreads();
     // Every warp finds the digit for itself, eight bins a lane from the top.
     uint32_t bins[8], mine = 0;
     {
-      const uint4 hi = *reinterpret_cast<const uint4*>(&all[252 - 8 * lane]), lo = *reinterpret_cast<const uint4*>(&all[248 - 8 * lane]);
+      const uint4 hi = *reinterpret_cast<const uint4*>(&sum[252 - 8 * lane]), lo = *reinterpret_cast<const uint4*>(&sum[248 - 8 * lane]);
       bins[0] = hi.w; bins[1] = hi.z; bins[2] = hi.y; bins[3] = hi.x;
       bins[4] = lo.w; bins[5] = lo.z; bins[6] = lo.y; bins[7] = lo.x;
     }
@@ -196,7 +188,9 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(EvictArgs args) {
   // ---- in slot order: freed slots below `keep` are listed from the front, staying rows at or above it
   // from the back of the span's part of `slots` (or, few pairs of one CTA, in shared memory).
   const bool in_smem = alone && min(keep, n - keep) <= kMaxIndex;
-  const int run = min(kRun, (s1 - s0 + THREADS - 1) / THREADS);   // neighbouring slots of a thread
+  if (idx)   // slots that keep their row; the pairs below overwrite the others
+    for (int s = s0 + tid; s < min(s1, keep); s += THREADS) idx[s] = s;
+  const int run = min(kRun, (s1 - s0 + THREADS - 1) / THREADS | 1);   // neighbouring slots of a thread
   int n_free = 0, n_stay = 0;
   for (int base = s0; base < s1; base += run * THREADS) {
     const int t0 = min((int64_t)s1, (int64_t)base + tid * run), t1 = min((int64_t)s1, (int64_t)t0 + run);
@@ -236,8 +230,6 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(EvictArgs args) {
         else
           slots[s1 - 1 - p] = s;
         at += 1 << 16;
-      } else if (idx && stay) {
-        idx[s] = s;
       }
     }
     n_free += total & 0xFFFF;
@@ -306,7 +298,7 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(EvictArgs args) {
       }
     }
     __syncthreads();
-    constexpr int kUnroll = 8;
+    constexpr int kUnroll = 4;
     const int items = count * 2 * kPieces;
     for (int u0 = tid; u0 < items; u0 += kUnroll * THREADS) {
       uint4 x[kUnroll];

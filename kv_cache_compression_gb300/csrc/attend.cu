@@ -221,6 +221,33 @@ template <int NG> __device__ __forceinline__ uint2 load_words(const uint8_t* at)
 // rows 2 i and 2 i + 1 of the four lanes that read together lie in different banks.
 template <bool MIXED> __device__ __forceinline__ int row_of(int j) { return MIXED ? (j >> 1) + 4 * (j & 1) : j; }
 
+// Counts this warp in, after what all its lanes wrote to shared memory; returns how many came before (and
+// what those wrote can then be read).
+__device__ __forceinline__ int arrive(int* count) {
+  __syncwarp();
+  int before = 0;
+  if (threadIdx.x % 32 == 0)
+    asm volatile("atom.acq_rel.cta.shared::cta.add.s32 %0, [%1], 1;" : "=r"(before) : "r"(ptx::smem_u32(count)) : "memory");
+  before = __shfl_sync(0xffffffffu, before, 0);
+  __syncwarp();
+  return before;
+}
+
+__device__ __forceinline__ void publish(int* value, int x) {
+  asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(ptx::smem_u32(value)), "r"(x) : "memory");
+}
+
+// Waits (about two seconds at most; false then) until *value >= x was published.
+__device__ __forceinline__ bool wait_for(int* value, int x) {
+  int seen;
+  const long long t0 = clock64();
+  do {
+    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(seen) : "r"(ptx::smem_u32(value)) : "memory");
+  } while (seen < x && clock64() - t0 < 4000000000LL);
+  __syncwarp();
+  return seen >= x;
+}
+
 // FOUR (bf16, at most four queries a pass): the second product's columns 4 .. 7 are the second parts of
 // the weights in columns 0 .. 3, and one instruction does for both. The first product then has every
 // query twice.
@@ -236,6 +263,7 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float warp_m[S::kWarps][kQueryTile], warp_l[S::kWarps][kQueryTile];
   __shared__ float head_m[kQueryTile], head_r[kQueryTile];
+  __shared__ int arrived, merged;   // warps whose part of this head is in `meet`; heads merged
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -247,6 +275,8 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
   const int jrow = row_of<Q4 || S::kWide>(j);         // row j of an 8-row tile, as it lies in the cache
   const int per_seq = a.heads * a.passes;   // heads of a sequence
   const Q4Ones ones = a.ones;
+  if (tid == 0) arrived = merged = 0;
+  __syncthreads();
 
   // ---- this CTA's share of the tiles, and the sequence it starts in (every warp finds them for itself)
   int64_t at, end, before;
@@ -289,6 +319,10 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
   // A place in the list: a tile of a head, and what its addresses need.
   struct Place {
     int seq, head, rows, tiles, tile;   // head: within the sequence, over passes
+    int64_t row0;                       // the KV head's first row in the cache
+  };
+  auto first_row = [&](const Place& p) {
+    return ((int64_t)p.seq * a.heads + (a.passes == 1 ? p.head : p.head / a.passes)) * a.cap;
   };
   Place here;
   here.seq = first_seq;
@@ -298,6 +332,7 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
     const int64_t in_seq = at - before * per_seq;
     here.head = in_seq < ((int64_t)1 << 32) ? (int)((uint32_t)in_seq / (uint32_t)here.tiles) : (int)(in_seq / here.tiles);
     here.tile = (int)(in_seq - (int64_t)here.head * here.tiles);
+    here.row0 = first_row(here);
   }
   // Moves p, whose tile may have run past its head, to the head that holds it (which exists).
   auto settle = [&](Place& p) {
@@ -310,6 +345,7 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
           p.tiles = (p.rows + S::kTile - 1) / S::kTile;
         } while (p.tiles == 0);
       }
+      p.row0 = first_row(p);
     }
   };
 
@@ -320,7 +356,7 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
   auto fetch = [&](const Place& p, int slot) {
     constexpr int kPieces = S::kRow / 16, kAll = S::kTile * kPieces;
     uint8_t* dst = ring + slot * S::kStage;
-    const int64_t row0 = ((int64_t)p.seq * a.heads + p.head / a.passes) * a.cap + (int64_t)p.tile * S::kTile;
+    const int64_t row0 = p.row0 + (int64_t)p.tile * S::kTile;
     const int left = p.rows - p.tile * S::kTile;   // > 0
     auto copy = [&](auto whole) {   // whole tiles, all but a head's last, need no look at each row
 #pragma unroll
@@ -342,6 +378,7 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
           uint8_t* mto = dst + 2 * (S::kTile * S::kRow) + kv * (S::kTile * S::kMeta) + lane * S::kMeta;
 #pragma unroll
           for (int row = 0; row < S::kTile; row += 32) {
+            if (row + 32 > S::kTile && lane >= S::kTile - row) continue;
             if constexpr (decltype(whole)::value) {
               cp_async_small<S::kMeta>(mto + row * S::kMeta, msrc + row * S::kMeta, S::kMeta);
             } else {
@@ -377,10 +414,10 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
   int64_t mine_at = at + warp;            // this warp's next tile
   const int64_t share0 = at;
 
-  while (at < end) {   // one head, or the part of it that lies in the share
-    const int pass = here.head % a.passes;
+  for (int segment = 0; at < end; ++segment) {   // one head, or the part of it that lies in the share
+    const int pass = a.passes == 1 ? 0 : here.head % a.passes;
     const int tile_q = min(a.tile_q, a.group - pass * a.tile_q);
-    const int64_t bh = (int64_t)here.seq * a.heads + here.head / a.passes;
+    const int64_t bh = (int64_t)here.seq * a.heads + (a.passes == 1 ? here.head : here.head / a.passes);
     const int64_t vh = (int64_t)here.seq * per_seq + here.head;
     const int64_t q0 = bh * a.group + (int64_t)pass * a.tile_q;
     const int64_t seg_end = min(end, at + (here.tiles - here.tile));
@@ -706,7 +743,8 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
       }
     }
 
-    // ---- the warps meet
+    // ---- the warps meet: each leaves its part, the last to arrive merges them, and the others go on with the
+    // next head (at whose end they wait, in case, until this one is merged)
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
@@ -723,7 +761,7 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[t][e] += __shfl_xor_sync(0xffffffffu, o[t][e], 2);
     }
-    __syncthreads();   // every warp has left the last meeting
+    if (!wait_for(&merged, segment) && lane == 0) report(a.dev_status, SNAPKV_ERR_TIMEOUT);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int qq = qa + e;
@@ -750,36 +788,47 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
         }
       }
     }
-    __syncthreads();
-    const bool whole = here.tile == 0 && seg_end == at + here.tiles;   // the head lies in this share
-    float* part = a.parts + ((int64_t)blockIdx.x * 2 + (at > share0 ? 1 : 0)) * a.tile_q * (D + 2);
-    for (int u = tid; u < tile_q * D; u += S::kThreads) {
-      const int qq = u / D, c = u % D;
-      float top = -INFINITY;
+    const bool last = arrive(&arrived) == S::kWarps - 1;
+    if (last) {
+      const bool whole = here.tile == 0 && seg_end == at + here.tiles;   // the head lies in this share
+      float* part = a.parts + ((int64_t)blockIdx.x * 2 + (at > share0 ? 1 : 0)) * a.tile_q * (D + 2);
+      for (int qq = 0; qq < tile_q; ++qq) {
+        float top = -INFINITY, sum = 0.f, f[S::kWarps];
 #pragma unroll
-      for (int w = 0; w < S::kWarps; ++w) top = fmaxf(top, warp_m[w][qq]);
-      float x = 0.f, sum = 0.f;
+        for (int w = 0; w < S::kWarps; ++w) top = fmaxf(top, warp_m[w][qq]);
 #pragma unroll
-      for (int w = 0; w < S::kWarps; ++w) {
-        const float f = warp_m[w][qq] == -INFINITY ? 0.f : ex2(warp_m[w][qq] - top);
-        x = fmaf(meet[(w * a.tile_q + qq) * D + c], f, x);
-        sum = fmaf(warp_l[w][qq], f, sum);
+        for (int w = 0; w < S::kWarps; ++w) {
+          f[w] = warp_m[w][qq] == -INFINITY ? 0.f : ex2(warp_m[w][qq] - top);
+          sum = fmaf(warp_l[w][qq], f[w], sum);
+        }
+        const float scale = sum == 0.f ? 0.f : 1.0f / sum;   // a NaN stays one
+#pragma unroll
+        for (int c = lane; c < D; c += 32) {
+          float x = 0.f;
+#pragma unroll
+          for (int w = 0; w < S::kWarps; ++w) x = fmaf(meet[(w * a.tile_q + qq) * D + c], f[w], x);
+          if (whole)
+            store1<IO>(static_cast<IO*>(a.out) + (q0 + qq) * D + c, x * scale);
+          else
+            part[qq * D + c] = x;
+        }
+        if (lane == 0) {
+          if (!whole) {
+            part[a.tile_q * D + qq] = top;
+            part[a.tile_q * (D + 1) + qq] = sum;
+          } else if (a.direct) {
+            head_m[qq] = top == -INFINITY ? 0.f : top;
+            head_r[qq] = scale;
+          } else if (a.score) {
+            a.stats[vh * 2 * a.tile_q + qq] = top;
+            a.stats[(vh * 2 + 1) * a.tile_q + qq] = sum;
+          }
+        }
       }
-      if (whole) {
-        store1<IO>(static_cast<IO*>(a.out) + q0 * D + u, sum == 0.f ? 0.f : x / sum);
-        if (c == 0 && a.direct) {
-          head_m[qq] = top == -INFINITY ? 0.f : top;
-          head_r[qq] = sum == 0.f ? 0.f : 1.0f / sum;
-        } else if (c == 0 && a.score) {
-          a.stats[vh * 2 * a.tile_q + qq] = top;
-          a.stats[(vh * 2 + 1) * a.tile_q + qq] = sum;
-        }
-      } else {
-        part[u] = x;
-        if (c == 0) {
-          part[a.tile_q * D + qq] = top;
-          part[a.tile_q * (D + 1) + qq] = sum;
-        }
+      __syncwarp();
+      if (lane == 0) {
+        arrived = 0;
+        publish(&merged, segment + 1);
       }
     }
     if (a.direct && a.score) {   // (one pass: the launcher saw to it)

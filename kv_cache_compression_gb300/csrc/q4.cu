@@ -1,8 +1,9 @@
 // Rows into and out of a cache held in 4 bits (the format of include/snapkv_cache.h).
 //
-// One thread holds eight channels of a row, eight neighbouring threads a group of 64: the group's
-// largest and smallest value are three shuffles away, and a thread's eight levels are one word of
-// the row. Both kernels read and write every byte once and are bound by HBM.
+// One thread holds sixteen channels of a row, four neighbouring threads a group of 64: the group's
+// largest and smallest value are two shuffles away, and a thread's levels are two words of the row.
+// Both kernels read and write every byte once. Writing 16-bit rows costs 2.6 bytes of HBM traffic per
+// value against about half a warp instruction per lane: the instructions are counted, not only the bytes.
 #include "cache_internal.h"
 #include "q4.cuh"
 #include "snapkv_internal.h"
@@ -11,6 +12,7 @@ namespace snapkv {
 namespace {
 
 constexpr int kQ4Threads = 256;
+constexpr int kQ4Each = 16;   // channels of a thread
 
 // max.NaN / min.NaN: a NaN in the group must reach its scale.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -24,13 +26,33 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return r;
 }
 
-template <typename T> __device__ __forceinline__ void load8(const T* p, float* x);
-template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* x) {
-  Elem<__nv_bfloat16>::widen(ld_stream_v4(p), x);
+// Sixteen values, and the largest and smallest of them.
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float* x, float* hi, float* lo) {
+  const uint4 a = ld_stream_v4(p), b = ld_stream_v4(p + 8);
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t top = w[0], low = w[0];   // two at a time
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(w[i]));
+    asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(low) : "r"(w[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+  *hi = max_nan(__uint_as_float(top << 16), __uint_as_float(top & 0xFFFF0000u));
+  *lo = min_nan(__uint_as_float(low << 16), __uint_as_float(low & 0xFFFF0000u));
 }
-template <> __device__ __forceinline__ void load8<float>(const float* p, float* x) {
-  Elem<float>::widen(ld_stream_v4(p), x);
-  Elem<float>::widen(ld_stream_v4(p + 4), x + 4);
+__device__ __forceinline__ void load16(const float* p, float* x, float* hi, float* lo) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) Elem<float>::widen(ld_stream_v4(p + 4 * i), x + 4 * i);
+  *hi = *lo = x[0];
+#pragma unroll
+  for (int e = 1; e < 16; ++e) {
+    *hi = max_nan(*hi, x[e]);
+    *lo = min_nan(*lo, x[e]);
+  }
 }
 
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
@@ -81,14 +103,15 @@ template <bool kExact, bool kClamp> __device__ __forceinline__ uint32_t levels(c
     side[e] = s.x;
     side[e + 1] = s.y;
   }
-  // k + 8, less one below the border, or on it if that is odd: (bits of s) - (k & 1) is negative just then.
+  // k + 8, less one below the border, or on it if that is odd: as a whole number, the bits of s are then less
+  // than k & 1.
   constexpr int kOrder[8] = {5, 7, 1, 3, 4, 6, 0, 2};   // from the top nibble down
   uint32_t u = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t k = __float_as_uint(whole[kOrder[i]]);
-    const int below = (__float_as_int(side[kOrder[i]]) - (int)(k & 1u)) >> 31;
-    u = u * 16u + k + (uint32_t)below;
+    u = u * 16u + k;
+    if (__float_as_int(side[kOrder[i]]) < (int)(k & 1u)) --u;
   }
   // each k came with the bits of 1.5 * 2^23, and 8 is still missing: whole nibbles again, mod 2^32
   constexpr uint32_t kBits = 0x4B400000u;
@@ -96,55 +119,57 @@ template <bool kExact, bool kClamp> __device__ __forceinline__ uint32_t levels(c
   return u - kAll + 0x88888888u;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(Q4Job a) {
-  constexpr int kTpr = D / 8;               // threads per row
-  constexpr int kNg = D / kQ4Group;
-  const int64_t bh = blockIdx.y;
-  const int b = (int)(bh / a.heads);
-  const int which = blockIdx.z;             // K or V
-  int64_t n = a.rows;
-  const int len = a.len[b];
-  bool fits = len >= 0;
-  if (a.n_new) {
-    n = a.n_new[b];
-    if (n < 0 || n > a.rows) {
-      if (blockIdx.x == 0 && which == 0 && bh % a.heads == 0 && threadIdx.x == 0)
-        report(a.dev_status, SNAPKV_ERR_INVALID_ARG);
-      fits = false;
-      n = 0;
+// The rows of a launch. Long calls have a head per blockIdx.y, whose blocks take turns; calls of few rows
+// are one list over all heads, as a head's rows would leave most of a block idle.
+struct Q4Grid {
+  bool flat;
+  unsigned flat_rows;   // of all heads
+};
+
+// Calls f(bh, row, mine) for this thread's rows, the whole warp at once (row and bh are those of row 0 of
+// head 0 where mine is false).
+template <int TPR, typename F> __device__ __forceinline__ void for_rows(const Q4Grid& grid, int64_t rows, F f) {
+  constexpr int kRows = kQ4Threads / TPR;
+  if (grid.flat) {
+    const unsigned at = blockIdx.x * kRows + threadIdx.x / TPR;
+    const bool mine = at < grid.flat_rows;
+    const unsigned bh = mine ? at / (unsigned)rows : 0u;
+    f((int64_t)bh, (int64_t)(mine ? at - bh * (unsigned)rows : 0u), mine);
+  } else {
+    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < rows; r0 += (int64_t)gridDim.x * kRows) {
+      const int64_t row = r0 + threadIdx.x / TPR;
+      f((int64_t)blockIdx.y, row < rows ? row : 0, row < rows);
     }
   }
-  if (!fits || (int64_t)len + n > a.cap) {
-    if (len < 0 || (int64_t)len + n > a.cap)
-      if (blockIdx.x == 0 && which == 0 && bh % a.heads == 0 && threadIdx.x == 0)
-        report(a.dev_status, SNAPKV_ERR_CAPACITY);
-    n = 0;
-  }
-  if (blockIdx.x == 0 && which == 0 && bh % a.heads == 0 && threadIdx.x == 0) a.len_out[b] = (int)(len + n);
-  const T* in = static_cast<const T*>(which ? a.in[1] : a.in[0]) + bh * a.rows * D;
-  uint32_t* codes = static_cast<uint32_t*>(which ? a.codes[1] : a.codes[0]) + (bh * a.cap + len) * (D / 8);
-  uint32_t* meta = static_cast<uint32_t*>(which ? a.meta[1] : a.meta[0]) + (bh * a.cap + len) * kNg;
-  const int c = threadIdx.x % kTpr, g = c / 8, o = c % 8;   // group, and which eight of its channels
-  // Every lane of a warp takes the same number of turns (the shuffles below need them all).
-  for (int64_t r0 = (int64_t)blockIdx.x * (kQ4Threads / kTpr); r0 < n; r0 += (int64_t)gridDim.x * (kQ4Threads / kTpr)) {
-    const int64_t row = r0 + threadIdx.x / kTpr;
-    const bool mine = row < n;
-    float x[8];
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(Q4Job a, Q4Grid grid) {
+  constexpr int kTpr = D / kQ4Each;         // threads per row
+  constexpr int kNg = D / kQ4Group;
+  const int which = blockIdx.z;             // K or V
+  const int c = threadIdx.x % kTpr, g = c / 4, o = 2 * (c % 4);   // group, and the first of its eights
+  for_rows<kTpr>(grid, a.rows, [&](int64_t bh, int64_t row, bool mine) {
+    const int b = (int)(bh / a.heads);
+    const int len = a.len[b];
+    const int64_t n = a.n_new ? a.n_new[b] : a.rows;
+    const bool counts = n >= 0 && n <= a.rows, fits = len >= 0 && counts && len + n <= a.cap;
+    if (mine && row == 0 && c == 0 && which == 0 && bh - (int64_t)b * a.heads == 0) {   // once per sequence
+      a.len_out[b] = fits ? (int)(len + n) : len;
+      if (!counts) report(a.dev_status, SNAPKV_ERR_INVALID_ARG);
+      if (len < 0 || (counts && len + n > a.cap)) report(a.dev_status, SNAPKV_ERR_CAPACITY);
+    }
+    mine = mine && fits && row < n;
+    if (!__any_sync(0xffffffffu, mine)) return;
+    float x[kQ4Each], hi = 0.f, lo = 0.f;
     if (mine) {
-      load8<T>(in + row * D + 8 * c, x);
+      load16(static_cast<const T*>(which ? a.in[1] : a.in[0]) + (bh * a.rows + row) * D + kQ4Each * c, x, &hi, &lo);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    }
-    float hi = x[0], lo = x[0];
-#pragma unroll
-    for (int e = 1; e < 8; ++e) {
-      hi = max_nan(hi, x[e]);
-      lo = min_nan(lo, x[e]);
+      for (int e = 0; e < kQ4Each; ++e) x[e] = 0.f;
     }
 #pragma unroll
-    for (int off = 1; off < 8; off <<= 1) {
+    for (int off = 1; off < 4; off <<= 1) {
       hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
       lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
     }
@@ -154,98 +179,114 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(Q4Job a) {
     const float err = (hi - (diff + back)) + (back - lo);
     float q = diff * (1.0f / 30.0f);
     q = fmaf(fmaf(-q, 30.0f, diff) + err, 1.0f / 30.0f, q);
-    __nv_bfloat16 hb = __float2bfloat16_rn(q), zb = __float2bfloat16_rn(0.5f * (hi + lo));
-    float h = __bfloat162float(hb), z = __bfloat162float(zb);
+    float h = __bfloat162float(__float2bfloat16_rn(q)), z = __bfloat162float(__float2bfloat16_rn(0.5f * (hi + lo)));
     if (h < 0x1p-126f) h = 0.f;
-    uint32_t u = 0x88888888u;
+    uint32_t u[2] = {0x88888888u, 0x88888888u};
     if (!(h < INFINITY) || !(fabsf(z) < INFINITY)) {
       h = z = __uint_as_float(0x7FC00000u);
     } else if (h > 0.f) {
       const float r = __fdividef(1.0f, 2.0f * h);
       constexpr bool kExact = sizeof(T) == 4;
-      u = fmaxf(hi - z, z - lo) < 15.9f * h ? levels<kExact, false>(x, h, z, r) : levels<kExact, true>(x, h, z, r);
+      const bool near = fmaxf(hi - z, z - lo) < 15.9f * h;
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        u[w] = near ? levels<kExact, false>(x + 8 * w, h, z, r) : levels<kExact, true>(x + 8 * w, h, z, r);
     }
-    if (mine) {
-      codes[row * (D / 8) + q4_word<kNg>(g, o)] = q4_pack(u);
-      if (o == 0) meta[row * kNg + g] = (__float_as_uint(h) >> 16) | (__float_as_uint(z) & 0xFFFF0000u);
+    if (mine && in_bounds(len + row < a.cap, a.dev_status)) {
+      const int64_t at = bh * a.cap + len + row;
+      uint32_t* codes = static_cast<uint32_t*>(which ? a.codes[1] : a.codes[0]) + at * (D / 8);
+      codes[q4_word<kNg>(g, o)] = q4_pack(u[0]);
+      codes[q4_word<kNg>(g, o + 1)] = q4_pack(u[1]);
+      if (o == 0)
+        static_cast<uint32_t*>(which ? a.meta[1] : a.meta[0])[at * kNg + g] =
+            (__float_as_uint(h) >> 16) | (__float_as_uint(z) & 0xFFFF0000u);
     }
+  });
+}
+
+// The values of a word's eight channels: its operands (levels in units of 2^-131 and 2^-133) as fp32.
+__device__ __forceinline__ void q4_values(const Q4Ones& one, uint32_t w, float h, float z, float* x) {
+  uint32_t e[4];
+  q4_operands(one, w, prmt(w, w, 0x2301), e);
+  const float2 up = make_float2(0x1p127f, 0x1p127f), zz = make_float2(z, z);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float s = j & 1 ? h * 64.0f : h * 16.0f;
+    // h t is exact in fp32, so that the value is rounded once
+    const float2 t = mul2(make_float2(__uint_as_float(e[j] << 16), __uint_as_float(e[j] & 0xFFFF0000u)), up);
+    const float2 v = fma2(t, make_float2(s, s), zz);
+    x[2 * j] = v.x;
+    x[2 * j + 1] = v.y;
   }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(Q4Job a) {
-  constexpr int kTpr = D / 8;
+__global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(Q4Job a, Q4Grid grid, Q4Ones one) {
+  constexpr int kTpr = D / kQ4Each;
   constexpr int kNg = D / kQ4Group;
-  const int64_t bh = blockIdx.y;
-  const int b = (int)(bh / a.heads);
   const int which = blockIdx.z;
-  const int64_t start = a.len ? a.len[b] : 0;
-  const uint32_t* codes = static_cast<const uint32_t*>(which ? a.codes[1] : a.codes[0]) + bh * a.cap * (D / 8);
-  const uint32_t* meta = static_cast<const uint32_t*>(which ? a.meta[1] : a.meta[0]) + bh * a.cap * kNg;
-  T* out = static_cast<T*>(which ? a.out[1] : a.out[0]) + bh * a.rows * D;
-  const int c = threadIdx.x % kTpr, g = c / 8, o = c % 8;
-  for (int64_t r0 = (int64_t)blockIdx.x * (kQ4Threads / kTpr); r0 < a.rows;
-       r0 += (int64_t)gridDim.x * (kQ4Threads / kTpr)) {
-    const int64_t row = r0 + threadIdx.x / kTpr, src = start + row;
-    if (row >= a.rows) break;
-    float x[8];
+  const int c = threadIdx.x % kTpr, g = c / 4, o = 2 * (c % 4);
+  for_rows<kTpr>(grid, a.rows, [&](int64_t bh, int64_t row, bool mine) {
+    if (!mine) return;
+    const int64_t src = (a.len ? a.len[bh / a.heads] : 0) + row;
+    float x[kQ4Each];
     if (src >= 0 && src < a.cap) {
-      const uint32_t w = __ldg(codes + src * (D / 8) + q4_word<kNg>(g, o));
-      const uint32_t m = __ldg(meta + src * kNg + g);
+      const int64_t at = bh * a.cap + src;
+      const uint32_t* codes = static_cast<const uint32_t*>(which ? a.codes[1] : a.codes[0]) + at * (D / 8);
+      const uint32_t m = __ldg(static_cast<const uint32_t*>(which ? a.meta[1] : a.meta[0]) + at * kNg + g);
       const float h = __uint_as_float(m << 16), z = __uint_as_float(m & 0xFFFF0000u);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = fmaf(h, (float)q4_level(w, e), z);   // h t is exact in fp32
+      for (int w = 0; w < 2; ++w) q4_values(one, __ldg(codes + q4_word<kNg>(g, o + w)), h, z, x + 8 * w);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = 0.f;
+      for (int e = 0; e < kQ4Each; ++e) x[e] = 0.f;
     }
-    store8(out + row * D + 8 * c, x);
-  }
+    T* out = static_cast<T*>(which ? a.out[1] : a.out[0]) + (bh * a.rows + row) * D + kQ4Each * c;
+    store8(out, x);
+    store8(out + 8, x + 8);
+  });
 }
 
-// A block takes 256 / (d / 8) rows at a turn. All blocks together are about eight waves, so that a
-// long prompt amortises the head's set-up over several turns.
-dim3 q4_grid(const Q4Job& job) {
-  const int per_turn = kQ4Threads / (job.head_dim / 8);
-  const int64_t turns = (job.rows + per_turn - 1) / per_turn;
+// Blocks and threads: a flat list below 32 rows a head; above, all blocks together are about eight waves,
+// so that a long prompt amortises a block's set-up over several turns.
+dim3 q4_grid(const Q4Job& job, Q4Grid* grid) {
+  const int per_turn = kQ4Threads / (job.head_dim / kQ4Each);
   const int64_t bh = (int64_t)job.batch * job.heads;
+  grid->flat = job.rows < 32;
+  grid->flat_rows = grid->flat ? (unsigned)(bh * job.rows) : 0u;
+  if (grid->flat) return dim3((unsigned)((bh * job.rows + per_turn - 1) / per_turn), 1, 2);
+  const int64_t turns = (job.rows + per_turn - 1) / per_turn;
   int64_t blocks = ((int64_t)device_sm_count() * 8 * 8 + 2 * bh - 1) / (2 * bh);
   if (blocks > turns) blocks = turns;
   return dim3((unsigned)(blocks < 1 ? 1 : blocks), (unsigned)bh, 2);
 }
 
-}  // namespace
-
-cudaError_t launch_q4_append(const Q4Job& job) {
-  const dim3 grid = q4_grid(job);
-  if (job.dtype == SNAPKV_BF16) {
-    if (job.head_dim == 64)
-      q4_append_kernel<__nv_bfloat16, 64><<<grid, kQ4Threads, 0, job.stream>>>(job);
-    else
-      q4_append_kernel<__nv_bfloat16, 128><<<grid, kQ4Threads, 0, job.stream>>>(job);
-  } else {
-    if (job.head_dim == 64)
-      q4_append_kernel<float, 64><<<grid, kQ4Threads, 0, job.stream>>>(job);
-    else
-      q4_append_kernel<float, 128><<<grid, kQ4Threads, 0, job.stream>>>(job);
-  }
+template <typename T, int D> cudaError_t q4_append_typed(const Q4Job& job) {
+  Q4Grid rows;
+  const dim3 grid = q4_grid(job, &rows);
+  q4_append_kernel<T, D><<<grid, kQ4Threads, 0, job.stream>>>(job, rows);
   return cudaGetLastError();
 }
 
-cudaError_t launch_q4_read(const Q4Job& job) {
-  const dim3 grid = q4_grid(job);
-  if (job.dtype == SNAPKV_BF16) {
-    if (job.head_dim == 64)
-      q4_read_kernel<__nv_bfloat16, 64><<<grid, kQ4Threads, 0, job.stream>>>(job);
-    else
-      q4_read_kernel<__nv_bfloat16, 128><<<grid, kQ4Threads, 0, job.stream>>>(job);
-  } else {
-    if (job.head_dim == 64)
-      q4_read_kernel<float, 64><<<grid, kQ4Threads, 0, job.stream>>>(job);
-    else
-      q4_read_kernel<float, 128><<<grid, kQ4Threads, 0, job.stream>>>(job);
-  }
+template <typename T, int D> cudaError_t q4_read_typed(const Q4Job& job) {
+  Q4Grid rows;
+  const dim3 grid = q4_grid(job, &rows);
+  q4_read_kernel<T, D><<<grid, kQ4Threads, 0, job.stream>>>(job, rows, Q4Ones());
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_q4_append(const Q4Job& job) {
+  if (job.dtype == SNAPKV_BF16)
+    return job.head_dim == 64 ? q4_append_typed<__nv_bfloat16, 64>(job) : q4_append_typed<__nv_bfloat16, 128>(job);
+  return job.head_dim == 64 ? q4_append_typed<float, 64>(job) : q4_append_typed<float, 128>(job);
+}
+
+cudaError_t launch_q4_read(const Q4Job& job) {
+  if (job.dtype == SNAPKV_BF16)
+    return job.head_dim == 64 ? q4_read_typed<__nv_bfloat16, 64>(job) : q4_read_typed<__nv_bfloat16, 128>(job);
+  return job.head_dim == 64 ? q4_read_typed<float, 64>(job) : q4_read_typed<float, 128>(job);
 }
 
 }  // namespace snapkv

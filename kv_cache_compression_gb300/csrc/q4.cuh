@@ -71,13 +71,4 @@ __device__ __forceinline__ uint32_t q4_pack(uint32_t x) {
   return (mag & 0x07070707u) | ((mag >> 1) & 0x38383838u) | (s & 0x80808080u) | ((s << 3) & 0x40404040u);
 }
 
-// The level of channel e (0 .. 7) of a word.
-__device__ __forceinline__ int q4_level(uint32_t w, int e) {
-  const uint32_t half = w >> (16 * (e & 1));
-  const int j = e >> 1;
-  const int sign = j == 0 ? 15 : j == 1 ? 14 : j == 2 ? 7 : 6, at = j == 0 ? 3 : j == 1 ? 0 : j == 2 ? 11 : 8;
-  const int t = 2 * (int)((half >> at) & 7u) + 1;
-  return (half >> sign) & 1u ? -t : t;
-}
-
 }  // namespace snapkv

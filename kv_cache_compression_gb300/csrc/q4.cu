@@ -26,8 +26,8 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return r;
 }
 
-// Sixteen values, and the largest and smallest of them.
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float* x, float* hi, float* lo) {
+// Sixteen values in pairs, and the largest and smallest of them.
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float2* x, float* hi, float* lo) {
   const uint4 a = ld_stream_v4(p), b = ld_stream_v4(p + 8);
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   uint32_t top = w[0], low = w[0];   // two at a time
@@ -37,21 +37,23 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* p, float* x, float* 
     asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(low) : "r"(w[i]));
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 8; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
   *hi = max_nan(__uint_as_float(top << 16), __uint_as_float(top & 0xFFFF0000u));
   *lo = min_nan(__uint_as_float(low << 16), __uint_as_float(low & 0xFFFF0000u));
 }
-__device__ __forceinline__ void load16(const float* p, float* x, float* hi, float* lo) {
+__device__ __forceinline__ void load16(const float* p, float2* x, float* hi, float* lo) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) Elem<float>::widen(ld_stream_v4(p + 4 * i), x + 4 * i);
-  *hi = *lo = x[0];
+  for (int i = 0; i < 4; ++i) {
+    const uint4 w = ld_stream_v4(p + 4 * i);
+    x[2 * i] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+    x[2 * i + 1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+  }
+  *hi = max_nan(x[0].x, x[0].y);
+  *lo = min_nan(x[0].x, x[0].y);
 #pragma unroll
-  for (int e = 1; e < 16; ++e) {
-    *hi = max_nan(*hi, x[e]);
-    *lo = min_nan(*lo, x[e]);
+  for (int e = 1; e < 8; ++e) {
+    *hi = max_nan(*hi, max_nan(x[e].x, x[e].y));
+    *lo = min_nan(*lo, min_nan(x[e].x, x[e].y));
   }
 }
 
@@ -72,51 +74,47 @@ __device__ __forceinline__ void store8(float* p, const float* x) {
 // The level numbers of eight values as nibbles, in q4_pack's order. (x - z) / (2h) + 7.5 has to be
 // rounded as if computed exactly: ties are common (0.7 % of normal bf16 values lie half-way between
 // two levels). So no quotient is trusted: a product with r = 1 / (2h) only finds the nearest border
-// between levels, z + 2h k, and the sign of x - z - 2h k, exact in fp32 up to the difference's own
-// rounding error (which kExact puts back; bf16 values leave none that a border is near to), says on
-// which side x lies. The border's error of one does not matter where it can occur, half-way between two
-// borders. On the border itself the even level wins: level numbers there are k + 7 and k + 8.
+// between levels, z + 2h k, and the sign of s = x - (z + 2h k) says on which side x lies. For bf16 rows the
+// border is exact in fp32 (z is zero or a multiple of 2^-9 of the group's largest value), so the sign is;
+// for fp32 rows (kExact) s is (x - z) - 2h k, exact but for the rounding error of x - z, which is put back.
+// An error of one in k does not matter where it can occur, half-way between two borders. s then becomes 0, 1/2 or 1 (anything but zero, times 2^127, saturates), and k + 7 plus that is
+// rounded to the even level where x lies on the border.
 // kClamp is for groups whose rounded h and z leave a value more than a step outside the levels.
-template <bool kExact, bool kClamp> __device__ __forceinline__ uint32_t levels(const float* x, float h, float z, float r) {
+template <bool kExact, bool kClamp>
+__device__ __forceinline__ uint32_t levels(const float2* x, float h, float z, float r) {
   constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: adding it rounds to a whole number, in the low bits
   const float nz = 0.0f - z;              // (not -z: x + nz is never -0)
   const float2 nz2 = make_float2(nz, nz), r2 = make_float2(r, r), magic = make_float2(kMagic, kMagic),
-               unmagic = make_float2(-kMagic, -kMagic), step = make_float2(-2.0f * h, -2.0f * h);
-  float whole[8], side[8];
+               unmagic = make_float2(-kMagic, -kMagic), step = make_float2(-2.0f * h, -2.0f * h),
+               magic7 = make_float2(kMagic + 7.0f, kMagic + 7.0f);
+  float2 level[4];
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) {
-    const float2 v = make_float2(x[e], x[e + 1]);
-    const float2 d = add2(v, nz2);
-    float2 w = fma2(d, r2, magic);
+  for (int e = 0; e < 4; ++e) {
+    const float2 d = add2(x[e], nz2);
+    float2 k = add2(fma2(d, r2, magic), unmagic);
     if (kClamp) {
-      w.x = fminf(fmaxf(w.x, kMagic - 7.0f), kMagic + 7.0f);
-      w.y = fminf(fmaxf(w.y, kMagic - 7.0f), kMagic + 7.0f);
+      k.x = fminf(fmaxf(k.x, -7.0f), 7.0f);
+      k.y = fminf(fmaxf(k.y, -7.0f), 7.0f);
     }
-    float2 s = fma2(add2(w, unmagic), step, d);
-    if (kExact) {
-      const float bx = d.x - v.x, by = d.y - v.y;
-      s.x += (v.x - (d.x - bx)) + (nz - bx);
-      s.y += (v.y - (d.y - by)) + (nz - by);
+    float2 s;
+    if (!kExact) {
+      s = add2(x[e], fma2(k, step, nz2));
+    } else {
+      s = fma2(k, step, d);
+      const float bx = d.x - x[e].x, by = d.y - x[e].y;
+      s.x += (x[e].x - (d.x - bx)) + (nz - bx);
+      s.y += (x[e].y - (d.y - by)) + (nz - by);
     }
-    whole[e] = w.x;
-    whole[e + 1] = w.y;
-    side[e] = s.x;
-    side[e + 1] = s.y;
+    const float2 side = make_float2(__saturatef(fmaf(s.x, 0x1p127f, 0.5f)), __saturatef(fmaf(s.y, 0x1p127f, 0.5f)));
+    level[e] = add2(add2(k, side), magic7);
   }
-  // k + 8, less one below the border, or on it if that is odd: as a whole number, the bits of s are then less
-  // than k & 1.
-  constexpr int kOrder[8] = {5, 7, 1, 3, 4, 6, 0, 2};   // from the top nibble down
+  // whole numbers in the low bits, as nibbles (the bits of 1.5 * 2^23 that came with each are taken off, mod 2^32)
+  constexpr int kOrder[8] = {5, 7, 1, 3, 4, 6, 0, 2};   // channels, from the top nibble down
   uint32_t u = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t k = __float_as_uint(whole[kOrder[i]]);
-    u = u * 16u + k;
-    if (__float_as_int(side[kOrder[i]]) < (int)(k & 1u)) --u;
-  }
-  // each k came with the bits of 1.5 * 2^23, and 8 is still missing: whole nibbles again, mod 2^32
-  constexpr uint32_t kBits = 0x4B400000u;
-  constexpr uint32_t kAll = kBits * 0x11111111u;
-  return u - kAll + 0x88888888u;
+  for (int i = 0; i < 8; ++i)
+    u = u * 16u + __float_as_uint(kOrder[i] & 1 ? level[kOrder[i] / 2].y : level[kOrder[i] / 2].x);
+  return u - 0x4B400000u * 0x11111111u;
 }
 
 // The rows of a launch. Long calls have a head per blockIdx.y, whose blocks take turns; calls of few rows
@@ -126,19 +124,21 @@ struct Q4Grid {
   unsigned flat_rows;   // of all heads
 };
 
-// Calls f(bh, row, mine) for this thread's rows, the whole warp at once (row and bh are those of row 0 of
-// head 0 where mine is false).
-template <int TPR, typename F> __device__ __forceinline__ void for_rows(const Q4Grid& grid, int64_t rows, F f) {
+// Calls f(sequence, head of all, row, mine) for this thread's rows, the whole warp at once (mine false: some
+// other row that exists).
+template <int TPR, typename F> __device__ __forceinline__ void for_rows(const Q4Grid& grid, int heads, int64_t rows, F f) {
   constexpr int kRows = kQ4Threads / TPR;
   if (grid.flat) {
     const unsigned at = blockIdx.x * kRows + threadIdx.x / TPR;
     const bool mine = at < grid.flat_rows;
     const unsigned bh = mine ? at / (unsigned)rows : 0u;
-    f((int64_t)bh, (int64_t)(mine ? at - bh * (unsigned)rows : 0u), mine);
+    f((int)(bh / (unsigned)heads), bh, (int)(mine ? at - bh * (unsigned)rows : 0u), mine);
   } else {
-    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < rows; r0 += (int64_t)gridDim.x * kRows) {
-      const int64_t row = r0 + threadIdx.x / TPR;
-      f((int64_t)blockIdx.y, row < rows ? row : 0, row < rows);
+    const unsigned bh = blockIdx.y;
+    const int b = (int)(bh / (unsigned)heads);
+    for (int r0 = (int)blockIdx.x * kRows; r0 < (int)rows; r0 += (int)gridDim.x * kRows) {
+      const int row = r0 + (int)threadIdx.x / TPR;
+      f(b, bh, row < (int)rows ? row : 0, row < (int)rows);
     }
   }
 }
@@ -149,24 +149,24 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(Q4Job a, Q4Grid g
   constexpr int kNg = D / kQ4Group;
   const int which = blockIdx.z;             // K or V
   const int c = threadIdx.x % kTpr, g = c / 4, o = 2 * (c % 4);   // group, and the first of its eights
-  for_rows<kTpr>(grid, a.rows, [&](int64_t bh, int64_t row, bool mine) {
-    const int b = (int)(bh / a.heads);
+  for_rows<kTpr>(grid, a.heads, a.rows, [&](int b, unsigned bh, int row, bool mine) {
     const int len = a.len[b];
-    const int64_t n = a.n_new ? a.n_new[b] : a.rows;
-    const bool counts = n >= 0 && n <= a.rows, fits = len >= 0 && counts && len + n <= a.cap;
-    if (mine && row == 0 && c == 0 && which == 0 && bh - (int64_t)b * a.heads == 0) {   // once per sequence
-      a.len_out[b] = fits ? (int)(len + n) : len;
+    const int n = a.n_new ? a.n_new[b] : (int)a.rows;
+    const bool counts = n >= 0 && n <= (int)a.rows, fits = len >= 0 && counts && (int64_t)len + n <= a.cap;
+    if (mine && row == 0 && c == 0 && which == 0 && bh == (unsigned)b * a.heads) {   // once per sequence
+      a.len_out[b] = fits ? len + n : len;
       if (!counts) report(a.dev_status, SNAPKV_ERR_INVALID_ARG);
-      if (len < 0 || (counts && len + n > a.cap)) report(a.dev_status, SNAPKV_ERR_CAPACITY);
+      if (len < 0 || (counts && (int64_t)len + n > a.cap)) report(a.dev_status, SNAPKV_ERR_CAPACITY);
     }
     mine = mine && fits && row < n;
     if (!__any_sync(0xffffffffu, mine)) return;
-    float x[kQ4Each], hi = 0.f, lo = 0.f;
+    float2 x[kQ4Each / 2];
+    float hi = 0.f, lo = 0.f;
     if (mine) {
-      load16(static_cast<const T*>(which ? a.in[1] : a.in[0]) + (bh * a.rows + row) * D + kQ4Each * c, x, &hi, &lo);
+      load16(static_cast<const T*>(which ? a.in[1] : a.in[0]) + ((int64_t)bh * a.rows + row) * D + kQ4Each * c, x, &hi, &lo);
     } else {
 #pragma unroll
-      for (int e = 0; e < kQ4Each; ++e) x[e] = 0.f;
+      for (int e = 0; e < kQ4Each / 2; ++e) x[e] = make_float2(0.f, 0.f);
     }
 #pragma unroll
     for (int off = 1; off < 4; off <<= 1) {
@@ -190,10 +190,10 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(Q4Job a, Q4Grid g
       const bool near = fmaxf(hi - z, z - lo) < 15.9f * h;
 #pragma unroll
       for (int w = 0; w < 2; ++w)
-        u[w] = near ? levels<kExact, false>(x + 8 * w, h, z, r) : levels<kExact, true>(x + 8 * w, h, z, r);
+        u[w] = near ? levels<kExact, false>(x + 4 * w, h, z, r) : levels<kExact, true>(x + 4 * w, h, z, r);
     }
-    if (mine && in_bounds(len + row < a.cap, a.dev_status)) {
-      const int64_t at = bh * a.cap + len + row;
+    if (mine && in_bounds((int64_t)len + row < a.cap, a.dev_status)) {
+      const int64_t at = bh * a.cap + (len + row);
       uint32_t* codes = static_cast<uint32_t*>(which ? a.codes[1] : a.codes[0]) + at * (D / 8);
       codes[q4_word<kNg>(g, o)] = q4_pack(u[0]);
       codes[q4_word<kNg>(g, o + 1)] = q4_pack(u[1]);
@@ -226,9 +226,9 @@ __global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(Q4Job a, Q4Grid gri
   constexpr int kNg = D / kQ4Group;
   const int which = blockIdx.z;
   const int c = threadIdx.x % kTpr, g = c / 4, o = 2 * (c % 4);
-  for_rows<kTpr>(grid, a.rows, [&](int64_t bh, int64_t row, bool mine) {
+  for_rows<kTpr>(grid, a.heads, a.rows, [&](int b, unsigned bh, int row, bool mine) {
     if (!mine) return;
-    const int64_t src = (a.len ? a.len[bh / a.heads] : 0) + row;
+    const int64_t src = (int64_t)(a.len ? a.len[b] : 0) + row;
     float x[kQ4Each];
     if (src >= 0 && src < a.cap) {
       const int64_t at = bh * a.cap + src;
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(Q4Job a, Q4Grid gri
 #pragma unroll
       for (int e = 0; e < kQ4Each; ++e) x[e] = 0.f;
     }
-    T* out = static_cast<T*>(which ? a.out[1] : a.out[0]) + (bh * a.rows + row) * D + kQ4Each * c;
+    T* out = static_cast<T*>(which ? a.out[1] : a.out[0]) + ((int64_t)bh * a.rows + row) * D + kQ4Each * c;
     store8(out, x);
     store8(out + 8, x + 8);
   });

@@ -106,6 +106,9 @@ def test_groups_where_rounding_is_hard(dev, dtype):
         rows.append(base * 2.0 ** (i - 32))
         rows.append(100.0 + base * 2.0 ** -(i % 8))
         rows.append(torch.full((128,), float(base[0])))
+        # magnitudes far apart: the difference to the centre is rounded, a border may lie at zero
+        rows.append(base * 10.0 ** torch.randint(-6, 2, (128,), generator=g))
+        rows.append(torch.where(base > 0, base, base * 2.0 ** -30))
         rows.append(torch.where(torch.arange(128) == i, base[0] * 1e-30, torch.zeros(128)))
         rows.append(torch.where(torch.arange(128) == 2 * i, torch.tensor(float("nan")), base))
         rows.append(torch.where(torch.arange(128) == i, torch.tensor(float("-inf")), base))

@@ -486,10 +486,14 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
       for (int g = 0; g < kNg; ++g) oz[g][0] = oz[g][1] = 0.f;
     }
 
-    // First product: B in one part (bf16), or three (fp32).
-    auto mma_q = [&](float* c, const uint32_t* w, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-#pragma unroll
-      for (int part = 0; part < (S::kWide ? 3 : 1); ++part) mma16816(c, a0, a1, a2, a3, w[2 * part], w[2 * part + 1]);
+    // First product: B in one part (bf16), or three (fp32: the small parts' products have an accumulator of
+    // their own, as a tensor-core addition truncates at its accumulator's magnitude).
+    auto mma_q = [&](float* c, float* small, const uint32_t* w, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+      mma16816(c, a0, a1, a2, a3, w[0], w[1]);
+      if constexpr (S::kWide) {
+        mma16816(small, a0, a1, a2, a3, w[2], w[3]);
+        mma16816(small, a0, a1, a2, a3, w[4], w[5]);
+      }
     };
 
     // Weights of rows j (x[0]) and j + 8 (x[1]), for queries qa and qa + 1, as B operands in parts.
@@ -542,7 +546,7 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
           float d[4] = {}, zq[4] = {};
 #pragma unroll
           for (int g = 0; g < kNg; ++g) {
-            float dot[4] = {};
+            float dot[4] = {}, small[4] = {};
 #pragma unroll
             for (int o2 = 0; o2 < 2; ++o2) {
               uint32_t e[2][4];
@@ -551,19 +555,19 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
                 const uint32_t word = w[half][q4_word<kNg>(g, o2)];
                 q4_operands(ones, word, prmt(word, word, 0x2301), e[half]);
               }
-              mma_q(dot, qb[4 * g + 2 * o2], e[0][0], e[1][0], e[0][1], e[1][1]);
-              mma_q(dot, qb[4 * g + 2 * o2 + 1], e[0][2], e[1][2], e[0][3], e[1][3]);
+              mma_q(dot, small, qb[4 * g + 2 * o2], e[0][0], e[1][0], e[0][1], e[1][1]);
+              mma_q(dot, small, qb[4 * g + 2 * o2 + 1], e[0][2], e[1][2], e[0][3], e[1][3]);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              d[e] = fmaf(hz[e / 2][g].x, dot[e], d[e]);
+              d[e] = fmaf(hz[e / 2][g].x, S::kWide ? dot[e] + small[e] : dot[e], d[e]);
               zq[e] = fmaf(hz[e / 2][g].y, qsum[g][e % 2], zq[e]);
             }
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) sv[sub][e] = fmaf(d[e], dot_scale, zq[e]);
         } else if constexpr (S::kWide) {
-          float dot[4] = {};
+          float dot[4] = {}, small[4] = {};
 #pragma unroll
           for (int s4 = 0; s4 < kSteps; ++s4) {
             float2 f[2][2];   // [rows j, j + 8][channels 4 i, + 1 and 4 i + 2, + 3 of the step's 16]
@@ -578,11 +582,11 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
               const uint32_t a0 = split2(f[0][0]), a1 = split2(f[1][0]), a2 = split2(f[0][1]), a3 = split2(f[1][1]);
 #pragma unroll
               for (int part = 0; part < 3 - kp; ++part)
-                mma16816(dot, a0, a1, a2, a3, qb[s4][2 * part], qb[s4][2 * part + 1]);
+                mma16816(kp + part ? small : dot, a0, a1, a2, a3, qb[s4][2 * part], qb[s4][2 * part + 1]);
             }
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sv[sub][e] = dot[e] * dot_scale;
+          for (int e = 0; e < 4; ++e) sv[sub][e] = (dot[e] + small[e]) * dot_scale;
         } else {
           float dot[4] = {};
 #pragma unroll
@@ -590,7 +594,7 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
             // matrices: rows 0 .. 7 and 8 .. 15 of the step's first eight channels, then of the others
             uint32_t x[4];
             load_matrices<false>(kt + piece_at<S::kRow>(16 * sub + lane % 16, 2 * s4 + lane / 16), x);
-            mma_q(dot, qb[s4], x[0], x[1], x[2], x[3]);
+            mma_q(dot, dot, qb[s4], x[0], x[1], x[2], x[3]);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) sv[sub][e] = dot[e] * dot_scale;
@@ -699,10 +703,17 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
               q4_operands(ones, prmt(w[2][g], w[3][g], sel), prmt(w[2][g], w[3][g], swap), hi[odd]);
             }
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c) {
+              float t[4] = {};   // fp32: these rows' sum, from the smallest part, then added with rounding
+              float* acc = S::kWide ? t : o[4 * g + c];
 #pragma unroll
-              for (int part = 0; part < kParts; ++part)
-                mma16816(o[4 * g + c], lo[0][c], lo[1][c], hi[0][c], hi[1][c], pb[part][0], pb[part][1]);
+              for (int part = kParts - 1; part >= 0; --part)
+                mma16816(acc, lo[0][c], lo[1][c], hi[0][c], hi[1][c], pb[part][0], pb[part][1]);
+              if constexpr (S::kWide) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[4 * g + c][e] += t[e];
+              }
+            }
           }
         } else if constexpr (S::kWide) {
           uint32_t pb[S::kParts][2];
@@ -719,13 +730,22 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
             for (int c = 0; c < 4; c += 2) {
               float2 v0 = make_float2(f[0][c], f[1][c]), v2 = make_float2(f[2][c], f[3][c]);
               float2 v1 = make_float2(f[0][c + 1], f[1][c + 1]), v3 = make_float2(f[2][c + 1], f[3][c + 1]);
+              uint32_t va[3][4];
 #pragma unroll
-              for (int vp = 0; vp < 3; ++vp) {   // parts of the values; those of the weights with them
-                const uint32_t a0 = split2(v0), a1 = split2(v1), a2 = split2(v2), a3 = split2(v3);
-#pragma unroll
-                for (int part = 0; part < 3 - vp; ++part)
-                  mma16816(o[2 * c4 + c / 2], a0, a1, a2, a3, pb[part][0], pb[part][1]);
+              for (int vp = 0; vp < 3; ++vp) {
+                va[vp][0] = split2(v0);
+                va[vp][1] = split2(v1);
+                va[vp][2] = split2(v2);
+                va[vp][3] = split2(v3);
               }
+              float t[4] = {};   // these rows' sum, from the smallest products, then added with rounding
+#pragma unroll
+              for (int order = 2; order >= 0; --order)
+#pragma unroll
+                for (int vp = 0; vp <= order; ++vp)
+                  mma16816(t, va[vp][0], va[vp][1], va[vp][2], va[vp][3], pb[order - vp][0], pb[order - vp][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[2 * c4 + c / 2][e] += t[e];
             }
           }
         } else {

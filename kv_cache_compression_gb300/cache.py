@@ -4,6 +4,10 @@ Decode attention with grouped queries that keeps a running score of every cached
 that score, and a cache held in 4 bits. As in ``snapkv``, every computation runs in the library's
 CUDA kernels and arguments mirror the header; calls run on ``stream`` (default: the current stream
 of the tensors' device), allocate what the caller does not pass, and raise on a refused call.
+
+A decode step makes several of these calls, and its kernels take microseconds each: the checks are
+written to cost little where they pass, and calls with their buffers (``out``, ``workspace``, ...)
+passed in cost less still.
 """
 from __future__ import annotations
 
@@ -17,6 +21,9 @@ from . import snapkv as _sk
 from .snapkv import ERR_INVALID_ARG, OK, SnapKVError
 
 GROUP = 64   # channels of a 4-bit row that share one (h, z)
+
+_INT32, _FP32, _BF16, _BYTE = torch.int32, torch.float32, torch.bfloat16, torch.uint8
+_DTYPES = {_FP32: _sk.F32, _BF16: _sk.BF16}
 
 
 class _Q4Struct(ctypes.Structure):
@@ -35,6 +42,7 @@ def lib():
     if not _functions:
         P, I32, I64, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
         C = ctypes.POINTER(_Q4Struct)
+        found = {}
         for name, res, args in [
                 ("snapkv_scored_workspace_size", SZ, [I32, I32, I32, I32, I64, I32]),
                 ("snapkv_decode_attend_scored", I32,
@@ -47,7 +55,8 @@ def lib():
                 ("snapkv_q4_evict", I32, [C, P, P, P, I64, I64, P, P, SZ, P, P])]:
             f = getattr(L, name)
             f.restype, f.argtypes = res, args
-            _functions[name] = f
+            found[name] = f
+        _functions.update(found)
     return L
 
 
@@ -64,44 +73,32 @@ def _check(name, t, shape, dtype, device):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _lengths(name, t, batch, device):
-    _check(name, t, (batch,), torch.int32, device)
+def _code(dtype):
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
+    return code
 
 
 def _status(t, device):
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.device != device or t.numel() < 1:
+    if t.dtype != _INT32 or t.device != device or t.numel() < 1:
         raise ValueError(f"dev_status must be an int32 tensor on {device}")
     return t.data_ptr()
-
-
-_DTYPES = {torch.float32: _sk.F32, torch.bfloat16: _sk.BF16}
-
-
-def _dtype_code(t):
-    code = _DTYPES.get(t.dtype)
-    return _sk._dtype_code(t) if code is None else code   # (which raises)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
 
 
 def _room(workspace, need, device):
     """The caller's workspace or a new one, and its bytes."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device), need
+        return torch.empty(need, dtype=_BYTE, device=device), need
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace, workspace.numel() * workspace.element_size()
 
 
 def _call(name, device, stream, *args):
-    """Calls a library function with `device` current (kernels launch there) and the stream last.
-
-    A decode step makes several of these calls and each kernel takes microseconds, so the usual case
-    (the tensors' device is the current one) takes the raw stream handle and no context manager."""
+    """Calls a library function with `device` current (kernels launch there) and the stream last."""
     if device.type != "cuda":
         raise ValueError(f"{name} needs CUDA tensors, not {device}")
     f = _functions.get(name)
@@ -110,7 +107,7 @@ def _call(name, device, stream, *args):
         f = _functions[name]
     index = device.index
     handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         st = f(*args, handle)
     else:
         with torch.cuda.device(index):
@@ -134,10 +131,11 @@ class Q4Cache:
             raise ValueError("k_codes must be [B, H, cap, d / 2] with d 64 or 128")
         B, H, cap, half = self.k_codes.shape
         dev = self.k_codes.device
-        _check("k_codes", self.k_codes, (B, H, cap, half), torch.uint8, dev)
-        _check("v_codes", self.v_codes, (B, H, cap, half), torch.uint8, dev)
-        for name, t in (("k_meta", self.k_meta), ("v_meta", self.v_meta)):
-            _check(name, t, (B, H, cap, half * 2 // GROUP, 2), torch.bfloat16, dev)
+        _check("k_codes", self.k_codes, (B, H, cap, half), _BYTE, dev)
+        _check("v_codes", self.v_codes, (B, H, cap, half), _BYTE, dev)
+        meta = (B, H, cap, half * 2 // GROUP, 2)
+        _check("k_meta", self.k_meta, meta, _BF16, dev)
+        _check("v_meta", self.v_meta, meta, _BF16, dev)
         object.__setattr__(self, "shape", (B, H, cap, 2 * half))   # B, H, cap, d
         object.__setattr__(self, "device", dev)
 
@@ -149,20 +147,21 @@ class Q4Cache:
     @classmethod
     def empty(cls, batch, heads, cap, head_dim, device):
         """An uninitialised cache (rows are written by q4_append)."""
-        codes = [torch.empty((batch, heads, cap, head_dim // 2), dtype=torch.uint8, device=device) for _ in "kv"]
-        meta = [torch.empty((batch, heads, cap, head_dim // GROUP, 2), dtype=torch.bfloat16, device=device)
-                for _ in "kv"]
+        codes = [torch.empty((batch, heads, cap, head_dim // 2), dtype=_BYTE, device=device) for _ in "kv"]
+        meta = [torch.empty((batch, heads, cap, head_dim // GROUP, 2), dtype=_BF16, device=device) for _ in "kv"]
         return cls(codes[0], meta[0], codes[1], meta[1])
 
 
 @lru_cache(maxsize=256)
 def scored_workspace_size(batch, q_heads, heads, head_dim, cap, scored=True) -> int:
-    return int(lib().snapkv_scored_workspace_size(batch, q_heads, heads, head_dim, cap, bool(scored)))
+    lib()
+    return int(_functions["snapkv_scored_workspace_size"](batch, q_heads, heads, head_dim, cap, bool(scored)))
 
 
 @lru_cache(maxsize=256)
 def evict_workspace_size(batch, heads, cap) -> int:
-    return int(lib().snapkv_evict_workspace_size(batch, heads, cap))
+    lib()
+    return int(_functions["snapkv_evict_workspace_size"](batch, heads, cap))
 
 
 def _attend_args(where, q, shape, dev, len_, score, out, workspace):
@@ -174,15 +173,15 @@ def _attend_args(where, q, shape, dev, len_, score, out, workspace):
     if q_heads < 1 or q_heads % H:
         raise SnapKVError(ERR_INVALID_ARG, where)
     _check("q", q, (B, q_heads, d), q.dtype, dev)
-    _lengths("len_", len_, B, dev)
+    _check("len_", len_, (B,), _INT32, dev)
+    if score is not None:
+        _check("score", score, (B, H, cap), _FP32, dev)
     if out is None:
         out = torch.empty_like(q)
     else:
         _check("out", out, q.shape, q.dtype, dev)
-    if score is not None:
-        _check("score", score, (B, H, cap), torch.float32, dev)
     workspace, ws_bytes = _room(workspace, scored_workspace_size(B, q_heads, H, d, cap, score is not None), dev)
-    return q_heads, out, workspace, ws_bytes
+    return q_heads, None if score is None else score.data_ptr(), out, workspace, ws_bytes
 
 
 def decode_attend_scored(q, k_cache, v_cache, len_, score=None, *, decay=1.0, out=None, workspace=None,
@@ -190,17 +189,17 @@ def decode_attend_scored(q, k_cache, v_cache, len_, score=None, *, decay=1.0, ou
     """snapkv_decode_attend_scored: q [B,Hq,d] over rows < len_[b] of k_cache, v_cache [B,H,cap,d] (Hq a
     multiple of H) -> out [B,Hq,d]. ``score`` fp32 [B,H,cap], if given, becomes decay * score + the
     attention each row received, in place (rows < len_[b] only; clear it before the first step)."""
-    if k_cache.dim() != 4:
+    shape, dev, dtype = k_cache.shape, k_cache.device, q.dtype
+    if len(shape) != 4:
         raise ValueError("k_cache must be [B, H, cap, d]")
-    B, H, cap, d = k_cache.shape
-    dev = k_cache.device
-    _check("k_cache", k_cache, k_cache.shape, q.dtype, dev)
-    _check("v_cache", v_cache, k_cache.shape, q.dtype, dev)
-    q_heads, out, workspace, ws_bytes = _attend_args("snapkv_decode_attend_scored", q, k_cache.shape, dev, len_,
-                                                     score, out, workspace)
-    _call("snapkv_decode_attend_scored", dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), cap,
-          _ptr(len_), _ptr(score), float(decay), _ptr(out), B, q_heads, H, d, _dtype_code(q),
-          _ptr(workspace), ws_bytes, _status(dev_status, dev))
+    _check("k_cache", k_cache, shape, dtype, dev)
+    _check("v_cache", v_cache, shape, dtype, dev)
+    q_heads, score_at, out, workspace, ws_bytes = _attend_args("snapkv_decode_attend_scored", q, shape, dev, len_,
+                                                               score, out, workspace)
+    B, H, cap, d = shape
+    _call("snapkv_decode_attend_scored", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), cap,
+          len_.data_ptr(), score_at, decay, out.data_ptr(), B, q_heads, H, d, _code(dtype), workspace.data_ptr(),
+          ws_bytes, _status(dev_status, dev))
     return out
 
 
@@ -208,45 +207,54 @@ def q4_decode_attend(q, cache, len_, score=None, *, decay=1.0, out=None, workspa
                      stream=None):
     """snapkv_q4_decode_attend: decode_attend_scored over a Q4Cache; q and out are bf16 or fp32."""
     dev = cache.device
-    q_heads, out, workspace, ws_bytes = _attend_args("snapkv_q4_decode_attend", q, cache.shape, dev, len_, score,
-                                                     out, workspace)
-    _call("snapkv_q4_decode_attend", dev, stream, _ptr(q), cache._struct(), _ptr(len_), _ptr(score),
-          float(decay), _ptr(out), q_heads, _dtype_code(q), _ptr(workspace), ws_bytes,
-          _status(dev_status, dev))
+    q_heads, score_at, out, workspace, ws_bytes = _attend_args("snapkv_q4_decode_attend", q, cache.shape, dev, len_,
+                                                               score, out, workspace)
+    _call("snapkv_q4_decode_attend", dev, stream, q.data_ptr(), cache._struct(), len_.data_ptr(), score_at, decay,
+          out.data_ptr(), q_heads, _code(q.dtype), workspace.data_ptr(), ws_bytes, _status(dev_status, dev))
     return out
+
+
+def _new_lengths(len_in, len_out, batch, dev):
+    _check("len_in", len_in, (batch,), _INT32, dev)
+    if len_out is None:
+        return torch.empty_like(len_in)
+    _check("len_out", len_out, (batch,), _INT32, dev)
+    return len_out
 
 
 def q4_append(cache, k_new, v_new, len_in, len_out=None, *, n_new=None, dev_status=None, stream=None):
     """snapkv_q4_append: quantises k_new, v_new [B,H,rows,d] (or [B,H,d], one row) into rows len_in[b] on of a
     Q4Cache, n_new[b] of them if given. Returns len_out [B] (len_in is only read)."""
-    B, H, cap, d = cache.shape
-    dev = cache.device
-    rows = k_new.shape[2] if k_new.dim() == 4 else 1
-    shape = (B, H, rows, d) if k_new.dim() == 4 else (B, H, d)
-    _check("k_new", k_new, shape, k_new.dtype, dev)
-    _check("v_new", v_new, shape, k_new.dtype, dev)
-    _lengths("len_in", len_in, B, dev)
-    if n_new is not None:
-        _lengths("n_new", n_new, B, dev)
-    if len_out is None:
-        len_out = torch.empty_like(len_in)
+    B, H, _, d = cache.shape
+    dev, dtype = cache.device, k_new.dtype
+    if k_new.dim() == 4:
+        rows = k_new.shape[2]
+        shape = (B, H, rows, d)
     else:
-        _lengths("len_out", len_out, B, dev)
-    _call("snapkv_q4_append", dev, stream, cache._struct(), _ptr(k_new), _ptr(v_new), rows,
-          _ptr(n_new), _ptr(len_in), _ptr(len_out), _dtype_code(k_new), _status(dev_status, dev))
+        rows = 1
+        shape = (B, H, d)
+    _check("k_new", k_new, shape, dtype, dev)
+    _check("v_new", v_new, shape, dtype, dev)
+    if n_new is not None:
+        _check("n_new", n_new, (B,), _INT32, dev)
+    len_out = _new_lengths(len_in, len_out, B, dev)
+    _call("snapkv_q4_append", dev, stream, cache._struct(), k_new.data_ptr(), v_new.data_ptr(), rows,
+          None if n_new is None else n_new.data_ptr(), len_in.data_ptr(), len_out.data_ptr(), _code(dtype),
+          _status(dev_status, dev))
     return len_out
 
 
 def q4_read(cache, rows, *, start=None, dtype=None, k_out=None, v_out=None, stream=None):
     """snapkv_q4_read: the values (dtype: bf16 or fp32, default bf16) that rows start[b] .. start[b] + rows - 1
     of a Q4Cache stand for, as k, v [B,H,rows,d]; rows outside the cache are zeros."""
-    B, H, cap, d = cache.shape
+    B, H, _, d = cache.shape
     dev = cache.device
     if dtype is None:
-        dtype = torch.bfloat16 if k_out is None else k_out.dtype
+        dtype = _BF16 if k_out is None else k_out.dtype
+    code = _code(dtype)
     if start is not None:
-        _lengths("start", start, B, dev)
-    shape = (B, H, rows, d)
+        _check("start", start, (B,), _INT32, dev)
+    shape = (B, H, int(rows), d)
     if k_out is None:
         k_out = torch.empty(shape, dtype=dtype, device=dev)
     else:
@@ -255,27 +263,23 @@ def q4_read(cache, rows, *, start=None, dtype=None, k_out=None, v_out=None, stre
         v_out = torch.empty_like(k_out)
     else:
         _check("v_out", v_out, shape, dtype, dev)
-    _call("snapkv_q4_read", dev, stream, cache._struct(), _ptr(start), int(rows), _ptr(k_out),
-          _ptr(v_out), _dtype_code(k_out))
+    _call("snapkv_q4_read", dev, stream, cache._struct(), None if start is None else start.data_ptr(), shape[2],
+          k_out.data_ptr(), v_out.data_ptr(), code)
     return k_out, v_out
 
 
 def _evict_args(shape, dev, score, len_in, len_out, keep, recent, idx_out, want_idx, workspace):
     """Checks and completes what the two evictions share."""
-    B, H, cap, d = shape
-    _check("score", score, (B, H, cap), torch.float32, dev)
-    _lengths("len_in", len_in, B, dev)
-    if len_out is None:
-        len_out = torch.empty_like(len_in)
-    else:
-        _lengths("len_out", len_out, B, dev)
-    left = int(keep) + int(recent)
+    B, H, cap, _ = shape
+    _check("score", score, (B, H, cap), _FP32, dev)
+    len_out = _new_lengths(len_in, len_out, B, dev)
+    left = keep + recent
     if idx_out is not None:
-        _check("idx_out", idx_out, (B, H, left), torch.int32, dev)
+        _check("idx_out", idx_out, (B, H, left), _INT32, dev)
     elif want_idx and left > 0:
-        idx_out = torch.empty((B, H, left), dtype=torch.int32, device=dev)
+        idx_out = torch.empty((B, H, left), dtype=_INT32, device=dev)
     workspace, ws_bytes = _room(workspace, evict_workspace_size(B, H, cap), dev)
-    return len_out, idx_out, workspace, ws_bytes
+    return len_out, idx_out, None if idx_out is None else idx_out.data_ptr(), workspace, ws_bytes
 
 
 def evict(k_cache, v_cache, score, len_in, len_out=None, *, keep, recent, idx_out=None, want_idx=True,
@@ -283,17 +287,17 @@ def evict(k_cache, v_cache, score, len_in, len_out=None, *, keep, recent, idx_ou
     """snapkv_evict: brings sequences of more than keep + recent rows down to the ``keep`` rows of largest score
     and the newest ``recent``, per head and in place (k_cache, v_cache [B,H,cap,d], score [B,H,cap]). Returns
     (len_out [B], idx [B,H,keep+recent] or None): the new lengths and the slot each row came from."""
-    if k_cache.dim() != 4:
+    shape, dev, dtype = k_cache.shape, k_cache.device, k_cache.dtype
+    if len(shape) != 4:
         raise ValueError("k_cache must be [B, H, cap, d]")
-    B, H, cap, d = k_cache.shape
-    dev = k_cache.device
-    _check("k_cache", k_cache, k_cache.shape, k_cache.dtype, dev)
-    _check("v_cache", v_cache, k_cache.shape, k_cache.dtype, dev)
-    len_out, idx_out, workspace, ws_bytes = _evict_args(k_cache.shape, dev, score, len_in, len_out, keep, recent,
-                                                        idx_out, want_idx, workspace)
-    _call("snapkv_evict", dev, stream, _ptr(k_cache), _ptr(v_cache), cap, _ptr(score),
-          _ptr(len_in), _ptr(len_out), int(keep), int(recent), _ptr(idx_out), B, H, d,
-          _dtype_code(k_cache), _ptr(workspace), ws_bytes, _status(dev_status, dev))
+    _check("k_cache", k_cache, shape, dtype, dev)
+    _check("v_cache", v_cache, shape, dtype, dev)
+    len_out, idx_out, idx_at, workspace, ws_bytes = _evict_args(shape, dev, score, len_in, len_out, keep, recent,
+                                                                idx_out, want_idx, workspace)
+    B, H, cap, d = shape
+    _call("snapkv_evict", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), cap, score.data_ptr(),
+          len_in.data_ptr(), len_out.data_ptr(), keep, recent, idx_at, B, H, d, _code(dtype), workspace.data_ptr(),
+          ws_bytes, _status(dev_status, dev))
     return len_out, idx_out
 
 
@@ -301,8 +305,8 @@ def q4_evict(cache, score, len_in, len_out=None, *, keep, recent, idx_out=None, 
              dev_status=None, stream=None):
     """snapkv_q4_evict: evict for a Q4Cache."""
     dev = cache.device
-    len_out, idx_out, workspace, ws_bytes = _evict_args(cache.shape, dev, score, len_in, len_out, keep, recent,
-                                                        idx_out, want_idx, workspace)
-    _call("snapkv_q4_evict", dev, stream, cache._struct(), _ptr(score), _ptr(len_in), _ptr(len_out),
-          int(keep), int(recent), _ptr(idx_out), _ptr(workspace), ws_bytes, _status(dev_status, dev))
+    len_out, idx_out, idx_at, workspace, ws_bytes = _evict_args(cache.shape, dev, score, len_in, len_out, keep,
+                                                                recent, idx_out, want_idx, workspace)
+    _call("snapkv_q4_evict", dev, stream, cache._struct(), score.data_ptr(), len_in.data_ptr(), len_out.data_ptr(),
+          keep, recent, idx_at, workspace.data_ptr(), ws_bytes, _status(dev_status, dev))
     return len_out, idx_out

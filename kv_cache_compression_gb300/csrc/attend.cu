@@ -201,7 +201,7 @@ template <bool Q4, typename IO, int D> struct Shape {
   static constexpr int kWarps = snapkv::kWarps;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kCtasPerSm = kRow >= 512 ? 1 : 2;   // what the ring leaves room for
+  static constexpr int kCtasPerSm = Q4 ? (kWide ? 2 : 3) : kRow >= 512 ? 1 : 2;   // what the ring leaves room for
   static constexpr int smem(int tile_q) { return kRing + kWarps * tile_q * D * 4; }
 };
 
@@ -870,7 +870,7 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
   cp_wait<0>();
 }
 
-// The second launch. The warps of its first blocks each join 32 channels of an output row whose head was
+// The second launch. The warps of its first blocks each join 64 channels of an output row whose head was
 // cut (or is empty); the other blocks each add the weights of kJoinRows rows to a head's scores. Where a head's
 // parts lie follows from the schedule. The kernel is all latency: loads are issued together and early,
 // and registers are kept to what lets four blocks share an SM.
@@ -913,8 +913,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
   const int tid = threadIdx.x, lane = tid % 32;
   const int per_seq = a.heads * a.passes;
   const bool scores = (int)blockIdx.x >= out_blocks;
-  // This block's head, or this warp's output row and 32 of its channels.
-  constexpr int kSlices = D / 32;
+  // This block's head, or this warp's output row and 64 of its channels.
+  constexpr int kSlices = D / 64;
   const int64_t slice = (int64_t)blockIdx.x * (kJoinThreads / 32) + tid / 32;
   const int block = (int)blockIdx.x - out_blocks;
   const int64_t out_row = slice / kSlices;
@@ -945,8 +945,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
 
   if (!scores) {
     const int g = (int)(out_row - (int64_t)bh * a.group), pass = g / a.tile_q, q = g - pass * a.tile_q;
-    const int c = (int)(slice % kSlices) * 32 + lane;
-    float x = 0.f, sum = 0.f;
+    const int c = (int)(slice % kSlices) * 64 + 2 * lane;
+    float x = 0.f, y = 0.f, sum = 0.f;
     if (tiles > 0) {
       if (parts.more == 0) return;   // finished in the first launch
       const int at_m = a.tile_q * D + q, at_l = a.tile_q * (D + 1) + q;
@@ -959,19 +959,28 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
         const float f = m == -INFINITY ? 0.f : ex2(m - next), old = top == -INFINITY ? 0.f : ex2(top - next);
         top = next;
         x *= old;
+        y *= old;
         sum = fmaf(sum, old, warp_sum(l * f));
         const int here = min(32, parts.more + 1 - i0);
 #pragma unroll 1
         for (int i = 0; i < here; i += 8) {
-          float v[8];
+          float2 v[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = i + e < here ? __ldcg(parts[i0 + i + e] + q * D + c) : 0.f;
+          for (int e = 0; e < 8; ++e)
+            v[e] = i + e < here ? __ldcg(reinterpret_cast<const float2*>(parts[i0 + i + e] + q * D + c)) : make_float2(0.f, 0.f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x = fmaf(v[e], __shfl_sync(0xffffffffu, f, (i + e) & 31), x);
+          for (int e = 0; e < 8; ++e) {
+            const float w = __shfl_sync(0xffffffffu, f, (i + e) & 31);
+            x = fmaf(v[e].x, w, x);
+            y = fmaf(v[e].y, w, y);
+          }
         }
       }
     }
-    store1<IO>(static_cast<IO*>(a.out) + out_row * D + c, sum == 0.f ? 0.f : x / sum);   // (a NaN stays one)
+    const float scale = sum == 0.f ? 0.f : 1.0f / sum;   // a NaN stays one
+    IO* out = static_cast<IO*>(a.out) + out_row * D + c;
+    store1<IO>(out, x * scale);
+    store1<IO>(out + 1, y * scale);
     return;
   }
 
@@ -1087,7 +1096,7 @@ cudaError_t launch_typed(const AttendJob& job) {
   if (err != cudaSuccess || a.direct) return err;
   const int64_t chunks = job.score ? (job.cap + kJoinRows - 1) / kJoinRows : 0;
   const int64_t score_blocks = (int64_t)job.batch * job.heads * chunks;
-  const int64_t slices = (int64_t)job.batch * job.q_heads * (D / 32);
+  const int64_t slices = (int64_t)job.batch * job.q_heads * (D / 64);
   const int64_t out_blocks = (slices + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
   const int64_t blocks = out_blocks + score_blocks;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;

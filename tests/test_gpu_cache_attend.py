@@ -126,6 +126,60 @@ def test_long_and_wide(dev, q4, B, H, G, cap, dtype):
                  **{name: t[sel] for name, t in sizes.items()})
 
 
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("lens,cap", [
+    ([0, 0, 700, 0, 1, 0, 64, 129, 0, 700] * 4 + [0, 0, 0], 700),       # 43 sequences, empty ones at both ends
+    ([0] * 5, 400), ([0, 0, 3, 0], 3000), ([300] * 70, 300), ([5, 4000, 17, 0, 3999, 1], 4000)])
+def test_schedules_with_empty_and_uneven_sequences(dev, q4, lens, cap):
+    """Shares that start and end inside sequences, empty sequences anywhere, fewer tiles than CTAs."""
+    import kv_cache_compression_gb300 as kv
+    g = torch.Generator().manual_seed(len(lens) + cap)
+    B, H, G, d = len(lens), 2, 3, 64
+    dtype = torch.bfloat16
+    score = torch.rand(B, H, cap, generator=g)
+    s = score.to(dev)
+    n = torch.tensor(lens, dtype=torch.int32, device=dev)
+    if q4:
+        c = four_bits(g, B, H, cap, d, lens)
+        q = (torch.randn(B, G * H, d, generator=g) * 1.5).to(dtype)
+        out = kv.q4_decode_attend(q.to(dev), kv.Q4Cache(*(t.to(dev) for t in (*c["k"][:2], *c["v"][:2]))), n, s)
+        k64, v64, sizes = c["k"][2], c["v"][2], dict(k_size=c["k"][3], v_size=c["v"][3])
+    else:
+        q, k, v, _, _ = dense(g, B, G * H, H, cap, d, dtype, lens)
+        out = kv.decode_attend_scored(q.to(dev), k.to(dev), v.to(dev), n, s)
+        k64, v64, sizes = to64(k), to64(v), {}
+    torch.cuda.synchronize()
+    check_attend(q, k64, v64, lens, out, score0=score, score=s.cpu(), where=f"{len(lens)} of {cap}", **sizes)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_shapes(dev, seed):
+    import random
+    import kv_cache_compression_gb300 as kv
+    rng = random.Random(seed)
+    g = torch.Generator().manual_seed(seed)
+    B, H, G, d = rng.choice([1, 2, 3, 7, 40]), rng.choice([1, 2, 5]), rng.choice([1, 2, 4, 6, 8, 10, 17]), rng.choice([64, 128])
+    cap = rng.choice([17, 100, 255, 256, 257, 513, 1000, 2049]) if B < 40 else rng.choice([65, 300])
+    dtype, q4, decay = rng.choice([torch.bfloat16, torch.float32]), rng.random() < 0.5, rng.choice([0.0, 0.5, 1.0])
+    lens = [rng.choice([0, 1, cap, cap, rng.randrange(cap + 1)]) for _ in range(B)]
+    n = torch.tensor(lens, dtype=torch.int32, device=dev)
+    score = torch.rand(B, H, cap, generator=g)
+    s = score.to(dev)
+    if q4:
+        c = four_bits(g, B, H, cap, d, lens)
+        q = (torch.randn(B, G * H, d, generator=g) * 1.5).to(dtype)
+        cache = kv.Q4Cache(*(t.to(dev) for t in (*c["k"][:2], *c["v"][:2])))
+        out = kv.q4_decode_attend(q.to(dev), cache, n, s, decay=decay)
+        k64, v64, sizes = c["k"][2], c["v"][2], dict(k_size=c["k"][3], v_size=c["v"][3])
+    else:
+        q, k, v, _, _ = dense(g, B, G * H, H, cap, d, dtype, lens)
+        out = kv.decode_attend_scored(q.to(dev), k.to(dev), v.to(dev), n, s, decay=decay)
+        k64, v64, sizes = to64(k), to64(v), {}
+    torch.cuda.synchronize()
+    check_attend(q, k64, v64, lens, out, score0=score, score=s.cpu(), decay=decay,
+                 where=f"seed {seed}: {dtype} q4 {q4} B{B} H{H} G{G} d{d} cap{cap}", **sizes)
+
+
 def test_one_query_per_head_matches_the_existing_decode(dev):
     """Without a score and with G = 1 the call computes what snapkv_decode_attend computes."""
     import kv_cache_compression_gb300 as kv

@@ -71,6 +71,8 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(EvictArgs args) {
   extern __shared__ uint32_t key_smem[];
   __shared__ __align__(16) uint32_t hist[4][256];       // one per digit, read by the whole cluster
   __shared__ __align__(16) uint32_t all[256];
+  __shared__ uint32_t found[3];           // a digit, how many keys of it are kept, and of how many
+  __shared__ int listed;
   __shared__ int counts[3];               // ties, freed slots, staying rows of this CTA's span
   __shared__ int sums_a[kWarps], sums_b[kWarps];
   __shared__ int first_free[kMaxCluster + 1], first_stay[kMaxCluster + 1];
@@ -108,8 +110,11 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(EvictArgs args) {
   const int per = (n + (int)csize - 1) / (int)csize;
   const int s0 = min((int64_t)n, (int64_t)rank * per), s1 = min((int64_t)n, (int64_t)s0 + per);
 
+  int* list = pair_to;        // (free until the pairs are)
+  uint32_t among_16 = 0;
   // The keys arrive while the histograms are cleared; the first digit is counted from them on the way.
   if (tid < 3) counts[tid] = 0;
+  if (tid == 0) listed = 0;
   for (int i = tid; i < 4 * 256; i += THREADS) (&hist[0][0])[i] = 0;
   __syncthreads();
   auto key_of = [&](int s) { return args.keys_in_smem ? key_smem[s - s0] : order_key(score[s]); };
@@ -122,16 +127,25 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(EvictArgs args) {
 
   // ---- the key of rank `keep` from the top, digit by digit; `want` of the keys that share the digits
   // found so far are kept, of `among`. (keep = 0: none, and the search runs to the largest key.)
-  uint32_t prefix = 0, want = (uint32_t)keep, among = 0;
+  uint32_t prefix = 0, want = (uint32_t)keep, among = (uint32_t)n;
   for (int d = 3; d >= 0; --d) {
     const int shift = 8 * d;
-    if (d < 3)
+    auto count = [&](uint32_t key) { atomicAdd(&hist[d][(key >> shift) & 255u], 1u); };
+    if (d == 0 && among_16 <= (uint32_t)kMaxIndex) {
+      for (int i = tid; i < listed; i += THREADS)
+        if ((uint32_t)list[i] >> 8 == prefix) count((uint32_t)list[i]);
+    } else if (d < 3) {
+      if (d == 1) among_16 = among;   // few keys share two digits: they are listed for the last one
+      const bool keep_list = d == 1 && among <= (uint32_t)kMaxIndex;
       for (int s = s0 + tid; s < s1; s += THREADS) {
         const uint32_t key = key_of(s);
-        if (key >> (shift + 8) == prefix) atomicAdd(&hist[d][(key >> shift) & 255u], 1u);
+        if (key >> (shift + 8) == prefix) {
+          count(key);
+          if (keep_list) list[atomicAdd(&listed, 1)] = (int)key;
+        }
       }
+    }
     sync_head();
-    const uint32_t* sum = hist[d];
     if (!alone) {
       for (int i = tid; i < 256; i += THREADS) {
         uint32_t x = 0;
@@ -139,39 +153,40 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(EvictArgs args) {
         all[i] = x;
       }
       __syncthreads();
-      sum = all;
     }
-    // Every warp finds the digit for itself, eight bins a lane from the top.
-    uint32_t bins[8], mine = 0;
-    {
+    if (tid < 32) {   // one warp finds the digit, eight bins a lane from the top
+      const uint32_t* sum = alone ? hist[d] : all;
       const uint4 hi = *reinterpret_cast<const uint4*>(&sum[252 - 8 * lane]), lo = *reinterpret_cast<const uint4*>(&sum[248 - 8 * lane]);
-      bins[0] = hi.w; bins[1] = hi.z; bins[2] = hi.y; bins[3] = hi.x;
-      bins[4] = lo.w; bins[5] = lo.z; bins[6] = lo.y; bins[7] = lo.x;
-    }
+      const uint32_t bins[8] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};
+      uint32_t mine = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) mine += bins[i];
-    uint32_t upto = mine;
+      for (int i = 0; i < 8; ++i) mine += bins[i];
+      uint32_t above = mine;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, upto, off);
-      if (lane >= off) upto += y;
-    }
-    const uint32_t owner = __ballot_sync(0xffffffffu, want > upto - mine && want <= upto);
-    uint32_t digit = 255, next = 0, count = 0, above = upto - mine;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (want > above && want <= above + bins[i]) {
-        digit = 255 - (8 * lane + i);
-        next = want - above;
-        count = bins[i];
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, above, off);
+        if (lane >= off) above += y;
       }
-      above += bins[i];
+      above -= mine;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (want > above && want <= above + bins[i]) {
+          found[0] = 255 - (8 * lane + i);
+          found[1] = want - above;
+          found[2] = bins[i];
+        }
+        above += bins[i];
+      }
+      if (keep == 0 && lane == 0) {
+        found[0] = 255;
+        found[1] = found[2] = 0;
+      }
     }
-    const int from = owner ? __ffs(owner) - 1 : 0;   // none with keep = 0 (lane 0 then has the defaults)
-    prefix = (prefix << 8) | __shfl_sync(0xffffffffu, digit, from);
-    want = __shfl_sync(0xffffffffu, next, from);
-    among = __shfl_sync(0xffffffffu, count, from);
-    // (`all` is written again behind the next digit's first barrier)
+    __syncthreads();
+    prefix = (prefix << 8) | found[0];
+    want = found[1];
+    among = found[2];
+    // (`found` and `all` are written again behind the next digit's first barrier)
   }
 
   // ---- ties before this span, where not all of them stay
@@ -201,7 +216,7 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(EvictArgs args) {
       tie_rank = ties + block_scan<kWarps>(mine, sums_a, &tie_total);
       ties += tie_total;
     }
-    uint32_t stays = 0;   // bit per slot of the run
+    uint32_t marks = 0;   // slots of the run to list: freed below `keep`, staying above
     int mine = 0, total;
     for (int s = t0; s < t1; ++s) {
       const uint32_t key = key_of(s);
@@ -210,20 +225,22 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(EvictArgs args) {
         stay = want > 0 && (!rank_ties || tie_rank < (int)want);
         ++tie_rank;
       }
-      if (stay) stays |= 1u << (s - t0);
-      mine += stay ? (s >= keep ? 1 << 16 : 0) : (s < keep ? 1 : 0);   // two counts of at most run * THREADS < 2^15
+      if (stay != (s < keep)) {
+        marks |= 1u << (s - t0);
+        mine += stay ? 1 << 16 : 1;   // two counts of at most run * THREADS < 2^15
+      }
     }
     int at = block_scan<kWarps>(mine, sums_b, &total);
-    for (int s = t0; s < t1; ++s) {
-      const bool stay = stays >> (s - t0) & 1u;
-      if (!stay && s < keep) {
+    for (; marks; marks &= marks - 1) {
+      const int s = t0 + __ffs(marks) - 1;
+      if (s < keep) {
         const int p = n_free + (at & 0xFFFF);
         if (in_smem)
           pair_to[p] = s;
         else
           slots[s0 + p] = s;
         at += 1;
-      } else if (stay && s >= keep) {
+      } else {
         const int p = n_stay + (at >> 16);
         if (in_smem)
           pair_from[p] = s;
@@ -298,25 +315,22 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(EvictArgs args) {
       }
     }
     __syncthreads();
-    constexpr int kUnroll = 4;
-    const int items = count * 2 * kPieces;
-    for (int u0 = tid; u0 < items; u0 += kUnroll * THREADS) {
-      uint4 x[kUnroll];
+    // A thread has one 16-byte column of K or V (two where a row of both has 64), and every kStep-th pair.
+    constexpr int kCols = 2 * kPieces < 64 ? 2 * kPieces : 32;
+    constexpr int kStep = THREADS / kCols, kUnroll = 4;
+    const int first_pair = tid / kCols;
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        const int u = u0 + i * THREADS;
-        if (u < items) {
-          const int p = u / (2 * kPieces), kv = (u / kPieces) & 1, c = u % kPieces;
-          x[i] = static_cast<const uint4*>(j.rows[kv])[(bh * j.cap + pair_from[p]) * kPieces + c];
-        }
-      }
+    for (int half = 0; half < 2 * kPieces / kCols; ++half) {
+      const int col = half * kCols + tid % kCols, kv = col / kPieces;
+      uint4* rows = static_cast<uint4*>(kv ? j.rows[1] : j.rows[0]) + bh * j.cap * kPieces + col % kPieces;
+      for (int p = first_pair; p < count; p += kUnroll * kStep) {
+        uint4 x[kUnroll];
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        const int u = u0 + i * THREADS;
-        if (u < items) {
-          const int p = u / (2 * kPieces), kv = (u / kPieces) & 1, c = u % kPieces;
-          static_cast<uint4*>(j.rows[kv])[(bh * j.cap + pair_to[p]) * kPieces + c] = x[i];
-        }
+        for (int i = 0; i < kUnroll; ++i)
+          if (p + i * kStep < count) x[i] = rows[(int64_t)pair_from[p + i * kStep] * kPieces];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i)
+          if (p + i * kStep < count) rows[(int64_t)pair_to[p + i * kStep] * kPieces] = x[i];
       }
     }
     __syncthreads();

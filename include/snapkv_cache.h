@@ -42,7 +42,8 @@ extern "C" {
  * dtype    snapkv_dtype of q, k_cache, v_cache and out. Products and sums are of fp32 accuracy: bf16
  *          weights enter the second product as two bf16 parts, fp32 values as three.
  * workspace device, >= snapkv_scored_workspace_size(...) bytes, 256-byte aligned (contents on entry
- *          do not matter); `scored` says whether a score is given (its logits then need most of the room)
+ *          do not matter); `scored` says whether a score is given (its logits then need most of the room).
+ *          Where the size is 0 (short caches; also the answer for invalid sizes) it is not used and may be NULL.
  * Sums run in a fixed order: the same call on the same device gives the same bits.
  */
 SNAPKV_API size_t snapkv_scored_workspace_size(int32_t batch, int32_t q_heads, int32_t heads, int32_t head_dim,
@@ -139,7 +140,7 @@ SNAPKV_API snapkv_status snapkv_q4_decode_attend(const void* q, const snapkv_q4_
  * idx_out  device int32 [B, H, keep + recent] (NULL: not returned): the slot that each slot's row came
  *          from (a sequence that stays as it is gets the identity)
  * workspace device, >= snapkv_evict_workspace_size(...) bytes, 256-byte aligned (contents on entry do not
- *          matter)
+ *          matter); not used, and may be NULL, where that is 0 (short caches; also the answer for invalid sizes)
  */
 SNAPKV_API size_t snapkv_evict_workspace_size(int32_t batch, int32_t heads, int64_t cap);
 SNAPKV_API snapkv_status snapkv_evict(void* k_cache, void* v_cache, int64_t cap, float* score,

@@ -12,7 +12,6 @@ passed in cost less still.
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass
 from functools import lru_cache
 
 import torch
@@ -89,12 +88,15 @@ def _status(t, device):
 
 
 def _room(workspace, need, device):
-    """The caller's workspace or a new one, and its bytes."""
+    """The caller's workspace or a new one (None where nothing is needed), its address and its bytes."""
     if workspace is None:
-        return torch.empty(need, dtype=_BYTE, device=device), need
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=_BYTE, device=device)
+        return workspace, workspace.data_ptr(), need
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _call(name, device, stream, *args):
@@ -116,28 +118,24 @@ def _call(name, device, stream, *args):
         raise SnapKVError(st, name)
 
 
-@dataclass(frozen=True, eq=False)
 class Q4Cache:
     """A K/V cache held in 4 bits (the layout of snapkv_q4_cache): k_codes, v_codes uint8 [B,H,cap,d/2] and
     k_meta, v_meta bfloat16 [B,H,cap,d/64,2] (step h, centre z). 144 bytes per row of K and V at d = 128,
     against 512 in bf16."""
-    k_codes: object
-    k_meta: object
-    v_codes: object
-    v_meta: object
+    __slots__ = ("k_codes", "k_meta", "v_codes", "v_meta", "shape", "device")
 
-    def __post_init__(self):
-        if self.k_codes.dim() != 4 or self.k_codes.shape[-1] not in (32, 64):
+    def __init__(self, k_codes, k_meta, v_codes, v_meta):
+        shape, dev = k_codes.shape, k_codes.device
+        if len(shape) != 4 or shape[3] not in (32, 64):
             raise ValueError("k_codes must be [B, H, cap, d / 2] with d 64 or 128")
-        B, H, cap, half = self.k_codes.shape
-        dev = self.k_codes.device
-        _check("k_codes", self.k_codes, (B, H, cap, half), _BYTE, dev)
-        _check("v_codes", self.v_codes, (B, H, cap, half), _BYTE, dev)
+        B, H, cap, half = shape
+        _check("k_codes", k_codes, shape, _BYTE, dev)
+        _check("v_codes", v_codes, shape, _BYTE, dev)
         meta = (B, H, cap, half * 2 // GROUP, 2)
-        _check("k_meta", self.k_meta, meta, _BF16, dev)
-        _check("v_meta", self.v_meta, meta, _BF16, dev)
-        object.__setattr__(self, "shape", (B, H, cap, 2 * half))   # B, H, cap, d
-        object.__setattr__(self, "device", dev)
+        _check("k_meta", k_meta, meta, _BF16, dev)
+        _check("v_meta", v_meta, meta, _BF16, dev)
+        self.k_codes, self.k_meta, self.v_codes, self.v_meta = k_codes, k_meta, v_codes, v_meta
+        self.shape, self.device = (B, H, cap, 2 * half), dev   # B, H, cap, d
 
     def _struct(self):
         B, H, cap, d = self.shape
@@ -180,8 +178,8 @@ def _attend_args(where, q, shape, dev, len_, score, out, workspace):
         out = torch.empty_like(q)
     else:
         _check("out", out, q.shape, q.dtype, dev)
-    workspace, ws_bytes = _room(workspace, scored_workspace_size(B, q_heads, H, d, cap, score is not None), dev)
-    return q_heads, None if score is None else score.data_ptr(), out, workspace, ws_bytes
+    room = _room(workspace, scored_workspace_size(B, q_heads, H, d, cap, score is not None), dev)
+    return q_heads, None if score is None else score.data_ptr(), out, room
 
 
 def decode_attend_scored(q, k_cache, v_cache, len_, score=None, *, decay=1.0, out=None, workspace=None,
@@ -194,12 +192,12 @@ def decode_attend_scored(q, k_cache, v_cache, len_, score=None, *, decay=1.0, ou
         raise ValueError("k_cache must be [B, H, cap, d]")
     _check("k_cache", k_cache, shape, dtype, dev)
     _check("v_cache", v_cache, shape, dtype, dev)
-    q_heads, score_at, out, workspace, ws_bytes = _attend_args("snapkv_decode_attend_scored", q, shape, dev, len_,
+    q_heads, score_at, out, room = _attend_args("snapkv_decode_attend_scored", q, shape, dev, len_,
                                                                score, out, workspace)
     B, H, cap, d = shape
     _call("snapkv_decode_attend_scored", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), cap,
-          len_.data_ptr(), score_at, decay, out.data_ptr(), B, q_heads, H, d, _code(dtype), workspace.data_ptr(),
-          ws_bytes, _status(dev_status, dev))
+          len_.data_ptr(), score_at, decay, out.data_ptr(), B, q_heads, H, d, _code(dtype), room[1], room[2],
+          _status(dev_status, dev))
     return out
 
 
@@ -207,10 +205,10 @@ def q4_decode_attend(q, cache, len_, score=None, *, decay=1.0, out=None, workspa
                      stream=None):
     """snapkv_q4_decode_attend: decode_attend_scored over a Q4Cache; q and out are bf16 or fp32."""
     dev = cache.device
-    q_heads, score_at, out, workspace, ws_bytes = _attend_args("snapkv_q4_decode_attend", q, cache.shape, dev, len_,
+    q_heads, score_at, out, room = _attend_args("snapkv_q4_decode_attend", q, cache.shape, dev, len_,
                                                                score, out, workspace)
     _call("snapkv_q4_decode_attend", dev, stream, q.data_ptr(), cache._struct(), len_.data_ptr(), score_at, decay,
-          out.data_ptr(), q_heads, _code(q.dtype), workspace.data_ptr(), ws_bytes, _status(dev_status, dev))
+          out.data_ptr(), q_heads, _code(q.dtype), room[1], room[2], _status(dev_status, dev))
     return out
 
 
@@ -278,8 +276,8 @@ def _evict_args(shape, dev, score, len_in, len_out, keep, recent, idx_out, want_
         _check("idx_out", idx_out, (B, H, left), _INT32, dev)
     elif want_idx and left > 0:
         idx_out = torch.empty((B, H, left), dtype=_INT32, device=dev)
-    workspace, ws_bytes = _room(workspace, evict_workspace_size(B, H, cap), dev)
-    return len_out, idx_out, None if idx_out is None else idx_out.data_ptr(), workspace, ws_bytes
+    room = _room(workspace, evict_workspace_size(B, H, cap), dev)
+    return len_out, idx_out, None if idx_out is None else idx_out.data_ptr(), room
 
 
 def evict(k_cache, v_cache, score, len_in, len_out=None, *, keep, recent, idx_out=None, want_idx=True,
@@ -292,12 +290,12 @@ def evict(k_cache, v_cache, score, len_in, len_out=None, *, keep, recent, idx_ou
         raise ValueError("k_cache must be [B, H, cap, d]")
     _check("k_cache", k_cache, shape, dtype, dev)
     _check("v_cache", v_cache, shape, dtype, dev)
-    len_out, idx_out, idx_at, workspace, ws_bytes = _evict_args(shape, dev, score, len_in, len_out, keep, recent,
+    len_out, idx_out, idx_at, room = _evict_args(shape, dev, score, len_in, len_out, keep, recent,
                                                                 idx_out, want_idx, workspace)
     B, H, cap, d = shape
     _call("snapkv_evict", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), cap, score.data_ptr(),
-          len_in.data_ptr(), len_out.data_ptr(), keep, recent, idx_at, B, H, d, _code(dtype), workspace.data_ptr(),
-          ws_bytes, _status(dev_status, dev))
+          len_in.data_ptr(), len_out.data_ptr(), keep, recent, idx_at, B, H, d, _code(dtype), room[1], room[2],
+          _status(dev_status, dev))
     return len_out, idx_out
 
 
@@ -305,8 +303,8 @@ def q4_evict(cache, score, len_in, len_out=None, *, keep, recent, idx_out=None, 
              dev_status=None, stream=None):
     """snapkv_q4_evict: evict for a Q4Cache."""
     dev = cache.device
-    len_out, idx_out, idx_at, workspace, ws_bytes = _evict_args(cache.shape, dev, score, len_in, len_out, keep,
+    len_out, idx_out, idx_at, room = _evict_args(cache.shape, dev, score, len_in, len_out, keep,
                                                                 recent, idx_out, want_idx, workspace)
     _call("snapkv_q4_evict", dev, stream, cache._struct(), score.data_ptr(), len_in.data_ptr(), len_out.data_ptr(),
-          keep, recent, idx_at, workspace.data_ptr(), ws_bytes, _status(dev_status, dev))
+          keep, recent, idx_at, room[1], room[2], _status(dev_status, dev))
     return len_out, idx_out

@@ -41,10 +41,6 @@
 namespace snapkv {
 namespace {
 
-// Caches of up to this many rows leave a head to one CTA, in one launch: 4 heads of 83 fp32 rows take 5.9 us so
-// and 9.0 in two launches, 4 heads of 1000 4-bit rows 12.0 and 8.0.
-constexpr int kDirectRows = 256;
-
 struct AttendArgs {
   const void* q;
   const uint8_t* k;
@@ -202,7 +198,9 @@ template <bool Q4, typename IO, int D> struct Shape {
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kCtasPerSm = Q4 ? (kWide ? 2 : 3) : kRow >= 512 ? 1 : 2;   // what the ring leaves room for
-  static constexpr int smem(int tile_q) { return kRing + kWarps * tile_q * D * 4; }
+  static constexpr int smem(int tile_q, bool direct) {   // and a direct head's logits
+    return kRing + kWarps * tile_q * D * 4 + (direct ? tile_q * kDirectRows * 4 : 0);
+  }
 };
 
 // 16-byte pieces of a row are stored XORed with the row's low three bits where rows are a multiple of
@@ -424,7 +422,7 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
     const int64_t q0 = bh * a.group + (int64_t)pass * a.tile_q;
     const int64_t seg_end = min(end, at + (here.tiles - here.tile));
     const int n = here.rows;
-    float* logits = a.score ? a.logits + vh * a.tile_q * a.logit_stride : nullptr;
+    float* logits = !a.score ? nullptr : a.direct ? meet + S::kWarps * a.tile_q * D : a.logits + vh * a.tile_q * a.logit_stride;
 
     // B operands of the first product: channels c .. c + 3 of the query of column j for each step, as the
     // lane's share of the rows is laid out (see `first product` below).
@@ -1065,17 +1063,18 @@ cudaError_t launch_typed(const AttendJob& job) {
   a.group = job.q_heads / job.heads;
   a.passes = L.passes;
   a.tile_q = L.tile_q;
-  a.parts = reinterpret_cast<float*>(ws + L.parts);
+  a.parts = reinterpret_cast<float*>(ws + L.parts);   // (no workspace, and none of these, for a direct call)
   a.stats = reinterpret_cast<float*>(ws + L.stats);
   a.logits = reinterpret_cast<float*>(ws + L.logits);
   a.logit_stride = L.logit_stride;
   a.dev_status = job.dev_status;
   // One wave of CTAs, or fewer where their warps would have no tile each.
-  const int smem = S::smem(L.tile_q);
-  cudaError_t err = allow_dynamic_smem<attend_kernel<Q4, IO, D, FOUR>>(S::smem(kQueryTile));
+  a.direct = L.direct;
+  const int smem = S::smem(L.tile_q, L.direct);
+  cudaError_t err = allow_dynamic_smem<attend_kernel<Q4, IO, D, FOUR>>(S::smem(kQueryTile, true));
   if (err != cudaSuccess) return err;
   static std::atomic<int> occupancy[kQueryTile + 1];   // CTAs per SM by tile_q (0: not asked yet)
-  int resident = occupancy[L.tile_q].load(std::memory_order_relaxed);
+  int resident = L.direct ? 1 : occupancy[L.tile_q].load(std::memory_order_relaxed);
   if (resident < 1) {
     err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, attend_kernel<Q4, IO, D, FOUR>, S::kThreads, smem);
     if (err != cudaSuccess) return err;
@@ -1083,8 +1082,6 @@ cudaError_t launch_typed(const AttendJob& job) {
     occupancy[L.tile_q].store(resident, std::memory_order_relaxed);
   }
   const int64_t heads = (int64_t)job.batch * job.heads * L.passes;
-  // Short caches: a CTA per head, in one launch.
-  a.direct = job.cap <= kDirectRows && L.passes == 1;
   const int64_t tiles = heads * ((job.cap + S::kTile - 1) / S::kTile);
   int64_t ctas = (int64_t)device_sm_count() * resident;
   if (ctas > (tiles + kWarps - 1) / kWarps) ctas = (tiles + kWarps - 1) / kWarps;
@@ -1129,6 +1126,7 @@ AttendLayout attend_layout(int batch, int q_heads, int heads, int head_dim, int6
   const int group = q_heads / heads;
   L.tile_q = group < kQueryTile ? group : kQueryTile;
   L.passes = (group + kQueryTile - 1) / kQueryTile;
+  L.direct = cap <= kDirectRows && L.passes == 1;
   const size_t vh = (size_t)batch * heads * L.passes;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   // No more CTAs than there can be tiles for their warps (the smallest tile has 16 rows).
@@ -1137,8 +1135,11 @@ AttendLayout attend_layout(int batch, int q_heads, int heads, int head_dim, int6
   L.parts = 0;
   L.stats = L.parts + up((size_t)L.max_ctas * 2 * L.tile_q * (head_dim + 2) * sizeof(float));
   L.logits = L.stats + up(vh * 2 * L.tile_q * sizeof(float));
-  L.logit_stride = (cap + 7) / 8 * 8;
-  L.total = L.logits + (scored ? up(vh * (size_t)L.logit_stride * L.tile_q * sizeof(float)) : 0);
+  L.logit_stride = L.direct ? kDirectRows : (cap + 7) / 8 * 8;
+  if (L.direct)   // shared memory holds everything
+    L.total = 0;
+  else
+    L.total = L.logits + (scored ? up(vh * (size_t)L.logit_stride * L.tile_q * sizeof(float)) : 0);
   return L;
 }
 

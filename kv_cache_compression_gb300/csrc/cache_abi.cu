@@ -60,7 +60,7 @@ snapkv_status run_attend(AttendJob& job, size_t kv_bytes, size_t kv_meta_bytes, 
     return SNAPKV_ERR_INVALID_ARG;
   const size_t need =
       attend_layout(job.batch, job.q_heads, job.heads, job.head_dim, job.cap, job.score != nullptr).total;
-  if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)) return SNAPKV_ERR_WORKSPACE;
+  if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u))) return SNAPKV_ERR_WORKSPACE;
   const size_t q_bytes = (size_t)job.batch * job.q_heads * job.head_dim * elem_bytes(job.dtype);
   const Span spans[] = {{job.q, q_bytes, false},
                         {job.k, kv_bytes, false},
@@ -70,7 +70,7 @@ snapkv_status run_attend(AttendJob& job, size_t kv_bytes, size_t kv_meta_bytes, 
                         {job.len, (size_t)job.batch * 4, false},
                         {job.score, (size_t)job.batch * job.heads * (size_t)job.cap * 4, true},
                         {job.out, q_bytes, true},
-                        {workspace, need, true},
+                        {need ? workspace : nullptr, need, true},
                         {job.dev_status, 4, true}};
   if (!disjoint(spans)) return SNAPKV_ERR_INVALID_ARG;
   job.workspace = workspace;
@@ -87,8 +87,8 @@ snapkv_status run_evict(EvictJob& job, void* workspace, size_t workspace_bytes) 
       !aligned4(job.len_out) || !aligned4(job.idx) || !aligned4(job.dev_status))
     return SNAPKV_ERR_INVALID_ARG;
   const size_t slots = (size_t)job.batch * job.heads * (size_t)job.cap;
-  const size_t need = slots * sizeof(int32_t);
-  if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)) return SNAPKV_ERR_WORKSPACE;
+  const size_t need = evict_slots_bytes(job.batch, job.heads, job.cap);
+  if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u))) return SNAPKV_ERR_WORKSPACE;
   const Span spans[] = {{job.rows[0], slots * job.row_bytes, true},
                         {job.rows[1], slots * job.row_bytes, true},
                         {job.meta[0], slots * job.meta_bytes, true},
@@ -97,7 +97,7 @@ snapkv_status run_evict(EvictJob& job, void* workspace, size_t workspace_bytes) 
                         {job.len, (size_t)job.batch * 4, false},
                         {job.len_out, (size_t)job.batch * 4, true},
                         {job.idx, (size_t)job.batch * job.heads * (size_t)(job.keep + job.recent) * 4, true},
-                        {workspace, need, true},
+                        {need ? workspace : nullptr, need, true},
                         {job.dev_status, 4, true}};
   if (!disjoint(spans)) return SNAPKV_ERR_INVALID_ARG;
   job.slots = static_cast<int32_t*>(workspace);
@@ -253,7 +253,7 @@ snapkv_status snapkv_q4_read(const snapkv_q4_cache* cache, const int32_t* start,
 
 size_t snapkv_evict_workspace_size(int32_t batch, int32_t heads, int64_t cap) {
   if (check_sizes(batch, heads, 64, cap) != SNAPKV_OK) return 0;
-  return up256((size_t)batch * heads * (size_t)cap * sizeof(int32_t));
+  return up256(evict_slots_bytes(batch, heads, cap));
 }
 
 snapkv_status snapkv_evict(void* k_cache, void* v_cache, int64_t cap, float* score, const int32_t* len_in,

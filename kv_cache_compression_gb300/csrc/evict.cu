@@ -26,6 +26,7 @@ namespace {
 constexpr int kMaxCluster = 8;
 constexpr int kKeysSmem = 64 * 1024;   // a span's keys stay in shared memory up to this size
 constexpr int kMaxIndex = 1024;        // pairs resolved at a time
+static_assert(kEvictNoListCap <= 2 * kMaxIndex, "min(keep, n - keep) pairs at most");
 constexpr int kRun = 15;               // keys a thread looks at between two scans, at most (odd: no bank conflicts)
 
 struct EvictArgs {
@@ -431,7 +432,7 @@ template <int ROW, int META> cudaError_t launch_typed(const EvictJob& job) {
   const int64_t bh = (int64_t)job.batch * job.heads;
   // CTAs per head: up to one per 2048 candidates, while all heads together fill two per SM.
   int64_t csize = 2 * (int64_t)device_sm_count() / bh;
-  const int64_t most = (job.cap + 2047) / 2048;
+  const int64_t most = (job.cap + kEvictNoListCap - 1) / kEvictNoListCap;
   if (csize > most) csize = most;
   if (csize > kMaxCluster) csize = kMaxCluster;
   if (csize < 1) csize = 1;

@@ -42,13 +42,16 @@ def test_workspace_sizes(lib):
     assert wide[1] - wide[0] == 2 * 64 * 1000 * 4
     assert kc.scored_workspace_size(1, 3, 2, 128, 1000) == 0                          # not a multiple
     assert kc.scored_workspace_size(1, 2, 2, 96, 1000) == 0
-    assert kc.evict_workspace_size(2, 3, 100) == 2560                                  # 2400, in 256s
+    assert kc.scored_workspace_size(2, 8, 4, 128, 256) == 0                            # short: none
+    assert kc.scored_workspace_size(2, 64, 4, 128, 256) > 0                            # unless in several passes
+    assert kc.evict_workspace_size(2, 3, 2048) == 0                                    # short: none
+    assert kc.evict_workspace_size(2, 3, 2049) == 49408                                # 49176, in 256s
     assert kc.evict_workspace_size(2, 3, 0) == 0
     assert kc.evict_workspace_size(65536, 1, 10) == 0
 
 
 def _attend(lib, **kw):
-    a = dict(q=MB, k=2 * MB, v=4 * MB, cap=100, len_=6 * MB, score=7 * MB, decay=1.0, out=8 * MB, B=2, Hq=4, H=2,
+    a = dict(q=MB, k=2 * MB, v=4 * MB, cap=300, len_=6 * MB, score=7 * MB, decay=1.0, out=8 * MB, B=2, Hq=4, H=2,
              d=64, dt=1, ws=9 * MB, wsb=1 << 19, dev=None)
     a.update(kw)
     return lib.snapkv_decode_attend_scored(P(a["q"]), P(a["k"]), P(a["v"]), a["cap"], P(a["len_"]), P(a["score"]),
@@ -78,7 +81,7 @@ def test_attend_refusals(lib, kw, status):
 
 
 def _cache(**kw):
-    a = dict(kc=16 * MB, km=17 * MB, vc=18 * MB, vm=19 * MB, cap=100, B=2, H=2, d=64)
+    a = dict(kc=16 * MB, km=17 * MB, vc=18 * MB, vm=19 * MB, cap=300, B=2, H=2, d=64)
     a.update(kw)
     return kc._Q4Struct(a["kc"], a["km"], a["vc"], a["vm"], a["cap"], a["B"], a["H"], a["d"])
 
@@ -122,15 +125,15 @@ def test_q4_refusals(lib):
 @pytest.mark.parametrize("kw,status", [
     (dict(k=0), sk.ERR_INVALID_ARG), (dict(score=0), sk.ERR_INVALID_ARG), (dict(lin=0), sk.ERR_INVALID_ARG),
     (dict(keep=-1), sk.ERR_INVALID_ARG), (dict(recent=-1), sk.ERR_INVALID_ARG),
-    (dict(keep=0, recent=0), sk.ERR_INVALID_ARG), (dict(keep=96), sk.ERR_INVALID_ARG),
+    (dict(keep=0, recent=0), sk.ERR_INVALID_ARG), (dict(keep=2996), sk.ERR_INVALID_ARG),
     (dict(keep=1 << 62, recent=1 << 62), sk.ERR_INVALID_ARG),
-    (dict(lout=3 * MB), sk.ERR_INVALID_ARG), (dict(idx=4 * MB), sk.ERR_INVALID_ARG), (dict(v=MB), sk.ERR_INVALID_ARG),
-    (dict(ws=0), sk.ERR_WORKSPACE), (dict(wsb=1599), sk.ERR_WORKSPACE), (dict(ws=7 * MB + 128), sk.ERR_WORKSPACE),
+    (dict(lout=3 * MB), sk.ERR_INVALID_ARG), (dict(idx=4 * MB), sk.ERR_INVALID_ARG), (dict(v=10 * MB), sk.ERR_INVALID_ARG),
+    (dict(ws=0), sk.ERR_WORKSPACE), (dict(wsb=47999), sk.ERR_WORKSPACE), (dict(ws=7 * MB + 128), sk.ERR_WORKSPACE),
     (dict(ws=5 * MB), sk.ERR_INVALID_ARG), (dict(d=80), sk.ERR_UNSUPPORTED), (dict(dt=9), sk.ERR_INVALID_ARG),
 ])
 def test_evict_refusals(lib, kw, status):
-    a = dict(k=MB, v=2 * MB, cap=100, score=5 * MB, lin=3 * MB, lout=4 * MB, keep=50, recent=5, idx=6 * MB, d=64, dt=1,
-             ws=7 * MB, wsb=1600)
+    a = dict(k=10 * MB, v=20 * MB, cap=3000, score=5 * MB, lin=3 * MB, lout=4 * MB, keep=50, recent=5, idx=6 * MB, d=64,
+             dt=1, ws=7 * MB, wsb=48000)
     a.update(kw)
     assert lib.snapkv_evict(P(a["k"]), P(a["v"]), a["cap"], P(a["score"]), P(a["lin"]), P(a["lout"]), a["keep"],
                             a["recent"], P(a["idx"]), 2, 2, a["d"], a["dt"], P(a["ws"]), a["wsb"], None, None) == status

@@ -33,7 +33,8 @@ extern "C" {
  * q        device [B, Hq, d]
  * k_cache, v_cache  device [B, H, cap, d]; rows at or past len[b] are not used, whatever they hold
  * len      device int32 [B]; len[b] > cap is clamped to cap and reported as SNAPKV_ERR_CAPACITY;
- *          len[b] <= 0 gives o = 0 and leaves the scores as they were
+ *          len[b] <= 0 gives o = 0 and leaves the scores as they were (a query whose logits are all -inf
+ *          gives o = 0 too, and adds nothing)
  * score    device fp32 [B, H, cap] (NULL: not accumulated). Entries at or past len[b] are left as
  *          they were, so a caller clears the array once; snapkv_evict keeps them cleared.
  * decay    in [0, 1]: 1 accumulates plain sums; 0 stores this step's weights alone (the old entries

@@ -12,7 +12,7 @@ passed in cost less still.
 from __future__ import annotations
 
 import ctypes
-from functools import lru_cache
+from functools import lru_cache, wraps
 
 import torch
 
@@ -99,8 +99,20 @@ def _room(workspace, need, device):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _call(name, device, stream, *args):
-    """Calls a library function with `device` current (kernels launch there) and the stream last."""
+def _on_stream(f):
+    """Adds the ``stream`` argument: the whole call runs with that stream current, so that what it allocates
+    belongs to the stream that uses it."""
+    @wraps(f)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return f(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return f(*args, **kwargs)
+    return call
+
+
+def _call(name, device, *args):
+    """Calls a library function with `device` current (kernels launch there) on the device's current stream."""
     if device.type != "cuda":
         raise ValueError(f"{name} needs CUDA tensors, not {device}")
     f = _functions.get(name)
@@ -108,7 +120,7 @@ def _call(name, device, stream, *args):
         lib()
         f = _functions[name]
     index = device.index
-    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    handle = torch._C._cuda_getCurrentRawStream(index)
     if torch._C._cuda_getDevice() == index:
         st = f(*args, handle)
     else:
@@ -182,8 +194,9 @@ def _attend_args(where, q, shape, dev, len_, score, out, workspace):
     return q_heads, None if score is None else score.data_ptr(), out, room
 
 
+@_on_stream
 def decode_attend_scored(q, k_cache, v_cache, len_, score=None, *, decay=1.0, out=None, workspace=None,
-                         dev_status=None, stream=None):
+                         dev_status=None):
     """snapkv_decode_attend_scored: q [B,Hq,d] over rows < len_[b] of k_cache, v_cache [B,H,cap,d] (Hq a
     multiple of H) -> out [B,Hq,d]. ``score`` fp32 [B,H,cap], if given, becomes decay * score + the
     attention each row received, in place (rows < len_[b] only; clear it before the first step)."""
@@ -195,19 +208,19 @@ def decode_attend_scored(q, k_cache, v_cache, len_, score=None, *, decay=1.0, ou
     q_heads, score_at, out, room = _attend_args("snapkv_decode_attend_scored", q, shape, dev, len_,
                                                                score, out, workspace)
     B, H, cap, d = shape
-    _call("snapkv_decode_attend_scored", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), cap,
+    _call("snapkv_decode_attend_scored", dev, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), cap,
           len_.data_ptr(), score_at, decay, out.data_ptr(), B, q_heads, H, d, _code(dtype), room[1], room[2],
           _status(dev_status, dev))
     return out
 
 
-def q4_decode_attend(q, cache, len_, score=None, *, decay=1.0, out=None, workspace=None, dev_status=None,
-                     stream=None):
+@_on_stream
+def q4_decode_attend(q, cache, len_, score=None, *, decay=1.0, out=None, workspace=None, dev_status=None):
     """snapkv_q4_decode_attend: decode_attend_scored over a Q4Cache; q and out are bf16 or fp32."""
     dev = cache.device
     q_heads, score_at, out, room = _attend_args("snapkv_q4_decode_attend", q, cache.shape, dev, len_,
                                                                score, out, workspace)
-    _call("snapkv_q4_decode_attend", dev, stream, q.data_ptr(), cache._struct(), len_.data_ptr(), score_at, decay,
+    _call("snapkv_q4_decode_attend", dev, q.data_ptr(), cache._struct(), len_.data_ptr(), score_at, decay,
           out.data_ptr(), q_heads, _code(q.dtype), room[1], room[2], _status(dev_status, dev))
     return out
 
@@ -220,7 +233,8 @@ def _new_lengths(len_in, len_out, batch, dev):
     return len_out
 
 
-def q4_append(cache, k_new, v_new, len_in, len_out=None, *, n_new=None, dev_status=None, stream=None):
+@_on_stream
+def q4_append(cache, k_new, v_new, len_in, len_out=None, *, n_new=None, dev_status=None):
     """snapkv_q4_append: quantises k_new, v_new [B,H,rows,d] (or [B,H,d], one row) into rows len_in[b] on of a
     Q4Cache, n_new[b] of them if given. Returns len_out [B] (len_in is only read)."""
     B, H, _, d = cache.shape
@@ -236,13 +250,14 @@ def q4_append(cache, k_new, v_new, len_in, len_out=None, *, n_new=None, dev_stat
     if n_new is not None:
         _check("n_new", n_new, (B,), _INT32, dev)
     len_out = _new_lengths(len_in, len_out, B, dev)
-    _call("snapkv_q4_append", dev, stream, cache._struct(), k_new.data_ptr(), v_new.data_ptr(), rows,
+    _call("snapkv_q4_append", dev, cache._struct(), k_new.data_ptr(), v_new.data_ptr(), rows,
           None if n_new is None else n_new.data_ptr(), len_in.data_ptr(), len_out.data_ptr(), _code(dtype),
           _status(dev_status, dev))
     return len_out
 
 
-def q4_read(cache, rows, *, start=None, dtype=None, k_out=None, v_out=None, stream=None):
+@_on_stream
+def q4_read(cache, rows, *, start=None, dtype=None, k_out=None, v_out=None):
     """snapkv_q4_read: the values (dtype: bf16 or fp32, default bf16) that rows start[b] .. start[b] + rows - 1
     of a Q4Cache stand for, as k, v [B,H,rows,d]; rows outside the cache are zeros."""
     B, H, _, d = cache.shape
@@ -261,7 +276,7 @@ def q4_read(cache, rows, *, start=None, dtype=None, k_out=None, v_out=None, stre
         v_out = torch.empty_like(k_out)
     else:
         _check("v_out", v_out, shape, dtype, dev)
-    _call("snapkv_q4_read", dev, stream, cache._struct(), None if start is None else start.data_ptr(), shape[2],
+    _call("snapkv_q4_read", dev, cache._struct(), None if start is None else start.data_ptr(), shape[2],
           k_out.data_ptr(), v_out.data_ptr(), code)
     return k_out, v_out
 
@@ -280,8 +295,9 @@ def _evict_args(shape, dev, score, len_in, len_out, keep, recent, idx_out, want_
     return len_out, idx_out, None if idx_out is None else idx_out.data_ptr(), room
 
 
+@_on_stream
 def evict(k_cache, v_cache, score, len_in, len_out=None, *, keep, recent, idx_out=None, want_idx=True,
-          workspace=None, dev_status=None, stream=None):
+          workspace=None, dev_status=None):
     """snapkv_evict: brings sequences of more than keep + recent rows down to the ``keep`` rows of largest score
     and the newest ``recent``, per head and in place (k_cache, v_cache [B,H,cap,d], score [B,H,cap]). Returns
     (len_out [B], idx [B,H,keep+recent] or None): the new lengths and the slot each row came from."""
@@ -293,18 +309,19 @@ def evict(k_cache, v_cache, score, len_in, len_out=None, *, keep, recent, idx_ou
     len_out, idx_out, idx_at, room = _evict_args(shape, dev, score, len_in, len_out, keep, recent,
                                                                 idx_out, want_idx, workspace)
     B, H, cap, d = shape
-    _call("snapkv_evict", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), cap, score.data_ptr(),
+    _call("snapkv_evict", dev, k_cache.data_ptr(), v_cache.data_ptr(), cap, score.data_ptr(),
           len_in.data_ptr(), len_out.data_ptr(), keep, recent, idx_at, B, H, d, _code(dtype), room[1], room[2],
           _status(dev_status, dev))
     return len_out, idx_out
 
 
+@_on_stream
 def q4_evict(cache, score, len_in, len_out=None, *, keep, recent, idx_out=None, want_idx=True, workspace=None,
-             dev_status=None, stream=None):
+             dev_status=None):
     """snapkv_q4_evict: evict for a Q4Cache."""
     dev = cache.device
     len_out, idx_out, idx_at, room = _evict_args(cache.shape, dev, score, len_in, len_out, keep,
                                                                 recent, idx_out, want_idx, workspace)
-    _call("snapkv_q4_evict", dev, stream, cache._struct(), score.data_ptr(), len_in.data_ptr(), len_out.data_ptr(),
+    _call("snapkv_q4_evict", dev, cache._struct(), score.data_ptr(), len_in.data_ptr(), len_out.data_ptr(),
           keep, recent, idx_at, room[1], room[2], _status(dev_status, dev))
     return len_out, idx_out

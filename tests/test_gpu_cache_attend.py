@@ -336,3 +336,34 @@ def test_two_calls_at_once(dev):
         torch.cuda.synchronize()
         for (o, s), (wo, ws) in zip(got, want):
             assert torch.equal(o, wo) and torch.equal(s, ws)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_buffers_of_a_call_on_another_stream_are_not_reused_early(dev, q4):
+    """The workspace that a call on a side stream allocates is free for that stream alone: memory taken and
+    overwritten on the current stream right after the call must not be it."""
+    import kv_cache_compression_gb300 as kv
+    g = torch.Generator().manual_seed(12)
+    q, k, v, n, score = (t.to(dev) for t in dense(g, 2, 8, 4, 3000, 64, torch.bfloat16, [3000, 2990], poison=False))
+    cache = kv.Q4Cache.empty(2, 4, 3000, 64, dev)
+    kv.q4_append(cache, k, v, torch.zeros(2, dtype=torch.int32, device=dev))
+
+    def attend(s, **kw):
+        if q4:
+            return kv.q4_decode_attend(q, cache, n, s, **kw)
+        return kv.decode_attend_scored(q, k, v, n, s, **kw)
+    want_s = score.clone()
+    want = attend(want_s)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream(dev)
+    need = kv.scored_workspace_size(2, 8, 4, 64, 3000)
+    s = score.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)                   # some 10 ms: the call's kernels start after what follows
+    out = attend(s, stream=side)
+    for _ in range(4):
+        torch.empty(need, dtype=torch.uint8, device=dev).fill_(0xFF)
+        torch.empty_like(q).fill_(7.0)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(s, want_s)

@@ -184,20 +184,20 @@ template <> __device__ __forceinline__ void store1<__nv_bfloat16>(__nv_bfloat16*
 constexpr float kQ4QEven = 0x1p62f, kQ4QOdd = 0x1p64f, kQ4Dot = 0x1p69f;
 constexpr float kQ4P = 0x1p80f, kQ4OutEven = 0x1p51f, kQ4OutOdd = 0x1p53f;
 
-// Format Q4 (codes and pairs) or dense rows of IO; IO is the type of q and out.
-template <bool Q4, typename IO, int D> struct Shape {
+// Format Q4 (codes and pairs) or dense rows of IO; IO is the type of q and out; QT: tiles of eight queries.
+template <bool Q4, typename IO, int D, int QT> struct Shape {
   static constexpr bool kWide = sizeof(IO) == 4;                    // fp32: three bf16 parts
   static constexpr int kParts = kWide ? 3 : 2;                      // of a weight
   static constexpr int kNg = D / kQ4Group;
   static constexpr int kRow = Q4 ? D / 2 : D * (int)sizeof(IO);     // bytes of a row of K (and of V)
   static constexpr int kMeta = Q4 ? 4 * kNg : 0;
-  static constexpr int kTile = Q4 ? 64 : (kRow >= 256 ? 16 : 32);   // rows
+  static constexpr int kTile = Q4 ? (QT == 1 ? 64 : 32) : (kRow >= 256 ? 16 : 32);   // rows
   static constexpr int kStage = 2 * kTile * (kRow + kMeta);         // 4 to 16 KB of K and V together
   static constexpr int kStages = Q4 ? 2 : 3;
   static constexpr int kWarps = snapkv::kWarps;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kCtasPerSm = Q4 ? (kWide ? 2 : 3) : kRow >= 512 ? 1 : 2;   // what the ring leaves room for
+  static constexpr int kCtasPerSm = Q4 ? (kWide || QT > 1 ? 2 : 3) : kRow >= 512 ? 1 : 2;   // what the ring leaves room for
   static constexpr int smem(int tile_q, bool direct) {   // and a direct head's logits
     return kRing + kWarps * tile_q * D * 4 + (direct ? tile_q * kDirectRows * 4 : 0);
   }
@@ -251,18 +251,20 @@ __device__ __forceinline__ bool wait_for(int* value, int x) {
 // FOUR (bf16, at most four queries a pass): the second product's columns 4 .. 7 are the second parts of
 // the weights in columns 0 .. 3, and one instruction does for both. The first product then has every
 // query twice.
-template <bool Q4, typename IO, int D, bool FOUR>
-__global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::kCtasPerSm) attend_kernel(AttendArgs a) {
-  using S = Shape<Q4, IO, D>;
-  static_assert(!FOUR || !S::kWide, "two parts");
+// QT = 2 (bf16): sixteen queries a pass share the work on each row's operands.
+template <bool Q4, typename IO, int D, int QT, bool FOUR>
+__global__ void __launch_bounds__(Shape<Q4, IO, D, QT>::kThreads, Shape<Q4, IO, D, QT>::kCtasPerSm) attend_kernel(AttendArgs a) {
+  using S = Shape<Q4, IO, D, QT>;
+  static_assert(!FOUR || (!S::kWide && QT == 1), "two parts of four queries");
+  static_assert(QT == 1 || !S::kWide, "registers");
   constexpr int kParts = FOUR ? 1 : S::kParts;
   constexpr int kSteps = D / 16;          // 16-channel steps of the first product
   constexpr int kPairs = D / 16;          // 16-channel tiles of the second: two of a lane's D / 8 channels
   constexpr int kSub = S::kTile / 16;     // 16-row parts of a tile
   constexpr int kNg = S::kNg;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float warp_m[S::kWarps][kQueryTile], warp_l[S::kWarps][kQueryTile];
-  __shared__ float head_m[kQueryTile], head_r[kQueryTile];
+  __shared__ float warp_m[S::kWarps][8 * QT], warp_l[S::kWarps][8 * QT];
+  __shared__ float head_m[8 * QT], head_r[8 * QT];
   __shared__ int arrived, merged;   // warps whose part of this head is in `meet`; heads merged
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -426,10 +428,11 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
 
     // B operands of the first product: channels c .. c + 3 of the query of column j for each step, as the
     // lane's share of the rows is laid out (see `first product` below).
-    const int qcol = FOUR ? j % 4 : j;
-    uint32_t qb[kSteps][S::kWide ? 6 : 2];
-    float qsum[Q4 ? kNg : 1][2];   // per group, of queries qa and qa + 1
-    {
+    uint32_t qb[QT][kSteps][S::kWide ? 6 : 2];
+    float qsum[QT][Q4 ? kNg : 1][2];   // per group, of queries qa and qa + 1
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      const int qcol = 8 * t + (FOUR ? j % 4 : j);
       const IO* qp = static_cast<const IO*>(a.q) + (q0 + (qcol < tile_q ? qcol : 0)) * D;
       float sum[Q4 ? kNg : 1] = {};
 #pragma unroll
@@ -457,8 +460,8 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
         }
 #pragma unroll
         for (int part = 0; part < (S::kWide ? 3 : 1); ++part) {
-          qb[s][2 * part] = split2(x);
-          qb[s][2 * part + 1] = split2(y);
+          qb[t][s][2 * part] = split2(x);
+          qb[t][s][2 * part + 1] = split2(y);
         }
       }
       if constexpr (Q4) {
@@ -467,23 +470,26 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
           sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
           sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
           sum[g] *= a.scale_log2;
-          qsum[g][0] = __shfl_sync(0xffffffffu, sum[g], 4 * qa);
-          qsum[g][1] = __shfl_sync(0xffffffffu, sum[g], 4 * qa + 4);
+          qsum[t][g][0] = __shfl_sync(0xffffffffu, sum[g], 4 * qa);
+          qsum[t][g][1] = __shfl_sync(0xffffffffu, sum[g], 4 * qa + 4);
         }
       }
     }
     const float dot_scale = Q4 ? a.scale_log2 * kQ4Dot : a.scale_log2;
 
-    // Per query qa, qa + 1:
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // Per query qa, qa + 1 of each tile of queries:
+    float m[QT][2], l[QT][2];
     // Channel pair t of the lane: [0], [1] its first channel for queries qa, qa + 1; [2], [3] its second.
-    float o[kPairs][4];
+    float o[QT][kPairs][4];
+    float oz[QT][Q4 ? kNg : 1][2];   // sum of p z over this lane's rows
 #pragma unroll
-    for (int t = 0; t < kPairs; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-    float oz[Q4 ? kNg : 1][2];   // sum of p z over this lane's rows
-    if constexpr (Q4) {
+    for (int q = 0; q < QT; ++q) {
+      m[q][0] = m[q][1] = -INFINITY;
+      l[q][0] = l[q][1] = 0.f;
 #pragma unroll
-      for (int g = 0; g < kNg; ++g) oz[g][0] = oz[g][1] = 0.f;
+      for (int t = 0; t < kPairs; ++t) o[q][t][0] = o[q][t][1] = o[q][t][2] = o[q][t][3] = 0.f;
+#pragma unroll
+      for (int g = 0; g < (Q4 ? kNg : 1); ++g) oz[q][g][0] = oz[q][g][1] = 0.f;
     }
 
     // First product: B in one part (bf16), or three (fp32: the small parts' products have an accumulator of
@@ -523,7 +529,7 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
       const int base = (here.tile + (int)(mine_at - at)) * S::kTile;
 
       // ---- first product: logits of kSub x 16 rows
-      float sv[kSub][4];   // row j of a part for queries qa, qa + 1, then row j + 8
+      float sv[QT][kSub][4];   // row j of a part for queries qa, qa + 1, then row j + 8
 #pragma unroll
       for (int sub = 0; sub < kSub; ++sub) {
         if constexpr (Q4) {
@@ -543,10 +549,10 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
               w[half][0] = x.x; w[half][1] = x.y;
             }
           }
-          float d[4] = {}, zq[4] = {};
+          float d[QT][4] = {}, zq[QT][4] = {};
 #pragma unroll
           for (int g = 0; g < kNg; ++g) {
-            float dot[4] = {}, small[4] = {};
+            float dot[QT][4] = {}, small[QT][4] = {};
 #pragma unroll
             for (int o2 = 0; o2 < 2; ++o2) {
               uint32_t e[2][4];
@@ -555,17 +561,24 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
                 const uint32_t word = w[half][q4_word<kNg>(g, o2)];
                 q4_operands(ones, word, prmt(word, word, 0x2301), e[half]);
               }
-              mma_q(dot, small, qb[4 * g + 2 * o2], e[0][0], e[1][0], e[0][1], e[1][1]);
-              mma_q(dot, small, qb[4 * g + 2 * o2 + 1], e[0][2], e[1][2], e[0][3], e[1][3]);
+#pragma unroll
+              for (int q = 0; q < QT; ++q) {
+                mma_q(dot[q], small[q], qb[q][4 * g + 2 * o2], e[0][0], e[1][0], e[0][1], e[1][1]);
+                mma_q(dot[q], small[q], qb[q][4 * g + 2 * o2 + 1], e[0][2], e[1][2], e[0][3], e[1][3]);
+              }
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              d[e] = fmaf(hz[e / 2][g].x, S::kWide ? dot[e] + small[e] : dot[e], d[e]);
-              zq[e] = fmaf(hz[e / 2][g].y, qsum[g][e % 2], zq[e]);
-            }
+            for (int q = 0; q < QT; ++q)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                d[q][e] = fmaf(hz[e / 2][g].x, S::kWide ? dot[q][e] + small[q][e] : dot[q][e], d[q][e]);
+                zq[q][e] = fmaf(hz[e / 2][g].y, qsum[q][g][e % 2], zq[q][e]);
+              }
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sv[sub][e] = fmaf(d[e], dot_scale, zq[e]);
+          for (int q = 0; q < QT; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sv[q][sub][e] = fmaf(d[q][e], dot_scale, zq[q][e]);
         } else if constexpr (S::kWide) {
           float dot[4] = {}, small[4] = {};
 #pragma unroll
@@ -582,89 +595,100 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
               const uint32_t a0 = split2(f[0][0]), a1 = split2(f[1][0]), a2 = split2(f[0][1]), a3 = split2(f[1][1]);
 #pragma unroll
               for (int part = 0; part < 3 - kp; ++part)
-                mma16816(kp + part ? small : dot, a0, a1, a2, a3, qb[s4][2 * part], qb[s4][2 * part + 1]);
+                mma16816(kp + part ? small : dot, a0, a1, a2, a3, qb[0][s4][2 * part], qb[0][s4][2 * part + 1]);
             }
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sv[sub][e] = (dot[e] + small[e]) * dot_scale;
+          for (int e = 0; e < 4; ++e) sv[0][sub][e] = (dot[e] + small[e]) * dot_scale;
         } else {
-          float dot[4] = {};
+          float dot[QT][4] = {};
 #pragma unroll
           for (int s4 = 0; s4 < kSteps; ++s4) {
             // matrices: rows 0 .. 7 and 8 .. 15 of the step's first eight channels, then of the others
             uint32_t x[4];
             load_matrices<false>(kt + piece_at<S::kRow>(16 * sub + lane % 16, 2 * s4 + lane / 16), x);
-            mma_q(dot, dot, qb[s4], x[0], x[1], x[2], x[3]);
+#pragma unroll
+            for (int q = 0; q < QT; ++q) mma_q(dot[q], dot[q], qb[q][s4], x[0], x[1], x[2], x[3]);
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sv[sub][e] = dot[e] * dot_scale;
+          for (int q = 0; q < QT; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sv[q][sub][e] = dot[q][e] * dot_scale;
         }
       }
 
       // ---- masks, the running maximum, and the logits that the scores will need
       const int left = n - base - jrow;   // rows 16 sub + 8 half of the tile below this are visible
-      if (base + S::kTile > n) {
+      float2 shift[QT];
 #pragma unroll
-        for (int sub = 0; sub < kSub; ++sub)
+      for (int q = 0; q < QT; ++q) {
+        if (base + S::kTile > n) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (16 * sub + 8 * (e / 2) >= left) sv[sub][e] = -INFINITY;
-      }
-      if (logits && !(FOUR && i >= 2)) {
+          for (int sub = 0; sub < kSub; ++sub)
 #pragma unroll
-        for (int e2 = 0; e2 < 2; ++e2) {
-          float* to = logits + (qa + e2) * a.logit_stride + base + jrow;
-          if (qa + e2 < tile_q) {
+            for (int e = 0; e < 4; ++e)
+              if (16 * sub + 8 * (e / 2) >= left) sv[q][sub][e] = -INFINITY;
+        }
+        if (logits && !(FOUR && i >= 2)) {
 #pragma unroll
-            for (int sub = 0; sub < kSub; ++sub)
+          for (int e2 = 0; e2 < 2; ++e2) {
+            const int qq = 8 * q + qa + e2;
+            float* to = logits + qq * a.logit_stride + base + jrow;
+            if (qq < tile_q) {
 #pragma unroll
-              for (int half = 0; half < 2; ++half)
-                if (16 * sub + 8 * half < left) to[16 * sub + 8 * half] = sv[sub][2 * half + e2];
+              for (int sub = 0; sub < kSub; ++sub)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                  if (16 * sub + 8 * half < left) to[16 * sub + 8 * half] = sv[q][sub][2 * half + e2];
+            }
           }
         }
-      }
-      float top[2] = {m[0], m[1]};
+        float top[2] = {m[q][0], m[q][1]};
 #pragma unroll
-      for (int sub = 0; sub < kSub; ++sub) {
-        top[0] = fmaxf(top[0], fmaxf(sv[sub][0], sv[sub][2]));
-        top[1] = fmaxf(top[1], fmaxf(sv[sub][1], sv[sub][3]));
-      }
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-        top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], off));
-        top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], off));
-      }
-      if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
-        const float c0 = m[0] == -INFINITY ? 0.f : ex2(m[0] - top[0]), c1 = m[1] == -INFINITY ? 0.f : ex2(m[1] - top[1]);
-        l[0] *= c0;
-        l[1] *= c1;
-#pragma unroll
-        for (int t = 0; t < kPairs; ++t) {
-          o[t][0] *= c0; o[t][1] *= c1; o[t][2] *= c0; o[t][3] *= c1;
+        for (int sub = 0; sub < kSub; ++sub) {
+          top[0] = fmaxf(top[0], fmaxf(sv[q][sub][0], sv[q][sub][2]));
+          top[1] = fmaxf(top[1], fmaxf(sv[q][sub][1], sv[q][sub][3]));
         }
-        if constexpr (Q4) {
 #pragma unroll
-          for (int g = 0; g < kNg; ++g) {
-            oz[g][0] *= c0;
-            oz[g][1] *= c1;
+        for (int off = 4; off < 32; off <<= 1) {
+          top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], off));
+          top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], off));
+        }
+        if (__any_sync(0xffffffffu, top[0] > m[q][0] || top[1] > m[q][1])) {
+          const float c0 = m[q][0] == -INFINITY ? 0.f : ex2(m[q][0] - top[0]);
+          const float c1 = m[q][1] == -INFINITY ? 0.f : ex2(m[q][1] - top[1]);
+          l[q][0] *= c0;
+          l[q][1] *= c1;
+#pragma unroll
+          for (int t = 0; t < kPairs; ++t) {
+            o[q][t][0] *= c0; o[q][t][1] *= c1; o[q][t][2] *= c0; o[q][t][3] *= c1;
           }
+          if constexpr (Q4) {
+#pragma unroll
+            for (int g = 0; g < kNg; ++g) {
+              oz[q][g][0] *= c0;
+              oz[q][g][1] *= c1;
+            }
+          }
+          m[q][0] = top[0];
+          m[q][1] = top[1];
         }
-        m[0] = top[0];
-        m[1] = top[1];
+        shift[q] = make_float2(m[q][0] == -INFINITY ? 0.f : -m[q][0], m[q][1] == -INFINITY ? 0.f : -m[q][1]);
       }
-      const float2 shift = make_float2(m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]);
 
       // ---- second product
 #pragma unroll
       for (int sub = 0; sub < kSub; ++sub) {
-        float2 p[2];   // rows j, j + 8
+        float2 p[QT][2];   // rows j, j + 8
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float2 x = add2(make_float2(sv[sub][2 * half], sv[sub][2 * half + 1]), shift);
-          p[half] = make_float2(ex2(x.x), ex2(x.y));
-          l[0] += p[half].x;
-          l[1] += p[half].y;
-        }
+        for (int q = 0; q < QT; ++q)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const float2 x = add2(make_float2(sv[q][sub][2 * half], sv[q][sub][2 * half + 1]), shift[q]);
+            p[q][half] = make_float2(ex2(x.x), ex2(x.y));
+            l[q][0] += p[q][half].x;
+            l[q][1] += p[q][half].y;
+          }
         if constexpr (Q4) {
           float2 hz[2][kNg];
 #pragma unroll
@@ -681,19 +705,24 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
             if constexpr (kNg == 2) w[e][1] = x.y;
           }
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
+          for (int q = 0; q < QT; ++q)
 #pragma unroll
-            for (int g = 0; g < kNg; ++g) {
-              oz[g][0] = fmaf(p[half].x, hz[half][g].y, oz[g][0]);
-              oz[g][1] = fmaf(p[half].y, hz[half][g].y, oz[g][1]);
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+              for (int g = 0; g < kNg; ++g) {
+                oz[q][g][0] = fmaf(p[q][half].x, hz[half][g].y, oz[q][g][0]);
+                oz[q][g][1] = fmaf(p[q][half].y, hz[half][g].y, oz[q][g][1]);
+              }
+              p[q][half] = mul2(p[q][half], make_float2(kQ4P, kQ4P));
             }
-            p[half] = mul2(p[half], make_float2(kQ4P, kQ4P));
-          }
 #pragma unroll
           for (int g = 0; g < kNg; ++g) {
-            float2 ph[2] = {mul2(p[0], make_float2(hz[0][g].x, hz[0][g].x)), mul2(p[1], make_float2(hz[1][g].x, hz[1][g].x))};
-            uint32_t pb[S::kParts][2];
-            weight_parts(ph, pb);
+            uint32_t pb[QT][S::kParts][2];
+#pragma unroll
+            for (int q = 0; q < QT; ++q) {
+              float2 ph[2] = {mul2(p[q][0], make_float2(hz[0][g].x, hz[0][g].x)), mul2(p[q][1], make_float2(hz[1][g].x, hz[1][g].x))};
+              weight_parts(ph, pb[q]);
+            }
             // channels 2 c (odd = 0) and 2 c + 1 of rows 2 i, 2 i + 1 and of rows 2 i + 8, 2 i + 9
             uint32_t lo[2][4], hi[2][4];
 #pragma unroll
@@ -703,21 +732,23 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
               q4_operands(ones, prmt(w[2][g], w[3][g], sel), prmt(w[2][g], w[3][g], swap), hi[odd]);
             }
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float t[4] = {};   // fp32: these rows' sum, from the smallest part, then added with rounding
-              float* acc = S::kWide ? t : o[4 * g + c];
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int part = kParts - 1; part >= 0; --part)
-                mma16816(acc, lo[0][c], lo[1][c], hi[0][c], hi[1][c], pb[part][0], pb[part][1]);
-              if constexpr (S::kWide) {
+              for (int q = 0; q < QT; ++q) {
+                float t[4] = {};   // fp32: these rows' sum, from the smallest part, then added with rounding
+                float* acc = S::kWide ? t : o[q][4 * g + c];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[4 * g + c][e] += t[e];
+                for (int part = kParts - 1; part >= 0; --part)
+                  mma16816(acc, lo[0][c], lo[1][c], hi[0][c], hi[1][c], pb[q][part][0], pb[q][part][1]);
+                if constexpr (S::kWide) {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[q][4 * g + c][e] += t[e];
+                }
               }
-            }
           }
         } else if constexpr (S::kWide) {
           uint32_t pb[S::kParts][2];
-          weight_parts(p, pb);
+          weight_parts(p[0], pb);
 #pragma unroll
           for (int c4 = 0; c4 < kPairs / 2; ++c4) {   // channels 4 of 32 c4 + 4 j on
             float f[4][4];
@@ -745,19 +776,23 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
                 for (int vp = 0; vp <= order; ++vp)
                   mma16816(t, va[vp][0], va[vp][1], va[vp][2], va[vp][3], pb[order - vp][0], pb[order - vp][1]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[2 * c4 + c / 2][e] += t[e];
+              for (int e = 0; e < 4; ++e) o[0][2 * c4 + c / 2][e] += t[e];
             }
           }
         } else {
-          uint32_t pb[S::kParts][2];
-          weight_parts(p, pb);
+          uint32_t pb[QT][S::kParts][2];
+#pragma unroll
+          for (int q = 0; q < QT; ++q) weight_parts(p[q], pb[q]);
 #pragma unroll
           for (int t = 0; t < kPairs; ++t) {
             // transposed matrices: the first and the second eight channels by rows 0 .. 7, then by rows 8 .. 15
             uint32_t x[4];
             load_matrices<true>(vt + piece_at<S::kRow>(16 * sub + lane % 8 + 8 * (lane / 16), 2 * t + (lane / 8) % 2), x);
 #pragma unroll
-            for (int part = 0; part < kParts; ++part) mma16816(o[t], x[0], x[1], x[2], x[3], pb[part][0], pb[part][1]);
+            for (int q = 0; q < QT; ++q)
+#pragma unroll
+              for (int part = 0; part < kParts; ++part)
+                mma16816(o[q][t], x[0], x[1], x[2], x[3], pb[q][part][0], pb[q][part][1]);
           }
         }
       }
@@ -766,48 +801,52 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D>::kThreads, Shape<Q4, IO, D>::
     // ---- the warps meet: each leaves its part, the last to arrive merges them, and the others go on with the
     // next head (at whose end they wait, in case, until this one is merged)
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1)
+    for (int q = 0; q < QT; ++q)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], off);
-        if constexpr (Q4) {
+      for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
-          for (int g = 0; g < kNg; ++g) oz[g][e] += __shfl_xor_sync(0xffffffffu, oz[g][e], off);
+        for (int e = 0; e < 2; ++e) {
+          l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], off);
+          if constexpr (Q4) {
+#pragma unroll
+            for (int g = 0; g < kNg; ++g) oz[q][g][e] += __shfl_xor_sync(0xffffffffu, oz[q][g][e], off);
+          }
         }
-      }
     if constexpr (FOUR) {   // columns 4 .. 7 onto columns 0 .. 3
 #pragma unroll
       for (int t = 0; t < kPairs; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[t][e] += __shfl_xor_sync(0xffffffffu, o[t][e], 2);
+        for (int e = 0; e < 4; ++e) o[0][t][e] += __shfl_xor_sync(0xffffffffu, o[0][t][e], 2);
     }
     if (!wait_for(&merged, segment) && lane == 0) report(a.dev_status, SNAPKV_ERR_TIMEOUT);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int qq = qa + e;
-      if (qq < tile_q && !(FOUR && i >= 2)) {
-        if (j == 0) {
-          warp_m[warp][qq] = m[e];
-          warp_l[warp][qq] = l[e];
-        }
-        float* to = meet + (warp * a.tile_q + qq) * D;
+    for (int q = 0; q < QT; ++q)
 #pragma unroll
-        for (int t = 0; t < kPairs; ++t) {
-          float x = o[t][e], y = o[t][e + 2];
-          int c;   // the pair's first channel
-          if constexpr (Q4) {
-            const int g = t / 4, pair = t % 4;
-            c = 64 * g + 8 * j + 2 * pair;
-            x = fmaf(x, pair & 1 ? kQ4OutOdd : kQ4OutEven, oz[g][e]);
-            y = fmaf(y, pair & 1 ? kQ4OutOdd : kQ4OutEven, oz[g][e]);
-          } else {
-            c = S::kWide ? 32 * (t / 2) + 4 * j + 2 * (t % 2) : 16 * t + j;
+      for (int e = 0; e < 2; ++e) {
+        const int qq = 8 * q + qa + e;
+        if (qq < tile_q && !(FOUR && i >= 2)) {
+          if (j == 0) {
+            warp_m[warp][qq] = m[q][e];
+            warp_l[warp][qq] = l[q][e];
           }
-          to[c] = x;
-          to[c + (Q4 || S::kWide ? 1 : 8)] = y;
+          float* to = meet + (warp * a.tile_q + qq) * D;
+#pragma unroll
+          for (int t = 0; t < kPairs; ++t) {
+            float x = o[q][t][e], y = o[q][t][e + 2];
+            int c;   // the pair's first channel
+            if constexpr (Q4) {
+              const int g = t / 4, pair = t % 4;
+              c = 64 * g + 8 * j + 2 * pair;
+              x = fmaf(x, pair & 1 ? kQ4OutOdd : kQ4OutEven, oz[q][g][e]);
+              y = fmaf(y, pair & 1 ? kQ4OutOdd : kQ4OutEven, oz[q][g][e]);
+            } else {
+              c = S::kWide ? 32 * (t / 2) + 4 * j + 2 * (t % 2) : 16 * t + j;
+            }
+            to[c] = x;
+            to[c + (Q4 || S::kWide ? 1 : 8)] = y;
+          }
         }
       }
-    }
     const bool last = arrive(&arrived) == S::kWarps - 1;
     if (last) {
       const bool whole = here.tile == 0 && seg_end == at + here.tiles;   // the head lies in this share
@@ -907,7 +946,7 @@ __device__ __forceinline__ void join(float& top, float& sum, float m, float l) {
 
 template <typename IO, int D, int TILE>
 __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs a, int out_blocks, int chunks) {
-  __shared__ float head_m[kQueryTile], head_r[kQueryTile];
+  __shared__ float head_m[kMaxQueryTile], head_r[kMaxQueryTile];
   const int tid = threadIdx.x, lane = tid % 32;
   const int per_seq = a.heads * a.passes;
   const bool scores = (int)blockIdx.x >= out_blocks;
@@ -1002,10 +1041,9 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
 #pragma unroll
     for (int q = 0; q < kAtOnce; ++q)
       if (q < tile_q) load(q, x[q]);
-    const int q = tid / 32;   // a warp per query
-    if (q < tile_q) {
+    if (pass > 0) parts = find_parts<D>(a, total, f0 + (int64_t)pass * tiles, tiles);
+    for (int q = tid / 32; q < tile_q; q += kJoinThreads / 32) {   // a warp per query
       float top = -INFINITY, sum = 0.f;
-      if (pass > 0) parts = find_parts<D>(a, total, f0 + (int64_t)pass * tiles, tiles);
       if (parts.more == 0) {
         top = __ldcg(a.stats + vh * 2 * a.tile_q + q);
         sum = __ldcg(a.stats + (vh * 2 + 1) * a.tile_q + q);
@@ -1041,10 +1079,10 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
     if (row + i * kJoinThreads < n) sc[i * kJoinThreads] = w[i];
 }
 
-template <bool Q4, typename IO, int D, bool FOUR>
+template <bool Q4, typename IO, int D, int QT, bool FOUR>
 cudaError_t launch_typed(const AttendJob& job) {
-  using S = Shape<Q4, IO, D>;
-  const AttendLayout L = attend_layout(job.batch, job.q_heads, job.heads, D, job.cap, job.score != nullptr);
+  using S = Shape<Q4, IO, D, QT>;
+  const AttendLayout L = attend_layout(job.batch, job.q_heads, job.heads, D, job.cap, job.score != nullptr, 8 * QT);
   char* ws = static_cast<char*>(job.workspace);
   AttendArgs a;
   a.q = job.q;
@@ -1071,12 +1109,12 @@ cudaError_t launch_typed(const AttendJob& job) {
   // One wave of CTAs, or fewer where their warps would have no tile each.
   a.direct = L.direct;
   const int smem = S::smem(L.tile_q, L.direct);
-  cudaError_t err = allow_dynamic_smem<attend_kernel<Q4, IO, D, FOUR>>(S::smem(kQueryTile, true));
+  cudaError_t err = allow_dynamic_smem<attend_kernel<Q4, IO, D, QT, FOUR>>(S::smem(8 * QT, true));
   if (err != cudaSuccess) return err;
-  static std::atomic<int> occupancy[kQueryTile + 1];   // CTAs per SM by tile_q (0: not asked yet)
+  static std::atomic<int> occupancy[8 * QT + 1];   // CTAs per SM by tile_q (0: not asked yet)
   int resident = L.direct ? 1 : occupancy[L.tile_q].load(std::memory_order_relaxed);
   if (resident < 1) {
-    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, attend_kernel<Q4, IO, D, FOUR>, S::kThreads, smem);
+    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, attend_kernel<Q4, IO, D, QT, FOUR>, S::kThreads, smem);
     if (err != cudaSuccess) return err;
     if (resident < 1) return cudaErrorInvalidConfiguration;
     occupancy[L.tile_q].store(resident, std::memory_order_relaxed);
@@ -1088,7 +1126,7 @@ cudaError_t launch_typed(const AttendJob& job) {
   if (ctas > L.max_ctas) ctas = L.max_ctas;
   if (a.direct) ctas = heads;
   a.ctas = (int)ctas;
-  attend_kernel<Q4, IO, D, FOUR><<<(unsigned)ctas, S::kThreads, smem, job.stream>>>(a);
+  attend_kernel<Q4, IO, D, QT, FOUR><<<(unsigned)ctas, S::kThreads, smem, job.stream>>>(a);
   err = cudaGetLastError();
   if (err != cudaSuccess || a.direct) return err;
   const int64_t chunks = job.score ? (job.cap + kJoinRows - 1) / kJoinRows : 0;
@@ -1110,9 +1148,12 @@ cudaError_t launch_typed(const AttendJob& job) {
 }
 
 template <bool Q4, int D> cudaError_t launch_dim(const AttendJob& job) {
-  if (job.dtype == SNAPKV_F32) return launch_typed<Q4, float, D, false>(job);
-  return job.q_heads / job.heads <= 4 ? launch_typed<Q4, __nv_bfloat16, D, true>(job)
-                                      : launch_typed<Q4, __nv_bfloat16, D, false>(job);
+  const int group = job.q_heads / job.heads;
+  if (job.dtype == SNAPKV_F32) return launch_typed<Q4, float, D, 1, false>(job);
+  // Grouped queries, 8 sequences of 8192 rows and 4 KV heads, bf16 with scores: 16 queries a head take 33 us in one
+  // pass of sixteen and 56 us in two of eight.
+  if (group > 8) return launch_typed<Q4, __nv_bfloat16, D, 2, false>(job);
+  return group <= 4 ? launch_typed<Q4, __nv_bfloat16, D, 1, true>(job) : launch_typed<Q4, __nv_bfloat16, D, 1, false>(job);
 }
 
 template <bool Q4> cudaError_t launch_format(const AttendJob& job) {
@@ -1121,11 +1162,11 @@ template <bool Q4> cudaError_t launch_format(const AttendJob& job) {
 
 }  // namespace
 
-AttendLayout attend_layout(int batch, int q_heads, int heads, int head_dim, int64_t cap, bool scored) {
+AttendLayout attend_layout(int batch, int q_heads, int heads, int head_dim, int64_t cap, bool scored, int most_q) {
   AttendLayout L;
   const int group = q_heads / heads;
-  L.tile_q = group < kQueryTile ? group : kQueryTile;
-  L.passes = (group + kQueryTile - 1) / kQueryTile;
+  L.passes = (group + most_q - 1) / most_q;
+  L.tile_q = (group + L.passes - 1) / L.passes;   // passes of about equal size
   L.direct = cap <= kDirectRows && L.passes == 1;
   const size_t vh = (size_t)batch * heads * L.passes;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
@@ -1141,6 +1182,12 @@ AttendLayout attend_layout(int batch, int q_heads, int heads, int head_dim, int6
   else
     L.total = L.logits + (scored ? up(vh * (size_t)L.logit_stride * L.tile_q * sizeof(float)) : 0);
   return L;
+}
+
+size_t attend_workspace_bytes(int batch, int q_heads, int heads, int head_dim, int64_t cap, bool scored) {
+  const size_t a = attend_layout(batch, q_heads, heads, head_dim, cap, scored, 8).total;    // fp32
+  const size_t b = attend_layout(batch, q_heads, heads, head_dim, cap, scored, 16).total;   // bf16
+  return a > b ? a : b;
 }
 
 cudaError_t launch_attend(const AttendJob& job) {

@@ -23,7 +23,7 @@ template <auto* Kernel> cudaError_t allow_dynamic_smem(int bytes) {
   return err;
 }
 
-constexpr int kQueryTile = 8;   // query heads of one KV head that one pass over its rows serves
+constexpr int kMaxQueryTile = 16;   // query heads of one KV head that one pass over its rows serves, at most
 
 // One scored decode attention, dense (k_meta null: k, v of `dtype`) or over a 4-bit cache.
 struct AttendJob {
@@ -38,7 +38,7 @@ struct AttendJob {
   float* score;         // may be null
   float decay;
   void* out;
-  void* workspace;      // attend_layout(...).total bytes
+  void* workspace;      // attend_workspace_bytes(...)
   int32_t* dev_status;
   cudaStream_t stream;
 };
@@ -57,7 +57,9 @@ constexpr int kDirectRows = 256;
 
 constexpr int kMaxAttendCtas = 1024;   // bounds the workspace, not tied to a device's SM count
 
-AttendLayout attend_layout(int batch, int q_heads, int heads, int head_dim, int64_t cap, bool scored);
+// (for passes of at most `most_q` queries) and the workspace of a call of either type.
+AttendLayout attend_layout(int batch, int q_heads, int heads, int head_dim, int64_t cap, bool scored, int most_q);
+size_t attend_workspace_bytes(int batch, int q_heads, int heads, int head_dim, int64_t cap, bool scored);
 cudaError_t launch_attend(const AttendJob& job);
 
 struct Q4Job {

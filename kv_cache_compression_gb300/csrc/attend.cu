@@ -908,11 +908,10 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D, QT>::kThreads, Shape<Q4, IO, 
 }
 
 // The second launch. The warps of its first blocks each join 64 channels of an output row whose head was
-// cut (or is empty); the other blocks each add the weights of kJoinRows rows to a head's scores. Where a head's
+// cut (or is empty); the other blocks each add the weights of PER rows a thread to a head's scores. Where a head's
 // parts lie follows from the schedule. The kernel is all latency: loads are issued together and early,
 // and registers are kept to what lets four blocks share an SM.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 2048;
 
 // A head's parts: the last segment of one CTA (its slot 1, unless the share starts with the head) and the
 // first of `more` others after it.
@@ -944,8 +943,9 @@ __device__ __forceinline__ void join(float& top, float& sum, float m, float l) {
   top = next;
 }
 
-template <typename IO, int D, int TILE>
+template <typename IO, int D, int TILE, int PER>
 __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs a, int out_blocks, int chunks) {
+  constexpr int kRows = PER * kJoinThreads;
   __shared__ float head_m[kMaxQueryTile], head_r[kMaxQueryTile];
   const int tid = threadIdx.x, lane = tid % 32;
   const int per_seq = a.heads * a.passes;
@@ -959,7 +959,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
   const int bh = scores ? block / chunks : (int)(out_row / a.group);
   const int b = bh / a.heads, h = bh - b * a.heads;
   const int n = visible_rows(a, b), tiles = tiles_of<TILE>(a, b);
-  const int r0 = scores ? (block - bh * chunks) * kJoinRows : 0;
+  const int r0 = scores ? (block - bh * chunks) * kRows : 0;
   if (scores && r0 >= n) return;
   int64_t total, f0;   // tiles in all, and before this head's first pass
   {
@@ -1021,7 +1021,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
     return;
   }
 
-  constexpr int kPer = kJoinRows / kJoinThreads;
+  constexpr int kPer = PER;
   const int row = r0 + tid;   // + kJoinThreads, ...
   float* sc = a.score + (int64_t)bh * a.cap + row;
   float w[kPer];
@@ -1036,7 +1036,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
       for (int i = 0; i < kPer; ++i)
         x[i] = row + i * kJoinThreads < n ? __ldcg(logits + q * a.logit_stride + i * kJoinThreads) : -INFINITY;
     };
-    constexpr int kAtOnce = 2;
+    constexpr int kAtOnce = 16 / PER;   // sixteen loads a thread
     float x[kAtOnce][kPer];   // some queries' logits are under way while the maxima are found
 #pragma unroll
     for (int q = 0; q < kAtOnce; ++q)
@@ -1129,11 +1129,15 @@ cudaError_t launch_typed(const AttendJob& job) {
   attend_kernel<Q4, IO, D, QT, FOUR><<<(unsigned)ctas, S::kThreads, smem, job.stream>>>(a);
   err = cudaGetLastError();
   if (err != cudaSuccess || a.direct) return err;
-  const int64_t chunks = job.score ? (job.cap + kJoinRows - 1) / kJoinRows : 0;
-  const int64_t score_blocks = (int64_t)job.batch * job.heads * chunks;
   const int64_t slices = (int64_t)job.batch * job.q_heads * (D / 64);
   const int64_t out_blocks = (slices + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
-  const int64_t blocks = out_blocks + score_blocks;
+  // Rows of a block: eight a thread where that fills the GPU (four blocks per SM), else two, so that more
+  // queries' loads are under way at once.
+  const int64_t kv_heads = (int64_t)job.batch * job.heads;
+  const bool many = kv_heads * ((job.cap + 8 * kJoinThreads - 1) / (8 * kJoinThreads)) >= 2 * (int64_t)device_sm_count();
+  const int64_t rows = (many ? 8 : 2) * kJoinThreads;
+  const int64_t chunks = job.score ? (job.cap + rows - 1) / rows : 0;
+  const int64_t blocks = out_blocks + kv_heads * chunks;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
@@ -1144,7 +1148,8 @@ cudaError_t launch_typed(const AttendJob& job) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_join_kernel<IO, D, S::kTile>, a, (int)out_blocks, (int)chunks);
+  return many ? cudaLaunchKernelEx(&cfg, attend_join_kernel<IO, D, S::kTile, 8>, a, (int)out_blocks, (int)chunks)
+              : cudaLaunchKernelEx(&cfg, attend_join_kernel<IO, D, S::kTile, 2>, a, (int)out_blocks, (int)chunks);
 }
 
 template <bool Q4, int D> cudaError_t launch_dim(const AttendJob& job) {

@@ -78,7 +78,8 @@ __device__ __forceinline__ void store8(float* p, const float* x) {
 // border is exact in fp32 (z is zero or a multiple of 2^-9 of the group's largest value), so the sign is;
 // for fp32 rows (kExact) s is (x - z) - 2h k, exact but for the rounding error of x - z, which is put back.
 // An error of one in k does not matter where it can occur, half-way between two borders. s then becomes 0, 1/2 or 1 (anything but zero, times 2^127, saturates), and k + 7 plus that is
-// rounded to the even level where x lies on the border.
+// rounded to the even level where x lies on the border. (fp32 instructions of two values each do most of it,
+// as the logic pipe is what this kernel runs out of.)
 // kClamp is for groups whose rounded h and z leave a value more than a step outside the levels.
 template <bool kExact, bool kClamp>
 __device__ __forceinline__ uint32_t levels(const float2* x, float h, float z, float r) {
@@ -106,15 +107,12 @@ __device__ __forceinline__ uint32_t levels(const float2* x, float h, float z, fl
       s.y += (x[e].y - (d.y - by)) + (nz - by);
     }
     const float2 side = make_float2(__saturatef(fmaf(s.x, 0x1p127f, 0.5f)), __saturatef(fmaf(s.y, 0x1p127f, 0.5f)));
-    level[e] = add2(add2(k, side), magic7);
+    level[e] = add2(add2(add2(k, side), magic7), unmagic);
   }
-  // whole numbers in the low bits, as nibbles (the bits of 1.5 * 2^23 that came with each are taken off, mod 2^32)
-  constexpr int kOrder[8] = {5, 7, 1, 3, 4, 6, 0, 2};   // channels, from the top nibble down
-  uint32_t u = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    u = u * 16u + __float_as_uint(kOrder[i] & 1 ? level[kOrder[i] / 2].y : level[kOrder[i] / 2].x);
-  return u - 0x4B400000u * 0x11111111u;
+  // The halves' nibbles, both at once in fp32 (16 bits are exact): pairs 2, 3, 0, 1 from the top.
+  const float2 up = make_float2(16.0f, 16.0f);
+  const float2 half = add2(fma2(fma2(fma2(level[2], up, level[3]), up, level[0]), up, level[1]), make_float2(8388608.0f, 8388608.0f));
+  return prmt(__float_as_uint(half.x), __float_as_uint(half.y), 0x5410);
 }
 
 // The rows of a launch. Long calls have a head per blockIdx.y, whose blocks take turns; calls of few rows
@@ -124,24 +122,30 @@ struct Q4Grid {
   unsigned flat_rows;   // of all heads
 };
 
-// Calls f(sequence, head of all, row, mine) for this thread's rows, the whole warp at once (mine false: some
-// other row that exists).
-template <int TPR, typename F> __device__ __forceinline__ void for_rows(const Q4Grid& grid, int heads, int64_t rows, F f) {
+// Calls f(head, row, mine, seq(sequence)) for this thread's rows, the whole warp at once (mine false: some other
+// row that exists). seq, what a row needs to know of its sequence, is asked once per head where it can be.
+template <int TPR, typename Seq, typename F>
+__device__ __forceinline__ void for_rows(const Q4Grid& grid, int heads, int64_t rows, Seq seq, F f) {
   constexpr int kRows = kQ4Threads / TPR;
   if (grid.flat) {
     const unsigned at = blockIdx.x * kRows + threadIdx.x / TPR;
     const bool mine = at < grid.flat_rows;
     const unsigned bh = mine ? at / (unsigned)rows : 0u;
-    f((int)(bh / (unsigned)heads), bh, (int)(mine ? at - bh * (unsigned)rows : 0u), mine);
+    f(bh, (int)(mine ? at - bh * (unsigned)rows : 0u), mine, seq((int)(bh / (unsigned)heads)));
   } else {
     const unsigned bh = blockIdx.y;
-    const int b = (int)(bh / (unsigned)heads);
+    const auto known = seq((int)(bh / (unsigned)heads));
     for (int r0 = (int)blockIdx.x * kRows; r0 < (int)rows; r0 += (int)gridDim.x * kRows) {
       const int row = r0 + (int)threadIdx.x / TPR;
-      f(b, bh, row < (int)rows ? row : 0, row < (int)rows);
+      f(bh, row < (int)rows ? row : 0, row < (int)rows, known);
     }
   }
 }
+
+struct AppendSeq {
+  int b, len, n;     // rows held, rows to write
+  bool counts, fits; // n_new is in range; the rows fit
+};
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(Q4Job a, Q4Grid grid) {
@@ -149,16 +153,22 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(Q4Job a, Q4Grid g
   constexpr int kNg = D / kQ4Group;
   const int which = blockIdx.z;             // K or V
   const int c = threadIdx.x % kTpr, g = c / 4, o = 2 * (c % 4);   // group, and the first of its eights
-  for_rows<kTpr>(grid, a.heads, a.rows, [&](int b, unsigned bh, int row, bool mine) {
-    const int len = a.len[b];
-    const int n = a.n_new ? a.n_new[b] : (int)a.rows;
-    const bool counts = n >= 0 && n <= (int)a.rows, fits = len >= 0 && counts && (int64_t)len + n <= a.cap;
-    if (mine && row == 0 && c == 0 && which == 0 && bh == (unsigned)b * a.heads) {   // once per sequence
-      a.len_out[b] = fits ? len + n : len;
-      if (!counts) report(a.dev_status, SNAPKV_ERR_INVALID_ARG);
-      if (len < 0 || (counts && (int64_t)len + n > a.cap)) report(a.dev_status, SNAPKV_ERR_CAPACITY);
+  auto seq = [&](int b) {
+    AppendSeq s;
+    s.b = b;
+    s.len = a.len[b];
+    s.n = a.n_new ? a.n_new[b] : (int)a.rows;
+    s.counts = s.n >= 0 && s.n <= (int)a.rows;
+    s.fits = s.len >= 0 && s.counts && (int64_t)s.len + s.n <= a.cap;
+    return s;
+  };
+  for_rows<kTpr>(grid, a.heads, a.rows, seq, [&](unsigned bh, int row, bool mine, const AppendSeq& s) {
+    if (mine && row == 0 && c == 0 && which == 0 && bh == (unsigned)s.b * a.heads) {   // once per sequence
+      a.len_out[s.b] = s.fits ? s.len + s.n : s.len;
+      if (!s.counts) report(a.dev_status, SNAPKV_ERR_INVALID_ARG);
+      if (s.len < 0 || (s.counts && (int64_t)s.len + s.n > a.cap)) report(a.dev_status, SNAPKV_ERR_CAPACITY);
     }
-    mine = mine && fits && row < n;
+    mine = mine && s.fits && row < s.n;
     if (!__any_sync(0xffffffffu, mine)) return;
     float2 x[kQ4Each / 2];
     float hi = 0.f, lo = 0.f;
@@ -192,8 +202,8 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(Q4Job a, Q4Grid g
       for (int w = 0; w < 2; ++w)
         u[w] = near ? levels<kExact, false>(x + 4 * w, h, z, r) : levels<kExact, true>(x + 4 * w, h, z, r);
     }
-    if (mine && in_bounds((int64_t)len + row < a.cap, a.dev_status)) {
-      const int64_t at = bh * a.cap + (len + row);
+    if (mine && in_bounds((int64_t)s.len + row < a.cap, a.dev_status)) {
+      const int64_t at = bh * a.cap + (s.len + row);
       uint32_t* codes = static_cast<uint32_t*>(which ? a.codes[1] : a.codes[0]) + at * (D / 8);
       codes[q4_word<kNg>(g, o)] = q4_pack(u[0]);
       codes[q4_word<kNg>(g, o + 1)] = q4_pack(u[1]);
@@ -226,9 +236,10 @@ __global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(Q4Job a, Q4Grid gri
   constexpr int kNg = D / kQ4Group;
   const int which = blockIdx.z;
   const int c = threadIdx.x % kTpr, g = c / 4, o = 2 * (c % 4);
-  for_rows<kTpr>(grid, a.heads, a.rows, [&](int b, unsigned bh, int row, bool mine) {
+  auto seq = [&](int b) { return a.len ? a.len[b] : 0; };
+  for_rows<kTpr>(grid, a.heads, a.rows, seq, [&](unsigned bh, int row, bool mine, int start) {
     if (!mine) return;
-    const int64_t src = (int64_t)(a.len ? a.len[b] : 0) + row;
+    const int64_t src = (int64_t)start + row;
     float x[kQ4Each];
     if (src >= 0 && src < a.cap) {
       const int64_t at = bh * a.cap + src;

@@ -8,7 +8,7 @@
  * dense row-major tensors, 16-byte aligned, work enqueued on `stream`, nothing allocated, kept or
  * synchronised, argument errors found on the host before anything is enqueued. All sizes are
  * B = batch, H = heads (KV heads), Hq = q_heads (a multiple of H; query heads h*G .. h*G + G - 1,
- * G = Hq / H, share KV head h), d = head_dim (64 or 128). A pointer array of a call must not overlap
+ * G = Hq / H, share KV head h), d = head_dim (64 or 128); B * H <= 65535, B * Hq <= 2^22. A pointer array of a call must not overlap
  * one that the call writes.
  *
  * Every call may be captured into a CUDA graph. Calls that share a workspace (also as nodes of two

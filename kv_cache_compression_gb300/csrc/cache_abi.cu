@@ -8,6 +8,8 @@
 namespace snapkv {
 namespace {
 
+constexpr int64_t kMaxQueries = (int64_t)1 << 22;   // B * Hq of an attention call (32-bit schedules)
+
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 struct Span {
@@ -54,6 +56,7 @@ snapkv_status run_attend(AttendJob& job, size_t kv_bytes, size_t kv_meta_bytes, 
                          size_t workspace_bytes) {
   if (!job.q || !job.k || !job.v || !job.len || !job.out) return SNAPKV_ERR_INVALID_ARG;
   if (job.q_heads < job.heads || job.q_heads % job.heads != 0) return SNAPKV_ERR_INVALID_ARG;
+  if ((int64_t)job.batch * job.q_heads > kMaxQueries) return SNAPKV_ERR_INVALID_ARG;
   if (!known_dtype(job.dtype) || !(job.decay >= 0.f && job.decay <= 1.f)) return SNAPKV_ERR_INVALID_ARG;
   if (!aligned16(job.q) || !aligned16(job.k) || !aligned16(job.v) || !aligned16(job.out) || !aligned16(job.score) ||
       !aligned4(job.len) || !aligned4(job.dev_status))
@@ -114,7 +117,7 @@ extern "C" {
 size_t snapkv_scored_workspace_size(int32_t batch, int32_t q_heads, int32_t heads, int32_t head_dim, int64_t cap,
                                     int32_t scored) {
   if (check_sizes(batch, heads, head_dim, cap) != SNAPKV_OK) return 0;
-  if (q_heads < heads || q_heads % heads != 0) return 0;
+  if (q_heads < heads || q_heads % heads != 0 || (int64_t)batch * q_heads > kMaxQueries) return 0;
   return attend_workspace_bytes(batch, q_heads, heads, head_dim, cap, scored != 0);
 }
 

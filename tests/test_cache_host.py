@@ -66,7 +66,7 @@ def _attend(lib, **kw):
     (dict(Hq=3), sk.ERR_INVALID_ARG), (dict(Hq=0), sk.ERR_INVALID_ARG), (dict(Hq=1), sk.ERR_INVALID_ARG),
     (dict(d=96), sk.ERR_UNSUPPORTED), (dict(d=0), sk.ERR_INVALID_ARG), (dict(dt=2), sk.ERR_INVALID_ARG),
     (dict(cap=0), sk.ERR_INVALID_ARG), (dict(cap=(1 << 30) + 1), sk.ERR_INVALID_ARG), (dict(B=0), sk.ERR_INVALID_ARG),
-    (dict(B=32768, H=2, Hq=2), sk.ERR_INVALID_ARG), (dict(decay=-0.1), sk.ERR_INVALID_ARG),
+    (dict(B=32768, H=2, Hq=2), sk.ERR_INVALID_ARG), (dict(Hq=1 << 22), sk.ERR_INVALID_ARG), (dict(decay=-0.1), sk.ERR_INVALID_ARG),
     (dict(decay=1.5), sk.ERR_INVALID_ARG), (dict(decay=float("nan")), sk.ERR_INVALID_ARG),
     (dict(ws=0), sk.ERR_WORKSPACE), (dict(ws=9 * MB + 16), sk.ERR_WORKSPACE), (dict(wsb=100), sk.ERR_WORKSPACE),
     (dict(out=2 * MB), sk.ERR_INVALID_ARG),          # the output over the keys

@@ -101,11 +101,14 @@ def _room(workspace, need, device):
 
 def _on_stream(f):
     """Adds the ``stream`` argument: the whole call runs with that stream current, so that what it allocates
-    belongs to the stream that uses it."""
+    belongs to the stream that uses it. The stream has to be one of the tensors' device."""
     @wraps(f)
     def call(*args, stream=None, **kwargs):
         if stream is None:
             return f(*args, **kwargs)
+        for t in (*args, *kwargs.values()):
+            if isinstance(t, (torch.Tensor, Q4Cache)) and t.device != stream.device:
+                raise ValueError(f"stream is of {stream.device}, but a tensor is on {t.device}")
         with torch.cuda.stream(stream):
             return f(*args, **kwargs)
     return call
@@ -180,7 +183,7 @@ def _attend_args(where, q, shape, dev, len_, score, out, workspace):
     if q.dim() != 3:
         raise ValueError("q must be [B, q_heads, d]")
     q_heads = q.shape[1]
-    if q_heads < 1 or q_heads % H:
+    if H < 1 or q_heads < 1 or q_heads % H:
         raise SnapKVError(ERR_INVALID_ARG, where)
     _check("q", q, (B, q_heads, d), q.dtype, dev)
     _check("len_", len_, (B,), _INT32, dev)
@@ -205,8 +208,8 @@ def decode_attend_scored(q, k_cache, v_cache, len_, score=None, *, decay=1.0, ou
         raise ValueError("k_cache must be [B, H, cap, d]")
     _check("k_cache", k_cache, shape, dtype, dev)
     _check("v_cache", v_cache, shape, dtype, dev)
-    q_heads, score_at, out, room = _attend_args("snapkv_decode_attend_scored", q, shape, dev, len_,
-                                                               score, out, workspace)
+    q_heads, score_at, out, room = _attend_args("snapkv_decode_attend_scored", q, shape, dev, len_, score, out,
+                                                workspace)
     B, H, cap, d = shape
     _call("snapkv_decode_attend_scored", dev, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), cap,
           len_.data_ptr(), score_at, decay, out.data_ptr(), B, q_heads, H, d, _code(dtype), room[1], room[2],
@@ -218,8 +221,8 @@ def decode_attend_scored(q, k_cache, v_cache, len_, score=None, *, decay=1.0, ou
 def q4_decode_attend(q, cache, len_, score=None, *, decay=1.0, out=None, workspace=None, dev_status=None):
     """snapkv_q4_decode_attend: decode_attend_scored over a Q4Cache; q and out are bf16 or fp32."""
     dev = cache.device
-    q_heads, score_at, out, room = _attend_args("snapkv_q4_decode_attend", q, cache.shape, dev, len_,
-                                                               score, out, workspace)
+    q_heads, score_at, out, room = _attend_args("snapkv_q4_decode_attend", q, cache.shape, dev, len_, score, out,
+                                                workspace)
     _call("snapkv_q4_decode_attend", dev, q.data_ptr(), cache._struct(), len_.data_ptr(), score_at, decay,
           out.data_ptr(), q_heads, _code(q.dtype), room[1], room[2], _status(dev_status, dev))
     return out
@@ -289,7 +292,7 @@ def _evict_args(shape, dev, score, len_in, len_out, keep, recent, idx_out, want_
     left = keep + recent
     if idx_out is not None:
         _check("idx_out", idx_out, (B, H, left), _INT32, dev)
-    elif want_idx and left > 0:
+    elif want_idx and 0 < left <= cap:   # (else the library refuses the call)
         idx_out = torch.empty((B, H, left), dtype=_INT32, device=dev)
     room = _room(workspace, evict_workspace_size(B, H, cap), dev)
     return len_out, idx_out, None if idx_out is None else idx_out.data_ptr(), room
@@ -306,8 +309,8 @@ def evict(k_cache, v_cache, score, len_in, len_out=None, *, keep, recent, idx_ou
         raise ValueError("k_cache must be [B, H, cap, d]")
     _check("k_cache", k_cache, shape, dtype, dev)
     _check("v_cache", v_cache, shape, dtype, dev)
-    len_out, idx_out, idx_at, room = _evict_args(shape, dev, score, len_in, len_out, keep, recent,
-                                                                idx_out, want_idx, workspace)
+    len_out, idx_out, idx_at, room = _evict_args(shape, dev, score, len_in, len_out, keep, recent, idx_out, want_idx,
+                                                 workspace)
     B, H, cap, d = shape
     _call("snapkv_evict", dev, k_cache.data_ptr(), v_cache.data_ptr(), cap, score.data_ptr(),
           len_in.data_ptr(), len_out.data_ptr(), keep, recent, idx_at, B, H, d, _code(dtype), room[1], room[2],
@@ -320,8 +323,8 @@ def q4_evict(cache, score, len_in, len_out=None, *, keep, recent, idx_out=None, 
              dev_status=None):
     """snapkv_q4_evict: evict for a Q4Cache."""
     dev = cache.device
-    len_out, idx_out, idx_at, room = _evict_args(cache.shape, dev, score, len_in, len_out, keep,
-                                                                recent, idx_out, want_idx, workspace)
+    len_out, idx_out, idx_at, room = _evict_args(cache.shape, dev, score, len_in, len_out, keep, recent, idx_out,
+                                                 want_idx, workspace)
     _call("snapkv_q4_evict", dev, cache._struct(), score.data_ptr(), len_in.data_ptr(), len_out.data_ptr(),
           keep, recent, idx_at, room[1], room[2], _status(dev_status, dev))
     return len_out, idx_out

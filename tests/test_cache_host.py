@@ -193,6 +193,24 @@ def _unpack(codes):
     return t
 
 
+def test_the_binding_refuses_what_it_cannot_serve(lib):
+    q, none = torch.zeros(1, 4, 64), torch.zeros(1, 0, 8, 64)
+    n = torch.ones(1, dtype=torch.int32)
+    with pytest.raises(sk.SnapKVError):   # no heads
+        kc.decode_attend_scored(q, none, none, n)
+    k, score = torch.zeros(1, 4, 8, 64), torch.zeros(1, 4, 8)
+    with pytest.raises(ValueError, match="CUDA"):   # (and no index of 2^50 rows is allocated first)
+        kc.evict(k, k.clone(), score, n, keep=1 << 50, recent=0)
+
+    class Elsewhere:
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="stream is of cuda:1"):
+        kc.decode_attend_scored(q, k, k, n, stream=Elsewhere())
+    with pytest.raises(ValueError, match="stream is of cuda:1"):
+        kc.q4_read(kc.Q4Cache.empty(1, 4, 8, 64, "cpu"), 1, stream=Elsewhere())
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_every_level_survives_the_format(d):
     rng = np.random.default_rng(d)

@@ -8,8 +8,8 @@
  * dense row-major tensors, 16-byte aligned, work enqueued on `stream`, nothing allocated, kept or
  * synchronised, argument errors found on the host before anything is enqueued. All sizes are
  * B = batch, H = heads (KV heads), Hq = q_heads (a multiple of H; query heads h*G .. h*G + G - 1,
- * G = Hq / H, share KV head h), d = head_dim (64 or 128); B * H <= 65535, B * Hq <= 2^22. A pointer array of a call must not overlap
- * one that the call writes.
+ * G = Hq / H, share KV head h), d = head_dim (64 or 128); B * H <= 65535, B * Hq <= 2^22. An array of a call
+ * must not overlap one that the call writes.
  *
  * Every call may be captured into a CUDA graph. Calls that share a workspace (also as nodes of two
  * graphs) must not overlap on the GPU.
@@ -41,7 +41,9 @@ extern "C" {
  *          are then not read)
  * out      device [B, Hq, d]
  * dtype    snapkv_dtype of q, k_cache, v_cache and out. Products and sums are of fp32 accuracy: bf16
- *          weights enter the second product as two bf16 parts, fp32 values as three.
+ *          weights enter the second product as two bf16 parts, fp32 values as three. Visible values must
+ *          be finite, fp32 ones below 2^127 in size: as the parts of an infinity are not all infinite, an
+ *          output or score that it reaches may be NaN.
  * workspace device, >= snapkv_scored_workspace_size(...) bytes, 256-byte aligned (contents on entry
  *          do not matter); `scored` says whether a score is given (its logits then need most of the room).
  *          Where the size is 0 (short caches; also the answer for invalid sizes) it is not used and may be NULL.
@@ -112,8 +114,9 @@ SNAPKV_API snapkv_status snapkv_q4_read(const snapkv_q4_cache* cache, const int3
 
 /*
  * snapkv_q4_decode_attend — snapkv_decode_attend_scored over a 4-bit cache: K_cache[r] and V_cache[r]
- * are the values that the rows stand for. Arguments as there; dtype is that of q and out; the workspace
- * size is snapkv_scored_workspace_size(...) of the cache's sizes.
+ * are the values that the rows stand for. Arguments as there; dtype is that of q and out; q must be below
+ * 2^56 in size (it is scaled on its way to the tensor cores); the workspace size is
+ * snapkv_scored_workspace_size(...) of the cache's sizes.
  */
 SNAPKV_API snapkv_status snapkv_q4_decode_attend(const void* q, const snapkv_q4_cache* cache, const int32_t* len,
                                                  float* score, float decay, void* out, int32_t q_heads,

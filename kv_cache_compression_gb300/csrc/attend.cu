@@ -89,7 +89,7 @@ __device__ __forceinline__ int64_t share_start(int64_t total, int ctas, int c) {
 // The CTA whose share holds flat tile t: the last one that starts at or before it.
 __device__ __forceinline__ int share_of(int64_t total, int ctas, int64_t t) {
   int c = total < (1 << 22) ? (int)((uint32_t)t * (uint32_t)ctas / (uint32_t)total) : (int)(t * ctas / total);
-  while (c + 1 < ctas && share_start(total, ctas, c + 1) <= t) ++c;   // (never behind: floor(t * ctas / total) starts at or before t)
+  while (c + 1 < ctas && share_start(total, ctas, c + 1) <= t) ++c;   // (the quotient's share starts at or before t)
   return c;
 }
 
@@ -398,6 +398,7 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D, QT>::kThreads, Shape<Q4, IO, 
         }
       }
     };
+    if (!in_bounds(p.seq < a.batch && p.head < per_seq && left > 0 && p.rows <= a.cap, a.dev_status)) return;
     if (left >= S::kTile)
       copy(std::true_type{});
     else
@@ -1162,8 +1163,8 @@ cudaError_t launch_typed(const AttendJob& job) {
 template <bool Q4, int D> cudaError_t launch_dim(const AttendJob& job) {
   const int group = job.q_heads / job.heads;
   if (job.dtype == SNAPKV_F32) return launch_typed<Q4, float, D, 1, false>(job);
-  // Grouped queries, 8 sequences of 8192 rows and 4 KV heads, bf16 with scores: 16 queries a head take 33 us in one
-  // pass of sixteen and 56 us in two of eight.
+  // 8 sequences of 8192 bf16 rows and 4 KV heads with scores: 16 queries a head take 49 us in one pass of
+  // sixteen, where two of eight take 56.
   if (group > 8) return launch_typed<Q4, __nv_bfloat16, D, 2, false>(job);
   return group <= 4 ? launch_typed<Q4, __nv_bfloat16, D, 1, true>(job) : launch_typed<Q4, __nv_bfloat16, D, 1, false>(job);
 }

@@ -970,6 +970,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
   const int r0 = scores ? (block - bh * chunks) * kRows : 0;
   if (scores && r0 >= n) return;
   int64_t total, f0;   // tiles in all, and before this head's first pass
+  Parts parts = {};    // of the first pass, or of the output row's
   {
     const SeqScan scan = scan_sequences<TILE>(a);
     total = scan.total * per_seq;
@@ -980,9 +981,6 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
     }
     const int owner = __ffs(__ballot_sync(0xffffffffu, upto >= 0)) - 1;
     f0 = __shfl_sync(0xffffffffu, upto, owner) * per_seq + (int64_t)h * a.passes * tiles;
-  }
-  Parts parts = {};   // of the first pass, or of the output row's
-  {
     const int pass = scores ? 0 : (int)(out_row - (int64_t)bh * a.group) / a.tile_q;
     if (tiles > 0) parts = find_parts<D>(a, total, f0 + (int64_t)pass * tiles, tiles);
   }
@@ -998,7 +996,15 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
       float top = -INFINITY;
       for (int i0 = 0; i0 <= parts.more; i0 += 32) {   // a part per lane, and eight parts' channels at a time
         const bool in = i0 + lane <= parts.more;
+        const int here = min(32, parts.more + 1 - i0);
+        float2 v[8];
+        auto load = [&](int i) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            v[e] = i + e < here ? __ldcg(reinterpret_cast<const float2*>(parts[i0 + i + e] + q * D + c)) : make_float2(0.f, 0.f);
+        };
         const float m = in ? __ldcg(parts[i0 + lane] + at_m) : -INFINITY, l = in ? __ldcg(parts[i0 + lane] + at_l) : 0.f;
+        load(0);
         const float next = fmaxf(top, warp_max(m));
         if (next == -INFINITY) continue;
         const float f = m == -INFINITY ? 0.f : ex2(m - next), old = top == -INFINITY ? 0.f : ex2(top - next);
@@ -1006,13 +1012,9 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
         x *= old;
         y *= old;
         sum = fmaf(sum, old, warp_sum(l * f));
-        const int here = min(32, parts.more + 1 - i0);
 #pragma unroll 1
         for (int i = 0; i < here; i += 8) {
-          float2 v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            v[e] = i + e < here ? __ldcg(reinterpret_cast<const float2*>(parts[i0 + i + e] + q * D + c)) : make_float2(0.f, 0.f);
+          if (i > 0) load(i);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float w = __shfl_sync(0xffffffffu, f, (i + e) & 31);
@@ -1139,12 +1141,17 @@ cudaError_t launch_typed(const AttendJob& job) {
   if (err != cudaSuccess || a.direct) return err;
   const int64_t slices = (int64_t)job.batch * job.q_heads * (D / 64);
   const int64_t out_blocks = (slices + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
-  // Rows of a block: eight a thread where that fills the GPU (four blocks per SM), else two, so that more
-  // queries' loads are under way at once.
+  // Rows a thread: as few as let all blocks run at once (four per SM), so that the loads of more queries are
+  // under way at a time. A second wave costs its blocks' set-up: 64 heads of 8192 4-bit rows, four queries,
+  // take 29.1 us in one wave of four rows a thread, 30.6 with eight and 33.4 in two waves with two.
   const int64_t kv_heads = (int64_t)job.batch * job.heads;
-  const bool many = kv_heads * ((job.cap + 8 * kJoinThreads - 1) / (8 * kJoinThreads)) >= 2 * (int64_t)device_sm_count();
-  const int64_t rows = (many ? 8 : 2) * kJoinThreads;
-  const int64_t chunks = job.score ? (job.cap + rows - 1) / rows : 0;
+  int per = 2;
+  int64_t chunks = 0;
+  if (job.score)
+    for (;; per *= 2) {
+      chunks = (job.cap + per * kJoinThreads - 1) / (per * kJoinThreads);
+      if (per == 8 || out_blocks + kv_heads * chunks <= 4 * (int64_t)device_sm_count()) break;
+    }
   const int64_t blocks = out_blocks + kv_heads * chunks;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
@@ -1156,8 +1163,9 @@ cudaError_t launch_typed(const AttendJob& job) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return many ? cudaLaunchKernelEx(&cfg, attend_join_kernel<IO, D, S::kTile, 8>, a, (int)out_blocks, (int)chunks)
-              : cudaLaunchKernelEx(&cfg, attend_join_kernel<IO, D, S::kTile, 2>, a, (int)out_blocks, (int)chunks);
+  auto* join = per == 2 ? attend_join_kernel<IO, D, S::kTile, 2>
+               : per == 4 ? attend_join_kernel<IO, D, S::kTile, 4> : attend_join_kernel<IO, D, S::kTile, 8>;
+  return cudaLaunchKernelEx(&cfg, join, a, (int)out_blocks, (int)chunks);
 }
 
 template <bool Q4, int D> cudaError_t launch_dim(const AttendJob& job) {

@@ -1143,14 +1143,16 @@ cudaError_t launch_typed(const AttendJob& job) {
   const int64_t out_blocks = (slices + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
   // Rows a thread: as few as let all blocks run at once (four per SM), so that the loads of more queries are
   // under way at a time. A second wave costs its blocks' set-up: 64 heads of 8192 4-bit rows, four queries,
-  // take 29.1 us in one wave of four rows a thread, 30.6 with eight and 33.4 in two waves with two.
+  // take 29.1 us in one wave of four rows a thread, 30.6 with eight and 33.4 in two waves with two. (Several
+  // passes have work enough for their blocks: 32 heads of 16384 bf16 rows, 64 queries, take 229, 236, 247 us
+  // with two, four and eight.)
   const int64_t kv_heads = (int64_t)job.batch * job.heads;
   int per = 2;
   int64_t chunks = 0;
   if (job.score)
     for (;; per *= 2) {
       chunks = (job.cap + per * kJoinThreads - 1) / (per * kJoinThreads);
-      if (per == 8 || out_blocks + kv_heads * chunks <= 4 * (int64_t)device_sm_count()) break;
+      if (per == 8 || L.passes > 1 || out_blocks + kv_heads * chunks <= 4 * (int64_t)device_sm_count()) break;
     }
   const int64_t blocks = out_blocks + kv_heads * chunks;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;

@@ -16,7 +16,7 @@ namespace {
 constexpr int kQ4Threads = 128;   // (writing that prompt: 73 us, 77 with 256, 81 with 512)
 // Words (of eight channels of one group) of a thread. Four share more of the work on a group, where there are
 // rows enough: writing 16384 rows of 32 heads takes 77 us with four words, 88 with two and 108 with all
-// eight; one row of 2048 heads 3.4, 3.0 and 5.2 us. Reading has little to share: 70, 59 and 65 us with one, two
+// eight (in blocks of 256 threads); one row of 2048 heads 3.4, 3.0 and 5.2 us. Reading has little to share: 70, 59 and 65 us with one, two
 // and four, and 2.2, 2.3 and 2.6.
 template <bool FLAT> constexpr int kAppendWords = FLAT ? 2 : 4;
 constexpr int kReadWords = 2;

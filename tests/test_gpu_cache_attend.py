@@ -367,3 +367,44 @@ def test_buffers_of_a_call_on_another_stream_are_not_reused_early(dev, q4):
         torch.empty_like(q).fill_(7.0)
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(s, want_s)
+
+
+@pytest.mark.parametrize("B,H,G,cap", [
+    (12, 5, 6, 9001),     # four rows a thread in the joining kernel
+    (2, 1, 40, 3001),     # three passes, two rows a thread
+    (1, 1, 70, 300),      # five passes over few tiles
+])
+def test_joins_of_every_size(dev, B, H, G, cap):
+    import kv_cache_compression_gb300 as kv
+    g = torch.Generator().manual_seed(B + G)
+    d, dtype = 64, torch.bfloat16
+    lens = [cap - 97 * b for b in range(B)]
+    q, k, v, n, score = dense(g, B, G * H, H, cap, d, dtype, lens)
+    s = score.to(dev)
+    out = kv.decode_attend_scored(q.to(dev), k.to(dev), v.to(dev), n.to(dev), s, decay=0.5)
+    torch.cuda.synchronize()
+    sel = [0, B - 1]
+    check_attend(q[sel], to64(k[sel]), to64(v[sel]), [lens[b] for b in sel], out[sel], score0=score[sel],
+                 score=s.cpu()[sel], decay=0.5, heads=[0, H - 1], where=f"B{B} H{H} G{G}")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("power", [-40, 0, 44, 55])
+def test_large_and_small_queries_over_four_bits(dev, dtype, power):
+    """Queries are scaled on their way to the tensor cores; 2^55 is as large as they may be."""
+    import kv_cache_compression_gb300 as kv
+    g = torch.Generator().manual_seed(power + 50)
+    B, H, G, d, cap = 1, 2, 2, 128, 300
+    made = {}
+    for name, scale in (("k", 2.0 ** -power), ("v", 1.0)):
+        x = (torch.randn(B, H, cap, d, generator=g) * scale).bfloat16()
+        u, h, z = co.quantise(to64(x))
+        made[name] = (*(t.to(dev) for t in q4_inputs(u, h, z)), co.values(u, h, z), co.magnitudes(u, h, z))
+    q = (torch.randn(B, G * H, d, generator=g).clamp(-1.9, 1.9) * 2.0 ** power).to(dtype)
+    score = torch.zeros(B, H, cap)
+    s = score.to(dev)
+    n = torch.tensor([cap], dtype=torch.int32, device=dev)
+    out = kv.q4_decode_attend(q.to(dev), kv.Q4Cache(*made["k"][:2], *made["v"][:2]), n, s)
+    torch.cuda.synchronize()
+    check_attend(q, made["k"][2], made["v"][2], [cap], out, k_size=made["k"][3], v_size=made["v"][3], score0=score,
+                 score=s.cpu(), where=f"{dtype} 2^{power}")

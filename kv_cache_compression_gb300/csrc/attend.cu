@@ -67,6 +67,7 @@ struct AttendArgs {
   float* logits;        // [heads][tile_q][logit_stride] (scores only)
   int64_t logit_stride; // cap, rounded up to whole 32-byte sectors
   float* stats;         // [heads][2][tile_q]: maximum and sum of a head that one CTA finished
+  int64_t* upto;        // [batch + 1]: tiles of a head in the sequences before, and of all (more than kWarpBatch)
   float* parts;         // [ctas][2] of (o [tile_q][D], m [tile_q], l [tile_q])
   int32_t* dev_status;
   Q4Ones ones;
@@ -104,28 +105,56 @@ template <int TILE> __device__ __forceinline__ int tiles_of(const AttendArgs& a,
   return (visible_rows(a, b) + TILE - 1) / TILE;
 }
 
-// Sums over the sequences: lane i takes a run of them, `mine` tiles after `upto`.
+// Sums over the sequences: a thread takes sequences b0 .. b1 - 1, with `mine` tiles after `upto`, of `total`.
+// Up to kWarpBatch sequences every warp asks for itself, lane by lane, and the joining kernel asks again. More are
+// summed up by all threads of a CTA of the first launch, whose CTAs also leave `upto` of every sequence and the
+// total for the joining kernel: bf16, scores, 500 to 1000 rows of 64 channels, 1024 sequences of 8 heads take 310 us
+// [239 at 6.79 TB/s], 4096 of one head 168 [120]. With every warp of both kernels summing up they took 532 and 666.
+constexpr int kWarpBatch = 32;
 struct SeqScan {
   int b0, b1;
   int64_t upto, mine, total;
 };
-template <int TILE> __device__ __forceinline__ SeqScan scan_sequences(const AttendArgs& a) {
-  const int lane = threadIdx.x % 32;
-  const int chunk = (a.batch + 31) / 32;
-  SeqScan s;
-  s.b0 = min(a.batch, lane * chunk);
-  s.b1 = min(a.batch, s.b0 + chunk);
-  s.mine = 0;
-#pragma unroll 4
-  for (int b = s.b0; b < s.b1; ++b) s.mine += tiles_of<TILE>(a, b);
-  int64_t x = s.mine;
+
+// Inclusive sum over the warp's lanes.
+__device__ __forceinline__ int64_t warp_scan(int64_t x) {
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
-    if (lane >= off) x += y;
+    if ((int)threadIdx.x % 32 >= off) x += y;
   }
+  return x;
+}
+
+template <int TILE> __device__ __forceinline__ SeqScan scan_by_warp(const AttendArgs& a) {
+  SeqScan s;
+  s.b0 = min(a.batch, (int)threadIdx.x % 32);
+  s.b1 = min(a.batch, s.b0 + 1);
+  s.mine = s.b0 < s.b1 ? tiles_of<TILE>(a, s.b0) : 0;
+  const int64_t x = warp_scan(s.mine);
   s.total = __shfl_sync(0xffffffffu, x, 31);
   s.upto = x - s.mine;
+  return s;
+}
+
+template <int TILE> __device__ __forceinline__ SeqScan scan_by_block(const AttendArgs& a, int64_t (&sums)[kWarps]) {
+  const int tid = threadIdx.x, chunk = (a.batch + 32 * kWarps - 1) / (32 * kWarps);
+  SeqScan s;
+  s.b0 = min(a.batch, tid * chunk);
+  s.b1 = min(a.batch, s.b0 + chunk);
+  s.mine = 0;
+#pragma unroll 8
+  for (int b = s.b0; b < s.b1; ++b) s.mine += tiles_of<TILE>(a, b);
+  const int64_t x = warp_scan(s.mine);
+  if (tid % 32 == 31) sums[tid / 32] = x;
+  __syncthreads();
+  s.total = 0;
+  s.upto = x - s.mine;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < tid / 32) s.upto += sums[w];
+    s.total += sums[w];
+  }
   return s;
 }
 
@@ -272,6 +301,8 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D, QT>::kThreads, Shape<Q4, IO, 
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float warp_m[S::kWarps][8 * QT], warp_l[S::kWarps][8 * QT];
   __shared__ float head_m[8 * QT], head_r[8 * QT];
+  __shared__ int64_t sums[kWarps], shared_before;   // (more than kWarpBatch sequences)
+  __shared__ int shared_seq;
   __shared__ int arrived, merged;   // warps whose part of this head is in `meet`; heads merged
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -305,10 +336,20 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D, QT>::kThreads, Shape<Q4, IO, 
       return;
     }
   } else {
-    const SeqScan scan = scan_sequences<S::kTile>(a);
-    if (blockIdx.x == 0 && warp == 0)
-      for (int b = scan.b0; b < scan.b1; ++b)
+    const bool by_warp = a.batch <= kWarpBatch;
+    const SeqScan scan = by_warp ? scan_by_warp<S::kTile>(a) : scan_by_block<S::kTile>(a, sums);
+    // Each thread's sequences are looked after by one CTA.
+    if (by_warp ? blockIdx.x == 0 && warp == 0 : tid % gridDim.x == blockIdx.x) {
+      int64_t upto = scan.upto;
+      for (int b = scan.b0; b < scan.b1; ++b) {
         if ((int64_t)a.len[b] > a.cap) report(a.dev_status, SNAPKV_ERR_CAPACITY);
+        if (!by_warp) {
+          a.upto[b] = upto;
+          upto += tiles_of<S::kTile>(a, b);
+        }
+      }
+      if (!by_warp && tid == 0) a.upto[a.batch] = scan.total;
+    }
     const int64_t total = scan.total * per_seq;
     const int ctas = working_ctas(total, a.ctas);
     if ((int)blockIdx.x >= ctas) return;
@@ -320,9 +361,19 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D, QT>::kThreads, Shape<Q4, IO, 
       seq = scan.b0;
       for (int t; at >= (upto + (t = tiles_of<S::kTile>(a, seq))) * per_seq; ++seq) upto += t;
     }
-    const int owner = __ffs(__ballot_sync(0xffffffffu, seq >= 0)) - 1;
-    first_seq = __shfl_sync(0xffffffffu, seq, owner);
-    before = __shfl_sync(0xffffffffu, upto, owner);
+    if (by_warp) {
+      const int owner = __ffs(__ballot_sync(0xffffffffu, seq >= 0)) - 1;
+      first_seq = __shfl_sync(0xffffffffu, seq, owner);
+      before = __shfl_sync(0xffffffffu, upto, owner);
+    } else {
+      if (seq >= 0) {
+        shared_seq = seq;
+        shared_before = upto;
+      }
+      __syncthreads();
+      first_seq = shared_seq;
+      before = shared_before;
+    }
   }
 
   // A place in the list: a tile of a head, and what its addresses need.
@@ -971,20 +1022,21 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
   if (scores && r0 >= n) return;
   int64_t total, f0;   // tiles in all, and before this head's first pass
   Parts parts = {};    // of the first pass, or of the output row's
-  {
-    const SeqScan scan = scan_sequences<TILE>(a);
-    total = scan.total * per_seq;
-    int64_t upto = -1;
-    if (b >= scan.b0 && b < scan.b1) {
-      upto = scan.upto;
-      for (int s = scan.b0; s < b; ++s) upto += tiles_of<TILE>(a, s);
-    }
-    const int owner = __ffs(__ballot_sync(0xffffffffu, upto >= 0)) - 1;
-    f0 = __shfl_sync(0xffffffffu, upto, owner) * per_seq + (int64_t)h * a.passes * tiles;
+  auto find = [&](int64_t upto) {
+    f0 = upto * per_seq + (int64_t)h * a.passes * tiles;
     const int pass = scores ? 0 : (int)(out_row - (int64_t)bh * a.group) / a.tile_q;
     if (tiles > 0) parts = find_parts<D>(a, total, f0 + (int64_t)pass * tiles, tiles);
+  };
+  if (a.batch <= kWarpBatch) {
+    const SeqScan scan = scan_by_warp<TILE>(a);
+    total = scan.total * per_seq;
+    find(__shfl_sync(0xffffffffu, scan.upto, b));
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (a.batch > kWarpBatch) {
+    total = __ldcg(a.upto + a.batch) * per_seq;
+    find(__ldcg(a.upto + b));
+  }
 
   if (!scores) {
     const int g = (int)(out_row - (int64_t)bh * a.group), pass = g / a.tile_q, q = g - pass * a.tile_q;
@@ -1111,6 +1163,7 @@ cudaError_t launch_typed(const AttendJob& job) {
   a.group = job.q_heads / job.heads;
   a.passes = L.passes;
   a.tile_q = L.tile_q;
+  a.upto = reinterpret_cast<int64_t*>(ws + L.upto);
   a.parts = reinterpret_cast<float*>(ws + L.parts);   // (no workspace, and none of these, for a direct call)
   a.stats = reinterpret_cast<float*>(ws + L.stats);
   a.logits = reinterpret_cast<float*>(ws + L.logits);
@@ -1198,7 +1251,8 @@ AttendLayout attend_layout(int batch, int q_heads, int heads, int head_dim, int6
   L.max_ctas = (int)(tiles < kMaxAttendCtas ? tiles : kMaxAttendCtas);
   L.parts = 0;
   L.stats = L.parts + up((size_t)L.max_ctas * 2 * L.tile_q * (head_dim + 2) * sizeof(float));
-  L.logits = L.stats + up(vh * 2 * L.tile_q * sizeof(float));
+  L.upto = L.stats + up(vh * 2 * L.tile_q * sizeof(float));
+  L.logits = L.upto + up(batch > kWarpBatch ? ((size_t)batch + 1) * sizeof(int64_t) : 0);
   L.logit_stride = L.direct ? kDirectRows : (cap + 7) / 8 * 8;
   if (L.direct)   // shared memory holds everything
     L.total = 0;

@@ -45,7 +45,7 @@ struct AttendJob {
 
 // Workspace layout of an attention call (byte offsets, each 256-aligned), and how its queries are cut.
 struct AttendLayout {
-  size_t parts, stats, logits, total;
+  size_t parts, stats, upto, logits, total;
   int64_t logit_stride;
   int tile_q, passes, max_ctas;
   bool direct;          // a CTA per head in one launch, without workspace

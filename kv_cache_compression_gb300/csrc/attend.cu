@@ -967,9 +967,9 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D, QT>::kThreads, Shape<Q4, IO, 
 }
 
 // The second launch. The warps of its first blocks each join 64 channels of an output row whose head was
-// cut (or is empty); the other blocks each add the weights of PER rows a thread to a head's scores. Where a head's
-// parts lie follows from the schedule. The kernel is all latency: loads are issued together and early,
-// and registers are kept to what lets four blocks share an SM.
+// cut (or is empty); the other blocks each add the weights of PER rows a thread to a head's scores, or of every
+// `chunks`-th such run of its rows. Where a head's parts lie follows from the schedule. The kernel is all
+// latency: loads are issued together and early, and registers are kept to what lets four blocks share an SM.
 constexpr int kJoinThreads = 256;
 
 // A head's parts: the last segment of one CTA (its slot 1, unless the share starts with the head) and the
@@ -1083,62 +1083,65 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
     return;
   }
 
-  constexpr int kPer = PER;
-  const int row = r0 + tid;   // + kJoinThreads, ...
-  float* sc = a.score + (int64_t)bh * a.cap + row;
-  float w[kPer];
+  constexpr int kAtOnce = 16 / PER;   // sixteen loads a thread
+  for (int64_t row0 = r0; row0 < n; row0 += (int64_t)chunks * kRows) {
+    const int row = (int)row0 + tid;   // + kJoinThreads, ...
+    float* sc = a.score + (int64_t)bh * a.cap + row;
+    float w[PER];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) w[i] = a.decay != 0.f && row + i * kJoinThreads < n ? a.decay * sc[i * kJoinThreads] : 0.f;
-  for (int pass = 0; pass < a.passes; ++pass) {
-    const int tile_q = min(a.tile_q, a.group - pass * a.tile_q);
-    const int64_t vh = (int64_t)bh * a.passes + pass;
-    const float* logits = a.logits + vh * a.tile_q * a.logit_stride + row;
-    auto load = [&](int q, float (&x)[kPer]) {
+    for (int i = 0; i < PER; ++i) w[i] = a.decay != 0.f && row + i * kJoinThreads < n ? a.decay * sc[i * kJoinThreads] : 0.f;
+    for (int pass = 0; pass < a.passes; ++pass) {
+      const int tile_q = min(a.tile_q, a.group - pass * a.tile_q);
+      const int64_t vh = (int64_t)bh * a.passes + pass;
+      const float* logits = a.logits + vh * a.tile_q * a.logit_stride + row;
+      auto load = [&](int q, float (&x)[PER]) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        x[i] = row + i * kJoinThreads < n ? __ldcg(logits + q * a.logit_stride + i * kJoinThreads) : -INFINITY;
-    };
-    constexpr int kAtOnce = 16 / PER;   // sixteen loads a thread
-    float x[kAtOnce][kPer];   // some queries' logits are under way while the maxima are found
+        for (int i = 0; i < PER; ++i)
+          x[i] = row + i * kJoinThreads < n ? __ldcg(logits + q * a.logit_stride + i * kJoinThreads) : -INFINITY;
+      };
+      float x[kAtOnce][PER];   // some queries' logits are under way while the maxima are found
 #pragma unroll
-    for (int q = 0; q < kAtOnce; ++q)
-      if (q < tile_q) load(q, x[q]);
-    if (pass > 0) parts = find_parts<D>(a, total, f0 + (int64_t)pass * tiles, tiles);
-    for (int q = tid / 32; q < tile_q; q += kJoinThreads / 32) {   // a warp per query
-      float top = -INFINITY, sum = 0.f;
-      if (parts.more == 0) {
-        top = __ldcg(a.stats + vh * 2 * a.tile_q + q);
-        sum = __ldcg(a.stats + (vh * 2 + 1) * a.tile_q + q);
-      } else {
-        for (int i = lane; i <= parts.more; i += 32) {
-          const float* p = parts[i] + a.tile_q * D + q;
-          join(top, sum, __ldcg(p), __ldcg(p + a.tile_q));
+      for (int q = 0; q < kAtOnce; ++q)
+        if (q < tile_q) load(q, x[q]);
+      if (a.passes > 1 || row0 == r0) {
+        if (a.passes > 1) parts = find_parts<D>(a, total, f0 + (int64_t)pass * tiles, tiles);
+        for (int q = tid / 32; q < tile_q; q += kJoinThreads / 32) {   // a warp per query
+          float top = -INFINITY, sum = 0.f;
+          if (parts.more == 0) {
+            top = __ldcg(a.stats + vh * 2 * a.tile_q + q);
+            sum = __ldcg(a.stats + (vh * 2 + 1) * a.tile_q + q);
+          } else {
+            for (int i = lane; i <= parts.more; i += 32) {
+              const float* p = parts[i] + a.tile_q * D + q;
+              join(top, sum, __ldcg(p), __ldcg(p + a.tile_q));
+            }
+            const float all = warp_max(top);
+            sum = warp_sum(top == -INFINITY ? 0.f : sum * ex2(top - all));
+            top = all;
+          }
+          if (lane == 0) {
+            head_m[q] = top == -INFINITY ? 0.f : top;
+            head_r[q] = sum == 0.f ? 0.f : 1.0f / sum;
+          }
         }
-        const float all = warp_max(top);
-        sum = warp_sum(top == -INFINITY ? 0.f : sum * ex2(top - all));
-        top = all;
+        __syncthreads();
       }
-      if (lane == 0) {
-        head_m[q] = top == -INFINITY ? 0.f : top;
-        head_r[q] = sum == 0.f ? 0.f : 1.0f / sum;
+      for (int q0 = 0; q0 < tile_q; q0 += kAtOnce) {
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e)
+          if (q0 + e < tile_q) {
+            const float m = head_m[q0 + e], r = head_r[q0 + e];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) w[i] = fmaf(ex2(x[e][i] - m), r, w[i]);
+            if (q0 + e + kAtOnce < tile_q) load(q0 + e + kAtOnce, x[e]);
+          }
       }
+      if (a.passes > 1) __syncthreads();   // the maxima have been used
     }
-    __syncthreads();
-    for (int q0 = 0; q0 < tile_q; q0 += kAtOnce) {
 #pragma unroll
-      for (int e = 0; e < kAtOnce; ++e)
-        if (q0 + e < tile_q) {
-          const float m = head_m[q0 + e], r = head_r[q0 + e];
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) w[i] = fmaf(ex2(x[e][i] - m), r, w[i]);
-          if (q0 + e + kAtOnce < tile_q) load(q0 + e + kAtOnce, x[e]);
-        }
-    }
-    if (pass + 1 < a.passes) __syncthreads();   // the maxima have been used
+    for (int i = 0; i < PER; ++i)
+      if (row + i * kJoinThreads < n) sc[i * kJoinThreads] = w[i];
   }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (row + i * kJoinThreads < n) sc[i * kJoinThreads] = w[i];
 }
 
 template <bool Q4, typename IO, int D, int QT, bool FOUR>
@@ -1207,6 +1210,10 @@ cudaError_t launch_typed(const AttendJob& job) {
       chunks = (job.cap + per * kJoinThreads - 1) / (per * kJoinThreads);
       if (per == 8 || L.passes > 1 || out_blocks + kv_heads * chunks <= 4 * (int64_t)device_sm_count()) break;
     }
+  // No more than two waves of blocks, which then take turns: caches are often longer than what they hold (512 heads
+  // of 1000 bf16 rows, 64 channels, in caches of 65536 rows: 37 us, 49 with a block for each run of rows).
+  const int64_t turns = (kv_heads * chunks + 8 * (int64_t)device_sm_count() - 1) / (8 * (int64_t)device_sm_count());
+  if (turns > 1) chunks = (chunks + turns - 1) / turns;
   const int64_t blocks = out_blocks + kv_heads * chunks;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};

@@ -97,3 +97,21 @@ def test_evictions_past_32_bits(dev):
     for h in (0, H - 1):
         check_evicted((0, h), (k, v), (k2, v2), score0, s, idx, length, keep, recent)
     assert torch.equal(k2[0, H - 1, keep + recent:], k[0, H - 1, keep + recent:])
+
+
+@pytest.mark.parametrize("B,H,G", [(32, 5, 1), (16, 4, 20)])
+def test_caches_much_longer_than_their_sequences(dev, B, H, G):
+    """The joining kernel's blocks take turns over a head's rows (with twenty queries, in several passes)."""
+    import kv_cache_compression_gb300 as kv
+    d, cap = 64, 20011
+    g = torch.Generator(device=dev).manual_seed(B)
+    k, v = (torch.randn(B, H, cap, d, generator=g, device=dev).bfloat16() for _ in range(2))
+    q = torch.randn(B, H * G, d, generator=g, device=dev).bfloat16()
+    score0 = torch.rand(B, H, cap, generator=g, device=dev)
+    lens = [(0, cap, 1000, 2049, cap - 1, 1)[b % 6] for b in range(B)]
+    s = score0.clone()
+    out = kv.decode_attend_scored(q, k, v, torch.tensor(lens, dtype=torch.int32, device=dev), s, decay=0.5)
+    torch.cuda.synchronize()
+    some = [0, 1, 2, 3, B - 4, B - 1]
+    check_attend(q[some].cpu(), to64(k[some].cpu()), to64(v[some].cpu()), [lens[b] for b in some], out[some].cpu(),
+                 score0=score0[some].cpu(), score=s[some].cpu(), decay=0.5, heads=[0, H - 1])

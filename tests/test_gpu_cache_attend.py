@@ -88,10 +88,10 @@ def test_q4_ragged_lengths(dev, dtype, d, G):
 
 @pytest.mark.parametrize("q4", [False, True])
 @pytest.mark.parametrize("B,H,G,cap,dtype", [
-    (1, 1, 1, 40000, torch.bfloat16),        # one head over a whole cluster
+    (1, 1, 1, 40000, torch.bfloat16),        # one head over all CTAs
     (1, 2, 8, 12011, torch.float32),
-    (40, 8, 8, 2311, torch.bfloat16),        # many heads: one CTA each, logits in the workspace
-    (1, 3, 16, 30011, torch.bfloat16),       # two passes of eight queries, logits in the workspace
+    (40, 8, 8, 2311, torch.bfloat16),        # many heads in every CTA's share
+    (1, 3, 16, 30011, torch.bfloat16),       # sixteen queries a pass
     (300, 1, 1, 70, torch.float32),
 ])
 def test_long_and_wide(dev, q4, B, H, G, cap, dtype):

@@ -28,7 +28,7 @@ namespace snapkv {
 namespace {
 
 constexpr int kMaxCluster = 8;
-constexpr int kKeysSmem = 64 * 1024;   // a span's keys stay in shared memory up to this size
+constexpr int kKeysSmem = 96 * 1024;   // a span's keys stay in shared memory up to this size (two CTAs per SM)
 constexpr int kMaxIndex = 1024;        // pairs resolved at a time
 static_assert(kEvictNoListCap <= 2 * kMaxIndex, "min(keep, n - keep) pairs at most");
 constexpr int kRun = 15;               // keys a thread looks at between two scans, at most (odd: no bank conflicts)
@@ -434,10 +434,16 @@ template <int ROW, int META, int THREADS> cudaError_t launch_sized(const EvictJo
 
 template <int ROW, int META> cudaError_t launch_typed(const EvictJob& job) {
   const int64_t bh = (int64_t)job.batch * job.heads;
-  // CTAs per head: up to one per 2048 candidates, while all heads together fill two per SM.
+  // CTAs per head: up to one per 2048 candidates, while all heads together fill two per SM; and, up to about 600
+  // heads, as many as hold all keys in shared memory, although they do not all run at once then: full caches of
+  // 65536 bf16 rows of 64 channels, 512 heads, 244 us (291 with one CTA, which reads the scores six times),
+  // 131072 rows, 256 heads, 275 (325). Beyond, heads in plenty hide the reads better: 2048 heads of 32768 rows
+  // 434 us (502 with clusters), 1024 heads 236 (258).
   int64_t csize = 2 * (int64_t)device_sm_count() / bh;
   const int64_t most = (job.cap + kEvictNoListCap - 1) / kEvictNoListCap;
   if (csize > most) csize = most;
+  const int64_t fit = (job.cap * 4 + kKeysSmem - 1) / kKeysSmem;
+  if (bh <= 4 * (int64_t)device_sm_count() && csize < fit) csize = fit;
   if (csize > kMaxCluster) csize = kMaxCluster;
   if (csize < 1) csize = 1;
   return (job.cap + csize - 1) / csize <= 4096 ? launch_sized<ROW, META, 256>(job, csize)

@@ -115,3 +115,22 @@ def test_caches_much_longer_than_their_sequences(dev, B, H, G):
     some = [0, 1, 2, 3, B - 4, B - 1]
     check_attend(q[some].cpu(), to64(k[some].cpu()), to64(v[some].cpu()), [lens[b] for b in some], out[some].cpu(),
                  score0=score0[some].cpu(), score=s[some].cpu(), decay=0.5, heads=[0, H - 1])
+
+
+@pytest.mark.parametrize("B,H,cap", [(16, 32, 30011), (32, 32, 25013)])
+def test_evictions_of_long_caches_of_many_heads(dev, B, H, cap):
+    """More keys than one CTA's shared memory holds: clusters that do not all run at once, or keys read again."""
+    import kv_cache_compression_gb300 as kv
+    d, keep, recent = 64, cap - 900, 32
+    g = torch.Generator(device=dev).manual_seed(cap)
+    k, v = (torch.randn(B, H, cap, d, generator=g, device=dev).bfloat16() for _ in range(2))
+    score0 = torch.rand(B, H, cap, generator=g, device=dev).argsort(-1).float()      # no ties
+    lens = [cap - 7 * b for b in range(B)]
+    k2, v2, s = k.clone(), v.clone(), score0.clone()
+    after, idx = kv.evict(k2, v2, s, torch.tensor(lens, dtype=torch.int32, device=dev), keep=keep, recent=recent)
+    torch.cuda.synchronize()
+    assert after.tolist() == [min(n, keep + recent) for n in lens]
+    for b in (0, 1, B - 1):
+        for h in (0, H - 1):
+            if lens[b] > keep + recent:
+                check_evicted((b, h), (k, v), (k2, v2), score0, s, idx, lens[b], keep, recent)

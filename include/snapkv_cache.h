@@ -44,6 +44,8 @@ extern "C" {
  *          weights enter the second product as two bf16 parts, fp32 values as three. Visible values must
  *          be finite, fp32 ones below 2^127 in size: as the parts of an infinity are not all infinite, an
  *          output or score that it reaches may be NaN.
+ *          A NaN reaches, whatever the lengths, all of a query's outputs (if it is in the query or in a
+ *          visible row of K) and the scores of all visible rows of the KV head.
  * workspace device, >= snapkv_scored_workspace_size(...) bytes, 256-byte aligned (contents on entry
  *          do not matter); `scored` says whether a score is given (its logits then need most of the room).
  *          Where the size is 0 (short caches; also the answer for invalid sizes) it is not used and may be NULL.

@@ -994,11 +994,14 @@ template <int D> __device__ __forceinline__ Parts find_parts(const AttendArgs& a
   return p;
 }
 
+// What sums that belong to maximum m are multiplied by under the maximum `top` (of at least m). Sums under -inf are
+// zero, or NaN where a logit is (maxima pass NaN over): multiplied, not left out, they keep it.
+__device__ __forceinline__ float rescale(float m, float top) { return m == -INFINITY ? 0.f : ex2(m - top); }
+
 // Adds a part's maximum and sum to a running pair.
 __device__ __forceinline__ void join(float& top, float& sum, float m, float l) {
-  if (m == -INFINITY) return;
   const float next = fmaxf(top, m);
-  sum = fmaf(l, ex2(m - next), top == -INFINITY ? 0.f : sum * ex2(top - next));
+  sum = fmaf(l, rescale(m, next), sum * rescale(top, next));
   top = next;
 }
 
@@ -1058,8 +1061,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
         const float m = in ? __ldcg(parts[i0 + lane] + at_m) : -INFINITY, l = in ? __ldcg(parts[i0 + lane] + at_l) : 0.f;
         load(0);
         const float next = fmaxf(top, warp_max(m));
-        if (next == -INFINITY) continue;
-        const float f = m == -INFINITY ? 0.f : ex2(m - next), old = top == -INFINITY ? 0.f : ex2(top - next);
+        const float f = rescale(m, next), old = rescale(top, next);
         top = next;
         x *= old;
         y *= old;
@@ -1116,7 +1118,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
               join(top, sum, __ldcg(p), __ldcg(p + a.tile_q));
             }
             const float all = warp_max(top);
-            sum = warp_sum(top == -INFINITY ? 0.f : sum * ex2(top - all));
+            sum = warp_sum(sum * rescale(top, all));
             top = all;
           }
           if (lane == 0) {

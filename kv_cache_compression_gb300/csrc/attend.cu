@@ -1179,13 +1179,22 @@ cudaError_t launch_typed(const AttendJob& job) {
   const int smem = S::smem(L.tile_q, L.direct);
   cudaError_t err = allow_dynamic_smem<attend_kernel<Q4, IO, D, QT, FOUR>>(S::smem(8 * QT, true));
   if (err != cudaSuccess) return err;
-  static std::atomic<int> occupancy[8 * QT + 1];   // CTAs per SM by tile_q (0: not asked yet)
-  int resident = L.direct ? 1 : occupancy[L.tile_q].load(std::memory_order_relaxed);
-  if (resident < 1) {
-    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, attend_kernel<Q4, IO, D, QT, FOUR>, S::kThreads, smem);
+  // CTAs per SM by device and tile_q (0: not asked yet), as the shares, and with them a result's bits, follow from it.
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> occupancy[kMaxDev][8 * QT + 1];
+  int resident = 1;
+  if (!L.direct) {
+    int dev = 0;
+    err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
-    if (resident < 1) return cudaErrorInvalidConfiguration;
-    occupancy[L.tile_q].store(resident, std::memory_order_relaxed);
+    std::atomic<int>* known = dev < kMaxDev ? &occupancy[dev][L.tile_q] : nullptr;
+    resident = known ? known->load(std::memory_order_relaxed) : 0;
+    if (resident < 1) {
+      err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, attend_kernel<Q4, IO, D, QT, FOUR>, S::kThreads, smem);
+      if (err != cudaSuccess) return err;
+      if (resident < 1) return cudaErrorInvalidConfiguration;
+      if (known) known->store(resident, std::memory_order_relaxed);
+    }
   }
   const int64_t heads = (int64_t)job.batch * job.heads * L.passes;
   const int64_t tiles = heads * ((job.cap + S::kTile - 1) / S::kTile);

@@ -233,7 +233,10 @@ template <bool Q4, typename IO, int D, int QT> struct Shape {
   static constexpr int kWarps = snapkv::kWarps;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kCtasPerSm = Q4 ? (kWide || QT > 1 ? 2 : 3) : kRow >= 512 ? 1 : 2;   // what the ring leaves room for
+  // What the ring, the meeting area and the registers leave room for. Sixteen queries over dense rows of 128 channels: 96 KB
+  // of ring and 18 to 32 of meeting, one CTA. Its four warps then wait for one another's latency more than for anything else
+  // (64 heads of 8192 rows: an instruction in 24 % of a scheduler's cycles, DRAM at 60 %).
+  static constexpr int kCtasPerSm = Q4 ? (kWide || QT > 1 ? 2 : 3) : kRow * QT >= 512 ? 1 : 2;
   static constexpr int smem(int tile_q, bool direct) {   // and a direct head's logits
     return kRing + kWarps * tile_q * D * 4 + (direct ? tile_q * kDirectRows * 4 : 0);
   }

@@ -48,7 +48,9 @@ extern "C" {
  *          visible row of K) and the scores of all visible rows of the KV head.
  * workspace device, >= snapkv_scored_workspace_size(...) bytes, 256-byte aligned (contents on entry
  *          do not matter); `scored` says whether a score is given (its logits then need most of the room).
- *          Where the size is 0 (short caches; also the answer for invalid sizes) it is not used and may be NULL.
+ *          Where the size is 0 (short caches; also the answer for invalid sizes) it is not used and may be NULL. The
+ *          size serves calls of either dtype; bf16 calls of 9 to 16 queries a KV head use none, and take NULL, over
+ *          caches for which calls of up to 8 use none.
  * Sums run in a fixed order: the same call on the same device gives the same bits.
  */
 SNAPKV_API size_t snapkv_scored_workspace_size(int32_t batch, int32_t q_heads, int32_t heads, int32_t head_dim,

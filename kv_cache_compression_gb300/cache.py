@@ -166,8 +166,12 @@ class Q4Cache:
 
 
 @lru_cache(maxsize=256)
-def scored_workspace_size(batch, q_heads, heads, head_dim, cap, scored=True) -> int:
+def scored_workspace_size(batch, q_heads, heads, head_dim, cap, scored=True, dtype=None) -> int:
+    """snapkv_scored_workspace_size: bytes for calls of either type, or of ``dtype`` alone."""
     lib()
+    if dtype is _BF16 and 8 * heads < q_heads <= 16 * heads and q_heads % heads == 0 and \
+            scored_workspace_size(batch, heads, heads, head_dim, cap, scored) == 0:
+        return 0   # one pass without workspace (or sizes that are invalid)
     return int(_functions["snapkv_scored_workspace_size"](batch, q_heads, heads, head_dim, cap, bool(scored)))
 
 
@@ -193,7 +197,7 @@ def _attend_args(where, q, shape, dev, len_, score, out, workspace):
         out = torch.empty_like(q)
     else:
         _check("out", out, q.shape, q.dtype, dev)
-    room = _room(workspace, scored_workspace_size(B, q_heads, H, d, cap, score is not None), dev)
+    room = _room(workspace, scored_workspace_size(B, q_heads, H, d, cap, score is not None, q.dtype), dev)
     return q_heads, None if score is None else score.data_ptr(), out, room
 
 

@@ -1282,10 +1282,8 @@ AttendLayout attend_layout(int batch, int q_heads, int heads, int head_dim, int6
   return L;
 }
 
-size_t attend_workspace_bytes(int batch, int q_heads, int heads, int head_dim, int64_t cap, bool scored) {
-  const size_t a = attend_layout(batch, q_heads, heads, head_dim, cap, scored, 8).total;    // fp32
-  const size_t b = attend_layout(batch, q_heads, heads, head_dim, cap, scored, 16).total;   // bf16
-  return a > b ? a : b;
+size_t attend_workspace_bytes(int batch, int q_heads, int heads, int head_dim, int64_t cap, bool scored, int dtype) {
+  return attend_layout(batch, q_heads, heads, head_dim, cap, scored, dtype == SNAPKV_F32 ? 8 : kMaxQueryTile).total;
 }
 
 cudaError_t launch_attend(const AttendJob& job) {

@@ -62,7 +62,7 @@ snapkv_status run_attend(AttendJob& job, size_t kv_bytes, size_t kv_meta_bytes, 
       !aligned4(job.len) || !aligned4(job.dev_status))
     return SNAPKV_ERR_INVALID_ARG;
   const size_t need =
-      attend_workspace_bytes(job.batch, job.q_heads, job.heads, job.head_dim, job.cap, job.score != nullptr);
+      attend_workspace_bytes(job.batch, job.q_heads, job.heads, job.head_dim, job.cap, job.score != nullptr, job.dtype);
   if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u))) return SNAPKV_ERR_WORKSPACE;
   const size_t q_bytes = (size_t)job.batch * job.q_heads * job.head_dim * elem_bytes(job.dtype);
   const Span spans[] = {{job.q, q_bytes, false},
@@ -118,7 +118,9 @@ size_t snapkv_scored_workspace_size(int32_t batch, int32_t q_heads, int32_t head
                                     int32_t scored) {
   if (check_sizes(batch, heads, head_dim, cap) != SNAPKV_OK) return 0;
   if (q_heads < heads || q_heads % heads != 0 || (int64_t)batch * q_heads > kMaxQueries) return 0;
-  return attend_workspace_bytes(batch, q_heads, heads, head_dim, cap, scored != 0);
+  const size_t f32 = attend_workspace_bytes(batch, q_heads, heads, head_dim, cap, scored != 0, SNAPKV_F32);
+  const size_t bf16 = attend_workspace_bytes(batch, q_heads, heads, head_dim, cap, scored != 0, SNAPKV_BF16);
+  return f32 > bf16 ? f32 : bf16;
 }
 
 snapkv_status snapkv_decode_attend_scored(const void* q, const void* k_cache, const void* v_cache, int64_t cap,

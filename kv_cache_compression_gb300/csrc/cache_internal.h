@@ -57,9 +57,9 @@ constexpr int kDirectRows = 256;
 
 constexpr int kMaxAttendCtas = 1024;   // bounds the workspace, not tied to a device's SM count
 
-// The layout for passes of at most `most_q` queries, and the workspace that a call of either type needs.
+// The layout for passes of at most `most_q` queries, and the workspace that a call of a type needs.
 AttendLayout attend_layout(int batch, int q_heads, int heads, int head_dim, int64_t cap, bool scored, int most_q);
-size_t attend_workspace_bytes(int batch, int q_heads, int heads, int head_dim, int64_t cap, bool scored);
+size_t attend_workspace_bytes(int batch, int q_heads, int heads, int head_dim, int64_t cap, bool scored, int dtype);
 cudaError_t launch_attend(const AttendJob& job);
 
 struct Q4Job {

@@ -80,6 +80,21 @@ def test_attend_refusals(lib, kw, status):
     assert _attend(lib, **kw) == status
 
 
+def test_short_bf16_calls_of_up_to_sixteen_queries_need_no_workspace(lib):
+    """The size serves either type; a call asks for what its own type needs. (These calls are refused after that, for an
+    output that lies over the queries.)"""
+    short = dict(ws=0, wsb=0, cap=256, out=MB, Hq=32, H=2)
+    assert kc.scored_workspace_size(2, 32, 2, 64, 256) > 0
+    assert _attend(lib, **short) == sk.ERR_INVALID_ARG
+    assert _attend(lib, **short, dt=0) == sk.ERR_WORKSPACE                 # fp32: two passes
+    assert _attend(lib, **dict(short, cap=257)) == sk.ERR_WORKSPACE
+    assert _attend(lib, **dict(short, Hq=34)) == sk.ERR_WORKSPACE          # seventeen queries: two passes
+    for q_heads, cap, dtype, none in ((32, 256, torch.bfloat16, True), (32, 256, torch.float32, False), (18, 1, torch.bfloat16, True),
+                                      (34, 256, torch.bfloat16, False), (32, 257, torch.bfloat16, False)):
+        assert (kc.scored_workspace_size(2, q_heads, 2, 64, cap, True, dtype) == 0) == none
+    assert kc.scored_workspace_size(2, 8, 2, 64, 1000, True, torch.bfloat16) == kc.scored_workspace_size(2, 8, 2, 64, 1000)
+
+
 def _cache(**kw):
     a = dict(kc=16 * MB, km=17 * MB, vc=18 * MB, vm=19 * MB, cap=300, B=2, H=2, d=64)
     a.update(kw)

@@ -408,3 +408,29 @@ def test_large_and_small_queries_over_four_bits(dev, dtype, power):
     torch.cuda.synchronize()
     check_attend(q, made["k"][2], made["v"][2], [cap], out, k_size=made["k"][3], v_size=made["v"][3], score0=score,
                  score=s.cpu(), where=f"{dtype} 2^{power}")
+
+
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("G", [9, 16])
+def test_short_bf16_calls_allocate_no_workspace(dev, q4, G):
+    import kv_cache_compression_gb300 as kv
+    g = torch.Generator().manual_seed(G)
+    B, H, cap, d, lens = 2, 2, 256, 128, [256, 77]
+    q, k, v, n, score = dense(g, B, G * H, H, cap, d, torch.bfloat16, lens, poison=False)
+    cache = kv.Q4Cache.empty(B, H, cap, d, dev)
+    kv.q4_append(cache, k.to(dev), v.to(dev), torch.zeros(B, dtype=torch.int32, device=dev))
+    qd, kd, vd, nd, s = (t.to(dev) for t in (q, k, v, n, score))
+    out = torch.empty_like(qd)
+    before = torch.cuda.memory_stats(dev)["allocation.all.allocated"]
+    if q4:
+        kv.q4_decode_attend(qd, cache, nd, s, out=out)
+    else:
+        kv.decode_attend_scored(qd, kd, vd, nd, s, out=out)
+    assert torch.cuda.memory_stats(dev)["allocation.all.allocated"] == before
+    torch.cuda.synchronize()
+    sizes = {}
+    k64, v64 = to64(k), to64(v)
+    if q4:
+        k64, v64 = (to64(t) for t in kv.q4_read(cache, cap, dtype=torch.float32))
+        sizes = {name: 3 * np.broadcast_to(np.abs(t).max(-1, keepdims=True), t.shape) for name, t in (("k_size", k64), ("v_size", v64))}
+    check_attend(q, k64, v64, lens, out, score0=score, score=s.cpu(), where=f"q4 {q4} G{G}", **sizes)

@@ -288,9 +288,11 @@ def q4_read(cache, rows, *, start=None, dtype=None, k_out=None, v_out=None):
     return k_out, v_out
 
 
-def _evict_args(shape, dev, score, len_in, len_out, keep, recent, idx_out, want_idx, workspace):
+def _evict_args(where, shape, dev, score, len_in, len_out, keep, recent, idx_out, want_idx, workspace):
     """Checks and completes what the two evictions share."""
     B, H, cap, _ = shape
+    if (keep | recent) >> 62:   # (negative, or more than the call's integers hold)
+        raise SnapKVError(ERR_INVALID_ARG, where)
     _check("score", score, (B, H, cap), _FP32, dev)
     len_out = _new_lengths(len_in, len_out, B, dev)
     left = keep + recent
@@ -313,8 +315,8 @@ def evict(k_cache, v_cache, score, len_in, len_out=None, *, keep, recent, idx_ou
         raise ValueError("k_cache must be [B, H, cap, d]")
     _check("k_cache", k_cache, shape, dtype, dev)
     _check("v_cache", v_cache, shape, dtype, dev)
-    len_out, idx_out, idx_at, room = _evict_args(shape, dev, score, len_in, len_out, keep, recent, idx_out, want_idx,
-                                                 workspace)
+    len_out, idx_out, idx_at, room = _evict_args("snapkv_evict", shape, dev, score, len_in, len_out, keep, recent,
+                                                 idx_out, want_idx, workspace)
     B, H, cap, d = shape
     _call("snapkv_evict", dev, k_cache.data_ptr(), v_cache.data_ptr(), cap, score.data_ptr(),
           len_in.data_ptr(), len_out.data_ptr(), keep, recent, idx_at, B, H, d, _code(dtype), room[1], room[2],
@@ -327,8 +329,8 @@ def q4_evict(cache, score, len_in, len_out=None, *, keep, recent, idx_out=None, 
              dev_status=None):
     """snapkv_q4_evict: evict for a Q4Cache."""
     dev = cache.device
-    len_out, idx_out, idx_at, room = _evict_args(cache.shape, dev, score, len_in, len_out, keep, recent, idx_out,
-                                                 want_idx, workspace)
+    len_out, idx_out, idx_at, room = _evict_args("snapkv_q4_evict", cache.shape, dev, score, len_in, len_out, keep,
+                                                 recent, idx_out, want_idx, workspace)
     _call("snapkv_q4_evict", dev, cache._struct(), score.data_ptr(), len_in.data_ptr(), len_out.data_ptr(),
           keep, recent, idx_at, room[1], room[2], _status(dev_status, dev))
     return len_out, idx_out

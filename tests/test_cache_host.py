@@ -226,6 +226,17 @@ def test_the_binding_refuses_what_it_cannot_serve(lib):
         kc.q4_read(kc.Q4Cache.empty(1, 4, 8, 64, "cpu"), 1, stream=Elsewhere())
 
 
+@pytest.mark.parametrize("keep,recent", [((1 << 64) + 3, 2), (3, 1 << 64), (1 << 63, 1 << 63), (-1, 4), (4, -1)])
+def test_the_binding_refuses_counts_that_its_integers_do_not_hold(lib, keep, recent):
+    """2^64 + 3 must not evict down to 3 rows."""
+    k, score, n = torch.zeros(1, 4, 8, 64), torch.zeros(1, 4, 8), torch.ones(1, dtype=torch.int32)
+    for want_idx in (True, False):
+        with pytest.raises(sk.SnapKVError, match="snapkv_evict"):
+            kc.evict(k, k.clone(), score, n, keep=keep, recent=recent, want_idx=want_idx)
+        with pytest.raises(sk.SnapKVError, match="snapkv_q4_evict"):
+            kc.q4_evict(kc.Q4Cache.empty(1, 4, 8, 64, "cpu"), score, n, keep=keep, recent=recent, want_idx=want_idx)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_every_level_survives_the_format(d):
     rng = np.random.default_rng(d)

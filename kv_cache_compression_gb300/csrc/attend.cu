@@ -487,6 +487,11 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D, QT>::kThreads, Shape<Q4, IO, 
     const int64_t seg_end = min(end, at + (here.tiles - here.tile));
     const int n = here.rows;
     float* logits = !a.score ? nullptr : a.direct ? meet + S::kWarps * a.tile_q * D : a.logits + vh * a.tile_q * a.logit_stride;
+    // (Every address of the segment follows from these; the whole CTA agrees.)
+    if (!in_bounds(here.seq < a.batch && here.head < per_seq && tile_q >= 1 && tile_q <= 8 * QT && n <= a.cap &&
+                       n <= a.logit_stride && here.tile + (seg_end - at) <= here.tiles && (a.direct || (int)blockIdx.x < a.ctas),
+                   a.dev_status))
+      break;
 
     // B operands of the first product: channels c .. c + 3 of the query of column j for each step, as the
     // lane's share of the rows is laid out (see `first product` below).
@@ -701,7 +706,8 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D, QT>::kThreads, Shape<Q4, IO, 
               for (int sub = 0; sub < kSub; ++sub)
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
-                  if (16 * sub + 8 * half < left) to[16 * sub + 8 * half] = sv[q][sub][2 * half + e2];
+                  if (16 * sub + 8 * half < left && in_bounds(base + jrow + 16 * sub + 8 * half < n, a.dev_status))
+                    to[16 * sub + 8 * half] = sv[q][sub][2 * half + e2];
             }
           }
         }
@@ -982,6 +988,7 @@ struct Parts {
   const float* rest;
   int64_t stride;   // from one of the rest to the next
   int more;
+  bool inside = true;   // of the parts that there are (checked build)
   __device__ __forceinline__ const float* operator[](int i) const { return i ? rest + (i - 1) * stride : first; }
 };
 
@@ -991,6 +998,7 @@ template <int D> __device__ __forceinline__ Parts find_parts(const AttendArgs& a
   const int c0 = share_of(total, ctas, f0);
   Parts p;
   p.more = share_of(total, ctas, f0 + tiles - 1) - c0;
+  p.inside = in_bounds(f0 >= 0 && f0 + tiles <= total && c0 >= 0 && p.more >= 0 && c0 + p.more < a.ctas, a.dev_status);
   p.first = a.parts + ((int64_t)c0 * 2 + (share_start(total, ctas, c0) < f0 ? 1 : 0)) * size;
   p.rest = a.parts + ((int64_t)c0 + 1) * 2 * size;
   p.stride = 2 * size;
@@ -1027,7 +1035,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
   const int r0 = scores ? (block - bh * chunks) * kRows : 0;
   if (scores && r0 >= n) return;
   int64_t total, f0;   // tiles in all, and before this head's first pass
-  Parts parts = {};    // of the first pass, or of the output row's
+  Parts parts = {};   // of the first pass, or of the output row's
   auto find = [&](int64_t upto) {
     f0 = upto * per_seq + (int64_t)h * a.passes * tiles;
     const int pass = scores ? 0 : (int)(out_row - (int64_t)bh * a.group) / a.tile_q;
@@ -1049,7 +1057,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
     const int c = (int)(slice % kSlices) * 64 + 2 * lane;
     float x = 0.f, y = 0.f, sum = 0.f;
     if (tiles > 0) {
-      if (parts.more == 0) return;   // finished in the first launch
+      if (parts.more == 0 || !parts.inside) return;   // finished in the first launch
       const int at_m = a.tile_q * D + q, at_l = a.tile_q * (D + 1) + q;
       float top = -INFINITY;
       for (int i0 = 0; i0 <= parts.more; i0 += 32) {   // a part per lane, and eight parts' channels at a time
@@ -1091,6 +1099,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
   constexpr int kAtOnce = 16 / PER;   // sixteen loads a thread
   for (int64_t row0 = r0; row0 < n; row0 += (int64_t)chunks * kRows) {
     const int row = (int)row0 + tid;   // + kJoinThreads, ...
+    if (!in_bounds(bh < a.batch * a.heads && row0 >= 0 && n <= a.cap && n <= a.logit_stride, a.dev_status)) break;
     float* sc = a.score + (int64_t)bh * a.cap + row;
     float w[PER];
 #pragma unroll
@@ -1110,6 +1119,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attend_join_kernel(AttendArgs
         if (q < tile_q) load(q, x[q]);
       if (a.passes > 1 || row0 == r0) {
         if (a.passes > 1) parts = find_parts<D>(a, total, f0 + (int64_t)pass * tiles, tiles);
+        if (!parts.inside) return;   // (the whole block)
         for (int q = tid / 32; q < tile_q; q += kJoinThreads / 32) {   // a warp per query
           float top = -INFINITY, sum = 0.f;
           if (parts.more == 0) {

@@ -146,7 +146,10 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(EvictArgs args) {
         const uint32_t key = key_of(s);
         if (key >> (shift + 8) == prefix) {
           count(key);
-          if (keep_list) list[atomicAdd(&listed, 1)] = (int)key;
+          if (keep_list) {
+            const int at = atomicAdd(&listed, 1);
+            if (in_bounds(at < kMaxIndex, j.dev_status)) list[at] = (int)key;
+          }
         }
       }
     }
@@ -240,6 +243,7 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(EvictArgs args) {
       const int s = t0 + __ffs(marks) - 1;
       if (s < keep) {
         const int p = n_free + (at & 0xFFFF);
+        if (!in_bounds(p < (in_smem ? kMaxIndex : s1 - s0), j.dev_status)) break;
         if (in_smem)
           pair_to[p] = s;
         else
@@ -247,6 +251,7 @@ __global__ void __launch_bounds__(THREADS) evict_kernel(EvictArgs args) {
         at += 1;
       } else {
         const int p = n_stay + (at >> 16);
+        if (!in_bounds(p < (in_smem ? kMaxIndex : s1 - s0), j.dev_status)) break;
         if (in_smem)
           pair_from[p] = s;
         else

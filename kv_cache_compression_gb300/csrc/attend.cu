@@ -439,9 +439,9 @@ __global__ void __launch_bounds__(Shape<Q4, IO, D, QT>::kThreads, Shape<Q4, IO, 
         if constexpr (Q4) {
           const uint8_t* msrc = (kv ? a.vm : a.km) + row0 * S::kMeta + lane * S::kMeta;
           uint8_t* mto = dst + 2 * (S::kTile * S::kRow) + kv * (S::kTile * S::kMeta) + lane * S::kMeta;
+          static_assert(S::kTile % 32 == 0, "a pair of each row per lane and turn");
 #pragma unroll
           for (int row = 0; row < S::kTile; row += 32) {
-            if (row + 32 > S::kTile && lane >= S::kTile - row) continue;
             if constexpr (decltype(whole)::value) {
               cp_async_small<S::kMeta>(mto + row * S::kMeta, msrc + row * S::kMeta, S::kMeta);
             } else {

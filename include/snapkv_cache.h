@@ -5,7 +5,7 @@
  * makes it grow again, and these keep it small.
  *
  * Conventions, status codes and types are those of snapkv.h: device pointers of the current device,
- * dense row-major tensors, 16-byte aligned, work enqueued on `stream`, nothing allocated, kept or
+ * dense row-major tensors, 16-byte aligned (lengths, indices and status words: 4), work enqueued on `stream`, nothing allocated, kept or
  * synchronised, argument errors found on the host before anything is enqueued. All sizes are
  * B = batch, H = heads (KV heads), Hq = q_heads (a multiple of H; query heads h*G .. h*G + G - 1,
  * G = Hq / H, share KV head h), d = head_dim (64 or 128); B * H <= 65535, B * Hq <= 2^22. An array of a call
@@ -28,7 +28,9 @@ extern "C" {
  * also accumulates how much attention every cached row receives:
  *   s_gr = q_g . K_cache[r] / sqrt(d),  p_gr = softmax over r < len[b],  o_g = sum_r p_gr V_cache[r]
  *   score[b,h,r] = decay * score[b,h,r] + sum over the G queries of head h of p_gr,   r < len[b]
- * With G = 1 and no score it computes what snapkv_decode_attend computes.
+ * With G = 1 and no score it computes what snapkv_decode_attend computes. That one is the faster for the caches of
+ * one layer of one sequence (32 heads of 1057 bf16 rows: 8 us, 12 here) and for short ones, this one for lengths that
+ * differ much and long caches (64 heads of 8192 to 16384 rows: 65 us, 81 there); the rest are within 2 %.
  *
  * q        device [B, Hq, d]
  * k_cache, v_cache  device [B, H, cap, d]; rows at or past len[b] are not used, whatever they hold

@@ -3,7 +3,9 @@
 Decode attention with grouped queries that keeps a running score of every cached row, eviction by
 that score, and a cache held in 4 bits. As in ``snapkv``, every computation runs in the library's
 CUDA kernels and arguments mirror the header; calls run on ``stream`` (default: the current stream
-of the tensors' device), allocate what the caller does not pass, and raise on a refused call.
+of the tensors' device), allocate what the caller does not pass, and raise on a refused call. Tensors
+start on 16 bytes: of stacked scores [layers, B, H, cap] every layer's slice does if B * H * cap is a
+multiple of four.
 
 A decode step makes several of these calls, and its kernels take microseconds each: the checks are
 written to cost little where they pass, and calls with their buffers (``out``, ``workspace``, ...)

@@ -11,14 +11,16 @@
 // memory. A head that lies in one share is finished there; the parts of others, and the logits that a
 // score will need, go to the workspace. The second launch joins the parts and turns logits into
 // weights. It is released early (programmatic dependent launch) and waits on the device for the first.
-// Rows are read once. (One cluster per head with the logits in shared memory, and everything in one
-// launch, was measured first: 222 us where this takes 131 on 2048 4-bit heads of 2208 rows, and 115 us
-// where this takes 76 on 64 bf16 heads of 8192 to 16384 rows with four queries each.)
+// Rows are read once per pass of up to sixteen queries (fp32: eight) a KV head. (One cluster per head with
+// the logits in shared memory, and everything in one launch, was measured first: 222 us where this takes 131
+// on 2048 4-bit heads of 2208 rows, and 115 us where this takes 76 on 64 bf16 heads of 8192 to 16384 rows
+// with four queries each.)
 //
 // Both products run on the tensor cores as m16n8k16 with eight queries as the columns: K Q^T has sixteen
 // cached rows by sixteen channels as A, V^T P^T sixteen channels by sixteen cached rows. Weights cross
 // from one's accumulators to the other's B operand by an 8 x 8 transpose in registers (movmatrix). They
-// enter the second product in two bf16 parts (16 bits of mantissa); fp32 calls split q, p and the cached
+// enter the second product in two bf16 parts (16 bits of mantissa: 0.1 to 0.3 % of the bf16 outputs are the
+// neighbours of the exact ones, and 0.05 to 0.25 % with fp32 operations throughout); fp32 calls split q, p and the cached
 // values into three (24 bits) and drop nothing above 2^-24 of a product's factors. (With the queries as
 // rows of A in the first product no transpose is needed, but half of A is zeros, which cost twice the
 // instructions and, as A takes four neighbouring registers, moves around each: 475 instructions per
@@ -33,11 +35,14 @@
 // ends of heads; at the end of a head a warp leaves its part and goes on.
 //
 // Measured (GB300, first launch and join; HBM floor at 6.79 TB/s in brackets): bf16, 2048 heads of about 2140
-// rows 370 us [336]; 64 heads of 8192 to 16384 rows, four queries, with scores 76 us [60]; 4 bits, the same
-// 131 us [93] and 38 us [18]; 32 heads of 131072 rows 115 us [89]. Dense rows run at 96 % of HBM, and
-// the join's 8 to 10 us of latency is what scores add. 4-bit rows are bound by instructions: 318 per 16 rows,
-// 140 of them on the logic pipe, which is 70 of the 137 cycles that an SM takes (98 would be HBM's); copying
-// the same tiles and computing nothing takes 103 and 98 us where this takes 131 and 115.
+// rows 322 us without scores [331] and 368 with [336]; 64 heads of 8192 to 16384 rows, four queries, with scores
+// 77 us [60]; 32 heads of 1057 rows 12 us without scores [2.6]; fp32, 64 heads of 8192 rows, four queries, with
+// scores 100 us [80]. 4 bits: the 2048 heads 131 us without scores [93] and 157 with [98], the grouped ones with
+// scores 38 us [18], 32 heads of 131072 rows without 115 us [89].
+// Dense rows are read at the rate of a copy; scores add their logits' traffic and the second launch (8 to 10 us
+// on the grouped heads). 4-bit rows are bound by instructions: 318 per 16 rows, 140 of them on the logic pipe,
+// which is 70 of the 137 cycles that an SM takes (98 would be HBM's); copying the same tiles and computing
+// nothing takes 103 and 98 us where this takes 131 and 115.
 #include <type_traits>
 
 #include "cache_internal.h"
@@ -80,7 +85,7 @@ __device__ __forceinline__ int working_ctas(int64_t total, int ctas) {
   return most < ctas ? (int)most : ctas;
 }
 
-// CTA c's share of `total` tiles starts here. (c <= ctas <= 1024 and total < 2^43: no product overflows;
+// CTA c's share of `total` tiles starts here. (c <= ctas <= 1024 and total <= 2^45: no product overflows;
 // short lists, where the latency counts, get by with a 32-bit division.)
 __device__ __forceinline__ int64_t share_start(int64_t total, int ctas, int c) {
   if (total < (1 << 22)) return (uint32_t)total * (uint32_t)c / (uint32_t)ctas;

@@ -13,12 +13,16 @@
 // columns of the rows (columns never meet), loads a batch of rows, waits for its threads, stores it, and
 // goes on upwards; a batch's stores land below every later load.
 //
-// The bytes are few: 4 per candidate's score, and the rows that change their slot. 2048 heads of 2208 bf16
-// rows, 128 of which leave, take 72 us (350 MB, 52 us at 6.79 TB/s): the selection's instructions and the
-// latency of its steps show, with six CTAs per SM to hide them. 32 heads of 131072 rows, an eighth of which
-// leaves, take 119 us (75 at that rate): about 35 select, in clusters of eight, and the moves run at 5 TB/s,
-// as rows of 256 bytes lie far apart. (Clusters of sixteen or blocks of 1024 threads no longer fit the GPU
-// at once and take 200 us.) 4 heads of 97 rows take 6.7 us.
+// The bytes are few: 4 per candidate's score, and the rows that change their slot. Selection (with the newest rows) and the
+// other moves, measured apart by shuffling heavy scores below slot `keep` and light ones above it (GB300; in brackets the
+// floor of both at 6.79 TB/s):
+//   2048 heads of 2208 bf16 rows of 128 channels, 128 leave:   33 us, and  40 for 250 MB  [52]
+//   32 heads of 131072 such rows, an eighth leaves:            30 us, and  90 for 470 MB  [75]
+//   512 heads of 65536 rows of 64 channels, 1504 leave:       132 us, and 115 for 385 MB  [93]
+// The selection's instructions and the latency of its steps show, with six CTAs per SM to hide them in the batch and
+// clusters of eight over the long caches. The moves run at 6.2, 5.2 and 3.3 TB/s: rows of 256 or 128 bytes that lie far
+// apart. (Over the 32 long caches, clusters of sixteen or blocks of 1024 threads no longer fit the GPU at once and take
+// 200 us.) 4-bit rows: 2048 heads of 2208 58 us [19]; 4 heads of 97 6.9 us.
 #include "cache_internal.h"
 #include "sm100_ptx.cuh"
 #include "snapkv_common.cuh"

@@ -40,7 +40,7 @@ _functions = {}   # name -> library function with its prototype
 def lib():
     """The loaded library with the prototypes of include/snapkv_cache.h."""
     L = _sk.lib()
-    if not _functions:
+    if "snapkv_q4_evict" not in _functions:
         P, I32, I64, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
         C = ctypes.POINTER(_Q4Struct)
         found = {}
@@ -109,8 +109,9 @@ def _on_stream(f):
         if stream is None:
             return f(*args, **kwargs)
         for t in (*args, *kwargs.values()):
-            if isinstance(t, (torch.Tensor, Q4Cache)) and t.device != stream.device:
-                raise ValueError(f"stream is of {stream.device}, but a tensor is on {t.device}")
+            dev = getattr(t, "device", None)   # (of a tensor or a cache)
+            if dev is not None and dev != stream.device:
+                raise ValueError(f"stream is of {stream.device}, but a tensor is on {dev}")
         with torch.cuda.stream(stream):
             return f(*args, **kwargs)
     return call

@@ -10,34 +10,6 @@ namespace {
 
 constexpr int64_t kMaxQueries = (int64_t)1 << 22;   // B * Hq of an attention call (32-bit schedules)
 
-bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
-
-struct Span {
-  const void* at;
-  size_t bytes;
-  bool written;
-};
-
-// Whether no array that a call writes overlaps another of its arrays (NULL ones are skipped).
-template <int N> bool disjoint(const Span (&s)[N]) {
-  for (int i = 0; i < N; ++i)
-    for (int k = i + 1; k < N; ++k)
-      if (s[i].at && s[k].at && (s[i].written || s[k].written) && overlaps(s[i].at, s[i].bytes, s[k].at, s[k].bytes))
-        return false;
-  return true;
-}
-
-snapkv_status check_sizes(int32_t batch, int32_t heads, int32_t head_dim, int64_t cap) {
-  if (batch < 1 || heads < 1 || head_dim < 1 || cap < 1 || cap > kMaxPrompt) return SNAPKV_ERR_INVALID_ARG;
-  if ((int64_t)batch * heads > 65535) return SNAPKV_ERR_INVALID_ARG;  // grid.y limit
-  if (head_dim != 64 && head_dim != 128) return SNAPKV_ERR_UNSUPPORTED;
-  return SNAPKV_OK;
-}
-
-bool known_dtype(int32_t dtype) { return dtype == SNAPKV_F32 || dtype == SNAPKV_BF16; }
-
-size_t elem_bytes(int32_t dtype) { return dtype == SNAPKV_BF16 ? 2 : 4; }
-
 snapkv_status check_cache(const snapkv_q4_cache* c) {
   if (!c || !c->k_codes || !c->k_meta || !c->v_codes || !c->v_meta) return SNAPKV_ERR_INVALID_ARG;
   const snapkv_status st = check_sizes(c->batch, c->heads, c->head_dim, c->cap);

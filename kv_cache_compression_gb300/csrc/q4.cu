@@ -8,12 +8,12 @@
 // division wherever a value lies close to half-way between two levels, as 0.7 % of normal bf16 values do.
 #include "cache_internal.h"
 #include "q4.cuh"
+#include "row_list.cuh"
 #include "snapkv_internal.h"
 
 namespace snapkv {
 namespace {
 
-constexpr int kQ4Threads = 128;   // (writing that prompt: 73 us, 77 with 256, 81 with 512)
 // Words (of eight channels of one group) of a thread. Four share more of the work on a group, where there are
 // rows enough: writing 16384 rows of 32 heads takes 77 us with four words, 88 with two and 108 with all
 // eight (in blocks of 256 threads); one row of 2048 heads 3.4, 3.0 and 5.2 us. Reading has little to share: 70, 59 and 65 us with one, two
@@ -68,20 +68,6 @@ template <int W> __device__ __forceinline__ void load_values(const float* p, int
   }
 }
 
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 two = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&two);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void store8(float* p, const float* x) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-
 // The level numbers of eight values as nibbles, in q4_pack's order. (x - z) / (2h) + 7.5 has to be
 // rounded as if computed exactly: ties are common (0.7 % of normal bf16 values lie half-way between
 // two levels). So no quotient is trusted: a product with r = 1 / (2h) only finds the nearest border
@@ -127,36 +113,13 @@ __device__ __forceinline__ uint32_t levels(const float2* x, float h, float z, fl
   return prmt(__float_as_uint(half.x), __float_as_uint(half.y), 0x5410);
 }
 
-// The rows of a launch. Long calls have a head per blockIdx.y, whose blocks take turns; calls of few rows
-// (FLAT) are one list of `flat_rows` rows over all heads, as a head's rows would leave most of a block idle.
-
-// Calls f(head, row, mine, seq(sequence)) for this thread's rows, the whole warp at once (mine false: some other
-// row that exists). seq, what a row needs to know of its sequence, is asked once per head where it can be.
-template <bool FLAT, int TPR, typename Seq, typename F>
-__device__ __forceinline__ void for_rows(unsigned flat_rows, int heads, int64_t rows, Seq seq, F f) {
-  constexpr int kRows = kQ4Threads / TPR;
-  if constexpr (FLAT) {
-    const unsigned at = blockIdx.x * kRows + threadIdx.x / TPR;
-    const bool mine = at < flat_rows;
-    const unsigned bh = mine ? at / (unsigned)rows : 0u;
-    f(bh, (int)(mine ? at - bh * (unsigned)rows : 0u), mine, seq((int)(bh / (unsigned)heads)));
-  } else {
-    const unsigned bh = blockIdx.y;
-    const auto known = seq((int)(bh / (unsigned)heads));
-    for (int r0 = (int)blockIdx.x * kRows; r0 < (int)rows; r0 += (int)gridDim.x * kRows) {
-      const int row = r0 + (int)threadIdx.x / TPR;
-      f(bh, row < (int)rows ? row : 0, row < (int)rows, known);
-    }
-  }
-}
-
 struct AppendSeq {
   int b, len, n;     // rows held, rows to write
   bool counts, fits; // n_new is in range; the rows fit
 };
 
 template <typename T, int D, bool FLAT>
-__global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(Q4Job a, unsigned flat_rows) {
+__global__ void __launch_bounds__(kRowThreads) q4_append_kernel(Q4Job a, unsigned flat_rows) {
   constexpr int W = kAppendWords<FLAT>;
   constexpr int kTpr = D / (8 * W), kTpg = 8 / W;   // threads per row, and per group
   constexpr int kNg = D / kQ4Group;
@@ -243,7 +206,7 @@ __device__ __forceinline__ void q4_values(const Q4Ones& one, uint32_t w, float h
 }
 
 template <typename T, int D, bool FLAT>
-__global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(Q4Job a, unsigned flat_rows, Q4Ones one) {
+__global__ void __launch_bounds__(kRowThreads) q4_read_kernel(Q4Job a, unsigned flat_rows, Q4Ones one) {
   constexpr int W = kReadWords;
   constexpr int kTpr = D / (8 * W), kTpg = 8 / W;
   constexpr int kNg = D / kQ4Group;
@@ -271,31 +234,14 @@ __global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(Q4Job a, unsigned f
   });
 }
 
-constexpr int64_t kFlatRows = 32;   // calls of fewer rows a head are one list
-
-// Blocks and threads: a flat list of few rows; else all blocks together are about `waves` waves of sixteen per
-// SM, so that a long prompt amortises a block's set-up over several turns. Writing a bf16 prompt of 16384 rows
-// and 32 heads (K and V: 344 MB of traffic, 51 us at 6.79 TB/s) takes 74 us in 2 waves, 77 in 1 and (in
-// blocks of 256 threads) 82 in 8; reading it back 79 in 2, 58 in 8 and 61 in 24. One row of 2048 heads: 3.0
-// and 2.3 us, 9.5 with a block per head.
-dim3 q4_grid(const Q4Job& job, int words, int waves) {
-  const int per_turn = kQ4Threads / (job.head_dim / (8 * words));
-  const int64_t bh = (int64_t)job.batch * job.heads;
-  if (job.rows < kFlatRows) return dim3((unsigned)((bh * job.rows + per_turn - 1) / per_turn), 1, 2);
-  const int64_t turns = (job.rows + per_turn - 1) / per_turn;
-  int64_t blocks = ((int64_t)device_sm_count() * 16 * waves + 2 * bh - 1) / (2 * bh);
-  if (blocks > turns) blocks = turns;
-  return dim3((unsigned)(blocks < 1 ? 1 : blocks), (unsigned)bh, 2);
-}
-
 template <typename T, int D, bool FLAT> cudaError_t q4_append_typed(const Q4Job& job) {
-  q4_append_kernel<T, D, FLAT><<<q4_grid(job, kAppendWords<FLAT>, 2), kQ4Threads, 0, job.stream>>>(
+  q4_append_kernel<T, D, FLAT><<<row_grid(job.batch, job.heads, job.rows, job.head_dim / (8 * kAppendWords<FLAT>), 2), kRowThreads, 0, job.stream>>>(
       job, FLAT ? (unsigned)(job.batch * job.heads * job.rows) : 0u);
   return cudaGetLastError();
 }
 
 template <typename T, int D, bool FLAT> cudaError_t q4_read_typed(const Q4Job& job) {
-  q4_read_kernel<T, D, FLAT><<<q4_grid(job, kReadWords, 8), kQ4Threads, 0, job.stream>>>(
+  q4_read_kernel<T, D, FLAT><<<row_grid(job.batch, job.heads, job.rows, job.head_dim / (8 * kReadWords), 8), kRowThreads, 0, job.stream>>>(
       job, FLAT ? (unsigned)(job.batch * job.heads * job.rows) : 0u, Q4Ones());
   return cudaGetLastError();
 }

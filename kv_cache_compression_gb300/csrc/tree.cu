@@ -1,0 +1,74 @@
+// Host side of the tree attention (see tree_schedule.cuh): workspace, the cut of a call, and which kernel takes it.
+#include <math.h>
+
+#include "tree_launch.h"
+#include "tree_schedule.cuh"
+
+namespace snapkv {
+namespace {
+
+size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Tiles of a call that are possible, all passes apart.
+int64_t most_tiles(int batch, int heads, int64_t passes, int tokens, int64_t cap, int tile) {
+  return (int64_t)batch * heads * passes * ((cap + tile - 1) / tile + (tokens + tile - 1) / tile);
+}
+
+size_t upto_bytes(int batch) { return up(((size_t)batch + 1) * sizeof(int64_t)); }
+
+size_t parts_bytes(int64_t ctas, int tile_q, int head_dim) {
+  return up((size_t)ctas * 2 * tile_q * (head_dim + 2) * sizeof(float));
+}
+
+int64_t bounded(int64_t tiles, int64_t most) { return tiles < most ? tiles : most; }
+
+}  // namespace
+
+size_t tree_workspace_bytes(int batch, int q_heads, int heads, int head_dim, int tokens, int64_t cap) {
+  const int64_t rows = (int64_t)(q_heads / heads) * tokens;
+  const int simt = rows <= 8 ? 8 : kSimtRows;
+  const int64_t ctas = bounded(most_tiles(batch, heads, (rows + simt - 1) / simt, tokens, cap, 64), kMaxTreeCtas);
+  return upto_bytes(batch) + parts_bytes(ctas, simt, head_dim);
+}
+
+tree::Args tree_args(const TreeJob& job, int tile_q) {
+  tree::Args a = {};
+  a.q = job.q;
+  a.k = job.k;
+  a.v = job.v;
+  a.k_step = static_cast<const float*>(job.k_step);
+  a.v_step = static_cast<const float*>(job.v_step);
+  a.len = job.len;
+  a.k_new = job.k_new;
+  a.v_new = job.v_new;
+  a.n_new = job.n_new;
+  a.mask = static_cast<const uint8_t*>(job.mask);
+  a.mask_stride = job.mask_stride;
+  a.out = job.out;
+  a.lse = job.lse;
+  a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)job.head_dim));
+  a.cap = job.cap;
+  a.batch = job.batch;
+  a.heads = job.heads;
+  a.group = job.q_heads / job.heads;
+  a.tokens = job.tokens;
+  a.tile_q = tile_q;
+  a.siblings = 1;
+  a.dev_status = job.dev_status;
+  return a;
+}
+
+cudaError_t tree_fill(tree::Args& a, const TreeJob& job, int head_dim, int tile, int64_t ctas) {
+  const int64_t rows = (int64_t)a.group * a.tokens, passes = (rows + a.tile_q - 1) / a.tile_q;
+  ctas = bounded(ctas, bounded(most_tiles(a.batch, a.heads, passes, a.tokens, a.cap, tile), kMaxTreeCtas));
+  a.ctas = (int)ctas;
+  char* ws = static_cast<char*>(job.workspace);
+  a.upto = reinterpret_cast<int64_t*>(ws);
+  a.parts = reinterpret_cast<float*>(ws + upto_bytes(a.batch));
+  (void)head_dim;
+  return cudaSuccess;
+}
+
+cudaError_t launch_tree(const TreeJob& job) { return launch_tree_simt(job); }
+
+}  // namespace snapkv

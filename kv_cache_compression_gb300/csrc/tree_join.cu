@@ -1,0 +1,108 @@
+// The second launch of the tree attention: joins the parts of the heads that the first launch cut, and writes the
+// rows that see nothing. All latency: a warp takes a query row, finds its parts from the schedule, and has a part's
+// maximum per lane and eight parts' channels under way at a time.
+#include "tree_schedule.cuh"
+
+#include "snapkv_internal.h"
+
+namespace snapkv {
+namespace {
+
+using namespace tree;
+constexpr int kJoinThreads = 256;
+
+template <int D> struct Vec;
+template <> struct Vec<64> { using T = float2; };
+template <> struct Vec<128> { using T = float4; };
+
+template <typename IO, int D, int TILE>
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(Args a) {
+  constexpr int kPer = D / 32;   // channels of a lane
+  const int lane = threadIdx.x % 32;
+  const int64_t rows = (int64_t)a.batch * a.heads * a.group * a.tokens;
+  const int64_t warps = (int64_t)gridDim.x * (kJoinThreads / 32);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t total = __ldcg(a.upto + a.batch);
+  const int shares = working_shares(a, total);
+  for (int64_t at = (int64_t)blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32; at < rows; at += warps) {
+    const int64_t hq = at / a.tokens;
+    const int t = (int)(at - hq * a.tokens);
+    const int bh = (int)(hq / a.group), g = (int)(hq - (int64_t)bh * a.group);
+    const int b = bh / a.heads, h = bh - b * a.heads;
+    const Seq s = seq_of<TILE>(a, b);
+    float x[kPer] = {}, top = kNoMax, sum = 0.f;
+    if (t < s.n && s.tiles > 0) {
+      const int r = g * s.n + t, pass = r / a.tile_q, i = r - pass * a.tile_q;
+      const int64_t f0 = __ldcg(a.upto + b) + ((int64_t)h * s.passes + (a.siblings > 1 ? 0 : pass)) * s.tiles;
+      const int c0 = share_of(total, shares, f0), more = share_of(total, shares, f0 + s.tiles - 1) - c0;
+      if (more == 0) continue;   // finished in the first launch
+      if (!in_bounds(c0 >= 0 && c0 + more < shares && i < a.tile_q, a.dev_status)) continue;
+      const int slot0 = share_start(total, shares, c0) < f0 ? 1 : 0;
+      const int sib = a.siblings > 1 ? pass : 0;
+      auto part = [&](int k) { return part_at<D>(a, (c0 + k) * a.siblings + sib, k == 0 ? slot0 : 0); };
+      for (int k0 = 0; k0 <= more; k0 += 32) {
+        const int here = min(32, more + 1 - k0);
+        float m = kNoMax, l = 0.f;
+        if (lane < here) {
+          const float* p = part(k0 + lane) + (int64_t)a.tile_q * D + i;
+          m = __ldcg(p);
+          l = __ldcg(p + a.tile_q);
+        }
+        const float next = fmaxf(top, warp_max(m));
+        const float f = rescale(m, next), old = rescale(top, next);
+        top = next;
+        sum = fmaf(sum, old, warp_sum(l * f));
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) x[e] *= old;
+        for (int k = 0; k < here; k += 8) {
+          typename Vec<D>::T v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (k + e < here) v[e] = __ldcg(reinterpret_cast<const typename Vec<D>::T*>(part(k0 + k + e) + (int64_t)i * D) + lane);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float w = __shfl_sync(0xffffffffu, f, (k + e) & 31);
+            if (k + e < here) {
+              const float* y = reinterpret_cast<const float*>(&v[e]);
+#pragma unroll
+              for (int c = 0; c < kPer; ++c) x[c] = fmaf(y[c], w, x[c]);
+            }
+          }
+        }
+      }
+    }
+    const float scale = sum == 0.f ? 0.f : 1.0f / sum;   // a NaN stays one
+    IO* out = static_cast<IO*>(a.out) + at * D + lane * kPer;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) store1<IO>(out + e, x[e] * scale);
+    if (a.lse && lane == 0) a.lse[at] = lse_of(top, sum);
+  }
+}
+
+}  // namespace
+
+template <typename IO, int D, int TILE> cudaError_t launch_tree_join(const Args& a, cudaStream_t stream) {
+  const int64_t rows = (int64_t)a.batch * a.heads * a.group * a.tokens;
+  int64_t blocks = (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+  const int64_t most = 8 * (int64_t)device_sm_count();
+  if (blocks > most) blocks = most;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_join_kernel<IO, D, TILE>, a);
+}
+
+#define INSTANCE(IO, D, TILE) template cudaError_t launch_tree_join<IO, D, TILE>(const Args&, cudaStream_t);
+INSTANCE(float, 64, 64)
+INSTANCE(float, 128, 64)
+INSTANCE(__nv_bfloat16, 64, 64)
+INSTANCE(__nv_bfloat16, 128, 64)
+#undef INSTANCE
+
+}  // namespace snapkv

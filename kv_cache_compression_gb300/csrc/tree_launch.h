@@ -1,0 +1,22 @@
+// Host side of the tree attention: how a call is cut, its workspace, and its launchers.
+#pragma once
+
+#include "draft_internal.h"
+
+namespace snapkv {
+
+namespace tree {
+struct Args;
+}
+
+constexpr int kMaxTreeCtas = 320;     // of a first launch: bounds the workspace, not tied to a device's SM count
+constexpr int kSimtRows = 32;         // query rows of a pass, at most
+
+// The call's arguments, for passes of `tile_q` query rows.
+tree::Args tree_args(const TreeJob& job, int tile_q);
+// Cuts the call for at most `ctas` CTAs of one wave with tiles of `tile` keys, and lays out its workspace.
+cudaError_t tree_fill(tree::Args& a, const TreeJob& job, int head_dim, int tile, int64_t ctas);
+
+cudaError_t launch_tree_simt(const TreeJob& job);
+
+}  // namespace snapkv

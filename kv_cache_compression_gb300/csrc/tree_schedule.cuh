@@ -1,0 +1,190 @@
+// What the kernels of the tree attention share: a call's arguments, how its work is cut, and the parts that are joined.
+//
+// The query rows of a KV head are (g, t), g < G query heads, t < n tokens that the sequence has: r = g n + t of M = G n.
+// A pass serves QT of them. The keys of a head are cut into tiles of TILE cached rows and, after those, TILE drafted rows.
+// All tiles of all heads (and passes) are one flat list, of which every share takes an equal, contiguous piece, whatever
+// the sequences' lengths: the end of one head, whole heads, the start of another. A head that lies in one share is
+// finished there; of others the shares leave parts (outputs not yet normalised, maxima, sums), and a second launch joins
+// them. Fixed order, no atomics: repeats give the same bits.
+//
+// With `siblings` = P > 1 the list has each head once, not once a pass, and a share belongs to P CTAs, a pass each, that
+// walk the same tiles side by side, so that all but the first read them from L2.
+#pragma once
+
+#include "draft_internal.h"
+#include "snapkv_common.cuh"
+
+namespace snapkv {
+namespace tree {
+
+struct Args {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* k_step;
+  const float* v_step;
+  const int32_t* len;
+  const void* k_new;
+  const void* v_new;
+  const int32_t* n_new;
+  const uint8_t* mask;
+  int64_t mask_stride;
+  void* out;
+  float* lse;
+  float scale_log2;     // log2(e) / sqrt(d)
+  int64_t cap;
+  int batch, heads, group, tokens;
+  int tile_q;           // query rows of a pass (of a part)
+  int ctas, siblings;   // of the first launch; shares = ctas / siblings
+  // workspace
+  int64_t* upto;        // [batch + 1]: tiles in the sequences before, and in all
+  float* parts;         // [ctas][2] of (o [tile_q][D], m [tile_q] (log2 domain), l [tile_q])
+  int32_t* dev_status;
+};
+
+constexpr float kNoMax = -3.402823466e38f;   // the lowest finite value, so that differences to it are no NaN
+
+__device__ __forceinline__ int cached_rows(const Args& a, int b) {
+  const int n = a.len[b];
+  return n < 0 ? 0 : (int64_t)n > a.cap ? (int)a.cap : n;
+}
+__device__ __forceinline__ int tokens_of(const Args& a, int b) {
+  const int n = a.n_new ? a.n_new[b] : a.tokens;
+  return n < 0 ? 0 : n > a.tokens ? a.tokens : n;
+}
+
+// A sequence: its cached rows, tokens, passes in the list and tiles of a pass.
+struct Seq {
+  int rows, n, passes, cache_tiles, tiles;
+  __device__ __forceinline__ int64_t units(int heads) const { return (int64_t)heads * passes * tiles; }
+};
+template <int TILE> __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
+  Seq s;
+  s.rows = cached_rows(a, b);
+  s.n = tokens_of(a, b);
+  s.passes = a.siblings > 1 ? 1 : (a.group * s.n + a.tile_q - 1) / a.tile_q;
+  s.cache_tiles = (s.rows + TILE - 1) / TILE;
+  s.tiles = s.n == 0 ? 0 : s.cache_tiles + (a.k_new ? (s.n + TILE - 1) / TILE : 0);
+  return s;
+}
+
+__device__ __forceinline__ int working_shares(const Args& a, int64_t total) {
+  const int shares = a.ctas / a.siblings;
+  return total < shares ? (int)total : shares;
+}
+// (shares <= 1024 and total <= 2^48: no product overflows)
+__device__ __forceinline__ int64_t share_start(int64_t total, int shares, int c) { return total * c / shares; }
+// The share that holds flat tile t: the last one that starts at or before it.
+__device__ __forceinline__ int share_of(int64_t total, int shares, int64_t t) {
+  int c = (int)(t * shares / total);
+  while (c + 1 < shares && share_start(total, shares, c + 1) <= t) ++c;
+  return c;
+}
+
+// Where a CTA's share lies: tiles at .. end - 1 of the list, from sequence `seq`, which starts at tile `before`.
+struct Share {
+  int64_t at, end, before;
+  int seq;
+};
+
+// All threads of a block of THREADS find their CTA's share (at == end: none). Sequence lengths are summed up by every
+// CTA for itself; CTA 0 leaves the sums for the joining launch and reports what is out of range.
+template <int TILE, int THREADS> __device__ __forceinline__ Share find_share(const Args& a) {
+  __shared__ int64_t warp_sums[THREADS / 32];
+  __shared__ Share found;
+  const int tid = threadIdx.x, lane = tid % 32;
+  const int chunk = (a.batch + THREADS - 1) / THREADS;
+  const int b0 = min(a.batch, tid * chunk), b1 = min(a.batch, b0 + chunk);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += seq_of<TILE>(a, b).units(a.heads);
+  int64_t x = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  if (lane == 31) warp_sums[tid / 32] = x;
+  if (tid == 0) found = Share{0, 0, 0, 0};
+  __syncthreads();
+  int64_t total = 0, upto = x - mine;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < tid / 32) upto += warp_sums[w];
+    total += warp_sums[w];
+  }
+  if (blockIdx.x == 0) {
+    int64_t sum = upto;
+    for (int b = b0; b < b1; ++b) {
+      a.upto[b] = sum;
+      sum += seq_of<TILE>(a, b).units(a.heads);
+      if ((int64_t)a.len[b] > a.cap) report(a.dev_status, SNAPKV_ERR_CAPACITY);
+      if (a.n_new && (a.n_new[b] < 0 || a.n_new[b] > a.tokens)) report(a.dev_status, SNAPKV_ERR_INVALID_ARG);
+    }
+    if (tid == 0) a.upto[a.batch] = total;
+  }
+  const int shares = working_shares(a, total), c = (int)blockIdx.x / a.siblings;
+  if (c < shares) {
+    const int64_t at = share_start(total, shares, c);
+    if (at >= upto && at < upto + mine) {
+      int b = b0;
+      for (int64_t u; at >= upto + (u = seq_of<TILE>(a, b).units(a.heads)); ++b) upto += u;
+      found = Share{at, share_start(total, shares, c + 1), upto, b};
+    }
+  }
+  __syncthreads();
+  return found;
+}
+
+// A place in the list: a tile of a head's pass, and what its sequence is.
+struct Place {
+  int seq, head, pass, tile;
+  Seq s;
+};
+template <int TILE> __device__ __forceinline__ Place first_place(const Args& a, const Share& share) {
+  Place p;
+  p.seq = share.seq;
+  p.s = seq_of<TILE>(a, p.seq);
+  const int64_t in = share.at - share.before;
+  const int64_t unit = in / p.s.tiles;
+  p.tile = (int)(in - unit * p.s.tiles);
+  p.head = (int)(unit / p.s.passes);
+  p.pass = (int)(unit - (int64_t)p.head * p.s.passes);
+  return p;
+}
+// The next head's (or pass's) first tile, which exists.
+template <int TILE> __device__ __forceinline__ void next_head(const Args& a, Place& p) {
+  p.tile = 0;
+  if (++p.pass < p.s.passes) return;
+  p.pass = 0;
+  if (++p.head < a.heads) return;
+  p.head = 0;
+  do p.s = seq_of<TILE>(a, ++p.seq);
+  while (p.s.tiles == 0);
+}
+
+// This CTA's pass of the place's head, and its query rows q0 .. q0 + count - 1 (count <= 0: none of this pass).
+__device__ __forceinline__ int pass_of(const Args& a, const Place& p) {
+  return a.siblings > 1 ? (int)blockIdx.x % a.siblings : p.pass;
+}
+
+template <int D> __device__ __forceinline__ float* part_at(const Args& a, int cta, int slot) {
+  return a.parts + ((int64_t)cta * 2 + slot) * a.tile_q * (D + 2);
+}
+
+// What sums that belong to maximum m are multiplied by under the maximum `top` (of at least m).
+__device__ __forceinline__ float rescale(float m, float top) { return ex2(m - top); }
+
+template <typename T> __device__ __forceinline__ void store1(T* p, float x);
+template <> __device__ __forceinline__ void store1<float>(float* p, float x) { *p = x; }
+template <> __device__ __forceinline__ void store1<__nv_bfloat16>(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// log of sum exp from the maximum (log2 domain) and the sum under it.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+}  // namespace tree
+
+// The joining launch: out and lse of the rows whose heads were cut, and of those that see nothing.
+template <typename IO, int D, int TILE> cudaError_t launch_tree_join(const tree::Args& a, cudaStream_t stream);
+
+}  // namespace snapkv

@@ -1,0 +1,355 @@
+// Tree attention in fp32 instructions: fp32 calls, over a dense cache or one in 8 bits (tree_schedule.cuh has the schedule).
+//
+//   s_rk = q_r . k_k / sqrt(d) over the keys k that row r sees,  p = softmax,  o_r = sum p_rk v_k
+//
+// A CTA walks its share of the 64-key tiles with an online softmax: products of QT query rows with a tile's keys (each
+// thread some rows by some keys, channels in steps of four), weights through shared memory, and products with the
+// tile's values (each thread four rows by four channels of a KS-th of the keys). Products and sums are fp32 FMAs that
+// round to nearest, which tensor cores do not: their cut sums and three bf16 parts an operand would cost six products.
+// K's and V's tiles have a buffer each: V's rows are under way while the logits are computed, the next K's while the
+// outputs are, and a second CTA per SM fills the rest.
+#include "tree_schedule.cuh"
+
+#include <atomic>
+
+#include "cache_internal.h"
+#include "q4.cuh"
+#include "sm100_ptx.cuh"
+#include "snapkv_internal.h"
+#include "tree_launch.h"
+
+namespace snapkv {
+namespace {
+
+using namespace tree;
+
+constexpr int kThreads = 256;
+constexpr int kTile = 64;   // keys
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// A tile: where its rows lie, and how many it has.
+struct Rows {
+  const void* k;
+  const void* v;
+  const float* k_step;   // null: rows of the call's type
+  const float* v_step;
+  int count;             // rows of the tile that may be seen (the rest of kTile is zeros)
+  int draft0;            // the first one's number among the drafted rows; -1: cached rows
+};
+
+template <typename IO, bool Q8, int D> __device__ __forceinline__ Rows rows_of(const Args& a, const Place& p) {
+  Rows r;
+  const int64_t bh = (int64_t)p.seq * a.heads + p.head;
+  if (p.tile < p.s.cache_tiles) {
+    const int64_t row = bh * a.cap + (int64_t)p.tile * kTile;
+    const int64_t bytes = Q8 ? D : D * (int)sizeof(IO);
+    r.k = static_cast<const uint8_t*>(a.k) + row * bytes;
+    r.v = static_cast<const uint8_t*>(a.v) + row * bytes;
+    r.k_step = Q8 ? a.k_step + row : nullptr;
+    r.v_step = Q8 ? a.v_step + row : nullptr;
+    r.count = min(kTile, p.s.rows - p.tile * kTile);
+    r.draft0 = -1;
+    if (!in_bounds(row >= 0 && row + r.count <= (int64_t)a.batch * a.heads * a.cap, a.dev_status)) r.count = 0;
+  } else {
+    r.draft0 = (p.tile - p.s.cache_tiles) * kTile;
+    const int64_t row = bh * a.tokens + r.draft0;
+    r.k = static_cast<const IO*>(a.k_new) + row * D;
+    r.v = static_cast<const IO*>(a.v_new) + row * D;
+    r.k_step = r.v_step = nullptr;
+    r.count = min(kTile, p.s.n - r.draft0);
+    if (!in_bounds(row >= 0 && row + r.count <= (int64_t)a.batch * a.heads * a.tokens, a.dev_status)) r.count = 0;
+  }
+  return r;
+}
+
+// Four values of a row from codes, or of IO.
+template <typename IO> __device__ __forceinline__ float4 widen4(const IO* p) {
+  if constexpr (sizeof(IO) == 4) return *reinterpret_cast<const float4*>(p);
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ float code_value(uint32_t byte, float h) {
+  const float v = (__uint_as_float(0x4B000000u | (byte & 0x7Fu)) - 8388608.0f) * h;
+  return __uint_as_float(__float_as_uint(v) ^ ((byte & 0x80u) << 24));
+}
+
+// Copies a tile's rows to `to` as fp32, a row's 16-byte pieces XORed with hash(row); rows past `count` become zeros.
+// fp32 rows are only on their way (cp.async) when it returns.
+template <typename IO, int D, typename Hash>
+__device__ __forceinline__ void load_rows(float* to, const void* from, const float* step, int count, Hash hash) {
+  constexpr int kPieces = D / 4;
+#pragma unroll 4
+  for (int u = threadIdx.x; u < kTile * kPieces; u += kThreads) {
+    const int row = u / kPieces, c = u % kPieces;
+    float* dst = to + row * D + 4 * (c ^ hash(row));
+    const bool there = row < count;
+    if (step) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (there) {
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(from) + row * kPieces + c);
+        const float h = __ldg(step + row);
+        x = make_float4(code_value(w & 0xFF, h), code_value((w >> 8) & 0xFF, h), code_value((w >> 16) & 0xFF, h), code_value(w >> 24, h));
+      }
+      *reinterpret_cast<float4*>(dst) = x;
+    } else if constexpr (sizeof(IO) == 4) {
+      const float* src = static_cast<const float*>(from) + (there ? (int64_t)u * 4 : 0);
+      cp_async16(dst, src, there);
+    } else {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (there) x = widen4<IO>(static_cast<const IO*>(from) + (int64_t)u * 4);
+      *reinterpret_cast<float4*>(dst) = x;
+    }
+  }
+}
+
+template <int D, int QT> struct Shape {
+  static constexpr int kRq = QT == 32 ? 4 : 2, kRk = QT == 32 ? 2 : 1;      // logits of a thread: rows by keys
+  static constexpr int kQg = QT / kRq;                                      // threads along the rows
+  static_assert(kQg * (kTile / kRk) == kThreads, "a thread for every block of logits");
+  static constexpr int kKs = kThreads * 16 / (QT * D);                      // key groups of the second product
+  static constexpr int kPs = QT + 4;                                        // floats between two keys' weights
+  static constexpr int smem() { return 4 * (QT * D + 2 * kTile * D + kTile * kPs + 3 * QT); }
+};
+
+template <typename IO, bool Q8, int D, int QT>
+__global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
+  using S = Shape<D, QT>;
+  constexpr int kRq = S::kRq, kRk = S::kRk, kKs = S::kKs, kPs = S::kPs;
+  extern __shared__ __align__(16) float smem[];
+  float* const qs = smem;                  // [QT][D], pieces XORed
+  float* const ks = qs + QT * D;           // [kTile][D], pieces XORed
+  float* const vs = ks + kTile * D;        // [kTile][D]
+  float* const ps = vs + kTile * D;        // [kTile][kPs]: logits, then weights
+  float* const ms = ps + kTile * kPs;      // [QT]: running maxima, sums, and this tile's factors
+  float* const ls = ms + QT;
+  float* const fs = ls + QT;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  auto q_hash = [](int row) { return (row / kRq) & 7; };
+  auto k_hash = [](int row) { return (row / kRk) & 7; };
+  auto v_hash = [](int) { return 0; };
+  const Share share = find_share<kTile, kThreads>(a);
+  if (share.at >= share.end) return;
+  Place here = first_place<kTile>(a, share);
+  // first product: rows kRq qg .. by keys kRk kg ..
+  const int qg = tid % S::kQg, kg = tid / S::kQg;
+  // second product: rows 4 og .. by channels 4 cg .. of the keys of group kh
+  const int kh = tid / (kThreads / kKs), in = tid % (kThreads / kKs);
+  constexpr int kOg = QT / 4;
+  constexpr int kOw = kOg < 4 ? kOg : 4;   // of a warp's lanes along the rows
+  const int cg = (in / kOw) % (D / 4), og = in % kOw + kOw * (in / (kOw * (D / 4)));
+
+  int64_t at = share.at;
+  while (at < share.end) {
+    const int64_t left = share.end - at;
+    const int seg = left < here.s.tiles - here.tile ? (int)left : here.s.tiles - here.tile;   // tiles of this head in this share
+    const bool whole = seg == here.s.tiles;
+    const int pass = pass_of(a, here), r0 = pass * a.tile_q, n = here.s.n;
+    const int count = min(a.tile_q, a.group * n - r0);   // (at least one: passes follow from the rows there are)
+    const int64_t bh = (int64_t)here.seq * a.heads + here.head;
+    auto row_at = [&](int i) {   // the query row in [B, Hq, T]
+      const int r = r0 + i, g = r / n;
+      return (bh * a.group + g) * a.tokens + (r - g * n);
+    };
+    // ---- queries, and the first tile's keys
+    Rows tile = rows_of<IO, Q8, D>(a, here);
+    load_rows<IO, D>(ks, tile.k, tile.k_step, tile.count, k_hash);
+    cp_commit();
+    for (int u = tid; u < QT * (D / 4); u += kThreads) {
+      const int i = u / (D / 4), c = u % (D / 4);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < count) x = widen4<IO>(static_cast<const IO*>(a.q) + row_at(i) * D + 4 * c);
+      *reinterpret_cast<float4*>(qs + i * D + 4 * (c ^ q_hash(i))) = x;
+    }
+    for (int i = tid; i < QT; i += kThreads) {
+      ms[i] = kNoMax;
+      ls[i] = 0.f;
+    }
+    float2 o[4][2];   // rows by pairs of channels
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r][0] = o[r][1] = make_float2(0.f, 0.f);
+
+    for (int j = 0; j < seg; ++j, ++here.tile) {
+      load_rows<IO, D>(vs, tile.v, tile.v_step, tile.count, v_hash);
+      cp_commit();
+      cp_wait<1>();
+      __syncthreads();   // K and Q are there
+      // ---- logits
+      float2 s[kRq][kRk];
+#pragma unroll
+      for (int x = 0; x < kRq; ++x)
+#pragma unroll
+        for (int y = 0; y < kRk; ++y) s[x][y] = make_float2(0.f, 0.f);
+#pragma unroll 4
+      for (int c = 0; c < D / 4; ++c) {
+        float4 qv[kRq], kv[kRk];
+#pragma unroll
+        for (int x = 0; x < kRq; ++x) qv[x] = *reinterpret_cast<const float4*>(qs + (kRq * qg + x) * D + 4 * (c ^ (qg & 7)));
+#pragma unroll
+        for (int y = 0; y < kRk; ++y) kv[y] = *reinterpret_cast<const float4*>(ks + (kRk * kg + y) * D + 4 * (c ^ (kg & 7)));
+#pragma unroll
+        for (int x = 0; x < kRq; ++x)
+#pragma unroll
+          for (int y = 0; y < kRk; ++y) {
+            s[x][y] = fma2(make_float2(qv[x].x, qv[x].y), make_float2(kv[y].x, kv[y].y), s[x][y]);
+            s[x][y] = fma2(make_float2(qv[x].z, qv[x].w), make_float2(kv[y].z, kv[y].w), s[x][y]);
+          }
+      }
+#pragma unroll
+      for (int y = 0; y < kRk; ++y) {
+        const int key = kRk * kg + y;
+        float l[kRq];
+#pragma unroll
+        for (int x = 0; x < kRq; ++x) {
+          l[x] = (s[x][y].x + s[x][y].y) * a.scale_log2;
+          bool seen = key < tile.count;
+          if (tile.draft0 >= 0 && seen) {
+            const int i = kRq * qg + x;
+            const int t = (r0 + i) % n, k = tile.draft0 + key;
+            seen = i < count && (a.mask ? a.mask[here.seq * a.mask_stride + (int64_t)t * a.tokens + k] != 0 : k <= t);
+          }
+          if (!seen) l[x] = -INFINITY;
+        }
+        if constexpr (kRq == 4)
+          *reinterpret_cast<float4*>(ps + key * kPs + 4 * qg) = make_float4(l[0], l[1], l[2], l[3]);
+        else
+          *reinterpret_cast<float2*>(ps + key * kPs + 2 * qg) = make_float2(l[0], l[1]);
+      }
+      __syncthreads();   // the logits are there, and K's buffer is free
+      const Rows now = tile;
+      if (j + 1 < seg) {
+        Place next = here;
+        ++next.tile;
+        tile = rows_of<IO, Q8, D>(a, next);
+        load_rows<IO, D>(ks, tile.k, tile.k_step, tile.count, k_hash);
+      }
+      cp_commit();
+      // ---- weights: eight lanes a row
+      for (int r = warp * 4 + lane % 4; r < QT; r += 32) {
+        float* p = ps + (lane / 4) * kPs + r;
+        float x[kTile / 8], top = kNoMax;
+#pragma unroll
+        for (int e = 0; e < kTile / 8; ++e) {
+          x[e] = p[8 * e * kPs];
+          top = fmaxf(top, x[e]);
+        }
+        const unsigned lanes = __activemask();
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, off));
+        const float old = ms[r], m = fmaxf(old, top);
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < kTile / 8; ++e) {
+          x[e] = ex2(x[e] - m);
+          sum += x[e];
+          p[8 * e * kPs] = x[e];
+        }
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(lanes, sum, off);
+        __syncwarp(lanes);
+        if (lane / 4 == 0) {
+          const float f = rescale(old, m);
+          fs[r] = f;
+          ms[r] = m;
+          ls[r] = fmaf(ls[r], f, sum);
+        }
+      }
+      cp_wait<1>();
+      __syncthreads();   // the weights and V are there
+      // ---- outputs
+      const float4 f = *reinterpret_cast<const float4*>(fs + 4 * og);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float fr = r == 0 ? f.x : r == 1 ? f.y : r == 2 ? f.z : f.w;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) o[r][c] = mul2(o[r][c], make_float2(fr, fr));
+      }
+      // A row that nobody may see (or that is masked) has weight zero, but its values may be anything: a drafted
+      // row's infinity or NaN must not reach the rows that do not see it.
+      const bool careful = now.draft0 >= 0;
+#pragma unroll 4
+      for (int e = 0; e < kTile / kKs; ++e) {
+        const int key = kh + e * kKs;
+        const float4 w = *reinterpret_cast<const float4*>(ps + key * kPs + 4 * og);
+        const float4 v = *reinterpret_cast<const float4*>(vs + key * D + 4 * cg);
+        const float wr[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float2 ww = make_float2(wr[r], wr[r]);
+          if (!careful || wr[r] != 0.f) {
+            o[r][0] = fma2(ww, make_float2(v.x, v.y), o[r][0]);
+            o[r][1] = fma2(ww, make_float2(v.z, v.w), o[r][1]);
+          }
+        }
+      }
+      __syncthreads();   // V's buffer and the weights are free
+    }
+
+    // ---- the head's end in this share: the key groups meet, in the keys' buffer
+    float* const meet = ks;   // [kKs][QT][D]
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      *reinterpret_cast<float4*>(meet + (kh * QT + 4 * og + r) * D + 4 * cg) = make_float4(o[r][0].x, o[r][0].y, o[r][1].x, o[r][1].y);
+    __syncthreads();
+    float* const part = part_at<D>(a, (int)blockIdx.x, at > share.at ? 1 : 0);
+    for (int u = tid; u < count * D; u += kThreads) {
+      const int i = u / D, c = u % D;
+      float x = meet[u];
+#pragma unroll
+      for (int g = 1; g < kKs; ++g) x += meet[g * QT * D + u];
+      if (whole)
+        store1<IO>(static_cast<IO*>(a.out) + row_at(i) * D + c, x * (ls[i] == 0.f ? 0.f : 1.0f / ls[i]));
+      else
+        part[u] = x;
+    }
+    for (int i = tid; i < count; i += kThreads) {
+      if (!whole) {
+        part[a.tile_q * D + i] = ms[i];
+        part[a.tile_q * (D + 1) + i] = ls[i];
+      } else if (a.lse) {
+        a.lse[row_at(i)] = lse_of(ms[i], ls[i]);
+      }
+    }
+    __syncthreads();
+    at += seg;
+    if (at < share.end) next_head<kTile>(a, here);
+  }
+  cp_wait<0>();
+}
+
+template <typename IO, bool Q8, int D, int QT> cudaError_t launch_typed(const TreeJob& job) {
+  using S = Shape<D, QT>;
+  Args a = tree_args(job, QT);
+  cudaError_t err = allow_dynamic_smem<tree_simt_kernel<IO, Q8, D, QT>>(S::smem());
+  if (err != cudaSuccess) return err;
+  int64_t ctas = 2 * (int64_t)device_sm_count();
+  err = tree_fill(a, job, D, kTile, ctas);
+  if (err != cudaSuccess) return err;
+  tree_simt_kernel<IO, Q8, D, QT><<<a.ctas, kThreads, S::smem(), job.stream>>>(a);
+  err = cudaGetLastError();
+  return err != cudaSuccess ? err : launch_tree_join<IO, D, kTile>(a, job.stream);
+}
+
+template <typename IO, bool Q8, int D> cudaError_t launch_dim(const TreeJob& job) {
+  const int rows = job.q_heads / job.heads * job.tokens;
+  return rows <= 8 ? launch_typed<IO, Q8, D, 8>(job) : launch_typed<IO, Q8, D, 32>(job);
+}
+
+template <typename IO, bool Q8> cudaError_t launch_format(const TreeJob& job) {
+  return job.head_dim == 64 ? launch_dim<IO, Q8, 64>(job) : launch_dim<IO, Q8, 128>(job);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_simt(const TreeJob& job) {
+  if (job.dtype == SNAPKV_F32) return job.k_step ? launch_format<float, true>(job) : launch_format<float, false>(job);
+  return job.k_step ? launch_format<__nv_bfloat16, true>(job) : launch_format<__nv_bfloat16, false>(job);
+}
+
+}  // namespace snapkv

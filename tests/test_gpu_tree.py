@@ -1,0 +1,84 @@
+"""Tree attention over dense and 8-bit caches against the fp64 oracle (include/snapkv_draft.h)."""
+import numpy as np
+import pytest
+import torch
+
+import kv_cache_compression_gb300 as kv
+from tests.cache_cases import to64
+from tests.draft_cases import check_tree, q8_rows, random_tree
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+def make(dev, seed, B, H, G, d, T, cap, dtype, *, q8=False, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    x = {"q": (torch.randn(B, H * G, T, d, generator=g) * 1.5 * scale).to(dtype)}
+    for n in ("k", "v"):
+        rows = torch.randn(B, H, cap, d, generator=g).to(dtype)
+        if q8:
+            code, step, x[n + "64"] = q8_rows(rows.double().numpy())
+            x[n + "_codes"], x[n + "_step"] = code.to(dev), step.to(dev)
+        else:
+            x[n], x[n + "64"] = rows.to(dev), rows.double().numpy()
+        x[n + "_new"] = torch.randn(B, H, T, d, generator=g).to(dtype).to(dev)
+    x["q"] = x["q"].to(dev)
+    return x
+
+
+def run(x, lens, *, drafts=True, mask=None, n_new=None, lse=True, **kw):
+    dev = x["q"].device
+    B, Hq, T, d = x["q"].shape
+    lens = torch.tensor(lens, dtype=torch.int32, device=dev)
+    n = None if n_new is None else torch.tensor(n_new, dtype=torch.int32, device=dev)
+    m = None if mask is None else torch.from_numpy(mask).to(dev)
+    ls = torch.full((B, Hq, T), float("nan"), device=dev) if lse else None
+    new = (x["k_new"], x["v_new"], m) if drafts else ()
+    out = torch.full_like(x["q"], float("nan"))
+    if "k" in x:
+        kv.tree_attend(x["q"], x["k"], x["v"], lens, *new, n_new=n, lse=ls, out=out, **kw)
+    else:
+        cache = kv.Q8Cache(x["k_codes"], x["k_step"], x["v_codes"], x["v_step"])
+        kv.q8_tree_attend(x["q"], cache, lens, *new, n_new=n, lse=ls, out=out, **kw)
+    return out, ls
+
+
+def check(x, lens, out, lse, *, drafts=True, mask=None, n_new=None, **kw):
+    new = dict(k_new=x["k_new"], v_new=x["v_new"], mask=mask) if drafts else {}
+    check_tree(x["q"], x["k64"], x["v64"], lens, out, lse, n_new=n_new, **new, **kw)
+
+
+SHAPES = [  # B, H, G, d, T, cap, lengths
+    (1, 1, 1, 64, 1, 1, [1]), (1, 2, 1, 128, 1, 17, [0]), (2, 1, 1, 64, 3, 63, [63, 0]), (1, 4, 1, 64, 5, 83, [83]),
+    (2, 3, 2, 128, 4, 65, [64, 65]), (3, 2, 4, 64, 16, 129, [128, 1, 129]), (2, 2, 7, 128, 9, 200, [200, 127]),
+    (1, 2, 4, 128, 33, 300, [257]), (1, 1, 8, 128, 64, 500, [499]), (2, 1, 4, 64, 65, 130, [130, 5]), (1, 1, 3, 64, 130, 70, [70]),
+    (5, 2, 1, 128, 2, 1500, [1500, 3, 0, 700, 1024]), (1, 2, 1, 64, 8, 4000, [3999]),
+]
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s[:6])))
+def test_trees(gpu_device, shape, dtype, q8):
+    B, H, G, d, T, cap, lens = shape
+    x = make(gpu_device, 7, B, H, G, d, T, cap, dtype, q8=q8)
+    mask = random_tree(np.random.default_rng(T), B, T)
+    out, lse = run(x, lens, mask=mask)
+    check(x, lens, out, lse, mask=mask)
+    again, lse2 = run(x, lens, mask=mask)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+@pytest.mark.parametrize("shape", SHAPES[1:11:2], ids=lambda s: "x".join(map(str, s[:6])))
+def test_causal_ragged_and_without_drafts(gpu_device, shape, dtype, q8):
+    B, H, G, d, T, cap, lens = shape
+    x = make(gpu_device, 8, B, H, G, d, T, cap, dtype, q8=q8)
+    n_new = [(T * (b + 1) // B) if b else T // 2 for b in range(B)]
+    for drafts in (True, False):
+        out, lse = run(x, lens, drafts=drafts, n_new=n_new)
+        check(x, lens, out, lse, drafts=drafts, n_new=n_new)
+        out, lse = run(x, lens, drafts=drafts)
+        check(x, lens, out, lse, drafts=drafts)

@@ -1,7 +1,9 @@
 // Host side of the tree attention (see tree_schedule.cuh): workspace, the cut of a call, and which kernel takes it.
 #include <math.h>
 
+#include "tc_common.cuh"
 #include "tree_launch.h"
+#include "tree_maps.h"
 #include "tree_schedule.cuh"
 
 namespace snapkv {
@@ -10,8 +12,8 @@ namespace {
 size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Tiles of a call that are possible, all passes apart.
-int64_t most_tiles(int batch, int heads, int64_t passes, int tokens, int64_t cap, int tile) {
-  return (int64_t)batch * heads * passes * ((cap + tile - 1) / tile + (tokens + tile - 1) / tile);
+int64_t most_tiles(int batch, int heads, int64_t passes, int tokens, int64_t cap, int tile, int fresh) {
+  return (int64_t)batch * heads * passes * ((cap + tile - 1) / tile + (tokens + fresh - 1) / fresh);
 }
 
 size_t upto_bytes(int batch) { return up(((size_t)batch + 1) * sizeof(int64_t)); }
@@ -27,7 +29,7 @@ int64_t bounded(int64_t tiles, int64_t most) { return tiles < most ? tiles : mos
 size_t tree_workspace_bytes(int batch, int q_heads, int heads, int head_dim, int tokens, int64_t cap) {
   const int64_t rows = (int64_t)(q_heads / heads) * tokens;
   const int simt = rows <= 8 ? 8 : kSimtRows;
-  const int64_t ctas = bounded(most_tiles(batch, heads, (rows + simt - 1) / simt, tokens, cap, 64), kMaxTreeCtas);
+  const int64_t ctas = bounded(most_tiles(batch, heads, (rows + simt - 1) / simt, tokens, cap, 16, 16), kMaxTreeCtas);
   return upto_bytes(batch) + parts_bytes(ctas, simt, head_dim);
 }
 
@@ -54,21 +56,57 @@ tree::Args tree_args(const TreeJob& job, int tile_q) {
   a.tokens = job.tokens;
   a.tile_q = tile_q;
   a.siblings = 1;
+  a.least = 1;
   a.dev_status = job.dev_status;
   return a;
 }
 
-cudaError_t tree_fill(tree::Args& a, const TreeJob& job, int head_dim, int tile, int64_t ctas) {
+cudaError_t tree_fill(tree::Args& a, const TreeJob& job, int tile, int fresh, int64_t ctas) {
   const int64_t rows = (int64_t)a.group * a.tokens, passes = (rows + a.tile_q - 1) / a.tile_q;
-  ctas = bounded(ctas, bounded(most_tiles(a.batch, a.heads, passes, a.tokens, a.cap, tile), kMaxTreeCtas));
-  a.ctas = (int)ctas;
+  a.ctas = (int)bounded(ctas, bounded(most_tiles(a.batch, a.heads, passes, a.tokens, a.cap, tile, fresh), kMaxTreeCtas));
   char* ws = static_cast<char*>(job.workspace);
   a.upto = reinterpret_cast<int64_t*>(ws);
   a.parts = reinterpret_cast<float*>(ws + upto_bytes(a.batch));
-  (void)head_dim;
   return cudaSuccess;
 }
 
-cudaError_t launch_tree(const TreeJob& job) { return launch_tree_simt(job); }
+namespace {
+
+bool code_map(CUtensorMap* map, const void* codes, const TreeJob& job, int tile) {
+  auto enc = tc::encode_fn();
+  if (!enc) return false;
+  const int d = job.head_dim;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)job.cap, (cuuint64_t)job.batch * job.heads};
+  const cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)job.cap * d};
+  const cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)tile, 1}, one[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool tree_maps(TreeMaps* maps, const TreeJob& job, int tile, int fresh) {
+  const int64_t bh = (int64_t)job.batch * job.heads;
+  if (job.k_step) {
+    if (!code_map(&maps->k, job.k, job, tile) || !code_map(&maps->v, job.v, job, tile)) return false;
+  } else if (!tc::make_map(&maps->k, job.k, job.head_dim, job.cap, bh, tile) ||
+             !tc::make_map(&maps->v, job.v, job.head_dim, job.cap, bh, tile)) {
+    return false;
+  }
+  if (!job.k_new) {
+    maps->k_new = maps->k;
+    maps->v_new = maps->v;
+    return true;
+  }
+  return tc::make_map(&maps->k_new, job.k_new, job.head_dim, job.tokens, bh, fresh) &&
+         tc::make_map(&maps->v_new, job.v_new, job.head_dim, job.tokens, bh, fresh);
+}
+
+cudaError_t launch_tree(const TreeJob& job) {
+  if (job.dtype == SNAPKV_F32) return launch_tree_simt(job);
+  const int64_t rows = (int64_t)(job.q_heads / job.heads) * job.tokens;
+  return rows <= 16 ? launch_tree_mma(job) : launch_tree_simt(job);
+}
 
 }  // namespace snapkv

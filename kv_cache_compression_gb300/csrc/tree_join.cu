@@ -15,7 +15,7 @@ template <int D> struct Vec;
 template <> struct Vec<64> { using T = float2; };
 template <> struct Vec<128> { using T = float4; };
 
-template <typename IO, int D, int TILE>
+template <typename IO, int D, int TILE, int NEW>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(Args a) {
   constexpr int kPer = D / 32;   // channels of a lane
   const int lane = threadIdx.x % 32;
@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(Args a) {
     const int t = (int)(at - hq * a.tokens);
     const int bh = (int)(hq / a.group), g = (int)(hq - (int64_t)bh * a.group);
     const int b = bh / a.heads, h = bh - b * a.heads;
-    const Seq s = seq_of<TILE>(a, b);
+    const Seq s = seq_of<TILE, NEW>(a, b);
     float x[kPer] = {}, top = kNoMax, sum = 0.f;
     if (t < s.n && s.tiles > 0) {
       const int r = g * s.n + t, pass = r / a.tile_q, i = r - pass * a.tile_q;
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(Args a) {
 
 }  // namespace
 
-template <typename IO, int D, int TILE> cudaError_t launch_tree_join(const Args& a, cudaStream_t stream) {
+template <typename IO, int D, int TILE, int NEW> cudaError_t launch_tree_join(const Args& a, cudaStream_t stream) {
   const int64_t rows = (int64_t)a.batch * a.heads * a.group * a.tokens;
   int64_t blocks = (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
   const int64_t most = 8 * (int64_t)device_sm_count();
@@ -95,14 +95,17 @@ template <typename IO, int D, int TILE> cudaError_t launch_tree_join(const Args&
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_join_kernel<IO, D, TILE>, a);
+  return cudaLaunchKernelEx(&cfg, tree_join_kernel<IO, D, TILE, NEW>, a);
 }
 
-#define INSTANCE(IO, D, TILE) template cudaError_t launch_tree_join<IO, D, TILE>(const Args&, cudaStream_t);
-INSTANCE(float, 64, 64)
-INSTANCE(float, 128, 64)
-INSTANCE(__nv_bfloat16, 64, 64)
-INSTANCE(__nv_bfloat16, 128, 64)
+#define INSTANCE(IO, D, TILE, NEW) template cudaError_t launch_tree_join<IO, D, TILE, NEW>(const Args&, cudaStream_t);
+INSTANCE(float, 64, 64, 64)
+INSTANCE(float, 128, 64, 64)
+INSTANCE(__nv_bfloat16, 64, 64, 64)
+INSTANCE(__nv_bfloat16, 128, 64, 64)
+INSTANCE(__nv_bfloat16, 64, 32, 16)
+INSTANCE(__nv_bfloat16, 128, 32, 16)
+INSTANCE(__nv_bfloat16, 128, 16, 16)
 #undef INSTANCE
 
 }  // namespace snapkv

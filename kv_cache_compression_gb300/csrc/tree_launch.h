@@ -14,9 +14,11 @@ constexpr int kSimtRows = 32;         // query rows of a pass, at most
 
 // The call's arguments, for passes of `tile_q` query rows.
 tree::Args tree_args(const TreeJob& job, int tile_q);
-// Cuts the call for at most `ctas` CTAs of one wave with tiles of `tile` keys, and lays out its workspace.
-cudaError_t tree_fill(tree::Args& a, const TreeJob& job, int head_dim, int tile, int64_t ctas);
+// Cuts the call for at most `ctas` CTAs of one wave with tiles of `tile` cached and `fresh` drafted rows, and lays out
+// its workspace.
+cudaError_t tree_fill(tree::Args& a, const TreeJob& job, int tile, int fresh, int64_t ctas);
 
-cudaError_t launch_tree_simt(const TreeJob& job);
+cudaError_t launch_tree_simt(const TreeJob& job);   // fp32 instructions: fp32 calls
+cudaError_t launch_tree_mma(const TreeJob& job);    // mma.sync: bf16 calls of up to sixteen query rows a KV head
 
 }  // namespace snapkv

@@ -1,7 +1,7 @@
 // What the kernels of the tree attention share: a call's arguments, how its work is cut, and the parts that are joined.
 //
 // The query rows of a KV head are (g, t), g < G query heads, t < n tokens that the sequence has: r = g n + t of M = G n.
-// A pass serves QT of them. The keys of a head are cut into tiles of TILE cached rows and, after those, TILE drafted rows.
+// A pass serves QT of them. The keys of a head are cut into tiles of TILE cached rows and, after those, NEW drafted rows.
 // All tiles of all heads (and passes) are one flat list, of which every share takes an equal, contiguous piece, whatever
 // the sequences' lengths: the end of one head, whole heads, the start of another. A head that lies in one share is
 // finished there; of others the shares leave parts (outputs not yet normalised, maxima, sums), and a second launch joins
@@ -36,6 +36,7 @@ struct Args {
   int batch, heads, group, tokens;
   int tile_q;           // query rows of a pass (of a part)
   int ctas, siblings;   // of the first launch; shares = ctas / siblings
+  int least;            // tiles that a share has at least, where there are as many
   // workspace
   int64_t* upto;        // [batch + 1]: tiles in the sequences before, and in all
   float* parts;         // [ctas][2] of (o [tile_q][D], m [tile_q] (log2 domain), l [tile_q])
@@ -58,19 +59,19 @@ struct Seq {
   int rows, n, passes, cache_tiles, tiles;
   __device__ __forceinline__ int64_t units(int heads) const { return (int64_t)heads * passes * tiles; }
 };
-template <int TILE> __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
+template <int TILE, int NEW> __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
   Seq s;
   s.rows = cached_rows(a, b);
   s.n = tokens_of(a, b);
   s.passes = a.siblings > 1 ? 1 : (a.group * s.n + a.tile_q - 1) / a.tile_q;
   s.cache_tiles = (s.rows + TILE - 1) / TILE;
-  s.tiles = s.n == 0 ? 0 : s.cache_tiles + (a.k_new ? (s.n + TILE - 1) / TILE : 0);
+  s.tiles = s.n == 0 ? 0 : s.cache_tiles + (a.k_new ? (s.n + NEW - 1) / NEW : 0);
   return s;
 }
 
 __device__ __forceinline__ int working_shares(const Args& a, int64_t total) {
-  const int shares = a.ctas / a.siblings;
-  return total < shares ? (int)total : shares;
+  const int64_t shares = a.ctas / a.siblings, most = (total + a.least - 1) / a.least;
+  return (int)(most < shares ? most : shares);
 }
 // (shares <= 1024 and total <= 2^48: no product overflows)
 __device__ __forceinline__ int64_t share_start(int64_t total, int shares, int c) { return total * c / shares; }
@@ -89,14 +90,14 @@ struct Share {
 
 // All threads of a block of THREADS find their CTA's share (at == end: none). Sequence lengths are summed up by every
 // CTA for itself; CTA 0 leaves the sums for the joining launch and reports what is out of range.
-template <int TILE, int THREADS> __device__ __forceinline__ Share find_share(const Args& a) {
+template <int TILE, int NEW, int THREADS> __device__ __forceinline__ Share find_share(const Args& a) {
   __shared__ int64_t warp_sums[THREADS / 32];
   __shared__ Share found;
   const int tid = threadIdx.x, lane = tid % 32;
   const int chunk = (a.batch + THREADS - 1) / THREADS;
   const int b0 = min(a.batch, tid * chunk), b1 = min(a.batch, b0 + chunk);
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += seq_of<TILE>(a, b).units(a.heads);
+  for (int b = b0; b < b1; ++b) mine += seq_of<TILE, NEW>(a, b).units(a.heads);
   int64_t x = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -115,7 +116,7 @@ template <int TILE, int THREADS> __device__ __forceinline__ Share find_share(con
     int64_t sum = upto;
     for (int b = b0; b < b1; ++b) {
       a.upto[b] = sum;
-      sum += seq_of<TILE>(a, b).units(a.heads);
+      sum += seq_of<TILE, NEW>(a, b).units(a.heads);
       if ((int64_t)a.len[b] > a.cap) report(a.dev_status, SNAPKV_ERR_CAPACITY);
       if (a.n_new && (a.n_new[b] < 0 || a.n_new[b] > a.tokens)) report(a.dev_status, SNAPKV_ERR_INVALID_ARG);
     }
@@ -126,7 +127,7 @@ template <int TILE, int THREADS> __device__ __forceinline__ Share find_share(con
     const int64_t at = share_start(total, shares, c);
     if (at >= upto && at < upto + mine) {
       int b = b0;
-      for (int64_t u; at >= upto + (u = seq_of<TILE>(a, b).units(a.heads)); ++b) upto += u;
+      for (int64_t u; at >= upto + (u = seq_of<TILE, NEW>(a, b).units(a.heads)); ++b) upto += u;
       found = Share{at, share_start(total, shares, c + 1), upto, b};
     }
   }
@@ -139,10 +140,10 @@ struct Place {
   int seq, head, pass, tile;
   Seq s;
 };
-template <int TILE> __device__ __forceinline__ Place first_place(const Args& a, const Share& share) {
+template <int TILE, int NEW> __device__ __forceinline__ Place first_place(const Args& a, const Share& share) {
   Place p;
   p.seq = share.seq;
-  p.s = seq_of<TILE>(a, p.seq);
+  p.s = seq_of<TILE, NEW>(a, p.seq);
   const int64_t in = share.at - share.before;
   const int64_t unit = in / p.s.tiles;
   p.tile = (int)(in - unit * p.s.tiles);
@@ -151,13 +152,13 @@ template <int TILE> __device__ __forceinline__ Place first_place(const Args& a, 
   return p;
 }
 // The next head's (or pass's) first tile, which exists.
-template <int TILE> __device__ __forceinline__ void next_head(const Args& a, Place& p) {
+template <int TILE, int NEW> __device__ __forceinline__ void next_head(const Args& a, Place& p) {
   p.tile = 0;
   if (++p.pass < p.s.passes) return;
   p.pass = 0;
   if (++p.head < a.heads) return;
   p.head = 0;
-  do p.s = seq_of<TILE>(a, ++p.seq);
+  do p.s = seq_of<TILE, NEW>(a, ++p.seq);
   while (p.s.tiles == 0);
 }
 
@@ -185,6 +186,6 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 }  // namespace tree
 
 // The joining launch: out and lse of the rows whose heads were cut, and of those that see nothing.
-template <typename IO, int D, int TILE> cudaError_t launch_tree_join(const tree::Args& a, cudaStream_t stream);
+template <typename IO, int D, int TILE, int NEW> cudaError_t launch_tree_join(const tree::Args& a, cudaStream_t stream);
 
 }  // namespace snapkv

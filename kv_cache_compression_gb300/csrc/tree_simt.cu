@@ -134,9 +134,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
   auto q_hash = [](int row) { return (row / kRq) & 7; };
   auto k_hash = [](int row) { return (row / kRk) & 7; };
   auto v_hash = [](int) { return 0; };
-  const Share share = find_share<kTile, kThreads>(a);
+  const Share share = find_share<kTile, kTile, kThreads>(a);
   if (share.at >= share.end) return;
-  Place here = first_place<kTile>(a, share);
+  Place here = first_place<kTile, kTile>(a, share);
   // first product: rows kRq qg .. by keys kRk kg ..
   const int qg = tid % S::kQg, kg = tid / S::kQg;
   // second product: rows 4 og .. by channels 4 cg .. of the keys of group kh
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
     }
     __syncthreads();
     at += seg;
-    if (at < share.end) next_head<kTile>(a, here);
+    if (at < share.end) next_head<kTile, kTile>(a, here);
   }
   cp_wait<0>();
 }
@@ -329,11 +329,11 @@ template <typename IO, bool Q8, int D, int QT> cudaError_t launch_typed(const Tr
   cudaError_t err = allow_dynamic_smem<tree_simt_kernel<IO, Q8, D, QT>>(S::smem());
   if (err != cudaSuccess) return err;
   int64_t ctas = 2 * (int64_t)device_sm_count();
-  err = tree_fill(a, job, D, kTile, ctas);
+  err = tree_fill(a, job, kTile, kTile, ctas);
   if (err != cudaSuccess) return err;
   tree_simt_kernel<IO, Q8, D, QT><<<a.ctas, kThreads, S::smem(), job.stream>>>(a);
   err = cudaGetLastError();
-  return err != cudaSuccess ? err : launch_tree_join<IO, D, kTile>(a, job.stream);
+  return err != cudaSuccess ? err : launch_tree_join<IO, D, kTile, kTile>(a, job.stream);
 }
 
 template <typename IO, bool Q8, int D> cudaError_t launch_dim(const TreeJob& job) {

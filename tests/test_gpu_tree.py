@@ -82,3 +82,16 @@ def test_causal_ragged_and_without_drafts(gpu_device, shape, dtype, q8):
         check(x, lens, out, lse, drafts=drafts, n_new=n_new)
         out, lse = run(x, lens, drafts=drafts)
         check(x, lens, out, lse, drafts=drafts)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,T", [(1, 1), (2, 3), (1, 8), (3, 3), (1, 16), (16, 1), (1, 17), (4, 8), (1, 33), (5, 13), (1, 100), (8, 16), (3, 43), (4, 64), (1, 257)])
+def test_every_number_of_rows(gpu_device, G, T, d, q8):
+    """bf16 calls of one query row a KV head up to three times 128, whose kernels differ."""
+    B, H, cap = 2, 2, 700
+    x = make(gpu_device, 9, B, H, G, d, T, cap, BF16, q8=q8)
+    mask = random_tree(np.random.default_rng(T), B, T)
+    for lens, n_new in (([700, 129], None), ([1, 640], [T, max(1, T - 5)]), ([0, 16], [max(1, T // 2), 0])):
+        out, lse = run(x, lens, mask=mask, n_new=n_new)
+        check(x, lens, out, lse, mask=mask, n_new=n_new)

@@ -14,7 +14,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _CSRC = os.path.join(_HERE, "csrc")
 _BUILD = os.path.join(_HERE, "_build")
 SOURCES = ["abi.cu", "vote_simt.cu", "vote_tc.cu", "vote_cluster.cu", "pool_topk.cu", "gather.cu", "decode.cu", "hit_rate.cu",
-           "cache_abi.cu", "attend.cu", "q4.cu", "evict.cu", "draft_abi.cu", "q8.cu", "tree.cu", "tree_simt.cu", "tree_mma.cu",
+           "cache_abi.cu", "attend.cu", "q4.cu", "evict.cu", "draft_abi.cu", "q8.cu", "tree.cu", "tree_simt.cu", "tree_mma.cu", "tree_tc.cu",
            "tree_join.cu"]
 HEADERS = ["snapkv_common.cuh", "snapkv_internal.h", "sm100_ptx.cuh", "tc_common.cuh", "abi_common.h",
            "cache_internal.h", "q4.cuh", "row_list.cuh", "draft_internal.h", "tree_launch.h", "tree_maps.h", "tree_schedule.cuh"]

@@ -29,8 +29,13 @@ int64_t bounded(int64_t tiles, int64_t most) { return tiles < most ? tiles : mos
 size_t tree_workspace_bytes(int batch, int q_heads, int heads, int head_dim, int tokens, int64_t cap) {
   const int64_t rows = (int64_t)(q_heads / heads) * tokens;
   const int simt = rows <= 8 ? 8 : kSimtRows;
-  const int64_t ctas = bounded(most_tiles(batch, heads, (rows + simt - 1) / simt, tokens, cap, 16, 16), kMaxTreeCtas);
-  return upto_bytes(batch) + parts_bytes(ctas, simt, head_dim);
+  size_t parts = parts_bytes(bounded(most_tiles(batch, heads, (rows + simt - 1) / simt, tokens, cap, 16, 16), kMaxTreeCtas), simt, head_dim);
+  if (rows > 16) {
+    const int wide = rows <= 128 ? 128 : 256;
+    const size_t tc = parts_bytes(bounded(most_tiles(batch, heads, (rows + wide - 1) / wide, tokens, cap, 128, 128), kMaxTcCtas), wide, head_dim);
+    parts = tc > parts ? tc : parts;
+  }
+  return upto_bytes(batch) + parts;
 }
 
 tree::Args tree_args(const TreeJob& job, int tile_q) {
@@ -63,7 +68,8 @@ tree::Args tree_args(const TreeJob& job, int tile_q) {
 
 cudaError_t tree_fill(tree::Args& a, const TreeJob& job, int tile, int fresh, int64_t ctas) {
   const int64_t rows = (int64_t)a.group * a.tokens, passes = (rows + a.tile_q - 1) / a.tile_q;
-  a.ctas = (int)bounded(ctas, bounded(most_tiles(a.batch, a.heads, passes, a.tokens, a.cap, tile, fresh), kMaxTreeCtas));
+  a.ctas = (int)bounded(ctas, most_tiles(a.batch, a.heads, passes, a.tokens, a.cap, tile, fresh));
+  a.ctas -= a.ctas % a.siblings;
   char* ws = static_cast<char*>(job.workspace);
   a.upto = reinterpret_cast<int64_t*>(ws);
   a.parts = reinterpret_cast<float*>(ws + upto_bytes(a.batch));
@@ -106,7 +112,7 @@ bool tree_maps(TreeMaps* maps, const TreeJob& job, int tile, int fresh) {
 cudaError_t launch_tree(const TreeJob& job) {
   if (job.dtype == SNAPKV_F32) return launch_tree_simt(job);
   const int64_t rows = (int64_t)(job.q_heads / job.heads) * job.tokens;
-  return rows <= 16 ? launch_tree_mma(job) : launch_tree_simt(job);
+  return rows <= 16 ? launch_tree_mma(job) : launch_tree_tc(job);
 }
 
 }  // namespace snapkv

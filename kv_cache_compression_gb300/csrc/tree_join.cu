@@ -103,6 +103,8 @@ INSTANCE(float, 64, 64, 64)
 INSTANCE(float, 128, 64, 64)
 INSTANCE(__nv_bfloat16, 64, 64, 64)
 INSTANCE(__nv_bfloat16, 128, 64, 64)
+INSTANCE(__nv_bfloat16, 64, 128, 128)
+INSTANCE(__nv_bfloat16, 128, 128, 128)
 INSTANCE(__nv_bfloat16, 64, 32, 16)
 INSTANCE(__nv_bfloat16, 128, 32, 16)
 INSTANCE(__nv_bfloat16, 128, 16, 16)

@@ -10,6 +10,7 @@ struct Args;
 }
 
 constexpr int kMaxTreeCtas = 320;     // of a first launch: bounds the workspace, not tied to a device's SM count
+constexpr int kMaxTcCtas = 160;       // the same for the kernel whose passes have up to 256 rows
 constexpr int kSimtRows = 32;         // query rows of a pass, at most
 
 // The call's arguments, for passes of `tile_q` query rows.
@@ -20,5 +21,7 @@ cudaError_t tree_fill(tree::Args& a, const TreeJob& job, int tile, int fresh, in
 
 cudaError_t launch_tree_simt(const TreeJob& job);   // fp32 instructions: fp32 calls
 cudaError_t launch_tree_mma(const TreeJob& job);    // mma.sync: bf16 calls of up to sixteen query rows a KV head
+
+cudaError_t launch_tree_tc(const TreeJob& job);     // tcgen05: bf16 calls of more
 
 }  // namespace snapkv

@@ -361,21 +361,28 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
       const int r0 = r0_of(seg), rows = rows_of(seg), n = seg.p.s.n;
       const int64_t bh = (int64_t)seg.p.seq * a.heads + seg.p.head;
       const int slots = TWO && rows > 128 ? 2 : 1;
-      constexpr int kPieces = D / 8;
-      for (int u = at; u < slots * kTile * kPieces; u += 64) {
-        const int r = u / kPieces, c = u % kPieces;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows) {
-          const int row = r0 + r, g = row / n;
-          x = ld_nc_v4(static_cast<const __nv_bfloat16*>(a.q) + ((bh * a.group + g) * a.tokens + (row - g * n)) * D + 8 * c);
-        }
-        if constexpr (Q8) {
-          uint32_t* const w = &x.x;
+      // A thread has every (64 / kPieces)-th row's piece c, eight of them under way at a time.
+      constexpr int kPieces = D / 8, kStep = 64 / kPieces;
+      const int c = at % kPieces;
+#pragma unroll 1
+      for (int x = at / kPieces; x < slots * kTile; x += 8 * kStep) {
+        uint4 v[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = pack2(__uint_as_float(w[e] << 16) * kQ8Q, __uint_as_float(w[e] & 0xFFFF0000u) * kQ8Q);
+        for (int e = 0; e < 8; ++e) {
+          const int r = x + e * kStep, row = r0 + r, g = row / n;
+          v[e] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < rows) v[e] = ld_nc_v4(static_cast<const __nv_bfloat16*>(a.q) + ((bh * a.group + g) * a.tokens + (row - g * n)) * D + 8 * c);
         }
-        const int slot = TWO ? r / kTile : buf;
-        *reinterpret_cast<uint4*>(smem + S::kQ + slot * S::kSlotQ + piece_at(r % kTile, c)) = x;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int r = x + e * kStep;
+          if constexpr (Q8) {
+            uint32_t* const w = &v[e].x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = pack2(__uint_as_float(w[i] << 16) * kQ8Q, __uint_as_float(w[i] & 0xFFFF0000u) * kQ8Q);
+          }
+          *reinterpret_cast<uint4*>(smem + S::kQ + (TWO ? r / kTile : buf) * S::kSlotQ + piece_at(r % kTile, c)) = v[e];
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       ptx::mbar_arrive(&bars.q_full[buf]);
@@ -409,18 +416,24 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
 #pragma unroll
           for (int w = 0; w < 4; ++w) see[w] = valid >= 32 * w + 32 ? ~0u : valid > 32 * w ? (1u << (valid - 32 * w)) - 1u : 0u;
           if (drafted && a.mask) {
-            const uint8_t* mask = a.mask + seg.p.seq * a.mask_stride + key0 + lane;
+            // lane e looks at key 32 w + e for one row after the other (rows that are not there have a token, too)
+            const uint8_t* const mask = a.mask + seg.p.seq * a.mask_stride + key0;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
               if (valid <= 32 * w) break;
+              const uint8_t* const from = mask + min(32 * w + lane, valid - 1);
               uint32_t word = 0;
               if (mine)
-#pragma unroll 8
-                for (int x = 0; x < 32; ++x) {
-                  const int64_t t = __shfl_sync(0xffffffffu, token, x);
-                  const bool bit = 32 * w + lane < valid && quarter * 32 + x < rows && mask[t * a.tokens + 32 * w] != 0;
-                  const uint32_t votes = __ballot_sync(0xffffffffu, bit);
-                  if (lane == x) word = votes;
+#pragma unroll 1
+                for (int x = 0; x < 32; x += 16) {
+                  uint8_t bit[16];
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) bit[e] = __ldg(from + (int64_t)__shfl_sync(0xffffffffu, token, x + e) * a.tokens);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) {
+                    const uint32_t votes = __ballot_sync(0xffffffffu, bit[e] != 0);
+                    if (lane == x + e) word = votes;
+                  }
                 }
               see[w] &= word;
             }
@@ -482,32 +495,19 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
         }
         wait(&bars.s_full[slot], steps);
         ptx::tc_fence_after();
-        if (mine) {
-          // ---- the row's maximum
-          float top = -INFINITY;
+        // Logits of chunk c (32 keys) as they are compared: 8-bit keys' steps are in.
+        auto scaled = [&](uint32_t (&x)[32], int c) {
+          if constexpr (Q8) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[32];
-            tmem_ld32(s_at + 32 * c, x);
-            ptx::tmem_wait_ld();
-            if constexpr (Q8) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 k = *reinterpret_cast<const float4*>(fk + 32 * c + e);
-                const float2 y = mul2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), make_float2(k.x, k.y));
-                const float2 z = mul2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), make_float2(k.z, k.w));
-                x[e] = __float_as_uint(y.x), x[e + 1] = __float_as_uint(y.y), x[e + 2] = __float_as_uint(z.x), x[e + 3] = __float_as_uint(z.y);
-              }
-            }
-            if (edge) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (see[c] >> e & 1) top = fmaxf(top, __uint_as_float(x[e]));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) top = fmaxf(fmaxf(top, __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
+            for (int e = 0; e < 32; e += 4) {
+              const float4 k = *reinterpret_cast<const float4*>(fk + 32 * c + e);
+              const float2 y = mul2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), make_float2(k.x, k.y));
+              const float2 z = mul2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), make_float2(k.z, k.w));
+              x[e] = __float_as_uint(y.x), x[e + 1] = __float_as_uint(y.y), x[e + 2] = __float_as_uint(z.x), x[e + 3] = __float_as_uint(z.y);
             }
           }
+        };
+        auto raise = [&](float top) {   // the row's maximum, and what stands under it
           if constexpr (!Q8) top *= a.scale_log2;
           if (first) {
             m = fmaxf(m, top);
@@ -515,48 +515,106 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
             const float next = top > m + kSlack ? top : m, fall = rescale(m, next);
             m = next;
             l *= fall;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
               uint32_t x[32];
-              tmem_ld32(o_lane + S::kO(slot) + 32 * c, x);
+              tmem_ld32(o_lane + S::kO(slot) + c, x);
               ptx::tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * fall);
-              tmem_st32(o_lane + S::kO(slot) + 32 * c, x);
+              tmem_st32(o_lane + S::kO(slot) + c, x);
             }
             ptx::tmem_wait_st();
           }
-          // ---- weights
+        };
+        // Weights of chunk c from its (scaled) logits; `keep` and `nan` are this row's bits of its keys.
+        float2 sum = make_float2(0.f, 0.f);
+        auto weigh = [&](const uint32_t (&x)[32], int c, auto masked, uint32_t keep, uint32_t nan) {
           const float2 down = make_float2(-m, -m), by = make_float2(a.scale_log2, a.scale_log2);
-          float2 sum = make_float2(0.f, 0.f);
+          uint32_t p[32];   // first parts, then second parts
 #pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float2 y = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+            y = Q8 ? add2(y, down) : fma2(y, by, down);
+            y = make_float2(ex2(y.x), ex2(y.y));
+            if constexpr (decltype(masked)::value) {
+              if (!(keep >> e & 1)) y.x = 0.f;
+              if (!(keep >> (e + 1) & 1)) y.y = 0.f;
+              if (nan >> e & 1) y.x = __uint_as_float(0x7FC00000u);
+              if (nan >> (e + 1) & 1) y.y = __uint_as_float(0x7FC00000u);
+            }
+            sum = add2(sum, y);
+            if constexpr (Q8) y = mul2(y, *reinterpret_cast<const float2*>(fk + kTile + 32 * c + e));
+            const uint32_t w = pack2(y.x, y.y);
+            p[e / 2] = w;
+            p[16 + e / 2] = pack2(y.x - __uint_as_float(w << 16), y.y - __uint_as_float(w & 0xFFFF0000u));
+          }
+          tmem_st32(s_at + 32 * c, p);
+        };
+        auto highest = [](const uint32_t (&x)[32], float top) {
+          float other = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            top = fmaxf(fmaxf(top, __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
+            other = fmaxf(fmaxf(other, __uint_as_float(x[e + 2])), __uint_as_float(x[e + 3]));
+          }
+          return fmaxf(top, other);
+        };
+        if (mine && !edge) {
+          // Chunks 0 and 1, then 2 and 3 for the maximum; weights from 2 and 3 while they are there, then 0 and 1 again.
+          uint32_t x[32], y[32];
+          float top = -INFINITY;
+          tmem_ld32(s_at, x);
+          ptx::tmem_wait_ld();
+          tmem_ld32(s_at + 32, y);
+          scaled(x, 0);
+          top = highest(x, top);
+          ptx::tmem_wait_ld();
+          tmem_ld32(s_at + 64, x);
+          scaled(y, 1);
+          top = highest(y, top);
+          ptx::tmem_wait_ld();
+          tmem_ld32(s_at + 96, y);
+          scaled(x, 2);
+          top = highest(x, top);
+          ptx::tmem_wait_ld();
+          scaled(y, 3);
+          raise(highest(y, top));
+          weigh(x, 2, std::false_type(), 0u, 0u);
+          tmem_ld32(s_at, x);
+          weigh(y, 3, std::false_type(), 0u, 0u);
+          ptx::tmem_wait_ld();
+          tmem_ld32(s_at + 32, y);
+          scaled(x, 0);
+          weigh(x, 0, std::false_type(), 0u, 0u);
+          ptx::tmem_wait_ld();
+          scaled(y, 1);
+          weigh(y, 1, std::false_type(), 0u, 0u);
+        } else if (mine) {
+          auto word = [](const uint32_t (&w)[4], int c) { return c == 0 ? w[0] : c == 1 ? w[1] : c == 2 ? w[2] : w[3]; };
+          float top = -INFINITY;
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t x[32];
             tmem_ld32(s_at + 32 * c, x);
             ptx::tmem_wait_ld();
-            uint32_t p[32];   // first parts, then second parts
+            scaled(x, c);
+            const uint32_t keep = word(see, c);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float2 y = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-              if constexpr (Q8)
-                y = fma2(y, *reinterpret_cast<const float2*>(fk + 32 * c + e), down);
-              else
-                y = fma2(y, by, down);
-              y = make_float2(ex2(y.x), ex2(y.y));
-              if (edge) {
-                if (!(see[c] >> e & 1)) y.x = 0.f;
-                if (!(see[c] >> (e + 1) & 1)) y.y = 0.f;
-                if (bad[c] >> e & 1) y.x = __uint_as_float(0x7FC00000u);
-                if (bad[c] >> (e + 1) & 1) y.y = __uint_as_float(0x7FC00000u);
-              }
-              sum = add2(sum, y);
-              if constexpr (Q8) y = mul2(y, *reinterpret_cast<const float2*>(fk + kTile + 32 * c + e));
-              const uint32_t w = pack2(y.x, y.y);
-              p[e / 2] = w;
-              p[16 + e / 2] = pack2(y.x - __uint_as_float(w << 16), y.y - __uint_as_float(w & 0xFFFF0000u));
-            }
-            tmem_st32(s_at + 32 * c, p);
+            for (int e = 0; e < 32; ++e)
+              if (keep >> e & 1) top = fmaxf(top, __uint_as_float(x[e]));
           }
+          raise(top);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32];
+            tmem_ld32(s_at + 32 * c, x);
+            ptx::tmem_wait_ld();
+            scaled(x, c);
+            weigh(x, c, std::true_type(), word(see, c), word(bad, c));
+          }
+        }
+        if (mine) {
           l += sum.x + sum.y;
           ptx::tmem_wait_st();
         }

@@ -45,18 +45,20 @@ template <bool Q8, int D, bool TWO> struct Shape {
   static constexpr int kWarps = Q8 ? 16 : 12;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kSlotQ = kTile * D * 2;                 // bytes of 128 rows of queries
-  static constexpr int kQBufs = TWO || Q8 ? 1 : 2;
   static constexpr int kStage = kTile * D * 2;                 // of a tile of K or V
-  static constexpr int kStages = (Q8 ? (TWO ? 3 : 4) : 5) * (128 / D);
+  static constexpr int kStages = (Q8 ? (TWO ? 3 : 4) : TWO ? 5 : 6) * (128 / D);   // (TWO: of one ring; else of two, a slot's each)
+  static constexpr int kTurn = TWO ? kStages : kStages / 2;
   static constexpr int kRaw = kTile * D;                       // of a tile of codes
   static constexpr int kRaws = Q8 ? 3 * (128 / D) : 0;
   static constexpr int kQ = 0;
-  static constexpr int kRing = kQ + (TWO ? 2 : kQBufs) * kSlotQ;
+  static constexpr int kRing = kQ + (TWO ? 2 : 1) * kSlotQ;
   static constexpr int kRawRing = kRing + kStages * kStage;
   static constexpr int kMeet = kRawRing + kRaws * kRaw;        // [128] float2
   static constexpr int kFactors = kMeet + kTile * 8;           // [2 slots][2][K, V][128] floats (8 bits)
   static constexpr int kBytes = kFactors + (Q8 ? 2 * 2 * 2 * kTile * 4 : 0);
   static constexpr int smem() { return 1024 + kBytes; }
+  // The stage of a ring's tile `at`: of a slot's tile i, K is 2 i and V 2 i + 1.
+  __device__ __forceinline__ static uint32_t stage(int slot, uint32_t at) { return (TWO ? 0 : slot * kTurn) + at % kTurn; }
   static constexpr int kS(int slot) { return slot * 128; }     // TMEM columns
   static constexpr int kO(int slot) { return 256 + slot * D; }
   static constexpr int kColumns = 512;
@@ -64,8 +66,8 @@ template <bool Q8, int D, bool TWO> struct Shape {
 
 struct Bars {
   uint64_t kv_full[12], kv_empty[12], raw_full[8], raw_empty[8];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2];
-  uint64_t o_full, o_free, drain;
+  uint64_t q_full, q_empty, s_full[2], p_ready[2][2];   // (p_ready: of a slot, by halves of the keys)
+  uint64_t o_full, o_free, drain[2];
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
@@ -89,20 +91,39 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) 
       : "memory");
 }
 
-// D (+)= A[tmem] B[smem], bf16 operands, fp32 sums.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// The MMA warp runs as a whole, so that descriptors stay in uniform registers (computed by one thread, each product took 90
+// clocks to issue, of which it executes in 64); its first thread alone issues. A value of which the compiler cannot see that it
+// is the same in all threads goes through a reduction, whose result is.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+
+// D (+)= A B^T, bf16 operands, fp32 sums; A in shared memory (ss) or TMEM (ts). lo: the low words of descriptors.
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a),
-      "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 e, %0, 0;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 x, {%2, %4};\n\tmov.b64 y, {%3, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%1], x, y, %5, p;\n\t}" ::"r"(leader),
+      "r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 y;\n\tsetp.ne.b32 e, %0, 0;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 y, {%3, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], y, %5, p;\n\t}" ::"r"(leader),
+      "r"(d), "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %0, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(leader), "r"(ptx::smem_u32(bar))
       : "memory");
 }
 
-// Descriptor of V as B: keys (the product's k) are rows of 128 bytes of 64 channels (its n), 128-byte swizzle; eight keys
-// are 1024 bytes apart, 64 channels a block of kTile rows.
-__device__ __forceinline__ uint64_t v_desc(uint32_t at) {
-  return (uint64_t)((at >> 4) & 0x3FFFu) | (uint64_t)((kTile * 128) >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
-         (uint64_t)2 << 61;
-}
+// Descriptors, low and high words. Queries and K: rows of 128 bytes (64 channels, the products' k), 128-byte swizzle, eight rows
+// 1024 bytes apart. V as B: keys (the product's k) are rows of 128 bytes of 64 channels (its n), eight keys 1024 bytes
+// apart, 64 channels a block of kTile rows.
+__device__ __forceinline__ constexpr uint32_t k_desc(uint32_t at) { return ((at >> 4) & 0x3FFFu) | 1u << 16; }
+__device__ __forceinline__ constexpr uint32_t v_desc(uint32_t at) { return ((at >> 4) & 0x3FFFu) | (uint32_t)((kTile * 128) >> 4) << 16; }
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;   // stride, version, swizzle
 
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
   const __nv_bfloat162 two = __floats2bfloat162_rn(x, y);
@@ -147,28 +168,32 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
   __shared__ uint32_t tmem_at;
   __shared__ int abort;
   __shared__ uint32_t bad_keys[2][4];
+  __shared__ uint8_t pending[12];   // of a stage's last load, if any: 1 + its phase's parity
   uint8_t* const smem = raw_smem + ((1024 - (ptx::smem_u32(raw_smem) & 1023)) & 1023);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid % 32, warp = __shfl_sync(0xffffffffu, tid / 32, 0);
   if (tid == 0) {
     abort = 0;
+    for (int i = 0; i < 12; ++i) pending[i] = 0;
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&bars.kv_full[i], Q8 ? 4 : 1);   // (four unpacking warps)
-      ptx::mbar_init(&bars.kv_empty[i], 1);
+      ptx::mbar_init(&bars.kv_empty[i], TWO ? 2 : 1);   // (slots)
     }
     for (int i = 0; i < kRaws; ++i) {
       ptx::mbar_init(&bars.raw_full[i], 1);
       ptx::mbar_init(&bars.raw_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&bars.q_full[i], 64);
-      ptx::mbar_init(&bars.q_empty[i], 1);
       ptx::mbar_init(&bars.s_full[i], 1);
-      ptx::mbar_init(&bars.p_ready[i], 4);
+      ptx::mbar_init(&bars.p_ready[i][0], 4);
+      ptx::mbar_init(&bars.p_ready[i][1], 4);
     }
-    ptx::mbar_init(&bars.o_full, 1);
+    ptx::mbar_init(&bars.q_full, 32);
+    ptx::mbar_init(&bars.q_empty, 2);
+    ptx::mbar_init(&bars.o_full, 2);
     ptx::mbar_init(&bars.o_free, 8);
-    ptx::mbar_init(&bars.drain, 1);
+    ptx::mbar_init(&bars.drain[0], 1);
+    ptx::mbar_init(&bars.drain[1], 1);
     ptx::fence_mbar_init();
   }
   const Share share = find_share<kTile, kTile, S::kThreads>(a);   // (with barriers)
@@ -193,20 +218,30 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
   // The query rows r0 .. r0 + rows - 1 of a segment.
   auto r0_of = [&](const Segments& s) { return (a.siblings > 1 ? pass0 : s.p.pass) * a.tile_q; };
   auto rows_of = [&](const Segments& s) { return min(a.tile_q, a.group * s.p.s.n - r0_of(s)); };
-  const int64_t total = share.end - share.at;   // tiles
+  const uint32_t total = (uint32_t)(share.end - share.at);   // tiles
+  constexpr uint32_t kPair = TWO ? 1 : 2;                    // they are loaded, K before V
+
+  // Registers go from the warps that move data to those of the softmax (the shares sum up to what the block was launched with).
+  if constexpr (Q8) {
+    static_assert(S::kThreads == 512 && 256 * 184 + 256 * 72 == 512 * 128, "registers");
+    if (warp >= 4 && warp < 12)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  }
 
   if (warp == 0) {
-    // ---- loads, in the order in which the products take them. Up to 128 rows: K0 K1 V0 K2 V1 K3 ..; more: K0 V0 K1 V1 ..
+    // ---- loads, in the order in which the products take them
     if (lane == 0) {
       Segments ks(a, share), vs(a, share);
       int kf = 0, vf = 0;   // tiles of the segments so far
-      uint32_t sent = 0;
-      auto send = [&](Segments& s, int& f, bool key) {
-        constexpr int kSlots = Q8 ? kRaws : kStages;
-        const uint32_t slot = sent % kSlots, turn = sent / kSlots;
+      uint32_t sent = 0;    // raw ones (8 bits)
+      auto send = [&](Segments& s, int& f, uint32_t t, bool key) {   // K or V of the share's tile t
         const int tile = s.p.tile + f, bh = s.p.seq * a.heads + s.p.head;
         const bool cached = tile < s.p.s.cache_tiles;
         if (!Q8 || cached) {   // (drafted rows beside an 8-bit cache are copied by the warps that unpack)
+          const uint32_t at = 2 * (TWO ? t : t / 2) + (key ? 0 : 1);
+          const uint32_t slot = Q8 ? sent % kRaws : S::stage(t & 1, at), turn = Q8 ? sent / kRaws : at / S::kTurn;
           if (turn > 0 && !wait(Q8 ? &bars.raw_empty[slot] : &bars.kv_empty[slot], turn - 1)) return false;
           uint64_t* const bar = Q8 ? &bars.raw_full[slot] : &bars.kv_full[slot];
           uint8_t* const to = smem + (Q8 ? S::kRawRing + slot * S::kRaw : S::kRing + slot * S::kStage);
@@ -215,6 +250,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           ptx::mbar_arrive_expect_tx(bar, Q8 ? S::kRaw : S::kStage);
 #pragma unroll
           for (int c = 0; c < (Q8 ? 1 : D / 64); ++c) ptx::tma_load_3d(to + c * kTile * 128, map, 64 * c, row0, bh, bar);
+          pending[slot] = (uint8_t)(1 + (turn & 1));
           ++sent;
         }
         if (++f == s.tiles) {
@@ -223,169 +259,190 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
         }
         return true;
       };
-      bool ok = send(ks, kf, true);
-      if (ok && !TWO && total > 1) ok = send(ks, kf, true);
-      for (int64_t t = 0; ok && t < total; ++t) {
-        ok = send(vs, vf, false);
-        if (ok && t + (TWO ? 1 : 2) < total) ok = send(ks, kf, true);
-      }
-      // Copies in flight land before the block ends, also after a wait ran out.
-      constexpr uint32_t kSlots = Q8 ? kRaws : kStages;
-      const int none = 0;
-      for (uint32_t i = sent > kSlots ? sent - kSlots : 0; i < sent; ++i)
-        ptx::mbar_wait(Q8 ? &bars.raw_full[i % kSlots] : &bars.kv_full[i % kSlots], (i / kSlots) & 1, &none, kWaitLimit);
-    }
-  } else if (warp == 1) {
-    // ---- products
-    if (lane == 0) {
-      constexpr uint32_t kIdescQk = ptx::idesc_bf16_f32(128, kTile), kIdescPv = ptx::idesc_bf16_f32(128, D) | 1u << 16;   // (V: n-major)
-      Segments qs(a, share), ps(a, share);
-      int qf = 0, pf = 0;
-      uint32_t taken = 0;              // ring tiles so far, in order
-      uint32_t s_steps[2] = {0, 0}, p_steps[2] = {0, 0};
-      uint32_t k_slot = 0, v_slot = 0;
-      auto take = [&](uint32_t& slot) {
-        slot = taken % kStages;
-        const bool ok = wait(&bars.kv_full[slot], taken / kStages);
-        ++taken;
-        ptx::tc_fence_after();
-        return ok;
-      };
-      // S of a slot = Q K^T of the tile in k_slot.
-      auto qk = [&](int slot) {
-        const uint32_t q_at = q_smem + (TWO ? slot : qs.index % S::kQBufs) * S::kSlotQ, k_at = ring + k_slot * S::kStage;
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint32_t off = (s / 4) * (kTile * 128) + (s % 4) * 32;
-          ptx::mma_bf16(tmem + S::kS(slot), ptx::smem_desc_k_sw128(q_at + off), ptx::smem_desc_k_sw128(k_at + off), kIdescQk, s > 0);
-        }
-        ptx::mma_commit(&bars.s_full[slot]);
-        ++s_steps[slot];
-      };
-      // O of a slot += P V of the tile in v_slot, `fresh`: O =.
-      auto pv = [&](int slot, bool fresh) {
-        const uint32_t v_at = ring + v_slot * S::kStage;
-#pragma unroll
-        for (int s = 0; s < kTile / 16; ++s)
-#pragma unroll
-          for (int part = 0; part < 2; ++part)
-            mma_ts(tmem + S::kO(slot), tmem + S::kS(slot) + (s / 2) * 32 + part * 16 + (s % 2) * 8, v_desc(v_at + s * 2048), kIdescPv,
-                   !(fresh && s == 0 && part == 0));
-      };
-      auto weights = [&](int slot) {
-        const bool ok = wait(&bars.p_ready[slot], p_steps[slot]);
-        ++p_steps[slot];
-        ptx::tc_fence_after();
-        return ok;
-      };
-      auto queries = [&] { return qf > 0 || wait(&bars.q_full[qs.index % S::kQBufs], qs.index / S::kQBufs); };
-      auto outputs = [&] { return pf > 0 || ps.index == 0 || wait(&bars.o_free, ps.index - 1); };
-      auto qk_done = [&] {             // of the tile, by all slots
-        ptx::mma_commit(&bars.kv_empty[k_slot]);
-        if (++qf == qs.tiles) {
-          ptx::mma_commit(&bars.q_empty[qs.index % S::kQBufs]);
-          qf = 0;
-          qs.next(a);
-        }
-      };
-      auto pv_done = [&] {
-        ptx::mma_commit(&bars.kv_empty[v_slot]);
-        if (++pf == ps.tiles) {
-          ptx::mma_commit(&bars.o_full);
-          pf = 0;
-          ps.next(a);
-        }
-      };
       bool ok = true;
-      if constexpr (!TWO) {
-        uint32_t step = 0;
-        auto next_qk = [&](int slot) {
-          if (!queries() || !take(k_slot)) return false;
-          qk(slot);
-          qk_done();
-          return true;
-        };
-        ok = next_qk(0) && (total < 2 || next_qk(1));
-        for (int64_t t = 0; ok && t < total; ++t, ++step) {
-          const int slot = (int)(step & 1);
-          ok = weights(slot) && take(v_slot) && outputs();
-          if (!ok) break;
-          pv(slot, pf < 2);            // (a segment's first two tiles are its slots' first)
-          pv_done();
-          if (t + 2 < total) ok = next_qk(slot);
-        }
-      } else {
-        bool two = rows_of(qs) > 128;  // the second slot has rows of the segment qs
-        ok = queries() && take(k_slot);
-        if (ok) {
-          qk(0);
-          if (two) qk(1);
-          qk_done();
-        }
-        for (int64_t t = 0; ok && t < total; ++t) {
-          const bool second = rows_of(ps) > 128, more = t + 1 < total;
-          ok = weights(0) && take(v_slot) && outputs();
-          if (!ok) break;
-          const bool fresh = pf == 0;
-          pv(0, fresh);
-          if (more) {
-            two = rows_of(qs) > 128;
-            ok = queries() && take(k_slot);
-            if (!ok) break;
-            qk(0);
-          }
-          if (second) {
-            ok = weights(1);
-            if (!ok) break;
-            pv(1, fresh);
-          }
-          pv_done();
-          if (more) {
-            if (two) qk(1);
-            qk_done();
-          }
-        }
-      }
-      // Products in flight end before the block does.
-      ptx::mma_commit(&bars.drain);
+      for (uint32_t t = 0; ok && t < total; t += kPair)
+        for (int key = 1; ok && key >= 0; --key)
+          for (uint32_t u = t; ok && u < t + kPair && u < total; ++u) ok = key ? send(ks, kf, u, true) : send(vs, vf, u, false);
+      // Copies in flight land before the block ends, also after a wait ran out.
       const int none = 0;
-      ptx::mbar_wait(&bars.drain, 0, &none, kWaitLimit);
+      for (int i = 0; i < (Q8 ? kRaws : kStages); ++i)
+        if (pending[i]) ptx::mbar_wait(Q8 ? &bars.raw_full[i] : &bars.kv_full[i], pending[i] - 1, &none, kWaitLimit);
     }
-  } else if (warp < 4) {
+  } else if (warp < 3) {
+    // ---- products of a slot. (One warp for both slots left the tensor core idle for 2000 of a tile's 5200 clocks, while it
+    // waited on barriers that had long been reached and counted: a product is issued no more than a few ahead.)
+    const int slot = warp - 1;
+    constexpr uint32_t kIdescQk = ptx::idesc_bf16_f32(128, kTile), kIdescPv = ptx::idesc_bf16_f32(128, D) | 1u << 16;   // (V: n-major)
+    const uint32_t leader = lane == 0;
+    const uint32_t s_at = uniform(tmem + S::kS(slot)), o_at = uniform(tmem + S::kO(slot));
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };   // (the warp stays together)
+    uint32_t steps = 0;   // P V of this slot so far
+    // S = Q K^T of the ring's tile `at`.
+    auto qk = [&](uint32_t at) {
+      const uint32_t stage = S::stage(slot, at);
+      if (!wait_all(&bars.kv_full[stage], at / S::kTurn)) return false;
+      ptx::tc_fence_after();
+      const uint32_t q_lo = uniform(k_desc(q_smem + (TWO ? slot : 0) * S::kSlotQ)), k_lo = uniform(k_desc(ring + stage * S::kStage));
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        const uint32_t off = ((s / 4) * (kTile * 128) + (s % 4) * 32) >> 4;
+        mma_ss(leader, s_at, q_lo + off, k_lo + off, kDescHigh, kIdescQk, s > 0);
+      }
+      commit(leader, &bars.s_full[slot]);
+      commit(leader, &bars.kv_empty[stage]);
+      return true;
+    };
+    // O += P V of the ring's tile `at`, the upper half of the keys first, as their weights are there first; `fresh`: O =.
+    auto pv = [&](uint32_t at, bool fresh) {
+      const uint32_t stage = S::stage(slot, at);
+      if (!wait_all(&bars.kv_full[stage], at / S::kTurn)) return false;
+      const uint32_t v_lo = uniform(v_desc(ring + stage * S::kStage));
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (!wait_all(&bars.p_ready[slot][half], steps)) return false;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < kTile / 32; ++i)
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            const int s = (1 - half) * (kTile / 32) + i;
+            mma_ts(leader, o_at, s_at + (s / 2) * 32 + part * 16 + (s % 2) * 8, v_lo + s * (2048 >> 4), kDescHigh, kIdescPv,
+                   !(fresh && half == 0 && i == 0 && part == 0));
+          }
+      }
+      ++steps;
+      commit(leader, &bars.kv_empty[stage]);
+      return true;
+    };
+    // Walks of the Q K^T and of the P V, the first a tile of the slot's ahead. A slot waits for every segment's queries and outputs
+    // and counts in on q_empty and o_full at its end, whether it had tiles of it or not: barriers know a phase by its parity
+    // alone, so that none may be passed over.
+    Segments qs(a, share), ps(a, share);
+    bool q_end = false, p_end = false;
+    uint32_t q_t = 0, p_t = 0;   // the slot's tiles so far
+    auto q_next = [&] {
+      commit(leader, &bars.q_empty);
+      q_end = !qs.next(a);
+    };
+    auto p_next = [&] {
+      commit(leader, &bars.o_full);
+      p_end = !ps.next(a);
+    };
+    auto queries = [&] { return wait_all(&bars.q_full, qs.index); };
+    auto outputs = [&] { return ps.index == 0 || wait_all(&bars.o_free, ps.index - 1); };
+    bool ok = true;
+    if constexpr (!TWO) {
+      int qf_tiles = 0;            // of a segment that is left
+      // every second tile of the share
+      int qf = slot, pf = slot;    // within their segments
+      auto do_qk = [&] {           // (nothing where there is no other)
+        for (; !q_end && qf >= qs.tiles; qf -= qf_tiles) {   // a segment without tiles of the slot's
+          if (!queries()) return false;
+          qf_tiles = qs.tiles;
+          q_next();
+        }
+        if (q_end) return true;
+        if (qf < 2 && !queries()) return false;   // (a segment's first two tiles are its slots' first)
+        if (!qk(2 * q_t)) return false;
+        ++q_t;
+        qf += 2;
+        if (qf >= qs.tiles) {
+          qf -= qs.tiles;
+          q_next();
+        }
+        return true;
+      };
+      ok = do_qk();
+      while (ok) {
+        for (; ok && !p_end && pf >= ps.tiles; pf -= qf_tiles) {
+          ok = outputs();
+          qf_tiles = ps.tiles;
+          if (ok) p_next();
+        }
+        if (!ok || p_end) break;
+        ok = (pf >= 2 || outputs()) && pv(2 * p_t + 1, pf < 2);
+        if (!ok) break;
+        ++p_t;
+        pf += 2;
+        if (pf >= ps.tiles) {
+          pf -= ps.tiles;
+          p_next();
+        }
+        ok = do_qk();
+      }
+    } else {
+      // all tiles of the segments of which the slot has rows; of the others it only lets the loads go on
+      int qf = 0, pf = 0;
+      bool q_mine = slot == 0 || rows_of(qs) > kTile, p_mine = q_mine;
+      auto skip = [&](uint32_t at) {
+        const bool there = wait_all(&bars.kv_full[S::stage(slot, at)], at / S::kTurn);
+        if (there && leader) ptx::mbar_arrive(&bars.kv_empty[S::stage(slot, at)]);
+        __syncwarp();
+        return there;
+      };
+      auto do_qk = [&] {
+        if (qf == 0 && !queries()) return false;
+        if (!(q_mine ? qk(2 * q_t) : skip(2 * q_t))) return false;
+        ++q_t;
+        if (++qf == qs.tiles) {
+          qf = 0;
+          q_next();
+          if (!q_end) q_mine = slot == 0 || rows_of(qs) > kTile;
+        }
+        return true;
+      };
+      ok = do_qk();
+      while (ok && !p_end) {
+        ok = (pf > 0 || outputs()) && (p_mine ? pv(2 * p_t + 1, pf == 0) : skip(2 * p_t + 1));
+        if (!ok) break;
+        ++p_t;
+        if (++pf == ps.tiles) {
+          pf = 0;
+          p_next();
+          if (!p_end) p_mine = slot == 0 || rows_of(ps) > kTile;
+        }
+        if (!q_end) ok = do_qk();
+      }
+    }
+    // Products in flight end before the block does.
+    commit(leader, &bars.drain[slot]);
+    const int none = 0;
+    ptx::mbar_wait(&bars.drain[slot], 0, &none, kWaitLimit);
+  } else if (warp == 3) {
     // ---- queries into shared memory
-    const int at = tid - 64;
+    const int at = lane;
     Segments seg(a, share);
     do {
-      const int buf = seg.index % S::kQBufs, turn = seg.index / S::kQBufs;
-      if (turn > 0) wait(&bars.q_empty[buf], turn - 1);
+      if (seg.index > 0) wait(&bars.q_empty, seg.index - 1);
       const int r0 = r0_of(seg), rows = rows_of(seg), n = seg.p.s.n;
       const int64_t bh = (int64_t)seg.p.seq * a.heads + seg.p.head;
       const int slots = TWO && rows > 128 ? 2 : 1;
-      // A thread has every (64 / kPieces)-th row's piece c, eight of them under way at a time.
-      constexpr int kPieces = D / 8, kStep = 64 / kPieces;
+      // A thread has every (32 / kPieces)-th row's piece c, all of them under way at a time.
+      constexpr int kPieces = D / 8, kStep = 32 / kPieces;
       const int c = at % kPieces;
-#pragma unroll 1
-      for (int x = at / kPieces; x < slots * kTile; x += 8 * kStep) {
-        uint4 v[8];
+      int g = (r0 + at / kPieces) / n, t = (r0 + at / kPieces) % n;
+      const __nv_bfloat16* const from = static_cast<const __nv_bfloat16*>(a.q) + bh * a.group * a.tokens * D + 8 * c;
+#pragma unroll 4
+      for (int r = at / kPieces; r < slots * kTile; r += kStep) {
+        const bool there = r < rows;
+        const uint32_t to = q_smem + (r / kTile) * S::kSlotQ + piece_at(r % kTile, c);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from + (there ? ((int64_t)g * a.tokens + t) * D : 0)), "r"(there ? 16 : 0) : "memory");
+        for (t += kStep; t >= n; t -= n) ++g;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if constexpr (Q8) {
+#pragma unroll 4
+        for (int r = at / kPieces; r < min(rows, slots * kTile); r += kStep) {
+          uint4* const u = reinterpret_cast<uint4*>(smem + S::kQ + (r / kTile) * S::kSlotQ + piece_at(r % kTile, c));
+          uint4 v = *u;
+          uint32_t* const w = &v.x;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int r = x + e * kStep, row = r0 + r, g = row / n;
-          v[e] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < rows) v[e] = ld_nc_v4(static_cast<const __nv_bfloat16*>(a.q) + ((bh * a.group + g) * a.tokens + (row - g * n)) * D + 8 * c);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int r = x + e * kStep;
-          if constexpr (Q8) {
-            uint32_t* const w = &v[e].x;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = pack2(__uint_as_float(w[i] << 16) * kQ8Q, __uint_as_float(w[i] & 0xFFFF0000u) * kQ8Q);
-          }
-          *reinterpret_cast<uint4*>(smem + S::kQ + (TWO ? r / kTile : buf) * S::kSlotQ + piece_at(r % kTile, c)) = v[e];
+          for (int i = 0; i < 4; ++i) w[i] = pack2(__uint_as_float(w[i] << 16) * kQ8Q, __uint_as_float(w[i] & 0xFFFF0000u) * kQ8Q);
+          *u = v;
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      ptx::mbar_arrive(&bars.q_full[buf]);
+      ptx::mbar_arrive(&bars.q_full);
     } while (seg.next(a) && !aborted());
   } else if (warp < 12) {
     // ---- softmax: a thread per row of a slot
@@ -460,15 +517,17 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           fk[kTile + row] = v;
           ptx::named_barrier(1 + slot, 128);
         }
+        wait(&bars.s_full[slot], steps);
+        ptx::tc_fence_after();
         uint32_t bad[4] = {0u, 0u, 0u, 0u};
         if (edge && (!Q8 || drafted)) {
           // V's rows that nobody sees become zeros, as do drafted ones with an infinity or NaN, which the rows that see
-          // them get as a NaN weight: 0 times it must not reach the others. A thread looks after a key.
+          // them get as a NaN weight: 0 times it must not reach the others. A thread looks after a key. (S is there, so the slot's
+          // last P V is done, and the stage's phase before V's has passed.)
           if (!TWO || slot == 0) {
-            const uint32_t t = done + f;
-            const uint32_t at = TWO ? 2 * t + 1 : (int64_t)t + 1 == total ? 2 * t + 1 : 2 * t + 2;   // V's place in the ring's order
-            wait(&bars.kv_full[at % kStages], at / kStages);
-            uint8_t* const v = smem + S::kRing + (at % kStages) * S::kStage;
+            const uint32_t at = 2 * (TWO ? done + f : steps) + 1, stage = S::stage(slot, at);   // V's place in the ring
+            wait(&bars.kv_full[stage], at / S::kTurn);
+            uint8_t* const v = smem + S::kRing + stage * S::kStage;
             bool fix = row >= valid;
             if (drafted) {
               bool inf = false;
@@ -485,16 +544,14 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
               for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(v + piece_at(row, c)) = make_uint4(0u, 0u, 0u, 0u);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
+          const bool both = TWO && rows_of(seg) > kTile;
+          if (drafted || both) ptx::named_barrier(both ? 3 : 1 + slot, both ? 256 : 128);   // (the other slot's products read V, too)
           if (drafted) {
-            const bool both = TWO && rows_of(seg) > 128;
-            ptx::named_barrier(both ? 3 : 1 + slot, both ? 256 : 128);
 #pragma unroll
             for (int w = 0; w < 4; ++w) bad[w] = bad_keys[TWO ? 0 : slot][w] & see[w];
             ptx::named_barrier(both ? 3 : 1 + slot, both ? 256 : 128);   // (before the next tile's are written)
           }
         }
-        wait(&bars.s_full[slot], steps);
-        ptx::tc_fence_after();
         // Logits of chunk c (32 keys) as they are compared: 8-bit keys' steps are in.
         auto scaled = [&](uint32_t (&x)[32], int c) {
           if constexpr (Q8) {
@@ -551,6 +608,12 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           }
           tmem_st32(s_at + 32 * c, p);
         };
+        auto ready = [&](int half) {
+          if (mine) ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&bars.p_ready[slot][half]);
+        };
         auto highest = [](const uint32_t (&x)[32], float top) {
           float other = -INFINITY;
 #pragma unroll
@@ -561,7 +624,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           return fmaxf(top, other);
         };
         if (mine && !edge) {
-          // Chunks 0 and 1, then 2 and 3 for the maximum; weights from 2 and 3 while they are there, then 0 and 1 again.
+          // Chunks 0 to 3 for the maximum; weights from 2 and 3, which are still there, then from 0 and 1 once more.
           uint32_t x[32], y[32];
           float top = -INFINITY;
           tmem_ld32(s_at, x);
@@ -583,6 +646,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           weigh(x, 2, std::false_type(), 0u, 0u);
           tmem_ld32(s_at, x);
           weigh(y, 3, std::false_type(), 0u, 0u);
+          ready(0);
           ptx::tmem_wait_ld();
           tmem_ld32(s_at + 32, y);
           scaled(x, 0);
@@ -590,6 +654,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           ptx::tmem_wait_ld();
           scaled(y, 1);
           weigh(y, 1, std::false_type(), 0u, 0u);
+          ready(1);
         } else if (mine) {
           auto word = [](const uint32_t (&w)[4], int c) { return c == 0 ? w[0] : c == 1 ? w[1] : c == 2 ? w[2] : w[3]; };
           float top = -INFINITY;
@@ -606,22 +671,21 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           }
           raise(top);
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int i = 0; i < 4; ++i) {
+            const int c = i ^ 2;
             uint32_t x[32];
             tmem_ld32(s_at + 32 * c, x);
             ptx::tmem_wait_ld();
             scaled(x, c);
             weigh(x, c, std::true_type(), word(see, c), word(bad, c));
+            if (i % 2) ready(i / 2);
           }
+        } else {
+          ready(0);
+          ready(1);
         }
-        if (mine) {
-          l += sum.x + sum.y;
-          ptx::tmem_wait_st();
-        }
+        l += sum.x + sum.y;
         first = false;
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&bars.p_ready[slot]);
         ++steps;
       }
 
@@ -716,9 +780,9 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
     const int key = tid - 12 * 32;
     Segments ks(a, share), vs(a, share);
     int kf = 0, vf = 0;
-    uint32_t made = 0, used = 0;       // tiles made, and raw ones used
-    auto make = [&](Segments& s, int& f, bool is_key) {
-      const uint32_t slot = made % kStages, turn = made / kStages;
+    uint32_t used = 0;                 // raw tiles
+    auto make = [&](Segments& s, int& f, uint32_t t, bool is_key) {
+      const uint32_t place = 2 * (TWO ? t : t / 2) + (is_key ? 0 : 1), slot = S::stage(t & 1, place), turn = place / S::kTurn;
       const int tile = s.p.tile + f;
       const int64_t bh = (int64_t)s.p.seq * a.heads + s.p.head;
       const bool cached = tile < s.p.s.cache_tiles;
@@ -757,17 +821,14 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&bars.kv_full[slot]);
-      ++made;
       if (++f == s.tiles) {
         f = 0;
         s.next(a);
       }
     };
-    make(ks, kf, true);
-    if (!TWO && total > 1) make(ks, kf, true);
-    for (int64_t t = 0; t < total && !__any_sync(0xffffffffu, aborted()); ++t) {   // (all of a warp leave together)
-      make(vs, vf, false);
-      if (t + (TWO ? 1 : 2) < total) make(ks, kf, true);
+    for (uint32_t t = 0; t < total && !__any_sync(0xffffffffu, aborted()); t += kPair) {   // (all of a warp leave together)
+      for (uint32_t u = t; u < t + kPair && u < total; ++u) make(ks, kf, u, true);
+      for (uint32_t u = t; u < t + kPair && u < total; ++u) make(vs, vf, u, false);
     }
   }
 

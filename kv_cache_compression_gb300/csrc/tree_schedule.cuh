@@ -39,7 +39,7 @@ struct Args {
   int least;            // tiles that a share has at least, where there are as many
   // workspace
   int64_t* upto;        // [batch + 1]: tiles in the sequences before, and in all
-  float* parts;         // [ctas][2] of (o [tile_q][D], m [tile_q] (log2 domain), l [tile_q])
+  float* parts;         // [ctas][2] of (o [tile_q][D] or [D][tile_q], m [tile_q] (log2 domain), l [tile_q])
   int32_t* dev_status;
 };
 
@@ -187,5 +187,7 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 
 // The joining launch: out and lse of the rows whose heads were cut, and of those that see nothing.
 template <typename IO, int D, int TILE, int NEW> cudaError_t launch_tree_join(const tree::Args& a, cudaStream_t stream);
+// The same for bf16 calls of passes of 128 or 256 rows, whose parts hold o as [D][tile_q].
+template <int D, int TILE> cudaError_t launch_tree_join_wide(const tree::Args& a, cudaStream_t stream);
 
 }  // namespace snapkv

@@ -348,8 +348,7 @@ template <typename IO, bool Q8> cudaError_t launch_format(const TreeJob& job) {
 }  // namespace
 
 cudaError_t launch_tree_simt(const TreeJob& job) {
-  if (job.dtype == SNAPKV_F32) return job.k_step ? launch_format<float, true>(job) : launch_format<float, false>(job);
-  return job.k_step ? launch_format<__nv_bfloat16, true>(job) : launch_format<__nv_bfloat16, false>(job);
+  return job.k_step ? launch_format<float, true>(job) : launch_format<float, false>(job);
 }
 
 }  // namespace snapkv

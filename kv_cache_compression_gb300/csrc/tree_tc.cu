@@ -66,8 +66,8 @@ template <bool Q8, int D, bool TWO> struct Shape {
 
 struct Bars {
   uint64_t kv_full[12], kv_empty[12], raw_full[8], raw_empty[8];
-  uint64_t q_full, q_empty, s_full[2], p_ready[2][2];   // (p_ready: of a slot, by halves of the keys)
-  uint64_t o_full, o_free, drain[2];
+  uint64_t q_full, q_empty, s_full[2], p_ready[2];
+  uint64_t o_full, o_free, drain[2], turn[2];   // (turn: the slot may issue its next products)
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
@@ -185,8 +185,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&bars.s_full[i], 1);
-      ptx::mbar_init(&bars.p_ready[i][0], 4);
-      ptx::mbar_init(&bars.p_ready[i][1], 4);
+      ptx::mbar_init(&bars.p_ready[i], 4);
     }
     ptx::mbar_init(&bars.q_full, 32);
     ptx::mbar_init(&bars.q_empty, 2);
@@ -194,6 +193,8 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
     ptx::mbar_init(&bars.o_free, 8);
     ptx::mbar_init(&bars.drain[0], 1);
     ptx::mbar_init(&bars.drain[1], 1);
+    ptx::mbar_init(&bars.turn[0], 1);
+    ptx::mbar_init(&bars.turn[1], 1);
     ptx::fence_mbar_init();
   }
   const Share share = find_share<kTile, kTile, S::kThreads>(a);   // (with barriers)
@@ -276,132 +277,101 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
     const uint32_t leader = lane == 0;
     const uint32_t s_at = uniform(tmem + S::kS(slot)), o_at = uniform(tmem + S::kO(slot));
     auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };   // (the warp stays together)
-    uint32_t steps = 0;   // P V of this slot so far
-    // S = Q K^T of the ring's tile `at`.
-    auto qk = [&](uint32_t at) {
-      const uint32_t stage = S::stage(slot, at);
-      if (!wait_all(&bars.kv_full[stage], at / S::kTurn)) return false;
+    // The slots issue in turn: P V of a tile and Q K^T of the slot's next as a block, all that they wait for before. (Left to
+    // themselves both slots' products mix, and then both softmaxes run, and both products wait, at the same time; and a wait
+    // between products, even for a barrier long reached, leaves the tensor core idle.)
+    uint32_t steps = 0, turns = 0;   // P V of this slot, and turns, so far
+    auto my_turn = [&] {
+      const bool mine = slot == 0 && turns == 0 ? true : wait_all(&bars.turn[slot], slot == 0 ? turns - 1 : turns);
+      ++turns;
       ptx::tc_fence_after();
-      const uint32_t q_lo = uniform(k_desc(q_smem + (TWO ? slot : 0) * S::kSlotQ)), k_lo = uniform(k_desc(ring + stage * S::kStage));
+      return mine;
+    };
+    auto pass_on = [&] {
+      if (leader) ptx::mbar_arrive(&bars.turn[1 - slot]);
+      __syncwarp();
+    };
+    auto full = [&](uint32_t at) { return wait_all(&bars.kv_full[S::stage(slot, at)], at / S::kTurn); };
+    // S = Q K^T of the ring's tile `at`.
+    const uint32_t q_lo = uniform(k_desc(q_smem + (TWO ? slot : 0) * S::kSlotQ));
+    auto qk = [&](uint32_t at) {
+      const uint32_t k_lo = uniform(k_desc(ring + S::stage(slot, at) * S::kStage));
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
         const uint32_t off = ((s / 4) * (kTile * 128) + (s % 4) * 32) >> 4;
         mma_ss(leader, s_at, q_lo + off, k_lo + off, kDescHigh, kIdescQk, s > 0);
       }
-      commit(leader, &bars.s_full[slot]);
-      commit(leader, &bars.kv_empty[stage]);
-      return true;
     };
-    // O += P V of the ring's tile `at`, the upper half of the keys first, as their weights are there first; `fresh`: O =.
+    // O += P V of the ring's tile `at`; `fresh`: O =.
     auto pv = [&](uint32_t at, bool fresh) {
-      const uint32_t stage = S::stage(slot, at);
-      if (!wait_all(&bars.kv_full[stage], at / S::kTurn)) return false;
-      const uint32_t v_lo = uniform(v_desc(ring + stage * S::kStage));
+      const uint32_t v_lo = uniform(v_desc(ring + S::stage(slot, at) * S::kStage));
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (!wait_all(&bars.p_ready[slot][half], steps)) return false;
-        ptx::tc_fence_after();
+      for (int s = 0; s < kTile / 16; ++s)
 #pragma unroll
-        for (int i = 0; i < kTile / 32; ++i)
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            const int s = (1 - half) * (kTile / 32) + i;
-            mma_ts(leader, o_at, s_at + (s / 2) * 32 + part * 16 + (s % 2) * 8, v_lo + s * (2048 >> 4), kDescHigh, kIdescPv,
-                   !(fresh && half == 0 && i == 0 && part == 0));
-          }
-      }
-      ++steps;
-      commit(leader, &bars.kv_empty[stage]);
-      return true;
+        for (int part = 0; part < 2; ++part)
+          mma_ts(leader, o_at, s_at + (s / 2) * 32 + part * 16 + (s % 2) * 8, v_lo + s * (2048 >> 4), kDescHigh, kIdescPv,
+                 !(fresh && s == 0 && part == 0));
     };
     // Walks of the Q K^T and of the P V, the first a tile of the slot's ahead. A slot waits for every segment's queries and outputs
     // and counts in on q_empty and o_full at its end, whether it had tiles of it or not: barriers know a phase by its parity
-    // alone, so that none may be passed over.
+    // alone, so that none may be passed over. Up to 128 rows the slot's tiles are every second of the share; of more, all tiles,
+    // but of segments in whose rows it has no part it only lets the loads go on.
+    constexpr int kBy = TWO ? 1 : 2;
     Segments qs(a, share), ps(a, share);
-    bool q_end = false, p_end = false;
-    uint32_t q_t = 0, p_t = 0;   // the slot's tiles so far
-    auto q_next = [&] {
-      commit(leader, &bars.q_empty);
-      q_end = !qs.next(a);
-    };
-    auto p_next = [&] {
-      commit(leader, &bars.o_full);
-      p_end = !ps.next(a);
-    };
+    int qf = TWO ? 0 : slot, pf = qf;        // within the segments
+    uint32_t q_t = 0, p_t = 0;               // the slot's tiles so far
+    bool q_end = false, p_end = false, ok = true;
+    auto takes_part = [&](const Segments& s) { return !TWO || slot == 0 || rows_of(s) > kTile; };
+    bool q_mine = takes_part(qs), p_mine = q_mine;
     auto queries = [&] { return wait_all(&bars.q_full, qs.index); };
     auto outputs = [&] { return ps.index == 0 || wait_all(&bars.o_free, ps.index - 1); };
-    bool ok = true;
-    if constexpr (!TWO) {
-      int qf_tiles = 0;            // of a segment that is left
-      // every second tile of the share
-      int qf = slot, pf = slot;    // within their segments
-      auto do_qk = [&] {           // (nothing where there is no other)
-        for (; !q_end && qf >= qs.tiles; qf -= qf_tiles) {   // a segment without tiles of the slot's
-          if (!queries()) return false;
-          qf_tiles = qs.tiles;
-          q_next();
-        }
-        if (q_end) return true;
-        if (qf < 2 && !queries()) return false;   // (a segment's first two tiles are its slots' first)
-        if (!qk(2 * q_t)) return false;
-        ++q_t;
-        qf += 2;
-        if (qf >= qs.tiles) {
-          qf -= qs.tiles;
-          q_next();
-        }
-        return true;
-      };
-      ok = do_qk();
-      while (ok) {
-        for (; ok && !p_end && pf >= ps.tiles; pf -= qf_tiles) {
+    auto q_next = [&] {
+      qf -= qs.tiles;
+      commit(leader, &bars.q_empty);
+      q_end = !qs.next(a);
+      if (!q_end) q_mine = takes_part(qs);
+    };
+    auto p_next = [&] {
+      pf -= ps.tiles;
+      commit(leader, &bars.o_full);
+      p_end = !ps.next(a);
+      if (!p_end) p_mine = takes_part(ps);
+    };
+    for (bool begin = true; ok; begin = false) {
+      // what this turn's products need
+      if (!begin) {
+        while (ok && !p_end && pf >= ps.tiles) {   // a segment without tiles of the slot's
           ok = outputs();
-          qf_tiles = ps.tiles;
           if (ok) p_next();
         }
         if (!ok || p_end) break;
-        ok = (pf >= 2 || outputs()) && pv(2 * p_t + 1, pf < 2);
-        if (!ok) break;
-        ++p_t;
-        pf += 2;
-        if (pf >= ps.tiles) {
-          pf -= ps.tiles;
-          p_next();
-        }
-        ok = do_qk();
+        ok = (pf >= kBy || outputs()) && full(2 * p_t + 1);   // (a segment's first tiles are its slots' first)
+        if (ok && p_mine) ok = wait_all(&bars.p_ready[slot], steps);
       }
-    } else {
-      // all tiles of the segments of which the slot has rows; of the others it only lets the loads go on
-      int qf = 0, pf = 0;
-      bool q_mine = slot == 0 || rows_of(qs) > kTile, p_mine = q_mine;
-      auto skip = [&](uint32_t at) {
-        const bool there = wait_all(&bars.kv_full[S::stage(slot, at)], at / S::kTurn);
-        if (there && leader) ptx::mbar_arrive(&bars.kv_empty[S::stage(slot, at)]);
-        __syncwarp();
-        return there;
-      };
-      auto do_qk = [&] {
-        if (qf == 0 && !queries()) return false;
-        if (!(q_mine ? qk(2 * q_t) : skip(2 * q_t))) return false;
-        ++q_t;
-        if (++qf == qs.tiles) {
-          qf = 0;
-          q_next();
-          if (!q_end) q_mine = slot == 0 || rows_of(qs) > kTile;
-        }
-        return true;
-      };
-      ok = do_qk();
-      while (ok && !p_end) {
-        ok = (pf > 0 || outputs()) && (p_mine ? pv(2 * p_t + 1, pf == 0) : skip(2 * p_t + 1));
-        if (!ok) break;
+      while (ok && !q_end && qf >= qs.tiles) {
+        ok = queries();
+        if (ok) q_next();
+      }
+      const bool more = !q_end;
+      if (ok && more) ok = (qf >= kBy || queries()) && full(2 * q_t);
+      if (!ok || !my_turn()) break;
+      if (!begin && p_mine) pv(2 * p_t + 1, pf < kBy);
+      if (more && q_mine) qk(2 * q_t);
+      pass_on();
+      // what waits for them
+      if (more && q_mine) commit(leader, &bars.s_full[slot]);
+      if (!begin) {
+        commit(leader, &bars.kv_empty[S::stage(slot, 2 * p_t + 1)]);
+        if (p_mine) ++steps;
         ++p_t;
-        if (++pf == ps.tiles) {
-          pf = 0;
-          p_next();
-          if (!p_end) p_mine = slot == 0 || rows_of(ps) > kTile;
-        }
-        if (!q_end) ok = do_qk();
+        pf += kBy;
+        if (pf >= ps.tiles) p_next();
+      }
+      if (more) {
+        commit(leader, &bars.kv_empty[S::stage(slot, 2 * q_t)]);
+        ++q_t;
+        qf += kBy;
+        if (qf >= qs.tiles) q_next();
       }
     }
     // Products in flight end before the block does.
@@ -417,22 +387,31 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
       const int r0 = r0_of(seg), rows = rows_of(seg), n = seg.p.s.n;
       const int64_t bh = (int64_t)seg.p.seq * a.heads + seg.p.head;
       const int slots = TWO && rows > 128 ? 2 : 1;
-      // A thread has every (32 / kPieces)-th row's piece c, all of them under way at a time.
+      // A thread has every (32 / kPieces)-th row's piece c, all of them under way at a time. Rows follow one another in memory but for
+      // the tokens that a sequence does not have. (A warp alone: what it computes for a piece is what the load takes.)
       constexpr int kPieces = D / 8, kStep = 32 / kPieces;
-      const int c = at % kPieces;
-      int g = (r0 + at / kPieces) / n, t = (r0 + at / kPieces) % n;
-      const __nv_bfloat16* const from = static_cast<const __nv_bfloat16*>(a.q) + bh * a.group * a.tokens * D + 8 * c;
-#pragma unroll 4
-      for (int r = at / kPieces; r < slots * kTile; r += kStep) {
-        const bool there = r < rows;
-        const uint32_t to = q_smem + (r / kTile) * S::kSlotQ + piece_at(r % kTile, c);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from + (there ? ((int64_t)g * a.tokens + t) * D : 0)), "r"(there ? 16 : 0) : "memory");
-        for (t += kStep; t >= n; t -= n) ++g;
+      const int c = at % kPieces, first = at / kPieces;
+      int t = (r0 + first) % n;
+      const int64_t gap = (int64_t)(a.tokens - n) * D;
+      const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.q) + (bh * a.group + (r0 + first) / n) * a.tokens * D + (int64_t)t * D + 8 * c;
+      uint32_t place[8 / kStep];   // of rows first + e kStep, and of those 8, 16, ... further on but for a multiple of 1024
+#pragma unroll
+      for (int e = 0; e < 8 / kStep; ++e) place[e] = q_smem + piece_at(first + e * kStep, c);
+#pragma unroll 1
+      for (int x = 0; x < slots * kTile; x += 8) {
+        const uint32_t base = (x / kTile) * S::kSlotQ + (x % kTile) * 128;
+#pragma unroll
+        for (int e = 0; e < 8 / kStep; ++e) {
+          const bool there = x + first + e * kStep < rows;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(place[e] + base), "l"(there ? from : static_cast<const __nv_bfloat16*>(a.q)), "r"(there ? 16 : 0) : "memory");
+          from += kStep * D;
+          for (t += kStep; t >= n; t -= n) from += gap;
+        }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       if constexpr (Q8) {
 #pragma unroll 4
-        for (int r = at / kPieces; r < min(rows, slots * kTile); r += kStep) {
+        for (int r = first; r < min(rows, slots * kTile); r += kStep) {
           uint4* const u = reinterpret_cast<uint4*>(smem + S::kQ + (r / kTile) * S::kSlotQ + piece_at(r % kTile, c));
           uint4 v = *u;
           uint32_t* const w = &v.x;
@@ -608,12 +587,6 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           }
           tmem_st32(s_at + 32 * c, p);
         };
-        auto ready = [&](int half) {
-          if (mine) ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&bars.p_ready[slot][half]);
-        };
         auto highest = [](const uint32_t (&x)[32], float top) {
           float other = -INFINITY;
 #pragma unroll
@@ -646,7 +619,6 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           weigh(x, 2, std::false_type(), 0u, 0u);
           tmem_ld32(s_at, x);
           weigh(y, 3, std::false_type(), 0u, 0u);
-          ready(0);
           ptx::tmem_wait_ld();
           tmem_ld32(s_at + 32, y);
           scaled(x, 0);
@@ -654,7 +626,6 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           ptx::tmem_wait_ld();
           scaled(y, 1);
           weigh(y, 1, std::false_type(), 0u, 0u);
-          ready(1);
         } else if (mine) {
           auto word = [](const uint32_t (&w)[4], int c) { return c == 0 ? w[0] : c == 1 ? w[1] : c == 2 ? w[2] : w[3]; };
           float top = -INFINITY;
@@ -671,20 +642,19 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           }
           raise(top);
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            const int c = i ^ 2;
+          for (int c = 0; c < 4; ++c) {
             uint32_t x[32];
             tmem_ld32(s_at + 32 * c, x);
             ptx::tmem_wait_ld();
             scaled(x, c);
             weigh(x, c, std::true_type(), word(see, c), word(bad, c));
-            if (i % 2) ready(i / 2);
           }
-        } else {
-          ready(0);
-          ready(1);
         }
         l += sum.x + sum.y;
+        if (mine) ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars.p_ready[slot]);
         first = false;
         ++steps;
       }
@@ -715,9 +685,9 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           for (int e = 0; e < 4; ++e)
             u[e] = make_uint4(pack2(x[8 * e], x[8 * e + 1]), pack2(x[8 * e + 2], x[8 * e + 3]), pack2(x[8 * e + 4], x[8 * e + 5]), pack2(x[8 * e + 6], x[8 * e + 7]));
         } else {
-          float4* const u = reinterpret_cast<float4*>(part + (int64_t)pr * D + c);
+          float* const u = part + c * S::kRows + pr;   // (a warp's rows lie side by side)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) u[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+          for (int e = 0; e < 32; ++e) u[e * S::kRows] = x[e];
         }
       };
       if constexpr (TWO) {
@@ -859,7 +829,7 @@ template <bool Q8, int D, bool TWO> cudaError_t launch_typed(const TreeJob& job)
   if (err != cudaSuccess) return err;
   tree_tc_kernel<Q8, D, TWO><<<a.ctas, S::kThreads, S::smem(), job.stream>>>(a, maps);
   err = cudaGetLastError();
-  return err != cudaSuccess ? err : launch_tree_join<__nv_bfloat16, D, kTile, kTile>(a, job.stream);
+  return err != cudaSuccess ? err : launch_tree_join_wide<D, kTile>(a, job.stream);
 }
 
 template <bool Q8, int D> cudaError_t launch_dim(const TreeJob& job) {

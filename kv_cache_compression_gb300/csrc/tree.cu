@@ -100,6 +100,7 @@ bool tree_maps(TreeMaps* maps, const TreeJob& job, int tile, int fresh) {
              !tc::make_map(&maps->v, job.v, job.head_dim, job.cap, bh, tile)) {
     return false;
   }
+  if (!tc::make_map(&maps->q, job.q, job.head_dim, (int64_t)job.batch * job.q_heads * job.tokens, 1, tile)) return false;
   if (!job.k_new) {
     maps->k_new = maps->k;
     maps->v_new = maps->v;

@@ -127,7 +127,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const Args a, con
       for (int s = 0; s < kStages; ++s) ptx::mbar_init(&full[w][s], Q8 ? 33 : 1);
     ptx::fence_mbar_init();
   }
-  const Share share = find_share<kTile, kNew, kThreads>(a);   // (with barriers)
+  __shared__ ShareScratch<kThreads> scratch;
+  const Share share = find_share<kTile, kNew, kThreads>(a, scratch);   // (with barriers)
   if (share.at >= share.end) return;
   Place here = first_place<kTile, kNew>(a, share);
   Place ahead = here;              // the next tile to load

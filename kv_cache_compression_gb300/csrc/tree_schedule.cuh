@@ -90,9 +90,13 @@ struct Share {
 
 // All threads of a block of THREADS find their CTA's share (at == end: none). Sequence lengths are summed up by every
 // CTA for itself; CTA 0 leaves the sums for the joining launch and reports what is out of range.
-template <int TILE, int NEW, int THREADS> __device__ __forceinline__ Share find_share(const Args& a) {
-  __shared__ int64_t warp_sums[THREADS / 32];
-  __shared__ Share found;
+template <int THREADS> struct ShareScratch {   // shared memory
+  int64_t warp_sums[THREADS / 32];
+  Share found;
+};
+template <int TILE, int NEW, int THREADS> __device__ __forceinline__ Share find_share(const Args& a, ShareScratch<THREADS>& scratch) {
+  int64_t (&warp_sums)[THREADS / 32] = scratch.warp_sums;
+  Share& found = scratch.found;
   const int tid = threadIdx.x, lane = tid % 32;
   const int chunk = (a.batch + THREADS - 1) / THREADS;
   const int b0 = min(a.batch, tid * chunk), b1 = min(a.batch, b0 + chunk);

@@ -134,7 +134,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
   auto q_hash = [](int row) { return (row / kRq) & 7; };
   auto k_hash = [](int row) { return (row / kRk) & 7; };
   auto v_hash = [](int) { return 0; };
-  const Share share = find_share<kTile, kTile, kThreads>(a);
+  __shared__ ShareScratch<kThreads> scratch;
+  const Share share = find_share<kTile, kTile, kThreads>(a, scratch);
   if (share.at >= share.end) return;
   Place here = first_place<kTile, kTile>(a, share);
   // first product: rows kRq qg .. by keys kRk kg ..

@@ -40,34 +40,44 @@ constexpr float kSlack = 8.0f;                   // log2 of what weights may exc
 constexpr float kQ8Q = 0x1p64f, kQ8Dot = 0x1p69f, kQ8P = 0x1p80f, kQ8Out = 0x1p53f;
 constexpr float kNewDot = 0x1p-64f, kNewP = 0x1p-53f;   // for drafted rows, whose values are as they are
 
+// What is small in shared memory. (All of it is laid out here: with 192 KB of tiles 160 bytes are left.)
+struct Bars {
+  uint64_t kv_full[12], kv_empty[12], raw_full[8], raw_empty[8];
+  uint64_t q_full, q_empty, s_full[2], p_ready[2];
+  uint64_t o_full, o_free, drain[2], turn[2];   // (turn: the slot may issue its next products)
+};
+template <int THREADS> struct Small {
+  Bars bars;
+  uint32_t tmem;
+  int abort;
+  uint32_t bad_keys[2][4];
+  uint8_t pending[12];   // of a stage's last load, if any: 1 + its phase's parity
+  ShareScratch<THREADS> share;
+};
+
 template <bool Q8, int D, bool TWO> struct Shape {
   static constexpr int kRows = TWO ? 256 : 128;                // query rows of a pass
-  static constexpr int kWarps = Q8 ? 16 : 12;
+  static constexpr int kSoft = 16;                             // softmax warps: two for 32 rows of a slot, half of the keys each
+  static constexpr int kWarps = 4 + kSoft + (Q8 ? 4 : 0);
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kSlotQ = kTile * D * 2;                 // bytes of 128 rows of queries
   static constexpr int kStage = kTile * D * 2;                 // of a tile of K or V
-  static constexpr int kStages = (Q8 ? (TWO ? 3 : 4) : TWO ? 5 : 6) * (128 / D);   // (TWO: of one ring; else of two, a slot's each)
+  static constexpr int kStages = (Q8 ? (TWO ? 3 : 4) : TWO ? 4 : 6) * (128 / D);   // (TWO: of one ring; else of two, a slot's each)
   static constexpr int kTurn = TWO ? kStages : kStages / 2;
   static constexpr int kRaw = kTile * D;                       // of a tile of codes
   static constexpr int kRaws = Q8 ? 3 * (128 / D) : 0;
   static constexpr int kQ = 0;
   static constexpr int kRing = kQ + (TWO ? 2 : 1) * kSlotQ;
   static constexpr int kRawRing = kRing + kStages * kStage;
-  static constexpr int kMeet = kRawRing + kRaws * kRaw;        // [128] float2
-  static constexpr int kFactors = kMeet + kTile * 8;           // [2 slots][2][K, V][128] floats (8 bits)
-  static constexpr int kBytes = kFactors + (Q8 ? 2 * 2 * 2 * kTile * 4 : 0);
-  static constexpr int smem() { return 1024 + kBytes; }
+  static constexpr int kSwap = kRawRing + kRaws * kRaw;        // [2 slots][2 halves][128] floats
+  static constexpr int kFactors = kSwap + 4 * kTile * 4;       // [2 slots][2][K, V][128] floats (8 bits)
+  static constexpr int kSmall = kFactors + (Q8 ? 2 * 2 * 2 * kTile * 4 : 0);
+  static constexpr int smem() { return kSmall + (int)sizeof(Small<kThreads>); }
   // The stage of a ring's tile `at`: of a slot's tile i, K is 2 i and V 2 i + 1.
   __device__ __forceinline__ static uint32_t stage(int slot, uint32_t at) { return (TWO ? 0 : slot * kTurn) + at % kTurn; }
   static constexpr int kS(int slot) { return slot * 128; }     // TMEM columns
   static constexpr int kO(int slot) { return 256 + slot * D; }
   static constexpr int kColumns = 512;
-};
-
-struct Bars {
-  uint64_t kv_full[12], kv_empty[12], raw_full[8], raw_empty[8];
-  uint64_t q_full, q_empty, s_full[2], p_ready[2];
-  uint64_t o_full, o_free, drain[2], turn[2];   // (turn: the slot may issue its next products)
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
@@ -79,6 +89,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
         "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(at));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) {
   asm volatile(
@@ -163,18 +185,19 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
   using S = Shape<Q8, D, TWO>;
   constexpr int kStages = S::kStages, kRaws = S::kRaws > 0 ? S::kRaws : 1;
   static_assert(kStages <= 12 && kRaws <= 8, "barriers");
-  extern __shared__ uint8_t raw_smem[];
-  __shared__ Bars bars;
-  __shared__ uint32_t tmem_at;
-  __shared__ int abort;
-  __shared__ uint32_t bad_keys[2][4];
-  __shared__ uint8_t pending[12];   // of a stage's last load, if any: 1 + its phase's parity
-  uint8_t* const smem = raw_smem + ((1024 - (ptx::smem_u32(raw_smem) & 1023)) & 1023);
+  extern __shared__ __align__(1024) uint8_t smem[];   // (swizzled tiles: 1024 bytes)
+  Small<S::kThreads>& small = *reinterpret_cast<Small<S::kThreads>*>(smem + S::kSmall);
+  Bars& bars = small.bars;
+  int& abort = small.abort;
+  if ((ptx::smem_u32(smem) & 1023) != 0) {
+    report(a.dev_status, SNAPKV_ERR_INTERNAL);
+    return;
+  }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid % 32, warp = __shfl_sync(0xffffffffu, tid / 32, 0);
   if (tid == 0) {
     abort = 0;
-    for (int i = 0; i < 12; ++i) pending[i] = 0;
+    for (int i = 0; i < 12; ++i) small.pending[i] = 0;
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&bars.kv_full[i], Q8 ? 4 : 1);   // (four unpacking warps)
       ptx::mbar_init(&bars.kv_empty[i], TWO ? 2 : 1);   // (slots)
@@ -185,28 +208,28 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&bars.s_full[i], 1);
-      ptx::mbar_init(&bars.p_ready[i], 4);
+      ptx::mbar_init(&bars.p_ready[i], S::kSoft / 2);
     }
-    ptx::mbar_init(&bars.q_full, 32);
+    ptx::mbar_init(&bars.q_full, 1);
     ptx::mbar_init(&bars.q_empty, 2);
     ptx::mbar_init(&bars.o_full, 2);
-    ptx::mbar_init(&bars.o_free, 8);
+    ptx::mbar_init(&bars.o_free, S::kSoft);
     ptx::mbar_init(&bars.drain[0], 1);
     ptx::mbar_init(&bars.drain[1], 1);
     ptx::mbar_init(&bars.turn[0], 1);
     ptx::mbar_init(&bars.turn[1], 1);
     ptx::fence_mbar_init();
   }
-  const Share share = find_share<kTile, kTile, S::kThreads>(a);   // (with barriers)
+  const Share share = find_share<kTile, kTile, S::kThreads>(a, small.share);   // (with barriers)
   if (share.at >= share.end) return;
   if (warp == 1) {
-    ptx::tmem_alloc(&tmem_at, S::kColumns);
+    ptx::tmem_alloc(&small.tmem, S::kColumns);
     ptx::tmem_relinquish();
     ptx::tc_fence_before();
   }
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = tmem_at;
+  const uint32_t tmem = small.tmem;
   const uint32_t ring = ptx::smem_u32(smem + S::kRing), q_smem = ptx::smem_u32(smem + S::kQ);
   const int pass0 = a.siblings > 1 ? (int)blockIdx.x % a.siblings : 0;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -221,15 +244,6 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
   auto rows_of = [&](const Segments& s) { return min(a.tile_q, a.group * s.p.s.n - r0_of(s)); };
   const uint32_t total = (uint32_t)(share.end - share.at);   // tiles
   constexpr uint32_t kPair = TWO ? 1 : 2;                    // they are loaded, K before V
-
-  // Registers go from the warps that move data to those of the softmax (the shares sum up to what the block was launched with).
-  if constexpr (Q8) {
-    static_assert(S::kThreads == 512 && 256 * 184 + 256 * 72 == 512 * 128, "registers");
-    if (warp >= 4 && warp < 12)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-    else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  }
 
   if (warp == 0) {
     // ---- loads, in the order in which the products take them
@@ -251,7 +265,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           ptx::mbar_arrive_expect_tx(bar, Q8 ? S::kRaw : S::kStage);
 #pragma unroll
           for (int c = 0; c < (Q8 ? 1 : D / 64); ++c) ptx::tma_load_3d(to + c * kTile * 128, map, 64 * c, row0, bh, bar);
-          pending[slot] = (uint8_t)(1 + (turn & 1));
+          small.pending[slot] = (uint8_t)(1 + (turn & 1));
           ++sent;
         }
         if (++f == s.tiles) {
@@ -267,7 +281,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
       // Copies in flight land before the block ends, also after a wait ran out.
       const int none = 0;
       for (int i = 0; i < (Q8 ? kRaws : kStages); ++i)
-        if (pending[i]) ptx::mbar_wait(Q8 ? &bars.raw_full[i] : &bars.kv_full[i], pending[i] - 1, &none, kWaitLimit);
+        if (small.pending[i]) ptx::mbar_wait(Q8 ? &bars.raw_full[i] : &bars.kv_full[i], small.pending[i] - 1, &none, kWaitLimit);
     }
   } else if (warp < 3) {
     // ---- products of a slot. (One warp for both slots left the tensor core idle for 2000 of a tile's 5200 clocks, while it
@@ -387,6 +401,15 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
       const int r0 = r0_of(seg), rows = rows_of(seg), n = seg.p.s.n;
       const int64_t bh = (int64_t)seg.p.seq * a.heads + seg.p.head;
       const int slots = TWO && rows > 128 ? 2 : 1;
+      if (!Q8 && (a.group == 1 || n == a.tokens)) {   // the rows follow one another: whole tiles, whatever lies behind the head's
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(&bars.q_full, slots * S::kSlotQ);
+          const int row0 = (int)(bh * a.group * a.tokens) + r0;
+          for (int x = 0; x < slots; ++x)
+            for (int c = 0; c < D / 64; ++c) ptx::tma_load_3d(smem + S::kQ + x * S::kSlotQ + c * kTile * 128, &maps.q, 64 * c, row0 + x * kTile, 0, &bars.q_full);
+        }
+        continue;
+      }
       // A thread has every (32 / kPieces)-th row's piece c, all of them under way at a time. Rows follow one another in memory but for
       // the tokens that a sequence does not have. (A warp alone: what it computes for a piece is what the load takes.)
       constexpr int kPieces = D / 8, kStep = 32 / kPieces;
@@ -421,15 +444,21 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      ptx::mbar_arrive(&bars.q_full);
-    } while (seg.next(a) && !aborted());
-  } else if (warp < 12) {
-    // ---- softmax: a thread per row of a slot
-    const int slot = (warp - 4) / 4, quarter = warp % 4, row = quarter * 32 + lane;
-    const uint32_t s_at = tmem + ((uint32_t)(quarter * 32) << 16) + S::kS(slot);
-    const uint32_t o_lane = tmem + ((uint32_t)(quarter * 32) << 16);
-    float2* const meet = reinterpret_cast<float2*>(smem + S::kMeet);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bars.q_full);
+    } while (seg.next(a) && !__any_sync(0xffffffffu, aborted()));
+    if (lane == 0) {   // (a copy in flight lands before the block ends)
+      const int none = 0;
+      ptx::mbar_wait(&bars.q_full, seg.index & 1, &none, kWaitLimit);
+    }
+  } else if (warp < 4 + S::kSoft) {
+    // ---- softmax: two threads per row of a slot, half of the keys each
+    const int slot = (warp - 4) / 8, half = (warp - 4) / 4 % 2, quarter = warp % 4, row = quarter * 32 + lane;
+    const uint32_t o_lane = tmem + ((uint32_t)(quarter * 32) << 16), s_at = o_lane + S::kS(slot);
+    float* const swap = reinterpret_cast<float*>(smem + S::kSwap) + slot * 2 * kTile;   // [half][row]
     float* const factors = reinterpret_cast<float*>(smem + S::kFactors) + slot * 4 * kTile;
+    const int pair = 4 + slot * 4 + quarter;   // the named barrier of the warps that share rows
+    constexpr int kSlotThreads = 32 * S::kSoft / 2;
     uint32_t steps = 0;                // of this slot
     uint32_t done = 0;                 // tiles of the share in the segments so far
     Segments seg(a, share);
@@ -439,7 +468,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
       const bool mine = quarter * 32 < rows;                                  // this warp has rows
       const int64_t bh = (int64_t)seg.p.seq * a.heads + seg.p.head;
       const int r = r0 + row, g = r / n, token = r - g * n;
-      float m = kNoMax, l = 0.f;
+      float m = kNoMax, l = 0.f;       // l: of this thread's keys
       bool first = true;
       for (int f = TWO ? 0 : (int)((done ^ slot) & 1); rows > 0 && f < seg.tiles; f += TWO ? 1 : 2) {
         const int tile = seg.p.tile + f;
@@ -447,17 +476,22 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
         const int key0 = (drafted ? tile - seg.p.s.cache_tiles : tile) * kTile;
         const int valid = min(kTile, (drafted ? n : seg.p.s.rows) - key0);
         const bool edge = drafted || valid < kTile;
-        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+        // This row's bits of the thread's 64 keys: those that it sees, and (below) those that make it NaN.
+        uint32_t see[2] = {~0u, ~0u}, bad[2] = {0u, 0u};
         if (edge) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) see[w] = valid >= 32 * w + 32 ? ~0u : valid > 32 * w ? (1u << (valid - 32 * w)) - 1u : 0u;
+          for (int w = 0; w < 2; ++w) {
+            const int k0 = 64 * half + 32 * w;
+            see[w] = valid >= k0 + 32 ? ~0u : valid > k0 ? (1u << (valid - k0)) - 1u : 0u;
+          }
           if (drafted && a.mask) {
-            // lane e looks at key 32 w + e for one row after the other (rows that are not there have a token, too)
+            // lane e looks at key k0 + e for one row after the other (rows that are not there have a token, too)
             const uint8_t* const mask = a.mask + seg.p.seq * a.mask_stride + key0;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              if (valid <= 32 * w) break;
-              const uint8_t* const from = mask + min(32 * w + lane, valid - 1);
+            for (int w = 0; w < 2; ++w) {
+              const int k0 = 64 * half + 32 * w;
+              if (valid <= k0) break;
+              const uint8_t* const from = mask + min(k0 + lane, valid - 1);
               uint32_t word = 0;
               if (mine)
 #pragma unroll 1
@@ -474,36 +508,33 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
               see[w] &= word;
             }
           } else if (drafted) {   // causal
-            const int upto = token - key0 + 1;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) see[w] &= upto >= 32 * w + 32 ? ~0u : upto > 32 * w ? (1u << (upto - 32 * w)) - 1u : 0u;
+            for (int w = 0; w < 2; ++w) {
+              const int upto = token - key0 + 1 - (64 * half + 32 * w);
+              see[w] &= upto >= 32 ? ~0u : upto > 0 ? (1u << upto) - 1u : 0u;
+            }
           }
         }
         float* const fk = factors + (steps & 1) * 2 * kTile;   // this tile's factors of logits and weights (8 bits)
         if constexpr (Q8) {
-          float k = 0.f, v = 0.f;
+          float x = 0.f;               // half 0: of logits; half 1: of weights
           if (drafted) {
-            k = kNewDot;
-            v = kNewP;
+            x = half ? kNewP : kNewDot * a.scale_log2;
           } else if (row < valid) {
             const int64_t at = bh * a.cap + key0 + row;
-            if (in_bounds(at < (int64_t)a.batch * a.heads * a.cap, a.dev_status)) {
-              k = __ldg(a.k_step + at) * kQ8Dot;
-              v = __ldg(a.v_step + at) * kQ8P;
-            }
+            if (in_bounds(at < (int64_t)a.batch * a.heads * a.cap, a.dev_status))
+              x = half ? __ldg(a.v_step + at) * kQ8P : __ldg(a.k_step + at) * kQ8Dot * a.scale_log2;
           }
-          fk[row] = k * a.scale_log2;
-          fk[kTile + row] = v;
-          ptx::named_barrier(1 + slot, 128);
+          fk[half * kTile + row] = x;
+          ptx::named_barrier(1 + slot, kSlotThreads);
         }
         wait(&bars.s_full[slot], steps);
         ptx::tc_fence_after();
-        uint32_t bad[4] = {0u, 0u, 0u, 0u};
         if (edge && (!Q8 || drafted)) {
           // V's rows that nobody sees become zeros, as do drafted ones with an infinity or NaN, which the rows that see
           // them get as a NaN weight: 0 times it must not reach the others. A thread looks after a key. (S is there, so the slot's
           // last P V is done, and the stage's phase before V's has passed.)
-          if (!TWO || slot == 0) {
+          if (half == 1 && (!TWO || slot == 0)) {
             const uint32_t at = 2 * (TWO ? done + f : steps) + 1, stage = S::stage(slot, at);   // V's place in the ring
             wait(&bars.kv_full[stage], at / S::kTurn);
             uint8_t* const v = smem + S::kRing + stage * S::kStage;
@@ -516,7 +547,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
                   for (uint32_t x : {w.x, w.y, w.z, w.w}) inf |= (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
                 }
               const uint32_t votes = __ballot_sync(0xffffffffu, inf);
-              if (lane == 0) bad_keys[slot][quarter] = votes;
+              if (lane == 0) small.bad_keys[slot][quarter] = votes;
               fix |= inf;
             }
             if (fix)
@@ -524,35 +555,62 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
           const bool both = TWO && rows_of(seg) > kTile;
-          if (drafted || both) ptx::named_barrier(both ? 3 : 1 + slot, both ? 256 : 128);   // (the other slot's products read V, too)
+          if (drafted || both) ptx::named_barrier(both ? 3 : 1 + slot, both ? 2 * kSlotThreads : kSlotThreads);   // (the other slot's products read V, too)
           if (drafted) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) bad[w] = bad_keys[TWO ? 0 : slot][w] & see[w];
-            ptx::named_barrier(both ? 3 : 1 + slot, both ? 256 : 128);   // (before the next tile's are written)
+            for (int w = 0; w < 2; ++w) bad[w] = small.bad_keys[TWO ? 0 : slot][2 * half + w] & see[w];
+            ptx::named_barrier(both ? 3 : 1 + slot, both ? 2 * kSlotThreads : kSlotThreads);   // (before the next tile's are written)
           }
         }
-        // Logits of chunk c (32 keys) as they are compared: 8-bit keys' steps are in.
-        auto scaled = [&](uint32_t (&x)[32], int c) {
-          if constexpr (Q8) {
+        if (mine) {
+          // Logits of chunk w (32 keys) as they are compared: 8-bit keys' steps are in.
+          auto load = [&](uint32_t (&x)[32], int w) {
+            const int k0 = 64 * half + 32 * w;
+            tmem_ld32(s_at + k0, x);
+            ptx::tmem_wait_ld();
+            if constexpr (Q8) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 k = *reinterpret_cast<const float4*>(fk + 32 * c + e);
-              const float2 y = mul2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), make_float2(k.x, k.y));
-              const float2 z = mul2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), make_float2(k.z, k.w));
-              x[e] = __float_as_uint(y.x), x[e + 1] = __float_as_uint(y.y), x[e + 2] = __float_as_uint(z.x), x[e + 3] = __float_as_uint(z.y);
+              for (int e = 0; e < 32; e += 4) {
+                const float4 k = *reinterpret_cast<const float4*>(fk + k0 + e);
+                const float2 y = mul2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), make_float2(k.x, k.y));
+                const float2 z = mul2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), make_float2(k.z, k.w));
+                x[e] = __float_as_uint(y.x), x[e + 1] = __float_as_uint(y.y), x[e + 2] = __float_as_uint(z.x), x[e + 3] = __float_as_uint(z.y);
+              }
+            }
+          };
+          // ---- the row's maximum
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int w = 0; w < 2; ++w) {
+            uint32_t x[32];
+            load(x, w);
+            const uint32_t keep = w ? see[1] : see[0];
+            if (__all_sync(0xffffffffu, keep == ~0u)) {
+              float other = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                top = fmaxf(fmaxf(top, __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
+                other = fmaxf(fmaxf(other, __uint_as_float(x[e + 2])), __uint_as_float(x[e + 3]));
+              }
+              top = fmaxf(top, other);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (keep >> e & 1) top = fmaxf(top, __uint_as_float(x[e]));
             }
           }
-        };
-        auto raise = [&](float top) {   // the row's maximum, and what stands under it
+          swap[half * kTile + row] = top;
+          ptx::named_barrier(pair, 64);
+          top = fmaxf(top, swap[(half ^ 1) * kTile + row]);
           if constexpr (!Q8) top *= a.scale_log2;
           if (first) {
             m = fmaxf(m, top);
-          } else if (__any_sync(0xffffffffu, top > m + kSlack)) {
+          } else if (__any_sync(0xffffffffu, top > m + kSlack)) {   // (the same for both threads of a row)
             const float next = top > m + kSlack ? top : m, fall = rescale(m, next);
             m = next;
             l *= fall;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
+            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
               uint32_t x[32];
               tmem_ld32(o_lane + S::kO(slot) + c, x);
               ptx::tmem_wait_ld();
@@ -560,107 +618,58 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
               for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * fall);
               tmem_st32(o_lane + S::kO(slot) + c, x);
             }
-            ptx::tmem_wait_st();
           }
-        };
-        // Weights of chunk c from its (scaled) logits; `keep` and `nan` are this row's bits of its keys.
-        float2 sum = make_float2(0.f, 0.f);
-        auto weigh = [&](const uint32_t (&x)[32], int c, auto masked, uint32_t keep, uint32_t nan) {
+          // ---- weights
           const float2 down = make_float2(-m, -m), by = make_float2(a.scale_log2, a.scale_log2);
-          uint32_t p[32];   // first parts, then second parts
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+          for (int w = 0; w < 2; ++w) {
+            uint32_t x[32];
+            load(x, w);
+            const int k0 = 64 * half + 32 * w;
+            const uint32_t keep = w ? see[1] : see[0], nan = w ? bad[1] : bad[0];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float2 y = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-            y = Q8 ? add2(y, down) : fma2(y, by, down);
-            y = make_float2(ex2(y.x), ex2(y.y));
-            if constexpr (decltype(masked)::value) {
-              if (!(keep >> e & 1)) y.x = 0.f;
-              if (!(keep >> (e + 1) & 1)) y.y = 0.f;
-              if (nan >> e & 1) y.x = __uint_as_float(0x7FC00000u);
-              if (nan >> (e + 1) & 1) y.y = __uint_as_float(0x7FC00000u);
+            for (int e = 0; e < 32; e += 2) {
+              float2 y = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+              y = Q8 ? add2(y, down) : fma2(y, by, down);
+              x[e] = __float_as_uint(ex2(y.x)), x[e + 1] = __float_as_uint(ex2(y.y));
             }
-            sum = add2(sum, y);
-            if constexpr (Q8) y = mul2(y, *reinterpret_cast<const float2*>(fk + kTile + 32 * c + e));
-            const uint32_t w = pack2(y.x, y.y);
-            p[e / 2] = w;
-            p[16 + e / 2] = pack2(y.x - __uint_as_float(w << 16), y.y - __uint_as_float(w & 0xFFFF0000u));
-          }
-          tmem_st32(s_at + 32 * c, p);
-        };
-        auto highest = [](const uint32_t (&x)[32], float top) {
-          float other = -INFINITY;
+            if (!__all_sync(0xffffffffu, keep == ~0u)) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            top = fmaxf(fmaxf(top, __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
-            other = fmaxf(fmaxf(other, __uint_as_float(x[e + 2])), __uint_as_float(x[e + 3]));
-          }
-          return fmaxf(top, other);
-        };
-        if (mine && !edge) {
-          // Chunks 0 to 3 for the maximum; weights from 2 and 3, which are still there, then from 0 and 1 once more.
-          uint32_t x[32], y[32];
-          float top = -INFINITY;
-          tmem_ld32(s_at, x);
-          ptx::tmem_wait_ld();
-          tmem_ld32(s_at + 32, y);
-          scaled(x, 0);
-          top = highest(x, top);
-          ptx::tmem_wait_ld();
-          tmem_ld32(s_at + 64, x);
-          scaled(y, 1);
-          top = highest(y, top);
-          ptx::tmem_wait_ld();
-          tmem_ld32(s_at + 96, y);
-          scaled(x, 2);
-          top = highest(x, top);
-          ptx::tmem_wait_ld();
-          scaled(y, 3);
-          raise(highest(y, top));
-          weigh(x, 2, std::false_type(), 0u, 0u);
-          tmem_ld32(s_at, x);
-          weigh(y, 3, std::false_type(), 0u, 0u);
-          ptx::tmem_wait_ld();
-          tmem_ld32(s_at + 32, y);
-          scaled(x, 0);
-          weigh(x, 0, std::false_type(), 0u, 0u);
-          ptx::tmem_wait_ld();
-          scaled(y, 1);
-          weigh(y, 1, std::false_type(), 0u, 0u);
-        } else if (mine) {
-          auto word = [](const uint32_t (&w)[4], int c) { return c == 0 ? w[0] : c == 1 ? w[1] : c == 2 ? w[2] : w[3]; };
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[32];
-            tmem_ld32(s_at + 32 * c, x);
-            ptx::tmem_wait_ld();
-            scaled(x, c);
-            const uint32_t keep = word(see, c);
+              for (int e = 0; e < 32; ++e) {
+                if (!(keep >> e & 1)) x[e] = 0u;
+                if (nan >> e & 1) x[e] = 0x7FC00000u;
+              }
+            }
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (keep >> e & 1) top = fmaxf(top, __uint_as_float(x[e]));
+            for (int e = 0; e < 32; e += 16) {   // first and second parts of sixteen keys
+              uint32_t p[8], q[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float2 y = make_float2(__uint_as_float(x[e + 2 * i]), __uint_as_float(x[e + 2 * i + 1]));
+                sum = add2(sum, y);
+                if constexpr (Q8) y = mul2(y, *reinterpret_cast<const float2*>(fk + kTile + k0 + e + 2 * i));
+                p[i] = pack2(y.x, y.y);
+                y = add2(y, make_float2(-__uint_as_float(p[i] << 16), -__uint_as_float(p[i] & 0xFFFF0000u)));
+                q[i] = pack2(y.x, y.y);
+              }
+              tmem_st8(s_at + k0 + e / 2, p);
+              tmem_st8(s_at + k0 + 16 + e / 2, q);
+            }
           }
-          raise(top);
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[32];
-            tmem_ld32(s_at + 32 * c, x);
-            ptx::tmem_wait_ld();
-            scaled(x, c);
-            weigh(x, c, std::true_type(), word(see, c), word(bad, c));
-          }
+          l += sum.x + sum.y;
+          ptx::tmem_wait_st();
         }
-        l += sum.x + sum.y;
-        if (mine) ptx::tmem_wait_st();
+        first = false;
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars.p_ready[slot]);
-        first = false;
         ++steps;
       }
 
-      // ---- the head's end in this share
+      // ---- the head's end in this share: the halves' sums meet, and up to 128 rows the slots' m, sums and O
       const bool whole = seg.whole();
+      if (half == 1) swap[row] = l;    // (the other half has read what stood there: its own l is from after the last swap)
       wait(&bars.o_full, seg.index);
       ptx::tc_fence_after();
       float* const part = part_at<D>(a, (int)blockIdx.x, seg.at > share.at ? 1 : 0);
@@ -677,77 +686,89 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
         }
         return (Q8 ? kQ8Out : 1.0f) * (!whole ? 1.0f : sum == 0.f ? 0.f : 1.0f / sum);
       };
-      auto write = [&](int c, const float (&x)[32]) {   // channels c .. c + 31 of this thread's row
+      auto write = [&](int c, const uint32_t (&x)[16]) {   // channels c .. c + 15 of this thread's row
         if (row >= rows) return;
         if (whole) {
           uint4* const u = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + to * D + c);
+          uint32_t w[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            u[e] = make_uint4(pack2(x[8 * e], x[8 * e + 1]), pack2(x[8 * e + 2], x[8 * e + 3]), pack2(x[8 * e + 4], x[8 * e + 5]), pack2(x[8 * e + 6], x[8 * e + 7]));
+          for (int e = 0; e < 8; ++e) w[e] = pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+          u[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          u[1] = make_uint4(w[4], w[5], w[6], w[7]);
         } else {
           float* const u = part + c * S::kRows + pr;   // (a warp's rows lie side by side)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) u[e * S::kRows] = x[e];
+          for (int e = 0; e < 16; ++e) u[e * S::kRows] = __uint_as_float(x[e]);
         }
       };
+      ptx::named_barrier(pair, 64);
       if constexpr (TWO) {
+        if (half == 0) {
+          const float scale = finish(m, l + swap[row]);
+          swap[kTile + row] = scale;
+        }
+        ptx::named_barrier(pair, 64);
         if (mine) {
-          const float scale = finish(m, l);
-#pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t x[32];
-            float y[32];
-            tmem_ld32(o_lane + S::kO(slot) + c, x);
+          const float scale = swap[kTile + row];
+#pragma unroll 1
+          for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+            uint32_t x[16];
+            tmem_ld16(o_lane + S::kO(slot) + c, x);
             ptx::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(x[e]) * scale;
-            write(c, y);
+            for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * scale);
+            write(c, x);
           }
         }
       } else {
-        // the two slots' halves of the keys meet; each slot writes half of the channels
+        // each slot and half writes a quarter of the channels
         const bool other = seg.tiles > 1;   // (of one tile, one slot has none)
         const int only = (int)(done & 1);   // the first tile's slot
-        if (slot == 1) meet[row] = make_float2(m, l);
-        ptx::named_barrier(3, 256);
-        float2 f;
-        if (slot == 0) {
-          const float2 y = meet[row];
-          const float top = fmaxf(m, y.x), f0 = rescale(m, top), f1 = rescale(y.x, top);
-          const float scale = finish(top, fmaf(l, f0, y.y * f1));
-          f = make_float2(f0 * scale, f1 * scale);
-          meet[row] = f;
+        float* const factor = reinterpret_cast<float*>(smem + S::kSwap);   // slot 0's: the two factors of a row, in the end
+        if (half == 0) {
+          l += swap[row];
+          if (slot == 1) {
+            swap[row] = l;
+            swap[kTile + row] = m;
+          }
         }
-        ptx::named_barrier(3, 256);
-        if (slot == 1) f = meet[row];
+        ptx::named_barrier(3, 2 * kSlotThreads);
+        if (half == 0 && slot == 0) {
+          const float l1 = swap[2 * kTile + row], m1 = swap[3 * kTile + row];   // slot 1's
+          const float top = fmaxf(m, m1), f0 = rescale(m, top), f1 = rescale(m1, top);
+          const float scale = finish(top, fmaf(l, f0, l1 * f1));
+          factor[row] = f0 * scale;
+          factor[kTile + row] = f1 * scale;
+        }
+        ptx::named_barrier(3, 2 * kSlotThreads);
         if (mine) {
-#pragma unroll
-          for (int c = slot * (D / 2); c < (slot + 1) * (D / 2); c += 32) {
-            uint32_t x[32];
-            float y[32];
-            tmem_ld32(o_lane + S::kO(other ? 0 : only) + c, x);
+          const float f0 = factor[row], f1 = factor[kTile + row];
+          const float fx = other || only == 0 ? f0 : f1;
+          constexpr int kMine = D / 4;
+#pragma unroll 1
+          for (int c = (2 * slot + half) * kMine; c < (2 * slot + half + 1) * kMine; c += 16) {
+            uint32_t x[16], y[16];
+            tmem_ld16(o_lane + S::kO(other ? 0 : only) + c, x);
+            if (other) tmem_ld16(o_lane + S::kO(1) + c, y);
             ptx::tmem_wait_ld();
-            const float fx = other || only == 0 ? f.x : f.y;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(x[e]) * fx;
-            if (other) {
-              tmem_ld32(o_lane + S::kO(1) + c, x);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) y[e] = fmaf(__uint_as_float(x[e]), f.y, y[e]);
+            for (int e = 0; e < 16; ++e) {
+              const float z = __uint_as_float(x[e]) * fx;
+              x[e] = __float_as_uint(other ? fmaf(__uint_as_float(y[e]), f1, z) : z);
             }
-            write(c, y);
+            write(c, x);
           }
         }
       }
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&bars.o_free);
+      ptx::named_barrier(3, 2 * kSlotThreads);   // (the swap area is free)
       done += (uint32_t)seg.tiles;
     } while (seg.next(a));
   } else if constexpr (Q8) {
     // ---- codes into bf16 tiles: a thread per key
-    const int key = tid - 12 * 32;
+    const int key = tid - 32 * (4 + S::kSoft);
     Segments ks(a, share), vs(a, share);
     int kf = 0, vf = 0;
     uint32_t used = 0;                 // raw tiles

@@ -97,20 +97,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
         "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(at));
 }
-__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
-               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
-      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
-      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
-      "r"(r[31])
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+      "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+      "r"(r[14]), "r"(r[15])
       : "memory");
+}
+// Whether x is true in any thread of the two warps that meet at a named barrier.
+__device__ __forceinline__ bool any_of_pair(int barrier, bool x) {
+  uint32_t any;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(any) : "r"((uint32_t)x), "r"(barrier) : "memory");
+  return any != 0;
 }
 
 // The MMA warp runs as a whole, so that descriptors stay in uniform registers (computed by one thread, each product took 90
@@ -321,10 +319,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
       const uint32_t v_lo = uniform(v_desc(ring + S::stage(slot, at) * S::kStage));
 #pragma unroll
       for (int s = 0; s < kTile / 16; ++s)
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-          mma_ts(leader, o_at, s_at + (s / 2) * 32 + part * 16 + (s % 2) * 8, v_lo + s * (2048 >> 4), kDescHigh, kIdescPv,
-                 !(fresh && s == 0 && part == 0));
+        mma_ts(leader, o_at, s_at + (s / 2) * 32 + (s % 2) * 8, v_lo + s * (2048 >> 4), kDescHigh, kIdescPv, !(fresh && s == 0));
     };
     // Walks of the Q K^T and of the P V, the first a tile of the slot's ahead. A slot waits for every segment's queries and outputs
     // and counts in on q_empty and o_full at its end, whether it had tiles of it or not: barriers know a phase by its parity
@@ -563,101 +558,105 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           }
         }
         if (mine) {
-          // Logits of chunk w (32 keys) as they are compared: 8-bit keys' steps are in.
-          auto load = [&](uint32_t (&x)[32], int w) {
+          const float2 by = make_float2(a.scale_log2, a.scale_log2);
+          // Logits of chunk w (32 keys) less `low`, in the log2 domain; keys that the row does not see are -inf.
+          auto load = [&](float2 (&y)[16], int w, float low) {
             const int k0 = 64 * half + 32 * w;
+            uint32_t x[32];
             tmem_ld32(s_at + k0, x);
             ptx::tmem_wait_ld();
-            if constexpr (Q8) {
+            const float2 down = make_float2(-low, -low);
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 k = *reinterpret_cast<const float4*>(fk + k0 + e);
-                const float2 y = mul2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), make_float2(k.x, k.y));
-                const float2 z = mul2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), make_float2(k.z, k.w));
-                x[e] = __float_as_uint(y.x), x[e + 1] = __float_as_uint(y.y), x[e + 2] = __float_as_uint(z.x), x[e + 3] = __float_as_uint(z.y);
+            for (int e = 0; e < 16; ++e)
+              y[e] = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), Q8 ? *reinterpret_cast<const float2*>(fk + k0 + 2 * e) : by, down);
+            const uint32_t keep = w ? see[1] : see[0];
+            if (!__all_sync(0xffffffffu, keep == ~0u)) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                if (!(keep >> (2 * e) & 1)) y[e].x = -INFINITY;
+                if (!(keep >> (2 * e + 1) & 1)) y[e].y = -INFINITY;
               }
             }
           };
-          // ---- the row's maximum
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int w = 0; w < 2; ++w) {
-            uint32_t x[32];
-            load(x, w);
-            const uint32_t keep = w ? see[1] : see[0];
-            if (__all_sync(0xffffffffu, keep == ~0u)) {
-              float other = -INFINITY;
+          auto highest = [](const float2 (&y)[16], float top) {
+            float other = -INFINITY;
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                top = fmaxf(fmaxf(top, __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
-                other = fmaxf(fmaxf(other, __uint_as_float(x[e + 2])), __uint_as_float(x[e + 3]));
+            for (int e = 0; e < 16; e += 2) {
+              top = fmaxf(fmaxf(top, y[e].x), y[e].y);
+              other = fmaxf(fmaxf(other, y[e + 1].x), y[e + 1].y);
+            }
+            return fmaxf(top, other);
+          };
+          // Weights of chunk w, rounded to bf16, and their sum's share.
+          auto weigh = [&](float2 (&y)[16], int w, uint32_t (&p)[16]) {
+            const uint32_t nan = w ? bad[1] : bad[0];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
+            if (drafted && nan) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                if (nan >> (2 * e) & 1) y[e].x = __uint_as_float(0x7FC00000u);
+                if (nan >> (2 * e + 1) & 1) y[e].y = __uint_as_float(0x7FC00000u);
               }
-              top = fmaxf(top, other);
-            } else {
+            }
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (keep >> e & 1) top = fmaxf(top, __uint_as_float(x[e]));
+            for (int e = 0; e < 16; ++e) {
+              sum = add2(sum, y[e]);
+              if constexpr (Q8) y[e] = mul2(y[e], *reinterpret_cast<const float2*>(fk + kTile + 64 * half + 32 * w + 2 * e));
+              p[e] = pack2(y[e].x, y[e].y);
+            }
+            return sum.x + sum.y;
+          };
+          // With the maximum as it is: weights stay in registers until both threads of a row know that none is too large.
+          uint32_t p[2][16];
+          float top = -INFINITY, sum = 0.f;
+          if (!first) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              float2 y[16];
+              load(y, w, m);
+              top = highest(y, top);
+              sum += weigh(y, w, p[w]);
             }
           }
-          swap[half * kTile + row] = top;
-          ptx::named_barrier(pair, 64);
-          top = fmaxf(top, swap[(half ^ 1) * kTile + row]);
-          if constexpr (!Q8) top *= a.scale_log2;
-          if (first) {
-            m = fmaxf(m, top);
-          } else if (__any_sync(0xffffffffu, top > m + kSlack)) {   // (the same for both threads of a row)
-            const float next = top > m + kSlack ? top : m, fall = rescale(m, next);
+          if (any_of_pair(pair, first || top > kSlack)) {
+            // ---- the row's maximum, and what stands under the old one
+            top = -INFINITY;
+#pragma unroll 1
+            for (int w = 0; w < 2; ++w) {
+              float2 y[16];
+              load(y, w, 0.f);
+              top = highest(y, top);
+            }
+            swap[half * kTile + row] = top;
+            ptx::named_barrier(pair, 64);
+            top = fmaxf(top, swap[(half ^ 1) * kTile + row]);
+            const float next = first ? fmaxf(m, top) : top > m + kSlack ? top : m, fall = rescale(m, next);
             m = next;
-            l *= fall;
+            if (!first) {
+              l *= fall;
 #pragma unroll 1
-            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
-              uint32_t x[32];
-              tmem_ld32(o_lane + S::kO(slot) + c, x);
-              ptx::tmem_wait_ld();
+              for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+                uint32_t x[16];
+                tmem_ld16(o_lane + S::kO(slot) + c, x);
+                ptx::tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * fall);
-              tmem_st32(o_lane + S::kO(slot) + c, x);
-            }
-          }
-          // ---- weights
-          const float2 down = make_float2(-m, -m), by = make_float2(a.scale_log2, a.scale_log2);
-          float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 1
-          for (int w = 0; w < 2; ++w) {
-            uint32_t x[32];
-            load(x, w);
-            const int k0 = 64 * half + 32 * w;
-            const uint32_t keep = w ? see[1] : see[0], nan = w ? bad[1] : bad[0];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float2 y = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-              y = Q8 ? add2(y, down) : fma2(y, by, down);
-              x[e] = __float_as_uint(ex2(y.x)), x[e + 1] = __float_as_uint(ex2(y.y));
-            }
-            if (!__all_sync(0xffffffffu, keep == ~0u)) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                if (!(keep >> e & 1)) x[e] = 0u;
-                if (nan >> e & 1) x[e] = 0x7FC00000u;
+                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * fall);
+                tmem_st16(o_lane + S::kO(slot) + c, x);
               }
             }
+            sum = 0.f;
 #pragma unroll
-            for (int e = 0; e < 32; e += 16) {   // first and second parts of sixteen keys
-              uint32_t p[8], q[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                float2 y = make_float2(__uint_as_float(x[e + 2 * i]), __uint_as_float(x[e + 2 * i + 1]));
-                sum = add2(sum, y);
-                if constexpr (Q8) y = mul2(y, *reinterpret_cast<const float2*>(fk + kTile + k0 + e + 2 * i));
-                p[i] = pack2(y.x, y.y);
-                y = add2(y, make_float2(-__uint_as_float(p[i] << 16), -__uint_as_float(p[i] & 0xFFFF0000u)));
-                q[i] = pack2(y.x, y.y);
-              }
-              tmem_st8(s_at + k0 + e / 2, p);
-              tmem_st8(s_at + k0 + 16 + e / 2, q);
+            for (int w = 0; w < 2; ++w) {
+              float2 y[16];
+              load(y, w, m);
+              sum += weigh(y, w, p[w]);
             }
           }
-          l += sum.x + sum.y;
+          l += sum;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) tmem_st16(s_at + 64 * half + 32 * w, p[w]);
           ptx::tmem_wait_st();
         }
         first = false;
@@ -783,23 +782,27 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
         wait(&bars.raw_full[at], used / kRaws);
         const uint8_t* const from = smem + S::kRawRing + at * S::kRaw;
         const bool there = key < s.p.s.rows - tile * kTile;
-        uint4 w[D / 16];
+        if (turn > 0) wait(&bars.kv_empty[slot], turn - 1);
+        auto low = [](uint32_t x) { return prmt(x, x, 0x1100) & 0x807F807Fu; };
+        auto high = [](uint32_t x) { return prmt(x, x, 0x3322) & 0x807F807Fu; };
+#pragma unroll 1
+        for (int c0 = 0; c0 < D / 16; c0 += 4) {
+          uint4 w[4];
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const uint32_t off = D == 128 ? key * 128 + ((c ^ (key & 7)) << 4) : key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
-          w[c] = there ? *reinterpret_cast<const uint4*>(from + off) : make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < 4; ++i) {
+            const int c = c0 + i;
+            const uint32_t off = D == 128 ? key * 128 + ((c ^ (key & 7)) << 4) : key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
+            w[i] = there ? *reinterpret_cast<const uint4*>(from + off) : make_uint4(0u, 0u, 0u, 0u);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            *reinterpret_cast<uint4*>(to + piece_at(key, 2 * (c0 + i))) = make_uint4(low(w[i].x), high(w[i].x), low(w[i].y), high(w[i].y));
+            *reinterpret_cast<uint4*>(to + piece_at(key, 2 * (c0 + i) + 1)) = make_uint4(low(w[i].z), high(w[i].z), low(w[i].w), high(w[i].w));
+          }
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars.raw_empty[at]);
         ++used;
-        if (turn > 0) wait(&bars.kv_empty[slot], turn - 1);
-        auto low = [](uint32_t x) { return prmt(x, x, 0x1100) & 0x807F807Fu; };
-        auto high = [](uint32_t x) { return prmt(x, x, 0x3322) & 0x807F807Fu; };
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          *reinterpret_cast<uint4*>(to + piece_at(key, 2 * c)) = make_uint4(low(w[c].x), high(w[c].x), low(w[c].y), high(w[c].y));
-          *reinterpret_cast<uint4*>(to + piece_at(key, 2 * c + 1)) = make_uint4(low(w[c].z), high(w[c].z), low(w[c].w), high(w[c].w));
-        }
       } else {
         const int row = (tile - s.p.s.cache_tiles) * kTile + key;
         const bool there = row < s.p.s.n;

@@ -43,9 +43,13 @@ def check_tree(q, k, v, lens, out, lse=None, *, k_new=None, v_new=None, mask=Non
             for i in range(h * G, (h + 1) * G):
                 new = (None, None) if kn is None else (kn[b, h, :m], vn[b, h, :m])
                 ref, want, size, pv = do.attend(qh[b, i, :m], k[b, h, :n], v[b, h, :n], *new, sees)
+                # bf16 calls of more than sixteen rows a KV head round every weight to bf16, by half a step (a value
+                # 1.f x 2^e has steps of 2^(e - 7): at most 2^-8 of it), and sum the weights up as they were: the output moves by
+                # 2^-8 sum p |v| at most
+                coarse = 2.0 ** -8 if out.dtype == torch.bfloat16 and G * T > 16 else 0.0
                 for t in range(m):
                     at = f"{where} b{b} h{h} i{i} t{t} n{n}"
-                    tol = out_tolerance(ref[t], pv[t], d, n + m, size[t], out.dtype)
+                    tol = out_tolerance(ref[t], pv[t], d, n + m, size[t], out.dtype) + coarse * pv[t] * (1 + 2.0 ** -8)
                     err = np.abs(o[b, i, t] - ref[t])
                     assert np.all(err <= tol), f"{at}: {err.max():.3g} of {tol[err.argmax()]:.3g}"
                     if ls is None:

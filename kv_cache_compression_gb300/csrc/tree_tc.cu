@@ -80,22 +80,27 @@ template <bool Q8, int D, bool TWO> struct Shape {
   static constexpr int kColumns = 512;
 };
 
-__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
-      "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(at));
-}
 __device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
         "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(at));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+      "r"(r[31])
+      : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
@@ -319,7 +324,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
       const uint32_t v_lo = uniform(v_desc(ring + S::stage(slot, at) * S::kStage));
 #pragma unroll
       for (int s = 0; s < kTile / 16; ++s)
-        mma_ts(leader, o_at, s_at + (s / 2) * 32 + (s % 2) * 8, v_lo + s * (2048 >> 4), kDescHigh, kIdescPv, !(fresh && s == 0));
+        mma_ts(leader, o_at, s_at + (s / 4) * 64 + (s % 4) * 8, v_lo + s * (2048 >> 4), kDescHigh, kIdescPv, !(fresh && s == 0));
     };
     // Walks of the Q K^T and of the P V, the first a tile of the slot's ahead. A slot waits for every segment's queries and outputs
     // and counts in on q_empty and o_full at its end, whether it had tiles of it or not: barriers know a phase by its parity
@@ -461,8 +466,6 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
       const int r0 = r0_of(seg) + (TWO ? slot * kTile : 0), n = seg.p.s.n;
       const int rows = min(kTile, rows_of(seg) - (TWO ? slot * kTile : 0));   // this slot's (none or less: it rests)
       const bool mine = quarter * 32 < rows;                                  // this warp has rows
-      const int64_t bh = (int64_t)seg.p.seq * a.heads + seg.p.head;
-      const int r = r0 + row, g = r / n, token = r - g * n;
       float m = kNoMax, l = 0.f;       // l: of this thread's keys
       bool first = true;
       for (int f = TWO ? 0 : (int)((done ^ slot) & 1); rows > 0 && f < seg.tiles; f += TWO ? 1 : 2) {
@@ -474,6 +477,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
         // This row's bits of the thread's 64 keys: those that it sees, and (below) those that make it NaN.
         uint32_t see[2] = {~0u, ~0u}, bad[2] = {0u, 0u};
         if (edge) {
+          const int token = (r0 + row) % n;
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             const int k0 = 64 * half + 32 * w;
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           if (drafted) {
             x = half ? kNewP : kNewDot * a.scale_log2;
           } else if (row < valid) {
-            const int64_t at = bh * a.cap + key0 + row;
+            const int64_t at = ((int64_t)seg.p.seq * a.heads + seg.p.head) * a.cap + key0 + row;
             if (in_bounds(at < (int64_t)a.batch * a.heads * a.cap, a.dev_status))
               x = half ? __ldg(a.v_step + at) * kQ8P : __ldg(a.k_step + at) * kQ8Dot * a.scale_log2;
           }
@@ -559,82 +563,82 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
         }
         if (mine) {
           const float2 by = make_float2(a.scale_log2, a.scale_log2);
-          // Logits of chunk w (32 keys) less `low`, in the log2 domain; keys that the row does not see are -inf.
-          auto load = [&](float2 (&y)[16], int w, float low) {
-            const int k0 = 64 * half + 32 * w;
-            uint32_t x[32];
-            tmem_ld32(s_at + k0, x);
+          // Logits of chunk c (sixteen keys) less `low`, in the log2 domain.
+          auto load = [&](float2 (&y)[8], int c, float low) {
+            const int k0 = 64 * half + 16 * c;
+            uint32_t x[16];
+            tmem_ld16(s_at + k0, x);
             ptx::tmem_wait_ld();
             const float2 down = make_float2(-low, -low);
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
+            for (int e = 0; e < 8; ++e)
               y[e] = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), Q8 ? *reinterpret_cast<const float2*>(fk + k0 + 2 * e) : by, down);
-            const uint32_t keep = w ? see[1] : see[0];
-            if (!__all_sync(0xffffffffu, keep == ~0u)) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                if (!(keep >> (2 * e) & 1)) y[e].x = -INFINITY;
-                if (!(keep >> (2 * e + 1) & 1)) y[e].y = -INFINITY;
-              }
-            }
           };
-          auto highest = [](const float2 (&y)[16], float top) {
+          auto highest = [](const float2 (&y)[8], float top) {
             float other = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
+            for (int e = 0; e < 8; e += 2) {
               top = fmaxf(fmaxf(top, y[e].x), y[e].y);
               other = fmaxf(fmaxf(other, y[e + 1].x), y[e + 1].y);
             }
             return fmaxf(top, other);
           };
-          // Weights of chunk w, rounded to bf16, and their sum's share.
-          auto weigh = [&](float2 (&y)[16], int w, uint32_t (&p)[16]) {
-            const uint32_t nan = w ? bad[1] : bad[0];
+          // Weights of chunk c, rounded to bf16; they are summed up as they were.
+          float2 sum = make_float2(0.f, 0.f);
+          auto pack = [&](float2 (&y)[8], int c, uint32_t* p) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
-            if (drafted && nan) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                if (nan >> (2 * e) & 1) y[e].x = __uint_as_float(0x7FC00000u);
-                if (nan >> (2 * e + 1) & 1) y[e].y = __uint_as_float(0x7FC00000u);
-              }
-            }
-            float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < 8; ++e) {
               sum = add2(sum, y[e]);
-              if constexpr (Q8) y[e] = mul2(y[e], *reinterpret_cast<const float2*>(fk + kTile + 64 * half + 32 * w + 2 * e));
+              if constexpr (Q8) y[e] = mul2(y[e], *reinterpret_cast<const float2*>(fk + kTile + 64 * half + 16 * c + 2 * e));
               p[e] = pack2(y[e].x, y[e].y);
             }
-            return sum.x + sum.y;
           };
-          // With the maximum as it is: weights stay in registers until both threads of a row know that none is too large.
-          uint32_t p[2][16];
-          float top = -INFINITY, sum = 0.f;
-          if (!first) {
+          // Most tiles: the maximum as it is, and the weights in registers until both threads of a row know that none is too large.
+          // (Straight code, and little of it: sixteen warps out of step fetch it, and what all of the tile's cases take together
+          // in one piece cost 2800 clocks a tile, most of them without an instruction.)
+          bool left = true;
+          if (!first && !edge) {
+            uint32_t p[32];
+            float top = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              float2 y[16];
-              load(y, w, m);
+            for (int c = 0; c < 4; ++c) {
+              float2 y[8];
+              load(y, c, m);
               top = highest(y, top);
-              sum += weigh(y, w, p[w]);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
+              pack(y, c, p + 8 * c);
             }
+            left = any_of_pair(pair, top > kSlack);
+            if (!left) tmem_st32(s_at + 64 * half, p);
           }
-          if (any_of_pair(pair, first || top > kSlack)) {
-            // ---- the row's maximum, and what stands under the old one
-            top = -INFINITY;
+          if (left) {
+            // ---- a head's first tile, its last ones, and where the maximum grows: chunk by chunk
+            auto mask = [&](float2 (&y)[8], int c, bool nan) {
+              if (!edge) return;
+              const uint32_t keep = (c < 2 ? see[0] : see[1]) >> (16 * (c % 2)), not_a = (c < 2 ? bad[0] : bad[1]) >> (16 * (c % 2));
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                if (!(keep >> (2 * e) & 1)) y[e].x = -INFINITY;
+                if (!(keep >> (2 * e + 1) & 1)) y[e].y = -INFINITY;
+                if (nan && (not_a >> (2 * e) & 1)) y[e].x = __uint_as_float(0x7FC00000u);
+                if (nan && (not_a >> (2 * e + 1) & 1)) y[e].y = __uint_as_float(0x7FC00000u);
+              }
+            };
+            float top = -INFINITY;
 #pragma unroll 1
-            for (int w = 0; w < 2; ++w) {
-              float2 y[16];
-              load(y, w, 0.f);
+            for (int c = 0; c < 4; ++c) {
+              float2 y[8];
+              load(y, c, 0.f);
+              mask(y, c, false);
               top = highest(y, top);
             }
             swap[half * kTile + row] = top;
             ptx::named_barrier(pair, 64);
             top = fmaxf(top, swap[(half ^ 1) * kTile + row]);
-            const float next = first ? fmaxf(m, top) : top > m + kSlack ? top : m, fall = rescale(m, next);
-            m = next;
-            if (!first) {
+            const float next = first ? fmaxf(m, top) : top > m + kSlack ? top : m;
+            if (!first && __any_sync(0xffffffffu, next != m)) {   // (the same for both threads of a row)
+              const float fall = rescale(m, next);
               l *= fall;
 #pragma unroll 1
               for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
@@ -646,17 +650,21 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
                 tmem_st16(o_lane + S::kO(slot) + c, x);
               }
             }
-            sum = 0.f;
+            m = next;
+            sum = make_float2(0.f, 0.f);
+            uint32_t p[8];
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {   // (a chunk's weights stand where logits of the first chunks stood)
+              float2 y[8];
+              load(y, c, m);
+              mask(y, c, true);
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              float2 y[16];
-              load(y, w, m);
-              sum += weigh(y, w, p[w]);
+              for (int e = 0; e < 8; ++e) y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
+              pack(y, c, p);
+              tmem_st8(s_at + 64 * half + 8 * c, p);
             }
           }
-          l += sum;
-#pragma unroll
-          for (int w = 0; w < 2; ++w) tmem_st16(s_at + 64 * half + 32 * w, p[w]);
+          l += sum.x + sum.y;
           ptx::tmem_wait_st();
         }
         first = false;
@@ -673,7 +681,8 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
       ptx::tc_fence_after();
       float* const part = part_at<D>(a, (int)blockIdx.x, seg.at > share.at ? 1 : 0);
       const int pr = row + (TWO ? slot * kTile : 0);   // the row in a part
-      const int64_t to = (bh * a.group + g) * a.tokens + token;
+      const int r = r0 + row, g = r / n;
+      const int64_t to = (((int64_t)seg.p.seq * a.heads + seg.p.head) * a.group + g) * a.tokens + (r - g * n);
       auto finish = [&](float top, float sum) {        // what is written beside the row; returns the output's factor
         if (row < rows) {
           if (!whole) {

@@ -17,6 +17,8 @@ int64_t most_tiles(int batch, int heads, int64_t passes, int tokens, int64_t cap
 }
 
 size_t upto_bytes(int batch) { return up(((size_t)batch + 1) * sizeof(int64_t)); }
+constexpr size_t kCutBytes = (size_t)kMaxTreeCtas * 2 * sizeof(int4);
+static_assert(kCutBytes % 256 == 0, "parts follow");
 
 size_t parts_bytes(int64_t ctas, int tile_q, int head_dim) {
   return up((size_t)ctas * 2 * tile_q * (head_dim + 2) * sizeof(float));
@@ -35,7 +37,7 @@ size_t tree_workspace_bytes(int batch, int q_heads, int heads, int head_dim, int
     const size_t tc = parts_bytes(bounded(most_tiles(batch, heads, (rows + wide - 1) / wide, tokens, cap, 128, 128), kMaxTcCtas), wide, head_dim);
     parts = tc > parts ? tc : parts;
   }
-  return upto_bytes(batch) + parts;
+  return upto_bytes(batch) + kCutBytes + parts;
 }
 
 tree::Args tree_args(const TreeJob& job, int tile_q) {
@@ -72,7 +74,8 @@ cudaError_t tree_fill(tree::Args& a, const TreeJob& job, int tile, int fresh, in
   a.ctas -= a.ctas % a.siblings;
   char* ws = static_cast<char*>(job.workspace);
   a.upto = reinterpret_cast<int64_t*>(ws);
-  a.parts = reinterpret_cast<float*>(ws + upto_bytes(a.batch));
+  a.cuts = reinterpret_cast<int4*>(ws + upto_bytes(a.batch));
+  a.parts = reinterpret_cast<float*>(ws + upto_bytes(a.batch) + kCutBytes);
   return cudaSuccess;
 }
 

@@ -39,6 +39,8 @@ struct Args {
   int least;            // tiles that a share has at least, where there are as many
   // workspace
   int64_t* upto;        // [batch + 1]: tiles in the sequences before, and in all
+  int4* cuts;           // [shares][2]: (sequence, head, pass, tile), (tiles, tokens, -, -) where a share is the first to begin
+                        // inside a head; else tile 0
   float* parts;         // [ctas][2] of (o [tile_q][D] or [D][tile_q], m [tile_q] (log2 domain), l [tile_q])
   int32_t* dev_status;
 };
@@ -73,18 +75,36 @@ __device__ __forceinline__ int working_shares(const Args& a, int64_t total) {
   const int64_t shares = a.ctas / a.siblings, most = (total + a.least - 1) / a.least;
   return (int)(most < shares ? most : shares);
 }
-// (shares <= 1024 and total <= 2^48: no product overflows)
-__device__ __forceinline__ int64_t share_start(int64_t total, int shares, int c) { return total * c / shares; }
+// (c <= shares <= 320 and total <= 2^52: no product overflows; short lists, where the latency counts, get by with a
+// 32-bit division)
+__device__ __forceinline__ int64_t share_start(int64_t total, int shares, int c) {
+  if (total < (1 << 23)) return (uint32_t)total * (uint32_t)c / (uint32_t)shares;
+  return total * c / shares;
+}
 // The share that holds flat tile t: the last one that starts at or before it.
 __device__ __forceinline__ int share_of(int64_t total, int shares, int64_t t) {
-  int c = (int)(t * shares / total);
-  while (c + 1 < shares && share_start(total, shares, c + 1) <= t) ++c;
+  int c = total < (1 << 23) ? (int)((uint32_t)t * (uint32_t)shares / (uint32_t)total) : (int)(t * shares / total);
+  while (c + 1 < shares && share_start(total, shares, c + 1) <= t) ++c;   // (the quotient's share starts at or before t)
   return c;
 }
 
+// A place in the list: a tile of a head's pass, and what its sequence is.
+struct Place {
+  int seq, head, pass, tile;
+  Seq s;
+};
+// The place of tile `in` of the sequence p.seq (with p.s).
+__device__ __forceinline__ void place_at(Place& p, int64_t in) {
+  const int64_t unit = in < ((int64_t)1 << 31) ? (int64_t)((uint32_t)in / (uint32_t)p.s.tiles) : in / p.s.tiles;
+  p.tile = (int)(in - unit * p.s.tiles);
+  const uint32_t u = (uint32_t)unit;   // (heads and passes: 65535 by 2^22 at most, and fewer than 2^31 together)
+  p.head = (int)(u / (uint32_t)p.s.passes);
+  p.pass = (int)(u - (uint32_t)p.head * (uint32_t)p.s.passes);
+}
 // Where a CTA's share lies: tiles at .. end - 1 of the list, from sequence `seq`, which starts at tile `before`.
 struct Share {
   int64_t at, end, before;
+  int64_t previous;   // where the share before begins (the first one's: its own)
   int seq;
 };
 
@@ -109,7 +129,7 @@ template <int TILE, int NEW, int THREADS> __device__ __forceinline__ Share find_
     if (lane >= off) x += y;
   }
   if (lane == 31) warp_sums[tid / 32] = x;
-  if (tid == 0) found = Share{0, 0, 0, 0};
+  if (tid == 0) found = Share{0, 0, 0, 0, 0};
   __syncthreads();
   int64_t total = 0, upto = x - mine;
   for (int w = 0; w < THREADS / 32; ++w) {
@@ -132,28 +152,34 @@ template <int TILE, int NEW, int THREADS> __device__ __forceinline__ Share find_
     if (at >= upto && at < upto + mine) {
       int b = b0;
       for (int64_t u; at >= upto + (u = seq_of<TILE, NEW>(a, b).units(a.heads)); ++b) upto += u;
-      found = Share{at, share_start(total, shares, c + 1), upto, b};
+      found = Share{at, share_start(total, shares, c + 1), upto, share_start(total, shares, c > 0 ? c - 1 : 0), b};
     }
   }
   __syncthreads();
   return found;
 }
 
-// A place in the list: a tile of a head's pass, and what its sequence is.
-struct Place {
-  int seq, head, pass, tile;
-  Seq s;
-};
 template <int TILE, int NEW> __device__ __forceinline__ Place first_place(const Args& a, const Share& share) {
   Place p;
   p.seq = share.seq;
   p.s = seq_of<TILE, NEW>(a, p.seq);
-  const int64_t in = share.at - share.before;
-  const int64_t unit = in / p.s.tiles;
-  p.tile = (int)(in - unit * p.s.tiles);
-  p.head = (int)(unit / p.s.passes);
-  p.pass = (int)(unit - (int64_t)p.head * p.s.passes);
+  place_at(p, share.at - share.before);
   return p;
+}
+// Leaves a share's note for the joining launch (one thread of every CTA): whether it is the first to begin inside a head.
+template <int TILE, int NEW> __device__ __forceinline__ void leave_note(const Args& a, const Share& share) {
+  const int c = (int)blockIdx.x / a.siblings;
+  if (blockIdx.x % a.siblings != 0) return;
+  int tile = 0;
+  if (share.at < share.end && c > 0) {
+    const Place p = first_place<TILE, NEW>(a, share);
+    const bool first = p.tile > 0 && share.previous <= share.at - p.tile;
+    a.cuts[2 * c + 1] = make_int4(p.s.tiles, p.s.n, 0, 0);
+    tile = first ? p.tile : 0;
+    a.cuts[2 * c] = make_int4(p.seq, p.head, p.pass, tile);
+  } else {
+    a.cuts[2 * c] = make_int4(0, 0, 0, 0);
+  }
 }
 // The next head's (or pass's) first tile, which exists.
 template <int TILE, int NEW> __device__ __forceinline__ void next_head(const Args& a, Place& p) {

@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
     ptx::fence_mbar_init();
   }
   const Share share = find_share<kTile, kTile, S::kThreads>(a, small.share);   // (with barriers)
+  if (tid == 64) leave_note<kTile, kTile>(a, share);
   if (share.at >= share.end) return;
   if (warp == 1) {
     ptx::tmem_alloc(&small.tmem, S::kColumns);

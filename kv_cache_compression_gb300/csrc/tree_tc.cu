@@ -57,8 +57,12 @@ template <int THREADS> struct Small {
 
 template <bool Q8, int D, bool TWO> struct Shape {
   static constexpr int kRows = TWO ? 256 : 128;                // query rows of a pass
-  static constexpr int kSoft = 16;                             // softmax warps: two for 32 rows of a slot, half of the keys each
-  static constexpr int kWarps = 4 + kSoft + (Q8 ? 4 : 0);
+  // Softmax warps: two for 32 rows of a slot, half of the keys each. Beside an 8-bit cache one has time enough for all of
+  // them, and eight more unpack.
+  static constexpr int kHalves = Q8 ? 1 : 2;
+  static constexpr int kSoft = 8 * kHalves;
+  static constexpr int kUnpack = Q8 ? 8 : 0;
+  static constexpr int kWarps = 4 + kSoft + kUnpack;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kSlotQ = kTile * D * 2;                 // bytes of 128 rows of queries
   static constexpr int kStage = kTile * D * 2;                 // of a tile of K or V
@@ -202,12 +206,14 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
     abort = 0;
     for (int i = 0; i < 12; ++i) small.pending[i] = 0;
     for (int i = 0; i < kStages; ++i) {
-      ptx::mbar_init(&bars.kv_full[i], Q8 ? 4 : 1);   // (four unpacking warps)
+      ptx::mbar_init(&bars.kv_full[i], Q8 ? S::kUnpack : 1);
       ptx::mbar_init(&bars.kv_empty[i], TWO ? 2 : 1);   // (slots)
     }
-    for (int i = 0; i < kRaws; ++i) {
-      ptx::mbar_init(&bars.raw_full[i], 1);
-      ptx::mbar_init(&bars.raw_empty[i], 4);
+    if constexpr (Q8) {
+      for (int i = 0; i < kRaws; ++i) {
+        ptx::mbar_init(&bars.raw_full[i], 1);
+        ptx::mbar_init(&bars.raw_empty[i], S::kUnpack);
+      }
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&bars.s_full[i], 1);
@@ -323,9 +329,10 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
     // O += P V of the ring's tile `at`; `fresh`: O =.
     auto pv = [&](uint32_t at, bool fresh) {
       const uint32_t v_lo = uniform(v_desc(ring + S::stage(slot, at) * S::kStage));
+      constexpr int kHalf = kTile / S::kHalves / 16;   // (weights begin where their half's logits did)
 #pragma unroll
       for (int s = 0; s < kTile / 16; ++s)
-        mma_ts(leader, o_at, s_at + (s / 4) * 64 + (s % 4) * 8, v_lo + s * (2048 >> 4), kDescHigh, kIdescPv, !(fresh && s == 0));
+        mma_ts(leader, o_at, s_at + s / kHalf * (kTile / S::kHalves) + s % kHalf * 8, v_lo + s * (2048 >> 4), kDescHigh, kIdescPv, !(fresh && s == 0));
     };
     // Walks of the Q K^T and of the P V, the first a tile of the slot's ahead. A slot waits for every segment's queries and outputs
     // and counts in on q_empty and o_full at its end, whether it had tiles of it or not: barriers know a phase by its parity
@@ -453,8 +460,9 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
       ptx::mbar_wait(&bars.q_full, seg.index & 1, &none, kWaitLimit);
     }
   } else if (warp < 4 + S::kSoft) {
-    // ---- softmax: two threads per row of a slot, half of the keys each
-    const int slot = (warp - 4) / 8, half = (warp - 4) / 4 % 2, quarter = warp % 4, row = quarter * 32 + lane;
+    // ---- softmax: kHalves threads per row of a slot, a share of the keys each
+    constexpr int kHalves = S::kHalves, kKeys = kTile / kHalves, kWords = kKeys / 32, kChunks = kKeys / 16;
+    const int slot = (warp - 4) / (4 * kHalves), half = (warp - 4) / 4 % kHalves, quarter = warp % 4, row = quarter * 32 + lane;
     const uint32_t o_lane = tmem + ((uint32_t)(quarter * 32) << 16), s_at = o_lane + S::kS(slot);
     float* const swap = reinterpret_cast<float*>(smem + S::kSwap) + slot * 2 * kTile;   // [half][row]
     float* const factors = reinterpret_cast<float*>(smem + S::kFactors) + slot * 4 * kTile;
@@ -475,21 +483,23 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
         const int key0 = (drafted ? tile - seg.p.s.cache_tiles : tile) * kTile;
         const int valid = min(kTile, (drafted ? n : seg.p.s.rows) - key0);
         const bool edge = drafted || valid < kTile;
-        // This row's bits of the thread's 64 keys: those that it sees, and (below) those that make it NaN.
-        uint32_t see[2] = {~0u, ~0u}, bad[2] = {0u, 0u};
+        // This row's bits of the thread's keys: those that it sees, and (below) those that make it NaN.
+        uint32_t see[kWords], bad[kWords];
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) see[w] = ~0u, bad[w] = 0u;
         if (edge) {
           const int token = (r0 + row) % n;
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const int k0 = 64 * half + 32 * w;
+          for (int w = 0; w < kWords; ++w) {
+            const int k0 = kKeys * half + 32 * w;
             see[w] = valid >= k0 + 32 ? ~0u : valid > k0 ? (1u << (valid - k0)) - 1u : 0u;
           }
           if (drafted && a.mask) {
             // lane e looks at key k0 + e for one row after the other (rows that are not there have a token, too)
             const uint8_t* const mask = a.mask + seg.p.seq * a.mask_stride + key0;
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              const int k0 = 64 * half + 32 * w;
+            for (int w = 0; w < kWords; ++w) {
+              const int k0 = kKeys * half + 32 * w;
               if (valid <= k0) break;
               const uint8_t* const from = mask + min(k0 + lane, valid - 1);
               uint32_t word = 0;
@@ -509,23 +519,27 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
             }
           } else if (drafted) {   // causal
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              const int upto = token - key0 + 1 - (64 * half + 32 * w);
+            for (int w = 0; w < kWords; ++w) {
+              const int upto = token - key0 + 1 - (kKeys * half + 32 * w);
               see[w] &= upto >= 32 ? ~0u : upto > 0 ? (1u << upto) - 1u : 0u;
             }
           }
         }
         float* const fk = factors + (steps & 1) * 2 * kTile;   // this tile's factors of logits and weights (8 bits)
         if constexpr (Q8) {
-          float x = 0.f;               // half 0: of logits; half 1: of weights
+          float x = 0.f, y = 0.f;
           if (drafted) {
-            x = half ? kNewP : kNewDot * a.scale_log2;
+            x = kNewDot;
+            y = kNewP;
           } else if (row < valid) {
             const int64_t at = ((int64_t)seg.p.seq * a.heads + seg.p.head) * a.cap + key0 + row;
-            if (in_bounds(at < (int64_t)a.batch * a.heads * a.cap, a.dev_status))
-              x = half ? __ldg(a.v_step + at) * kQ8P : __ldg(a.k_step + at) * kQ8Dot * a.scale_log2;
+            if (in_bounds(at < (int64_t)a.batch * a.heads * a.cap, a.dev_status)) {
+              x = __ldg(a.k_step + at) * kQ8Dot;
+              y = __ldg(a.v_step + at) * kQ8P;
+            }
           }
-          fk[half * kTile + row] = x;
+          fk[row] = x * a.scale_log2;
+          fk[kTile + row] = y;
           ptx::named_barrier(1 + slot, kSlotThreads);
         }
         wait(&bars.s_full[slot], steps);
@@ -534,7 +548,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           // V's rows that nobody sees become zeros, as do drafted ones with an infinity or NaN, which the rows that see
           // them get as a NaN weight: 0 times it must not reach the others. A thread looks after a key. (S is there, so the slot's
           // last P V is done, and the stage's phase before V's has passed.)
-          if (half == 1 && (!TWO || slot == 0)) {
+          if (half == kHalves - 1 && (!TWO || slot == 0)) {
             const uint32_t at = 2 * (TWO ? done + f : steps) + 1, stage = S::stage(slot, at);   // V's place in the ring
             wait(&bars.kv_full[stage], at / S::kTurn);
             uint8_t* const v = smem + S::kRing + stage * S::kStage;
@@ -558,7 +572,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           if (drafted || both) ptx::named_barrier(both ? 3 : 1 + slot, both ? 2 * kSlotThreads : kSlotThreads);   // (the other slot's products read V, too)
           if (drafted) {
 #pragma unroll
-            for (int w = 0; w < 2; ++w) bad[w] = small.bad_keys[TWO ? 0 : slot][2 * half + w] & see[w];
+            for (int w = 0; w < kWords; ++w) bad[w] = small.bad_keys[TWO ? 0 : slot][kWords * half + w] & see[w];
             ptx::named_barrier(both ? 3 : 1 + slot, both ? 2 * kSlotThreads : kSlotThreads);   // (before the next tile's are written)
           }
         }
@@ -566,7 +580,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           const float2 by = make_float2(a.scale_log2, a.scale_log2);
           // Logits of chunk c (sixteen keys) less `low`, in the log2 domain.
           auto load = [&](float2 (&y)[8], int c, float low) {
-            const int k0 = 64 * half + 16 * c;
+            const int k0 = kKeys * half + 16 * c;
             uint32_t x[16];
             tmem_ld16(s_at + k0, x);
             ptx::tmem_wait_ld();
@@ -590,7 +604,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               sum = add2(sum, y[e]);
-              if constexpr (Q8) y[e] = mul2(y[e], *reinterpret_cast<const float2*>(fk + kTile + 64 * half + 16 * c + 2 * e));
+              if constexpr (Q8) y[e] = mul2(y[e], *reinterpret_cast<const float2*>(fk + kTile + kKeys * half + 16 * c + 2 * e));
               p[e] = pack2(y[e].x, y[e].y);
             }
           };
@@ -598,7 +612,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           // (Straight code, and little of it: sixteen warps out of step fetch it, and what all of the tile's cases take together
           // in one piece cost 2800 clocks a tile, most of them without an instruction.)
           bool left = true;
-          if (!first && !edge) {
+          if (kHalves == 2 && !first && !edge) {
             uint32_t p[32];
             float top = -INFINITY;
 #pragma unroll
@@ -611,13 +625,18 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
               pack(y, c, p + 8 * c);
             }
             left = any_of_pair(pair, top > kSlack);
-            if (!left) tmem_st32(s_at + 64 * half, p);
+            if (!left) tmem_st32(s_at + kKeys * half, p);
           }
           if (left) {
             // ---- a head's first tile, its last ones, and where the maximum grows: chunk by chunk
             auto mask = [&](float2 (&y)[8], int c, bool nan) {
               if (!edge) return;
-              const uint32_t keep = (c < 2 ? see[0] : see[1]) >> (16 * (c % 2)), not_a = (c < 2 ? bad[0] : bad[1]) >> (16 * (c % 2));
+              uint32_t keep = see[0], not_a = bad[0];
+#pragma unroll
+              for (int w = 1; w < kWords; ++w)
+                if (c / 2 == w) keep = see[w], not_a = bad[w];
+              keep >>= 16 * (c % 2);
+              not_a >>= 16 * (c % 2);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 if (!(keep >> (2 * e) & 1)) y[e].x = -INFINITY;
@@ -628,21 +647,23 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
             };
             float top = -INFINITY;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < kChunks; ++c) {
               float2 y[8];
               load(y, c, 0.f);
               mask(y, c, false);
               top = highest(y, top);
             }
-            swap[half * kTile + row] = top;
-            ptx::named_barrier(pair, 64);
-            top = fmaxf(top, swap[(half ^ 1) * kTile + row]);
+            if constexpr (kHalves == 2) {
+              swap[half * kTile + row] = top;
+              ptx::named_barrier(pair, 64);
+              top = fmaxf(top, swap[(half ^ 1) * kTile + row]);
+            }
             const float next = first ? fmaxf(m, top) : top > m + kSlack ? top : m;
             if (!first && __any_sync(0xffffffffu, next != m)) {   // (the same for both threads of a row)
               const float fall = rescale(m, next);
               l *= fall;
 #pragma unroll 1
-              for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+              for (int c = half * (D / kHalves); c < (half + 1) * (D / kHalves); c += 16) {
                 uint32_t x[16];
                 tmem_ld16(o_lane + S::kO(slot) + c, x);
                 ptx::tmem_wait_ld();
@@ -655,14 +676,14 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
             sum = make_float2(0.f, 0.f);
             uint32_t p[8];
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {   // (a chunk's weights stand where logits of the first chunks stood)
+            for (int c = 0; c < kChunks; ++c) {   // (a chunk's weights stand where logits of the first chunks stood)
               float2 y[8];
               load(y, c, m);
               mask(y, c, true);
 #pragma unroll
               for (int e = 0; e < 8; ++e) y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
               pack(y, c, p);
-              tmem_st8(s_at + 64 * half + 8 * c, p);
+              tmem_st8(s_at + kKeys * half + 8 * c, p);
             }
           }
           l += sum.x + sum.y;
@@ -677,7 +698,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
 
       // ---- the head's end in this share: the halves' sums meet, and up to 128 rows the slots' m, sums and O
       const bool whole = seg.whole();
-      if (half == 1) swap[row] = l;    // (the other half has read what stood there: its own l is from after the last swap)
+      if (half == 1) swap[row] = l;   // (the other half has read what stood there: its own l is from after the last swap)
       wait(&bars.o_full, seg.index);
       ptx::tc_fence_after();
       float* const part = part_at<D>(a, (int)blockIdx.x, seg.at > share.at ? 1 : 0);
@@ -710,17 +731,20 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           for (int e = 0; e < 16; ++e) u[e * S::kRows] = __uint_as_float(x[e]);
         }
       };
-      ptx::named_barrier(pair, 64);
+      if constexpr (kHalves == 2) {
+        ptx::named_barrier(pair, 64);
+        if (half == 0) l += swap[row];
+      }
       if constexpr (TWO) {
         if (half == 0) {
-          const float scale = finish(m, l + swap[row]);
+          const float scale = finish(m, l);
           swap[kTile + row] = scale;
         }
-        ptx::named_barrier(pair, 64);
+        if constexpr (kHalves == 2) ptx::named_barrier(pair, 64);
         if (mine) {
           const float scale = swap[kTile + row];
 #pragma unroll 1
-          for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+          for (int c = half * (D / kHalves); c < (half + 1) * (D / kHalves); c += 16) {
             uint32_t x[16];
             tmem_ld16(o_lane + S::kO(slot) + c, x);
             ptx::tmem_wait_ld();
@@ -730,16 +754,13 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           }
         }
       } else {
-        // each slot and half writes a quarter of the channels
+        // each slot and half writes its share of the channels
         const bool other = seg.tiles > 1;   // (of one tile, one slot has none)
         const int only = (int)(done & 1);   // the first tile's slot
         float* const factor = reinterpret_cast<float*>(smem + S::kSwap);   // slot 0's: the two factors of a row, in the end
-        if (half == 0) {
-          l += swap[row];
-          if (slot == 1) {
-            swap[row] = l;
-            swap[kTile + row] = m;
-          }
+        if (half == 0 && slot == 1) {
+          swap[row] = l;
+          swap[kTile + row] = m;
         }
         ptx::named_barrier(3, 2 * kSlotThreads);
         if (half == 0 && slot == 0) {
@@ -753,9 +774,9 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
         if (mine) {
           const float f0 = factor[row], f1 = factor[kTile + row];
           const float fx = other || only == 0 ? f0 : f1;
-          constexpr int kMine = D / 4;
+          constexpr int kMine = D / (2 * kHalves);
 #pragma unroll 1
-          for (int c = (2 * slot + half) * kMine; c < (2 * slot + half + 1) * kMine; c += 16) {
+          for (int c = (kHalves * slot + half) * kMine; c < (kHalves * slot + half + 1) * kMine; c += 16) {
             uint32_t x[16], y[16];
             tmem_ld16(o_lane + S::kO(other ? 0 : only) + c, x);
             if (other) tmem_ld16(o_lane + S::kO(1) + c, y);
@@ -776,8 +797,8 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
       done += (uint32_t)seg.tiles;
     } while (seg.next(a));
   } else if constexpr (Q8) {
-    // ---- codes into bf16 tiles: a thread per key
-    const int key = tid - 32 * (4 + S::kSoft);
+    // ---- codes into bf16 tiles: two threads per key, half of the channels each
+    const int key = tid % kTile, part = (tid - 32 * (4 + S::kSoft)) / kTile;
     Segments ks(a, share), vs(a, share);
     int kf = 0, vf = 0;
     uint32_t used = 0;                 // raw tiles
@@ -792,23 +813,22 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
         wait(&bars.raw_full[at], used / kRaws);
         const uint8_t* const from = smem + S::kRawRing + at * S::kRaw;
         const bool there = key < s.p.s.rows - tile * kTile;
+        constexpr int kMine = D / 32;   // pieces of sixteen codes
+        uint4 w[kMine];
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int c = part * kMine + i;
+          const uint32_t off = D == 128 ? key * 128 + ((c ^ (key & 7)) << 4) : key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
+          w[i] = there ? *reinterpret_cast<const uint4*>(from + off) : make_uint4(0u, 0u, 0u, 0u);
+        }
         if (turn > 0) wait(&bars.kv_empty[slot], turn - 1);
         auto low = [](uint32_t x) { return prmt(x, x, 0x1100) & 0x807F807Fu; };
         auto high = [](uint32_t x) { return prmt(x, x, 0x3322) & 0x807F807Fu; };
-#pragma unroll 1
-        for (int c0 = 0; c0 < D / 16; c0 += 4) {
-          uint4 w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = c0 + i;
-            const uint32_t off = D == 128 ? key * 128 + ((c ^ (key & 7)) << 4) : key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
-            w[i] = there ? *reinterpret_cast<const uint4*>(from + off) : make_uint4(0u, 0u, 0u, 0u);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            *reinterpret_cast<uint4*>(to + piece_at(key, 2 * (c0 + i))) = make_uint4(low(w[i].x), high(w[i].x), low(w[i].y), high(w[i].y));
-            *reinterpret_cast<uint4*>(to + piece_at(key, 2 * (c0 + i) + 1)) = make_uint4(low(w[i].z), high(w[i].z), low(w[i].w), high(w[i].w));
-          }
+        for (int i = 0; i < kMine; ++i) {
+          const int c = part * kMine + i;
+          *reinterpret_cast<uint4*>(to + piece_at(key, 2 * c)) = make_uint4(low(w[i].x), high(w[i].x), low(w[i].y), high(w[i].y));
+          *reinterpret_cast<uint4*>(to + piece_at(key, 2 * c + 1)) = make_uint4(low(w[i].z), high(w[i].z), low(w[i].w), high(w[i].w));
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars.raw_empty[at]);
@@ -819,7 +839,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
         const __nv_bfloat16* const from = static_cast<const __nv_bfloat16*>(is_key ? a.k_new : a.v_new) + (bh * a.tokens + (there ? row : 0)) * D;
         if (turn > 0) wait(&bars.kv_empty[slot], turn - 1);
 #pragma unroll 8
-        for (int c = 0; c < D / 8; ++c)
+        for (int c = part * (D / 16); c < (part + 1) * (D / 16); ++c)
           *reinterpret_cast<uint4*>(to + piece_at(key, c)) = there ? ld_nc_v4(from + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

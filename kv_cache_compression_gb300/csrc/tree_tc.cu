@@ -64,6 +64,9 @@ template <bool Q8, int D, bool TWO> struct Shape {
   static constexpr int kUnpack = Q8 ? 8 : 0;
   static constexpr int kWarps = 4 + kSoft + kUnpack;
   static constexpr int kThreads = 32 * kWarps;
+  // Registers go from the warps that move data to those of the softmax (both sum up to no more than the block is launched with).
+  static constexpr int kLaunchRegs = 96, kSoftRegs = 104, kMoveRegs = 64;
+  static_assert(Q8 || 32 * kSoft * kSoftRegs + (kThreads - 32 * kSoft) * kMoveRegs <= kThreads * kLaunchRegs, "registers");
   static constexpr int kSlotQ = kTile * D * 2;                 // bytes of 128 rows of queries
   static constexpr int kStage = kTile * D * 2;                 // of a tile of K or V
   static constexpr int kStages = (Q8 ? (TWO ? 3 : 4) : TWO ? 4 : 6) * (128 / D);   // (TWO: of one ring; else of two, a slot's each)
@@ -84,19 +87,29 @@ template <bool Q8, int D, bool TWO> struct Shape {
   static constexpr int kColumns = 512;
 };
 
-__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+      "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
         "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(at));
 }
-__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8]) {
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
                "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
       "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
@@ -106,7 +119,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) 
       "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at), "r"(r[0]), "r"(r[1]),
       "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
@@ -255,6 +268,8 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
   const uint32_t total = (uint32_t)(share.end - share.at);   // tiles
   constexpr uint32_t kPair = TWO ? 1 : 2;                    // they are loaded, K before V
 
+  if (warp < 4) {
+  if constexpr (!Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kMoveRegs));
   if (warp == 0) {
     // ---- loads, in the order in which the products take them
     if (lane == 0) {
@@ -400,7 +415,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
     commit(leader, &bars.drain[slot]);
     const int none = 0;
     ptx::mbar_wait(&bars.drain[slot], 0, &none, kWaitLimit);
-  } else if (warp == 3) {
+  } else {
     // ---- queries into shared memory
     const int at = lane;
     Segments seg(a, share);
@@ -459,9 +474,12 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
       const int none = 0;
       ptx::mbar_wait(&bars.q_full, seg.index & 1, &none, kWaitLimit);
     }
+  }
   } else if (warp < 4 + S::kSoft) {
+    if constexpr (!Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSoftRegs));
     // ---- softmax: kHalves threads per row of a slot, a share of the keys each
-    constexpr int kHalves = S::kHalves, kKeys = kTile / kHalves, kWords = kKeys / 32, kChunks = kKeys / 16;
+    constexpr int kHalves = S::kHalves, kKeys = kTile / kHalves, kWords = kKeys / 32;
+    constexpr int kChunk = 16, kChunks = kKeys / kChunk, kE = kChunk / 2;   // keys that are computed on at a time, and their pairs
     const int slot = (warp - 4) / (4 * kHalves), half = (warp - 4) / 4 % kHalves, quarter = warp % 4, row = quarter * 32 + lane;
     const uint32_t o_lane = tmem + ((uint32_t)(quarter * 32) << 16), s_at = o_lane + S::kS(slot);
     float* const swap = reinterpret_cast<float*>(smem + S::kSwap) + slot * 2 * kTile;   // [half][row]
@@ -578,21 +596,25 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
         }
         if (mine) {
           const float2 by = make_float2(a.scale_log2, a.scale_log2);
-          // Logits of chunk c (sixteen keys) less `low`, in the log2 domain.
-          auto load = [&](float2 (&y)[8], int c, float low) {
-            const int k0 = kKeys * half + 16 * c;
-            uint32_t x[16];
-            tmem_ld16(s_at + k0, x);
+          // Logits of chunk c less `low`, in the log2 domain.
+          auto load = [&](float2 (&y)[kE], int c, float low) {
+            const int k0 = kKeys * half + kChunk * c;
+            uint32_t x[kChunk];
+            tmem_ld(s_at + k0, x);
             ptx::tmem_wait_ld();
             const float2 down = make_float2(-low, -low);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              y[e] = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), Q8 ? *reinterpret_cast<const float2*>(fk + k0 + 2 * e) : by, down);
+            for (int e = 0; e < kE; e += 2) {
+              float4 k = make_float4(by.x, by.y, by.x, by.y);
+              if constexpr (Q8) k = *reinterpret_cast<const float4*>(fk + k0 + 2 * e);
+              y[e] = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(k.x, k.y), down);
+              y[e + 1] = fma2(make_float2(__uint_as_float(x[2 * e + 2]), __uint_as_float(x[2 * e + 3])), make_float2(k.z, k.w), down);
+            }
           };
-          auto highest = [](const float2 (&y)[8], float top) {
+          auto highest = [](const float2 (&y)[kE], float top) {
             float other = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
+            for (int e = 0; e < kE; e += 2) {
               top = fmaxf(fmaxf(top, y[e].x), y[e].y);
               other = fmaxf(fmaxf(other, y[e + 1].x), y[e + 1].y);
             }
@@ -600,45 +622,54 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
           };
           // Weights of chunk c, rounded to bf16; they are summed up as they were.
           float2 sum = make_float2(0.f, 0.f);
-          auto pack = [&](float2 (&y)[8], int c, uint32_t* p) {
+          auto pack = [&](float2 (&y)[kE], int c, uint32_t* p) {
+            float2 other = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < kE; e += 2) {
               sum = add2(sum, y[e]);
-              if constexpr (Q8) y[e] = mul2(y[e], *reinterpret_cast<const float2*>(fk + kTile + kKeys * half + 16 * c + 2 * e));
+              other = add2(other, y[e + 1]);
+              if constexpr (Q8) {
+                const float4 v = *reinterpret_cast<const float4*>(fk + kTile + kKeys * half + kChunk * c + 2 * e);
+                y[e] = mul2(y[e], make_float2(v.x, v.y));
+                y[e + 1] = mul2(y[e + 1], make_float2(v.z, v.w));
+              }
               p[e] = pack2(y[e].x, y[e].y);
+              p[e + 1] = pack2(y[e + 1].x, y[e + 1].y);
             }
+            sum = add2(sum, other);
           };
           // Most tiles: the maximum as it is, and the weights in registers until both threads of a row know that none is too large.
           // (Straight code, and little of it: sixteen warps out of step fetch it, and what all of the tile's cases take together
           // in one piece cost 2800 clocks a tile, most of them without an instruction.)
           bool left = true;
-          if (kHalves == 2 && !first && !edge) {
-            uint32_t p[32];
+          if (!Q8 && !first && !edge) {
+            uint32_t p[kKeys / 2];
             float top = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float2 y[8];
+            for (int c = 0; c < kChunks; ++c) {
+              float2 y[kE];
               load(y, c, m);
               top = highest(y, top);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
-              pack(y, c, p + 8 * c);
+              for (int e = 0; e < kE; ++e) y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
+              pack(y, c, p + kE * c);
             }
             left = any_of_pair(pair, top > kSlack);
-            if (!left) tmem_st32(s_at + kKeys * half, p);
+            if constexpr (!Q8)
+              if (!left) tmem_st(s_at + kKeys * half, p);
           }
           if (left) {
             // ---- a head's first tile, its last ones, and where the maximum grows: chunk by chunk
-            auto mask = [&](float2 (&y)[8], int c, bool nan) {
+            auto mask = [&](float2 (&y)[kE], int c, bool nan) {
               if (!edge) return;
               uint32_t keep = see[0], not_a = bad[0];
 #pragma unroll
               for (int w = 1; w < kWords; ++w)
-                if (c / 2 == w) keep = see[w], not_a = bad[w];
-              keep >>= 16 * (c % 2);
-              not_a >>= 16 * (c % 2);
+                if (kChunk * c / 32 == w) keep = see[w], not_a = bad[w];
+              keep >>= kChunk * c % 32;
+              not_a >>= kChunk * c % 32;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
+              for (int e = 0; e < kE; ++e) {
                 if (!(keep >> (2 * e) & 1)) y[e].x = -INFINITY;
                 if (!(keep >> (2 * e + 1) & 1)) y[e].y = -INFINITY;
                 if (nan && (not_a >> (2 * e) & 1)) y[e].x = __uint_as_float(0x7FC00000u);
@@ -648,7 +679,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
             float top = -INFINITY;
 #pragma unroll 1
             for (int c = 0; c < kChunks; ++c) {
-              float2 y[8];
+              float2 y[kE];
               load(y, c, 0.f);
               mask(y, c, false);
               top = highest(y, top);
@@ -665,25 +696,25 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
 #pragma unroll 1
               for (int c = half * (D / kHalves); c < (half + 1) * (D / kHalves); c += 16) {
                 uint32_t x[16];
-                tmem_ld16(o_lane + S::kO(slot) + c, x);
+                tmem_ld(o_lane + S::kO(slot) + c, x);
                 ptx::tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * fall);
-                tmem_st16(o_lane + S::kO(slot) + c, x);
+                tmem_st(o_lane + S::kO(slot) + c, x);
               }
             }
             m = next;
             sum = make_float2(0.f, 0.f);
-            uint32_t p[8];
+            uint32_t p[kE];
 #pragma unroll 1
             for (int c = 0; c < kChunks; ++c) {   // (a chunk's weights stand where logits of the first chunks stood)
-              float2 y[8];
+              float2 y[kE];
               load(y, c, m);
               mask(y, c, true);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
+              for (int e = 0; e < kE; ++e) y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
               pack(y, c, p);
-              tmem_st8(s_at + kKeys * half + 8 * c, p);
+              tmem_st(s_at + kKeys * half + kE * c, p);
             }
           }
           l += sum.x + sum.y;
@@ -746,7 +777,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
 #pragma unroll 1
           for (int c = half * (D / kHalves); c < (half + 1) * (D / kHalves); c += 16) {
             uint32_t x[16];
-            tmem_ld16(o_lane + S::kO(slot) + c, x);
+            tmem_ld(o_lane + S::kO(slot) + c, x);
             ptx::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * scale);
@@ -778,8 +809,8 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
 #pragma unroll 1
           for (int c = (kHalves * slot + half) * kMine; c < (kHalves * slot + half + 1) * kMine; c += 16) {
             uint32_t x[16], y[16];
-            tmem_ld16(o_lane + S::kO(other ? 0 : only) + c, x);
-            if (other) tmem_ld16(o_lane + S::kO(1) + c, y);
+            tmem_ld(o_lane + S::kO(other ? 0 : only) + c, x);
+            if (other) tmem_ld(o_lane + S::kO(1) + c, y);
             ptx::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e) {

@@ -46,11 +46,14 @@ extern "C" {
  * out      device [B, Hq, T, d]; tokens at or past n_new[b] and tokens that see no row (or whose logits are all -inf)
  *          get zeros
  * lse      device fp32 [B, Hq, T] (NULL: not returned); -inf where out is zeros for one of these reasons
- * dtype    snapkv_dtype of q, k_cache, v_cache, k_new, v_new and out. Products and sums are of fp32 accuracy; in bf16 calls
- *          weights enter the second product as two bf16 parts (16 bits). Values that a token sees must be finite;
- *          a NaN or infinity in a drafted row reaches none of the tokens that do not see the row
+ * dtype    snapkv_dtype of q, k_cache, v_cache, k_new, v_new and out. Products and sums are of fp32 accuracy. In bf16 calls
+ *          weights enter the second product rounded: to two bf16 parts (16 bits) in calls of up to 16 query rows (G * T) a KV head
+ *          (over 8-bit caches 32), to one (8 bits) in calls of more, which moves an output by 2^-8 sum_r p_r |V_r| at
+ *          most. Values that a token sees must be finite; a NaN or infinity in a drafted row reaches none of the tokens that
+ *          do not see the row (of those that do, it makes all outputs NaN where it lies in V of a bf16 call)
  * workspace device, >= snapkv_tree_workspace_size(...) bytes, 256-byte aligned (contents on entry do not matter); the size
- *          serves calls of either type and format. 0 for invalid sizes alone
+ *          serves calls of either type and format. Where it is 0 (caches of up to 256 rows with up to 16 query rows, G * T,
+ *          a KV head; also the answer for invalid sizes) the workspace is not used and may be NULL
  * Sums run in a fixed order: the same call on the same device gives the same bits.
  */
 SNAPKV_API size_t snapkv_tree_workspace_size(int32_t batch, int32_t q_heads, int32_t heads, int32_t head_dim,

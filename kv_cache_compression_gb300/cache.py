@@ -123,7 +123,8 @@ def _call(name, device, *args):
         raise ValueError(f"{name} needs CUDA tensors, not {device}")
     f = _functions.get(name)
     if f is None:
-        lib()
+        for load in _loaders:
+            load()
         f = _functions[name]
     index = device.index
     handle = torch._C._cuda_getCurrentRawStream(index)
@@ -166,6 +167,9 @@ class Q4Cache:
         codes = [torch.empty((batch, heads, cap, head_dim // 2), dtype=_BYTE, device=device) for _ in "kv"]
         meta = [torch.empty((batch, heads, cap, head_dim // GROUP, 2), dtype=_BF16, device=device) for _ in "kv"]
         return cls(codes[0], meta[0], codes[1], meta[1])
+
+
+_loaders = [lib]   # of the headers whose functions _call calls
 
 
 @lru_cache(maxsize=256)

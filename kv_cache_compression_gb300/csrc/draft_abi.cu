@@ -38,7 +38,7 @@ snapkv_status run_tree(const TreeJob& job, size_t kv_bytes, size_t kv_step_bytes
       !aligned16(job.out) || !aligned4(job.len) || !aligned4(job.n_new) || !aligned4(job.lse) || !aligned4(job.dev_status))
     return SNAPKV_ERR_INVALID_ARG;
   const size_t need = tree_workspace_bytes(job.batch, job.q_heads, job.heads, job.head_dim, job.tokens, job.cap);
-  if (!job.workspace || workspace_bytes < need || ((uintptr_t)job.workspace & 255u)) return SNAPKV_ERR_WORKSPACE;
+  if (need && (!job.workspace || workspace_bytes < need || ((uintptr_t)job.workspace & 255u))) return SNAPKV_ERR_WORKSPACE;
   const size_t rows = (size_t)job.batch * job.q_heads * job.tokens;
   const size_t q_bytes = rows * job.head_dim * elem_bytes(job.dtype);
   const size_t new_bytes = (size_t)job.batch * job.heads * job.tokens * job.head_dim * elem_bytes(job.dtype);
@@ -54,7 +54,7 @@ snapkv_status run_tree(const TreeJob& job, size_t kv_bytes, size_t kv_step_bytes
                         {job.mask, (size_t)(job.mask_stride ? job.batch : 1) * (size_t)square, false},
                         {job.out, q_bytes, true},
                         {job.lse, rows * 4, true},
-                        {job.workspace, need, true},
+                        {need ? job.workspace : nullptr, need, true},
                         {job.dev_status, 4, true}};
   if (!disjoint(spans)) return SNAPKV_ERR_INVALID_ARG;
   return launch_tree(job) == cudaSuccess ? SNAPKV_OK : SNAPKV_ERR_CUDA;

@@ -70,18 +70,12 @@ __device__ __forceinline__ bool cut_at(const Args& a, int64_t total, int shares,
   return in_bounds(c > 0 && note.y < a.heads && cut.more >= 1 && c - 1 + cut.more < shares, a.dev_status);
 }
 
-// Tokens that are not there, and all of sequences without rows to see: zeros.
-template <typename IO, int D, int TILE, int NEW> __device__ __forceinline__ void write_zeros(const Args& a) {
+// Tokens that are not there, and all of sequences without rows to see.
+template <typename IO, int D, int TILE, int NEW> __device__ __forceinline__ void write_all_zeros(const Args& a) {
   const int q_heads = a.heads * a.group;
   for (int64_t v = blockIdx.x; v < (int64_t)a.batch * q_heads; v += gridDim.x) {
-    const int b = (int)((uint32_t)v / (uint32_t)q_heads);
-    const Seq s = seq_of<TILE, NEW>(a, b);
-    const int first = s.tiles == 0 ? 0 : s.n, none = a.tokens - first;
-    const int64_t at = v * a.tokens + first;
-    uint4* const out = reinterpret_cast<uint4*>(static_cast<IO*>(a.out) + at * D);
-    for (int u = threadIdx.x; u < none * (D * (int)sizeof(IO) / 16); u += kJoinThreads) out[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (a.lse)
-      for (int u = threadIdx.x; u < none; u += kJoinThreads) a.lse[at + u] = -INFINITY;
+    const Seq s = seq_of<TILE, NEW>(a, (int)((uint32_t)v / (uint32_t)q_heads));
+    write_zeros<IO, D, kJoinThreads>(a, v, s.tiles == 0 ? 0 : s.n);
   }
 }
 
@@ -105,14 +99,15 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(Args a) {
     const Seq s = seq_of<TILE, NEW>(a, (int)b);
     if (t >= s.n || s.tiles == 0) continue;
     const int r = g * s.n + t, pass = r / a.tile_q, i = r - pass * a.tile_q;
-    const int64_t f0 = __ldcg(a.upto + b) + ((int64_t)h * s.passes + pass) * s.tiles;
+    const int64_t f0 = __ldcg(a.upto + b) + ((int64_t)h * s.passes + (a.siblings > 1 ? 0 : pass)) * s.tiles;
+    const int sib = a.siblings > 1 ? pass : 0;
     Cut cut;
     cut.first = share_of(total, shares, f0);
     cut.more = share_of(total, shares, f0 + s.tiles - 1) - cut.first;
     cut.slot = share_start(total, shares, cut.first) < f0 ? 1 : 0;
     if (cut.more == 0) continue;   // finished in the first launch
     if (!in_bounds(cut.first >= 0 && cut.first + cut.more < shares && i < a.tile_q, a.dev_status)) continue;
-    auto part = [&](int k) { return part_at<D>(a, cut.first + k, k == 0 ? cut.slot : 0); };
+    auto part = [&](int k) { return part_at<D>(a, (cut.first + k) * a.siblings + sib, k == 0 ? cut.slot : 0); };
     float x[kPer] = {}, top = kNoMax, sum = 0.f;
     for (int k0 = 0; k0 <= cut.more; k0 += 32) {
       const int here = min(32, cut.more + 1 - k0);
@@ -150,7 +145,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(Args a) {
     for (int e = 0; e < kPer; ++e) store1<IO>(out + e, x[e] * scale);
     if (a.lse && lane == 0) a.lse[at] = lse_of(top, sum);
   }
-  write_zeros<IO, D, TILE, NEW>(a);
+  write_all_zeros<IO, D, TILE, NEW>(a);
 }
 
 // Passes of many rows: a warp joins 32 rows (a lane each) and eight channels, four parts at a time.
@@ -207,7 +202,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_wide_kernel(Args a) {
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * D + c0) = *reinterpret_cast<const uint4*>(y);
     if (a.lse && c0 == 0) a.lse[at] = lse_of(top, sum);
   }
-  write_zeros<__nv_bfloat16, D, TILE, TILE>(a);
+  write_all_zeros<__nv_bfloat16, D, TILE, TILE>(a);
 }
 
 // Blocks for the units of work that there may be and for the heads that may have zeros, `per_sm` an SM at most.

@@ -128,9 +128,16 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const Args a, con
     ptx::fence_mbar_init();
   }
   __shared__ ShareScratch<kThreads> scratch;
-  const Share share = find_share<kTile, kNew, kThreads>(a, scratch);   // (with barriers)
-  if (share.at >= share.end) return;
-  Place here = first_place<kTile, kNew>(a, share);
+  Share share;
+  Place here;
+  if (a.direct) {
+    if (!direct_share<__nv_bfloat16, D, kTile, kNew, kThreads>(a, share, here)) return;
+    __syncthreads();   // the barriers are initialised
+  } else {
+    share = find_share<kTile, kNew, kThreads>(a, scratch);   // (with barriers)
+    if (share.at >= share.end) return;
+    here = first_place<kTile, kNew>(a, share);
+  }
   Place ahead = here;              // the next tile to load
   int64_t ahead_at = share.at + warp;
   uint8_t* const ring = smem + warp * (kStages * S::kStage);
@@ -150,6 +157,12 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const Args a, con
   auto send = [&](int stage) {
     uint8_t* const k = ring + stage * S::kStage;
     const int bh = ahead.seq * a.heads + ahead.head;
+    if (ahead.tile == 0) {   // a new head: its queries come into L2
+      const int r = (a.siblings > 1 ? (int)blockIdx.x % a.siblings : ahead.pass) * kRows + lane / (D / 64), g = r / ahead.s.n;
+      if (lane / (D / 64) < kRows && r < a.group * ahead.s.n)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const __nv_bfloat16*>(a.q) +
+                                                      (((int64_t)bh * a.group + g) * a.tokens + (r - g * ahead.s.n)) * D + lane % (D / 64) * 64));
+    }
     uint64_t* const bar = &full[warp][stage];
     if (ahead.tile < ahead.s.cache_tiles) {
       const int row0 = ahead.tile * kTile;
@@ -201,10 +214,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const Args a, con
     const int64_t left = share.end - at;
     const int seg = left < here.s.tiles - here.tile ? (int)left : here.s.tiles - here.tile;
     const bool whole = seg == here.s.tiles;
-    const int n = here.s.n, count = a.group * n;   // query rows (at most kRows)
+    const int n = here.s.n, pass = a.siblings > 1 ? (int)blockIdx.x % a.siblings : here.pass;
+    const int first_row = pass * kRows, count = min(kRows, a.group * n - first_row);   // query rows of this pass
     const int64_t bh = (int64_t)here.seq * a.heads + here.head;
-    auto row_at = [&](int r) {
-      const int g = r / n;
+    auto row_at = [&](int i) {
+      const int r = first_row + i, g = r / n;
       return (bh * a.group + g) * a.tokens + (r - g * n);
     };
     // ---- queries, as A operands: rows j and j + 8; dense: channels 16 s + 2 i, + 1, + 8, + 9; 8 bits: the four at
@@ -266,10 +280,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const Args a, con
           m[e] = top;
           l[e] *= f;
 #pragma unroll
-          for (int t = 0; t < kN; ++t) {
-            o[t][2 * e] *= f;
-            o[t][2 * e + 1] *= f;
-          }
+          for (int t = 0; t < kN; ++t)
+#pragma unroll
+            for (int x = HALF ? 0 : 2 * e; x < (HALF ? 4 : 2 * e + 2); ++x) o[t][x] *= f;
         }
         float sum = 0.f;
 #pragma unroll
@@ -281,27 +294,24 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const Args a, con
           }
         l[e] += sum;
       }
-      if constexpr (HALF)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) c[t][2] = c[t][3] = 0.f;
     };
-    // Two key tiles' weights as the A operands of the second product, part by part.
+    // Two key tiles' weights as the A operands of the second product, part by part. Of up to eight rows the second parts are
+    // rows eight and on, so that one product takes both and O's upper half is what they add.
     auto operands = [&](float (&x)[4], float (&y)[4], uint32_t (&p)[2][4]) {
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        p[part][0] = part ? pack2(x[0], x[1]) : split2(x[0], x[1]);
-        p[part][2] = part ? pack2(y[0], y[1]) : split2(y[0], y[1]);
-        if constexpr (HALF) {
-          p[part][1] = p[part][3] = 0u;
-        } else {
-          p[part][1] = part ? pack2(x[2], x[3]) : split2(x[2], x[3]);
-          p[part][3] = part ? pack2(y[2], y[3]) : split2(y[2], y[3]);
-        }
+      p[0][0] = split2(x[0], x[1]);
+      p[0][2] = split2(y[0], y[1]);
+      p[HALF ? 0 : 1][HALF ? 1 : 0] = pack2(x[0], x[1]);
+      p[HALF ? 0 : 1][HALF ? 3 : 2] = pack2(y[0], y[1]);
+      if constexpr (!HALF) {
+        p[0][1] = split2(x[2], x[3]);
+        p[0][3] = split2(y[2], y[3]);
+        p[1][1] = pack2(x[2], x[3]);
+        p[1][3] = pack2(y[2], y[3]);
       }
     };
     auto mma_p = [&](float (&c)[4], const uint32_t (&p)[2][4], uint32_t b0, uint32_t b1) {
       mma(c, p[0][0], p[0][1], p[0][2], p[0][3], b0, b1);
-      mma(c, p[1][0], p[1][1], p[1][2], p[1][3], b0, b1);
+      if constexpr (!HALF) mma(c, p[1][0], p[1][1], p[1][2], p[1][3], b0, b1);
     };
 
     // this warp's first tile of the segment: tiles of the share go to the warps in turn
@@ -445,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const Args a, con
           if (drafted) {
 #pragma unroll
             for (int e = 0; e < kH; ++e) {
-              const int r = j + 8 * e, token = r % n;
+              const int r = j + 8 * e, token = (first_row + r) % n;
               const uint8_t* see = a.mask ? a.mask + here.seq * a.mask_stride + (int64_t)token * a.tokens : nullptr;
 #pragma unroll
               for (int t = 0; t < R / 8; ++t)
@@ -536,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const Args a, con
         float* const to = meet + (warp % 2 * kRows + r) * D;
 #pragma unroll
         for (int t = 0; t < kN; ++t) {
-          const float x = o[t][2 * e] * f, y = o[t][2 * e + 1] * f;
+          const float x = (HALF ? o[t][0] + o[t][2] : o[t][2 * e]) * f, y = (HALF ? o[t][1] + o[t][3] : o[t][2 * e + 1]) * f;
           if constexpr (Q8) {
             float* const u = to + kN * 2 * i + t;
             u[0] = add ? u[0] + x : x;
@@ -588,11 +598,14 @@ template <bool Q8, int D, bool HALF> cudaError_t launch_typed(const TreeJob& job
   if (!tree_maps(&maps, job, S::kTile, S::kNew)) return cudaErrorInvalidValue;
   cudaError_t err = allow_dynamic_smem<tree_mma_kernel<Q8, D, HALF>>(S::smem());
   if (err != cudaSuccess) return err;
-  err = tree_fill(a, job, S::kTile, S::kNew, 2 * (int64_t)device_sm_count());
+  // Passes over the same rows side by side (where tokens differ, some siblings would have nothing to do).
+  const int64_t passes = ((int64_t)a.group * a.tokens + S::kRows - 1) / S::kRows, ctas = 2 * (int64_t)device_sm_count();
+  if (!job.n_new && passes > 1 && 4 * passes <= ctas) a.siblings = (int)passes;
+  err = tree_fill(a, job, S::kTile, S::kNew, ctas - ctas % a.siblings);
   if (err != cudaSuccess) return err;
   tree_mma_kernel<Q8, D, HALF><<<a.ctas, kThreads, S::smem(), job.stream>>>(a, maps);
   err = cudaGetLastError();
-  return err != cudaSuccess ? err : launch_tree_join<__nv_bfloat16, D, S::kTile, S::kNew>(a, job.stream);
+  return err != cudaSuccess || a.direct ? err : launch_tree_join<__nv_bfloat16, D, S::kTile, S::kNew>(a, job.stream);
 }
 
 template <bool Q8, int D> cudaError_t launch_dim(const TreeJob& job) {

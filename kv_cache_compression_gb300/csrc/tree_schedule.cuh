@@ -37,6 +37,7 @@ struct Args {
   int tile_q;           // query rows of a pass (of a part)
   int ctas, siblings;   // of the first launch; shares = ctas / siblings
   int least;            // tiles that a share has at least, where there are as many
+  bool direct;          // a CTA per head, which finishes it: no list, workspace or joining launch
   // workspace
   int64_t* upto;        // [batch + 1]: tiles in the sequences before, and in all
   int4* cuts;           // [shares][2]: (sequence, head, pass, tile), (tiles, tokens, -, -) where a share is the first to begin
@@ -199,6 +200,34 @@ __device__ __forceinline__ int pass_of(const Args& a, const Place& p) {
 
 template <int D> __device__ __forceinline__ float* part_at(const Args& a, int cta, int slot) {
   return a.parts + ((int64_t)cta * 2 + slot) * a.tile_q * (D + 2);
+}
+
+// A query head's tokens `first` and later: zeros, and lse -inf (all threads of a block).
+template <typename IO, int D, int THREADS> __device__ __forceinline__ void write_zeros(const Args& a, int64_t q_head, int first) {
+  const int64_t at = q_head * a.tokens + first;
+  const int none = a.tokens - first;
+  uint4* const out = reinterpret_cast<uint4*>(static_cast<IO*>(a.out) + at * D);
+  for (int u = threadIdx.x; u < none * (D * (int)sizeof(IO) / 16); u += THREADS) out[u] = make_uint4(0u, 0u, 0u, 0u);
+  if (a.lse)
+    for (int u = threadIdx.x; u < none; u += THREADS) a.lse[at + u] = -INFINITY;
+}
+
+// A direct call: this CTA's head as a share of its own, at its first tile in `p`; what is out of range is reported and what
+// nobody computes is written. False: nothing is left to do.
+template <typename IO, int D, int TILE, int NEW, int THREADS> __device__ __forceinline__ bool direct_share(const Args& a, Share& share, Place& p) {
+  p.seq = (int)blockIdx.x / a.heads;
+  p.head = (int)blockIdx.x - p.seq * a.heads;
+  p.pass = p.tile = 0;
+  p.s = seq_of<TILE, NEW>(a, p.seq);
+  share = Share{0, p.s.tiles, 0, 0, p.seq};
+  if (p.head == 0 && threadIdx.x == 0) {
+    if ((int64_t)a.len[p.seq] > a.cap) report(a.dev_status, SNAPKV_ERR_CAPACITY);
+    if (a.n_new && (a.n_new[p.seq] < 0 || a.n_new[p.seq] > a.tokens)) report(a.dev_status, SNAPKV_ERR_INVALID_ARG);
+  }
+  const int first = p.s.tiles == 0 ? 0 : p.s.n;
+  if (first < a.tokens)
+    for (int g = 0; g < a.group; ++g) write_zeros<IO, D, THREADS>(a, (int64_t)blockIdx.x * a.group + g, first);
+  return p.s.tiles > 0;
 }
 
 // What sums that belong to maximum m are multiplied by under the maximum `top` (of at least m).

@@ -135,9 +135,15 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
   auto k_hash = [](int row) { return (row / kRk) & 7; };
   auto v_hash = [](int) { return 0; };
   __shared__ ShareScratch<kThreads> scratch;
-  const Share share = find_share<kTile, kTile, kThreads>(a, scratch);
-  if (share.at >= share.end) return;
-  Place here = first_place<kTile, kTile>(a, share);
+  Share share;
+  Place here;
+  if (a.direct) {
+    if (!direct_share<IO, D, kTile, kTile, kThreads>(a, share, here)) return;
+  } else {
+    share = find_share<kTile, kTile, kThreads>(a, scratch);
+    if (share.at >= share.end) return;
+    here = first_place<kTile, kTile>(a, share);
+  }
   // first product: rows kRq qg .. by keys kRk kg ..
   const int qg = tid % S::kQg, kg = tid / S::kQg;
   // second product: rows 4 og .. by channels 4 cg .. of the keys of group kh
@@ -334,7 +340,7 @@ template <typename IO, bool Q8, int D, int QT> cudaError_t launch_typed(const Tr
   if (err != cudaSuccess) return err;
   tree_simt_kernel<IO, Q8, D, QT><<<a.ctas, kThreads, S::smem(), job.stream>>>(a);
   err = cudaGetLastError();
-  return err != cudaSuccess ? err : launch_tree_join<IO, D, kTile, kTile>(a, job.stream);
+  return err != cudaSuccess || a.direct ? err : launch_tree_join<IO, D, kTile, kTile>(a, job.stream);
 }
 
 template <typename IO, bool Q8, int D> cudaError_t launch_dim(const TreeJob& job) {

@@ -13,8 +13,7 @@ from functools import lru_cache
 import torch
 
 from . import snapkv as _sk
-from .cache import _call as _call_known
-from .cache import _check, _code, _functions, _new_lengths, _on_stream, _room, _status
+from .cache import _call, _check, _code, _functions, _loaders, _new_lengths, _on_stream, _room, _status
 from .snapkv import ERR_INVALID_ARG, SnapKVError
 
 _INT32, _FP32, _BF16, _BYTE = torch.int32, torch.float32, torch.bfloat16, torch.uint8
@@ -49,10 +48,7 @@ def lib():
     return L
 
 
-def _call(name, device, *args):
-    if name not in _functions:
-        lib()
-    _call_known(name, device, *args)
+_loaders.append(lib)
 
 
 class Q8Cache:

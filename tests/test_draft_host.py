@@ -36,6 +36,7 @@ def test_every_declared_function_is_exported(lib):
 
 def test_workspace_sizes(lib):
     size = kd.tree_workspace_size
+    assert size(2, 8, 4, 128, 8, 256) == 0 and size(2, 8, 4, 128, 9, 256) > 0 and size(2, 8, 4, 128, 8, 257) > 0   # short: none
     assert size(2, 8, 4, 128, 5, 1000) > 0 and size(2, 8, 4, 128, 5, 1000) % 256 == 0
     assert size(64, 32, 32, 128, 64, 1 << 30) < 64 << 20          # bounded, whatever the cache's length
     for bad in ((0, 8, 4, 128, 5, 9), (2, 9, 4, 128, 5, 9), (2, 8, 4, 96, 5, 9), (2, 8, 4, 128, 0, 9), (2, 8, 4, 128, 5, 0),

@@ -89,7 +89,8 @@ typedef struct {
 /*
  * snapkv_q8_tree_attend — snapkv_tree_attend over an 8-bit cache: K_cache[r] and V_cache[r] are the values that the
  * rows stand for. dtype is that of q, k_new, v_new and out; arguments and workspace as there. bf16 queries must be below
- * 2^48 in size and their products with drafted rows below 2^62 (queries are scaled on their way to the tensor cores).
+ * 2^48 in size and their products with drafted rows below 2^62 (queries are scaled on their way to the tensor cores, and
+ * outputs on their way back: what a row adds to an output below 2^-96 is lost).
  */
 SNAPKV_API snapkv_status snapkv_q8_tree_attend(const void* q, const snapkv_q8_cache* cache, const int32_t* len,
                                                const void* k_new, const void* v_new, const int32_t* n_new,

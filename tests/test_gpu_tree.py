@@ -5,7 +5,7 @@ import torch
 
 import kv_cache_compression_gb300 as kv
 from tests.cache_cases import to64
-from tests.draft_cases import check_tree, q8_rows, random_tree
+from tests.draft_cases import Q8_FLOOR, check_tree, q8_rows, random_tree
 
 pytestmark = pytest.mark.gpu
 
@@ -46,7 +46,8 @@ def run(x, lens, *, drafts=True, mask=None, n_new=None, lse=True, **kw):
 
 def check(x, lens, out, lse, *, drafts=True, mask=None, n_new=None, **kw):
     new = dict(k_new=x["k_new"], v_new=x["v_new"], mask=mask) if drafts else {}
-    check_tree(x["q"], x["k64"], x["v64"], lens, out, lse, n_new=n_new, **new, **kw)
+    floor = Q8_FLOOR if "k_codes" in x and out.dtype == BF16 else 0.0
+    check_tree(x["q"], x["k64"], x["v64"], lens, out, lse, n_new=n_new, floor=floor, **new, **kw)
 
 
 SHAPES = [  # B, H, G, d, T, cap, lengths

@@ -110,8 +110,7 @@ __device__ __forceinline__ void load_rows(float* to, const void* from, const flo
 
 template <int D, int QT> struct Shape {
   static constexpr int kRq = QT == 32 ? 4 : 2, kRk = QT == 32 ? 2 : 1;      // logits of a thread: rows by keys
-  static constexpr int kQg = QT / kRq;                                      // threads along the rows
-  static_assert(kQg * (kTile / kRk) == kThreads, "a thread for every block of logits");
+  static_assert(QT / kRq * (kTile / kRk) == kThreads, "a thread for every block of logits");
   static constexpr int kKs = kThreads * 16 / (QT * D);                      // key groups of the second product
   static constexpr int kPs = QT + 4;                                        // floats between two keys' weights
   static constexpr int smem() { return 4 * (QT * D + 2 * kTile * D + kTile * kPs + 3 * QT); }
@@ -144,8 +143,10 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
     if (share.at >= share.end) return;
     here = first_place<kTile, kTile>(a, share);
   }
-  // first product: rows kRq qg .. by keys kRk kg ..
-  const int qg = tid % S::kQg, kg = tid / S::kQg;
+  // first product: rows kRq qg .. by keys kRk kg .. (a warp has eight rows, so that where there are fewer rows some rest)
+  constexpr int kWarpQg = 8 / kRq, kWarpKg = 32 / kWarpQg;   // of a warp's lanes
+  constexpr int kRowWarps = QT / 8;                          // warps along the rows
+  const int qg = warp % kRowWarps * kWarpQg + lane % kWarpQg, kg = warp / kRowWarps * kWarpKg + lane / kWarpQg;
   // second product: rows 4 og .. by channels 4 cg .. of the keys of group kh
   const int kh = tid / (kThreads / kKs), in = tid % (kThreads / kKs);
   constexpr int kOg = QT / 4;
@@ -188,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
       cp_wait<1>();
       __syncthreads();   // K and Q are there
       // ---- logits
+      if (qg / kWarpQg * 8 < count) {
       float2 s[kRq][kRk];
 #pragma unroll
       for (int x = 0; x < kRq; ++x)
@@ -228,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
         else
           *reinterpret_cast<float2*>(ps + key * kPs + 2 * qg) = make_float2(l[0], l[1]);
       }
+      }
       __syncthreads();   // the logits are there, and K's buffer is free
       const Rows now = tile;
       if (j + 1 < seg) {
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
       }
       cp_commit();
       // ---- weights: eight lanes a row
-      for (int r = warp * 4 + lane % 4; r < QT; r += 32) {
+      for (int r = warp * 4 + lane % 4; r < QT && warp * 4 < count; r += 32) {
         float* p = ps + (lane / 4) * kPs + r;
         float x[kTile / 8], top = kNoMax;
 #pragma unroll
@@ -270,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
       cp_wait<1>();
       __syncthreads();   // the weights and V are there
       // ---- outputs
+      if (kOw * 4 * (in / (kOw * (D / 4))) < count) {   // (a warp has 4 kOw rows)
       const float4 f = *reinterpret_cast<const float4*>(fs + 4 * og);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -294,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
             o[r][1] = fma2(ww, make_float2(v.z, v.w), o[r][1]);
           }
         }
+      }
       }
       __syncthreads();   // V's buffer and the weights are free
     }

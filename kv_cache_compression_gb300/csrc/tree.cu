@@ -17,11 +17,15 @@ int64_t most_tiles(int batch, int heads, int64_t passes, int tokens, int64_t cap
 }
 
 size_t upto_bytes(int batch) { return up(((size_t)batch + 1) * sizeof(int64_t)); }
-// Short caches of few rows leave a head to one CTA, in one launch and without workspace (4 heads of 83 fp32 rows: 9 us with a list and
-// a joining launch).
+// Short caches of few rows leave a head to one CTA, in one launch and without workspace: 4 heads of 83 fp32 rows take 5.8 us, and 9
+// with a list and a joining launch.
 bool is_direct(int64_t rows, int64_t cap) { return rows <= 16 && cap <= 256; }
 
-constexpr int kMmaRowsQ8 = 32;
+// Query rows a KV head up to which bf16 calls take mma.sync. Dense caches: a pass of it, which memory bounds (sixteen rows over
+// 131072 keys of eight heads 92 us, where 32 rows on tcgen05 take 95; two passes would read everything twice). 8-bit caches: two
+// passes, of which the second reads from L2, against tcgen05's unpacking into shared memory: 32 rows over 131072 keys 107 us
+// against 127, 64 x 32 heads of 20 rows 550 against 678; but 64 rows 199 against 128.
+constexpr int kMmaRows = 16, kMmaRowsQ8 = 32;
 constexpr size_t kCutBytes = (size_t)kMaxTreeCtas * 2 * sizeof(int4);
 static_assert(kCutBytes % 256 == 0, "parts follow");
 
@@ -38,7 +42,7 @@ size_t tree_workspace_bytes(int batch, int q_heads, int heads, int head_dim, int
   if (is_direct(rows, cap)) return 0;
   const int simt = rows <= 8 ? 8 : kSimtRows;
   size_t parts = parts_bytes(bounded(most_tiles(batch, heads, (rows + simt - 1) / simt, tokens, cap, 16, 16), kMaxTreeCtas), simt, head_dim);
-  if (rows > 16) {
+  if (rows > kMmaRows) {
     const int wide = rows <= 128 ? 128 : 256;
     const size_t tc = parts_bytes(bounded(most_tiles(batch, heads, (rows + wide - 1) / wide, tokens, cap, 128, 128), kMaxTcCtas), wide, head_dim);
     parts = tc > parts ? tc : parts;
@@ -81,7 +85,7 @@ cudaError_t tree_fill(tree::Args& a, const TreeJob& job, int tile, int fresh, in
     return cudaSuccess;
   }
   const int64_t rows = (int64_t)a.group * a.tokens, passes = (rows + a.tile_q - 1) / a.tile_q;
-  a.ctas = (int)bounded(ctas, most_tiles(a.batch, a.heads, passes, a.tokens, a.cap, tile, fresh));
+  a.ctas = (int)bounded(bounded(ctas, kMaxTreeCtas), most_tiles(a.batch, a.heads, passes, a.tokens, a.cap, tile, fresh));
   a.ctas -= a.ctas % a.siblings;
   char* ws = static_cast<char*>(job.workspace);
   a.upto = reinterpret_cast<int64_t*>(ws);
@@ -127,7 +131,7 @@ bool tree_maps(TreeMaps* maps, const TreeJob& job, int tile, int fresh) {
 cudaError_t launch_tree(const TreeJob& job) {
   if (job.dtype == SNAPKV_F32) return launch_tree_simt(job);
   const int64_t rows = (int64_t)(job.q_heads / job.heads) * job.tokens;
-  return rows <= (job.k_step ? kMmaRowsQ8 : 16) ? launch_tree_mma(job) : launch_tree_tc(job);
+  return rows <= (job.k_step ? kMmaRowsQ8 : kMmaRows) ? launch_tree_mma(job) : launch_tree_tc(job);
 }
 
 }  // namespace snapkv

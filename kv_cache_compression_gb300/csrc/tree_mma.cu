@@ -1,5 +1,5 @@
-// Tree attention of up to sixteen query rows a KV head, bf16, over a dense cache or one in 8 bits (tree_schedule.cuh has
-// the schedule): few drafted tokens, or one.
+// Tree attention of few query rows a KV head, bf16, over a dense cache (up to sixteen) or one in 8 bits (up to 32, in passes
+// of sixteen): one token, or a few drafted ones (tree_schedule.cuh has the schedule).
 //
 //   S = Q K^T,  P = exp2(S - m),  O = sum P V,  running m and sum per row
 //
@@ -7,12 +7,18 @@
 // sixteen rows take 768 clocks of it per 128 keys of 128 channels, in which HBM delivers 60 keys' bf16 rows or 119 in 8
 // bits. Unlike tcgen05.mma it takes codes and weights from registers, where unpacking and the softmax leave them.
 // Every warp walks tiles of its own (TMA into a ring of its own) with its own m, sum and O; at the end of a head the four
-// warps meet in shared memory.
+// warps meet in shared memory. Two CTAs an SM: with 225 to 255 registers a thread there is room for no third.
 //
-// Weights enter the second product in two bf16 parts (16 bits). 8-bit codes become operands by one byte permute and one
-// AND per two values, as *subnormal* bf16: sign and seven magnitude bits are u 2^-133, which mma.sync multiplies
-// exactly. The powers of two are made up for where it costs nothing: queries are scaled by 2^64, weights by 2^80. A step
-// multiplies its key's logits and weights.
+// Weights enter the second product in two bf16 parts (16 bits): of up to eight rows (HALF) the second parts are the other
+// eight rows of the same product, so that they cost nothing (a token over 131072 8-bit rows 178 -> 173 us). 8-bit codes
+// become operands by one byte permute and one AND per two values, as *subnormal* bf16: sign and seven magnitude bits are
+// u 2^-133, which mma.sync multiplies exactly. The powers of two are made up for where it costs nothing: queries are
+// scaled by 2^64, weights by 2^80. A step multiplies its key's logits and weights.
+//
+// Measured (128 channels): one token over 32 heads of 131072 8-bit rows 170 us, 6.5 TB/s; 64 x 32 heads of 2208 8-bit rows, up
+// to six tokens each, 215 us, 5.4 TB/s (its joining launch and uneven ends); 64 x 32 heads of 2140 bf16 rows, four tokens,
+// 350 us, 6.4 TB/s; 32 heads of 1057 bf16 rows, eight tokens, 16 us, which is latency of two launches. Bytes bound it, and
+// over 8-bit rows the permutes come next (ALU 39 %).
 #include "tree_schedule.cuh"
 
 #include <type_traits>

@@ -5,9 +5,13 @@
 // A CTA walks its share of the 64-key tiles with an online softmax: products of QT query rows with a tile's keys (each
 // thread some rows by some keys, channels in steps of four), weights through shared memory, and products with the
 // tile's values (each thread four rows by four channels of a KS-th of the keys). Products and sums are fp32 FMAs that
-// round to nearest, which tensor cores do not: their cut sums and three bf16 parts an operand would cost six products.
-// K's and V's tiles have a buffer each: V's rows are under way while the logits are computed, the next K's while the
-// outputs are, and a second CTA per SM fills the rest.
+// round to nearest. K's and V's tiles have a buffer each: V's rows are under way while the logits are computed, the next
+// K's while the outputs are, and a second CTA per SM fills the rest.
+//
+// Measured (128 channels): 8 x 8 KV heads of 28 rows over 8192 keys, half of the sequences shorter, 201 us, 2.0 TB/s: loads from
+// shared memory take 58 % of its clocks, FMAs and the rest of the instructions 49 % of the schedulers', and the barriers between a
+// tile's steps keep them apart; eight rows 145 us, 3.6 TB/s. Three bf16 parts an operand on mma.sync (six products, as accurate)
+// took 214 us for the 28 rows and 155 for eight, blocks of 4 x 4 logits and 8 x 4 outputs a thread 210 and 140.
 #include "tree_schedule.cuh"
 
 #include <atomic>
@@ -190,46 +194,46 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
       __syncthreads();   // K and Q are there
       // ---- logits
       if (qg / kWarpQg * 8 < count) {
-      float2 s[kRq][kRk];
-#pragma unroll
-      for (int x = 0; x < kRq; ++x)
-#pragma unroll
-        for (int y = 0; y < kRk; ++y) s[x][y] = make_float2(0.f, 0.f);
-#pragma unroll 4
-      for (int c = 0; c < D / 4; ++c) {
-        float4 qv[kRq], kv[kRk];
-#pragma unroll
-        for (int x = 0; x < kRq; ++x) qv[x] = *reinterpret_cast<const float4*>(qs + (kRq * qg + x) * D + 4 * (c ^ (qg & 7)));
-#pragma unroll
-        for (int y = 0; y < kRk; ++y) kv[y] = *reinterpret_cast<const float4*>(ks + (kRk * kg + y) * D + 4 * (c ^ (kg & 7)));
+        float2 s[kRq][kRk];
 #pragma unroll
         for (int x = 0; x < kRq; ++x)
 #pragma unroll
-          for (int y = 0; y < kRk; ++y) {
-            s[x][y] = fma2(make_float2(qv[x].x, qv[x].y), make_float2(kv[y].x, kv[y].y), s[x][y]);
-            s[x][y] = fma2(make_float2(qv[x].z, qv[x].w), make_float2(kv[y].z, kv[y].w), s[x][y]);
-          }
-      }
+          for (int y = 0; y < kRk; ++y) s[x][y] = make_float2(0.f, 0.f);
+#pragma unroll 4
+        for (int c = 0; c < D / 4; ++c) {
+          float4 qv[kRq], kv[kRk];
 #pragma unroll
-      for (int y = 0; y < kRk; ++y) {
-        const int key = kRk * kg + y;
-        float l[kRq];
+          for (int x = 0; x < kRq; ++x) qv[x] = *reinterpret_cast<const float4*>(qs + (kRq * qg + x) * D + 4 * (c ^ (qg & 7)));
 #pragma unroll
-        for (int x = 0; x < kRq; ++x) {
-          l[x] = (s[x][y].x + s[x][y].y) * a.scale_log2;
-          bool seen = key < tile.count;
-          if (tile.draft0 >= 0 && seen) {
-            const int i = kRq * qg + x;
-            const int t = (r0 + i) % n, k = tile.draft0 + key;
-            seen = i < count && (a.mask ? a.mask[here.seq * a.mask_stride + (int64_t)t * a.tokens + k] != 0 : k <= t);
-          }
-          if (!seen) l[x] = -INFINITY;
+          for (int y = 0; y < kRk; ++y) kv[y] = *reinterpret_cast<const float4*>(ks + (kRk * kg + y) * D + 4 * (c ^ (kg & 7)));
+#pragma unroll
+          for (int x = 0; x < kRq; ++x)
+#pragma unroll
+            for (int y = 0; y < kRk; ++y) {
+              s[x][y] = fma2(make_float2(qv[x].x, qv[x].y), make_float2(kv[y].x, kv[y].y), s[x][y]);
+              s[x][y] = fma2(make_float2(qv[x].z, qv[x].w), make_float2(kv[y].z, kv[y].w), s[x][y]);
+            }
         }
-        if constexpr (kRq == 4)
-          *reinterpret_cast<float4*>(ps + key * kPs + 4 * qg) = make_float4(l[0], l[1], l[2], l[3]);
-        else
-          *reinterpret_cast<float2*>(ps + key * kPs + 2 * qg) = make_float2(l[0], l[1]);
-      }
+#pragma unroll
+        for (int y = 0; y < kRk; ++y) {
+          const int key = kRk * kg + y;
+          float l[kRq];
+#pragma unroll
+          for (int x = 0; x < kRq; ++x) {
+            l[x] = (s[x][y].x + s[x][y].y) * a.scale_log2;
+            bool seen = key < tile.count;
+            if (tile.draft0 >= 0 && seen) {
+              const int i = kRq * qg + x;
+              const int t = (r0 + i) % n, k = tile.draft0 + key;
+              seen = i < count && (a.mask ? a.mask[here.seq * a.mask_stride + (int64_t)t * a.tokens + k] != 0 : k <= t);
+            }
+            if (!seen) l[x] = -INFINITY;
+          }
+          if constexpr (kRq == 4)
+            *reinterpret_cast<float4*>(ps + key * kPs + 4 * qg) = make_float4(l[0], l[1], l[2], l[3]);
+          else
+            *reinterpret_cast<float2*>(ps + key * kPs + 2 * qg) = make_float2(l[0], l[1]);
+        }
       }
       __syncthreads();   // the logits are there, and K's buffer is free
       const Rows now = tile;
@@ -274,31 +278,31 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
       __syncthreads();   // the weights and V are there
       // ---- outputs
       if (kOw * 4 * (in / (kOw * (D / 4))) < count) {   // (a warp has 4 kOw rows)
-      const float4 f = *reinterpret_cast<const float4*>(fs + 4 * og);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float fr = r == 0 ? f.x : r == 1 ? f.y : r == 2 ? f.z : f.w;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) o[r][c] = mul2(o[r][c], make_float2(fr, fr));
-      }
-      // A row that nobody may see (or that is masked) has weight zero, but its values may be anything: a drafted
-      // row's infinity or NaN must not reach the rows that do not see it.
-      const bool careful = now.draft0 >= 0;
-#pragma unroll 4
-      for (int e = 0; e < kTile / kKs; ++e) {
-        const int key = kh + e * kKs;
-        const float4 w = *reinterpret_cast<const float4*>(ps + key * kPs + 4 * og);
-        const float4 v = *reinterpret_cast<const float4*>(vs + key * D + 4 * cg);
-        const float wr[4] = {w.x, w.y, w.z, w.w};
+        const float4 f = *reinterpret_cast<const float4*>(fs + 4 * og);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float2 ww = make_float2(wr[r], wr[r]);
-          if (!careful || wr[r] != 0.f) {
-            o[r][0] = fma2(ww, make_float2(v.x, v.y), o[r][0]);
-            o[r][1] = fma2(ww, make_float2(v.z, v.w), o[r][1]);
+          const float fr = r == 0 ? f.x : r == 1 ? f.y : r == 2 ? f.z : f.w;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) o[r][c] = mul2(o[r][c], make_float2(fr, fr));
+        }
+        // A row that nobody may see (or that is masked) has weight zero, but its values may be anything: a drafted
+        // row's infinity or NaN must not reach the rows that do not see it.
+        const bool careful = now.draft0 >= 0;
+#pragma unroll 4
+        for (int e = 0; e < kTile / kKs; ++e) {
+          const int key = kh + e * kKs;
+          const float4 w = *reinterpret_cast<const float4*>(ps + key * kPs + 4 * og);
+          const float4 v = *reinterpret_cast<const float4*>(vs + key * D + 4 * cg);
+          const float wr[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float2 ww = make_float2(wr[r], wr[r]);
+            if (!careful || wr[r] != 0.f) {
+              o[r][0] = fma2(ww, make_float2(v.x, v.y), o[r][0]);
+              o[r][1] = fma2(ww, make_float2(v.z, v.w), o[r][1]);
+            }
           }
         }
-      }
       }
       __syncthreads();   // V's buffer and the weights are free
     }

@@ -4,19 +4,28 @@
 //   S = Q K^T,  P = exp2(S - m),  O = sum P V,  running m and sum per row
 //
 // tcgen05 with 128 query rows by 128 keys: S (fp32) and O stand in TMEM, P goes back over S as the second product's A
-// operand, K and V are B operands in shared memory. Two slots, each an S, an O and four softmax warps (a thread per row),
-// keep the tensor cores busy while the other slot's weights are computed. Up to 128 rows (TWO false) both slots serve the
-// same rows and take the key tiles in turn, and their halves of O meet at the head's end; up to 256 a slot has 128 rows
-// each and every key tile serves both, so that the cache is read once. MMAs are issued in the order P V of a tile, then
-// Q K^T of the slot's next, which overwrites what P V has read: the tensor core takes them one after the other.
+// operand, K and V are B operands in shared memory. Two slots, each an S, an O and its softmax warps, keep the tensor
+// cores busy while the other slot's weights are computed. Up to 128 rows (TWO false) both slots serve the same rows and
+// take the key tiles in turn, each from a ring of its own, and their halves of O meet at the head's end; up to 256 a slot
+// has 128 rows each and every key tile serves both, so that the cache is read once. More rows are passes, side by side
+// where all sequences have as many. A slot issues P V of a tile and Q K^T of its next as one block (S is overwritten when
+// P V has read P: the tensor core takes them one after the other), and passes the turn on.
 //
-// Weights enter the second product in two bf16 parts (16 bits), P V twice as long as Q K^T: 1536 clocks for a tile of 128
-// channels, in which HBM delivers 70 keys' bf16 rows. A row's maximum is only raised, and its O rescaled, when it would
-// grow by more than 2^8; sums and outputs stay under the same maximum, so that nothing is lost.
+// Weights enter the second product as one bf16 value, rounded by half a step (2^-8); they are summed up as they were. A
+// second part for what the rounding leaves made P V twice as long: 169 us instead of 142 where 4 x 8 KV heads, 256 rows
+// each, read 32768 keys. A row's maximum is only raised, and its O rescaled, when it would grow by more than 2^8; sums
+// and outputs stay under the same maximum, so that nothing is lost.
 //
-// 8-bit rows arrive as they are; four more warps unpack them into the tiles that TMA writes for bf16 rows. As operands
-// they are *subnormal* bf16 (sign and seven magnitude bits, u 2^-133: a byte permute and an AND per two values), for
-// which queries are scaled by 2^64 and weights by 2^80; a step multiplies its key's logits and weights.
+// Measured (128 channels): 4 x 8 KV heads of 256 rows over 32768 keys 126 us, 1040 TFLOP/s; 8 x 8 heads of 64 rows over 16384
+// keys, half of the sequences shorter, 85 us, 4.8 TB/s. With up to 128 rows a KV head memory bounds it; with more, a slot's
+// way from S to P and back: 256 rows by 128 keys take 5600 clocks, of which the tensor cores are busy for 36 %, ex2 for 19 %
+// and the schedulers for 31 %. (1024 rows of 64 channels over 1500 keys, 84 us: the same way, half of the products.)
+// 8-bit rows arrive as they are; eight more warps unpack them into the tiles that TMA writes for bf16 rows (four: 134 us
+// instead of 116 for 128 rows a KV head over 8 x 8 heads of 16384 keys). As operands they are *subnormal* bf16 (sign and
+// seven magnitude bits, u 2^-133: a byte permute and an AND per two values), for which queries are scaled by 2^64 and
+// weights by 2^80; a step multiplies its key's logits and weights. The instructions of unpacking and softmax bound it: the
+// schedulers are busy for 42 % of a tile's time, the tensor cores for 20 %. More softmax warps (139 us), straight code for
+// whole tiles (127 us) and smaller pieces of a tile (128 us) did not pay beside the unpacking warps.
 #include "tree_schedule.cuh"
 
 #include <type_traits>
@@ -87,16 +96,6 @@ template <bool Q8, int D, bool TWO> struct Shape {
   static constexpr int kColumns = 512;
 };
 
-__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
-      "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(at));
-}
 __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -269,212 +268,212 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
   constexpr uint32_t kPair = TWO ? 1 : 2;                    // they are loaded, K before V
 
   if (warp < 4) {
-  if constexpr (!Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kMoveRegs));
-  if (warp == 0) {
-    // ---- loads, in the order in which the products take them
-    if (lane == 0) {
-      Segments ks(a, share), vs(a, share);
-      int kf = 0, vf = 0;   // tiles of the segments so far
-      uint32_t sent = 0;    // raw ones (8 bits)
-      auto send = [&](Segments& s, int& f, uint32_t t, bool key) {   // K or V of the share's tile t
-        const int tile = s.p.tile + f, bh = s.p.seq * a.heads + s.p.head;
-        const bool cached = tile < s.p.s.cache_tiles;
-        if (!Q8 || cached) {   // (drafted rows beside an 8-bit cache are copied by the warps that unpack)
-          const uint32_t at = 2 * (TWO ? t : t / 2) + (key ? 0 : 1);
-          const uint32_t slot = Q8 ? sent % kRaws : S::stage(t & 1, at), turn = Q8 ? sent / kRaws : at / S::kTurn;
-          if (turn > 0 && !wait(Q8 ? &bars.raw_empty[slot] : &bars.kv_empty[slot], turn - 1)) return false;
-          uint64_t* const bar = Q8 ? &bars.raw_full[slot] : &bars.kv_full[slot];
-          uint8_t* const to = smem + (Q8 ? S::kRawRing + slot * S::kRaw : S::kRing + slot * S::kStage);
-          const CUtensorMap* const map = cached ? (key ? &maps.k : &maps.v) : (key ? &maps.k_new : &maps.v_new);
-          const int row0 = (cached ? tile : tile - s.p.s.cache_tiles) * kTile;
-          ptx::mbar_arrive_expect_tx(bar, Q8 ? S::kRaw : S::kStage);
+    if constexpr (!Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kMoveRegs));
+    if (warp == 0) {
+      // ---- loads, in the order in which the products take them
+      if (lane == 0) {
+        Segments ks(a, share), vs(a, share);
+        int kf = 0, vf = 0;   // tiles of the segments so far
+        uint32_t sent = 0;    // raw ones (8 bits)
+        auto send = [&](Segments& s, int& f, uint32_t t, bool key) {   // K or V of the share's tile t
+          const int tile = s.p.tile + f, bh = s.p.seq * a.heads + s.p.head;
+          const bool cached = tile < s.p.s.cache_tiles;
+          if (!Q8 || cached) {   // (drafted rows beside an 8-bit cache are copied by the warps that unpack)
+            const uint32_t at = 2 * (TWO ? t : t / 2) + (key ? 0 : 1);
+            const uint32_t slot = Q8 ? sent % kRaws : S::stage(t & 1, at), turn = Q8 ? sent / kRaws : at / S::kTurn;
+            if (turn > 0 && !wait(Q8 ? &bars.raw_empty[slot] : &bars.kv_empty[slot], turn - 1)) return false;
+            uint64_t* const bar = Q8 ? &bars.raw_full[slot] : &bars.kv_full[slot];
+            uint8_t* const to = smem + (Q8 ? S::kRawRing + slot * S::kRaw : S::kRing + slot * S::kStage);
+            const CUtensorMap* const map = cached ? (key ? &maps.k : &maps.v) : (key ? &maps.k_new : &maps.v_new);
+            const int row0 = (cached ? tile : tile - s.p.s.cache_tiles) * kTile;
+            ptx::mbar_arrive_expect_tx(bar, Q8 ? S::kRaw : S::kStage);
 #pragma unroll
-          for (int c = 0; c < (Q8 ? 1 : D / 64); ++c) ptx::tma_load_3d(to + c * kTile * 128, map, 64 * c, row0, bh, bar);
-          small.pending[slot] = (uint8_t)(1 + (turn & 1));
-          ++sent;
-        }
-        if (++f == s.tiles) {
-          f = 0;
-          s.next(a);
-        }
-        return true;
+            for (int c = 0; c < (Q8 ? 1 : D / 64); ++c) ptx::tma_load_3d(to + c * kTile * 128, map, 64 * c, row0, bh, bar);
+            small.pending[slot] = (uint8_t)(1 + (turn & 1));
+            ++sent;
+          }
+          if (++f == s.tiles) {
+            f = 0;
+            s.next(a);
+          }
+          return true;
+        };
+        bool ok = true;
+        for (uint32_t t = 0; ok && t < total; t += kPair)
+          for (int key = 1; ok && key >= 0; --key)
+            for (uint32_t u = t; ok && u < t + kPair && u < total; ++u) ok = key ? send(ks, kf, u, true) : send(vs, vf, u, false);
+        // Copies in flight land before the block ends, also after a wait ran out.
+        const int none = 0;
+        for (int i = 0; i < (Q8 ? kRaws : kStages); ++i)
+          if (small.pending[i]) ptx::mbar_wait(Q8 ? &bars.raw_full[i] : &bars.kv_full[i], small.pending[i] - 1, &none, kWaitLimit);
+      }
+    } else if (warp < 3) {
+      // ---- products of a slot. (One warp for both slots left the tensor core idle for 2000 of a tile's 5200 clocks, while it
+      // waited on barriers that had long been reached and counted: a product is issued no more than a few ahead.)
+      const int slot = warp - 1;
+      constexpr uint32_t kIdescQk = ptx::idesc_bf16_f32(128, kTile), kIdescPv = ptx::idesc_bf16_f32(128, D) | 1u << 16;   // (V: n-major)
+      const uint32_t leader = lane == 0;
+      const uint32_t s_at = uniform(tmem + S::kS(slot)), o_at = uniform(tmem + S::kO(slot));
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };   // (the warp stays together)
+      // The slots issue in turn: P V of a tile and Q K^T of the slot's next as a block, all that they wait for before. (Left to
+      // themselves both slots' products mix, and then both softmaxes run, and both products wait, at the same time; and a wait
+      // between products, even for a barrier long reached, leaves the tensor core idle.)
+      uint32_t steps = 0, turns = 0;   // P V of this slot, and turns, so far
+      auto my_turn = [&] {
+        const bool mine = slot == 0 && turns == 0 ? true : wait_all(&bars.turn[slot], slot == 0 ? turns - 1 : turns);
+        ++turns;
+        ptx::tc_fence_after();
+        return mine;
       };
-      bool ok = true;
-      for (uint32_t t = 0; ok && t < total; t += kPair)
-        for (int key = 1; ok && key >= 0; --key)
-          for (uint32_t u = t; ok && u < t + kPair && u < total; ++u) ok = key ? send(ks, kf, u, true) : send(vs, vf, u, false);
-      // Copies in flight land before the block ends, also after a wait ran out.
+      auto pass_on = [&] {
+        if (leader) ptx::mbar_arrive(&bars.turn[1 - slot]);
+        __syncwarp();
+      };
+      auto full = [&](uint32_t at) { return wait_all(&bars.kv_full[S::stage(slot, at)], at / S::kTurn); };
+      // S = Q K^T of the ring's tile `at`.
+      const uint32_t q_lo = uniform(k_desc(q_smem + (TWO ? slot : 0) * S::kSlotQ));
+      auto qk = [&](uint32_t at) {
+        const uint32_t k_lo = uniform(k_desc(ring + S::stage(slot, at) * S::kStage));
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint32_t off = ((s / 4) * (kTile * 128) + (s % 4) * 32) >> 4;
+          mma_ss(leader, s_at, q_lo + off, k_lo + off, kDescHigh, kIdescQk, s > 0);
+        }
+      };
+      // O += P V of the ring's tile `at`; `fresh`: O =.
+      auto pv = [&](uint32_t at, bool fresh) {
+        const uint32_t v_lo = uniform(v_desc(ring + S::stage(slot, at) * S::kStage));
+        constexpr int kHalf = kTile / S::kHalves / 16;   // (weights begin where their half's logits did)
+#pragma unroll
+        for (int s = 0; s < kTile / 16; ++s)
+          mma_ts(leader, o_at, s_at + s / kHalf * (kTile / S::kHalves) + s % kHalf * 8, v_lo + s * (2048 >> 4), kDescHigh, kIdescPv, !(fresh && s == 0));
+      };
+      // Walks of the Q K^T and of the P V, the first a tile of the slot's ahead. A slot waits for every segment's queries and outputs
+      // and counts in on q_empty and o_full at its end, whether it had tiles of it or not: barriers know a phase by its parity
+      // alone, so that none may be passed over. Up to 128 rows the slot's tiles are every second of the share; of more, all tiles,
+      // but of segments in whose rows it has no part it only lets the loads go on.
+      constexpr int kBy = TWO ? 1 : 2;
+      Segments qs(a, share), ps(a, share);
+      int qf = TWO ? 0 : slot, pf = qf;        // within the segments
+      uint32_t q_t = 0, p_t = 0;               // the slot's tiles so far
+      bool q_end = false, p_end = false, ok = true;
+      auto takes_part = [&](const Segments& s) { return !TWO || slot == 0 || rows_of(s) > kTile; };
+      bool q_mine = takes_part(qs), p_mine = q_mine;
+      auto queries = [&] { return wait_all(&bars.q_full, qs.index); };
+      auto outputs = [&] { return ps.index == 0 || wait_all(&bars.o_free, ps.index - 1); };
+      auto q_next = [&] {
+        qf -= qs.tiles;
+        commit(leader, &bars.q_empty);
+        q_end = !qs.next(a);
+        if (!q_end) q_mine = takes_part(qs);
+      };
+      auto p_next = [&] {
+        pf -= ps.tiles;
+        commit(leader, &bars.o_full);
+        p_end = !ps.next(a);
+        if (!p_end) p_mine = takes_part(ps);
+      };
+      for (bool begin = true; ok; begin = false) {
+        // what this turn's products need
+        if (!begin) {
+          while (ok && !p_end && pf >= ps.tiles) {   // a segment without tiles of the slot's
+            ok = outputs();
+            if (ok) p_next();
+          }
+          if (!ok || p_end) break;
+          ok = (pf >= kBy || outputs()) && full(2 * p_t + 1);   // (a segment's first tiles are its slots' first)
+          if (ok && p_mine) ok = wait_all(&bars.p_ready[slot], steps);
+        }
+        while (ok && !q_end && qf >= qs.tiles) {
+          ok = queries();
+          if (ok) q_next();
+        }
+        const bool more = !q_end;
+        if (ok && more) ok = (qf >= kBy || queries()) && full(2 * q_t);
+        if (!ok || !my_turn()) break;
+        if (!begin && p_mine) pv(2 * p_t + 1, pf < kBy);
+        if (more && q_mine) qk(2 * q_t);
+        pass_on();
+        // what waits for them
+        if (more && q_mine) commit(leader, &bars.s_full[slot]);
+        if (!begin) {
+          commit(leader, &bars.kv_empty[S::stage(slot, 2 * p_t + 1)]);
+          if (p_mine) ++steps;
+          ++p_t;
+          pf += kBy;
+          if (pf >= ps.tiles) p_next();
+        }
+        if (more) {
+          commit(leader, &bars.kv_empty[S::stage(slot, 2 * q_t)]);
+          ++q_t;
+          qf += kBy;
+          if (qf >= qs.tiles) q_next();
+        }
+      }
+      // Products in flight end before the block does.
+      commit(leader, &bars.drain[slot]);
       const int none = 0;
-      for (int i = 0; i < (Q8 ? kRaws : kStages); ++i)
-        if (small.pending[i]) ptx::mbar_wait(Q8 ? &bars.raw_full[i] : &bars.kv_full[i], small.pending[i] - 1, &none, kWaitLimit);
-    }
-  } else if (warp < 3) {
-    // ---- products of a slot. (One warp for both slots left the tensor core idle for 2000 of a tile's 5200 clocks, while it
-    // waited on barriers that had long been reached and counted: a product is issued no more than a few ahead.)
-    const int slot = warp - 1;
-    constexpr uint32_t kIdescQk = ptx::idesc_bf16_f32(128, kTile), kIdescPv = ptx::idesc_bf16_f32(128, D) | 1u << 16;   // (V: n-major)
-    const uint32_t leader = lane == 0;
-    const uint32_t s_at = uniform(tmem + S::kS(slot)), o_at = uniform(tmem + S::kO(slot));
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };   // (the warp stays together)
-    // The slots issue in turn: P V of a tile and Q K^T of the slot's next as a block, all that they wait for before. (Left to
-    // themselves both slots' products mix, and then both softmaxes run, and both products wait, at the same time; and a wait
-    // between products, even for a barrier long reached, leaves the tensor core idle.)
-    uint32_t steps = 0, turns = 0;   // P V of this slot, and turns, so far
-    auto my_turn = [&] {
-      const bool mine = slot == 0 && turns == 0 ? true : wait_all(&bars.turn[slot], slot == 0 ? turns - 1 : turns);
-      ++turns;
-      ptx::tc_fence_after();
-      return mine;
-    };
-    auto pass_on = [&] {
-      if (leader) ptx::mbar_arrive(&bars.turn[1 - slot]);
-      __syncwarp();
-    };
-    auto full = [&](uint32_t at) { return wait_all(&bars.kv_full[S::stage(slot, at)], at / S::kTurn); };
-    // S = Q K^T of the ring's tile `at`.
-    const uint32_t q_lo = uniform(k_desc(q_smem + (TWO ? slot : 0) * S::kSlotQ));
-    auto qk = [&](uint32_t at) {
-      const uint32_t k_lo = uniform(k_desc(ring + S::stage(slot, at) * S::kStage));
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        const uint32_t off = ((s / 4) * (kTile * 128) + (s % 4) * 32) >> 4;
-        mma_ss(leader, s_at, q_lo + off, k_lo + off, kDescHigh, kIdescQk, s > 0);
-      }
-    };
-    // O += P V of the ring's tile `at`; `fresh`: O =.
-    auto pv = [&](uint32_t at, bool fresh) {
-      const uint32_t v_lo = uniform(v_desc(ring + S::stage(slot, at) * S::kStage));
-      constexpr int kHalf = kTile / S::kHalves / 16;   // (weights begin where their half's logits did)
-#pragma unroll
-      for (int s = 0; s < kTile / 16; ++s)
-        mma_ts(leader, o_at, s_at + s / kHalf * (kTile / S::kHalves) + s % kHalf * 8, v_lo + s * (2048 >> 4), kDescHigh, kIdescPv, !(fresh && s == 0));
-    };
-    // Walks of the Q K^T and of the P V, the first a tile of the slot's ahead. A slot waits for every segment's queries and outputs
-    // and counts in on q_empty and o_full at its end, whether it had tiles of it or not: barriers know a phase by its parity
-    // alone, so that none may be passed over. Up to 128 rows the slot's tiles are every second of the share; of more, all tiles,
-    // but of segments in whose rows it has no part it only lets the loads go on.
-    constexpr int kBy = TWO ? 1 : 2;
-    Segments qs(a, share), ps(a, share);
-    int qf = TWO ? 0 : slot, pf = qf;        // within the segments
-    uint32_t q_t = 0, p_t = 0;               // the slot's tiles so far
-    bool q_end = false, p_end = false, ok = true;
-    auto takes_part = [&](const Segments& s) { return !TWO || slot == 0 || rows_of(s) > kTile; };
-    bool q_mine = takes_part(qs), p_mine = q_mine;
-    auto queries = [&] { return wait_all(&bars.q_full, qs.index); };
-    auto outputs = [&] { return ps.index == 0 || wait_all(&bars.o_free, ps.index - 1); };
-    auto q_next = [&] {
-      qf -= qs.tiles;
-      commit(leader, &bars.q_empty);
-      q_end = !qs.next(a);
-      if (!q_end) q_mine = takes_part(qs);
-    };
-    auto p_next = [&] {
-      pf -= ps.tiles;
-      commit(leader, &bars.o_full);
-      p_end = !ps.next(a);
-      if (!p_end) p_mine = takes_part(ps);
-    };
-    for (bool begin = true; ok; begin = false) {
-      // what this turn's products need
-      if (!begin) {
-        while (ok && !p_end && pf >= ps.tiles) {   // a segment without tiles of the slot's
-          ok = outputs();
-          if (ok) p_next();
+      ptx::mbar_wait(&bars.drain[slot], 0, &none, kWaitLimit);
+    } else {
+      // ---- queries into shared memory
+      const int at = lane;
+      Segments seg(a, share);
+      do {
+        if (seg.index > 0) wait(&bars.q_empty, seg.index - 1);
+        const int r0 = r0_of(seg), rows = rows_of(seg), n = seg.p.s.n;
+        const int64_t bh = (int64_t)seg.p.seq * a.heads + seg.p.head;
+        const int slots = TWO && rows > 128 ? 2 : 1;
+        if (!Q8 && (a.group == 1 || n == a.tokens)) {   // the rows follow one another: whole tiles, whatever lies behind the head's
+          if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(&bars.q_full, slots * S::kSlotQ);
+            const int row0 = (int)(bh * a.group * a.tokens) + r0;
+            for (int x = 0; x < slots; ++x)
+              for (int c = 0; c < D / 64; ++c) ptx::tma_load_3d(smem + S::kQ + x * S::kSlotQ + c * kTile * 128, &maps.q, 64 * c, row0 + x * kTile, 0, &bars.q_full);
+          }
+          continue;
         }
-        if (!ok || p_end) break;
-        ok = (pf >= kBy || outputs()) && full(2 * p_t + 1);   // (a segment's first tiles are its slots' first)
-        if (ok && p_mine) ok = wait_all(&bars.p_ready[slot], steps);
-      }
-      while (ok && !q_end && qf >= qs.tiles) {
-        ok = queries();
-        if (ok) q_next();
-      }
-      const bool more = !q_end;
-      if (ok && more) ok = (qf >= kBy || queries()) && full(2 * q_t);
-      if (!ok || !my_turn()) break;
-      if (!begin && p_mine) pv(2 * p_t + 1, pf < kBy);
-      if (more && q_mine) qk(2 * q_t);
-      pass_on();
-      // what waits for them
-      if (more && q_mine) commit(leader, &bars.s_full[slot]);
-      if (!begin) {
-        commit(leader, &bars.kv_empty[S::stage(slot, 2 * p_t + 1)]);
-        if (p_mine) ++steps;
-        ++p_t;
-        pf += kBy;
-        if (pf >= ps.tiles) p_next();
-      }
-      if (more) {
-        commit(leader, &bars.kv_empty[S::stage(slot, 2 * q_t)]);
-        ++q_t;
-        qf += kBy;
-        if (qf >= qs.tiles) q_next();
-      }
-    }
-    // Products in flight end before the block does.
-    commit(leader, &bars.drain[slot]);
-    const int none = 0;
-    ptx::mbar_wait(&bars.drain[slot], 0, &none, kWaitLimit);
-  } else {
-    // ---- queries into shared memory
-    const int at = lane;
-    Segments seg(a, share);
-    do {
-      if (seg.index > 0) wait(&bars.q_empty, seg.index - 1);
-      const int r0 = r0_of(seg), rows = rows_of(seg), n = seg.p.s.n;
-      const int64_t bh = (int64_t)seg.p.seq * a.heads + seg.p.head;
-      const int slots = TWO && rows > 128 ? 2 : 1;
-      if (!Q8 && (a.group == 1 || n == a.tokens)) {   // the rows follow one another: whole tiles, whatever lies behind the head's
-        if (lane == 0) {
-          ptx::mbar_arrive_expect_tx(&bars.q_full, slots * S::kSlotQ);
-          const int row0 = (int)(bh * a.group * a.tokens) + r0;
-          for (int x = 0; x < slots; ++x)
-            for (int c = 0; c < D / 64; ++c) ptx::tma_load_3d(smem + S::kQ + x * S::kSlotQ + c * kTile * 128, &maps.q, 64 * c, row0 + x * kTile, 0, &bars.q_full);
-        }
-        continue;
-      }
-      // A thread has every (32 / kPieces)-th row's piece c, all of them under way at a time. Rows follow one another in memory but for
-      // the tokens that a sequence does not have. (A warp alone: what it computes for a piece is what the load takes.)
-      constexpr int kPieces = D / 8, kStep = 32 / kPieces;
-      const int c = at % kPieces, first = at / kPieces;
-      int t = (r0 + first) % n;
-      const int64_t gap = (int64_t)(a.tokens - n) * D;
-      const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.q) + (bh * a.group + (r0 + first) / n) * a.tokens * D + (int64_t)t * D + 8 * c;
-      uint32_t place[8 / kStep];   // of rows first + e kStep, and of those 8, 16, ... further on but for a multiple of 1024
+        // A thread has every (32 / kPieces)-th row's piece c, all of them under way at a time. Rows follow one another in memory but for
+        // the tokens that a sequence does not have. (A warp alone: what it computes for a piece is what the load takes.)
+        constexpr int kPieces = D / 8, kStep = 32 / kPieces;
+        const int c = at % kPieces, first = at / kPieces;
+        int t = (r0 + first) % n;
+        const int64_t gap = (int64_t)(a.tokens - n) * D;
+        const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.q) + (bh * a.group + (r0 + first) / n) * a.tokens * D + (int64_t)t * D + 8 * c;
+        uint32_t place[8 / kStep];   // of rows first + e kStep, and of those 8, 16, ... further on but for a multiple of 1024
 #pragma unroll
-      for (int e = 0; e < 8 / kStep; ++e) place[e] = q_smem + piece_at(first + e * kStep, c);
+        for (int e = 0; e < 8 / kStep; ++e) place[e] = q_smem + piece_at(first + e * kStep, c);
 #pragma unroll 1
-      for (int x = 0; x < slots * kTile; x += 8) {
-        const uint32_t base = (x / kTile) * S::kSlotQ + (x % kTile) * 128;
+        for (int x = 0; x < slots * kTile; x += 8) {
+          const uint32_t base = (x / kTile) * S::kSlotQ + (x % kTile) * 128;
 #pragma unroll
-        for (int e = 0; e < 8 / kStep; ++e) {
-          const bool there = x + first + e * kStep < rows;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(place[e] + base), "l"(there ? from : static_cast<const __nv_bfloat16*>(a.q)), "r"(there ? 16 : 0) : "memory");
-          from += kStep * D;
-          for (t += kStep; t >= n; t -= n) from += gap;
+          for (int e = 0; e < 8 / kStep; ++e) {
+            const bool there = x + first + e * kStep < rows;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(place[e] + base), "l"(there ? from : static_cast<const __nv_bfloat16*>(a.q)), "r"(there ? 16 : 0) : "memory");
+            from += kStep * D;
+            for (t += kStep; t >= n; t -= n) from += gap;
+          }
         }
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if constexpr (Q8) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if constexpr (Q8) {
 #pragma unroll 4
-        for (int r = first; r < min(rows, slots * kTile); r += kStep) {
-          uint4* const u = reinterpret_cast<uint4*>(smem + S::kQ + (r / kTile) * S::kSlotQ + piece_at(r % kTile, c));
-          uint4 v = *u;
-          uint32_t* const w = &v.x;
+          for (int r = first; r < min(rows, slots * kTile); r += kStep) {
+            uint4* const u = reinterpret_cast<uint4*>(smem + S::kQ + (r / kTile) * S::kSlotQ + piece_at(r % kTile, c));
+            uint4 v = *u;
+            uint32_t* const w = &v.x;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = pack2(__uint_as_float(w[i] << 16) * kQ8Q, __uint_as_float(w[i] & 0xFFFF0000u) * kQ8Q);
-          *u = v;
+            for (int i = 0; i < 4; ++i) w[i] = pack2(__uint_as_float(w[i] << 16) * kQ8Q, __uint_as_float(w[i] & 0xFFFF0000u) * kQ8Q);
+            *u = v;
+          }
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars.q_full);
+      } while (seg.next(a) && !__any_sync(0xffffffffu, aborted()));
+      if (lane == 0) {   // (a copy in flight lands before the block ends)
+        const int none = 0;
+        ptx::mbar_wait(&bars.q_full, seg.index & 1, &none, kWaitLimit);
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&bars.q_full);
-    } while (seg.next(a) && !__any_sync(0xffffffffu, aborted()));
-    if (lane == 0) {   // (a copy in flight lands before the block ends)
-      const int none = 0;
-      ptx::mbar_wait(&bars.q_full, seg.index & 1, &none, kWaitLimit);
     }
-  }
   } else if (warp < 4 + S::kSoft) {
     if constexpr (!Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSoftRegs));
     // ---- softmax: kHalves threads per row of a slot, a share of the keys each

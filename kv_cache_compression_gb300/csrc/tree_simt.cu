@@ -78,39 +78,70 @@ template <typename IO> __device__ __forceinline__ float4 widen4(const IO* p) {
   return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
                      __uint_as_float(w.y & 0xFFFF0000u));
 }
-__device__ __forceinline__ float code_value(uint32_t byte, float h) {
-  const float v = (__uint_as_float(0x4B000000u | (byte & 0x7Fu)) - 8388608.0f) * h;
-  return __uint_as_float(__float_as_uint(v) ^ ((byte & 0x80u) << 24));
+// The values of four codes of a row with step h: u h rounded once (2^23 + u less 2^23, times h, in one FMA), with the code's sign.
+__device__ __forceinline__ float4 values4(uint32_t codes, float h) {
+  const uint32_t u = codes & 0x7F7F7F7Fu;
+  const float less = -8388608.0f * h;
+  const float x = fmaf(__uint_as_float(prmt(u, 0x4B000000u, 0x7650)), h, less), y = fmaf(__uint_as_float(prmt(u, 0x4B000000u, 0x7651)), h, less),
+              z = fmaf(__uint_as_float(prmt(u, 0x4B000000u, 0x7652)), h, less), w = fmaf(__uint_as_float(prmt(u, 0x4B000000u, 0x7653)), h, less);
+  return make_float4(__uint_as_float(__float_as_uint(x) ^ (codes << 24 & 0x80000000u)), __uint_as_float(__float_as_uint(y) ^ (codes << 16 & 0x80000000u)),
+                     __uint_as_float(__float_as_uint(z) ^ (codes << 8 & 0x80000000u)), __uint_as_float(__float_as_uint(w) ^ (codes & 0x80000000u)));
 }
 
-// Copies a tile's rows to `to` as fp32, a row's 16-byte pieces XORed with hash(row); rows past `count` become zeros.
-// fp32 rows are only on their way (cp.async) when it returns.
-template <typename IO, int D, typename Hash>
-__device__ __forceinline__ void load_rows(float* to, const void* from, const float* step, int count, Hash hash) {
-  constexpr int kPieces = D / 4;
-#pragma unroll 4
-  for (int u = threadIdx.x; u < kTile * kPieces; u += kThreads) {
-    const int row = u / kPieces, c = u % kPieces;
-    float* dst = to + row * D + 4 * (c ^ hash(row));
-    const bool there = row < count;
-    if (step) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (there) {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(from) + row * kPieces + c);
-        const float h = __ldg(step + row);
-        x = make_float4(code_value(w & 0xFF, h), code_value((w >> 8) & 0xFF, h), code_value((w >> 16) & 0xFF, h), code_value(w >> 24, h));
+// A tile's rows on their way to `to`, a row's 16-byte pieces XORed with hash(row); rows past `count` become zeros. fp32 rows go
+// by cp.async; codes wait in registers, sixteen a vector, until put() writes their values (which takes the latency of their loads
+// off the tile: 8 x 8 heads of 8192 rows, 28 query rows each, 455 us -> 275; seven rows, 333 -> 141).
+template <typename IO, bool Q8, int D> struct Loader {
+  static constexpr int kN = Q8 ? kTile * D / 16 / kThreads : 1;   // vectors of a thread
+  uint4 codes[kN];
+  float h[kN];
+  bool coded;
+
+  template <typename Hash> __device__ __forceinline__ void load(float* to, const void* from, const float* step, int count, Hash hash) {
+    coded = Q8 && step;
+    if (coded) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const int u = threadIdx.x + i * kThreads, row = u / (D / 16);
+        codes[i] = make_uint4(0u, 0u, 0u, 0u);
+        h[i] = 0.f;
+        if (row < count) {
+          codes[i] = __ldg(static_cast<const uint4*>(from) + u);
+          h[i] = __ldg(step + row);
+        }
       }
-      *reinterpret_cast<float4*>(dst) = x;
-    } else if constexpr (sizeof(IO) == 4) {
-      const float* src = static_cast<const float*>(from) + (there ? (int64_t)u * 4 : 0);
-      cp_async16(dst, src, there);
-    } else {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (there) x = widen4<IO>(static_cast<const IO*>(from) + (int64_t)u * 4);
-      *reinterpret_cast<float4*>(dst) = x;
+      return;
+    }
+    constexpr int kPieces = D / 4;
+#pragma unroll 4
+    for (int u = threadIdx.x; u < kTile * kPieces; u += kThreads) {
+      const int row = u / kPieces, c = u % kPieces;
+      const bool there = row < count;
+      cp_async16(to + row * D + 4 * (c ^ hash(row)), static_cast<const IO*>(from) + (there ? (int64_t)u * 4 : 0), there);
     }
   }
-}
+  template <typename Hash> __device__ __forceinline__ void put(float* to, Hash hash) const {
+    if constexpr (!Q8) return;
+    if (!coded) return;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int u = threadIdx.x + i * kThreads, row = u / (D / 16), c = u % (D / 16);
+      const int turn = c / 2 % 4;   // (four codes at a time, from another of a vector's words in every other lane: eight lanes, eight pieces)
+      uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+      if (turn & 1) {
+        const uint32_t x = w[0];
+        w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = x;
+      }
+      if (turn & 2) {
+        const uint32_t x = w[0], y = w[1];
+        w[0] = w[2], w[1] = w[3], w[2] = x, w[3] = y;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<float4*>(to + row * D + 4 * ((4 * c + (j + turn) % 4) ^ hash(row))) = values4(w[j], h[i]);
+    }
+  }
+};
 
 template <int D, int QT> struct Shape {
   static constexpr int kRq = QT == 32 ? 4 : 2, kRk = QT == 32 ? 2 : 1;      // logits of a thread: rows by keys
@@ -171,7 +202,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
     };
     // ---- queries, and the first tile's keys
     Rows tile = rows_of<IO, Q8, D>(a, here);
-    load_rows<IO, D>(ks, tile.k, tile.k_step, tile.count, k_hash);
+    Loader<IO, Q8, D> k_rows, v_rows;
+    k_rows.load(ks, tile.k, tile.k_step, tile.count, k_hash);
     cp_commit();
     for (int u = tid; u < QT * (D / 4); u += kThreads) {
       const int i = u / (D / 4), c = u % (D / 4);
@@ -187,8 +219,10 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) o[r][0] = o[r][1] = make_float2(0.f, 0.f);
 
+    k_rows.put(ks, k_hash);
+
     for (int j = 0; j < seg; ++j, ++here.tile) {
-      load_rows<IO, D>(vs, tile.v, tile.v_step, tile.count, v_hash);
+      v_rows.load(vs, tile.v, tile.v_step, tile.count, v_hash);
       cp_commit();
       cp_wait<1>();
       __syncthreads();   // K and Q are there
@@ -235,13 +269,14 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
             *reinterpret_cast<float2*>(ps + key * kPs + 2 * qg) = make_float2(l[0], l[1]);
         }
       }
+      v_rows.put(vs, v_hash);
       __syncthreads();   // the logits are there, and K's buffer is free
       const Rows now = tile;
       if (j + 1 < seg) {
         Place next = here;
         ++next.tile;
         tile = rows_of<IO, Q8, D>(a, next);
-        load_rows<IO, D>(ks, tile.k, tile.k_step, tile.count, k_hash);
+        k_rows.load(ks, tile.k, tile.k_step, tile.count, k_hash);
       }
       cp_commit();
       // ---- weights: eight lanes a row
@@ -304,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
           }
         }
       }
+      if (j + 1 < seg) k_rows.put(ks, k_hash);
       __syncthreads();   // V's buffer and the weights are free
     }
 

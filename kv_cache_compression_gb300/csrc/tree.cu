@@ -23,8 +23,8 @@ bool is_direct(int64_t rows, int64_t cap) { return rows <= 16 && cap <= 256; }
 
 // Query rows a KV head up to which bf16 calls take mma.sync. Dense caches: a pass of it, which memory bounds (sixteen rows over
 // 131072 keys of eight heads 92 us, where 32 rows on tcgen05 take 95; two passes would read everything twice). 8-bit caches: two
-// passes, of which the second reads from L2, against tcgen05's unpacking into shared memory: 32 rows over 131072 keys 107 us
-// against 127, 64 x 32 heads of 20 rows 550 against 678; but 64 rows 199 against 128.
+// passes, of which the second reads from L2, against tcgen05's unpacking into shared memory: 32 rows over 131072 keys 106 us
+// against 109, 64 x 32 heads of 20 rows 550 against 635; but 64 rows 199 against 111.
 constexpr int kMmaRows = 16, kMmaRowsQ8 = 32;
 constexpr size_t kCutBytes = (size_t)kMaxTreeCtas * 2 * sizeof(int4);
 static_assert(kCutBytes % 256 == 0, "parts follow");

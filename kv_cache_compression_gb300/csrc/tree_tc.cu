@@ -20,12 +20,11 @@
 // keys, half of the sequences shorter, 85 us, 4.8 TB/s. With up to 128 rows a KV head memory bounds it; with more, a slot's
 // way from S to P and back: 256 rows by 128 keys take 5600 clocks, of which the tensor cores are busy for 36 %, ex2 for 19 %
 // and the schedulers for 31 %. (1024 rows of 64 channels over 1500 keys, 84 us: the same way, half of the products.)
-// 8-bit rows arrive as they are; eight more warps unpack them into the tiles that TMA writes for bf16 rows (four: 134 us
-// instead of 116 for 128 rows a KV head over 8 x 8 heads of 16384 keys). As operands they are *subnormal* bf16 (sign and
-// seven magnitude bits, u 2^-133: a byte permute and an AND per two values), for which queries are scaled by 2^64 and
-// weights by 2^80; a step multiplies its key's logits and weights. The instructions of unpacking and softmax bound it: the
-// schedulers are busy for 42 % of a tile's time, the tensor cores for 20 %. More softmax warps (139 us), straight code for
-// whole tiles (127 us) and smaller pieces of a tile (128 us) did not pay beside the unpacking warps.
+// 8-bit rows arrive as they are; eight more warps unpack them into the tiles that TMA writes for bf16 rows (8 x 8 KV heads of
+// 128 rows over 16384 keys, half of the sequences shorter: 109 us; four warps took 16 more, sixteen 13 more). As operands they
+// are *subnormal* bf16 (sign and seven magnitude bits, u 2^-133: a byte permute and an AND per two values), for which queries
+// are scaled by 2^64 and weights by 2^80; a step multiplies its key's logits and weights. The way of a tile through the
+// unpacking warps bounds it (two waits, loads, stores and a fence, 1400 clocks for K and for V each of the 3500 that a tile takes).
 #include "tree_schedule.cuh"
 
 #include <type_traits>
@@ -73,9 +72,11 @@ template <bool Q8, int D, bool TWO> struct Shape {
   static constexpr int kUnpack = Q8 ? 8 : 0;
   static constexpr int kWarps = 4 + kSoft + kUnpack;
   static constexpr int kThreads = 32 * kWarps;
-  // Registers go from the warps that move data to those of the softmax (both sum up to no more than the block is launched with).
-  static constexpr int kLaunchRegs = 96, kSoftRegs = 104, kMoveRegs = 64;
-  static_assert(Q8 || 32 * kSoft * kSoftRegs + (kThreads - 32 * kSoft) * kMoveRegs <= kThreads * kLaunchRegs, "registers");
+  // Registers go from the warps that move data to those of the softmax (both sum up to no more than the block is launched with):
+  // 128 us -> 126 for 4 x 8 KV heads of 256 rows over 32768 keys; beside an 8-bit cache they let 32 keys be computed on at a time,
+  // 118 us -> 109 for 8 x 8 heads of 128 rows over 16384.
+  static constexpr int kLaunchRegs = 96, kSoftRegs = Q8 ? 120 : 104, kMoveRegs = Q8 ? 80 : 64;
+  static_assert(32 * kSoft * kSoftRegs + (kThreads - 32 * kSoft) * kMoveRegs <= kThreads * kLaunchRegs, "registers");
   static constexpr int kSlotQ = kTile * D * 2;                 // bytes of 128 rows of queries
   static constexpr int kStage = kTile * D * 2;                 // of a tile of K or V
   static constexpr int kStages = (Q8 ? (TWO ? 3 : 4) : TWO ? 4 : 6) * (128 / D);   // (TWO: of one ring; else of two, a slot's each)
@@ -101,6 +102,16 @@ __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[16]) {
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
         "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+      "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(at));
 }
 __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&r)[8]) {
@@ -268,7 +279,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
   constexpr uint32_t kPair = TWO ? 1 : 2;                    // they are loaded, K before V
 
   if (warp < 4) {
-    if constexpr (!Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kMoveRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kMoveRegs));
     if (warp == 0) {
       // ---- loads, in the order in which the products take them
       if (lane == 0) {
@@ -475,10 +486,10 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
       }
     }
   } else if (warp < 4 + S::kSoft) {
-    if constexpr (!Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSoftRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSoftRegs));
     // ---- softmax: kHalves threads per row of a slot, a share of the keys each
     constexpr int kHalves = S::kHalves, kKeys = kTile / kHalves, kWords = kKeys / 32;
-    constexpr int kChunk = 16, kChunks = kKeys / kChunk, kE = kChunk / 2;   // keys that are computed on at a time, and their pairs
+    constexpr int kChunk = Q8 ? 32 : 16, kChunks = kKeys / kChunk, kE = kChunk / 2;   // keys that are computed on at a time, and their pairs
     const int slot = (warp - 4) / (4 * kHalves), half = (warp - 4) / 4 % kHalves, quarter = warp % 4, row = quarter * 32 + lane;
     const uint32_t o_lane = tmem + ((uint32_t)(quarter * 32) << 16), s_at = o_lane + S::kS(slot);
     float* const swap = reinterpret_cast<float*>(smem + S::kSwap) + slot * 2 * kTile;   // [half][row]
@@ -827,6 +838,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
       done += (uint32_t)seg.tiles;
     } while (seg.next(a));
   } else if constexpr (Q8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kMoveRegs));
     // ---- codes into bf16 tiles: two threads per key, half of the channels each
     const int key = tid % kTile, part = (tid - 32 * (4 + S::kSoft)) / kTile;
     Segments ks(a, share), vs(a, share);

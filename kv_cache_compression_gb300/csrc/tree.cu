@@ -43,7 +43,7 @@ size_t tree_workspace_bytes(int batch, int q_heads, int heads, int head_dim, int
   const int simt = rows <= 8 ? 8 : kSimtRows;
   size_t parts = parts_bytes(bounded(most_tiles(batch, heads, (rows + simt - 1) / simt, tokens, cap, 16, 16), kMaxTreeCtas), simt, head_dim);
   if (rows > kMmaRows) {
-    const int wide = rows <= 128 ? 128 : 256;
+    const int wide = rows <= 128 ? 128 : 256;   // (where more rows go in passes of 128, there are at most twice as many of half the parts)
     const size_t tc = parts_bytes(bounded(most_tiles(batch, heads, (rows + wide - 1) / wide, tokens, cap, 128, 128), kMaxTcCtas), wide, head_dim);
     parts = tc > parts ? tc : parts;
   }

@@ -5,10 +5,10 @@
 //
 // tcgen05 with 128 query rows by 128 keys: S (fp32) and O stand in TMEM, P goes back over S as the second product's A
 // operand, K and V are B operands in shared memory. Two slots, each an S, an O and its softmax warps, keep the tensor
-// cores busy while the other slot's weights are computed. Up to 128 rows (TWO false) both slots serve the same rows and
-// take the key tiles in turn, each from a ring of its own, and their halves of O meet at the head's end; up to 256 a slot
-// has 128 rows each and every key tile serves both, so that the cache is read once. More rows are passes, side by side
-// where all sequences have as many. A slot issues P V of a tile and Q K^T of its next as one block (S is overwritten when
+// cores busy while the other slot's weights are computed. In passes of 128 rows (TWO false) both slots serve the same
+// rows and take the key tiles in turn, each from a ring of its own, and their halves of O meet at the head's end; in passes of
+// 256 a slot has 128 rows each and every key tile serves both, so that the cache is read once. Passes go side by side where all
+// sequences have as many. A slot issues P V of a tile and Q K^T of its next as one block (S is overwritten when
 // P V has read P: the tensor core takes them one after the other), and passes the turn on.
 //
 // Weights enter the second product as one bf16 value, rounded by half a step (2^-8); they are summed up as they were. A
@@ -18,8 +18,10 @@
 //
 // Measured (128 channels): 4 x 8 KV heads of 256 rows over 32768 keys 126 us, 1040 TFLOP/s; 8 x 8 heads of 64 rows over 16384
 // keys, half of the sequences shorter, 85 us, 4.8 TB/s. With up to 128 rows a KV head memory bounds it; with more, a slot's
-// way from S to P and back: 256 rows by 128 keys take 5600 clocks, of which the tensor cores are busy for 36 %, ex2 for 19 %
-// and the schedulers for 31 %. (1024 rows of 64 channels over 1500 keys, 84 us: the same way, half of the products.)
+// way from S to P (1100 clocks), to the other warps and back (300), and through both products (1100 with 64 channels, 1400 with 128,
+// where the tensor cores need 512 and 1024), during which the other slot's is hidden but for its own products: 3400 clocks for
+// 256 rows by 128 keys, 3100 with 64 channels. A call's start and end take 28000, a head's end and its first tiles some 10000.
+//
 // 8-bit rows arrive as they are; eight more warps unpack them into the tiles that TMA writes for bf16 rows (8 x 8 KV heads of
 // 128 rows over 16384 keys, half of the sequences shorter: 109 us; four warps took 16 more, sixteen 13 more). As operands they
 // are *subnormal* bf16 (sign and seven magnitude bits, u 2^-133: a byte permute and an AND per two values), for which queries
@@ -928,8 +930,22 @@ template <bool Q8, int D, bool TWO> cudaError_t launch_typed(const TreeJob& job)
   return err != cudaSuccess ? err : launch_tree_join_wide<D, kTile>(a, job.stream);
 }
 
+// Passes of 128 rows or of 256, which read the cache half as often. Where all sequences have as many tokens, an odd number of
+// halves leaves one empty: 384 rows over 1500 keys of 64 channels take 88 us in passes of 128 (102 of 256), 280 over 16384 of 128
+// channels 102 (123), 600 over 8192 102 (111); but 1100 over 1500 226 (213), and even numbers are equal or better in passes of 256.
+// Where sequences have fewer tokens the same holds for most of them, but passes come one after the other: dense caches of 512 KB a
+// head and less are read from L2 (up to 300 tokens over 1500 keys of 64 channels 66 us (72), up to 440 79 (83)), longer ones are
+// not (up to 512 rows over 16384 keys 176 us (162)). Over 8 bits unpacking and softmax count, not reading (up to 256 rows over 16384
+// keys 146 us (171), up to 440 204 (235)).
+template <bool Q8, int D> bool narrow_passes(const TreeJob& job) {
+  const int64_t rows = (int64_t)(job.q_heads / job.heads) * job.tokens, halves = (rows + 127) / 128;
+  if (halves > 8) return false;
+  if (!job.n_new || halves == 1) return halves % 2 != 0;
+  return Q8 || (halves > 2 && job.cap * D * 4 <= 512 * 1024);
+}
+
 template <bool Q8, int D> cudaError_t launch_dim(const TreeJob& job) {
-  return job.q_heads / job.heads * job.tokens <= 128 ? launch_typed<Q8, D, false>(job) : launch_typed<Q8, D, true>(job);
+  return narrow_passes<Q8, D>(job) ? launch_typed<Q8, D, false>(job) : launch_typed<Q8, D, true>(job);
 }
 
 }  // namespace

@@ -96,3 +96,21 @@ def test_every_number_of_rows(gpu_device, G, T, d, q8):
     for lens, n_new in (([700, 129], None), ([1, 640], [T, max(1, T - 5)]), ([0, 16], [max(1, T // 2), 0])):
         out, lse = run(x, lens, mask=mask, n_new=n_new)
         check(x, lens, out, lse, mask=mask, n_new=n_new)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("shape", [  # B, H, G, d, T, cap, tokens of each sequence
+    (1, 2, 4, 128, 70, 300, None), (2, 1, 3, 64, 128, 150, None), (1, 1, 4, 128, 150, 400, None), (1, 2, 4, 64, 97, 260, None),
+    (1, 1, 2, 128, 448, 140, None), (1, 1, 1, 64, 1025, 130, None), (1, 1, 1, 64, 1153, 129, None),
+    (4, 2, 4, 128, 64, 700, [64, 33, 0, 1]), (3, 1, 4, 64, 110, 900, [110, 32, 97]), (3, 2, 1, 64, 440, 500, [129, 440, 300]),
+    (2, 1, 4, 128, 70, 1300, [69, 33]), (2, 1, 1, 128, 1030, 140, [1030, 900])])
+def test_passes_of_many_rows(gpu_device, shape, q8):
+    """Whole and half passes, side by side or one after the other."""
+    B, H, G, d, T, cap, n_new = shape
+    x = make(gpu_device, T + cap, B, H, G, d, T, cap, BF16, q8=q8)
+    lens = [cap, cap // 2, cap - 1, 3][:B]
+    rng = np.random.default_rng(T)
+    mask = random_tree(rng, B, T)
+    for drafts in (True, False):
+        out, lse = run(x, lens, drafts=drafts, mask=mask if drafts else None, n_new=n_new)
+        check(x, lens, out, lse, drafts=drafts, mask=mask if drafts else None, n_new=n_new, heads=[H - 1], where=f"{drafts}")

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_mma_kernel(const Args a, con
   } else {
     share = find_share<kTile, kNew, kThreads>(a, scratch);   // (with barriers)
     if (share.at >= share.end) return;
-    here = first_place<kTile, kNew>(a, share);
+    here = share.first;
   }
   Place ahead = here;              // the next tile to load
   int64_t ahead_at = share.at + warp;

@@ -102,23 +102,64 @@ __device__ __forceinline__ void place_at(Place& p, int64_t in) {
   p.head = (int)(u / (uint32_t)p.s.passes);
   p.pass = (int)(u - (uint32_t)p.head * (uint32_t)p.s.passes);
 }
-// Where a CTA's share lies: tiles at .. end - 1 of the list, from sequence `seq`, which starts at tile `before`.
+// Where a CTA's share lies: tiles at .. end - 1 of the list.
 struct Share {
-  int64_t at, end, before;
+  int64_t at, end;
   int64_t previous;   // where the share before begins (the first one's: its own)
-  int seq;
+  Place first;        // of tile `at`
 };
 
 // All threads of a block of THREADS find their CTA's share (at == end: none). Sequence lengths are summed up by every
-// CTA for itself; CTA 0 leaves the sums for the joining launch and reports what is out of range.
+// CTA for itself, of up to 32 sequences by every warp (with a block's
+// exchanges, and each role of tree_tc.cu looking for the first place by itself, 64 rows over 16384 keys of 64 heads took 85 us, 80 so); CTA 0 leaves the sums for the joining launch and reports what is
+// out of range.
 template <int THREADS> struct ShareScratch {   // shared memory
   int64_t warp_sums[THREADS / 32];
   Share found;
 };
 template <int TILE, int NEW, int THREADS> __device__ __forceinline__ Share find_share(const Args& a, ShareScratch<THREADS>& scratch) {
+  const int tid = threadIdx.x, lane = tid % 32;
+  auto note = [&](int b, int64_t sum) {   // (CTA 0)
+    a.upto[b] = sum;
+    if ((int64_t)a.len[b] > a.cap) report(a.dev_status, SNAPKV_ERR_CAPACITY);
+    if (a.n_new && (a.n_new[b] < 0 || a.n_new[b] > a.tokens)) report(a.dev_status, SNAPKV_ERR_INVALID_ARG);
+  };
+  if (a.batch <= 32) {
+    Seq s = {};
+    if (lane < a.batch) s = seq_of<TILE, NEW>(a, lane);
+    const int64_t mine = s.units(a.heads);
+    int64_t x = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
+    }
+    const int64_t total = __shfl_sync(0xffffffffu, x, 31), upto = x - mine;
+    if (blockIdx.x == 0 && tid < 32) {
+      if (lane < a.batch) note(lane, upto);
+      if (lane == 0) a.upto[a.batch] = total;
+    }
+    Share share = {};
+    const int shares = working_shares(a, total), c = (int)blockIdx.x / a.siblings;
+    if (c < shares) {
+      share.at = share_start(total, shares, c);
+      share.end = share_start(total, shares, c + 1);
+      share.previous = share_start(total, shares, c > 0 ? c - 1 : 0);
+      const int b = __ffs(__ballot_sync(0xffffffffu, share.at >= upto && share.at < x)) - 1;
+      Place& p = share.first;
+      p.seq = b;
+      p.s.rows = __shfl_sync(0xffffffffu, s.rows, b);
+      p.s.n = __shfl_sync(0xffffffffu, s.n, b);
+      p.s.passes = __shfl_sync(0xffffffffu, s.passes, b);
+      p.s.cache_tiles = __shfl_sync(0xffffffffu, s.cache_tiles, b);
+      p.s.tiles = __shfl_sync(0xffffffffu, s.tiles, b);
+      place_at(p, share.at - __shfl_sync(0xffffffffu, upto, b));
+    }
+    __syncthreads();   // (what the block initialised before can be seen, as below)
+    return share;
+  }
   int64_t (&warp_sums)[THREADS / 32] = scratch.warp_sums;
   Share& found = scratch.found;
-  const int tid = threadIdx.x, lane = tid % 32;
   const int chunk = (a.batch + THREADS - 1) / THREADS;
   const int b0 = min(a.batch, tid * chunk), b1 = min(a.batch, b0 + chunk);
   int64_t mine = 0;
@@ -130,7 +171,7 @@ template <int TILE, int NEW, int THREADS> __device__ __forceinline__ Share find_
     if (lane >= off) x += y;
   }
   if (lane == 31) warp_sums[tid / 32] = x;
-  if (tid == 0) found = Share{0, 0, 0, 0, 0};
+  if (tid == 0) found.at = found.end = 0;
   __syncthreads();
   int64_t total = 0, upto = x - mine;
   for (int w = 0; w < THREADS / 32; ++w) {
@@ -140,10 +181,8 @@ template <int TILE, int NEW, int THREADS> __device__ __forceinline__ Share find_
   if (blockIdx.x == 0) {
     int64_t sum = upto;
     for (int b = b0; b < b1; ++b) {
-      a.upto[b] = sum;
+      note(b, sum);
       sum += seq_of<TILE, NEW>(a, b).units(a.heads);
-      if ((int64_t)a.len[b] > a.cap) report(a.dev_status, SNAPKV_ERR_CAPACITY);
-      if (a.n_new && (a.n_new[b] < 0 || a.n_new[b] > a.tokens)) report(a.dev_status, SNAPKV_ERR_INVALID_ARG);
     }
     if (tid == 0) a.upto[a.batch] = total;
   }
@@ -153,27 +192,25 @@ template <int TILE, int NEW, int THREADS> __device__ __forceinline__ Share find_
     if (at >= upto && at < upto + mine) {
       int b = b0;
       for (int64_t u; at >= upto + (u = seq_of<TILE, NEW>(a, b).units(a.heads)); ++b) upto += u;
-      found = Share{at, share_start(total, shares, c + 1), upto, share_start(total, shares, c > 0 ? c - 1 : 0), b};
+      found.at = at;
+      found.end = share_start(total, shares, c + 1);
+      found.previous = share_start(total, shares, c > 0 ? c - 1 : 0);
+      found.first.seq = b;
+      found.first.s = seq_of<TILE, NEW>(a, b);
+      place_at(found.first, at - upto);
     }
   }
   __syncthreads();
   return found;
 }
 
-template <int TILE, int NEW> __device__ __forceinline__ Place first_place(const Args& a, const Share& share) {
-  Place p;
-  p.seq = share.seq;
-  p.s = seq_of<TILE, NEW>(a, p.seq);
-  place_at(p, share.at - share.before);
-  return p;
-}
 // Leaves a share's note for the joining launch (one thread of every CTA): whether it is the first to begin inside a head.
-template <int TILE, int NEW> __device__ __forceinline__ void leave_note(const Args& a, const Share& share) {
+__device__ __forceinline__ void leave_note(const Args& a, const Share& share) {
   const int c = (int)blockIdx.x / a.siblings;
   if (blockIdx.x % a.siblings != 0) return;
   int tile = 0;
   if (share.at < share.end && c > 0) {
-    const Place p = first_place<TILE, NEW>(a, share);
+    const Place& p = share.first;
     const bool first = p.tile > 0 && share.previous <= share.at - p.tile;
     a.cuts[2 * c + 1] = make_int4(p.s.tiles, p.s.n, 0, 0);
     tile = first ? p.tile : 0;
@@ -219,7 +256,7 @@ template <typename IO, int D, int TILE, int NEW, int THREADS> __device__ __force
   p.head = (int)blockIdx.x - p.seq * a.heads;
   p.pass = p.tile = 0;
   p.s = seq_of<TILE, NEW>(a, p.seq);
-  share = Share{0, p.s.tiles, 0, 0, p.seq};
+  share = Share{0, p.s.tiles, 0, p};
   if (p.head == 0 && threadIdx.x == 0) {
     if ((int64_t)a.len[p.seq] > a.cap) report(a.dev_status, SNAPKV_ERR_CAPACITY);
     if (a.n_new && (a.n_new[p.seq] < 0 || a.n_new[p.seq] > a.tokens)) report(a.dev_status, SNAPKV_ERR_INVALID_ARG);

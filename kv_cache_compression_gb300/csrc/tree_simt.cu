@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(Args a) {
   } else {
     share = find_share<kTile, kTile, kThreads>(a, scratch);
     if (share.at >= share.end) return;
-    here = first_place<kTile, kTile>(a, share);
+    here = share.first;
   }
   // first product: rows kRq qg .. by keys kRk kg .. (a warp has eight rows, so that where there are fewer rows some rest)
   constexpr int kWarpQg = 8 / kRq, kWarpKg = 32 / kWarpQg;   // of a warp's lanes

@@ -195,7 +195,7 @@ struct Segments {
   int64_t at, end;
   int tiles;       // of this segment
   int index;
-  __device__ __forceinline__ Segments(const Args& a, const Share& s) : p(first_place<kTile, kTile>(a, s)), at(s.at), end(s.end), index(0) { cut(); }
+  __device__ __forceinline__ Segments(const Args& a, const Share& s) : p(s.first), at(s.at), end(s.end), index(0) { cut(); }
   __device__ __forceinline__ void cut() {
     const int64_t left = end - at;
     const int more = p.s.tiles - p.tile;
@@ -254,9 +254,14 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
     ptx::mbar_init(&bars.turn[1], 1);
     ptx::fence_mbar_init();
   }
-  const Share share = find_share<kTile, kTile, S::kThreads>(a, small.share);   // (with barriers)
-  if (tid == 64) leave_note<kTile, kTile>(a, share);
-  if (share.at >= share.end) return;
+  {
+    const Share mine = find_share<kTile, kTile, S::kThreads>(a, small.share);   // (with barriers)
+    if (tid == 64) {
+      leave_note(a, mine);
+      small.share.found = mine;
+    }
+    if (mine.at >= mine.end) return;
+  }
   if (warp == 1) {
     ptx::tmem_alloc(&small.tmem, S::kColumns);
     ptx::tmem_relinquish();
@@ -265,6 +270,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = small.tmem;
+  const Share& share = small.share.found;
   const uint32_t ring = ptx::smem_u32(smem + S::kRing), q_smem = ptx::smem_u32(smem + S::kQ);
   const int pass0 = a.siblings > 1 ? (int)blockIdx.x % a.siblings : 0;
   auto wait = [&](uint64_t* bar, uint32_t parity) {

@@ -22,9 +22,10 @@ size_t upto_bytes(int batch) { return up(((size_t)batch + 1) * sizeof(int64_t));
 bool is_direct(int64_t rows, int64_t cap) { return rows <= 16 && cap <= 256; }
 
 // Query rows a KV head up to which bf16 calls take mma.sync. Dense caches: a pass of it, which memory bounds (sixteen rows over
-// 131072 keys of eight heads 92 us, where 32 rows on tcgen05 take 95; two passes would read everything twice). 8-bit caches: two
-// passes, of which the second reads from L2, against tcgen05's unpacking into shared memory: 32 rows over 131072 keys 106 us
-// against 109, 64 x 32 heads of 20 rows 550 against 635; but 64 rows 199 against 111.
+// 131072 keys of eight heads 92 us, where 32 rows on tcgen05 take 94; two passes would read everything twice). 8-bit caches: two
+// passes, of which the second reads from L2, against tcgen05's unpacking into shared memory: 64 x 32 heads of 20 rows over
+// 2140 keys 550 us against 577, 8 x 8 heads of 32 rows over 16384 keys of 64 channels 77 against 91 (32 rows over 131072 keys 108
+// against 102); but 64 rows 199 against 105.
 constexpr int kMmaRows = 16, kMmaRowsQ8 = 32;
 constexpr size_t kCutBytes = (size_t)kMaxTreeCtas * 2 * sizeof(int4);
 static_assert(kCutBytes % 256 == 0, "parts follow");

@@ -8,10 +8,10 @@
 // round to nearest. K's and V's tiles have a buffer each: V's rows are under way while the logits are computed, the next
 // K's while the outputs are, and a second CTA per SM fills the rest.
 //
-// Measured (128 channels): 8 x 8 KV heads of 28 rows over 8192 keys, half of the sequences shorter, 201 us, 2.0 TB/s: loads from
-// shared memory take 58 % of its clocks, FMAs and the rest of the instructions 49 % of the schedulers', and the barriers between a
-// tile's steps keep them apart; eight rows 145 us, 3.6 TB/s. Three bf16 parts an operand on mma.sync (six products, as accurate)
-// took 214 us for the 28 rows and 155 for eight, blocks of 4 x 4 logits and 8 x 4 outputs a thread 210 and 140.
+// Measured (128 channels): 8 x 8 KV heads of 28 rows over 8192 keys, half of the sequences shorter, 190 us, 2.1 TB/s: loads from
+// shared memory take 61 % of its clocks, FMAs and the rest of the instructions 50 % of the schedulers', and the barriers between a
+// tile's steps keep them apart; eight rows 127 us, 4.2 TB/s. Three bf16 parts an operand on mma.sync (six products, as accurate)
+// took 7 % more for the 28 rows and for eight, blocks of 4 x 4 logits and 8 x 4 outputs a thread 5 % more and 4 % less.
 #include "tree_schedule.cuh"
 
 #include <atomic>
@@ -381,7 +381,7 @@ template <bool Q8, int D, int QT> cudaError_t launch_typed(const TreeJob& job) {
   return err != cudaSuccess || a.direct ? err : launch_tree_join<float, D, kTile, kTile>(a, job.stream);
 }
 
-// Passes of eight rows where there are no more: 64 KV heads of 8192 fp32 rows take 145 us with them, 192 with 32.
+// Passes of eight rows where there are no more: 64 KV heads of 8192 fp32 rows took 145 us with them, 192 with 32 (127 now).
 template <bool Q8, int D> cudaError_t launch_dim(const TreeJob& job) {
   const int rows = job.q_heads / job.heads * job.tokens;
   return rows <= 8 ? launch_typed<Q8, D, 8>(job) : launch_typed<Q8, D, 32>(job);

@@ -13,17 +13,17 @@
 //
 // Weights enter the second product as one bf16 value, rounded by half a step (2^-8); they are summed up as they were. A
 // second part for what the rounding leaves made P V twice as long: 169 us instead of 142 where 4 x 8 KV heads, 256 rows
-// each, read 32768 keys. A row's maximum is only raised, and its O rescaled, when it would grow by more than 2^8; sums
+// each, read 32768 keys (119 now). A row's maximum is only raised, and its O rescaled, when it would grow by more than 2^8; sums
 // and outputs stay under the same maximum, so that nothing is lost.
 //
-// Measured (128 channels): 4 x 8 KV heads of 256 rows over 32768 keys 126 us, 1040 TFLOP/s; 8 x 8 heads of 64 rows over 16384
-// keys, half of the sequences shorter, 85 us, 4.8 TB/s. With up to 128 rows a KV head memory bounds it; with more, a slot's
+// Measured (128 channels): 4 x 8 KV heads of 256 rows over 32768 keys 119 us, 1100 TFLOP/s; 8 x 8 heads of 64 rows over 16384
+// keys, half of the sequences shorter, 80 us, 5.0 TB/s. With up to 128 rows a KV head memory bounds it; with more, a slot's
 // way from S to P (1100 clocks), to the other warps and back (300), and through both products (1100 with 64 channels, 1400 with 128,
 // where the tensor cores need 512 and 1024), during which the other slot's is hidden but for its own products: 3400 clocks for
-// 256 rows by 128 keys, 3100 with 64 channels. A call's start and end take 28000, a head's end and its first tiles some 10000.
+// 256 rows by 128 keys, 3100 with 64 channels.
 //
 // 8-bit rows arrive as they are; eight more warps unpack them into the tiles that TMA writes for bf16 rows (8 x 8 KV heads of
-// 128 rows over 16384 keys, half of the sequences shorter: 109 us; four warps took 16 more, sixteen 13 more). As operands they
+// 128 rows over 16384 keys, half of the sequences shorter: 101 us; four warps took 16 more, sixteen 13 more). As operands they
 // are *subnormal* bf16 (sign and seven magnitude bits, u 2^-133: a byte permute and an AND per two values), for which queries
 // are scaled by 2^64 and weights by 2^80; a step multiplies its key's logits and weights. The way of a tile through the
 // unpacking warps bounds it (two waits, loads, stores and a fence, 1400 clocks for K and for V each of the 3500 that a tile takes).
@@ -75,8 +75,8 @@ template <bool Q8, int D, bool TWO> struct Shape {
   static constexpr int kWarps = 4 + kSoft + kUnpack;
   static constexpr int kThreads = 32 * kWarps;
   // Registers go from the warps that move data to those of the softmax (both sum up to no more than the block is launched with):
-  // 128 us -> 126 for 4 x 8 KV heads of 256 rows over 32768 keys; beside an 8-bit cache they let 32 keys be computed on at a time,
-  // 118 us -> 109 for 8 x 8 heads of 128 rows over 16384.
+  // 2 % less time for 4 x 8 KV heads of 256 rows over 32768 keys; beside an 8-bit cache they let 32 keys be computed on at a time,
+  // 8 % less for 8 x 8 heads of 128 rows over 16384.
   static constexpr int kLaunchRegs = 96, kSoftRegs = Q8 ? 120 : 104, kMoveRegs = Q8 ? 80 : 64;
   static_assert(32 * kSoft * kSoftRegs + (kThreads - 32 * kSoft) * kMoveRegs <= kThreads * kLaunchRegs, "registers");
   static constexpr int kSlotQ = kTile * D * 2;                 // bytes of 128 rows of queries
@@ -937,12 +937,12 @@ template <bool Q8, int D, bool TWO> cudaError_t launch_typed(const TreeJob& job)
 }
 
 // Passes of 128 rows or of 256, which read the cache half as often. Where all sequences have as many tokens, an odd number of
-// halves leaves one empty: 384 rows over 1500 keys of 64 channels take 88 us in passes of 128 (102 of 256), 280 over 16384 of 128
-// channels 102 (123), 600 over 8192 102 (111); but 1100 over 1500 226 (213), and even numbers are equal or better in passes of 256.
+// halves leaves one empty: 384 rows over 1500 keys of 64 channels take 78 us in passes of 128 (93 of 256), 280 over 16384 of 128
+// channels 94 (114), 600 over 8192 94 (103); but 1100 over 1500 202 (197), and even numbers are equal or better in passes of 256.
 // Where sequences have fewer tokens the same holds for most of them, but passes come one after the other: dense caches of 512 KB a
-// head and less are read from L2 (up to 300 tokens over 1500 keys of 64 channels 66 us (72), up to 440 79 (83)), longer ones are
-// not (up to 512 rows over 16384 keys 176 us (162)). Over 8 bits unpacking and softmax count, not reading (up to 256 rows over 16384
-// keys 146 us (171), up to 440 204 (235)).
+// head and less are read from L2 (up to 300 tokens over 1500 keys of 64 channels 59 us (65), up to 440 71 (76)), longer ones are
+// not (up to 512 rows over 16384 keys 168 us (154)). Over 8 bits unpacking and softmax count, not reading (up to 256 rows over 16384
+// keys 136 us (159), up to 440 192 (215)).
 template <bool Q8, int D> bool narrow_passes(const TreeJob& job) {
   const int64_t rows = (int64_t)(job.q_heads / job.heads) * job.tokens, halves = (rows + 127) / 128;
   if (halves > 8) return false;

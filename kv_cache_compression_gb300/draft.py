@@ -159,7 +159,7 @@ def q8_tree_attend(q, cache, len_, k_new=None, v_new=None, mask=None, *, n_new=N
     return out
 
 
-def _append_args(shape, dev, dtype, k_new, v_new, len_in, len_out, n_new, pick):
+def _append_args(where, shape, dev, dtype, k_new, v_new, len_in, len_out, n_new, pick):
     """Checks and completes what the two appends share."""
     B, H, _, d = shape
     rows = k_new.shape[2] if k_new.dim() == 4 else 1
@@ -172,6 +172,8 @@ def _append_args(shape, dev, dtype, k_new, v_new, len_in, len_out, n_new, pick):
             raise ValueError("pick must be [B, picks]")
         picks = pick.shape[1]
         _check("pick", pick, (B, picks), _INT32, dev)
+        if picks < 1:   # (such a tensor's address is 0, which the library takes for no pick: all rows)
+            raise SnapKVError(ERR_INVALID_ARG, where)
     if n_new is not None:
         _check("n_new", n_new, (B,), _INT32, dev)
     len_out = _new_lengths(len_in, len_out, B, dev)
@@ -181,13 +183,14 @@ def _append_args(shape, dev, dtype, k_new, v_new, len_in, len_out, n_new, pick):
 @_on_stream
 def append_rows(k_cache, v_cache, k_new, v_new, len_in, len_out=None, *, n_new=None, pick=None, dev_status=None):
     """snapkv_append_rows: rows pick[b,i], i < n_new[b], of k_new, v_new [B,H,rows,d] (without ``pick`` [B,picks]: rows i) go
-    to rows len_in[b] + i of k_cache, v_cache [B,H,cap,d]. Returns len_out [B] (len_in is only read)."""
+    to rows len_in[b] + i of k_cache, v_cache [B,H,cap,d]. Returns len_out [B] (len_in is only read). A step that accepts nothing
+    has n_new[b] = 0; a pick without columns (picks = 0) is refused."""
     shape, dev, dtype = k_cache.shape, k_cache.device, k_cache.dtype
     if len(shape) != 4:
         raise ValueError("k_cache must be [B, H, cap, d]")
     _check("k_cache", k_cache, shape, dtype, dev)
     _check("v_cache", v_cache, shape, dtype, dev)
-    rows, picks, len_out = _append_args(shape, dev, dtype, k_new, v_new, len_in, len_out, n_new, pick)
+    rows, picks, len_out = _append_args("snapkv_append_rows", shape, dev, dtype, k_new, v_new, len_in, len_out, n_new, pick)
     B, H, cap, d = shape
     _call("snapkv_append_rows", dev, k_cache.data_ptr(), v_cache.data_ptr(), cap, k_new.data_ptr(), v_new.data_ptr(), rows,
           _at(pick), picks, _at(n_new), len_in.data_ptr(), len_out.data_ptr(), B, H, d, _code(dtype),
@@ -199,7 +202,8 @@ def append_rows(k_cache, v_cache, k_new, v_new, len_in, len_out=None, *, n_new=N
 def q8_append(cache, k_new, v_new, len_in, len_out=None, *, n_new=None, pick=None, dev_status=None):
     """snapkv_q8_append: append_rows for a Q8Cache, whose rows are quantised as they are written."""
     dev, dtype = cache.device, k_new.dtype
-    rows, picks, len_out = _append_args(cache.shape, dev, dtype, k_new, v_new, len_in, len_out, n_new, pick)
+    rows, picks, len_out = _append_args("snapkv_q8_append", cache.shape, dev, dtype, k_new, v_new, len_in, len_out, n_new,
+                                       pick)
     _call("snapkv_q8_append", dev, cache._struct(), k_new.data_ptr(), v_new.data_ptr(), rows, _at(pick), picks, _at(n_new),
           len_in.data_ptr(), len_out.data_ptr(), _code(dtype), _status(dev_status, dev))
     return len_out

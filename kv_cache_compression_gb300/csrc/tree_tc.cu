@@ -13,8 +13,8 @@
 //
 // Weights enter the second product as one bf16 value, rounded by half a step (2^-8); they are summed up as they were. A
 // second part for what the rounding leaves made P V twice as long: 169 us instead of 142 where 4 x 8 KV heads, 256 rows
-// each, read 32768 keys (119 now). A row's maximum is only raised, and its O rescaled, when it would grow by more than 2^8; sums
-// and outputs stay under the same maximum, so that nothing is lost.
+// each, read 32768 keys (119 now). A row's maximum is only raised, and its O rescaled, when it would grow by more than 2^8 (over
+// 8 bits 2^6); sums and outputs stay under the same maximum, so that nothing is lost.
 //
 // Measured (128 channels): 4 x 8 KV heads of 256 rows over 32768 keys 119 us, 1100 TFLOP/s; 8 x 8 heads of 64 rows over 16384
 // keys, half of the sequences shorter, 80 us, 5.0 TB/s. With up to 128 rows a KV head memory bounds it; with more, a slot's
@@ -45,7 +45,6 @@ using namespace tree;
 
 constexpr int kTile = 128;                       // keys; also a slot's query rows
 constexpr long long kWaitLimit = 4000000000LL;   // about two seconds
-constexpr float kSlack = 8.0f;                   // log2 of what weights may exceed 1 by
 
 constexpr float kQ8Q = 0x1p64f, kQ8Dot = 0x1p69f, kQ8P = 0x1p80f, kQ8Out = 0x1p53f;
 constexpr float kNewDot = 0x1p-64f, kNewP = 0x1p-53f;   // for drafted rows, whose values are as they are
@@ -79,6 +78,9 @@ template <bool Q8, int D, bool TWO> struct Shape {
   // 8 % less for 8 x 8 heads of 128 rows over 16384.
   static constexpr int kLaunchRegs = 96, kSoftRegs = Q8 ? 120 : 104, kMoveRegs = Q8 ? 80 : 64;
   static_assert(32 * kSoft * kSoftRegs + (kThreads - 32 * kSoft) * kMoveRegs <= kThreads * kLaunchRegs, "registers");
+  // log2 of what weights may exceed 1 by. Over 8 bits a weight is multiplied by its key's step, up to 2^48 / 127 < 2^41.02, and by
+  // kQ8P = 2^80: with 2^6 that stays below 2^127.02, with 2^8 it would be infinite for values of V above 2^47.
+  static constexpr float kSlack = Q8 ? 6.0f : 8.0f;
   static constexpr int kSlotQ = kTile * D * 2;                 // bytes of 128 rows of queries
   static constexpr int kStage = kTile * D * 2;                 // of a tile of K or V
   static constexpr int kStages = (Q8 ? (TWO ? 3 : 4) : TWO ? 4 : 6) * (128 / D);   // (TWO: of one ring; else of two, a slot's each)
@@ -672,7 +674,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
               for (int e = 0; e < kE; ++e) y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
               pack(y, c, p + kE * c);
             }
-            left = any_of_pair(pair, top > kSlack);
+            left = any_of_pair(pair, top > S::kSlack);
             if constexpr (!Q8)
               if (!left) tmem_st(s_at + kKeys * half, p);
           }
@@ -707,7 +709,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
               ptx::named_barrier(pair, 64);
               top = fmaxf(top, swap[(half ^ 1) * kTile + row]);
             }
-            const float next = first ? fmaxf(m, top) : top > m + kSlack ? top : m;
+            const float next = first ? fmaxf(m, top) : top > m + S::kSlack ? top : m;
             if (!first && __any_sync(0xffffffffu, next != m)) {   // (the same for both threads of a row)
               const float fall = rescale(m, next);
               l *= fall;

@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
               ptx::named_barrier(pair, 64);
               top = fmaxf(top, swap[(half ^ 1) * kTile + row]);
             }
-            const float next = first ? fmaxf(m, top) : top > m + S::kSlack ? top : m;
+            const float next = first ? fmaxf(m, top) : top - m > S::kSlack ? top : m;
             if (!first && __any_sync(0xffffffffu, next != m)) {   // (the same for both threads of a row)
               const float fall = rescale(m, next);
               l *= fall;
@@ -726,11 +726,20 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
             m = next;
             sum = make_float2(0.f, 0.f);
             uint32_t p[kE];
+            // The maximum is a logit as it was rounded. An FMA's difference to it is that of the logit before its rounding, off by
+            // half a unit of the logit, which from 2^30 on is a weight of 2^+-64 and more. For a row whose maximum is large logits
+            // are rounded alike before the difference. (Row by row: what one row does must not hang on its neighbours.)
+            const bool large = fabsf(m) > 0x1p20f, any = __any_sync(0xffffffffu, large);
+            const float low = large ? 0.f : m;
+            const float2 rest = large ? make_float2(-m, -m) : make_float2(-0.f, -0.f);
 #pragma unroll 1
             for (int c = 0; c < kChunks; ++c) {   // (a chunk's weights stand where logits of the first chunks stood)
               float2 y[kE];
-              load(y, c, m);
+              load(y, c, low);
               mask(y, c, true);
+              if (any)
+#pragma unroll
+                for (int e = 0; e < kE; ++e) y[e] = add2(y[e], rest);
 #pragma unroll
               for (int e = 0; e < kE; ++e) y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
               pack(y, c, p);

@@ -5,7 +5,7 @@ import torch
 
 from tests.cache_cases import to64
 from tests.draft_cases import q8_rows
-from tests.test_gpu_tree import BF16, check, make, run
+from tests.test_gpu_tree import BF16, FP32, check, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,58 @@ def test_the_largest_values_of_8_bits(gpu_device, G, T, d, rise):
     out, lse = run(x, [cap])
     assert torch.isfinite(out).all() and torch.isfinite(lse).all()
     check(x, [cap], out, lse, heads=[0, 17, H - 1])
+
+
+# one of every kernel: (dtype, 8-bit, G, T)
+KINDS = [(FP32, False, 2, 3), (FP32, False, 4, 9), (FP32, True, 4, 9), (BF16, False, 1, 5), (BF16, False, 3, 5), (BF16, False, 2, 20), (BF16, False, 4, 50),
+         *((BF16, True, *k) for k in Q8_KINDS)]
+kinds = pytest.mark.parametrize("kind", KINDS, ids=lambda k: f"{str(k[0])[6:]}-{'q8' if k[1] else 'dense'}-{k[2]}x{k[3]}")
+
+
+@kinds
+@pytest.mark.parametrize("size", [(2, 700), (64, 2600)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("log2", [24, 28, 30, 31, 32, 33, 37, 50, 90])
+def test_large_logits(gpu_device, kind, size, log2):
+    """One key's logit is about twice the others' (or half of them, where they are negative), by far more than a logit's error:
+    its weight is one and the others' are zero."""
+    dtype, q8, G, T = kind
+    (H, cap), d = size, 64
+    x = make(gpu_device, 33, 1, H, G, d, T, cap, dtype, q8=q8)
+    rng = np.random.default_rng(log2)
+    half = log2 // 2
+    for sign in (1.0, -1.0):
+        # every row of queries another mantissa, so that logits are rounded up and down
+        size_q = rng.integers(129, 256, size=(H * G, T)) / 128.0 * 2.0 ** half
+        x["q"] = torch.zeros_like(x["q"])
+        x["q"][0, ..., 0] = torch.from_numpy(size_q).to(x["q"])
+        best = rng.integers(0, cap, size=H)
+        best[:2] = 0, cap - 1
+        k = np.zeros((1, H, cap, d))
+        k[..., 0] = sign * (1.0 if sign > 0 else 1.9921875) * 2.0 ** (log2 - half)
+        k[0, np.arange(H), best, 0] = sign * (1.9921875 if sign > 0 else 1.0) * 2.0 ** (log2 - half)
+        put(x, "k", k, q8, gpu_device)
+        out, lse = run(x, [cap], drafts=False)
+        head = np.arange(H * G) // G
+        want = x["v64"][0, head, best[head]][:, None]
+        logit = to64(x["q"])[0, ..., 0] * x["k64"][0, head, best[head], 0][:, None] / np.sqrt(d)
+        # half a step of the output; the weight, one but for the rounding of the maximum that it is taken under (and over 8 bits times
+        # a step), is off by 2^-8 where it is held as one bf16 value and by 2^-16 as two; its own error (2^-22 for exp2) and fp32's in
+        # what follows
+        part = 0.0 if dtype == FP32 else 2.0 ** -8 if G * T > (32 if q8 else 16) else 2.0 ** -16
+        tol = (torch.finfo(dtype).eps / 2 * (1 + 2.0 ** -7) + part + 2.0 ** -20) * np.abs(want) + 2.0 ** -96
+        assert np.all(np.abs(to64(out)[0] - want) <= tol), f"sign {sign}"
+        assert np.all(np.abs(to64(lse)[0] - logit) <= 2.0 ** -20 * np.abs(logit)), f"sign {sign}"
+
+
+@pytest.mark.parametrize("kind", KINDS[5:7] + KINDS[-2:], ids=lambda k: f"{'q8' if k[1] else 'dense'}-{k[2]}x{k[3]}")
+def test_rows_of_large_logits_leave_their_neighbours_alone(gpu_device, kind):
+    dtype, q8, G, T = kind
+    H, cap, d = 2, 700, 64
+    x = make(gpu_device, 34, 1, H, G, d, T, cap, dtype, q8=q8)
+    want, lse = run(x, [cap])
+    x["q"] = x["q"].clone()
+    x["q"][:, :, ::3] *= 2.0 ** 30
+    got, lse2 = run(x, [cap])
+    rest = [t for t in range(T) if t % 3]
+    assert torch.equal(got[:, :, rest].view(torch.int16), want[:, :, rest].view(torch.int16)) and torch.equal(lse2[:, :, rest], lse[:, :, rest])
+    assert torch.isfinite(got).all()

@@ -109,8 +109,8 @@ def _on_stream(f):
         if stream is None:
             return f(*args, **kwargs)
         for t in (*args, *kwargs.values()):
-            dev = getattr(t, "device", None)   # (of a tensor or a cache)
-            if dev is not None and dev != stream.device:
+            dev = getattr(t, "device", None)   # (of a tensor or a cache; NumPy's numbers have one that is text)
+            if isinstance(dev, torch.device) and dev != stream.device:
                 raise ValueError(f"stream is of {stream.device}, but a tensor is on {dev}")
         with torch.cuda.stream(stream):
             return f(*args, **kwargs)

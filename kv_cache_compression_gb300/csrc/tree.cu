@@ -30,9 +30,9 @@ constexpr int kMmaRows = 16, kMmaRowsQ8 = 32;
 constexpr size_t kCutBytes = (size_t)kMaxTreeCtas * 2 * sizeof(int4);
 static_assert(kCutBytes % 256 == 0, "parts follow");
 
-size_t parts_bytes(int64_t ctas, int tile_q, int head_dim) {
-  return up((size_t)ctas * 2 * tile_q * (head_dim + 2) * sizeof(float));
-}
+// A CTA's two parts.
+size_t part_bytes(int tile_q, int head_dim) { return (size_t)2 * tile_q * (head_dim + 2) * sizeof(float); }
+size_t parts_bytes(int64_t ctas, int tile_q, int head_dim) { return up((size_t)ctas * part_bytes(tile_q, head_dim)); }
 
 int64_t bounded(int64_t tiles, int64_t most) { return tiles < most ? tiles : most; }
 
@@ -86,7 +86,10 @@ cudaError_t tree_fill(tree::Args& a, const TreeJob& job, int tile, int fresh, in
     return cudaSuccess;
   }
   const int64_t rows = (int64_t)a.group * a.tokens, passes = (rows + a.tile_q - 1) / a.tile_q;
-  a.ctas = (int)bounded(bounded(ctas, kMaxTreeCtas), most_tiles(a.batch, a.heads, passes, a.tokens, a.cap, tile, fresh));
+  // No more CTAs than there are parts and notes for in the workspace, whatever a launcher asks for.
+  const size_t room = tree_workspace_bytes(job.batch, job.q_heads, job.heads, job.head_dim, job.tokens, job.cap) - upto_bytes(a.batch) - kCutBytes;
+  const int64_t fit = bounded((int64_t)(room / part_bytes(a.tile_q, job.head_dim)), kMaxTreeCtas);
+  a.ctas = (int)bounded(bounded(ctas, fit), most_tiles(a.batch, a.heads, passes, a.tokens, a.cap, tile, fresh));
   a.ctas -= a.ctas % a.siblings;
   char* ws = static_cast<char*>(job.workspace);
   a.upto = reinterpret_cast<int64_t*>(ws);

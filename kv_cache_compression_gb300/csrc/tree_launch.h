@@ -16,7 +16,7 @@ constexpr int kSimtRows = 32;         // query rows of a pass, at most
 // The call's arguments, for passes of `tile_q` query rows.
 tree::Args tree_args(const TreeJob& job, int tile_q);
 // Cuts the call for at most `ctas` CTAs of one wave with tiles of `tile` cached and `fresh` drafted rows, and lays out
-// its workspace.
+// its workspace, whose parts bound the grid.
 cudaError_t tree_fill(tree::Args& a, const TreeJob& job, int tile, int fresh, int64_t ctas);
 
 cudaError_t launch_tree_simt(const TreeJob& job);   // fp32 instructions: fp32 calls

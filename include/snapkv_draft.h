@@ -49,8 +49,11 @@ extern "C" {
  * dtype    snapkv_dtype of q, k_cache, v_cache, k_new, v_new and out. Products and sums are of fp32 accuracy. In bf16 calls
  *          weights enter the second product rounded: to two bf16 parts (16 bits) in calls of up to 16 query rows (G * T) a KV head
  *          (over 8-bit caches 32), to one (8 bits) in calls of more, which moves an output by 2^-8 sum_r p_r |V_r| at
- *          most. Values that a token sees must be finite; a NaN or infinity in a drafted row reaches none of the tokens that
- *          do not see the row (of those that do, it makes all outputs NaN where it lies in V of a bf16 call)
+ *          most. Values that a token sees must be finite, and so must be, in fp32, the sum over the channels of |q_c K_r,c| for
+ *          each row and 2^8 times the sum over the rows of |V_r| for each channel (weights times V are summed up before they are
+ *          divided by the weights' sum; values of V below 2^89 are small enough for any cache). A NaN or infinity in a drafted row
+ *          reaches none of the tokens that do not see the row (of those that do, it makes all outputs NaN where it lies in V of a
+ *          bf16 call)
  * workspace device, >= snapkv_tree_workspace_size(...) bytes, 256-byte aligned (contents on entry do not matter); the size
  *          serves calls of either type and format. Where it is 0 (caches of up to 256 rows with up to 16 query rows, G * T,
  *          a KV head; also the answer for invalid sizes) the workspace is not used and may be NULL
@@ -88,9 +91,10 @@ typedef struct {
 
 /*
  * snapkv_q8_tree_attend — snapkv_tree_attend over an 8-bit cache: K_cache[r] and V_cache[r] are the values that the
- * rows stand for. dtype is that of q, k_new, v_new and out; arguments and workspace as there. bf16 queries must be below
- * 2^48 in size and their products with drafted rows below 2^62 (queries are scaled on their way to the tensor cores, and
- * outputs on their way back: what a row adds to an output below 2^-96 is lost).
+ * rows stand for. dtype is that of q, k_new, v_new and out; arguments and workspace as there. In bf16 calls queries must be
+ * below 2^48 in size and the sum over the channels of |q_c k_c| below 2^62 for a drafted row, as queries are scaled on their way
+ * to the tensor cores, and outputs on their way back: of a drafted row's weight what is below 2^-81 is lost, and of what a row
+ * adds to an output what is below 2^-96.
  */
 SNAPKV_API snapkv_status snapkv_q8_tree_attend(const void* q, const snapkv_q8_cache* cache, const int32_t* len,
                                                const void* k_new, const void* v_new, const int32_t* n_new,

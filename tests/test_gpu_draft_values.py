@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests.cache_cases import to64
-from tests.draft_cases import q8_rows
+from tests.draft_cases import Q8_FLOOR, check_tree, q8_rows
 from tests.test_gpu_tree import BF16, FP32, check, make, run
 
 pytestmark = pytest.mark.gpu
@@ -106,3 +106,97 @@ def test_rows_of_large_logits_leave_their_neighbours_alone(gpu_device, kind):
     rest = [t for t in range(T) if t % 3]
     assert torch.equal(got[:, :, rest].view(torch.int16), want[:, :, rest].view(torch.int16)) and torch.equal(lse2[:, :, rest], lse[:, :, rest])
     assert torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("kind", [k for k in KINDS if not k[1]], ids=lambda k: f"{str(k[0])[6:]}-{k[2]}x{k[3]}")
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_largest_values_of_dense_rows(gpu_device, kind, d):
+    """2^8 times the sum of |V| just below 2^128, under weights that may exceed one by 2^7.5."""
+    dtype, q8, G, T = kind
+    B, H, cap = 1, 64, 5000
+    x = make(gpu_device, 35, B, H, G, d, T, cap, dtype)
+    steps_of_logits(x, False, gpu_device)
+    rng = np.random.default_rng(36)
+    v = torch.from_numpy(rng.uniform(1, 2, size=(B, H, cap, d)) * 2.0 ** 106).to(dtype)   # 2^8 x 5000 x 2^107 < 2^127.3
+    put(x, "v", to64(v), False, gpu_device)
+    x["v_new"] = (x["v_new"].float().clamp(-1, 1) * 2.0 ** 107).to(dtype)
+    out, lse = run(x, [cap])
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    check(x, [cap], out, lse, heads=[0, 17, H - 1])
+
+
+q8_kinds = pytest.mark.parametrize("G,T", Q8_KINDS)
+
+
+@q8_kinds
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_largest_queries_over_8_bits(gpu_device, G, T, d):
+    x = make(gpu_device, 37, 1, 2, G, d, T, 700, BF16, q8=True)
+    x["q"] = (x["q"].float().clamp(-1.99, 1.99) * 2.0 ** 47).to(BF16)
+    put(x, "k", to64(torch.randn(1, 2, 700, d, generator=torch.Generator().manual_seed(38))) * 2.0 ** -48, True, gpu_device)
+    x["k_new"] = (x["k_new"].float() * 2.0 ** -48).to(BF16)
+    out, lse = run(x, [700])
+    check(x, [700], out, lse)
+
+
+@q8_kinds
+def test_the_largest_products_with_drafted_rows_over_8_bits(gpu_device, G, T):
+    """One drafted row's logit (of 2^61 sqrt(d), or of its half where they are negative) is far above all others."""
+    d = 128
+    for sign in (1.0, -1.0):
+        x = make(gpu_device, 39, 1, 2, G, d, T, 300, BF16, q8=True)
+        x["q"] = torch.zeros_like(x["q"])
+        x["q"][..., 0] = 1.5 * 2.0 ** 40
+        x["k_new"] = torch.zeros_like(x["k_new"])
+        x["k_new"][..., 0] = sign * 2.0 ** 20 * (1.0 if sign > 0 else 1.3125)
+        x["k_new"][:, :, 0, 0] = sign * 2.0 ** 20 * (1.3125 if sign > 0 else 1.0)       # (1.5 x 1.3125 x 2^60 < 2^61)
+        out, lse = run(x, [300 if sign > 0 else 0])
+        want = x["v_new"][:, :, :1].repeat_interleave(G, 1).double()
+        logit = 1.5 * 2.0 ** 60 * sign * (1.3125 if sign > 0 else 1.0) / d ** 0.5
+        assert torch.all((out.double() - want).abs() <= 2.0 ** -6.9 * want.abs())   # an output's and a weight's half step
+        assert torch.all((lse.double() - logit).abs() <= 2.0 ** -20 * abs(logit))
+
+
+@q8_kinds
+@pytest.mark.parametrize("log2", [-40, -60, -70, -80])
+def test_small_weights_of_large_drafted_rows_over_8_bits(gpu_device, G, T, log2):
+    """Cached zeros under weights of one, and drafted rows whose weights of about 2^log2 are all that outputs hang on."""
+    d = 64
+    x = make(gpu_device, 40, 1, 2, G, d, T, 300, BF16, q8=True)
+    x["q"] = torch.zeros_like(x["q"])
+    x["q"][..., 0] = 1.0
+    for name in ("k", "v"):
+        put(x, name, np.zeros((1, 2, 300, d)), True, gpu_device)
+    x["k_new"] = torch.zeros_like(x["k_new"])
+    x["k_new"][..., 0] = log2 * np.log(2.0) * d ** 0.5
+    x["v_new"] = (x["v_new"].float().clamp(-1, 1) * 2.0 ** 47).to(BF16)
+    out, lse = run(x, [300])
+    lost = 2.0 ** -81 * 2.0 ** 47      # of each drafted row's share, rounded to a multiple of 2^-80
+    check_tree(x["q"], x["k64"], x["v64"], [300], out, lse, k_new=x["k_new"], v_new=x["v_new"], floor=lost * T / (300 + T) / 300)
+    assert out.abs().max() > 0
+
+
+@q8_kinds
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("log2", [-60, -72])
+def test_the_smallest_values_of_8_bits(gpu_device, G, T, d, log2):
+    """Steps of V down to about 2^-79: outputs are right but for 2^-96 of each row."""
+    x = make(gpu_device, 41, 2, 2, G, d, T, 300, BF16, q8=True)
+    v = to64(torch.randn(2, 2, 300, d, generator=torch.Generator().manual_seed(42))) * 2.0 ** log2
+    put(x, "v", v, True, gpu_device)
+    x["v_new"] = (x["v_new"].float() * 2.0 ** log2).to(BF16)
+    out, lse = run(x, [300, 131])
+    check(x, [300, 131], out, lse)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,T", [(1, 17), (2, 12), (4, 8), (1, 32)])
+def test_weights_of_two_parts_up_to_32_rows_over_8_bits(gpu_device, G, T, d):
+    """Calls of 17 to 32 query rows a KV head over 8 bits hold weights to 16 bits, as those of fewer: every token is held to the
+    tolerance of a call of its own, with the drafted rows that it sees behind the cached ones."""
+    cap = 300
+    x = make(gpu_device, 43, 1, 2, G, d, T, cap, BF16, q8=True)
+    out, lse = run(x, [cap])
+    for t in range(T):
+        k, v = (np.concatenate([x[n + "64"], to64(x[n + "_new"])[:, :, :t + 1]], 2) for n in "kv")
+        check_tree(x["q"][:, :, t:t + 1], k, v, [cap + t + 1], out[:, :, t:t + 1], lse[:, :, t:t + 1], floor=Q8_FLOOR, where=f"token {t}")

@@ -17,8 +17,11 @@ int64_t most_tiles(int batch, int heads, int64_t passes, int tokens, int64_t cap
 }
 
 size_t upto_bytes(int batch) { return up(((size_t)batch + 1) * sizeof(int64_t)); }
-// Short caches of few rows leave a head to one CTA, in one launch and without workspace: 4 heads of 83 fp32 rows take 5.8 us, and 9
-// with a list and a joining launch.
+// Short caches of few rows leave a head to one CTA, in one launch and without workspace. One limit for both types, as a call's
+// workspace does not depend on its type. bf16 calls gain on both sides of it (128 channels, one query, 32 heads: 256 rows 8.3 us,
+// 12.9 with a list and a joining launch; 512 rows 11.3 and 14.0; 1024 rows 17.1 and 15.8; over 8 bits 7.8 and 14.6, 10.6 and 15.9, 14.7
+// and 17.3). fp32 calls gain up to 64 rows (8.2 us, 11.2) and, where heads are many, up to 256 (512 heads 48 and 52); few heads of 256
+// rows lose by it (one query of 32 heads 16.7 and 14.1, sixteen 27.6 and 17.1).
 bool is_direct(int64_t rows, int64_t cap) { return rows <= 16 && cap <= 256; }
 
 // Query rows a KV head up to which bf16 calls take mma.sync. Dense caches: a pass of it, which memory bounds (sixteen rows over

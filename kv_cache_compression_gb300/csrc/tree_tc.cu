@@ -948,17 +948,20 @@ template <bool Q8, int D, bool TWO> cudaError_t launch_typed(const TreeJob& job)
 }
 
 // Passes of 128 rows or of 256, which read the cache half as often. Where all sequences have as many tokens, an odd number of
-// halves leaves one empty: 384 rows over 1500 keys of 64 channels take 78 us in passes of 128 (93 of 256), 280 over 16384 of 128
-// channels 94 (114), 600 over 8192 94 (103); but 1100 over 1500 202 (197), and even numbers are equal or better in passes of 256.
-// Where sequences have fewer tokens the same holds for most of them, but passes come one after the other: dense caches of 512 KB a
-// head and less are read from L2 (up to 300 tokens over 1500 keys of 64 channels 59 us (65), up to 440 71 (76)), longer ones are
-// not (up to 512 rows over 16384 keys 168 us (154)). Over 8 bits unpacking and softmax count, not reading (up to 256 rows over 16384
-// keys 136 us (159), up to 440 192 (215)).
+// halves leaves one empty: 384 rows over 1500 keys of 64 channels take 79 us in passes of 128 (93 of 256), 280 over 16384 of 128
+// channels 94 (114), and nine halves (1100 rows) over 1500 keys of 256 heads of 64 channels 203 (210), over 2000 keys of 32 heads 39 (53).
+// Of eleven (1400) 257 (247) and 54 (60), so that nine are the last. Even numbers differ little where heads are few (900 rows over
+// 8192 keys of 16 heads 56 us either way) and are better in passes of 256 where they are many (over 1500 keys of 256 heads 182 (171)).
+// Where sequences have fewer tokens, most have an odd number of halves or one, and passes come one after the other, so that what
+// a wave of heads holds has to stay in L2: with 128 channels passes of 128 are as good or better up to 1 MB a head (128 heads, up to
+// 600 rows each: 0.9 MB 77 us (85), 1 MB 82 (85), 2 MB 136 (124), 8 MB 451 (361); up to 256 rows 54 (59), 52 (61), 83 (83), 264 (215)). With
+// 64 channels the way from logits to weights counts more than reading (0.5 MB 59 (64), 1 MB 85 (94), 8 MB 465 (523)), and over 8 bits
+// unpacking does (up to 256 rows over 16384 keys 136 us (159), up to 440 192 (215)).
 template <bool Q8, int D> bool narrow_passes(const TreeJob& job) {
   const int64_t rows = (int64_t)(job.q_heads / job.heads) * job.tokens, halves = (rows + 127) / 128;
-  if (halves > 8) return false;
+  if (halves > 9) return false;
   if (!job.n_new || halves == 1) return halves % 2 != 0;
-  return Q8 || (halves > 2 && job.cap * D * 4 <= 512 * 1024);
+  return Q8 || D == 64 || job.cap * D * 4 <= 1024 * 1024;
 }
 
 template <bool Q8, int D> cudaError_t launch_dim(const TreeJob& job) {

@@ -4,8 +4,8 @@
 //   S = Q K^T,  P = exp2(S - m),  O = sum P V,  running m and sum per row
 //
 // So few rows are bound by the cache's bytes, and mma.sync (1024 products a clock and SM, as measured) is fast enough:
-// sixteen rows take 768 clocks of it per 128 keys of 128 channels, in which HBM delivers 60 keys' bf16 rows or 119 in 8
-// bits. Unlike tcgen05.mma it takes codes and weights from registers, where unpacking and the softmax leave them.
+// sixteen rows take 768 clocks of it per 128 keys of 128 channels, in which HBM delivers 32 keys' bf16 rows or 63 in 8
+// bits (6787 GB/s over 152 SMs at 2.07 GHz: 21.6 bytes a clock and SM). Unlike tcgen05.mma it takes codes and weights from registers, where unpacking and the softmax leave them.
 // Every warp walks tiles of its own (TMA into a ring of its own) with its own m, sum and O; at the end of a head the four
 // warps meet in shared memory. Two CTAs an SM: with 225 to 255 registers a thread there is room for no third.
 //
@@ -38,12 +38,6 @@ using namespace tree;
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr long long kWaitLimit = 4000000000LL;   // about two seconds
-
-constexpr float kQ8Q = 0x1p64f;                  // queries
-constexpr float kQ8Dot = 0x1p69f;                // undoes 2^64 2^-133
-constexpr float kQ8P = 0x1p80f;                  // weights
-constexpr float kQ8Out = 0x1p53f;                // undoes 2^80 2^-133
-constexpr float kNewDot = 0x1p-64f, kNewP = 0x1p-53f;   // the same for drafted rows, whose values are as they are
 
 // HALF: up to eight rows, the lower half of sixteen.
 template <bool Q8, int D, bool HALF> struct Shape {
@@ -86,10 +80,6 @@ __device__ __forceinline__ uint32_t lds16(uint32_t at) {
 }
 __device__ __forceinline__ void sts128_zero(uint32_t at) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
-}
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-  const __nv_bfloat162 two = __floats2bfloat162_rn(x, y);
-  return *reinterpret_cast<const uint32_t*>(&two);
 }
 // The pair as bf16, and in x, y what that leaves.
 __device__ __forceinline__ uint32_t split2(float& x, float& y) {

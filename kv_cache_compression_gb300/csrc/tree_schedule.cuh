@@ -48,6 +48,19 @@ struct Args {
 
 constexpr float kNoMax = -3.402823466e38f;   // the lowest finite value, so that differences to it are no NaN
 
+// 8-bit codes as operands of bf16 products are subnormal: sign and magnitude stand for u 2^-133. Queries and weights carry the powers
+// of two that bring products back; with drafted rows, whose values are as they are, others do.
+constexpr float kQ8Q = 0x1p64f;                         // queries
+constexpr float kQ8Dot = 0x1p69f;                       // undoes 2^64 2^-133
+constexpr float kQ8P = 0x1p80f;                         // weights
+constexpr float kQ8Out = 0x1p53f;                       // undoes 2^80 2^-133
+constexpr float kNewDot = 0x1p-64f, kNewP = 0x1p-53f;   // drafted rows'
+
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  const __nv_bfloat162 two = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&two);
+}
+
 __device__ __forceinline__ int cached_rows(const Args& a, int b) {
   const int n = a.len[b];
   return n < 0 ? 0 : (int64_t)n > a.cap ? (int)a.cap : n;

@@ -11,10 +11,13 @@
 // sequences have as many. A slot issues P V of a tile and Q K^T of its next as one block (S is overwritten when
 // P V has read P: the tensor core takes them one after the other), and passes the turn on.
 //
-// Weights enter the second product as one bf16 value, rounded by half a step (2^-8); they are summed up as they were. A
-// second part for what the rounding leaves made P V twice as long: 169 us instead of 142 where 4 x 8 KV heads, 256 rows
-// each, read 32768 keys (119 now). A row's maximum is only raised, and its O rescaled, when it would grow by more than 2^8 (over
-// 8 bits 2^6); sums and outputs stay under the same maximum, so that nothing is lost.
+// Weights enter the second product as one bf16 value, rounded by half a step (2^-8); they are summed up as they were. That is a
+// choice: outputs are off by 0.0022 to 0.0024 of their norm so, and by 0.0017, their own rounding, with a second part for what the
+// first leaves. With both P V takes twice as long: 4 x 8 KV heads of 256 rows over 32768 keys 119 us, 153 with two parts; up to 440
+// tokens over 1500 keys of 256 heads of 64 channels 72 and 89; 64 x 32 heads of 20 rows over 2140 keys 376 and 438; 8 x 8 heads of
+// 128 rows over 8 bits 101 and 114; where memory binds most, 64 rows over 16384 keys, 79 and 85. Calls in fp32, over 8 bits too, round
+// no weight. A row's maximum is only raised, and its O rescaled, when it would grow by more than 2^8 (over 8 bits 2^6); sums and
+// outputs stay under the same maximum, so that nothing is lost.
 //
 // Measured (128 channels): 4 x 8 KV heads of 256 rows over 32768 keys 119 us, 1100 TFLOP/s; 8 x 8 heads of 64 rows over 16384
 // keys, half of the sequences shorter, 80 us, 5.0 TB/s. With up to 128 rows a KV head memory bounds it; with more, a slot's
@@ -45,9 +48,6 @@ using namespace tree;
 
 constexpr int kTile = 128;                       // keys; also a slot's query rows
 constexpr long long kWaitLimit = 4000000000LL;   // about two seconds
-
-constexpr float kQ8Q = 0x1p64f, kQ8Dot = 0x1p69f, kQ8P = 0x1p80f, kQ8Out = 0x1p53f;
-constexpr float kNewDot = 0x1p-64f, kNewP = 0x1p-53f;   // for drafted rows, whose values are as they are
 
 // What is small in shared memory. (All of it is laid out here: with 192 KB of tiles 160 bytes are left.)
 struct Bars {
@@ -180,11 +180,6 @@ __device__ __forceinline__ void commit(uint32_t leader, uint64_t* bar) {
 __device__ __forceinline__ constexpr uint32_t k_desc(uint32_t at) { return ((at >> 4) & 0x3FFFu) | 1u << 16; }
 __device__ __forceinline__ constexpr uint32_t v_desc(uint32_t at) { return ((at >> 4) & 0x3FFFu) | (uint32_t)((kTile * 128) >> 4) << 16; }
 constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;   // stride, version, swizzle
-
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-  const __nv_bfloat162 two = __floats2bfloat162_rn(x, y);
-  return *reinterpret_cast<const uint32_t*>(&two);
-}
 
 // A piece (eight channels) of a row of a tile in shared memory.
 __device__ __forceinline__ uint32_t piece_at(int row, int piece) {

@@ -722,24 +722,36 @@ __global__ void __launch_bounds__(Shape<Q8, D, TWO>::kThreads, 1) tree_tc_kernel
             sum = make_float2(0.f, 0.f);
             uint32_t p[kE];
             // The maximum is a logit as it was rounded. An FMA's difference to it is that of the logit before its rounding, off by
-            // half a unit of the logit, which from 2^30 on is a weight of 2^+-64 and more. For a row whose maximum is large logits
-            // are rounded alike before the difference. (Row by row: what one row does must not hang on its neighbours.)
-            const bool large = fabsf(m) > 0x1p20f, any = __any_sync(0xffffffffu, large);
-            const float low = large ? 0.f : m;
-            const float2 rest = large ? make_float2(-m, -m) : make_float2(-0.f, -0.f);
+            // half a unit of the logit, which from 2^30 on is a weight of 2^+-64 and more. So for a row whose maximum is large logits
+            // are rounded alike before the difference: an FMA less zero, and an addition (row by row, as what one row does must not hang
+            // on its neighbours; with a zero that the compiler can see it makes one FMA of both). Over 8 bits, where every tile comes this
+            // way, in a loop of its own (for all rows 3 % more time); the few tiles of dense caches that do have the one loop.
+            auto weigh = [&](auto rounded) {
+              const bool large = fabsf(m) > 0x1p20f;
 #pragma unroll 1
-            for (int c = 0; c < kChunks; ++c) {   // (a chunk's weights stand where logits of the first chunks stood)
-              float2 y[kE];
-              load(y, c, low);
-              mask(y, c, true);
-              if (any)
+              for (int c = 0; c < kChunks; ++c) {   // (a chunk's weights stand where logits of the first chunks stood)
+                float2 y[kE];
+                if constexpr (decltype(rounded)::value) {
+                  load(y, c, large ? 0.f : m);
+                  const float rest = large ? -m : -0.f;
 #pragma unroll
-                for (int e = 0; e < kE; ++e) y[e] = add2(y[e], rest);
+                  for (int e = 0; e < kE; ++e) y[e] = add2(y[e], make_float2(rest, rest));
+                } else {
+                  load(y, c, m);
+                }
+                mask(y, c, true);
 #pragma unroll
-              for (int e = 0; e < kE; ++e) y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
-              pack(y, c, p);
-              tmem_st(s_at + kKeys * half + kE * c, p);
-            }
+                for (int e = 0; e < kE; ++e) y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
+                pack(y, c, p);
+                tmem_st(s_at + kKeys * half + kE * c, p);
+              }
+            };
+            if constexpr (!Q8)
+              weigh(std::true_type());
+            else if (__any_sync(0xffffffffu, fabsf(m) > 0x1p20f))
+              weigh(std::true_type());
+            else
+              weigh(std::false_type());
           }
           l += sum.x + sum.y;
           ptx::tmem_wait_st();

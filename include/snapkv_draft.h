@@ -108,7 +108,8 @@ SNAPKV_API snapkv_status snapkv_q8_tree_attend(const void* q, const snapkv_q8_ca
  *
  * k_new, v_new  device [B, H, rows, d], rows >= 1
  * pick     device int32 [B, picks], picks >= 1 (NULL: rows 0 .. n_b - 1; picks is then not used). A row may be picked
- *          more than once
+ *          more than once. Every block that writes rows of a sequence reads all of its picks first, which counts where they are
+ *          many (16384 picked rows of 32 heads take 95 us, all rows without a pick 85; quantised 101 and 71)
  * n_new    device int32 [B], 0 <= n_new[b] <= picks (rows without a pick) (NULL: n_b = picks, or rows)
  * len_in   device int32 [B]; len_out device int32 [B], must not overlap len_in
  * A sequence whose rows do not fit (or with len_in[b] < 0, n_new[b] out of range, or one of its picks out of 0 ..

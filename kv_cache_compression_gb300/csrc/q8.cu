@@ -4,7 +4,8 @@
 // kTpr-th run of eight channels, so that neighbouring lanes load neighbouring 16 bytes (bf16). Every byte is read and
 // written once: 32 heads of 16384 bf16 rows of 128 channels, K and V, quantised and read back in 142 us (5.7 TB/s; bytes bound
 // the reading, while quantising has the schedulers busy for 74 %); 64 x 32 heads, up to six picked rows each, 7.6 us, the
-// latency of a launch.
+// latency of a launch. Picks are made for accepted tokens: every block checks all of its sequence's before it writes, so that a sequence
+// with a bad one is left as it was without a launch more. 33 picks cost nothing so, 16384 of 32 heads 10 us of 95 (dense) or 30 of 101.
 #include "draft_internal.h"
 #include "q4.cuh"
 #include "row_list.cuh"
